@@ -28,7 +28,8 @@
  *     the caller's next synchronisation.  TQ_ERR_CUDA reports a launch error
  *     whose cudaError_t value tq_last_cuda_error() returns.
  *   - fp16 data are IEEE binary16 bit patterns (uint16_t / __half).
- *   - Device buffers must be 16-byte aligned (TQ_ERR_ALIGN otherwise).
+ *   - Device buffers must be 16-byte aligned (TQ_ERR_ALIGN otherwise), except
+ *     where a call says less.
  *   - head_dim is any power of two from 16 to 1024 ("turboquant-mlx",
  *     "Walsh-Hadamard Rotation": WalshHadamardRotation(head_dim, seed)).  At
  *     head_dim = 128 every call and option below is available (decode with GQA
@@ -36,7 +37,8 @@
  *     tq_compress, tq_dequantize and tq_decode_attention (GQA 1 to 4) with the
  *     SRHT rotation and the Gaussian value codebook; QJL sketches (keys or
  *     values), dense rotations, the sphere codebook, attention-mass outputs
- *     and tq_requantize return TQ_ERR_UNSUPPORTED there.
+ *     and tq_requantize return TQ_ERR_UNSUPPORTED there.  tq_rope, tq_append,
+ *     tq_read and tq_tree_attention take every head_dim.
  */
 #ifndef TQ_H
 #define TQ_H
@@ -416,6 +418,165 @@ int tq_decode_last_launches(void);
 tq_status tq_decode_attention_static(const tq_layer_view *layers, int n_layers, int batch,
                                      int n_heads, int q_heads, int head_dim, const float *qjl_S,
                                      int jl_dim, const void *q, float *out, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Serving: rotary positions, writes and reads at each sequence's own          */
+/* position, attention of a tree of drafted tokens.  (No counterpart on the    */
+/* pages, which take post-projection keys of one new token per step.)          */
+/*                                                                             */
+/* These calls take sequences of unequal length: per-sequence numbers (int32)   */
+/* are device memory, read by the kernels and never by the host, so that a      */
+/* captured call can be replayed on other lengths.  What they hold is checked   */
+/* on the device: a row whose position or source lies outside its buffer is     */
+/* skipped, a length is clamped to its segment.  Strides are in elements and    */
+/* may have any order; the head dimension has unit stride.  16-byte alignment   */
+/* of rows is not required (of packed buffers it is), aligned rows are faster.  */
+/* Every call works on the current device, whose memory all pointers name.      */
+/* ------------------------------------------------------------------------ */
+#define TQ_DTYPE_F16 0
+#define TQ_DTYPE_BF16 1
+#define TQ_DTYPE_F32 2
+
+/* Frequencies of rotary positions: w_m = base^(-2 m / rotary_dim), pair m <
+ * rotary_dim / 2, the angle of position p is p w_m.  Longer contexts (scale
+ * factor s, original length L):
+ *   NONE    w_m;
+ *   LINEAR  w_m / s (positions interpolated);
+ *   BASE    w_m of the base times s^(r / (r - 2)), r = rotary_dim (the first pair keeps
+ *           its frequency, the last one's is divided by s);
+ *   TURNS   w_m (u + (1 - u) / s), u = clamp((n_m - slow) / (fast - slow), 0, 1),
+ *           n_m = L w_m / (2 pi) the pair's turns over the original length: pairs of
+ *           at least `fast` turns are kept, of at most `slow` turns divided by s;
+ *   INDEX   the same with u linear in the pair's index: u = 1 - clamp((m - lo) / (hi -
+ *           lo), 0, 1), m(n) = r ln(L / (2 pi n)) / (2 ln base) the (real) index with n
+ *           turns, lo = max(floor(m(fast)), 0), hi = min(ceil(m(slow)), r - 1), hi - lo
+ *           taken as 0.001 if they are equal.
+ * Every cosine and sine is multiplied by `amplitude`. */
+#define TQ_ROPE_SCALE_NONE 0
+#define TQ_ROPE_SCALE_LINEAR 1
+#define TQ_ROPE_SCALE_BASE 2
+#define TQ_ROPE_SCALE_TURNS 3
+#define TQ_ROPE_SCALE_INDEX 4
+typedef struct {
+    int rotary_dim;        /* r: even, 2..TQ_MAX_HEAD_DIM */
+    int scaling;           /* TQ_ROPE_SCALE_* */
+    double base;           /* > 1 */
+    double factor;         /* s > 0 (any scaling but NONE) */
+    double original_len;   /* L > 0 (TURNS, INDEX) */
+    double fast, slow;     /* fast > slow > 0 (TURNS, INDEX) */
+    double amplitude;      /* > 0 */
+} tq_rope_spec;
+
+/* freq (host, rotary_dim / 2 doubles): the frequencies of the pairs, binary64.
+ * TQ_ERR_ARG on a value outside the ranges above, a non-finite one, or BASE
+ * with rotary_dim 2. */
+tq_status tq_rope_frequencies(const tq_rope_spec *spec, double *freq);
+
+/* Fill table (device, float [n_pos][2][rotary_dim / 2], 16-byte aligned) with the
+ * cosines, then the sines, of positions first_pos .. first_pos + n_pos - 1, times
+ * the amplitude: angles, cosines and products in binary64, rounded to binary32
+ * once.  n_pos >= 0, first_pos >= 0, their sum at most 2^31 - 1. */
+tq_status tq_rope_table(const tq_rope_spec *spec, int first_pos, int n_pos, float *table, void *stream);
+
+#define TQ_ROPE_HALF 0         /* pair m = coordinates (m, m + rotary_dim / 2) */
+#define TQ_ROPE_INTERLEAVED 1  /* pair m = coordinates (2 m, 2 m + 1) */
+typedef struct {
+    int rotary_dim;        /* even, 2..head_dim; coordinates behind it are unchanged */
+    int layout;            /* TQ_ROPE_HALF or TQ_ROPE_INTERLEAVED */
+    int n_pos;             /* rows of the table */
+    const float *table;    /* device [n_pos][2][rotary_dim / 2], 16-byte aligned (tq_rope_table, or the caller's own) */
+} tq_rope_view;
+
+#define TQ_MAX_ROPE_TENSORS 4
+typedef struct {
+    const void *in;        /* element (b, h, t, i) at b*in_stride[0] + h*in_stride[1] + t*in_stride[2] + i */
+    void *out;             /* likewise with out_stride; out may be in (same strides), else they must not overlap */
+    int n_heads;           /* >= 0 */
+    int64_t in_stride[3];  /* any, zero included (broadcast) */
+    int64_t out_stride[3]; /* rows must not overlap: at least head_dim in absolute value on every axis longer than one */
+} tq_rope_tensor;
+
+/* Rotary positions of up to TQ_MAX_ROPE_TENSORS tensors of the same batch, tokens
+ * and head_dim (queries and keys) in one launch.  The pair (a, b) with the table's
+ * (c, s) of the token's position becomes (a c - b s, b c + a s); inverse != 0
+ * negates s (the transpose, which is the gradient).  Products and sums are
+ * binary32 operations (no fused multiply-add), rounded once to the tensors' type,
+ * so the result is a pure function of x and the table.  positions: device int32
+ * [batch][n_tokens], sequence b's at b*pos_stride_b; a token whose position is
+ * outside [0, n_pos) is copied unchanged.  head_dim: 1..TQ_MAX_HEAD_DIM here.
+ * positions: 4-byte aligned; tensors aligned to their element (else TQ_ERR_ALIGN). */
+tq_status tq_rope(const tq_rope_view *rope, int dtype, int batch, int n_tokens, int head_dim, const int *positions,
+                  int64_t pos_stride_b, const tq_rope_tensor *x, int n_tensors, int inverse, void *stream);
+
+/* Write new rows of unequal sequences into a segment (packed, or fp16).  For
+ * sequence b and j < min(n_new[b], n_max) the source row is s = index ?
+ * index[b*index_stride_b + j] : j and the target position t = t_begin[b] + j;
+ * with s in [0, n_source) and t in [0, capacity), position t gets key row s of
+ * K, rotated by positions[b*pos_stride_b + s] and rounded to fp16 if `rope` is
+ * given (the bits tq_rope writes), and value row s of V: compressed to exactly the
+ * codes and scales tq_compress gives them, or copied (fp16 segment).  Other rows
+ * of the segment stay as they are; its n_tokens is the caller's to update.
+ *   K, V    device fp16, element (b, h, s, i) at b*stride[0] + h*stride[1] + s*stride[2] + i;
+ *           must not overlap the segment
+ *   t_begin device int32 [batch]; n_new: likewise, NULL: n_max rows each; negative: none
+ *   index   device int32, NULL: row j itself
+ *   rot     the layer's rotation (SRHT); unused for fp16 segments (may be NULL)
+ * Packed segments with QJL heads (key or value) and dense rotations return
+ * TQ_ERR_UNSUPPORTED, as does the sphere law at head dims other than 128. */
+tq_status tq_append(const tq_segment *dst, const tq_rotation *rot, const tq_rope_view *rope, const int *positions,
+                    int64_t pos_stride_b, const void *K, const int64_t *k_stride, const void *V,
+                    const int64_t *v_stride, int n_source, int n_max, const int *t_begin, const int *n_new,
+                    const int *index, int64_t index_stride_b, void *stream);
+
+/* Read rows of a segment back: for sequence b and j < min(n_read[b], n_max)
+ * with t = t_begin[b] + j in [0, capacity), row j of K and V (device, `dtype`,
+ * element (b, h, j, i) at b*stride[0] + h*stride[1] + j*stride[2] + i; either may
+ * be NULL) gets the vector that position t stands for: R (m level(code)) and R
+ * (sigma centroid[code]) of a packed segment in binary32 rounded once to the type
+ * (rot == NULL: without R, in the rotated space), the fp16 rows of an fp16 one.
+ * Other rows of K and V stay as they are.  The rows written must not overlap.
+ * n_read NULL: n_max rows each.  QJL sketches are not applied (as in
+ * tq_dequantize); a dense rotation returns TQ_ERR_UNSUPPORTED, as does the sphere
+ * law at head dims other than 128. */
+tq_status tq_read(const tq_segment *src, const tq_rotation *rot, int n_max, const int *t_begin, const int *n_read,
+                  int dtype, void *K, const int64_t *k_stride, void *V, const int64_t *v_stride, void *stream);
+
+#define TQ_MAX_DRAFTS 256
+typedef struct {
+    int n_drafts;              /* N: 1..TQ_MAX_DRAFTS drafted tokens per sequence */
+    const void *q;             /* device fp16, element (b, i, j, e) of draft i, query head j at b*q_stride[0] + i*q_stride[1] + j*q_stride[2] + e */
+    const void *k, *v;         /* device fp16, element (b, h, i, e) of KV head h, draft i, strides likewise (b, h, i) */
+    int64_t q_stride[3], k_stride[3], v_stride[3];
+    const uint32_t *mask;      /* device: bit j % 32 of word b*mask_stride_b + i*ceil(N/32) + j/32 set: draft i sees
+                                  draft j (itself included only if set); NULL: j <= i (a chain) */
+    int64_t mask_stride_b;     /* words between sequences; 0: one tree for all */
+    const int *seg_len[TQ_MAX_SEGMENTS]; /* device int32 [batch] per segment of the view: sequence b holds
+                                  min(seg_len[b], n_tokens) of its tokens; NULL: n_tokens */
+    void *out;                 /* device fp16 [batch][N][q_heads][d], 16-byte aligned */
+} tq_tree;
+
+/* Bytes of device workspace tq_tree_attention needs; depends on the segments'
+ * kinds and n_tokens (an upper bound of the sequences' lengths) and the counts. */
+tq_status tq_tree_workspace_size(const tq_layer_view *layer, int batch, int n_heads, int q_heads, int head_dim,
+                                 int n_drafts, size_t *bytes);
+
+/* Attention of N drafted tokens per sequence over one layer's cache and each
+ * other, in one pass over the cache: out[b][i][j] = softmax(q . k / sqrt(d)) . v
+ * over the cached tokens of every segment (as tq_decode_attention; all drafts
+ * see all of them) and the drafted tokens that draft i sees.  A draft that sees
+ * nothing (an empty cache, an empty mask row) yields zeros.  q_heads: any
+ * multiple of n_heads.  The N drafts of the q_heads / n_heads query heads of one KV
+ * head share each unpacking of the cache.  Scores and the value sum of packed
+ * tokens run in the rotated space; one inverse rotation follows the merge.  fp16
+ * operands, binary32 sums, the result rounded to fp16.  All numbers on the device
+ * (lengths, mask) may change between replays of a captured call; two calls that
+ * may overlap need two workspaces.  QJL heads (key or value), dense rotations and
+ * segments with attn_mass return TQ_ERR_UNSUPPORTED, as does the sphere law at
+ * head dims other than 128.  No device memory is allocated and nothing is
+ * copied from the host.  tq_decode_error_flag reads the workspace's error flag
+ * (a wait for copies or tensor-core work that ran out; cleared by the next call). */
+tq_status tq_tree_attention(const tq_layer_view *layer, int batch, int n_heads, int q_heads, int head_dim,
+                            const tq_tree *tree, void *workspace, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

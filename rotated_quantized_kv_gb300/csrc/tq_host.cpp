@@ -14,6 +14,7 @@
 
 #include "tq_internal.h"
 #include "tq_mass.h"
+#include "tq_serve.h"
 
 using namespace tqk;
 
@@ -995,6 +996,14 @@ tq_status build_plan(const tq_layer_view *layers, int n_layers, int B, int H, in
 }  // namespace
 
 tq_status tqk::record_cuda_error(cudaError_t e) { return cuda_fail(e); }
+
+// what the serving calls (tq_serve_host.cpp) share with this file
+tq_status tqk::layout_status(const tq_segment_layout *L, bool need_bits) { return check_layout(L, need_bits); }
+void tqk::value_thresholds(float *flat, const uint8_t *bits, int H, int law) { fill_thresholds(flat, bits, H, law); }
+void tqk::value_centroids(float *flat, const uint8_t *bits, int H, int law) { fill_centroids(flat, bits, H, law); }
+float tqk::rotation_scale(int d) { return inv_sqrt_f32(d); }
+int tqk::decode_wait_polls() { return g_wait_polls.load(); }
+int tqk::current_sm_count() { return sm_count(); }
 
 // =============================================================== C ABI
 extern "C" {

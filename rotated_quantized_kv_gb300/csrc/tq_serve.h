@@ -1,0 +1,142 @@
+// tq_serve.h -- private declarations of the serving calls (rotary positions,
+// ragged writes and reads, tree attention): kernel parameters and launchers.
+#pragma once
+
+#include "tq_internal.h"
+
+namespace tqk {
+
+// ----------------------------------------------------------------- rotary positions
+struct RopeTable {               // tq_rope_table
+    double freq[TQ_MAX_HEAD_DIM / 2];
+    double amplitude;
+    int half, first, n;
+    float *table;
+};
+
+struct RopeView {
+    const float *table;          // [n_pos][2][half], or nullptr: no rotary positions
+    int half, interleaved, n_pos;
+};
+
+struct RopeTensorParams {
+    const void *in;
+    void *out;
+    int64_t is[3], os[3];        // strides of (b, h, t)
+    int head0;                   // first head in the concatenation of the call's tensors
+};
+
+struct RopeParams {
+    RopeView rope;
+    const int *positions;
+    int64_t pos_stride;
+    int B, T, d, inverse;
+    int n_tensors, heads;        // heads: over all tensors
+    RopeTensorParams x[TQ_MAX_ROPE_TENSORS];
+};
+cudaError_t launch_rope_table(const RopeTable &p, cudaStream_t s);
+cudaError_t launch_rope(const RopeParams &p, int dtype, cudaStream_t s);
+
+// ----------------------------------------------------------------- segments
+// A segment as the serving kernels address it: rows of (b, h, t).
+struct SegView {
+    int fp16;                    // fp16 segment: k, v are its rows
+    int capacity;
+    const uint8_t *k, *v;        // packed codes (or fp16 rows) of (0, 0, 0)
+    const float *ks, *vs;        // packed: scales of (0, 0, 0)
+    uint64_t kblock, vblock;     // bytes per batch element
+    uint64_t koff[kMaxH], voff[kMaxH];  // byte offset of a head inside a batch block
+    uint8_t kbits[kMaxH], vbits[kMaxH];
+};
+
+struct RowMap {                  // rows of a ragged write or read
+    const int *t_begin, *n_rows; // n_rows: nullptr: n_max
+    const int *index;            // source row of row j (writes), or nullptr
+    int64_t index_stride;
+    int n_max, n_source;
+};
+
+struct AppendParams {
+    SegView seg;
+    RowMap rows;
+    RopeView rope;
+    const int *positions;
+    int64_t pos_stride;
+    const uint16_t *K, *V;
+    int64_t ks[3], vs[3];        // strides of (b, h, s)
+    int B, H, d;
+    uint32_t sign_bits[kMaxD / 32];
+    float inv_sqrt_d;
+    float thr[kCbTotal];         // value thresholds, flat by bit width
+};
+cudaError_t launch_append(const AppendParams &p, cudaStream_t s);
+
+struct ReadParams {
+    SegView seg;
+    RowMap rows;
+    void *K, *V;                 // either may be null
+    int64_t ks[3], vs[3];
+    int B, H, d;
+    int rotate;                  // apply R
+    uint32_t sign_bits[kMaxD / 32];
+    float inv_sqrt_d;
+    float centroid[kCbTotal];
+};
+cudaError_t launch_read(const ReadParams &p, int dtype, cudaStream_t s);
+
+// ----------------------------------------------------------------- tree attention
+// The work is a list of 128-token tiles.  For sequence b in order, KV head h,
+// block of query rows rb (of R rows; row = draft * g + query head of the group):
+// the tiles of b's packed segments, then those of its fp16 segments.  G workers
+// take equal contiguous ranges of the list.  The tiles of one (b, h, rb) are cut
+// into parts: packed tiles every kTreePart, the fp16 ones likewise; every worker
+// leaves one record (m, l, sum per row) for each part that it touches, at slot
+// worker + part index (the pairs (worker, part) form a monotone path, so that
+// the sums are distinct).  The merge adds the drafted tokens.
+constexpr int kTreeTile = 128;
+constexpr int kTreePart = 128;   // tiles: bounds the length of one tensor-core sum
+
+struct TreeSeg {
+    SegView seg;
+    const int *len;              // per-sequence length or nullptr
+    int n_tokens;
+    int law;                     // value codebook
+};
+
+struct TreeParams {
+    int B, H, g, N, d, R, n_rb;  // g query heads per KV head, R rows per block, n_rb blocks
+    int n_seg;                   // packed segments first
+    int n_packed;
+    int ragged;                  // some segment has per-sequence lengths
+    int parts_packed, parts;     // parts per (b, h, rb): packed ones, all
+    TreeSeg seg[TQ_MAX_SEGMENTS];
+    const uint16_t *q, *k, *v;
+    int64_t qs[3], ks[3], vs[3];
+    const uint32_t *mask;
+    int64_t mask_stride;
+    int mask_words;
+    uint16_t *out;
+    float *part;                 // records: [slot][R][d + 4]: m (log2 units), l, pad, pad, sum
+    int *error;
+    int workers, wait_polls;
+    uint32_t sign_bits[kMaxD / 32];
+    float inv_sqrt_d, qk_scale;  // qk_scale: log2(e) / sqrt(d)
+    float centroid[2][kCbTotal]; // by law
+};
+// Rows per block, workers and the kernel's choice for a shape: the same rule
+// sizes the workspace and launches the kernel.
+struct TreeShape {
+    int R, n_rb, workers;
+};
+TreeShape tree_shape(int B, int H, int g, int N, int d, long long tiles_per_head);
+cudaError_t launch_tree(const TreeParams &p, cudaStream_t s);
+
+// ----------------------------------------------------------------- from tq_host.cpp
+tq_status layout_status(const tq_segment_layout *L, bool need_bits);
+void value_thresholds(float *flat, const uint8_t *bits, int H, int law);
+void value_centroids(float *flat, const uint8_t *bits, int H, int law);
+float rotation_scale(int d);
+int decode_wait_polls();
+int current_sm_count();
+
+}  // namespace tqk

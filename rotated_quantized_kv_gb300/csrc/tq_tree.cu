@@ -1,0 +1,330 @@
+// tq_tree.cu -- attention of a tree of drafted tokens over the compressed cache.
+//
+// For query row r (draft i, head j of the KV head's group) and token t with key
+// k_t, value v_t: x_t = q_r . k_t log2(e) / sqrt(d), m = max x_t, l = sum 2^(x_t -
+// m), o = sum 2^(x_t - m) v_t / l.  Packed tokens have k_t = R y_t, so x_t = (R q) .
+// y_t and their share of o is R sum 2^(x_t - m) z_t: scores and sums run in the
+// rotated space, one R follows the merge.
+//
+// This file holds the form for every head dimension and the merge.  A CTA takes an equal
+// range of the tile list (tq_serve.h), stages 8 to 32 tokens at a time as
+// binary32 rows in shared memory and keeps the running max, sum and values of up to
+// 16 query rows.
+#include <algorithm>
+
+#include <cuda_fp16.h>
+
+#include "tq_serve.h"
+#include "tq_team.cuh"
+#include "tq_tree.cuh"
+
+namespace tqk {
+namespace {
+
+using namespace tree;
+
+constexpr int kTreeThreads = 128;
+constexpr int kTreeWarps = kTreeThreads / 32;
+constexpr float kInf = __builtin_huge_valf();
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <int D>
+struct Plain {
+    static constexpr int R = D <= 256 ? 16 : 8;                    // query rows
+    static constexpr int TT = D <= 256 ? 32 : 8192 / D;            // tokens staged
+    static constexpr int DPT = (D + kTreeThreads - 1) / kTreeThreads;
+    static constexpr int LD = D + 1;                               // row stride: columns in different banks
+    static constexpr size_t smem = (2 * R * LD + TT * LD + R * TT + 3 * R) * sizeof(float);
+};
+
+// One row of K or V (element e of token t) in binary32, rotated space for packed ones.
+template <int D>
+__device__ __forceinline__ float tile_value(const TreeParams &p, const Pos &x, const Tile &w, int kv, int t, int e) {
+    const SegView &s = p.seg[w.seg].seg;
+    const uint8_t *base = (kv ? s.v : s.k) + x.b * (kv ? s.vblock : s.kblock) + (kv ? s.voff[x.h] : s.koff[x.h]);
+    if (s.fp16) return __half2float(reinterpret_cast<const __half *>(base)[static_cast<size_t>(t) * D + e]);
+    const int bits = kv ? s.vbits[x.h] : s.kbits[x.h];
+    const uint32_t c = code_at(base + static_cast<size_t>(t) * (D * bits / 8), e, bits);
+    const float sc = (kv ? s.vs : s.ks)[(static_cast<size_t>(x.b) * p.H + x.h) * s.capacity + t];
+    if (kv) return sc * p.centroid[p.seg[w.seg].law][cb_off(bits) + c];
+    return sc * (static_cast<float>(2 * c + 1) * __uint_as_float(static_cast<uint32_t>(127 - bits) << 23) - 1.0f);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTreeThreads) tree_plain_kernel(const __grid_constant__ TreeParams p) {
+    using C = Plain<D>;
+    constexpr int R = C::R, TT = C::TT, LD = C::LD, DPT = C::DPT;
+    extern __shared__ float sm[];
+    float *q0 = sm, *q1 = q0 + R * LD, *tok = q1 + R * LD, *S = tok + TT * LD;  // q, R q, tokens, scores
+    float *row_m = S + R * TT, *row_l = row_m + R, *row_c = row_l + R;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.error = 0;
+    const long long T = total_tiles(p), G = workers_of(p, T), c = blockIdx.x;
+    if (c >= G) return;
+    long long at = c * T / G;
+    const long long end = (c + 1) * T / G;
+    Pos x = seek(p, at);
+    float acc[R][DPT];
+    long long group = -1, part = -1;
+    auto restart = [&] {
+        __syncthreads();
+        for (int r = threadIdx.x; r < R; r += kTreeThreads) row_m[r] = -kInf, row_l[r] = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; r++)
+#pragma unroll
+            for (int e = 0; e < DPT; e++) acc[r][e] = 0.f;
+        __syncthreads();
+    };
+    auto flush = [&] {  // the record of `part`
+        __syncthreads();
+        float *rec = p.part + static_cast<size_t>(c + part) * R * (D + 4);
+        for (int r = threadIdx.x; r < R; r += kTreeThreads) {
+            rec[r * (D + 4)] = row_m[r];
+            rec[r * (D + 4) + 1] = row_l[r];
+        }
+#pragma unroll
+        for (int r = 0; r < R; r++)
+#pragma unroll
+            for (int e = 0; e < DPT; e++) {
+                const int i = threadIdx.x + e * kTreeThreads;
+                if (i < D) rec[r * (D + 4) + 4 + i] = acc[r][e];
+            }
+    };
+    for (; at < end; at++, advance(p, x)) {
+        const long long g = group_of(p, x), pt = part_of(p, g, x.tp, x.k);
+        if (pt != part) {
+            if (part >= 0) flush();
+            part = pt;
+            restart();
+        }
+        if (g != group) {  // the block's query rows, as they are and rotated
+            group = g;
+            __syncthreads();
+            for (int r = warp; r < R; r += kTreeWarps) {
+                const int row = x.rb * R + r;
+                float v[(D + 31) / 32];
+#pragma unroll
+                for (int j = 0; j < (D + 31) / 32; j++) {
+                    const int e = lane + 32 * j;
+                    v[j] = 0.f;
+                    if (row < p.N * p.g && e < D)
+                        v[j] = __half2float(__ushort_as_half(
+                            p.q[x.b * p.qs[0] + (row / p.g) * p.qs[1] + (x.h * p.g + row % p.g) * p.qs[2] + e]));
+                    if (e < D) q0[r * LD + e] = v[j];
+                }
+                warp_rotate_strided<D>(v, p.sign_bits, p.inv_sqrt_d, lane);
+#pragma unroll
+                for (int j = 0; j < (D + 31) / 32; j++)
+                    if (lane + 32 * j < D) q1[r * LD + lane + 32 * j] = v[j];
+            }
+        }
+        const Tile w = tile_at(p, x);
+        const float *q = x.k < x.tp ? q1 : q0;
+        for (int t0 = 0; t0 < w.n; t0 += TT) {
+            const int nt = min(TT, w.n - t0);
+            __syncthreads();
+            for (int i = threadIdx.x; i < nt * D; i += kTreeThreads)
+                tok[(i / D) * LD + i % D] = tile_value<D>(p, x, w, 0, w.t0 + t0 + i / D, i % D);
+            __syncthreads();
+            for (int i = threadIdx.x; i < R * TT; i += kTreeThreads) {
+                const int r = i / TT, t = i % TT;
+                float s = -kInf;
+                if (t < nt) {
+                    s = 0.f;
+                    for (int e = 0; e < D; e++) s = fmaf(q[r * LD + e], tok[t * LD + e], s);
+                    s *= p.qk_scale;
+                }
+                S[i] = s;
+            }
+            __syncthreads();
+            for (int r = warp; r < R; r += kTreeWarps) {
+                const float s = lane < TT ? S[r * TT + lane] : -kInf;
+                float m = s;
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const float old = row_m[r], now = fmaxf(old, m);
+                const float pr = s == -kInf ? 0.f : ex2(s - now);  // (no NaN from -inf - -inf)
+                float l = pr;
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                const float f = now == -kInf ? 1.f : ex2(old - now);
+                if (lane < TT) S[r * TT + lane] = pr;
+                __syncwarp();
+                if (lane == 0) row_m[r] = now, row_l[r] = row_l[r] * f + l, row_c[r] = f;
+            }
+            for (int i = threadIdx.x; i < nt * D; i += kTreeThreads)
+                tok[(i / D) * LD + i % D] = tile_value<D>(p, x, w, 1, w.t0 + t0 + i / D, i % D);
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < DPT; e++) {
+                const int i = threadIdx.x + e * kTreeThreads;
+                if (i < D) {
+#pragma unroll
+                    for (int r = 0; r < R; r++) acc[r][e] *= row_c[r];
+                    for (int t = 0; t < nt; t++) {
+                        const float v = tok[t * LD + i];
+#pragma unroll
+                        for (int r = 0; r < R; r++) acc[r][e] = fmaf(S[r * TT + t], v, acc[r][e]);
+                    }
+                }
+            }
+        }
+    }
+    flush();
+}
+
+// ---------------------------------------------------------------- merge
+// A warp per query row: every record of its group in order, R on the packed share,
+// then the drafted tokens that the row sees, in binary32 (few tokens per row, so
+// that neither the mask nor a non-finite value of an unseen draft can reach the
+// row), the quotient, and the fp16 row.
+template <int D>
+__global__ void __launch_bounds__(kTreeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+    constexpr int J = (D + 31) / 32;
+    __shared__ float draft_x[kTreeWarps][TQ_MAX_DRAFTS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long rows = static_cast<long long>(p.N) * p.g;
+    const long long id = blockIdx.x * static_cast<long long>(kTreeWarps) + warp;  // (b, h, row)
+    if (id >= rows * p.B * p.H) return;
+    const int row = static_cast<int>(id % rows), bh = static_cast<int>(id / rows);
+    const int b = bh / p.H, h = bh % p.H, rb = row / p.R, r = row % p.R;
+    const int draft = row / p.g, head = h * p.g + row % p.g;
+    const long long T = total_tiles(p), G = workers_of(p, T);
+    int tp, tf;
+    seq_tiles(p, b, tp, tf);
+    long long first = 0;  // first tile of the group
+    if (p.ragged) {
+        for (int i = lane; i < b; i += 32) {
+            int a, c;
+            seq_tiles(p, i, a, c);
+            first += a + c;
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
+    } else {
+        first = static_cast<long long>(b) * (tp + tf);
+    }
+    first = first * p.H * p.n_rb + (static_cast<long long>(h) * p.n_rb + rb) * (tp + tf);
+    const long long group = (static_cast<long long>(b) * p.H + h) * p.n_rb + rb;
+    const int np = (tp + kTreePart - 1) / kTreePart, nf = (tf + kTreePart - 1) / kTreePart;
+    float M = -kInf, L = 0.f, a[2][J];
+#pragma unroll
+    for (int j = 0; j < J; j++) a[0][j] = a[1][j] = 0.f;
+    // records of part i (packed ones, then the others): workers [lo, hi]
+    auto each = [&](auto &&f) {
+        for (int i = 0; i < np + nf; i++) {
+            const int k0 = i < np ? i * kTreePart : tp + (i - np) * kTreePart;
+            const int k1 = min(k0 + kTreePart, i < np ? tp : tp + tf);
+            const long long lo = worker_of(first + k0, T, G), hi = worker_of(first + k1 - 1, T, G);
+            const long long slot = part_of(p, group, tp, k0);
+            for (long long w = lo; w <= hi; w++)
+                f(p.part + (static_cast<size_t>(w + slot) * p.R + r) * (D + 4), i < np ? 0 : 1);
+        }
+    };
+    bool nan = false;  // fmaxf passes over NaN: a row that sees only NaN scores is NaN, not empty
+    each([&](const float *rec, int) {
+        const float l = __ldcg(rec + 1);
+        M = fmaxf(M, __ldcg(rec));
+        nan |= l != l;
+    });
+    // scores of the drafts that the row sees, one after the other
+    float q[J];
+#pragma unroll
+    for (int j = 0; j < J; j++) {
+        const int e = lane + 32 * j;
+        q[j] = e < D ? __half2float(__ushort_as_half(p.q[b * p.qs[0] + draft * p.qs[1] + head * p.qs[2] + e])) : 0.f;
+    }
+    const uint16_t *K = p.k + b * p.ks[0] + h * p.ks[1], *V = p.v + b * p.vs[0] + h * p.vs[1];
+    int n = 0;
+    for (int w = 0; w < p.mask_words; w++) {
+        for (uint32_t m = seen_word(p, b, draft, w); m; m &= m - 1) {
+            const uint16_t *k = K + (32 * w + __ffs(m) - 1) * p.ks[2];
+            float s = 0.f;
+#pragma unroll
+            for (int j = 0; j < J; j++)
+                if (lane + 32 * j < D) s = fmaf(q[j], __half2float(__ushort_as_half(k[lane + 32 * j])), s);
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            s *= p.qk_scale;
+            if (lane == 0) draft_x[warp][n] = s;
+            M = fmaxf(M, s);
+            nan |= s != s;
+            n++;
+        }
+    }
+    __syncwarp();
+    if (M != -kInf) {
+        each([&](const float *rec, int kind) {
+            const float f = ex2(__ldcg(rec) - M);
+            L = fmaf(__ldcg(rec + 1), f, L);
+#pragma unroll
+            for (int j = 0; j < J; j++)
+                if (lane + 32 * j < D) {
+                    const float v = __ldcg(rec + 4 + lane + 32 * j);
+                    if (kind) a[1][j] = fmaf(f, v, a[1][j]);
+                    else a[0][j] = fmaf(f, v, a[0][j]);
+                }
+        });
+        n = 0;
+        for (int w = 0; w < p.mask_words; w++) {
+            for (uint32_t m = seen_word(p, b, draft, w); m; m &= m - 1) {
+                const uint16_t *v = V + (32 * w + __ffs(m) - 1) * p.vs[2];
+                const float f = ex2(draft_x[warp][n++] - M);
+                L += f;
+#pragma unroll
+                for (int j = 0; j < J; j++)
+                    if (lane + 32 * j < D) a[1][j] = fmaf(f, __half2float(__ushort_as_half(v[lane + 32 * j])), a[1][j]);
+            }
+        }
+    }
+    warp_rotate_strided<D>(a[0], p.sign_bits, p.inv_sqrt_d, lane);
+    const float inv = nan ? __int_as_float(0x7fffffff) : L == 0.f ? 0.f : 1.0f / L;  // nothing seen: zeros
+    uint16_t *out = p.out + ((static_cast<size_t>(b) * p.N + draft) * p.H * p.g + head) * D;
+#pragma unroll
+    for (int j = 0; j < J; j++)
+        if (lane + 32 * j < D) out[lane + 32 * j] = __half_as_ushort(__float2half_rn((a[0][j] + a[1][j]) * inv));
+}
+
+template <int D>
+cudaError_t tree_dim(const TreeParams &p, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(tree_plain_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(Plain<D>::smem));
+    if (e != cudaSuccess) return e;
+    tree_plain_kernel<D><<<p.workers, kTreeThreads, Plain<D>::smem, s>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const long long rows = static_cast<long long>(p.N) * p.g * p.B * p.H;
+    tree_merge_kernel<D><<<static_cast<unsigned>((rows + kTreeWarps - 1) / kTreeWarps), kTreeThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+TreeShape tree_shape(int B, int H, int g, int N, int d, long long tiles_per_head) {
+    TreeShape t;
+    t.R = d <= 256 ? 16 : 8;
+    t.n_rb = (N * g + t.R - 1) / t.R;
+    const long long tiles = static_cast<long long>(B) * H * t.n_rb * tiles_per_head;
+    t.workers = static_cast<int>(std::min<long long>(std::max<long long>(tiles, 1), static_cast<long long>(current_sm_count()) * 4));
+    return t;
+}
+
+cudaError_t launch_tree(const TreeParams &p, cudaStream_t s) {
+    switch (p.d) {
+        case 16: return tree_dim<16>(p, s);
+        case 32: return tree_dim<32>(p, s);
+        case 64: return tree_dim<64>(p, s);
+        case 128: return tree_dim<128>(p, s);
+        case 256: return tree_dim<256>(p, s);
+        case 512: return tree_dim<512>(p, s);
+        case 1024: return tree_dim<1024>(p, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace tqk

@@ -1,0 +1,160 @@
+// tq_tree.cuh -- the tile list of tree attention and the walk along it, shared
+// by its kernels (tq_serve.h describes the list, its parts and their records).
+#pragma once
+
+#include "tq_serve.h"
+
+namespace tqk {
+namespace tree {
+
+__device__ __forceinline__ int seg_tokens(const TreeParams &p, int i, int b) {
+    const TreeSeg &s = p.seg[i];
+    return s.len ? min(max(s.len[b], 0), s.n_tokens) : s.n_tokens;
+}
+
+// Tiles of sequence b's packed segments, and of its fp16 ones.
+__device__ __forceinline__ void seq_tiles(const TreeParams &p, int b, int &tp, int &tf) {
+    tp = 0;
+    tf = 0;
+    for (int i = 0; i < p.n_seg; i++) {
+        const int n = (seg_tokens(p, i, b) + kTreeTile - 1) / kTreeTile;
+        if (i < p.n_packed) tp += n;
+        else tf += n;
+    }
+}
+
+// Tiles of the whole call.  A warp takes 32 sequences at a time; all lanes
+// return the sum.
+__device__ __forceinline__ long long total_tiles(const TreeParams &p) {
+    const long long per = static_cast<long long>(p.H) * p.n_rb;
+    int tp, tf;
+    if (!p.ragged) {
+        seq_tiles(p, 0, tp, tf);
+        return per * p.B * (tp + tf);
+    }
+    long long sum = 0;
+    for (int b = threadIdx.x & 31; b < p.B; b += 32) {
+        seq_tiles(p, b, tp, tf);
+        sum += tp + tf;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return per * sum;
+}
+
+// Workers that share T tiles: every one of them has a tile (the launch is sized
+// for the segments' n_tokens, the lengths on the device may be shorter).
+__device__ __forceinline__ long long workers_of(const TreeParams &p, long long T) {
+    return T < p.workers ? T : p.workers;
+}
+
+struct Pos {
+    int b, h, rb;   // sequence, KV head, block of query rows
+    int k;          // tile of (b, h, rb)
+    int tp, tf;     // its packed tiles and the others
+};
+
+// The place of tile `at` < total_tiles in the list (whole warp, `at` uniform).
+__device__ __forceinline__ Pos seek(const TreeParams &p, long long at) {
+    Pos x;
+    const long long per = static_cast<long long>(p.H) * p.n_rb;
+    x.b = 0;
+    if (!p.ragged) {
+        seq_tiles(p, 0, x.tp, x.tf);
+        const long long each = per * (x.tp + x.tf);
+        x.b = static_cast<int>(at / each);
+        at -= x.b * each;
+    } else {
+        const int lane = threadIdx.x & 31;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            int tp = 0, tf = 0;
+            if (b0 + lane < p.B) seq_tiles(p, b0 + lane, tp, tf);
+            long long end = per * (tp + tf);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, end, o);
+                if (lane >= o) end += y;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, end > at);
+            const int l = past ? __ffs(past) - 1 : 31;
+            const long long upto = __shfl_sync(0xffffffffu, end, l);
+            x.b = b0 + l;
+            x.tp = __shfl_sync(0xffffffffu, tp, l);
+            x.tf = __shfl_sync(0xffffffffu, tf, l);
+            if (past) {
+                at -= upto - per * (x.tp + x.tf);
+                break;
+            }
+            at -= upto;
+        }
+    }
+    const long long tiles = x.tp + x.tf;
+    const int hr = static_cast<int>(at / tiles);
+    x.k = static_cast<int>(at - hr * tiles);
+    x.h = hr / p.n_rb;
+    x.rb = hr - x.h * p.n_rb;
+    return x;
+}
+
+__device__ __forceinline__ void advance(const TreeParams &p, Pos &x) {
+    if (++x.k < x.tp + x.tf) return;
+    x.k = 0;
+    if (++x.rb < p.n_rb) return;
+    x.rb = 0;
+    if (++x.h < p.H) return;
+    x.h = 0;
+    ++x.b;
+    if (p.ragged) {
+        for (; x.b < p.B; ++x.b) {
+            seq_tiles(p, x.b, x.tp, x.tf);
+            if (x.tp + x.tf > 0) break;
+        }
+    }
+}
+
+__device__ __forceinline__ long long group_of(const TreeParams &p, const Pos &x) {
+    return (static_cast<long long>(x.b) * p.H + x.h) * p.n_rb + x.rb;
+}
+
+// Index of the part that tile k of group `group` belongs to.
+__device__ __forceinline__ long long part_of(const TreeParams &p, long long group, int tp, int k) {
+    return group * p.parts + (k < tp ? k / kTreePart : p.parts_packed + (k - tp) / kTreePart);
+}
+
+// Worker of tile t when G workers share T tiles, worker c taking [c T / G, (c + 1) T / G).
+__device__ __forceinline__ long long worker_of(long long t, long long T, long long G) {
+    return ((t + 1) * G + T - 1) / T - 1;
+}
+
+// What a tile holds: tokens [t0, t0 + n) of segment `seg`.
+struct Tile {
+    int seg, t0, n;
+};
+__device__ __forceinline__ Tile tile_at(const TreeParams &p, const Pos &x) {
+    Tile r;
+    int k = x.k < x.tp ? x.k : x.k - x.tp;
+    const int lo = x.k < x.tp ? 0 : p.n_packed, hi = x.k < x.tp ? p.n_packed : p.n_seg;
+    for (r.seg = lo; r.seg < hi; r.seg++) {
+        const int n = seg_tokens(p, r.seg, x.b), tiles = (n + kTreeTile - 1) / kTreeTile;
+        if (k < tiles) {
+            r.t0 = k * kTreeTile;
+            r.n = min(kTreeTile, n - r.t0);
+            return r;
+        }
+        k -= tiles;
+    }
+    r.seg = lo;  // (not reached: k counts the tiles of these segments)
+    r.t0 = r.n = 0;
+    return r;
+}
+
+// Word w of the drafts that draft i of sequence b sees.
+__device__ __forceinline__ uint32_t seen_word(const TreeParams &p, int b, int i, int w) {
+    const int left = p.N - 32 * w;
+    const uint32_t real = left >= 32 ? 0xffffffffu : (1u << left) - 1u;  // bits behind the last draft mean nothing
+    if (p.mask) return p.mask[b * p.mask_stride + static_cast<int64_t>(i) * p.mask_words + w] & real;
+    return (i >= 32 * w + 31 ? 0xffffffffu : i < 32 * w ? 0u : (2u << (i - 32 * w)) - 1u) & real;
+}
+
+}  // namespace tree
+}  // namespace tqk

@@ -7,7 +7,9 @@ to load; there is no fallback path.
 
 Functions keep the C names: ``tq_make_rotation``, ``tq_fit_codebook``,
 ``tq_make_qjl``, ``tq_packed_size``, ``tq_compress``, ``tq_dequantize``,
-``tq_age_tiers``, ``tq_decode_workspace_size``, ``tq_decode_attention``.
+``tq_age_tiers``, ``tq_decode_workspace_size``, ``tq_decode_attention``, and
+the serving calls ``tq_rope_table``, ``tq_rope``, ``tq_append``, ``tq_read``,
+``tq_tree_workspace_size``, ``tq_tree_attention``.
 Errors come back as ``TQError`` carrying the status and its message.
 """
 from __future__ import annotations
@@ -51,7 +53,14 @@ EXPORTED = ["tq_status_string", "tq_last_cuda_error", "tq_version", "tq_make_rot
             "tq_age_tiers", "tq_decode_workspace_size", "tq_decode_attention",
             "tq_set_decode_kernel_events", "tq_decode_attention_static", "tq_decode_error_flag",
             "tq_requantize", "tq_fit_codebook_sphere", "tq_make_haar_rotation", "tq_compress_error_flag", "tq_decode_last_launches",
-            "tq_set_decode_wait_polls", "tq_value_code_table"]
+            "tq_set_decode_wait_polls", "tq_value_code_table", "tq_rope_frequencies", "tq_rope_table", "tq_rope",
+            "tq_append", "tq_read", "tq_tree_workspace_size", "tq_tree_attention"]
+
+TQ_DTYPE_F16, TQ_DTYPE_BF16, TQ_DTYPE_F32 = 0, 1, 2
+TQ_ROPE_SCALE_NONE, TQ_ROPE_SCALE_LINEAR, TQ_ROPE_SCALE_BASE, TQ_ROPE_SCALE_TURNS, TQ_ROPE_SCALE_INDEX = range(5)
+TQ_ROPE_HALF, TQ_ROPE_INTERLEAVED = 0, 1
+TQ_MAX_ROPE_TENSORS = 4
+TQ_MAX_DRAFTS = 256
 
 
 class TQError(RuntimeError):
@@ -98,8 +107,31 @@ class tq_layer_view(ctypes.Structure):
                 ("seg", tq_segment * TQ_MAX_SEGMENTS), ("qjl_estimator", ctypes.c_int)]
 
 
+class tq_rope_spec(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("scaling", ctypes.c_int)] + [
+        (n, ctypes.c_double) for n in ("base", "factor", "original_len", "fast", "slow", "amplitude")]
+
+
+class tq_rope_view(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int), ("n_pos", ctypes.c_int),
+                ("table", ctypes.c_void_p)]
+
+
+class tq_rope_tensor(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n_heads", ctypes.c_int),
+                ("in_stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3)]
+
+
+class tq_tree(ctypes.Structure):
+    _fields_ = [("n_drafts", ctypes.c_int), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+                ("mask", ctypes.c_void_p), ("mask_stride_b", ctypes.c_int64),
+                ("seg_len", ctypes.c_void_p * TQ_MAX_SEGMENTS), ("out", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 _lib.tq_status_string.restype = ctypes.c_char_p
 _lib.tq_status_string.argtypes = [_I]
 _lib.tq_last_cuda_error.restype = _I
@@ -131,6 +163,17 @@ _lib.tq_decode_error_flag.argtypes = [_P, ctypes.POINTER(ctypes.c_int), _P]
 _lib.tq_set_decode_wait_polls.argtypes = [_I]
 _lib.tq_decode_attention_static.argtypes = [ctypes.POINTER(tq_layer_view), _I, _I, _I, _I, _I, _P, _I, _P,
                                             _P, _P]
+_lib.tq_rope_frequencies.argtypes = [ctypes.POINTER(tq_rope_spec), _P]
+_lib.tq_rope_table.argtypes = [ctypes.POINTER(tq_rope_spec), _I, _I, _P, _P]
+_lib.tq_rope.argtypes = [ctypes.POINTER(tq_rope_view), _I, _I, _I, _I, _P, _L, ctypes.POINTER(tq_rope_tensor), _I, _I,
+                         _P]
+_lib.tq_append.argtypes = [ctypes.POINTER(tq_segment), ctypes.POINTER(tq_rotation), ctypes.POINTER(tq_rope_view), _P, _L,
+                           _P, _P, _P, _P, _I, _I, _P, _P, _P, _L, _P]
+_lib.tq_read.argtypes = [ctypes.POINTER(tq_segment), ctypes.POINTER(tq_rotation), _I, _P, _P, _I, _P, _P, _P, _P, _P]
+_lib.tq_tree_workspace_size.argtypes = [ctypes.POINTER(tq_layer_view), _I, _I, _I, _I, _I,
+                                        ctypes.POINTER(ctypes.c_size_t)]
+_lib.tq_tree_attention.argtypes = [ctypes.POINTER(tq_layer_view), _I, _I, _I, _I, ctypes.POINTER(tq_tree), _P,
+                                   ctypes.c_size_t, _P]
 TQ_STATIC_WORKSPACE_BYTES = 16 << 20
 for _n in EXPORTED:
     if _n not in ("tq_status_string", "tq_last_cuda_error", "tq_version", "tq_decode_last_launches"):
@@ -443,3 +486,238 @@ def tq_set_decode_wait_polls(polls: int):
 def views_array(layers):
     """Prebuilt ctypes array of layer views (reuse across calls to skip marshalling)."""
     return _views(layers)
+
+
+# ----------------------------------------------------------------- serving
+_DTYPE = {torch.float16: TQ_DTYPE_F16, torch.bfloat16: TQ_DTYPE_BF16, torch.float32: TQ_DTYPE_F32}
+
+
+def _require(ok: bool, where: str):
+    if not ok:
+        raise TQError(-1, where)
+
+
+def _int32(t, where, *shape):
+    """Checks an int32 CUDA tensor of `shape` with unit stride in its last axis
+    (None: not given)."""
+    if t is not None:
+        _require(t.dtype == torch.int32 and tuple(t.shape) == shape and (shape[-1] <= 1 or t.stride(-1) == 1), where)
+
+
+def _same_device(where, *tensors):
+    devices = {t.device for t in tensors if t is not None}
+    _require(len(devices) == 1, where)
+    return devices.pop()
+
+
+def _call(device, stream, where, fn):
+    """fn(stream) with `device` current (the library works on the current
+    device), on the given stream or the device's current one."""
+    if device.type != "cuda":
+        raise TQError(-1, where)
+    if device.index == torch.cuda.current_device():
+        _check(fn(_stream(stream)), where)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(_stream(stream)), where)
+
+
+def _strides(t, axes=(0, 1, 2)):
+    return (_L * 3)(*(t.stride(a) for a in axes))
+
+
+def tq_make_rope(rotary_dim: int, base: float = 10000.0, scaling: int = TQ_ROPE_SCALE_NONE, factor: float = 1.0,
+                 original_len: float = 0.0, fast: float = 0.0, slow: float = 0.0,
+                 amplitude: float = 1.0) -> tq_rope_spec:
+    """Frequencies of rotary positions (see include/tq.h for the scalings)."""
+    s = tq_rope_spec(rotary_dim, scaling, base, factor, original_len, fast, slow, amplitude)
+    tq_rope_frequencies(s)  # argument errors here
+    return s
+
+
+def tq_rope_frequencies(spec: tq_rope_spec) -> np.ndarray:
+    """The pairs' frequencies, binary64."""
+    out = np.zeros(max(spec.rotary_dim // 2, 1))
+    _check(_lib.tq_rope_frequencies(ctypes.byref(spec), out.ctypes.data), "tq_rope_frequencies")
+    return out
+
+
+def tq_rope_table(spec: tq_rope_spec, n_pos: int, first_pos: int = 0, device="cuda", stream=None) -> torch.Tensor:
+    """float32 CUDA table [n_pos][2][rotary_dim / 2] of cosines and sines."""
+    _require(n_pos >= 0, "tq_rope_table")
+    t = torch.empty(n_pos, 2, spec.rotary_dim // 2, dtype=torch.float32, device=device)
+    _call(t.device, stream, "tq_rope_table",
+          lambda s: _lib.tq_rope_table(ctypes.byref(spec), first_pos, n_pos, _ptr(t), s))
+    return t
+
+
+class Rope:
+    """A table of cosines and sines [n_pos][2][rotary_dim / 2] (float32 CUDA,
+    contiguous; tq_rope_table or the caller's own) and the layout of the pairs."""
+
+    def __init__(self, table: torch.Tensor, layout: int = TQ_ROPE_HALF):
+        _require(table.dtype == torch.float32 and table.dim() == 3 and table.shape[1] == 2 and table.is_contiguous(),
+                 "Rope")
+        _require(layout in (TQ_ROPE_HALF, TQ_ROPE_INTERLEAVED), "Rope")
+        self.table, self.layout = table, layout
+        self.view = tq_rope_view(2 * table.shape[2], layout, table.shape[0], _ptr(table))
+
+
+def tq_rope(rope: Rope, positions: torch.Tensor, x, out=None, inverse: bool = False, stream=None):
+    """Rotary positions of x (a CUDA tensor [B][H][T][d] of any strides with unit
+    stride in d, or a list of up to four of the same B, T, d and type: queries
+    and keys) into `out` (likewise; None: in place).  positions: int32 [B][T] or
+    [T].  inverse: the transpose (the gradient of x)."""
+    xs = [x] if isinstance(x, torch.Tensor) else list(x)
+    outs = xs if out is None else ([out] if isinstance(out, torch.Tensor) else list(out))
+    _require(1 <= len(xs) <= TQ_MAX_ROPE_TENSORS and len(xs) == len(outs), "tq_rope")
+    B, _, T, d = xs[0].shape
+    arr = (tq_rope_tensor * len(xs))()
+    for a, i, o in zip(arr, xs, outs):
+        _require(i.dim() == 4 and i.shape == o.shape and (i.shape[0], i.shape[2], i.shape[3]) == (B, T, d) and
+                 i.dtype == o.dtype == xs[0].dtype and i.dtype in _DTYPE and
+                 (d == 1 or i.stride(3) == o.stride(3) == 1), "tq_rope")
+        a.in_, a.out, a.n_heads = _ptr(i), _ptr(o), i.shape[1]
+        a.in_stride, a.out_stride = _strides(i), _strides(o)
+    if positions.dim() == 1:
+        _int32(positions, "tq_rope", T)
+        ps = 0
+    else:
+        _int32(positions, "tq_rope", B, T)
+        ps = positions.stride(0)
+    dev = _same_device("tq_rope", rope.table, positions, *xs, *outs)
+    _call(dev, stream, "tq_rope",
+          lambda s: _lib.tq_rope(ctypes.byref(rope.view), _DTYPE[xs[0].dtype], B, T, d, _ptr(positions), ps, arr,
+                                 len(xs), int(inverse), s))
+    return outs[0] if isinstance(x, torch.Tensor) else outs
+
+
+def tq_append(seg, rot: tq_rotation | None, K: torch.Tensor, V: torch.Tensor, t_begin: torch.Tensor, n_new=None,
+              index=None, n_max: int | None = None, rope: Rope | None = None, positions=None, stream=None):
+    """Write rows of K, V (fp16 CUDA [B][H][S][d], unit stride in d) into `seg`
+    (PackedSegment or Fp16Segment) at each sequence's own position: row j <
+    min(n_new[b], n_max) of sequence b is source row index[b][j] (None: j) and
+    goes to position t_begin[b] + j.  t_begin, n_new: int32 [B]; index: int32
+    [B][n_max]; n_max: default the index's width, else S.  rope: rotates the keys
+    by positions (int32 [B][S] or [S]) first.  Rows outside the source or the
+    segment are skipped.  seg.n_tokens is left to the caller."""
+    where = "tq_append"
+    L = seg.layout
+    _require(K.dim() == 4 and K.shape == V.shape and K.dtype == V.dtype == torch.float16 and K.stride(3) == 1 and
+             V.stride(3) == 1 and (K.shape[0], K.shape[1], K.shape[3]) == (L.batch, L.n_heads, L.head_dim), where)
+    B, _, S, _ = K.shape
+    if n_max is None:
+        n_max = index.shape[1] if index is not None else S
+    _int32(t_begin, where, B)
+    _int32(n_new, where, B)
+    if index is not None:
+        _require(index.dim() == 2 and index.shape[1] >= n_max, where)
+        _int32(index, where, B, index.shape[1])
+    ps = 0
+    if rope is not None:
+        _require(positions is not None, where)
+        _int32(positions, where, *((S,) if positions.dim() == 1 else (B, S)))
+        ps = positions.stride(0) if positions.dim() == 2 else 0
+    own = seg.kcodes if seg.kind == TQ_SEG_PACKED else seg.k
+    dev = _same_device(where, own, K, V, t_begin, n_new, index, rope.table if rope else None,
+                       positions if rope else None)
+    sg = seg.segment()
+    _call(dev, stream, where,
+          lambda s: _lib.tq_append(ctypes.byref(sg), ctypes.byref(rot) if rot is not None else None,
+                                   ctypes.byref(rope.view) if rope is not None else None,
+                                   _ptr(positions) if rope is not None else None, ps, _ptr(K), _strides(K), _ptr(V),
+                                   _strides(V), S, n_max, _ptr(t_begin), _ptr(n_new), _ptr(index),
+                                   index.stride(0) if index is not None else 0, s))
+
+
+def tq_read(seg, rot: tq_rotation | None, t_begin: torch.Tensor, n_max: int, n_read=None, out=None,
+            dtype=torch.float16, stream=None):
+    """Rows of `seg` (PackedSegment or Fp16Segment) back as vectors: row j <
+    min(n_read[b], n_max) of sequence b is position t_begin[b] + j (int32 [B]
+    tensors).  out: [k, v] tensors [B][H][n_max][d] of fp16, bf16 or fp32 (any
+    strides with unit stride in d, None entries: not wanted), default new ones of
+    `dtype`, zero where nothing is read.  rot None: rotated-space vectors."""
+    where = "tq_read"
+    L = seg.layout
+    shape = (L.batch, L.n_heads, n_max, L.head_dim)
+    own = seg.kcodes if seg.kind == TQ_SEG_PACKED else seg.k
+    if out is None:
+        _require(n_max >= 0, where)
+        out = [torch.zeros(shape, dtype=dtype, device=own.device) for _ in range(2)]
+    k, v = out
+    some = [t for t in (k, v) if t is not None]
+    for t in some:
+        _require(tuple(t.shape) == shape and t.dtype == some[0].dtype and t.dtype in _DTYPE and t.stride(3) == 1, where)
+    _int32(t_begin, where, L.batch)
+    _int32(n_read, where, L.batch)
+    if some:
+        dev = _same_device(where, own, t_begin, n_read, *some)
+        sg = seg.segment()
+        _call(dev, stream, where,
+              lambda s: _lib.tq_read(ctypes.byref(sg), ctypes.byref(rot) if rot is not None else None, n_max,
+                                     _ptr(t_begin), _ptr(n_read), _DTYPE[some[0].dtype], _ptr(k),
+                                     _strides(k) if k is not None else None, _ptr(v),
+                                     _strides(v) if v is not None else None, s))
+    return out
+
+
+def tree_mask(parents: torch.Tensor) -> torch.Tensor:
+    """Visibility words of draft trees: parents int [B][N] (or [N]), the index of
+    each draft's parent (before it) or -1 at a root; a draft sees itself and its
+    ancestors.  int32 [B][N][ceil(N / 32)] (or without B), as tq_tree_attention
+    takes it, on the parents' device."""
+    p = parents if parents.dim() == 2 else parents[None]
+    B, N = p.shape
+    W = -(-N // 32)
+    i = torch.arange(N, device=p.device)
+    see = torch.zeros(B, N, W * 32, dtype=torch.bool, device=p.device)
+    at = i.expand(B, N).long()
+    for _ in range(N):  # one generation a step
+        see.scatter_(2, at.clamp(min=0)[..., None], (at >= 0)[..., None] | see.gather(2, at.clamp(min=0)[..., None]))
+        at = torch.where(at >= 0, p.long().gather(1, at.clamp(min=0)), at)
+    w = (see.view(B, N, W, 32).long() << torch.arange(32, device=p.device)).sum(-1)
+    w = torch.where(w >= 1 << 31, w - (1 << 32), w).int()
+    return w if parents.dim() == 2 else w[0]
+
+
+def tq_tree_workspace_size(view: tq_layer_view, batch: int, n_heads: int, q_heads: int, n_drafts: int,
+                           head_dim: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.tq_tree_workspace_size(ctypes.byref(view), batch, n_heads, q_heads, head_dim, n_drafts,
+                                       ctypes.byref(n)), "tq_tree_workspace_size")
+    return n.value
+
+
+def tq_tree_attention(view: tq_layer_view, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                      workspace: torch.Tensor, mask: torch.Tensor | None = None, seg_len=None, stream=None):
+    """out[b][i][j] = attention of drafted token i, query head j over the cache
+    `view` and the drafts it sees.  q fp16 [B][N][Hq][d], k, v fp16 [B][H][N][d]
+    (any strides with unit stride in d), out fp16 [B][N][Hq][d] contiguous.  mask:
+    int32 words [B][N][ceil(N / 32)] or [N][...] (tree_mask), None: a chain.
+    seg_len: one int32 [B] tensor (or None) per segment of the view: the tokens
+    each sequence holds of it."""
+    where = "tq_tree_attention"
+    _require(q.dim() == 4 and k.dim() == 4 and k.shape == v.shape, where)
+    B, N, Hq, d = q.shape
+    H = k.shape[1]
+    _require(tuple(k.shape) == (B, H, N, d) and q.dtype == k.dtype == v.dtype == out.dtype == torch.float16 and
+             tuple(out.shape) == (B, N, Hq, d) and out.is_contiguous() and workspace.is_contiguous() and
+             q.stride(3) == k.stride(3) == v.stride(3) == 1, where)
+    t = tq_tree()
+    t.n_drafts, t.q, t.k, t.v, t.out = N, _ptr(q), _ptr(k), _ptr(v), _ptr(out)
+    t.q_stride, t.k_stride, t.v_stride = _strides(q), _strides(k), _strides(v)
+    if mask is not None:
+        W = -(-N // 32)
+        _require(mask.dtype == torch.int32 and mask.is_contiguous() and tuple(mask.shape) in ((N, W), (B, N, W)), where)
+        t.mask = _ptr(mask)
+        t.mask_stride_b = N * W if mask.dim() == 3 else 0
+    lens = [] if seg_len is None else list(seg_len)
+    _require(len(lens) in (0, view.n_segments), where)
+    for i, n in enumerate(lens):
+        _int32(n, where, B)
+        t.seg_len[i] = _ptr(n)
+    dev = _same_device(where, q, k, v, out, workspace, mask, *lens)
+    _call(dev, stream, where,
+          lambda s: _lib.tq_tree_attention(ctypes.byref(view), B, H, Hq, d, ctypes.byref(t), _ptr(workspace),
+                                           workspace.numel() * workspace.element_size(), s))
+    return out
