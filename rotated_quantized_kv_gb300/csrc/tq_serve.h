@@ -128,6 +128,14 @@ struct TreeParams {
 struct TreeShape {
     int R, n_rb, workers;
 };
+// Value levels of the tensor-core form: fp16(s c_k) by law, flat by width, and 1/s.
+struct TreeLevels {
+    uint16_t half[2][kCbTotal];
+    float inv[2][9];
+};
+// Whether a head dimension takes the tensor-core form (64 and 128).
+inline bool tree_on_tensor_cores(int d) { return d == 64 || d == 128; }
+cudaError_t launch_tree_mma(const TreeParams &p, cudaStream_t s);
 TreeShape tree_shape(int B, int H, int g, int N, int d, long long tiles_per_head);
 cudaError_t launch_tree(const TreeParams &p, cudaStream_t s);
 

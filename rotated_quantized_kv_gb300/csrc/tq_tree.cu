@@ -292,12 +292,18 @@ __global__ void __launch_bounds__(kTreeThreads) tree_merge_kernel(const __grid_c
 
 template <int D>
 cudaError_t tree_dim(const TreeParams &p, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(tree_plain_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(Plain<D>::smem));
-    if (e != cudaSuccess) return e;
-    tree_plain_kernel<D><<<p.workers, kTreeThreads, Plain<D>::smem, s>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
+    if constexpr (D == 64 || D == 128) {
+        e = launch_tree_mma(p, s);
+        if (e != cudaSuccess) return e;
+    } else {
+        e = cudaFuncSetAttribute(tree_plain_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(Plain<D>::smem));
+        if (e != cudaSuccess) return e;
+        tree_plain_kernel<D><<<p.workers, kTreeThreads, Plain<D>::smem, s>>>(p);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
     const long long rows = static_cast<long long>(p.N) * p.g * p.B * p.H;
     tree_merge_kernel<D><<<static_cast<unsigned>((rows + kTreeWarps - 1) / kTreeWarps), kTreeThreads, 0, s>>>(p);
     return cudaGetLastError();
@@ -307,10 +313,15 @@ cudaError_t tree_dim(const TreeParams &p, cudaStream_t s) {
 
 TreeShape tree_shape(int B, int H, int g, int N, int d, long long tiles_per_head) {
     TreeShape t;
-    t.R = d <= 256 ? 16 : 8;
-    t.n_rb = (N * g + t.R - 1) / t.R;
+    const int rows = N * g;
+    // tensor cores: the least power of two that holds the rows, up to 64 (a block's
+    // columns), one CTA per SM
+    if (tree_on_tensor_cores(d)) t.R = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    else t.R = d <= 256 ? 16 : 8;
+    t.n_rb = (rows + t.R - 1) / t.R;
     const long long tiles = static_cast<long long>(B) * H * t.n_rb * tiles_per_head;
-    t.workers = static_cast<int>(std::min<long long>(std::max<long long>(tiles, 1), static_cast<long long>(current_sm_count()) * 4));
+    const long long ctas = static_cast<long long>(current_sm_count()) * (tree_on_tensor_cores(d) ? 1 : 4);
+    t.workers = static_cast<int>(std::min<long long>(std::max<long long>(tiles, 1), ctas));
     return t;
 }
 
