@@ -42,9 +42,10 @@ struct Plain {
     static constexpr size_t smem = (2 * R * LD + TT * LD + R * TT + 3 * R) * sizeof(float);
 };
 
-// One row of K or V (element e of token t) in binary32, rotated space for packed ones.
+// Element e of token t of K or V in binary32, rotated space for packed segments.
 template <int D>
-__device__ __forceinline__ float tile_value(const TreeParams &p, const Pos &x, const Tile &w, int kv, int t, int e) {
+__device__ __forceinline__ float tile_value(const TreeParams &p, const Walk &w, int kv, int t, int e) {
+    const Pos &x = w.x;
     const SegView &s = p.seg[w.seg].seg;
     const uint8_t *base = (kv ? s.v : s.k) + x.b * (kv ? s.vblock : s.kblock) + (kv ? s.voff[x.h] : s.koff[x.h]);
     if (s.fp16) return __half2float(reinterpret_cast<const __half *>(base)[static_cast<size_t>(t) * D + e]);
@@ -68,9 +69,9 @@ __global__ void __launch_bounds__(kTreeThreads) tree_plain_kernel(const __grid_c
     if (c >= G) return;
     long long at = c * T / G;
     const long long end = (c + 1) * T / G;
-    Pos x = seek(p, at);
+    Walk w = walk_begin(p, at);
     float acc[R][DPT];
-    long long group = -1, part = -1;
+    int part = -1;
     auto restart = [&] {
         __syncthreads();
         for (int r = threadIdx.x; r < R; r += kTreeThreads) row_m[r] = -kInf, row_l[r] = 0.f;
@@ -95,15 +96,14 @@ __global__ void __launch_bounds__(kTreeThreads) tree_plain_kernel(const __grid_c
                 if (i < D) rec[r * (D + 4) + 4 + i] = acc[r][e];
             }
     };
-    for (; at < end; at++, advance(p, x)) {
-        const long long g = group_of(p, x), pt = part_of(p, g, x.tp, x.k);
-        if (pt != part) {
+    for (; at < end; at++, walk_next(p, w)) {
+        const Pos &x = w.x;
+        if (w.first) {
             if (part >= 0) flush();
-            part = pt;
+            part = w.part;
             restart();
         }
-        if (g != group) {  // the block's query rows, as they are and rotated
-            group = g;
+        if (w.fresh) {  // the block's query rows, as they are and rotated
             __syncthreads();
             for (int r = warp; r < R; r += kTreeWarps) {
                 const int row = x.rb * R + r;
@@ -123,13 +123,13 @@ __global__ void __launch_bounds__(kTreeThreads) tree_plain_kernel(const __grid_c
                     if (lane + 32 * j < D) q1[r * LD + lane + 32 * j] = v[j];
             }
         }
-        const Tile w = tile_at(p, x);
         const float *q = x.k < x.tp ? q1 : q0;
-        for (int t0 = 0; t0 < w.n; t0 += TT) {
-            const int nt = min(TT, w.n - t0);
+        const int hi = min(w.n, (w.t + 1) * kTreeTile);
+        for (int t0 = w.t * kTreeTile; t0 < hi; t0 += TT) {
+            const int nt = min(TT, hi - t0);
             __syncthreads();
             for (int i = threadIdx.x; i < nt * D; i += kTreeThreads)
-                tok[(i / D) * LD + i % D] = tile_value<D>(p, x, w, 0, w.t0 + t0 + i / D, i % D);
+                tok[(i / D) * LD + i % D] = tile_value<D>(p, w, 0, t0 + i / D, i % D);
             __syncthreads();
             for (int i = threadIdx.x; i < R * TT; i += kTreeThreads) {
                 const int r = i / TT, t = i % TT;
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_plain_kernel(const __grid_c
                 if (lane == 0) row_m[r] = now, row_l[r] = row_l[r] * f + l, row_c[r] = f;
             }
             for (int i = threadIdx.x; i < nt * D; i += kTreeThreads)
-                tok[(i / D) * LD + i % D] = tile_value<D>(p, x, w, 1, w.t0 + t0 + i / D, i % D);
+                tok[(i / D) * LD + i % D] = tile_value<D>(p, w, 1, t0 + i / D, i % D);
             __syncthreads();
 #pragma unroll
             for (int e = 0; e < DPT; e++) {
@@ -187,6 +187,7 @@ template <int D>
 __global__ void __launch_bounds__(kTreeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p) {
     constexpr int J = (D + 31) / 32;
     __shared__ float draft_x[kTreeWarps][TQ_MAX_DRAFTS];
+    constexpr int U = J <= 4 ? 8 : 32 / J, F = J <= 4 ? 4 : J <= 16 ? 16 / J : 1;  // records and drafts in flight
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long rows = static_cast<long long>(p.N) * p.g;
     const long long id = blockIdx.x * static_cast<long long>(kTreeWarps) + warp;  // (b, h, row)
@@ -213,26 +214,24 @@ __global__ void __launch_bounds__(kTreeThreads) tree_merge_kernel(const __grid_c
     const long long group = (static_cast<long long>(b) * p.H + h) * p.n_rb + rb;
     const int np = (tp + kTreePart - 1) / kTreePart, nf = (tf + kTreePart - 1) / kTreePart;
     float M = -kInf, L = 0.f, a[2][J];
+    bool nan = false;  // fmaxf passes over NaN: a row that sees only NaN scores is NaN, not empty
 #pragma unroll
     for (int j = 0; j < J; j++) a[0][j] = a[1][j] = 0.f;
-    // records of part i (packed ones, then the others): workers [lo, hi]
-    auto each = [&](auto &&f) {
-        for (int i = 0; i < np + nf; i++) {
-            const int k0 = i < np ? i * kTreePart : tp + (i - np) * kTreePart;
-            const int k1 = min(k0 + kTreePart, i < np ? tp : tp + tf);
-            const long long lo = worker_of(first + k0, T, G), hi = worker_of(first + k1 - 1, T, G);
-            const long long slot = part_of(p, group, tp, k0);
-            for (long long w = lo; w <= hi; w++)
-                f(p.part + (static_cast<size_t>(w + slot) * p.R + r) * (D + 4), i < np ? 0 : 1);
-        }
+    // part i (packed ones, then the others): workers lo..hi hold its records
+    struct Part {
+        long long lo, hi, slot;
     };
-    bool nan = false;  // fmaxf passes over NaN: a row that sees only NaN scores is NaN, not empty
-    each([&](const float *rec, int) {
-        const float l = __ldcg(rec + 1);
-        M = fmaxf(M, __ldcg(rec));
-        nan |= l != l;
-    });
-    // scores of the drafts that the row sees, one after the other
+    auto part_at = [&](int i) {
+        const int k0 = i < np ? i * kTreePart : tp + (i - np) * kTreePart;
+        const int k1 = min(k0 + kTreePart, i < np ? tp : tp + tf);
+        Part q;
+        q.lo = worker_of(first + k0, T, G);
+        q.hi = worker_of(first + k1 - 1, T, G);
+        q.slot = part_of(p, group, tp, k0);
+        return q;
+    };
+    auto record = [&](const Part &q, long long w) { return p.part + (static_cast<size_t>(w + q.slot) * p.R + r) * (D + 4); };
+    // scores of the drafts that the row sees, each over the whole warp
     float q[J];
 #pragma unroll
     for (int j = 0; j < J; j++) {
@@ -242,43 +241,101 @@ __global__ void __launch_bounds__(kTreeThreads) tree_merge_kernel(const __grid_c
     const uint16_t *K = p.k + b * p.ks[0] + h * p.ks[1], *V = p.v + b * p.vs[0] + h * p.vs[1];
     int n = 0;
     for (int w = 0; w < p.mask_words; w++) {
-        for (uint32_t m = seen_word(p, b, draft, w); m; m &= m - 1) {
-            const uint16_t *k = K + (32 * w + __ffs(m) - 1) * p.ks[2];
-            float s = 0.f;
+        for (uint32_t m = seen_word(p, b, draft, w); m;) {
+            const int some = min(__popc(m), F);
+            float s[F];
 #pragma unroll
-            for (int j = 0; j < J; j++)
-                if (lane + 32 * j < D) s = fmaf(q[j], __half2float(__ushort_as_half(k[lane + 32 * j])), s);
+            for (int i = 0; i < F; i++) {
+                s[i] = 0.f;
+                if (i < some) {
+                    const uint16_t *k = K + (32 * w + __ffs(m) - 1) * p.ks[2];
+                    m &= m - 1;
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            s *= p.qk_scale;
-            if (lane == 0) draft_x[warp][n] = s;
-            M = fmaxf(M, s);
-            nan |= s != s;
-            n++;
+                    for (int j = 0; j < J; j++)
+                        if (lane + 32 * j < D) s[i] = fmaf(q[j], __half2float(__ushort_as_half(__ldg(k + lane + 32 * j))), s[i]);
+                }
+            }
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < F; i++) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+#pragma unroll
+            for (int i = 0; i < F; i++)
+                if (i < some) {
+                    s[i] *= p.qk_scale;
+                    if (lane == 0) draft_x[warp][n + i] = s[i];
+                    M = fmaxf(M, s[i]);
+                    nan |= s[i] != s[i];
+                }
+            n += some;
         }
     }
     __syncwarp();
-    if (M != -kInf) {
-        each([&](const float *rec, int kind) {
-            const float f = ex2(__ldcg(rec) - M);
-            L = fmaf(__ldcg(rec + 1), f, L);
+    // the largest of the records' maxima, a record per lane
+    for (int i = 0; i < np + nf; i++) {
+        const Part pt = part_at(i);
+        for (long long w = pt.lo + lane; w <= pt.hi; w += 32) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(record(pt, w)));
+            M = fmaxf(M, ml.x);
+            nan |= ml.y != ml.y;
+        }
+    }
 #pragma unroll
-            for (int j = 0; j < J; j++)
-                if (lane + 32 * j < D) {
-                    const float v = __ldcg(rec + 4 + lane + 32 * j);
-                    if (kind) a[1][j] = fmaf(f, v, a[1][j]);
-                    else a[0][j] = fmaf(f, v, a[0][j]);
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    nan = __any_sync(0xffffffffu, nan);
+    if (M != -kInf) {
+        for (int i = 0; i < np + nf; i++) {
+            const Part pt = part_at(i);
+            const int kind = i < np ? 0 : 1;
+            for (long long w0 = pt.lo; w0 <= pt.hi; w0 += U) {  // U records' loads in flight
+                const int cnt = static_cast<int>(min(static_cast<long long>(U), pt.hi - w0 + 1));
+                float2 ml = make_float2(-kInf, 0.f);
+                if (lane < cnt) ml = __ldcg(reinterpret_cast<const float2 *>(record(pt, w0 + lane)));
+                float v[U][J];
+#pragma unroll
+                for (int u = 0; u < U; u++)
+#pragma unroll
+                    for (int j = 0; j < J; j++)
+                        v[u][j] = u < cnt && lane + 32 * j < D ? __ldcg(record(pt, w0 + u) + 4 + lane + 32 * j) : 0.f;
+                const float f = ex2(ml.x - M);
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    const float fu = __shfl_sync(0xffffffffu, f, u);
+                    L = fmaf(__shfl_sync(0xffffffffu, ml.y, u), fu, L);
+#pragma unroll
+                    for (int j = 0; j < J; j++) {
+                        if (kind) a[1][j] = fmaf(fu, v[u][j], a[1][j]);
+                        else a[0][j] = fmaf(fu, v[u][j], a[0][j]);
+                    }
                 }
-        });
+            }
+        }
         n = 0;
         for (int w = 0; w < p.mask_words; w++) {
-            for (uint32_t m = seen_word(p, b, draft, w); m; m &= m - 1) {
-                const uint16_t *v = V + (32 * w + __ffs(m) - 1) * p.vs[2];
-                const float f = ex2(draft_x[warp][n++] - M);
-                L += f;
+            for (uint32_t m = seen_word(p, b, draft, w); m;) {
+                const int some = min(__popc(m), F);
+                float v[F][J], f[F];
 #pragma unroll
-                for (int j = 0; j < J; j++)
-                    if (lane + 32 * j < D) a[1][j] = fmaf(f, __half2float(__ushort_as_half(v[lane + 32 * j])), a[1][j]);
+                for (int i = 0; i < F; i++) {
+                    f[i] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < J; j++) v[i][j] = 0.f;
+                    if (i < some) {
+                        const uint16_t *at = V + (32 * w + __ffs(m) - 1) * p.vs[2];
+                        m &= m - 1;
+                        f[i] = ex2(draft_x[warp][n + i] - M);
+#pragma unroll
+                        for (int j = 0; j < J; j++)
+                            if (lane + 32 * j < D) v[i][j] = __half2float(__ushort_as_half(__ldg(at + lane + 32 * j)));
+                    }
+                }
+                n += some;
+#pragma unroll
+                for (int i = 0; i < F; i++) {
+                    L += f[i];
+#pragma unroll
+                    for (int j = 0; j < J; j++) a[1][j] = fmaf(f[i], v[i][j], a[1][j]);
+                }
             }
         }
     }

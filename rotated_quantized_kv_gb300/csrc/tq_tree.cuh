@@ -126,26 +126,53 @@ __device__ __forceinline__ long long worker_of(long long t, long long T, long lo
     return ((t + 1) * G + T - 1) / T - 1;
 }
 
-// What a tile holds: tokens [t0, t0 + n) of segment `seg`.
-struct Tile {
-    int seg, t0, n;
+// A walk along the list: the current tile holds tokens [128 t, min(128 (t + 1), n))
+// of segment `seg`, tile k of its (b, h, rb), and belongs to part `part`.
+struct Walk {
+    Pos x;
+    int seg, t, tiles, n;  // tiles, n: of the segment, for sequence b
+    int part;
+    bool fresh;            // first tile of its (group, segment)
+    bool first;            // first tile of its part
 };
-__device__ __forceinline__ Tile tile_at(const TreeParams &p, const Pos &x) {
-    Tile r;
-    int k = x.k < x.tp ? x.k : x.k - x.tp;
-    const int lo = x.k < x.tp ? 0 : p.n_packed, hi = x.k < x.tp ? p.n_packed : p.n_seg;
-    for (r.seg = lo; r.seg < hi; r.seg++) {
-        const int n = seg_tokens(p, r.seg, x.b), tiles = (n + kTreeTile - 1) / kTreeTile;
-        if (k < tiles) {
-            r.t0 = k * kTreeTile;
-            r.n = min(kTreeTile, n - r.t0);
-            return r;
-        }
-        k -= tiles;
+
+// Segment and part of tile w.x.k.
+__device__ __forceinline__ void walk_locate(const TreeParams &p, Walk &w) {
+    const bool packed = w.x.k < w.x.tp;
+    int k = packed ? w.x.k : w.x.k - w.x.tp;
+    w.part = static_cast<int>(part_of(p, group_of(p, w.x), w.x.tp, w.x.k));
+    w.seg = packed ? 0 : p.n_packed;
+    for (;; w.seg++) {  // (ends: k counts the tiles of these segments)
+        w.n = seg_tokens(p, w.seg, w.x.b);
+        w.tiles = (w.n + kTreeTile - 1) / kTreeTile;
+        if (k < w.tiles || w.seg + 1 >= p.n_seg) break;
+        k -= w.tiles;
     }
-    r.seg = lo;  // (not reached: k counts the tiles of these segments)
-    r.t0 = r.n = 0;
-    return r;
+    w.t = k;
+    w.fresh = true;
+}
+__device__ __forceinline__ Walk walk_begin(const TreeParams &p, long long at) {
+    Walk w;
+    w.x = seek(p, at);
+    walk_locate(p, w);
+    w.first = true;
+    return w;
+}
+__device__ __forceinline__ void walk_next(const TreeParams &p, Walk &w) {
+    if (w.t + 1 < w.tiles) {
+        w.t++;
+        w.x.k++;
+        const int k = w.x.k < w.x.tp ? w.x.k : w.x.k - w.x.tp;
+        w.first = k % kTreePart == 0;
+        w.part += w.first;
+        w.fresh = false;
+        return;
+    }
+    advance(p, w.x);
+    if (w.x.b >= p.B) return;  // behind the last tile
+    const int part = w.part;
+    walk_locate(p, w);
+    w.first = w.part != part;
 }
 
 // Word w of the drafts that draft i of sequence b sees.

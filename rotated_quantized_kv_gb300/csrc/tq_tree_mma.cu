@@ -29,8 +29,9 @@
 // V^T needs the dims on the lanes, so V goes through shared memory with tokens
 // as the K dimension (MN-major operand).
 //
-// Roles (18 warps): 0-7 softmax (two groups of four warps, half the rows each),
-// 8-11 keys, 12-15 values, 16 MMA issue, 17 record loads (cp.async into a ring).
+// Roles (27 warps, 19 with 16 rows): softmax in four groups of four warps (two), an
+// equal share of the rows each, four warps of keys, four of values, one that
+// issues the MMAs, two that load records and scales (cp.async into a ring).
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -47,9 +48,12 @@ namespace {
 
 using namespace tree;
 
-constexpr int kMmaThreads = 18 * 32;
-constexpr int kKeyWarp = 8, kValueWarp = 12, kIssueWarp = 16, kLoadWarp = 17;
 constexpr int kTableBytes = 8192;      // value levels
+constexpr int kScaleSlots = 8;         // tiles whose scales are kept (see kMaxStages)
+// Ring stages: the loader is at most this many packed tiles ahead of the key and value warps, and
+// these, when they release tile a, have waited for the softmax of tile a - 3; so a
+// slot of scales that is refilled 8 tiles later has been read for 5 stages at most.
+constexpr int kMaxStages = 4;
 constexpr int kSmemMax = 227 * 1024;
 constexpr float kInf = __builtin_huge_valf();
 constexpr int kDrainPolls = 1 << 20;
@@ -75,6 +79,29 @@ __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return r;
 }
+
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+    float2 r;
+    asm("{.reg .b64 ra, rb, rr;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n add.rn.f32x2 rr, ra, rb;\n"
+        " mov.b64 {%0, %1}, rr;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+    float2 r;
+    asm("{.reg .b64 ra, rb, rr;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n mul.rn.f32x2 rr, ra, rb;\n"
+        " mov.b64 {%0, %1}, rr;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 // ---------------------------------------------------------------- barriers
 __device__ __forceinline__ void bar_init(unsigned bar, unsigned count) {
@@ -116,9 +143,11 @@ struct Waiter {
     int *error;
     int polls;
     __device__ __forceinline__ void operator()(unsigned bar, unsigned parity) const {
-        if (*dead) return;
-        for (int i = 0; i < polls; i++)
+        if (polls > 0 && bar_try(bar, parity)) return;
+        for (int i = 1; i < polls; i++) {
+            if (*dead) return;
             if (bar_try(bar, parity)) return;
+        }
         *dead = 1;
         atomicExch(error, 1);
     }
@@ -154,6 +183,11 @@ __device__ __forceinline__ void mma_ss(unsigned d, uint64_t a, uint64_t b, uint3
         "l"(a), "l"(b), "r"(id), "r"(acc)
         : "memory");
 }
+__device__ __forceinline__ bool elect_one() {
+    unsigned r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r != 0;
+}
 __device__ __forceinline__ void mma_commit(unsigned bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
@@ -170,22 +204,7 @@ __device__ __forceinline__ void tmem_ld16(unsigned a, float *v) {
 #pragma unroll
     for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tmem_ld32(unsigned a, float *v) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(a)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
-}
-// C columns (8, 16 or 32), waited for in the same statement so that no use is scheduled before
+// C columns (8 or 16), waited for in the same statement so that no use is scheduled before
 template <int C>
 __device__ __forceinline__ void tmem_ld(unsigned a, float (&v)[C]) {
     if constexpr (C == 8) {
@@ -198,10 +217,9 @@ __device__ __forceinline__ void tmem_ld(unsigned a, float (&v)[C]) {
             : "memory");
 #pragma unroll
         for (int i = 0; i < 8; i++) v[i] = __uint_as_float(r[i]);
-    } else if constexpr (C == 16) {
-        tmem_ld16(a, v);
     } else {
-        tmem_ld32(a, v);
+        static_assert(C == 16, "8 or 16 columns");
+        tmem_ld16(a, v);
     }
 }
 __device__ __forceinline__ void tmem_st8(unsigned a, const uint32_t *r) {
@@ -307,7 +325,7 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t *w, int shl) {
 
 // 8 dims (one 16-byte chunk) of a record: chunk C
 template <int VB, int C>
-__device__ __forceinline__ uint4 level_chunk(const uint32_t *w, unsigned table, unsigned col) {
+__device__ __forceinline__ uint4 level_chunk(const uint32_t *w, const uint8_t *table) {
     uint32_t h[4];
     constexpr int kRow = level_columns(VB) * level_bytes(VB);  // bytes of an entry's columns
     constexpr int kLog = kRow == 256 ? 8 : kRow == 128 ? 7 : kRow == 64 ? 6 : 5;
@@ -315,16 +333,14 @@ __device__ __forceinline__ uint4 level_chunk(const uint32_t *w, unsigned table, 
     constexpr int n = VB * level_codes(VB);
     constexpr uint32_t mask = ((1u << n) - 1u) << kLog;
     if constexpr (VB == 1) {
-        const unsigned a0 = table + ((bits_at<8 * C, 4>(w, kLog) & mask) | col);
-        const unsigned a1 = table + ((bits_at<8 * C + 4, 4>(w, kLog) & mask) | col);
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(h[0]), "=r"(h[1]) : "r"(a0));
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(h[2]), "=r"(h[3]) : "r"(a1));
+        const uint2 a = *reinterpret_cast<const uint2 *>(table + (bits_at<8 * C, 4>(w, kLog) & mask));
+        const uint2 b = *reinterpret_cast<const uint2 *>(table + (bits_at<8 * C + 4, 4>(w, kLog) & mask));
+        h[0] = a.x, h[1] = a.y, h[2] = b.x, h[3] = b.y;
     } else if constexpr (VB <= 4) {
         const uint32_t f[4] = {bits_at<8 * VB * C, n>(w, kLog), bits_at<8 * VB * C + n, n>(w, kLog),
                                bits_at<8 * VB * C + 2 * n, n>(w, kLog), bits_at<8 * VB * C + 3 * n, n>(w, kLog)};
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(h[i]) : "r"(table + ((f[i] & mask) | col)));
+        for (int i = 0; i < 4; i++) h[i] = *reinterpret_cast<const uint32_t *>(table + (f[i] & mask));
     } else {
         const uint32_t f[8] = {bits_at<8 * VB * C, n>(w, kLog),          bits_at<8 * VB * C + n, n>(w, kLog),
                                bits_at<8 * VB * C + 2 * n, n>(w, kLog), bits_at<8 * VB * C + 3 * n, n>(w, kLog),
@@ -332,8 +348,7 @@ __device__ __forceinline__ uint4 level_chunk(const uint32_t *w, unsigned table, 
                                bits_at<8 * VB * C + 6 * n, n>(w, kLog), bits_at<8 * VB * C + 7 * n, n>(w, kLog)};
         uint32_t v[8];
 #pragma unroll
-        for (int i = 0; i < 8; i++)
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[i]) : "r"(table + ((f[i] & mask) | col)));
+        for (int i = 0; i < 8; i++) v[i] = *reinterpret_cast<const uint32_t *>(table + (f[i] & mask));
 #pragma unroll
         for (int i = 0; i < 4; i++) h[i] = prmt(v[2 * i], v[2 * i + 1], 0x7610u);
     }
@@ -343,7 +358,11 @@ __device__ __forceinline__ uint4 level_chunk(const uint32_t *w, unsigned table, 
 // ---------------------------------------------------------------- shared memory
 template <int D, int R>
 struct Mma {
-    static constexpr int CW = R / 2;                // rows per softmax group
+    static constexpr int NWG = R == 16 ? 2 : 4;     // softmax groups of four warps
+    static constexpr int CW = R / NWG;              // rows per group
+    static constexpr int kKeyWarp = 4 * NWG, kValueWarp = kKeyWarp + 4, kIssueWarp = kValueWarp + 4,
+                         kLoadWarp = kIssueWarp + 1;
+    static constexpr int kThreads = 32 * (kLoadWarp + 2);
     static constexpr int HALVES = D / 64;
     static constexpr int QPART = HALVES * R * 128;  // hi or lo of a block's queries
     static constexpr int QBUF = 2 * QPART;
@@ -351,16 +370,17 @@ struct Mma {
     static constexpr int PBUF = 128 * 128;
     static constexpr int KCOLS = D / 2;             // TMEM columns of a K tile
     static constexpr int T_K = 0, T_S = 2 * KCOLS, T_O = T_S + 2 * R;
-    static constexpr int TCOLS = T_O + R <= 128 ? 128 : T_O + R <= 256 ? 256 : 512;
+    static constexpr int TCOLS = 512;               // all of TMEM, so that its base is column 0
     static constexpr int O_Q = 0;
     static constexpr int O_V = O_Q + 2 * QBUF;
     static constexpr int O_P = O_V + 2 * VBUF;
     static constexpr int O_T = O_P + 2 * PBUF;
-    static constexpr int O_A = O_T + kTableBytes;   // [4][R] A, [4][R] B
+    static constexpr int O_S = O_T + kTableBytes;   // [kScaleSlots][2][128] scales
+    static constexpr int O_A = O_S + kScaleSlots * 1024;  // [4][R] A, [4][R] B
     static constexpr int O_M = O_A + 8 * R * 4;     // [R] m, [R] -m as used, [R] factors
-    static constexpr int O_X = O_M + 3 * R * 4;     // [2][4][CW + 1] maxima of the warps
-    static constexpr int O_B = (O_X + 2 * 4 * (CW + 1) * 4 + 15) / 16 * 16;
-    static constexpr int kBars = 2 * 8 + 4 + 1 + 1 + 16;
+    static constexpr int O_X = O_M + 3 * R * 4;     // [NWG][4][CW + 1] maxima of the warps
+    static constexpr int O_B = (O_X + NWG * 4 * (CW + 1) * 4 + 15) / 16 * 16;
+    static constexpr int kBars = 2 * 8 + 4 + 1 + 1 + 2 * kMaxStages;
     static constexpr int O_RING = (O_B + kBars * 8 + 16 + 127) / 128 * 128;
     static constexpr int kRing = kSmemMax - 1024 - O_RING;  // (1024: alignment)
 };
@@ -368,6 +388,121 @@ struct Mma {
 struct RingGeo {
     int stage, stages;
 };
+
+// The queries of a block's rows as the MMA's B operand, for keys of kb bits (0: fp16
+// keys, unrotated queries), and each row's (A, B).  TL lanes hold a row, 16
+// coordinates each; warp `wi` of `nw` takes every nw-th group of 32 / TL rows.
+template <int D, int R>
+__device__ __forceinline__ void prepare_queries(const TreeParams &p, const Pos &x, int kb, uint8_t *q, float *ab, int wi,
+                                                int nw) {
+    using C = Mma<D, R>;
+    constexpr int TL = D / 16, RPW = 32 / TL;
+    const int lane = threadIdx.x & 31, lt = lane % TL;
+    const bool vec = ((reinterpret_cast<uintptr_t>(p.q) | (p.qs[0] * 2) | (p.qs[1] * 2) | (p.qs[2] * 2)) & 15) == 0;
+    const uint32_t neg = p.sign_bits[lt >> 1] >> (16 * (lt & 1));
+    for (int r0 = wi * RPW; r0 < R; r0 += nw * RPW) {
+        const int r = r0 + lane / TL, row = x.rb * R + r;
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; i++) v[i] = 0.f;
+        if (row < p.N * p.g) {
+            const uint16_t *src = p.q + x.b * p.qs[0] + (row / p.g) * p.qs[1] + (x.h * p.g + row % p.g) * p.qs[2] + 16 * lt;
+            uint32_t w[8];
+            if (vec) {
+                const uint4 a = __ldg(reinterpret_cast<const uint4 *>(src)), c = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
+                w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = c.x, w[5] = c.y, w[6] = c.z, w[7] = c.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++) w[i] = __ldg(src + 2 * i) | static_cast<uint32_t>(__ldg(src + 2 * i + 1)) << 16;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                v[2 * i] = f.x, v[2 * i + 1] = f.y;
+            }
+        }
+        uint8_t *line = q + (R * 128) * (16 * lt / 64) + r * 128;  // the half of the row with this lane's coordinates
+        const int c0 = (16 * lt % 64) / 8;                        // its first 16-byte chunk there
+        if (kb == 0) {
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const __half2 h = __floats2half2_rn(v[8 * c + 2 * i], v[8 * c + 2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                *reinterpret_cast<uint4 *>(line + (((c0 + c) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            if (lt == 0) ab[r] = p.qk_scale, ab[4 * R + r] = 0.f;
+            continue;
+        }
+        // R q: signs, butterflies 1..8 in the lane, the others across lanes, signs, scale
+#pragma unroll
+        for (int i = 0; i < 16; i++)
+            if ((neg >> i) & 1u) v[i] = -v[i];
+#pragma unroll
+        for (int h = 1; h < 16; h <<= 1)
+#pragma unroll
+            for (int i = 0; i < 16; i++)
+                if (!(i & h)) {
+                    const float a = v[i], c = v[i + h];
+                    v[i] = a + c, v[i + h] = a - c;
+                }
+#pragma unroll
+        for (int h = 1; h < TL; h <<= 1) {
+            const float sg = (lt & h) ? -1.f : 1.f;
+#pragma unroll
+            for (int i = 0; i < 16; i++) v[i] = fmaf(v[i], sg, __shfl_xor_sync(0xffffffffu, v[i], h));
+        }
+        float mx = 0.f, sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+            v[i] *= ((neg >> i) & 1u) ? -p.inv_sqrt_d : p.inv_sqrt_d;
+            mx = fmaxf(mx, fabsf(v[i]));
+            sum += v[i];
+        }
+#pragma unroll
+        for (int h = 1; h < TL; h <<= 1) {
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, h));
+            sum += __shfl_xor_sync(0xffffffffu, sum, h);
+        }
+        // f = 2^-e, f mx in [0.5, 1) (non-finite rows: f = 1, they stay their own)
+        int e = 0;
+        if (mx > 0.f && mx < kInf) e = static_cast<int>((__float_as_uint(mx) >> 23) & 0xFFu) - 126;
+        e = max(-100, min(100, e));
+        // x = m_t qk_scale (2^(1-b) sum code q + (2^-b - 1) sum q), U = f 2^-11 sum code q
+        if (lt == 0) {
+            ab[r] = p.qk_scale * pow2(12 - kb + e);
+            ab[4 * R + r] = p.qk_scale * (pow2(-kb) - 1.0f) * sum;
+        }
+        // coordinate 32 g + i + 16 u meets the code at place 32 g + 2 i + u, at bit s_i: times 2^(13 - s_i)
+        uint32_t w[16];  // hi, lo
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+            const int pos = (kb * i) & 15, o = pos + kb <= 10 ? pos : pos >= 8 ? pos - 8 : pos;
+            const float y = v[i] * pow2(13 - e - min(o, 10 - kb));
+            const __half hi = __float2half_rn(y), lo = __float2half_rn(y - __half2float(hi));
+            w[i] = static_cast<uint32_t>(__half_as_ushort(hi)) | static_cast<uint32_t>(__half_as_ushort(lo)) << 16;
+        }
+        // the pair of lanes (u = 0, 1) shares its 32 places: the even lane takes i < 8
+        const int u = lt & 1;
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const uint32_t own = u ? w[8 + i] : w[i];
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, u ? w[i] : w[8 + i], 1);
+            hi[i] = u ? prmt(other, own, 0x5410u) : prmt(own, other, 0x5410u);
+            lo[i] = u ? prmt(other, own, 0x7632u) : prmt(own, other, 0x7632u);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+            const int at = ((c0 + c) ^ (r & 7)) << 4;
+            *reinterpret_cast<uint4 *>(line + at) = make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+            *reinterpret_cast<uint4 *>(line + C::QPART + at) = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+        }
+    }
+}
 
 template <int KB, int D>
 __device__ __forceinline__ void keys_to_tmem(unsigned raw, int token, unsigned release, unsigned dst, const Waiter &wait,
@@ -388,28 +523,20 @@ __device__ __forceinline__ void keys_to_tmem(unsigned raw, int token, unsigned r
 }
 
 template <int VB, int D, int... C>
-__device__ __forceinline__ void level_chunks(const uint32_t *w, unsigned table, unsigned col, unsigned dst, int token,
+__device__ __forceinline__ void level_chunks(const uint32_t *w, const uint8_t *table, uint8_t *line, int token,
                                              std::integer_sequence<int, C...>) {
-    (
-        [&] {
-            const uint4 x = level_chunk<VB, C>(w, table, col);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (C >> 3) * 16384 +
-                                                                          (((C & 7) ^ (token & 7)) << 4)),
-                         "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
-                         : "memory");
-        }(),
-        ...);
+    ((*reinterpret_cast<uint4 *>(line + (C >> 3) * 16384 + (((C & 7) ^ (token & 7)) << 4)) = level_chunk<VB, C>(w, table)), ...);
 }
 template <int VB, int D>
-__device__ __forceinline__ void values_to_smem(unsigned raw, int token, unsigned release, unsigned table, unsigned dst,
-                                               const Waiter &wait, unsigned vempty, unsigned parity) {
+__device__ __forceinline__ void values_to_smem(unsigned raw, int token, unsigned release, const uint8_t *table,
+                                               uint8_t *dst, const Waiter &wait, unsigned vempty, unsigned parity) {
     uint32_t w[D / 32 * VB];
     load_record<D / 32 * VB>(raw, token, w);
     __syncwarp();
     if ((threadIdx.x & 31) == 0) bar_arrive(release);
     wait(vempty, parity);
-    const unsigned col = (token & (level_columns(VB) - 1)) * level_bytes(VB);
-    level_chunks<VB, D>(w, table, col, dst + token * 128, token, std::make_integer_sequence<int, D / 8>{});
+    level_chunks<VB, D>(w, table + (token & (level_columns(VB) - 1)) * level_bytes(VB), dst + token * 128, token,
+                        std::make_integer_sequence<int, D / 8>{});
 }
 
 // Fill the value table of a width (the four value warps together).
@@ -436,12 +563,13 @@ __device__ __forceinline__ void cp16(unsigned dst, const void *src) {
 
 // ---------------------------------------------------------------- kernel
 template <int D, int R>
-__global__ void __launch_bounds__(kMmaThreads, 1)
+__global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
     tree_mma_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ TreeLevels lv, const RingGeo ring) {
     using C = Mma<D, R>;
-    constexpr int CW = C::CW;
+    constexpr int CW = C::CW, kKeyWarp = C::kKeyWarp, kValueWarp = C::kValueWarp, kIssueWarp = C::kIssueWarp,
+                  kLoadWarp = C::kLoadWarp;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sm = smem_raw + ((1024 - (su32(smem_raw) & 1023)) & 1023);
     const unsigned sb = su32(sm);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned bars = sb + C::O_B;
@@ -456,7 +584,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     auto c_full = [&](int i) { return bars + 8u * (16 + i); };
     const unsigned o_free = bars + 8u * 20, drain = bars + 8u * 21;
     auto r_full = [&](int i) { return bars + 8u * (22 + i); };
-    auto r_empty = [&](int i) { return bars + 8u * (30 + i); };
+    auto r_empty = [&](int i) { return bars + 8u * (22 + kMaxStages + i); };
     int *dead = reinterpret_cast<int *>(sm + C::O_B + C::kBars * 8);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(dead + 1);
 
@@ -473,15 +601,15 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             bar_init(v_full(i), 4);
             bar_init(v_empty(i), 1);
             bar_init(s_full(i), 1);
-            bar_init(s_empty(i), 8);
-            bar_init(p_full(i), 8);
+            bar_init(s_empty(i), 4 * C::NWG);
+            bar_init(p_full(i), 4 * C::NWG);
             bar_init(p_empty(i), 1);
         }
         for (int i = 0; i < 4; i++) bar_init(c_full(i), 4);
-        bar_init(o_free, 8);
+        bar_init(o_free, 4 * C::NWG);
         bar_init(drain, 1);
-        for (int i = 0; i < 8; i++) {
-            bar_init(r_full(i), 32);
+        for (int i = 0; i < kMaxStages; i++) {
+            bar_init(r_full(i), 64);
             bar_init(r_empty(i), 8);
         }
         *dead = 0;
@@ -496,135 +624,167 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     tc_before();
     __syncthreads();
     tc_after();
-    const unsigned tbase = *tmem_slot;
+    constexpr unsigned tbase = 0;
     const Waiter wait{dead, p.error, p.wait_polls};
-    Pos x = seek(p, at0);
+    Walk w = walk_begin(p, at0);
 
-    if (warp == kLoadWarp) {
-        // ------------------------------------------------------ records into the ring
-        int jp = 0;
-        for (int j = 0; j < n_tiles; j++, advance(p, x)) {
-            if (x.k >= x.tp) continue;
-            const Tile w = tile_at(p, x);
-            const SegView &s = p.seg[w.seg].seg;
-            const int st = jp % ring.stages;
+    // the first queries, by every warp that has nothing to do yet
+    if (warp < kValueWarp) {
+        prepare_queries<D, R>(p, w.x, p.seg[w.seg].seg.fp16 ? 0 : p.seg[w.seg].seg.kbits[w.x.h], sm + C::O_Q,
+                              reinterpret_cast<float *>(sm + C::O_A), warp, kValueWarp);
+        fence_async();
+        named_sync(6, 32 * kValueWarp);
+    }
+
+    if (warp >= kLoadWarp) {
+        // ------------------------------------------------------ records and scales: keys, values
+        const int kv = warp - kLoadWarp;
+        const uint8_t *src = nullptr;
+        const float *scale = nullptr;
+        int rec = 0, off = 0, jp = 0, st = 0;
+        for (int j = 0; j < n_tiles; j++, walk_next(p, w)) {
+            if (w.fresh) {
+                const SegView &s = p.seg[w.seg].seg;
+                rec = 0;
+                if (!s.fp16) {
+                    const int kb = s.kbits[w.x.h];
+                    rec = D / 8 * (kv ? s.vbits[w.x.h] : kb);
+                    off = C::O_RING + (kv ? kTreeTile * (D / 8) * kb : 0);
+                    src = (kv ? s.v + w.x.b * s.vblock + s.voff[w.x.h] : s.k + w.x.b * s.kblock + s.koff[w.x.h]) + 16 * lane;
+                    scale = (kv ? s.vs : s.ks) + (static_cast<size_t>(w.x.b) * p.H + w.x.h) * s.capacity + 4 * lane;
+                }
+            }
+            if (rec == 0) continue;
             wait(r_empty(st), ((jp / ring.stages) & 1) ^ 1);
             __syncwarp();
-            const unsigned base = sb + C::O_RING + st * ring.stage;
-#pragma unroll
-            for (int kv = 0; kv < 2; kv++) {
-                const int rec = D / 8 * (kv ? s.vbits[x.h] : s.kbits[x.h]);
-                const uint8_t *src = (kv ? s.v : s.k) + x.b * (kv ? s.vblock : s.kblock) +
-                                     (kv ? s.voff[x.h] : s.koff[x.h]) + static_cast<size_t>(w.t0) * rec;
-                const unsigned dst = base + (kv ? 128 * (D / 8) * s.kbits[x.h] : 0);
-                const int m = chunk_mask(rec), n = (w.n * rec + 15) / 16;
-                for (int c = lane; c < n; c += 32) cp16(dst + 16 * (c ^ ((c >> 3) & m)), src + 16 * static_cast<size_t>(c));
-            }
+            const int n = min(kTreeTile, w.n - w.t * kTreeTile);
+            const uint8_t *from = src + static_cast<size_t>(w.t) * (kTreeTile * rec);
+            const unsigned dst = sb + off + st * ring.stage;
+            // chunk c = lane + 32 i goes to c ^ ((c >> 3) & m): the same for every i but m = 7's third bit
+            const int m = chunk_mask(rec), chunks = (n * rec + 15) / 16;
+            const unsigned to = dst + 16 * (lane ^ ((lane >> 3) & m));
+            const unsigned to2 = m == 7 ? dst + 16 * (lane ^ (((lane + 32) >> 3) & 7)) : to;
+            if (4 * lane < n) cp16(sb + C::O_S + (jp % kScaleSlots) * 1024 + kv * 512 + 16 * lane, scale + w.t * kTreeTile);
+#pragma unroll 4
+            for (int i = 0; 32 * i + lane < chunks; i++) cp16(((i & 1) ? to2 : to) + 512 * i, from + 512 * i);
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(r_full(st)) : "memory");
             jp++;
+            if (++st == ring.stages) st = 0;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == kIssueWarp) {
         // ------------------------------------------------------ MMA issue
-        if (lane == 0) {
-            constexpr uint32_t id_s = idesc(R, false), id_o = idesc(R, true);
-            long long group = -1, part = -1;
-            int seg = -1, ev = -1, parts = 0;
-            bool first_prev = false;
-            for (int j = 0; j <= n_tiles; j++) {
-                bool first = false;
-                if (j < n_tiles) {
-                    const Tile w = tile_at(p, x);
-                    const long long g = group_of(p, x), pt = part_of(p, g, x.tp, x.k);
-                    if (g != group || w.seg != seg) ev++;
-                    first = pt != part;
-                    group = g;
-                    seg = w.seg;
-                    part = pt;
-                    const int b = j & 1;
-                    wait(k_full(b), (j >> 1) & 1);
-                    wait(s_empty(b), ((j >> 1) & 1) ^ 1);
-                    tc_after();
-                    const unsigned q = sb + C::O_Q + (ev & 1) * C::QBUF, a = tbase + C::T_K + b * C::KCOLS,
-                                   d = tbase + C::T_S + b * R;
-                    const int halves = p.seg[w.seg].seg.fp16 ? 1 : 2;  // fp16 queries are exact: no lo part
-                    for (int part2 = 0; part2 < halves; part2++)
+        constexpr uint32_t id_s = idesc(R, false), id_o = idesc(R, true);
+        int ev = -1, parts = 0;
+        bool fp16 = false, first_prev = false;
+        for (int j = 0; j <= n_tiles; j++) {
+            const bool first = w.first;
+            if (j < n_tiles) {
+                if (w.fresh) {
+                    ev++;
+                    fp16 = p.seg[w.seg].seg.fp16;
+                }
+                const int b = j & 1;
+                wait(k_full(b), (j >> 1) & 1);
+                wait(s_empty(b), ((j >> 1) & 1) ^ 1);
+                tc_after();
+                const uint64_t q = desc_k(sb + C::O_Q + (ev & 1) * C::QBUF);
+                const unsigned a = C::T_K + b * C::KCOLS, d = C::T_S + b * R;
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; k++)
+                        mma_ts(d, a + 8 * k, q + (((k >> 2) * R * 128 + 32 * (k & 3)) >> 4), id_s, k != 0);
+                    if (!fp16) {  // (fp16 queries are exact: no lo part)
 #pragma unroll
                         for (int k = 0; k < D / 16; k++)
-                            mma_ts(d, a + 8 * k, desc_k(q + part2 * C::QPART + (k >> 2) * R * 128 + 32 * (k & 3)), id_s,
-                                   (part2 | k) != 0);
+                            mma_ts(d, a + 8 * k, q + ((C::QPART + (k >> 2) * R * 128 + 32 * (k & 3)) >> 4), id_s, 1);
+                    }
                     mma_commit(k_empty(b));
                     mma_commit(s_full(b));
                 }
-                if (j > 0) {
-                    const int i = j - 1, b = i & 1;
-                    wait(v_full(b), (i >> 1) & 1);
-                    wait(p_full(b), (i >> 1) & 1);
-                    if (first_prev) {
-                        if (parts > 0) wait(o_free, (parts - 1) & 1);
-                        parts++;
-                    }
-                    tc_after();
-                    const unsigned v = sb + C::O_V + b * C::VBUF, pp = sb + C::O_P + b * C::PBUF, d = tbase + C::T_O;
+                __syncwarp();
+            }
+            if (j > 0) {
+                const int i = j - 1, b = i & 1;
+                wait(v_full(b), (i >> 1) & 1);
+                if (first_prev) {
+                    if (parts > 0) wait(o_free, (parts - 1) & 1);
+                    parts++;
+                }
+                wait(p_full(b), (i >> 1) & 1);
+                tc_after();
+                const uint64_t v = desc_mn(sb + C::O_V + b * C::VBUF, C::HALVES == 2 ? 16384 : 0),
+                               pp = desc_mn(sb + C::O_P + b * C::PBUF, 0);
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 8; k++)
-                        mma_ss(d, desc_mn(v + 2048 * k, C::HALVES == 2 ? 16384 : 0), desc_mn(pp + 2048 * k, 0), id_o,
-                               !(first_prev && k == 0));
+                        mma_ss(C::T_O, v + (2048 * k >> 4), pp + (2048 * k >> 4), id_o, k != 0 || !first_prev);
                     mma_commit(v_empty(b));
                     mma_commit(p_empty(b));
                 }
-                first_prev = first;
-                if (j < n_tiles) advance(p, x);
+                __syncwarp();
             }
-            // everything issued has completed before TMEM and shared memory go away
-            mma_commit(drain);
-            for (int i = 0; i < kDrainPolls; i++)
-                if (bar_try(drain, 0)) break;
+            first_prev = first;
+            if (j + 1 < n_tiles) walk_next(p, w);
         }
+        // everything issued has completed before TMEM and shared memory go away
+        if (elect_one()) mma_commit(drain);
+        __syncwarp();
+        for (int i = 0; i < kDrainPolls; i++)
+            if (bar_try(drain, 0)) break;
     } else if (warp >= kValueWarp) {
         // ------------------------------------------------------ values into shared memory
         const int tid = threadIdx.x - kValueWarp * 32;
-        int jp = 0, tvb = 0, tlaw = -1;
-        for (int j = 0; j < n_tiles; j++, advance(p, x)) {
-            const Tile w = tile_at(p, x);
+        int jp = 0, st = 0, tvb = 0, tlaw = -1, vb = 0;
+        unsigned raw_off = 0;
+        for (int j = 0; j < n_tiles; j++, walk_next(p, w)) {
             const SegView &s = p.seg[w.seg].seg;
             const int b = j & 1;
-            const unsigned dst = sb + C::O_V + b * C::VBUF, par = ((j >> 1) & 1) ^ 1;
-            if (s.fp16) {
-                const uint8_t *src = s.v + x.b * s.vblock + s.voff[x.h] + static_cast<size_t>(w.t0) * (2 * D);
-                wait(v_empty(b), par);
-                // 16-byte chunks, a row's consecutive in a quarter warp (coalesced); rows behind the tokens are zeros
-                for (int c = tid; c < 128 * D / 8; c += 128) {
-                    const int t = c / (D / 8), e = c % (D / 8);
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (t < w.n) v = __ldg(reinterpret_cast<const uint4 *>(src) + c);
-                    *reinterpret_cast<uint4 *>(sm + C::O_V + b * C::VBUF + (e >> 3) * 16384 + t * 128 +
-                                               (((e & 7) ^ (t & 7)) << 4)) = v;
-                }
-            } else {
-                const int vb = s.vbits[x.h], law = p.seg[w.seg].law;
-                if (vb != tvb || law != tlaw) {
-                    named_sync(4, 128);  // the other warps have done with the old table
+            uint8_t *dst = sm + C::O_V + b * C::VBUF;
+            const unsigned par = ((j >> 1) & 1) ^ 1;
+            if (w.fresh) {
+                vb = s.fp16 ? 0 : s.vbits[w.x.h];
+                raw_off = C::O_RING + (s.fp16 ? 0 : kTreeTile * (D / 8) * s.kbits[w.x.h]);
+                const int law = p.seg[w.seg].law;
+                if (vb && (vb != tvb || law != tlaw)) {
+                    named_sync(5, 128);  // the other warps have done with the old table
                     fill_levels(sm + C::O_T, lv.half[law] + cb_off(vb), vb, tid);
-                    named_sync(4, 128);
+                    named_sync(5, 128);
                     tvb = vb;
                     tlaw = law;
                 }
-                const int st = jp % ring.stages;
-                const unsigned raw = sb + C::O_RING + st * ring.stage + 128 * (D / 8) * s.kbits[x.h];
+            }
+            if (vb == 0) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(s.v + w.x.b * s.vblock + s.voff[w.x.h]) +
+                                   static_cast<size_t>(w.t) * (kTreeTile * D / 8);
+                const int n = min(kTreeTile, w.n - w.t * kTreeTile);
+                wait(v_empty(b), par);
+                // 16-byte chunks, consecutive threads on consecutive ones; rows behind the tokens are zeros
+#pragma unroll 4
+                for (int c = tid; c < kTreeTile * D / 8; c += 128) {
+                    const int t = c / (D / 8), e = c % (D / 8);
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (t < n) v = __ldg(src + c);
+                    *reinterpret_cast<uint4 *>(dst + (e >> 3) * 16384 + t * 128 + (((e & 7) ^ (t & 7)) << 4)) = v;
+                }
+            } else {
+                const unsigned raw = sb + raw_off + st * ring.stage;
                 wait(r_full(st), (jp / ring.stages) & 1);
                 __syncwarp();
+                const uint8_t *tab = sm + C::O_T;
+                const unsigned rel = r_empty(st), ve = v_empty(b);
                 switch (vb) {
-                    case 1: values_to_smem<1, D>(raw, tid, r_empty(st), sb + C::O_T, dst, wait, v_empty(b), par); break;
-                    case 2: values_to_smem<2, D>(raw, tid, r_empty(st), sb + C::O_T, dst, wait, v_empty(b), par); break;
-                    case 3: values_to_smem<3, D>(raw, tid, r_empty(st), sb + C::O_T, dst, wait, v_empty(b), par); break;
-                    case 4: values_to_smem<4, D>(raw, tid, r_empty(st), sb + C::O_T, dst, wait, v_empty(b), par); break;
-                    case 5: values_to_smem<5, D>(raw, tid, r_empty(st), sb + C::O_T, dst, wait, v_empty(b), par); break;
-                    case 6: values_to_smem<6, D>(raw, tid, r_empty(st), sb + C::O_T, dst, wait, v_empty(b), par); break;
-                    case 7: values_to_smem<7, D>(raw, tid, r_empty(st), sb + C::O_T, dst, wait, v_empty(b), par); break;
-                    default: values_to_smem<8, D>(raw, tid, r_empty(st), sb + C::O_T, dst, wait, v_empty(b), par); break;
+                    case 1: values_to_smem<1, D>(raw, tid, rel, tab, dst, wait, ve, par); break;
+                    case 2: values_to_smem<2, D>(raw, tid, rel, tab, dst, wait, ve, par); break;
+                    case 3: values_to_smem<3, D>(raw, tid, rel, tab, dst, wait, ve, par); break;
+                    case 4: values_to_smem<4, D>(raw, tid, rel, tab, dst, wait, ve, par); break;
+                    case 5: values_to_smem<5, D>(raw, tid, rel, tab, dst, wait, ve, par); break;
+                    case 6: values_to_smem<6, D>(raw, tid, rel, tab, dst, wait, ve, par); break;
+                    case 7: values_to_smem<7, D>(raw, tid, rel, tab, dst, wait, ve, par); break;
+                    default: values_to_smem<8, D>(raw, tid, rel, tab, dst, wait, ve, par); break;
                 }
                 jp++;
+                if (++st == ring.stages) st = 0;
             }
             fence_async();
             __syncwarp();
@@ -634,82 +794,30 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         // ------------------------------------------------------ queries, and keys into TMEM
         const int kw = warp - kKeyWarp, tid = threadIdx.x - kKeyWarp * 32;
         const unsigned lanes = static_cast<unsigned>(32 * kw) << 16;
-        long long group = -1;
-        int seg = -1, ev = -1, jp = 0;
-        for (int j = 0; j < n_tiles; j++, advance(p, x)) {
-            const Tile w = tile_at(p, x);
+        int ev = -1, jp = 0, st = 0, kb = 0;
+        for (int j = 0; j < n_tiles; j++, walk_next(p, w)) {
             const SegView &s = p.seg[w.seg].seg;
-            const long long g = group_of(p, x);
             const int b = j & 1;
             const unsigned dst = tbase + lanes + C::T_K + b * C::KCOLS, par = ((j >> 1) & 1) ^ 1;
-            if (g != group || w.seg != seg) {
-                // the block's queries for this segment: the buffer was last read two changes ago,
-                // by products before those of tile j - 2
+            if (w.fresh) {
                 ev++;
-                group = g;
-                seg = w.seg;
-                wait(k_empty(b), par);
-                __syncwarp();
-                const int kb = s.fp16 ? 0 : s.kbits[x.h];
-                uint8_t *q = sm + C::O_Q + (ev & 1) * C::QBUF;
-                float *ab = reinterpret_cast<float *>(sm + C::O_A) + (ev & 3) * R;
-                // place of this lane's coordinates and the power of two that meets the codes
-                int place = 0;
-                float pw = 1.f;
-                if (kb) {
-                    place = 2 * (lane & 15) + (lane >> 4);
-                    const int p0 = kb * (lane & 15), pos = p0 & 15;
-                    const int o = pos + kb <= 10 ? pos : (pos >= 8 ? pos - 8 : pos);
-                    const int sh = o + kb > 10 ? 10 - kb : o;
-                    pw = __uint_as_float(static_cast<uint32_t>(127 + 13 - sh) << 23);
+                kb = s.fp16 ? 0 : s.kbits[w.x.h];
+                if (ev > 0) {
+                    // this segment's queries: the buffer was last read two changes ago, by products
+                    // that came before those of tile j - 2 or were those
+                    wait(k_empty(b), par);
+                    __syncwarp();
+                    prepare_queries<D, R>(p, w.x, kb, sm + C::O_Q + (ev & 1) * C::QBUF,
+                                          reinterpret_cast<float *>(sm + C::O_A) + (ev & 3) * R, kw, 4);
+                    fence_async();
+                    __syncwarp();
                 }
-                for (int r = kw; r < R; r += 4) {
-                    const int row = x.rb * R + r;
-                    float v[D / 32];
-#pragma unroll
-                    for (int i = 0; i < D / 32; i++) v[i] = 0.f;
-                    if (row < p.N * p.g) {
-                        const uint16_t *src = p.q + x.b * p.qs[0] + (row / p.g) * p.qs[1] + (x.h * p.g + row % p.g) * p.qs[2];
-#pragma unroll
-                        for (int i = 0; i < D / 32; i++) v[i] = __half2float(__ushort_as_half(src[lane + 32 * i]));
-                    }
-                    float f = 1.f, A = p.qk_scale, B = 0.f;
-                    if (kb) {
-                        warp_rotate_strided<D>(v, p.sign_bits, p.inv_sqrt_d, lane);
-                        float mx = 0.f, sum = 0.f;
-#pragma unroll
-                        for (int i = 0; i < D / 32; i++) mx = fmaxf(mx, fabsf(v[i])), sum += v[i];
-#pragma unroll
-                        for (int o = 16; o >= 1; o >>= 1) {
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                            sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                        }
-                        int e = 0;  // f mx in [0.5, 1)
-                        if (mx > 0.f && mx < kInf) e = static_cast<int>((__float_as_uint(mx) >> 23) & 0xFFu) - 126;
-                        e = max(-100, min(100, e));
-                        f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                        // x = m_t qk_scale (2^(1-b) sum code q + (2^-b - 1) sum q), U = f 2^-11 sum code q
-                        A = p.qk_scale * __uint_as_float(static_cast<uint32_t>(127 + 12 - kb + e) << 23);
-                        B = p.qk_scale * (__uint_as_float(static_cast<uint32_t>(127 - kb) << 23) - 1.0f) * sum;
-                    }
-                    if (lane == 0) ab[r] = A, ab[4 * R + r] = B;
-#pragma unroll
-                    for (int i = 0; i < D / 32; i++) {
-                        const float y = v[i] * f * pw;
-                        const __half hi = __float2half_rn(y), lo = __float2half_rn(y - __half2float(hi));
-                        const int k = kb ? 32 * i + place : lane + 32 * i;
-                        const int off = (k >> 6) * R * 128 + r * 128 + ((((k & 63) >> 3) ^ (r & 7)) << 4) + (k & 7) * 2;
-                        *reinterpret_cast<__half *>(q + off) = hi;
-                        *reinterpret_cast<__half *>(q + C::QPART + off) = lo;
-                    }
-                }
-                fence_async();
-                __syncwarp();
                 if (lane == 0) bar_arrive(c_full(ev & 3));
             }
-            if (s.fp16) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(s.k + x.b * s.kblock + s.koff[x.h] +
-                                                                  static_cast<size_t>(w.t0 + tid) * (2 * D));
+            if (kb == 0) {
+                const int t = w.t * kTreeTile + tid;
+                const uint4 *src = reinterpret_cast<const uint4 *>(s.k + w.x.b * s.kblock + s.koff[w.x.h]) +
+                                   static_cast<size_t>(t) * (D / 8);
                 wait(k_empty(b), par);
                 __syncwarp();
                 tc_after();
@@ -719,27 +827,27 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 4; c++) {
                         uint4 v = make_uint4(0, 0, 0, 0);
-                        if (tid < w.n) v = __ldg(src + 4 * i + c);
+                        if (t < w.n) v = __ldg(src + 4 * i + c);
                         out[4 * c] = v.x, out[4 * c + 1] = v.y, out[4 * c + 2] = v.z, out[4 * c + 3] = v.w;
                     }
                     tmem_st16(dst + 16 * i, out);
                 }
             } else {
-                const int st = jp % ring.stages;
-                const unsigned raw = sb + C::O_RING + st * ring.stage;
+                const unsigned raw = sb + C::O_RING + st * ring.stage, rel = r_empty(st), ke = k_empty(b);
                 wait(r_full(st), (jp / ring.stages) & 1);
                 __syncwarp();
-                switch (s.kbits[x.h]) {
-                    case 1: keys_to_tmem<1, D>(raw, tid, r_empty(st), dst, wait, k_empty(b), par); break;
-                    case 2: keys_to_tmem<2, D>(raw, tid, r_empty(st), dst, wait, k_empty(b), par); break;
-                    case 3: keys_to_tmem<3, D>(raw, tid, r_empty(st), dst, wait, k_empty(b), par); break;
-                    case 4: keys_to_tmem<4, D>(raw, tid, r_empty(st), dst, wait, k_empty(b), par); break;
-                    case 5: keys_to_tmem<5, D>(raw, tid, r_empty(st), dst, wait, k_empty(b), par); break;
-                    case 6: keys_to_tmem<6, D>(raw, tid, r_empty(st), dst, wait, k_empty(b), par); break;
-                    case 7: keys_to_tmem<7, D>(raw, tid, r_empty(st), dst, wait, k_empty(b), par); break;
-                    default: keys_to_tmem<8, D>(raw, tid, r_empty(st), dst, wait, k_empty(b), par); break;
+                switch (kb) {
+                    case 1: keys_to_tmem<1, D>(raw, tid, rel, dst, wait, ke, par); break;
+                    case 2: keys_to_tmem<2, D>(raw, tid, rel, dst, wait, ke, par); break;
+                    case 3: keys_to_tmem<3, D>(raw, tid, rel, dst, wait, ke, par); break;
+                    case 4: keys_to_tmem<4, D>(raw, tid, rel, dst, wait, ke, par); break;
+                    case 5: keys_to_tmem<5, D>(raw, tid, rel, dst, wait, ke, par); break;
+                    case 6: keys_to_tmem<6, D>(raw, tid, rel, dst, wait, ke, par); break;
+                    case 7: keys_to_tmem<7, D>(raw, tid, rel, dst, wait, ke, par); break;
+                    default: keys_to_tmem<8, D>(raw, tid, rel, dst, wait, ke, par); break;
                 }
                 jp++;
+                if (++st == ring.stages) st = 0;
             }
             tmem_wait_st();
             tc_before();
@@ -752,40 +860,44 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         const unsigned lanes = static_cast<unsigned>(32 * qw) << 16;
         float *m_row = reinterpret_cast<float *>(sm + C::O_M) + wg * CW;  // m; + R: -m as used; + 2R: factors
         float *maxima = reinterpret_cast<float *>(sm + C::O_X) + wg * 4 * (CW + 1);
-        long long group = -1, part = -1;
-        int seg = -1, ev = -1, E = 0;
-        float l[CW];
+        int ev = -1, E = 0;
+        float2 l[CW / 2];
 #pragma unroll
-        for (int c = 0; c < CW; c++) l[c] = 0.f;
+        for (int c = 0; c < CW / 2; c++) l[c] = make_float2(0.f, 0.f);
+        int jp = 0;
+        bool fp16 = false;
+        float inv = 1.f;  // 1 / s of the value levels
         for (int j = 0; j < n_tiles; j++) {
-            const Tile w = tile_at(p, x);
-            const SegView &s = p.seg[w.seg].seg;
-            const long long g = group_of(p, x), pt = part_of(p, g, x.tp, x.k);
             const int b = j & 1;
             const unsigned par = (j >> 1) & 1;
-            const bool first = pt != part, valid = tok < w.n;
-            float ks = 1.f, vs = 1.f;
-            if (!s.fp16) {
-                ks = vs = 0.f;
-                if (valid) {
-                    const size_t at = (static_cast<size_t>(x.b) * p.H + x.h) * s.capacity + w.t0 + tok;
-                    ks = __ldg(s.ks + at);
-                    vs = __ldg(s.vs + at) * lv.inv[p.seg[w.seg].law][s.vbits[x.h]];
-                }
-            } else if (!valid) {
-                ks = vs = 0.f;
-            }
-            if (g != group || w.seg != seg) {
+            const bool first = w.first;
+            const int left = w.n - w.t * kTreeTile, part = w.part;
+            const bool full = left >= kTreeTile, valid = tok < left;
+            if (w.fresh) {
                 ev++;
+                const TreeSeg &s = p.seg[w.seg];
+                fp16 = s.seg.fp16;
+                inv = fp16 ? 1.f : lv.inv[s.law][s.seg.vbits[w.x.h]];
                 wait(c_full(ev & 3), (ev >> 2) & 1);
             }
-            group = g;
-            seg = w.seg;
-            part = pt;
+            bool last = true;
+            if (j + 1 < n_tiles) {
+                walk_next(p, w);
+                last = w.first;
+            }
             const float *ab = reinterpret_cast<const float *>(sm + C::O_A) + (ev & 3) * R + wg * CW;
             wait(s_full(b), par);
             __syncwarp();
             tc_after();
+            // the token's scales (landed before its keys were unpacked; behind the last token: anything)
+            float ks = 1.f, sig = 1.f;
+            if (!fp16) {
+                const float *sc = reinterpret_cast<const float *>(sm + C::O_S) + (jp % kScaleSlots) * 256 + tok;
+                ks = sc[0];
+                sig = sc[128] * inv;
+                jp++;
+            }
+            if (!valid) ks = sig = 0.f;
             float u[CW];
             const unsigned s_addr = tbase + lanes + C::T_S + b * R + wg * CW;
             // x = ks (A U + B), less m
@@ -805,14 +917,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 }
             };
             bool raise = first;
-            float scale = 1.f;  // 2^-E
             if (!first) {
                 scores(true);
-                float top = u[0];
+                float top = fmaxf(u[0], u[1]);
 #pragma unroll
-                for (int c = 1; c < CW; c++) top = fmaxf(top, u[c]);
-                scale = __uint_as_float(static_cast<uint32_t>(127 - E) << 23);
-                raise = valid && (top > 8.0f || vs * scale > 128.0f);
+                for (int c = 2; c < CW; c += 2) top = fmax3(top, u[c], u[c + 1]);
+                raise = valid && (top > 8.0f || sig * pow2(-E) > 128.0f);
             }
             if (named_or(1 + wg, 128, raise)) {
                 scores(false);
@@ -823,7 +933,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     asm("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(v));
                     if (lane == c) mine = v;
                 }
-                float big = valid ? vs : 0.f;
+                float big = valid ? sig : 0.f;
                 asm("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(big));
                 if (lane < CW) maxima[qw * (CW + 1) + lane] = mine;
                 if (lane == 0) maxima[qw * (CW + 1) + CW] = big;
@@ -831,7 +941,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 big = fmaxf(fmaxf(maxima[CW], maxima[2 * CW + 1]), fmaxf(maxima[3 * CW + 2], maxima[4 * CW + 3]));
                 // E: the largest sigma times 2^-E in [0.5, 1)
                 int e = 0;
-                if (!s.fp16 && big > 0.f && big < kInf)
+                if (!fp16 && big > 0.f && big < kInf)
                     e = max(-100, min(100, static_cast<int>((__float_as_uint(big) >> 23) & 0xFFu) - 126));
                 const int now = first ? e : max(E, e);
                 if (tok < CW) {
@@ -849,30 +959,37 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                     wait(p_empty((j - 1) & 1), ((j - 1) >> 1) & 1);
                     __syncwarp();
                     tc_after();
-                    const float down = __uint_as_float(static_cast<uint32_t>(127 - min(now - E, 126)) << 23);
+                    const float down = pow2(-min(now - E, 126));
 #pragma unroll
                     for (int c = 0; c < CW; c += 8) {
                         float o[8];
                         uint32_t r[8];
                         tmem_ld<8>(tbase + lanes + C::T_O + wg * CW + c, o);
 #pragma unroll
-                        for (int i = 0; i < 8; i++) {
-                            const float f = m_row[2 * R + c + i];
-                            l[c + i] *= f;
-                            r[i] = __float_as_uint(o[i] * (f * down));
+                        for (int i = 0; i < 8; i += 2) {
+                            const float f0 = m_row[2 * R + c + i], f1 = m_row[2 * R + c + i + 1];
+                            l[(c + i) / 2].x *= f0;
+                            l[(c + i) / 2].y *= f1;
+                            r[i] = __float_as_uint(o[i] * (f0 * down));
+                            r[i + 1] = __float_as_uint(o[i + 1] * (f1 * down));
                         }
                         tmem_st8(tbase + lanes + C::T_O + wg * CW + c, r);
                     }
                     tmem_wait_st();
                 }
                 E = now;
-                scale = __uint_as_float(static_cast<uint32_t>(127 - E) << 23);
                 scores(true);
             }
             tc_before();
             __syncwarp();
             if (lane == 0) bar_arrive(s_empty(b));
-            const float sv = vs * scale;
+            const float sv = sig * pow2(-E);
+            if (!full && !valid) {  // behind the last token: weight zero, whatever lies there
+#pragma unroll
+                for (int c = 0; c < CW; c++) u[c] = -kInf;
+            }
+#pragma unroll
+            for (int c = 0; c < CW; c++) u[c] = ex2(u[c]);
             if (j >= 2) wait(p_empty(b), par ^ 1);
             uint8_t *prow = sm + C::O_P + b * C::PBUF + tok * 128;
 #pragma unroll
@@ -880,10 +997,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 uint32_t h[4];
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const float p0 = valid ? ex2(u[c + 2 * i]) : 0.f, p1 = valid ? ex2(u[c + 2 * i + 1]) : 0.f;
-                    l[c + 2 * i] += p0;
-                    l[c + 2 * i + 1] += p1;
-                    const __half2 q = __floats2half2_rn(p0 * sv, p1 * sv);
+                    const float2 pr = make_float2(u[c + 2 * i], u[c + 2 * i + 1]);
+                    l[c / 2 + i] = fadd2(l[c / 2 + i], pr);
+                    const float2 wt = fmul2(pr, make_float2(sv, sv));
+                    const __half2 q = __floats2half2_rn(wt.x, wt.y);
                     h[i] = *reinterpret_cast<const uint32_t *>(&q);
                 }
                 *reinterpret_cast<uint4 *>(prow + ((((wg * CW + c) >> 3) ^ (tok & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
@@ -892,19 +1009,18 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             tc_before();
             __syncwarp();
             if (lane == 0) bar_arrive(p_full(b));
-            // the part's last tile: its record
-            advance(p, x);
-            if (j + 1 == n_tiles || part_of(p, group_of(p, x), x.tp, x.k) != part) {
+            if (last) {  // the part's record
                 float *rec = p.part + static_cast<size_t>(worker + part) * R * (D + 4);
-                // row sums over the tokens: lane c of each warp ends up with row c's
+                // row sums over the tokens
 #pragma unroll
                 for (int c = 0; c < CW; c++) {
-                    float v = l[c];
+                    float v = c & 1 ? l[c / 2].y : l[c / 2].x;
 #pragma unroll
                     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
                     if (lane == 0) maxima[qw * (CW + 1) + c] = v;
-                    l[c] = 0.f;
                 }
+#pragma unroll
+                for (int c = 0; c < CW / 2; c++) l[c] = make_float2(0.f, 0.f);
                 named_sync(1 + wg, 128);
                 if (tok < CW) {
                     float *row = rec + (wg * CW + tok) * (D + 4);
@@ -914,7 +1030,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                 wait(p_empty(b), par);
                 __syncwarp();
                 tc_after();
-                const float up = __uint_as_float(static_cast<uint32_t>(127 + E) << 23);
+                const float up = pow2(E);
 #pragma unroll
                 for (int c = 0; c < CW; c += 8) {
                     float o[8];
@@ -978,13 +1094,13 @@ cudaError_t tree_mma(const TreeParams &p, const TreeLevels &lv, cudaStream_t s) 
         for (int h = 0; h < p.H; h++) stage = std::max(stage, 128 * (D / 8) * (p.seg[i].seg.kbits[h] + p.seg[i].seg.vbits[h]));
     RingGeo ring;
     ring.stage = std::max(stage, 128);
-    ring.stages = std::min(8, C::kRing / ring.stage);
+    ring.stages = std::min(kMaxStages, C::kRing / ring.stage);
     if (ring.stages < 1) return cudaErrorInvalidConfiguration;
     const size_t smem = kSmemMax;
     cudaError_t e = cudaFuncSetAttribute(tree_mma_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    tree_mma_kernel<D, R><<<p.workers, kMmaThreads, smem, s>>>(p, lv, ring);
+    tree_mma_kernel<D, R><<<p.workers, C::kThreads, smem, s>>>(p, lv, ring);
     return cudaGetLastError();
 }
 
