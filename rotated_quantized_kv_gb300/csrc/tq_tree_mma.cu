@@ -29,9 +29,10 @@
 // V^T needs the dims on the lanes, so V goes through shared memory with tokens
 // as the K dimension (MN-major operand).
 //
-// Roles (27 warps, 19 with 16 rows): softmax in four groups of four warps (two), an
-// equal share of the rows each, four warps of keys, four of values, one that
-// issues the MMAs, two that load records and scales (cp.async into a ring).
+// Roles (31 warps, 23 with 16 rows): softmax in four groups of four warps (two), an
+// equal share of the rows each, four warps of keys, eight of values, one that
+// issues the MMAs, two that walk the list and load records and scales (cp.async
+// into a ring); the others learn from a descriptor what a tile is.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -49,10 +50,11 @@ namespace {
 using namespace tree;
 
 constexpr int kTableBytes = 8192;      // value levels
-constexpr int kScaleSlots = 8;         // tiles whose scales are kept (see kMaxStages)
-// Ring stages: the loader is at most this many packed tiles ahead of the key and value warps, and
-// these, when they release tile a, have waited for the softmax of tile a - 3; so a
-// slot of scales that is refilled 8 tiles later has been read for 5 stages at most.
+// Tiles whose descriptor and scales are kept, and ring stages: the loader is at most
+// kMaxStages tiles ahead of the key and value warps, and these, when they release
+// tile a, have waited for the MMA and the softmax of tile a - 3; so slot j % 8 has been
+// read by everyone when tile j + 8 overwrites it (5 stages would do).
+constexpr int kSlots = 8;
 constexpr int kMaxStages = 4;
 constexpr int kSmemMax = 227 * 1024;
 constexpr float kInf = __builtin_huge_valf();
@@ -113,9 +115,9 @@ __device__ __forceinline__ void bar_arrive(unsigned bar) {
 __device__ __forceinline__ bool bar_try(unsigned bar, unsigned parity) {
     unsigned ok;
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
-        : "r"(bar), "r"(parity)
+        : "r"(bar), "r"(parity), "r"(1000u)  // (may suspend for a microsecond)
         : "memory");
     return ok != 0;
 }
@@ -143,10 +145,9 @@ struct Waiter {
     int *error;
     int polls;
     __device__ __forceinline__ void operator()(unsigned bar, unsigned parity) const {
-        if (polls > 0 && bar_try(bar, parity)) return;
-        for (int i = 1; i < polls; i++) {
-            if (*dead) return;
+        for (int i = 0; i < polls; i++) {
             if (bar_try(bar, parity)) return;
+            if (*dead) return;
         }
         *dead = 1;
         atomicExch(error, 1);
@@ -355,12 +356,27 @@ __device__ __forceinline__ uint4 level_chunk(const uint32_t *w, const uint8_t *t
     return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
+// ---------------------------------------------------------------- tile descriptors
+// What the loader tells the other roles about a tile.
+struct TileDesc {
+    int flags;     // kFirst.. | key bits << 8 | value bits << 16
+    int left;      // tokens from the tile's first to the sequence's last in this segment
+    int part;
+    float inv;     // 1 / s of the value levels
+    int b, h, rb, seg;
+    int t, pad[7];
+};
+static_assert(sizeof(TileDesc) == 64, "slot size");
+constexpr int kFirst = 1, kLast = 2;  // of its part
+constexpr int kFresh = 4;             // first of its (group, segment)
+constexpr int kFp16 = 8;
+
 // ---------------------------------------------------------------- shared memory
 template <int D, int R>
 struct Mma {
     static constexpr int NWG = R == 16 ? 2 : 4;     // softmax groups of four warps
     static constexpr int CW = R / NWG;              // rows per group
-    static constexpr int kKeyWarp = 4 * NWG, kValueWarp = kKeyWarp + 4, kIssueWarp = kValueWarp + 4,
+    static constexpr int kKeyWarp = 4 * NWG, kValueWarp = kKeyWarp + 4, kIssueWarp = kValueWarp + 8,
                          kLoadWarp = kIssueWarp + 1;
     static constexpr int kThreads = 32 * (kLoadWarp + 2);
     static constexpr int HALVES = D / 64;
@@ -375,8 +391,9 @@ struct Mma {
     static constexpr int O_V = O_Q + 2 * QBUF;
     static constexpr int O_P = O_V + 2 * VBUF;
     static constexpr int O_T = O_P + 2 * PBUF;
-    static constexpr int O_S = O_T + kTableBytes;   // [kScaleSlots][2][128] scales
-    static constexpr int O_A = O_S + kScaleSlots * 1024;  // [4][R] A, [4][R] B
+    static constexpr int O_S = O_T + kTableBytes;   // [kSlots][2][128] scales
+    static constexpr int O_D = O_S + kSlots * 1024; // [kSlots] descriptors
+    static constexpr int O_A = O_D + kSlots * 64;   // [4][R] A, [4][R] B
     static constexpr int O_M = O_A + 8 * R * 4;     // [R] m, [R] -m as used, [R] factors
     static constexpr int O_X = O_M + 3 * R * 4;     // [NWG][4][CW + 1] maxima of the warps
     static constexpr int O_B = (O_X + NWG * 4 * (CW + 1) * 4 + 15) / 16 * 16;
@@ -522,28 +539,49 @@ __device__ __forceinline__ void keys_to_tmem(unsigned raw, int token, unsigned r
     }
 }
 
+// WORDS words of a token's record (of REC bytes) from word `first` on.
+template <int WORDS, int REC>
+__device__ __forceinline__ void load_part(const uint8_t *base, int token, int first, uint32_t (&w)[WORDS]) {
+    constexpr int m = chunk_mask(REC), step = WORDS % 2 ? 1 : 2;
+#pragma unroll
+    for (int i = 0; i < WORDS; i += step) {
+        const int at = token * REC + 4 * (first + i), c = at >> 4;
+        const uint8_t *q = base + 16 * (c ^ ((c >> 3) & m)) + (at & 15);
+        if constexpr (step == 2) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(q);
+            w[i] = x.x, w[i + 1] = x.y;
+        } else {
+            w[i] = *reinterpret_cast<const uint32_t *>(q);
+        }
+    }
+}
+// Half u of the dims of a token's values: record in the ring to fp16 rows.
 template <int VB, int D, int... C>
-__device__ __forceinline__ void level_chunks(const uint32_t *w, const uint8_t *table, uint8_t *line, int token,
+__device__ __forceinline__ void level_chunks(const uint32_t *w, const uint8_t *table, uint8_t *line, int token, int u,
                                              std::integer_sequence<int, C...>) {
-    ((*reinterpret_cast<uint4 *>(line + (C >> 3) * 16384 + (((C & 7) ^ (token & 7)) << 4)) = level_chunk<VB, C>(w, table)), ...);
+    // chunk C of the half: D = 128, block u of 64 dims; D = 64, chunk 4 u + C of the one block
+    ((*reinterpret_cast<uint4 *>(line + (D == 128 ? u * 16384 + ((C ^ (token & 7)) << 4) : (((4 * u + C) ^ (token & 7)) << 4))) =
+          level_chunk<VB, C>(w, table)),
+     ...);
 }
 template <int VB, int D>
-__device__ __forceinline__ void values_to_smem(unsigned raw, int token, unsigned release, const uint8_t *table,
+__device__ __forceinline__ void values_to_smem(const uint8_t *raw, int token, int u, unsigned release, const uint8_t *table,
                                                uint8_t *dst, const Waiter &wait, unsigned vempty, unsigned parity) {
-    uint32_t w[D / 32 * VB];
-    load_record<D / 32 * VB>(raw, token, w);
+    constexpr int words = D / 64 * VB;
+    uint32_t w[words];
+    load_part<words, D / 8 * VB>(raw, token, words * u, w);
     __syncwarp();
     if ((threadIdx.x & 31) == 0) bar_arrive(release);
     wait(vempty, parity);
-    level_chunks<VB, D>(w, table + (token & (level_columns(VB) - 1)) * level_bytes(VB), dst + token * 128, token,
-                        std::make_integer_sequence<int, D / 8>{});
+    level_chunks<VB, D>(w, table + (token & (level_columns(VB) - 1)) * level_bytes(VB), dst + token * 128, token, u,
+                        std::make_integer_sequence<int, D / 16>{});
 }
 
-// Fill the value table of a width (the four value warps together).
+// Fill the value table of a width (the eight value warps together).
 __device__ __forceinline__ void fill_levels(uint8_t *table, const uint16_t *half, int vb, int tid) {
     const int codes = level_codes(vb), entries = level_entries(vb), cols = level_columns(vb);
     const uint32_t m = (1u << vb) - 1u;
-    for (int i = tid; i < entries * cols; i += 128) {
+    for (int i = tid; i < entries * cols; i += 256) {
         const int e = i / cols;
         if (codes == 4) {
             uint32_t lo = half[e & 1] | static_cast<uint32_t>(half[(e >> 1) & 1]) << 16;
@@ -598,7 +636,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
         for (int i = 0; i < 2; i++) {
             bar_init(k_full(i), 4);
             bar_init(k_empty(i), 1);
-            bar_init(v_full(i), 4);
+            bar_init(v_full(i), 8);
             bar_init(v_empty(i), 1);
             bar_init(s_full(i), 1);
             bar_init(s_empty(i), 4 * C::NWG);
@@ -609,8 +647,8 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
         bar_init(o_free, 4 * C::NWG);
         bar_init(drain, 1);
         for (int i = 0; i < kMaxStages; i++) {
-            bar_init(r_full(i), 64);
-            bar_init(r_empty(i), 8);
+            bar_init(r_full(i), 65);
+            bar_init(r_empty(i), 12);
         }
         *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -626,10 +664,10 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
     tc_after();
     constexpr unsigned tbase = 0;
     const Waiter wait{dead, p.error, p.wait_polls};
-    Walk w = walk_begin(p, at0);
 
     // the first queries, by every warp that has nothing to do yet
     if (warp < kValueWarp) {
+        const Walk w = walk_begin(p, at0);
         prepare_queries<D, R>(p, w.x, p.seg[w.seg].seg.fp16 ? 0 : p.seg[w.seg].seg.kbits[w.x.h], sm + C::O_Q,
                               reinterpret_cast<float *>(sm + C::O_A), warp, kValueWarp);
         fence_async();
@@ -641,34 +679,53 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
         const int kv = warp - kLoadWarp;
         const uint8_t *src = nullptr;
         const float *scale = nullptr;
-        int rec = 0, off = 0, jp = 0, st = 0;
-        for (int j = 0; j < n_tiles; j++, walk_next(p, w)) {
+        int rec = 0, off = 0, st = 0, kind = 0;
+        float inv = 1.f;
+        Walk w = walk_begin(p, at0);
+        for (int j = 0; j < n_tiles; j++) {
             if (w.fresh) {
                 const SegView &s = p.seg[w.seg].seg;
                 rec = 0;
+                kind = kFp16;
+                inv = 1.f;
                 if (!s.fp16) {
-                    const int kb = s.kbits[w.x.h];
-                    rec = D / 8 * (kv ? s.vbits[w.x.h] : kb);
+                    const int kb = s.kbits[w.x.h], vb = s.vbits[w.x.h];
+                    kind = kb << 8 | vb << 16;
+                    inv = lv.inv[p.seg[w.seg].law][vb];
+                    rec = D / 8 * (kv ? vb : kb);
                     off = C::O_RING + (kv ? kTreeTile * (D / 8) * kb : 0);
                     src = (kv ? s.v + w.x.b * s.vblock + s.voff[w.x.h] : s.k + w.x.b * s.kblock + s.koff[w.x.h]) + 16 * lane;
                     scale = (kv ? s.vs : s.ks) + (static_cast<size_t>(w.x.b) * p.H + w.x.h) * s.capacity + 4 * lane;
                 }
             }
-            if (rec == 0) continue;
-            wait(r_empty(st), ((jp / ring.stages) & 1) ^ 1);
-            __syncwarp();
-            const int n = min(kTreeTile, w.n - w.t * kTreeTile);
+            TileDesc d;
+            d.left = w.n - w.t * kTreeTile;
+            d.part = w.part;
+            d.inv = inv;
+            d.b = w.x.b, d.h = w.x.h, d.rb = w.x.rb, d.seg = w.seg, d.t = w.t;
+            d.flags = kind | (w.first ? kFirst : 0) | (w.fresh || j == 0 ? kFresh : 0);
+            const int n = min(kTreeTile, d.left), chunks = (n * rec + 15) / 16;
             const uint8_t *from = src + static_cast<size_t>(w.t) * (kTreeTile * rec);
-            const unsigned dst = sb + off + st * ring.stage;
+            const float *sc = scale + static_cast<size_t>(w.t) * kTreeTile;
+            if (j + 1 < n_tiles) walk_next(p, w);
+            if (j + 1 == n_tiles || w.first) d.flags |= kLast;
+            wait(r_empty(st), ((j / ring.stages) & 1) ^ 1);
+            __syncwarp();
+            if (kv == 0 && lane == 0) {
+                TileDesc *to = reinterpret_cast<TileDesc *>(sm + C::O_D) + j % kSlots;
+                to->flags = d.flags, to->left = d.left, to->part = d.part, to->inv = d.inv;
+                to->b = d.b, to->h = d.h, to->rb = d.rb, to->seg = d.seg, to->t = d.t;
+                bar_arrive(r_full(st));
+            }
             // chunk c = lane + 32 i goes to c ^ ((c >> 3) & m): the same for every i but m = 7's third bit
-            const int m = chunk_mask(rec), chunks = (n * rec + 15) / 16;
+            const unsigned dst = sb + off + st * ring.stage;
+            const int m = chunk_mask(rec);
             const unsigned to = dst + 16 * (lane ^ ((lane >> 3) & m));
             const unsigned to2 = m == 7 ? dst + 16 * (lane ^ (((lane + 32) >> 3) & 7)) : to;
-            if (4 * lane < n) cp16(sb + C::O_S + (jp % kScaleSlots) * 1024 + kv * 512 + 16 * lane, scale + w.t * kTreeTile);
+            if (rec && 4 * lane < n) cp16(sb + C::O_S + (j % kSlots) * 1024 + kv * 512 + 16 * lane, sc);
 #pragma unroll 4
             for (int i = 0; 32 * i + lane < chunks; i++) cp16(((i & 1) ? to2 : to) + 512 * i, from + 512 * i);
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(r_full(st)) : "memory");
-            jp++;
             if (++st == ring.stages) st = 0;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -676,16 +733,16 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
         // ------------------------------------------------------ MMA issue
         constexpr uint32_t id_s = idesc(R, false), id_o = idesc(R, true);
         int ev = -1, parts = 0;
-        bool fp16 = false, first_prev = false;
+        bool first_prev = false;
         for (int j = 0; j <= n_tiles; j++) {
-            const bool first = w.first;
+            bool first = false;
             if (j < n_tiles) {
-                if (w.fresh) {
-                    ev++;
-                    fp16 = p.seg[w.seg].seg.fp16;
-                }
                 const int b = j & 1;
                 wait(k_full(b), (j >> 1) & 1);
+                const int flags = reinterpret_cast<const TileDesc *>(sm + C::O_D)[j % kSlots].flags;
+                first = flags & kFirst;
+                const bool fp16 = flags & kFp16;
+                if (flags & kFresh) ev++;
                 wait(s_empty(b), ((j >> 1) & 1) ^ 1);
                 tc_after();
                 const uint64_t q = desc_k(sb + C::O_Q + (ev & 1) * C::QBUF);
@@ -725,7 +782,6 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 __syncwarp();
             }
             first_prev = first;
-            if (j + 1 < n_tiles) walk_next(p, w);
         }
         // everything issued has completed before TMEM and shared memory go away
         if (elect_one()) mma_commit(drain);
@@ -734,58 +790,56 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             if (bar_try(drain, 0)) break;
     } else if (warp >= kValueWarp) {
         // ------------------------------------------------------ values into shared memory
-        const int tid = threadIdx.x - kValueWarp * 32;
-        int jp = 0, st = 0, tvb = 0, tlaw = -1, vb = 0;
-        unsigned raw_off = 0;
-        for (int j = 0; j < n_tiles; j++, walk_next(p, w)) {
-            const SegView &s = p.seg[w.seg].seg;
+        const int tid = threadIdx.x - kValueWarp * 32, token = tid & 127, half = tid >> 7;
+        int st = 0, table = 0, vb = 0, raw_off = 0;
+        for (int j = 0; j < n_tiles; j++) {
             const int b = j & 1;
             uint8_t *dst = sm + C::O_V + b * C::VBUF;
-            const unsigned par = ((j >> 1) & 1) ^ 1;
-            if (w.fresh) {
-                vb = s.fp16 ? 0 : s.vbits[w.x.h];
-                raw_off = C::O_RING + (s.fp16 ? 0 : kTreeTile * (D / 8) * s.kbits[w.x.h]);
-                const int law = p.seg[w.seg].law;
-                if (vb && (vb != tvb || law != tlaw)) {
-                    named_sync(5, 128);  // the other warps have done with the old table
+            const unsigned par = ((j >> 1) & 1) ^ 1, rel = r_empty(st), ve = v_empty(b);
+            wait(r_full(st), (j / ring.stages) & 1);
+            __syncwarp();
+            const TileDesc &d = reinterpret_cast<const TileDesc *>(sm + C::O_D)[j % kSlots];
+            if (d.flags & kFresh) {
+                vb = (d.flags >> 16) & 15;
+                raw_off = C::O_RING + kTreeTile * (D / 8) * ((d.flags >> 8) & 15);
+                const int law = p.seg[d.seg].law;
+                if (vb && vb * 2 + law != table) {
+                    named_sync(5, 256);  // the other warps have done with the old table
                     fill_levels(sm + C::O_T, lv.half[law] + cb_off(vb), vb, tid);
-                    named_sync(5, 128);
-                    tvb = vb;
-                    tlaw = law;
+                    named_sync(5, 256);
+                    table = vb * 2 + law;
                 }
             }
-            if (vb == 0) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(s.v + w.x.b * s.vblock + s.voff[w.x.h]) +
-                                   static_cast<size_t>(w.t) * (kTreeTile * D / 8);
-                const int n = min(kTreeTile, w.n - w.t * kTreeTile);
-                wait(v_empty(b), par);
-                // 16-byte chunks, consecutive threads on consecutive ones; rows behind the tokens are zeros
+            const uint8_t *raw = sm + raw_off + st * ring.stage, *tab = sm + C::O_T;
+            switch (vb) {
+                case 0: {
+                    const SegView &s = p.seg[d.seg].seg;
+                    const uint4 *src = reinterpret_cast<const uint4 *>(s.v + d.b * s.vblock + s.voff[d.h]) +
+                                       static_cast<size_t>(d.t) * (kTreeTile * D / 8);
+                    const int n = d.left;
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(rel);
+                    wait(ve, par);
+                    // 16-byte chunks, consecutive threads on consecutive ones; rows behind the tokens are zeros
 #pragma unroll 4
-                for (int c = tid; c < kTreeTile * D / 8; c += 128) {
-                    const int t = c / (D / 8), e = c % (D / 8);
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (t < n) v = __ldg(src + c);
-                    *reinterpret_cast<uint4 *>(dst + (e >> 3) * 16384 + t * 128 + (((e & 7) ^ (t & 7)) << 4)) = v;
+                    for (int c = tid; c < kTreeTile * D / 8; c += 256) {
+                        const int t = c / (D / 8), e = c % (D / 8);
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (t < n) v = __ldg(src + c);
+                        *reinterpret_cast<uint4 *>(dst + (e >> 3) * 16384 + t * 128 + (((e & 7) ^ (t & 7)) << 4)) = v;
+                    }
+                    break;
                 }
-            } else {
-                const unsigned raw = sb + raw_off + st * ring.stage;
-                wait(r_full(st), (jp / ring.stages) & 1);
-                __syncwarp();
-                const uint8_t *tab = sm + C::O_T;
-                const unsigned rel = r_empty(st), ve = v_empty(b);
-                switch (vb) {
-                    case 1: values_to_smem<1, D>(raw, tid, rel, tab, dst, wait, ve, par); break;
-                    case 2: values_to_smem<2, D>(raw, tid, rel, tab, dst, wait, ve, par); break;
-                    case 3: values_to_smem<3, D>(raw, tid, rel, tab, dst, wait, ve, par); break;
-                    case 4: values_to_smem<4, D>(raw, tid, rel, tab, dst, wait, ve, par); break;
-                    case 5: values_to_smem<5, D>(raw, tid, rel, tab, dst, wait, ve, par); break;
-                    case 6: values_to_smem<6, D>(raw, tid, rel, tab, dst, wait, ve, par); break;
-                    case 7: values_to_smem<7, D>(raw, tid, rel, tab, dst, wait, ve, par); break;
-                    default: values_to_smem<8, D>(raw, tid, rel, tab, dst, wait, ve, par); break;
-                }
-                jp++;
-                if (++st == ring.stages) st = 0;
+                case 1: values_to_smem<1, D>(raw, token, half, rel, tab, dst, wait, ve, par); break;
+                case 2: values_to_smem<2, D>(raw, token, half, rel, tab, dst, wait, ve, par); break;
+                case 3: values_to_smem<3, D>(raw, token, half, rel, tab, dst, wait, ve, par); break;
+                case 4: values_to_smem<4, D>(raw, token, half, rel, tab, dst, wait, ve, par); break;
+                case 5: values_to_smem<5, D>(raw, token, half, rel, tab, dst, wait, ve, par); break;
+                case 6: values_to_smem<6, D>(raw, token, half, rel, tab, dst, wait, ve, par); break;
+                case 7: values_to_smem<7, D>(raw, token, half, rel, tab, dst, wait, ve, par); break;
+                default: values_to_smem<8, D>(raw, token, half, rel, tab, dst, wait, ve, par); break;
             }
+            if (++st == ring.stages) st = 0;
             fence_async();
             __syncwarp();
             if (lane == 0) bar_arrive(v_full(b));
@@ -794,61 +848,65 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
         // ------------------------------------------------------ queries, and keys into TMEM
         const int kw = warp - kKeyWarp, tid = threadIdx.x - kKeyWarp * 32;
         const unsigned lanes = static_cast<unsigned>(32 * kw) << 16;
-        int ev = -1, jp = 0, st = 0, kb = 0;
-        for (int j = 0; j < n_tiles; j++, walk_next(p, w)) {
-            const SegView &s = p.seg[w.seg].seg;
+        int ev = -1, st = 0, kb = 0;
+        for (int j = 0; j < n_tiles; j++) {
             const int b = j & 1;
-            const unsigned dst = tbase + lanes + C::T_K + b * C::KCOLS, par = ((j >> 1) & 1) ^ 1;
-            if (w.fresh) {
+            const unsigned dst = tbase + lanes + C::T_K + b * C::KCOLS, par = ((j >> 1) & 1) ^ 1, rel = r_empty(st),
+                           ke = k_empty(b), raw = sb + C::O_RING + st * ring.stage;
+            wait(r_full(st), (j / ring.stages) & 1);
+            __syncwarp();
+            const TileDesc &d = reinterpret_cast<const TileDesc *>(sm + C::O_D)[j % kSlots];
+            if (d.flags & kFresh) {
                 ev++;
-                kb = s.fp16 ? 0 : s.kbits[w.x.h];
+                kb = (d.flags >> 8) & 15;
                 if (ev > 0) {
                     // this segment's queries: the buffer was last read two changes ago, by products
                     // that came before those of tile j - 2 or were those
-                    wait(k_empty(b), par);
+                    wait(ke, par);
                     __syncwarp();
-                    prepare_queries<D, R>(p, w.x, kb, sm + C::O_Q + (ev & 1) * C::QBUF,
+                    Pos x;
+                    x.b = d.b, x.h = d.h, x.rb = d.rb;
+                    prepare_queries<D, R>(p, x, kb, sm + C::O_Q + (ev & 1) * C::QBUF,
                                           reinterpret_cast<float *>(sm + C::O_A) + (ev & 3) * R, kw, 4);
                     fence_async();
                     __syncwarp();
                 }
                 if (lane == 0) bar_arrive(c_full(ev & 3));
             }
-            if (kb == 0) {
-                const int t = w.t * kTreeTile + tid;
-                const uint4 *src = reinterpret_cast<const uint4 *>(s.k + w.x.b * s.kblock + s.koff[w.x.h]) +
-                                   static_cast<size_t>(t) * (D / 8);
-                wait(k_empty(b), par);
-                __syncwarp();
-                tc_after();
+            switch (kb) {
+                case 0: {
+                    const SegView &s = p.seg[d.seg].seg;
+                    const uint4 *src = reinterpret_cast<const uint4 *>(s.k + d.b * s.kblock + s.koff[d.h]) +
+                                       (static_cast<size_t>(d.t) * kTreeTile + tid) * (D / 8);
+                    const bool valid = tid < d.left;
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(rel);
+                    wait(ke, par);
+                    __syncwarp();
+                    tc_after();
 #pragma unroll
-                for (int i = 0; i < D / 32; i++) {
-                    uint32_t out[16];
+                    for (int i = 0; i < D / 32; i++) {
+                        uint32_t out[16];
 #pragma unroll
-                    for (int c = 0; c < 4; c++) {
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (t < w.n) v = __ldg(src + 4 * i + c);
-                        out[4 * c] = v.x, out[4 * c + 1] = v.y, out[4 * c + 2] = v.z, out[4 * c + 3] = v.w;
+                        for (int c = 0; c < 4; c++) {
+                            uint4 v = make_uint4(0, 0, 0, 0);
+                            if (valid) v = __ldg(src + 4 * i + c);
+                            out[4 * c] = v.x, out[4 * c + 1] = v.y, out[4 * c + 2] = v.z, out[4 * c + 3] = v.w;
+                        }
+                        tmem_st16(dst + 16 * i, out);
                     }
-                    tmem_st16(dst + 16 * i, out);
+                    break;
                 }
-            } else {
-                const unsigned raw = sb + C::O_RING + st * ring.stage, rel = r_empty(st), ke = k_empty(b);
-                wait(r_full(st), (jp / ring.stages) & 1);
-                __syncwarp();
-                switch (kb) {
-                    case 1: keys_to_tmem<1, D>(raw, tid, rel, dst, wait, ke, par); break;
-                    case 2: keys_to_tmem<2, D>(raw, tid, rel, dst, wait, ke, par); break;
-                    case 3: keys_to_tmem<3, D>(raw, tid, rel, dst, wait, ke, par); break;
-                    case 4: keys_to_tmem<4, D>(raw, tid, rel, dst, wait, ke, par); break;
-                    case 5: keys_to_tmem<5, D>(raw, tid, rel, dst, wait, ke, par); break;
-                    case 6: keys_to_tmem<6, D>(raw, tid, rel, dst, wait, ke, par); break;
-                    case 7: keys_to_tmem<7, D>(raw, tid, rel, dst, wait, ke, par); break;
-                    default: keys_to_tmem<8, D>(raw, tid, rel, dst, wait, ke, par); break;
-                }
-                jp++;
-                if (++st == ring.stages) st = 0;
+                case 1: keys_to_tmem<1, D>(raw, tid, rel, dst, wait, ke, par); break;
+                case 2: keys_to_tmem<2, D>(raw, tid, rel, dst, wait, ke, par); break;
+                case 3: keys_to_tmem<3, D>(raw, tid, rel, dst, wait, ke, par); break;
+                case 4: keys_to_tmem<4, D>(raw, tid, rel, dst, wait, ke, par); break;
+                case 5: keys_to_tmem<5, D>(raw, tid, rel, dst, wait, ke, par); break;
+                case 6: keys_to_tmem<6, D>(raw, tid, rel, dst, wait, ke, par); break;
+                case 7: keys_to_tmem<7, D>(raw, tid, rel, dst, wait, ke, par); break;
+                default: keys_to_tmem<8, D>(raw, tid, rel, dst, wait, ke, par); break;
             }
+            if (++st == ring.stages) st = 0;
             tmem_wait_st();
             tc_before();
             __syncwarp();
@@ -864,38 +922,26 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
         float2 l[CW / 2];
 #pragma unroll
         for (int c = 0; c < CW / 2; c++) l[c] = make_float2(0.f, 0.f);
-        int jp = 0;
-        bool fp16 = false;
-        float inv = 1.f;  // 1 / s of the value levels
         for (int j = 0; j < n_tiles; j++) {
             const int b = j & 1;
             const unsigned par = (j >> 1) & 1;
-            const bool first = w.first;
-            const int left = w.n - w.t * kTreeTile, part = w.part;
-            const bool full = left >= kTreeTile, valid = tok < left;
-            if (w.fresh) {
-                ev++;
-                const TreeSeg &s = p.seg[w.seg];
-                fp16 = s.seg.fp16;
-                inv = fp16 ? 1.f : lv.inv[s.law][s.seg.vbits[w.x.h]];
-                wait(c_full(ev & 3), (ev >> 2) & 1);
-            }
-            bool last = true;
-            if (j + 1 < n_tiles) {
-                walk_next(p, w);
-                last = w.first;
-            }
-            const float *ab = reinterpret_cast<const float *>(sm + C::O_A) + (ev & 3) * R + wg * CW;
+            // S^T of this tile (and P^T V of tile j - 2, which came before it: its P buffer is free)
             wait(s_full(b), par);
             __syncwarp();
             tc_after();
-            // the token's scales (landed before its keys were unpacked; behind the last token: anything)
+            const int4 d = *reinterpret_cast<const int4 *>(sm + C::O_D + (j % kSlots) * 64);  // flags, left, part, inv
+            const bool first = d.x & kFirst, fp16 = d.x & kFp16, valid = tok < d.y;
+            if (d.x & kFresh) {
+                ev++;
+                wait(c_full(ev & 3), (ev >> 2) & 1);
+            }
+            const float *ab = reinterpret_cast<const float *>(sm + C::O_A) + (ev & 3) * R + wg * CW;
+            // the token's scales (behind the last token: anything)
             float ks = 1.f, sig = 1.f;
             if (!fp16) {
-                const float *sc = reinterpret_cast<const float *>(sm + C::O_S) + (jp % kScaleSlots) * 256 + tok;
+                const float *sc = reinterpret_cast<const float *>(sm + C::O_S) + (j % kSlots) * 256 + tok;
                 ks = sc[0];
-                sig = sc[128] * inv;
-                jp++;
+                sig = sc[128] * __int_as_float(d.w);
             }
             if (!valid) ks = sig = 0.f;
             float u[CW];
@@ -984,13 +1030,12 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             __syncwarp();
             if (lane == 0) bar_arrive(s_empty(b));
             const float sv = sig * pow2(-E);
-            if (!full && !valid) {  // behind the last token: weight zero, whatever lies there
+            if (!valid) {  // behind the last token: weight zero, whatever lies there
 #pragma unroll
                 for (int c = 0; c < CW; c++) u[c] = -kInf;
             }
 #pragma unroll
             for (int c = 0; c < CW; c++) u[c] = ex2(u[c]);
-            if (j >= 2) wait(p_empty(b), par ^ 1);
             uint8_t *prow = sm + C::O_P + b * C::PBUF + tok * 128;
 #pragma unroll
             for (int c = 0; c < CW; c += 8) {
@@ -1009,8 +1054,8 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             tc_before();
             __syncwarp();
             if (lane == 0) bar_arrive(p_full(b));
-            if (last) {  // the part's record
-                float *rec = p.part + static_cast<size_t>(worker + part) * R * (D + 4);
+            if (d.x & kLast) {  // the part's record
+                float *rec = p.part + static_cast<size_t>(worker + d.z) * R * (D + 4);
                 // row sums over the tokens
 #pragma unroll
                 for (int c = 0; c < CW; c++) {
