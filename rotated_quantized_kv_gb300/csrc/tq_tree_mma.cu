@@ -12,9 +12,9 @@
 // rows, so a small tree wastes no tensor rows, and a token's key scale is one
 // number per thread.  Key codes enter the MMA as they lie in the record: one
 // AND leaves a code at bit s of an fp16 half, the exact (sub)normal code 2^(s -
-// 24); the query element that meets it carries 2^(13 - s), and the affine map of
-// the level, the scale m_t and the row's power of two are applied to the sum:
-//   x = m_t (A_r U + B_r).
+// 24); the query element that meets it carries 2^(13 - s).  The affine map of the
+// level adds a constant per row, which one more 16-deep step (constant columns in TMEM)
+// brings into the sum, so that x = m_t A U with one A for the block.
 // q enters as fp16 hi + lo (22 bits; the lo products run over the same TMEM
 // operand), P as fp16 p sigma, value levels as fp16(s c_k) with s chosen on the
 // host so that the levels round closely; 1/s is part of sigma.
@@ -72,32 +72,6 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     return r;
 }
 
-// ---------------------------------------------------------------- packed binary32 pairs
-__device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("{.reg .b64 ra, rb, rc, rr;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n mov.b64 rc, {%6, %7};\n"
-        " fma.rn.f32x2 rr, ra, rb, rc;\n mov.b64 {%0, %1}, rr;}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
-
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
-    float2 r;
-    asm("{.reg .b64 ra, rb, rr;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n add.rn.f32x2 rr, ra, rb;\n"
-        " mov.b64 {%0, %1}, rr;}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
-    float2 r;
-    asm("{.reg .b64 ra, rb, rr;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n mul.rn.f32x2 rr, ra, rb;\n"
-        " mov.b64 {%0, %1}, rr;}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -155,6 +129,12 @@ struct Waiter {
 };
 
 // ---------------------------------------------------------------- tensor cores
+// K-major operand without swizzle, 16 of k: 8 rows of 16 bytes, the second 8 of k 128 B
+// further, the next 8 rows 256 B further.
+__device__ __forceinline__ uint64_t desc_k16(unsigned addr) {
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 16) |
+           (static_cast<uint64_t>(256 >> 4) << 32) | (1ull << 46);
+}
 // K-major operand, 128-byte swizzle: rows of 64 elements (128 B), 8-row groups 1024 B apart.
 __device__ __forceinline__ uint64_t desc_k(unsigned addr) {
     return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
@@ -381,20 +361,20 @@ struct Mma {
     static constexpr int kThreads = 32 * (kLoadWarp + 2);
     static constexpr int HALVES = D / 64;
     static constexpr int QPART = HALVES * R * 128;  // hi or lo of a block's queries
-    static constexpr int QBUF = 2 * QPART;
+    static constexpr int QBUF = 2 * QPART + (R * 32 + 1023) / 1024 * 1024;  // hi, lo, and the 16-deep step that adds the rows' constants
     static constexpr int VBUF = HALVES * 128 * 128;
     static constexpr int PBUF = 128 * 128;
     static constexpr int KCOLS = D / 2;             // TMEM columns of a K tile
-    static constexpr int T_K = 0, T_S = 2 * KCOLS, T_O = T_S + 2 * R;
+    static constexpr int T_K = 0, T_S = 2 * KCOLS, T_O = T_S + 2 * R, T_C = T_O + R;  // (T_C: 8 constant columns)
     static constexpr int TCOLS = 512;               // all of TMEM, so that its base is column 0
     static constexpr int O_Q = 0;
-    static constexpr int O_V = O_Q + 2 * QBUF;
+    static constexpr int O_V = (O_Q + 2 * QBUF + 1023) / 1024 * 1024;
     static constexpr int O_P = O_V + 2 * VBUF;
     static constexpr int O_T = O_P + 2 * PBUF;
     static constexpr int O_S = O_T + kTableBytes;   // [kSlots][2][128] scales
     static constexpr int O_D = O_S + kSlots * 1024; // [kSlots] descriptors
-    static constexpr int O_A = O_D + kSlots * 64;   // [4][R] A, [4][R] B
-    static constexpr int O_M = O_A + 8 * R * 4;     // [R] m, [R] -m as used, [R] factors
+    static constexpr int O_A = O_D + kSlots * 64;   // [4] A, then [32] maxima of the query preparation
+    static constexpr int O_M = O_A + 256;           // [R] m, [R] -m as used, [R] factors
     static constexpr int O_X = O_M + 3 * R * 4;     // [NWG][4][CW + 1] maxima of the warps
     static constexpr int O_B = (O_X + NWG * 4 * (CW + 1) * 4 + 15) / 16 * 16;
     static constexpr int kBars = 2 * 8 + 4 + 1 + 1 + 2 * kMaxStages;
@@ -407,52 +387,73 @@ struct RingGeo {
 };
 
 // The queries of a block's rows as the MMA's B operand, for keys of kb bits (0: fp16
-// keys, unrotated queries), and each row's (A, B).  TL lanes hold a row, 16
-// coordinates each; warp `wi` of `nw` takes every nw-th group of 32 / TL rows.
+// keys, unrotated queries), and the factor A.  TL lanes hold a row, 16 coordinates
+// each; warp `wi` of `nw` (which share barrier `id`) takes every nw-th group of 32 / TL
+// rows.  A power of two 2^-e common to the block brings every rotated coordinate
+// below 1: |(R q)_i| <= |q|_2 <= sqrt(d) max |q_i|.  (A row a thousand times smaller than
+// the block's largest still has the precision of fp16, 22 bits being carried.)
 template <int D, int R>
-__device__ __forceinline__ void prepare_queries(const TreeParams &p, const Pos &x, int kb, uint8_t *q, float *ab, int wi,
-                                                int nw) {
+__device__ __forceinline__ void prepare_queries(const TreeParams &p, const Pos &x, int kb, uint8_t *q, float *A,
+                                                unsigned *red, int wi, int nw, int id) {
     using C = Mma<D, R>;
     constexpr int TL = D / 16, RPW = 32 / TL;
     const int lane = threadIdx.x & 31, lt = lane % TL;
     const bool vec = ((reinterpret_cast<uintptr_t>(p.q) | (p.qs[0] * 2) | (p.qs[1] * 2) | (p.qs[2] * 2)) & 15) == 0;
     const uint32_t neg = p.sign_bits[lt >> 1] >> (16 * (lt & 1));
-    for (int r0 = wi * RPW; r0 < R; r0 += nw * RPW) {
-        const int r = r0 + lane / TL, row = x.rb * R + r;
-        float v[16];
+    auto load = [&](int r, uint32_t (&w)[8]) {
+        const int row = x.rb * R + r;
 #pragma unroll
-        for (int i = 0; i < 16; i++) v[i] = 0.f;
-        if (row < p.N * p.g) {
-            const uint16_t *src = p.q + x.b * p.qs[0] + (row / p.g) * p.qs[1] + (x.h * p.g + row % p.g) * p.qs[2] + 16 * lt;
+        for (int i = 0; i < 8; i++) w[i] = 0;
+        if (row >= p.N * p.g) return;
+        const uint16_t *src = p.q + x.b * p.qs[0] + (row / p.g) * p.qs[1] + (x.h * p.g + row % p.g) * p.qs[2] + 16 * lt;
+        if (vec) {
+            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(src)), c = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
+            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = c.x, w[5] = c.y, w[6] = c.z, w[7] = c.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++) w[i] = __ldg(src + 2 * i) | static_cast<uint32_t>(__ldg(src + 2 * i + 1)) << 16;
+        }
+    };
+    int e = 0;
+    if (kb) {
+        unsigned mx = 0;  // fp16 bits of the block's largest finite |q_i|
+        for (int r0 = wi * RPW; r0 < R; r0 += nw * RPW) {
             uint32_t w[8];
-            if (vec) {
-                const uint4 a = __ldg(reinterpret_cast<const uint4 *>(src)), c = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
-                w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = c.x, w[5] = c.y, w[6] = c.z, w[7] = c.w;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; i++) w[i] = __ldg(src + 2 * i) | static_cast<uint32_t>(__ldg(src + 2 * i + 1)) << 16;
-            }
+            load(r0 + lane / TL, w);
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-                v[2 * i] = f.x, v[2 * i + 1] = f.y;
+                const unsigned a = w[i] & 0x7FFFu, c = (w[i] >> 16) & 0x7FFFu;
+                mx = max(mx, max(a < 0x7C00u ? a : 0u, c < 0x7C00u ? c : 0u));
             }
         }
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        if (lane == 0) red[wi] = mx;
+        named_sync(id, 32 * nw);
+        for (int i = 0; i < nw; i++) mx = max(mx, red[i]);
+        const unsigned f = __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(mx))));
+        if (mx) e = static_cast<int>((f >> 23) & 0xFFu) - 126 + (D == 128 ? 4 : 3);
+    }
+    // x = m_t qk_scale (2^(1-b) sum code q + (2^-b - 1) sum q) = m_t A (U + c), U = 2^(-e - 11) sum code q,
+    // c = 2^(-e - 11) (1/2 - 2^(b-1)) sum q
+    if (wi == 0 && lane == 0) *A = kb ? p.qk_scale * pow2(12 - kb + e) : p.qk_scale;
+    for (int r0 = wi * RPW; r0 < R; r0 += nw * RPW) {
+        const int r = r0 + lane / TL;
+        uint32_t raw[8];
+        load(r, raw);
         uint8_t *line = q + (R * 128) * (16 * lt / 64) + r * 128;  // the half of the row with this lane's coordinates
         const int c0 = (16 * lt % 64) / 8;                        // its first 16-byte chunk there
         if (kb == 0) {
 #pragma unroll
-            for (int c = 0; c < 2; c++) {
-                uint32_t w[4];
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const __half2 h = __floats2half2_rn(v[8 * c + 2 * i], v[8 * c + 2 * i + 1]);
-                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
-                }
-                *reinterpret_cast<uint4 *>(line + (((c0 + c) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            if (lt == 0) ab[r] = p.qk_scale, ab[4 * R + r] = 0.f;
+            for (int c = 0; c < 2; c++)
+                *reinterpret_cast<uint4 *>(line + (((c0 + c) ^ (r & 7)) << 4)) =
+                    make_uint4(raw[4 * c], raw[4 * c + 1], raw[4 * c + 2], raw[4 * c + 3]);
             continue;
+        }
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&raw[i]));
+            v[2 * i] = f.x, v[2 * i + 1] = f.y;
         }
         // R q: signs, butterflies 1..8 in the lane, the others across lanes, signs, scale
 #pragma unroll
@@ -472,26 +473,22 @@ __device__ __forceinline__ void prepare_queries(const TreeParams &p, const Pos &
 #pragma unroll
             for (int i = 0; i < 16; i++) v[i] = fmaf(v[i], sg, __shfl_xor_sync(0xffffffffu, v[i], h));
         }
-        float mx = 0.f, sum = 0.f;
+        float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; i++) {
             v[i] *= ((neg >> i) & 1u) ? -p.inv_sqrt_d : p.inv_sqrt_d;
-            mx = fmaxf(mx, fabsf(v[i]));
             sum += v[i];
         }
 #pragma unroll
-        for (int h = 1; h < TL; h <<= 1) {
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, h));
-            sum += __shfl_xor_sync(0xffffffffu, sum, h);
-        }
-        // f = 2^-e, f mx in [0.5, 1) (non-finite rows: f = 1, they stay their own)
-        int e = 0;
-        if (mx > 0.f && mx < kInf) e = static_cast<int>((__float_as_uint(mx) >> 23) & 0xFFu) - 126;
-        e = max(-100, min(100, e));
-        // x = m_t qk_scale (2^(1-b) sum code q + (2^-b - 1) sum q), U = f 2^-11 sum code q
+        for (int h = 1; h < TL; h <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, h);
+        // the row's constant, met by 2^-11 twice (hi, lo): 8 rows of 16 bytes per k half
         if (lt == 0) {
-            ab[r] = p.qk_scale * pow2(12 - kb + e);
-            ab[4 * R + r] = p.qk_scale * (pow2(-kb) - 1.0f) * sum;
+            const float y = sum * pow2(-e) * (0.5f - pow2(kb - 1));
+            const __half hi = __float2half_rn(y), lo = __float2half_rn(y - __half2float(hi));
+            uint8_t *at = q + 2 * C::QPART + (r >> 3) * 256 + (r & 7) * 16;
+            *reinterpret_cast<uint4 *>(at) = make_uint4(
+                static_cast<uint32_t>(__half_as_ushort(hi)) | static_cast<uint32_t>(__half_as_ushort(lo)) << 16, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(at + 128) = make_uint4(0, 0, 0, 0);
         }
         // coordinate 32 g + i + 16 u meets the code at place 32 g + 2 i + u, at bit s_i: times 2^(13 - s_i)
         uint32_t w[16];  // hi, lo
@@ -669,7 +666,8 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
     if (warp < kValueWarp) {
         const Walk w = walk_begin(p, at0);
         prepare_queries<D, R>(p, w.x, p.seg[w.seg].seg.fp16 ? 0 : p.seg[w.seg].seg.kbits[w.x.h], sm + C::O_Q,
-                              reinterpret_cast<float *>(sm + C::O_A), warp, kValueWarp);
+                              reinterpret_cast<float *>(sm + C::O_A), reinterpret_cast<unsigned *>(sm + C::O_A) + 4, warp,
+                              kValueWarp, 6);
         fence_async();
         named_sync(6, 32 * kValueWarp);
     }
@@ -755,6 +753,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < D / 16; k++)
                             mma_ts(d, a + 8 * k, q + ((C::QPART + (k >> 2) * R * 128 + 32 * (k & 3)) >> 4), id_s, 1);
+                        mma_ts(d, C::T_C, desc_k16(sb + C::O_Q + (ev & 1) * C::QBUF + 2 * C::QPART), id_s, 1);
                     }
                     mma_commit(k_empty(b));
                     mma_commit(s_full(b));
@@ -849,6 +848,10 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
         const int kw = warp - kKeyWarp, tid = threadIdx.x - kKeyWarp * 32;
         const unsigned lanes = static_cast<unsigned>(32 * kw) << 16;
         int ev = -1, st = 0, kb = 0;
+        {
+            const uint32_t c[8] = {0x10001000u, 0, 0, 0, 0, 0, 0, 0};  // 2^-11 twice, zeros
+            tmem_st8(tbase + lanes + C::T_C, c);
+        }
         for (int j = 0; j < n_tiles; j++) {
             const int b = j & 1;
             const unsigned dst = tbase + lanes + C::T_K + b * C::KCOLS, par = ((j >> 1) & 1) ^ 1, rel = r_empty(st),
@@ -867,7 +870,9 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                     Pos x;
                     x.b = d.b, x.h = d.h, x.rb = d.rb;
                     prepare_queries<D, R>(p, x, kb, sm + C::O_Q + (ev & 1) * C::QBUF,
-                                          reinterpret_cast<float *>(sm + C::O_A) + (ev & 3) * R, kw, 4);
+                                          reinterpret_cast<float *>(sm + C::O_A) + (ev & 3),
+                                          // (maxima of two changes: a warp may be a change ahead of another's reads)
+                                          reinterpret_cast<unsigned *>(sm + C::O_A) + 28 + 4 * (ev & 1), kw, 4, 7);
                     fence_async();
                     __syncwarp();
                 }
@@ -919,9 +924,9 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
         float *m_row = reinterpret_cast<float *>(sm + C::O_M) + wg * CW;  // m; + R: -m as used; + 2R: factors
         float *maxima = reinterpret_cast<float *>(sm + C::O_X) + wg * 4 * (CW + 1);
         int ev = -1, E = 0;
-        float2 l[CW / 2];
+        float l[CW], A = 1.f, down_e = 1.f;  // down_e: 2^-E
 #pragma unroll
-        for (int c = 0; c < CW / 2; c++) l[c] = make_float2(0.f, 0.f);
+        for (int c = 0; c < CW; c++) l[c] = 0.f;
         for (int j = 0; j < n_tiles; j++) {
             const int b = j & 1;
             const unsigned par = (j >> 1) & 1;
@@ -934,8 +939,8 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             if (d.x & kFresh) {
                 ev++;
                 wait(c_full(ev & 3), (ev >> 2) & 1);
+                A = reinterpret_cast<const float *>(sm + C::O_A)[ev & 3];
             }
-            const float *ab = reinterpret_cast<const float *>(sm + C::O_A) + (ev & 3) * R + wg * CW;
             // the token's scales (behind the last token: anything)
             float ks = 1.f, sig = 1.f;
             if (!fp16) {
@@ -943,39 +948,36 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 ks = sc[0];
                 sig = sc[128] * __int_as_float(d.w);
             }
+            ks *= A;
             if (!valid) ks = sig = 0.f;
             float u[CW];
             const unsigned s_addr = tbase + lanes + C::T_S + b * R + wg * CW;
-            // x = ks (A U + B), less m
-            auto scores = [&](bool less) {
+            // x - m, x = ks U (ks holds the factor A too)
+            auto scores = [&] {
                 tmem_ld<CW>(s_addr, u);
 #pragma unroll
                 for (int c = 0; c < CW; c += 4) {
-                    const float4 A = *reinterpret_cast<const float4 *>(ab + c), B = *reinterpret_cast<const float4 *>(ab + 4 * R + c);
-                    float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (less) m = *reinterpret_cast<const float4 *>(m_row + R + c);
-                    float2 y = ffma2(make_float2(u[c], u[c + 1]), make_float2(A.x, A.y), make_float2(B.x, B.y));
-                    y = ffma2(y, make_float2(ks, ks), make_float2(m.x, m.y));
-                    u[c] = y.x, u[c + 1] = y.y;
-                    y = ffma2(make_float2(u[c + 2], u[c + 3]), make_float2(A.z, A.w), make_float2(B.z, B.w));
-                    y = ffma2(y, make_float2(ks, ks), make_float2(m.z, m.w));
-                    u[c + 2] = y.x, u[c + 3] = y.y;
+                    const float4 m = *reinterpret_cast<const float4 *>(m_row + R + c);
+                    u[c] = fmaf(u[c], ks, m.x);
+                    u[c + 1] = fmaf(u[c + 1], ks, m.y);
+                    u[c + 2] = fmaf(u[c + 2], ks, m.z);
+                    u[c + 3] = fmaf(u[c + 3], ks, m.w);
                 }
             };
             bool raise = first;
             if (!first) {
-                scores(true);
+                scores();
                 float top = fmaxf(u[0], u[1]);
 #pragma unroll
                 for (int c = 2; c < CW; c += 2) top = fmax3(top, u[c], u[c + 1]);
-                raise = valid && (top > 8.0f || sig * pow2(-E) > 128.0f);
+                raise = valid && (top > 8.0f || sig * down_e > 128.0f);
             }
             if (named_or(1 + wg, 128, raise)) {
-                scores(false);
+                tmem_ld<CW>(s_addr, u);
                 float mine = -kInf;
 #pragma unroll
                 for (int c = 0; c < CW; c++) {
-                    float v = valid ? u[c] : -kInf;
+                    float v = valid ? u[c] * ks : -kInf;
                     asm("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(v));
                     if (lane == c) mine = v;
                 }
@@ -1014,8 +1016,8 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 8; i += 2) {
                             const float f0 = m_row[2 * R + c + i], f1 = m_row[2 * R + c + i + 1];
-                            l[(c + i) / 2].x *= f0;
-                            l[(c + i) / 2].y *= f1;
+                            l[c + i] *= f0;
+                            l[c + i + 1] *= f1;
                             r[i] = __float_as_uint(o[i] * (f0 * down));
                             r[i + 1] = __float_as_uint(o[i + 1] * (f1 * down));
                         }
@@ -1024,28 +1026,27 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                     tmem_wait_st();
                 }
                 E = now;
-                scores(true);
+                down_e = pow2(-E);
+                scores();
             }
             tc_before();
             __syncwarp();
             if (lane == 0) bar_arrive(s_empty(b));
-            const float sv = sig * pow2(-E);
-            if (!valid) {  // behind the last token: weight zero, whatever lies there
+            const float sv = sig * down_e;
+            if (__any_sync(0xffffffffu, !valid)) {  // behind the last token: weight zero, whatever lies there
 #pragma unroll
-                for (int c = 0; c < CW; c++) u[c] = -kInf;
+                for (int c = 0; c < CW; c++) u[c] = valid ? u[c] : -kInf;
             }
-#pragma unroll
-            for (int c = 0; c < CW; c++) u[c] = ex2(u[c]);
             uint8_t *prow = sm + C::O_P + b * C::PBUF + tok * 128;
 #pragma unroll
             for (int c = 0; c < CW; c += 8) {
                 uint32_t h[4];
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const float2 pr = make_float2(u[c + 2 * i], u[c + 2 * i + 1]);
-                    l[c / 2 + i] = fadd2(l[c / 2 + i], pr);
-                    const float2 wt = fmul2(pr, make_float2(sv, sv));
-                    const __half2 q = __floats2half2_rn(wt.x, wt.y);
+                    const float p0 = ex2(u[c + 2 * i]), p1 = ex2(u[c + 2 * i + 1]);
+                    l[c + 2 * i] += p0;
+                    l[c + 2 * i + 1] += p1;
+                    const __half2 q = __floats2half2_rn(p0 * sv, p1 * sv);
                     h[i] = *reinterpret_cast<const uint32_t *>(&q);
                 }
                 *reinterpret_cast<uint4 *>(prow + ((((wg * CW + c) >> 3) ^ (tok & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
@@ -1059,13 +1060,13 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 // row sums over the tokens
 #pragma unroll
                 for (int c = 0; c < CW; c++) {
-                    float v = c & 1 ? l[c / 2].y : l[c / 2].x;
+                    float v = l[c];
 #pragma unroll
                     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
                     if (lane == 0) maxima[qw * (CW + 1) + c] = v;
                 }
 #pragma unroll
-                for (int c = 0; c < CW / 2; c++) l[c] = make_float2(0.f, 0.f);
+                for (int c = 0; c < CW; c++) l[c] = 0.f;
                 named_sync(1 + wg, 128);
                 if (tok < CW) {
                     float *row = rec + (wg * CW + tok) * (D + 4);
@@ -1133,7 +1134,7 @@ void fit_levels(HostLevels &h, const float *c, int bits) {
 template <int D, int R>
 cudaError_t tree_mma(const TreeParams &p, const TreeLevels &lv, cudaStream_t s) {
     using C = Mma<D, R>;
-    static_assert(C::T_O + R <= 512, "TMEM columns");
+    static_assert(C::T_C + 8 <= 512, "TMEM columns");
     int stage = 0;
     for (int i = 0; i < p.n_packed; i++)
         for (int h = 0; h < p.H; h++) stage = std::max(stage, 128 * (D / 8) * (p.seg[i].seg.kbits[h] + p.seg[i].seg.vbits[h]));
