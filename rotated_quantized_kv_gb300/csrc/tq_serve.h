@@ -87,8 +87,8 @@ cudaError_t launch_read(const ReadParams &p, int dtype, cudaStream_t s);
 // ----------------------------------------------------------------- tree attention
 // The work is a list of 128-token tiles.  For sequence b in order, KV head h,
 // block of query rows rb (of R rows; row = draft * g + query head of the group):
-// the tiles of b's packed segments, then those of its fp16 segments.  G workers
-// take equal contiguous ranges of the list.  The tiles of one (b, h, rb) are cut
+// the tiles of b's packed segments, then those of its fp16 segments.  The workers
+// take contiguous ranges of the list, all of the same length but the last.  The tiles of one (b, h, rb) are cut
 // into parts: packed tiles every kTreePart, the fp16 ones likewise; every worker
 // leaves one record (m, l, sum per row) for each part that it touches, at slot
 // worker + part index (the pairs (worker, part) form a monotone path, so that
@@ -101,6 +101,30 @@ struct TreeSeg {
     const int *len;              // per-sequence length or nullptr
     int n_tokens;
     int law;                     // value codebook
+};
+
+// What the merge needs of it: the list's geometry without the segments' data.
+struct TreeListSeg {
+    const int *len;
+    int n_tokens;
+};
+struct TreeList {
+    int B, H, g, N, R, n_rb;
+    int n_seg, n_packed, ragged;
+    int parts_packed, parts, workers;
+    TreeListSeg seg[TQ_MAX_SEGMENTS];
+};
+struct TreeMergeParams {
+    TreeList t;
+    const uint16_t *q, *k, *v;
+    int64_t qs[3], ks[3], vs[3];
+    const uint32_t *mask;
+    int64_t mask_stride;
+    int mask_words;
+    uint16_t *out;
+    const float *part;
+    uint32_t sign_bits[kMaxD / 32];
+    float inv_sqrt_d, qk_scale;
 };
 
 struct TreeParams {
@@ -117,6 +141,12 @@ struct TreeParams {
     int mask_words;
     uint16_t *out;
     float *part;                 // records: [slot][R][d + 4]: m (log2 units), l, pad, pad, sum
+    // tensor-core form: the query blocks as MMA operands, one image per (b, h, rb) and
+    // key width among the head's segments
+    uint8_t *images;
+    int n_var;
+    uint8_t var[TQ_MAX_SEGMENTS][kMaxH];     // image of a segment
+    uint8_t var_bits[TQ_MAX_SEGMENTS][kMaxH];  // key bits of image v (0: fp16 keys)
     int *error;
     int workers, wait_polls;
     uint32_t sign_bits[kMaxD / 32];
@@ -136,6 +166,9 @@ struct TreeLevels {
 // Whether a head dimension takes the tensor-core form (64 and 128).
 inline bool tree_on_tensor_cores(int d) { return d == 64 || d == 128; }
 cudaError_t launch_tree_mma(const TreeParams &p, cudaStream_t s);
+// Bytes of a query image: hi and lo parts (rows of d fp16), 32 bytes a row for the
+// constants' step, and the factor A.
+inline size_t tree_image_bytes(int d, int R) { return (static_cast<size_t>(4) * d * R + 32 * R + 16 + 127) / 128 * 128; }
 TreeShape tree_shape(int B, int H, int g, int N, int d, long long tiles_per_head);
 cudaError_t launch_tree(const TreeParams &p, cudaStream_t s);
 

@@ -162,8 +162,8 @@ tq_status check_tree_view(const tq_layer_view *lv, int B, int H, int Hq, int d, 
             if (L.capacity % 16) return TQ_ERR_ALIGN;
         }
     }
-    // blocks of query rows per KV head; the kernels count tiles and slots in 32 bits
-    if (static_cast<int64_t>(N) * (Hq / H) > (1 << 20)) return TQ_ERR_UNSUPPORTED;
+    // query rows are counted in 32 bits
+    if (static_cast<int64_t>(N) * Hq > 0x7fffffff / B) return TQ_ERR_UNSUPPORTED;
     return TQ_OK;
 }
 
@@ -173,7 +173,9 @@ int tiles_of(int n) { return n / kTreeTile + (n % kTreeTile ? 1 : 0); }
 struct TreeLayout {
     TreeShape shape;
     int parts_packed, parts;
-    size_t part_off, total;
+    int n_var;
+    uint8_t var[TQ_MAX_SEGMENTS][kMaxH], var_bits[TQ_MAX_SEGMENTS][kMaxH];  // packed segments first
+    size_t image_off, part_off, total;
 };
 
 tq_status tree_layout(const tq_layer_view *lv, int B, int H, int Hq, int d, int N, TreeLayout &o) {
@@ -183,10 +185,32 @@ tq_status tree_layout(const tq_layer_view *lv, int B, int H, int Hq, int d, int 
     o.shape = tree_shape(B, H, Hq / H, N, d, tp + tf);
     const int64_t pp = (tp + kTreePart - 1) / kTreePart, pf = (tf + kTreePart - 1) / kTreePart;
     const int64_t slots = o.shape.workers + static_cast<int64_t>(B) * H * o.shape.n_rb * (pp + pf);
-    if (slots > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
+    if (slots > 0x7fffffff || static_cast<int64_t>(B) * H * o.shape.n_rb * (tp + tf) > 0x7fffffff)
+        return TQ_ERR_UNSUPPORTED;  // tiles and slots are counted in 32 bits
     o.parts_packed = static_cast<int>(pp);
     o.parts = static_cast<int>(pp + pf);
-    o.part_off = 256;  // the error flag has the first 256 bytes
+    // distinct key widths among each head's segments (fp16: 0)
+    o.n_var = 0;
+    std::memset(o.var, 0, sizeof(o.var));
+    std::memset(o.var_bits, 0, sizeof(o.var_bits));
+    for (int h = 0; h < H; ++h) {
+        int n = 0, at = 0;
+        for (int pass = 0; pass < 2; ++pass)
+            for (int i = 0; i < lv->n_segments; ++i) {
+                const tq_segment &sg = lv->seg[i];
+                if ((sg.kind == TQ_SEG_FP16) != (pass == 1)) continue;
+                const uint8_t kb = pass ? 0 : sg.layout.kbits[h];
+                int v = 0;
+                while (v < n && o.var_bits[v][h] != kb) ++v;
+                if (v == n) o.var_bits[n++][h] = kb;
+                o.var[at++][h] = static_cast<uint8_t>(v);
+            }
+        o.n_var = std::max(o.n_var, n);
+    }
+    o.image_off = 256;  // the error flag has the first 256 bytes
+    o.part_off = o.image_off;
+    if (tree_on_tensor_cores(d))
+        o.part_off += static_cast<size_t>(B) * H * o.shape.n_rb * o.n_var * tree_image_bytes(d, o.shape.R);
     o.total = o.part_off + static_cast<size_t>(slots) * o.shape.R * (d + 4) * sizeof(float);
     return TQ_OK;
 }
@@ -441,6 +465,10 @@ tq_status tq_tree_attention(const tq_layer_view *layer, int batch, int n_heads, 
     p.mask_words = (p.N + 31) / 32;
     p.out = static_cast<uint16_t *>(tree->out);
     p.error = static_cast<int *>(workspace);
+    p.images = static_cast<uint8_t *>(workspace) + o.image_off;
+    p.n_var = o.n_var;
+    std::memcpy(p.var, o.var, sizeof(p.var));
+    std::memcpy(p.var_bits, o.var_bits, sizeof(p.var_bits));
     p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + o.part_off);
     p.wait_polls = decode_wait_polls();
     std::memcpy(p.sign_bits, layer->rot.sign_bits, sizeof(p.sign_bits));

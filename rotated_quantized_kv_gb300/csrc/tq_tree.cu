@@ -65,10 +65,11 @@ __global__ void __launch_bounds__(kTreeThreads) tree_plain_kernel(const __grid_c
     float *row_m = S + R * TT, *row_l = row_m + R, *row_c = row_l + R;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.error = 0;
-    const long long T = total_tiles(p), G = workers_of(p, T), c = blockIdx.x;
-    if (c >= G) return;
-    long long at = c * T / G;
-    const long long end = (c + 1) * T / G;
+    asm volatile("griddepcontrol.launch_dependents;");
+    const unsigned T = total_tiles(p), per = worker_tiles(p, T), c = blockIdx.x;
+    unsigned at = c * per;
+    if (at >= T) return;
+    const unsigned end = min(at + per, T);
     Walk w = walk_begin(p, at);
     float acc[R][DPT];
     int part = -1;
@@ -83,7 +84,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_plain_kernel(const __grid_c
     };
     auto flush = [&] {  // the record of `part`
         __syncthreads();
-        float *rec = p.part + static_cast<size_t>(c + part) * R * (D + 4);
+        float *rec = p.part + (static_cast<size_t>(c) + part) * R * (D + 4);
         for (int r = threadIdx.x; r < R; r += kTreeThreads) {
             rec[r * (D + 4)] = row_m[r];
             rec[r * (D + 4) + 1] = row_l[r];
@@ -179,69 +180,42 @@ __global__ void __launch_bounds__(kTreeThreads) tree_plain_kernel(const __grid_c
 }
 
 // ---------------------------------------------------------------- merge
-// A warp per query row: every record of its group in order, R on the packed share,
-// then the drafted tokens that the row sees, in binary32 (few tokens per row, so
-// that neither the mask nor a non-finite value of an unseen draft can reach the
-// row), the quotient, and the fp16 row.
+// A warp per query row: the drafted tokens that the row sees, in binary32 (few tokens
+// per row, so that neither the mask nor a non-finite value of an unseen draft can
+// reach the row), every record of its group in order, R on the packed share, the
+// quotient, and the fp16 row.  The call's bytes here are few; what counts is the
+// chain of loads, so F drafts' or U records' loads are in flight at a time, and the
+// drafts come before the wait for the records (the grid may start while the last
+// CTAs of the main kernel run).
 template <int D>
-__global__ void __launch_bounds__(kTreeThreads) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(kTreeThreads) tree_merge_kernel(const __grid_constant__ TreeMergeParams p) {
     constexpr int J = (D + 31) / 32;
+    constexpr int F = J <= 8 ? 4 : 32 / J, U = J <= 4 ? 8 : 32 / J;
     __shared__ float draft_x[kTreeWarps][TQ_MAX_DRAFTS];
-    constexpr int U = J <= 4 ? 8 : 32 / J, F = J <= 4 ? 4 : J <= 16 ? 16 / J : 1;  // records and drafts in flight
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long rows = static_cast<long long>(p.N) * p.g;
-    const long long id = blockIdx.x * static_cast<long long>(kTreeWarps) + warp;  // (b, h, row)
-    if (id >= rows * p.B * p.H) return;
-    const int row = static_cast<int>(id % rows), bh = static_cast<int>(id / rows);
-    const int b = bh / p.H, h = bh % p.H, rb = row / p.R, r = row % p.R;
-    const int draft = row / p.g, head = h * p.g + row % p.g;
-    const long long T = total_tiles(p), G = workers_of(p, T);
-    int tp, tf;
-    seq_tiles(p, b, tp, tf);
-    long long first = 0;  // first tile of the group
-    if (p.ragged) {
-        for (int i = lane; i < b; i += 32) {
-            int a, c;
-            seq_tiles(p, i, a, c);
-            first += a + c;
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
-    } else {
-        first = static_cast<long long>(b) * (tp + tf);
-    }
-    first = first * p.H * p.n_rb + (static_cast<long long>(h) * p.n_rb + rb) * (tp + tf);
-    const long long group = (static_cast<long long>(b) * p.H + h) * p.n_rb + rb;
-    const int np = (tp + kTreePart - 1) / kTreePart, nf = (tf + kTreePart - 1) / kTreePart;
+    const int rows = p.t.N * p.t.g;
+    const unsigned id = blockIdx.x * kTreeWarps + warp;  // (b, h, row)
+    if (id >= static_cast<unsigned>(rows) * p.t.B * p.t.H) return;
+    const int bh = id / rows, row = id - bh * rows;
+    const int b = bh / p.t.H, h = bh - b * p.t.H, rb = row / p.t.R, r = row - rb * p.t.R;
+    const int draft = row / p.t.g, head = h * p.t.g + row - draft * p.t.g;
     float M = -kInf, L = 0.f, a[2][J];
     bool nan = false;  // fmaxf passes over NaN: a row that sees only NaN scores is NaN, not empty
 #pragma unroll
     for (int j = 0; j < J; j++) a[0][j] = a[1][j] = 0.f;
-    // part i (packed ones, then the others): workers lo..hi hold its records
-    struct Part {
-        long long lo, hi, slot;
-    };
-    auto part_at = [&](int i) {
-        const int k0 = i < np ? i * kTreePart : tp + (i - np) * kTreePart;
-        const int k1 = min(k0 + kTreePart, i < np ? tp : tp + tf);
-        Part q;
-        q.lo = worker_of(first + k0, T, G);
-        q.hi = worker_of(first + k1 - 1, T, G);
-        q.slot = part_of(p, group, tp, k0);
-        return q;
-    };
-    auto record = [&](const Part &q, long long w) { return p.part + (static_cast<size_t>(w + q.slot) * p.R + r) * (D + 4); };
     // scores of the drafts that the row sees, each over the whole warp
     float q[J];
 #pragma unroll
     for (int j = 0; j < J; j++) {
         const int e = lane + 32 * j;
-        q[j] = e < D ? __half2float(__ushort_as_half(p.q[b * p.qs[0] + draft * p.qs[1] + head * p.qs[2] + e])) : 0.f;
+        q[j] = e < D ? __half2float(__ushort_as_half(__ldg(p.q + b * p.qs[0] + draft * p.qs[1] + head * p.qs[2] + e))) : 0.f;
     }
     const uint16_t *K = p.k + b * p.ks[0] + h * p.ks[1], *V = p.v + b * p.vs[0] + h * p.vs[1];
     int n = 0;
+#pragma unroll 1
     for (int w = 0; w < p.mask_words; w++) {
-        for (uint32_t m = seen_word(p, b, draft, w); m;) {
+#pragma unroll 1
+        for (uint32_t m = seen_word(p, p.t.N, b, draft, w); m;) {
             const int some = min(__popc(m), F);
             float s[F];
 #pragma unroll
@@ -271,77 +245,110 @@ __global__ void __launch_bounds__(kTreeThreads) tree_merge_kernel(const __grid_c
         }
     }
     __syncwarp();
-    // the largest of the records' maxima, a record per lane
-    for (int i = 0; i < np + nf; i++) {
-        const Part pt = part_at(i);
-        for (long long w = pt.lo + lane; w <= pt.hi; w += 32) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(record(pt, w)));
-            M = fmaxf(M, ml.x);
-            nan |= ml.y != ml.y;
-        }
-    }
+    n = 0;
+#pragma unroll 1
+    for (int w = 0; w < p.mask_words && M != -kInf; w++) {
+#pragma unroll 1
+        for (uint32_t m = seen_word(p, p.t.N, b, draft, w); m;) {
+            const int some = min(__popc(m), F);
+            float v[F][J], f[F];
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    nan = __any_sync(0xffffffffu, nan);
-    if (M != -kInf) {
-        for (int i = 0; i < np + nf; i++) {
-            const Part pt = part_at(i);
-            const int kind = i < np ? 0 : 1;
-            for (long long w0 = pt.lo; w0 <= pt.hi; w0 += U) {  // U records' loads in flight
-                const int cnt = static_cast<int>(min(static_cast<long long>(U), pt.hi - w0 + 1));
-                float2 ml = make_float2(-kInf, 0.f);
-                if (lane < cnt) ml = __ldcg(reinterpret_cast<const float2 *>(record(pt, w0 + lane)));
-                float v[U][J];
+            for (int i = 0; i < F; i++) {
+                f[i] = 0.f;
 #pragma unroll
-                for (int u = 0; u < U; u++)
+                for (int j = 0; j < J; j++) v[i][j] = 0.f;
+                if (i < some) {
+                    const uint16_t *at = V + (32 * w + __ffs(m) - 1) * p.vs[2];
+                    m &= m - 1;
+                    f[i] = ex2(draft_x[warp][n + i] - M);
 #pragma unroll
                     for (int j = 0; j < J; j++)
-                        v[u][j] = u < cnt && lane + 32 * j < D ? __ldcg(record(pt, w0 + u) + 4 + lane + 32 * j) : 0.f;
-                const float f = ex2(ml.x - M);
-#pragma unroll
-                for (int u = 0; u < U; u++) {
-                    const float fu = __shfl_sync(0xffffffffu, f, u);
-                    L = fmaf(__shfl_sync(0xffffffffu, ml.y, u), fu, L);
-#pragma unroll
-                    for (int j = 0; j < J; j++) {
-                        if (kind) a[1][j] = fmaf(fu, v[u][j], a[1][j]);
-                        else a[0][j] = fmaf(fu, v[u][j], a[0][j]);
-                    }
+                        if (lane + 32 * j < D) v[i][j] = __half2float(__ushort_as_half(__ldg(at + lane + 32 * j)));
                 }
             }
+            n += some;
+#pragma unroll
+            for (int i = 0; i < F; i++) {
+                L += f[i];
+#pragma unroll
+                for (int j = 0; j < J; j++) a[1][j] = fmaf(f[i], v[i][j], a[1][j]);
+            }
         }
-        n = 0;
-        for (int w = 0; w < p.mask_words; w++) {
-            for (uint32_t m = seen_word(p, b, draft, w); m;) {
-                const int some = min(__popc(m), F);
-                float v[F][J], f[F];
+    }
+    // where the group's tiles lie in the list
+    const unsigned T = total_tiles(p.t), per = worker_tiles(p.t, T);
+    int tp, tf;
+    seq_tiles(p.t, b, tp, tf);
+    unsigned first = 0;
+    if (p.t.ragged) {
+        for (int i = lane; i < b; i += 32) {
+            int x, y;
+            seq_tiles(p.t, i, x, y);
+            first += x + y;
+        }
+        first = __reduce_add_sync(0xffffffffu, first);
+    } else {
+        first = b * (tp + tf);
+    }
+    first = first * p.t.H * p.t.n_rb + (h * p.t.n_rb + rb) * (tp + tf);
+    const int group = bh * p.t.n_rb + rb;
+    const int np = (tp + kTreePart - 1) / kTreePart, nf = (tf + kTreePart - 1) / kTreePart;
+    // part i (packed ones, then the others): workers lo..hi hold its records
+    // (records in order: the parts', within one its workers')
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+#pragma unroll 1
+    for (int base = 0;; base += 32) {  // a record per lane, then U of them at a time
+        int slot = -1, kind = 0, before = 0;
+#pragma unroll 1
+        for (int i = 0; i < np + nf; i++) {
+            const int k0 = i < np ? i * kTreePart : tp + (i - np) * kTreePart;
+            const int k1 = min(k0 + kTreePart, i < np ? tp : tp + tf);
+            const int lo = (first + k0) / per, hi = (first + k1 - 1) / per, at = base + lane - before;
+            if (at >= 0 && at <= hi - lo) slot = lo + at + part_of(p.t, group, tp, k0), kind = i >= np;
+            before += hi - lo + 1;
+        }
+        if (base >= before) break;
+        const int count = min(32, before - base);
+        const float *rec = p.part + (static_cast<size_t>(max(slot, 0)) * p.t.R + r) * (D + 4);
+        float2 ml = make_float2(-kInf, 0.f);
+        if (slot >= 0) ml = __ldcg(reinterpret_cast<const float2 *>(rec));
+        float now = fmaxf(M, ml.x);
+        nan |= ml.y != ml.y;
 #pragma unroll
-                for (int i = 0; i < F; i++) {
-                    f[i] = 0.f;
+        for (int o = 16; o >= 1; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+        if (now == -kInf) continue;
+        const float old = M == -kInf ? 0.f : ex2(M - now), f = ex2(ml.x - now);
+        M = now;
+        L *= old;
 #pragma unroll
-                    for (int j = 0; j < J; j++) v[i][j] = 0.f;
-                    if (i < some) {
-                        const uint16_t *at = V + (32 * w + __ffs(m) - 1) * p.vs[2];
-                        m &= m - 1;
-                        f[i] = ex2(draft_x[warp][n + i] - M);
+        for (int j = 0; j < J; j++) a[0][j] *= old, a[1][j] *= old;
+#pragma unroll 1
+        for (int u0 = 0; u0 < count; u0 += U) {
+            float v[U][J];
 #pragma unroll
-                        for (int j = 0; j < J; j++)
-                            if (lane + 32 * j < D) v[i][j] = __half2float(__ushort_as_half(__ldg(at + lane + 32 * j)));
-                    }
-                }
-                n += some;
+            for (int u = 0; u < U; u++) {
+                const int s = __shfl_sync(0xffffffffu, slot, u0 + u);
+                const float *at = p.part + (static_cast<size_t>(max(s, 0)) * p.t.R + r) * (D + 4) + 4 + lane;
 #pragma unroll
-                for (int i = 0; i < F; i++) {
-                    L += f[i];
+                for (int j = 0; j < J; j++) v[u][j] = s >= 0 && lane + 32 * j < D ? __ldcg(at + 32 * j) : 0.f;
+            }
 #pragma unroll
-                    for (int j = 0; j < J; j++) a[1][j] = fmaf(f[i], v[i][j], a[1][j]);
+            for (int u = 0; u < U; u++) {
+                const float fu = __shfl_sync(0xffffffffu, f, u0 + u);
+                const bool raw = __shfl_sync(0xffffffffu, kind, u0 + u);
+                L = fmaf(__shfl_sync(0xffffffffu, ml.y, u0 + u), fu, L);
+#pragma unroll
+                for (int j = 0; j < J; j++) {
+                    a[0][j] = fmaf(raw ? 0.f : fu, v[u][j], a[0][j]);
+                    a[1][j] = fmaf(raw ? fu : 0.f, v[u][j], a[1][j]);
                 }
             }
         }
     }
+    nan = __any_sync(0xffffffffu, nan);
     warp_rotate_strided<D>(a[0], p.sign_bits, p.inv_sqrt_d, lane);
     const float inv = nan ? __int_as_float(0x7fffffff) : L == 0.f ? 0.f : 1.0f / L;  // nothing seen: zeros
-    uint16_t *out = p.out + ((static_cast<size_t>(b) * p.N + draft) * p.H * p.g + head) * D;
+    uint16_t *out = p.out + ((static_cast<size_t>(b) * p.t.N + draft) * p.t.H * p.t.g + head) * D;
 #pragma unroll
     for (int j = 0; j < J; j++)
         if (lane + 32 * j < D) out[lane + 32 * j] = __half_as_ushort(__float2half_rn((a[0][j] + a[1][j]) * inv));
@@ -350,7 +357,10 @@ __global__ void __launch_bounds__(kTreeThreads) tree_merge_kernel(const __grid_c
 template <int D>
 cudaError_t tree_dim(const TreeParams &p, cudaStream_t s) {
     cudaError_t e;
-    if constexpr (D == 64 || D == 128) {
+    if (p.n_seg == 0) {  // drafts alone
+        e = cudaMemsetAsync(p.error, 0, sizeof(int), s);
+        if (e != cudaSuccess) return e;
+    } else if constexpr (D == 64 || D == 128) {
         e = launch_tree_mma(p, s);
         if (e != cudaSuccess) return e;
     } else {
@@ -361,9 +371,27 @@ cudaError_t tree_dim(const TreeParams &p, cudaStream_t s) {
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
+    TreeMergeParams m;
+    m.t.B = p.B, m.t.H = p.H, m.t.g = p.g, m.t.N = p.N, m.t.R = p.R, m.t.n_rb = p.n_rb;
+    m.t.n_seg = p.n_seg, m.t.n_packed = p.n_packed, m.t.ragged = p.ragged;
+    m.t.parts_packed = p.parts_packed, m.t.parts = p.parts, m.t.workers = p.workers;
+    for (int i = 0; i < TQ_MAX_SEGMENTS; i++) m.t.seg[i].len = p.seg[i].len, m.t.seg[i].n_tokens = p.seg[i].n_tokens;
+    m.q = p.q, m.k = p.k, m.v = p.v, m.mask = p.mask, m.out = p.out, m.part = p.part;
+    m.mask_stride = p.mask_stride, m.mask_words = p.mask_words;
+    for (int i = 0; i < 3; i++) m.qs[i] = p.qs[i], m.ks[i] = p.ks[i], m.vs[i] = p.vs[i];
+    std::copy(p.sign_bits, p.sign_bits + kMaxD / 32, m.sign_bits);
+    m.inv_sqrt_d = p.inv_sqrt_d, m.qk_scale = p.qk_scale;
     const long long rows = static_cast<long long>(p.N) * p.g * p.B * p.H;
-    tree_merge_kernel<D><<<static_cast<unsigned>((rows + kTreeWarps - 1) / kTreeWarps), kTreeThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((rows + kTreeWarps - 1) / kTreeWarps));
+    cfg.blockDim = dim3(kTreeThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.n_seg > 0 ? 1 : 0;  // (behind a kernel)
+    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, m);
 }
 
 }  // namespace

@@ -7,13 +7,15 @@
 namespace tqk {
 namespace tree {
 
-__device__ __forceinline__ int seg_tokens(const TreeParams &p, int i, int b) {
-    const TreeSeg &s = p.seg[i];
+template <typename P>
+__device__ __forceinline__ int seg_tokens(const P &p, int i, int b) {
+    const auto &s = p.seg[i];
     return s.len ? min(max(s.len[b], 0), s.n_tokens) : s.n_tokens;
 }
 
 // Tiles of sequence b's packed segments, and of its fp16 ones.
-__device__ __forceinline__ void seq_tiles(const TreeParams &p, int b, int &tp, int &tf) {
+template <typename P>
+__device__ __forceinline__ void seq_tiles(const P &p, int b, int &tp, int &tf) {
     tp = 0;
     tf = 0;
     for (int i = 0; i < p.n_seg; i++) {
@@ -23,29 +25,30 @@ __device__ __forceinline__ void seq_tiles(const TreeParams &p, int b, int &tp, i
     }
 }
 
-// Tiles of the whole call.  A warp takes 32 sequences at a time; all lanes
-// return the sum.
-__device__ __forceinline__ long long total_tiles(const TreeParams &p) {
-    const long long per = static_cast<long long>(p.H) * p.n_rb;
+// Tiles of the whole call (below 2^31, which the host checks for the segments'
+// n_tokens).  A warp takes 32 sequences at a time; all lanes return the sum.
+template <typename P>
+__device__ __forceinline__ unsigned total_tiles(const P &p) {
+    const unsigned per = p.H * p.n_rb;
     int tp, tf;
     if (!p.ragged) {
         seq_tiles(p, 0, tp, tf);
         return per * p.B * (tp + tf);
     }
-    long long sum = 0;
+    unsigned sum = 0;
     for (int b = threadIdx.x & 31; b < p.B; b += 32) {
         seq_tiles(p, b, tp, tf);
         sum += tp + tf;
     }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return per * sum;
+    return per * __reduce_add_sync(0xffffffffu, sum);
 }
 
-// Workers that share T tiles: every one of them has a tile (the launch is sized
-// for the segments' n_tokens, the lengths on the device may be shorter).
-__device__ __forceinline__ long long workers_of(const TreeParams &p, long long T) {
-    return T < p.workers ? T : p.workers;
+// Tiles of a worker: worker c has [c n, (c + 1) n) of the T, n = ceil(T / workers)
+// (every worker that starts below T has a tile; the launch is sized for the
+// segments' n_tokens, the lengths on the device may be shorter).
+template <typename P>
+__device__ __forceinline__ unsigned worker_tiles(const P &p, unsigned T) {
+    return max((T + p.workers - 1) / p.workers, 1u);
 }
 
 struct Pos {
@@ -55,29 +58,29 @@ struct Pos {
 };
 
 // The place of tile `at` < total_tiles in the list (whole warp, `at` uniform).
-__device__ __forceinline__ Pos seek(const TreeParams &p, long long at) {
+__device__ __forceinline__ Pos seek(const TreeParams &p, unsigned at) {
     Pos x;
-    const long long per = static_cast<long long>(p.H) * p.n_rb;
+    const unsigned per = p.H * p.n_rb;
     x.b = 0;
     if (!p.ragged) {
         seq_tiles(p, 0, x.tp, x.tf);
-        const long long each = per * (x.tp + x.tf);
-        x.b = static_cast<int>(at / each);
+        const unsigned each = per * (x.tp + x.tf);
+        x.b = at / each;
         at -= x.b * each;
     } else {
         const int lane = threadIdx.x & 31;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             int tp = 0, tf = 0;
             if (b0 + lane < p.B) seq_tiles(p, b0 + lane, tp, tf);
-            long long end = per * (tp + tf);
+            unsigned end = per * (tp + tf);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, end, o);
+                const unsigned y = __shfl_up_sync(0xffffffffu, end, o);
                 if (lane >= o) end += y;
             }
             const unsigned past = __ballot_sync(0xffffffffu, end > at);
             const int l = past ? __ffs(past) - 1 : 31;
-            const long long upto = __shfl_sync(0xffffffffu, end, l);
+            const unsigned upto = __shfl_sync(0xffffffffu, end, l);
             x.b = b0 + l;
             x.tp = __shfl_sync(0xffffffffu, tp, l);
             x.tf = __shfl_sync(0xffffffffu, tf, l);
@@ -88,9 +91,8 @@ __device__ __forceinline__ Pos seek(const TreeParams &p, long long at) {
             at -= upto;
         }
     }
-    const long long tiles = x.tp + x.tf;
-    const int hr = static_cast<int>(at / tiles);
-    x.k = static_cast<int>(at - hr * tiles);
+    const unsigned tiles = x.tp + x.tf, hr = at / tiles;
+    x.k = at - hr * tiles;
     x.h = hr / p.n_rb;
     x.rb = hr - x.h * p.n_rb;
     return x;
@@ -112,18 +114,12 @@ __device__ __forceinline__ void advance(const TreeParams &p, Pos &x) {
     }
 }
 
-__device__ __forceinline__ long long group_of(const TreeParams &p, const Pos &x) {
-    return (static_cast<long long>(x.b) * p.H + x.h) * p.n_rb + x.rb;
-}
+__device__ __forceinline__ int group_of(const TreeParams &p, const Pos &x) { return (x.b * p.H + x.h) * p.n_rb + x.rb; }
 
 // Index of the part that tile k of group `group` belongs to.
-__device__ __forceinline__ long long part_of(const TreeParams &p, long long group, int tp, int k) {
+template <typename P>
+__device__ __forceinline__ int part_of(const P &p, int group, int tp, int k) {
     return group * p.parts + (k < tp ? k / kTreePart : p.parts_packed + (k - tp) / kTreePart);
-}
-
-// Worker of tile t when G workers share T tiles, worker c taking [c T / G, (c + 1) T / G).
-__device__ __forceinline__ long long worker_of(long long t, long long T, long long G) {
-    return ((t + 1) * G + T - 1) / T - 1;
 }
 
 // A walk along the list: the current tile holds tokens [128 t, min(128 (t + 1), n))
@@ -140,7 +136,7 @@ struct Walk {
 __device__ __forceinline__ void walk_locate(const TreeParams &p, Walk &w) {
     const bool packed = w.x.k < w.x.tp;
     int k = packed ? w.x.k : w.x.k - w.x.tp;
-    w.part = static_cast<int>(part_of(p, group_of(p, w.x), w.x.tp, w.x.k));
+    w.part = part_of(p, group_of(p, w.x), w.x.tp, w.x.k);
     w.seg = packed ? 0 : p.n_packed;
     for (;; w.seg++) {  // (ends: k counts the tiles of these segments)
         w.n = seg_tokens(p, w.seg, w.x.b);
@@ -151,7 +147,7 @@ __device__ __forceinline__ void walk_locate(const TreeParams &p, Walk &w) {
     w.t = k;
     w.fresh = true;
 }
-__device__ __forceinline__ Walk walk_begin(const TreeParams &p, long long at) {
+__device__ __forceinline__ Walk walk_begin(const TreeParams &p, unsigned at) {
     Walk w;
     w.x = seek(p, at);
     walk_locate(p, w);
@@ -176,8 +172,9 @@ __device__ __forceinline__ void walk_next(const TreeParams &p, Walk &w) {
 }
 
 // Word w of the drafts that draft i of sequence b sees.
-__device__ __forceinline__ uint32_t seen_word(const TreeParams &p, int b, int i, int w) {
-    const int left = p.N - 32 * w;
+template <typename P>
+__device__ __forceinline__ uint32_t seen_word(const P &p, int N, int b, int i, int w) {
+    const int left = N - 32 * w;
     const uint32_t real = left >= 32 ? 0xffffffffu : (1u << left) - 1u;  // bits behind the last draft mean nothing
     if (p.mask) return p.mask[b * p.mask_stride + static_cast<int64_t>(i) * p.mask_words + w] & real;
     return (i >= 32 * w + 31 ? 0xffffffffu : i < 32 * w ? 0u : (2u << (i - 32 * w)) - 1u) & real;

@@ -95,6 +95,15 @@ __device__ __forceinline__ bool bar_try(unsigned bar, unsigned parity) {
         : "memory");
     return ok != 0;
 }
+__device__ __forceinline__ void bar_expect_tx(unsigned bar, unsigned bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_load(unsigned dst, const void *src, unsigned bytes, unsigned bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+        "r"(bytes), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -343,8 +352,9 @@ struct TileDesc {
     int left;      // tokens from the tile's first to the sequence's last in this segment
     int part;
     float inv;     // 1 / s of the value levels
-    int b, h, rb, seg;
-    int t, pad[7];
+    int b, h, seg, t;
+    float A;       // of the query image
+    int pad[7];
 };
 static_assert(sizeof(TileDesc) == 64, "slot size");
 constexpr int kFirst = 1, kLast = 2;  // of its part
@@ -361,7 +371,8 @@ struct Mma {
     static constexpr int kThreads = 32 * (kLoadWarp + 2);
     static constexpr int HALVES = D / 64;
     static constexpr int QPART = HALVES * R * 128;  // hi or lo of a block's queries
-    static constexpr int QBUF = 2 * QPART + (R * 32 + 1023) / 1024 * 1024;  // hi, lo, and the 16-deep step that adds the rows' constants
+    static constexpr int QIMG = 2 * QPART + R * 32;  // hi, lo, and the 16-deep step that adds the rows' constants
+    static constexpr int QBUF = (QIMG + 1023) / 1024 * 1024;
     static constexpr int VBUF = HALVES * 128 * 128;
     static constexpr int PBUF = 128 * 128;
     static constexpr int KCOLS = D / 2;             // TMEM columns of a K tile
@@ -373,14 +384,18 @@ struct Mma {
     static constexpr int O_T = O_P + 2 * PBUF;
     static constexpr int O_S = O_T + kTableBytes;   // [kSlots][2][128] scales
     static constexpr int O_D = O_S + kSlots * 1024; // [kSlots] descriptors
-    static constexpr int O_A = O_D + kSlots * 64;   // [4] A, then [32] maxima of the query preparation
-    static constexpr int O_M = O_A + 256;           // [R] m, [R] -m as used, [R] factors
+    static constexpr int O_M = O_D + kSlots * 64;   // [R] m, [R] -m as used, [R] factors
     static constexpr int O_X = O_M + 3 * R * 4;     // [NWG][4][CW + 1] maxima of the warps
     static constexpr int O_B = (O_X + NWG * 4 * (CW + 1) * 4 + 15) / 16 * 16;
-    static constexpr int kBars = 2 * 8 + 4 + 1 + 1 + 2 * kMaxStages;
+    static constexpr int kBars = 2 * 8 + 2 * 2 + 1 + 1 + 2 * kMaxStages;
     static constexpr int O_RING = (O_B + kBars * 8 + 16 + 127) / 128 * 128;
     static constexpr int kRing = kSmemMax - 1024 - O_RING;  // (1024: alignment)
 };
+
+template <int D, int R>
+__host__ __device__ constexpr int tree_image_stride() {
+    return (Mma<D, R>::QIMG + 16 + 127) / 128 * 128;
+}
 
 struct RingGeo {
     int stage, stages;
@@ -388,24 +403,24 @@ struct RingGeo {
 
 // The queries of a block's rows as the MMA's B operand, for keys of kb bits (0: fp16
 // keys, unrotated queries), and the factor A.  TL lanes hold a row, 16 coordinates
-// each; warp `wi` of `nw` (which share barrier `id`) takes every nw-th group of 32 / TL
-// rows.  A power of two 2^-e common to the block brings every rotated coordinate
+// each; warp `wi` of the block's `nw` takes every nw-th group of 32 / TL rows.  A power
+// of two 2^-e common to the block brings every rotated coordinate
 // below 1: |(R q)_i| <= |q|_2 <= sqrt(d) max |q_i|.  (A row a thousand times smaller than
 // the block's largest still has the precision of fp16, 22 bits being carried.)
 template <int D, int R>
-__device__ __forceinline__ void prepare_queries(const TreeParams &p, const Pos &x, int kb, uint8_t *q, float *A,
-                                                unsigned *red, int wi, int nw, int id) {
+__device__ __forceinline__ void prepare_queries(const TreeParams &p, int b, int h, int rb, int kb, uint8_t *q, float *A,
+                                                unsigned *red, int wi, int nw) {
     using C = Mma<D, R>;
     constexpr int TL = D / 16, RPW = 32 / TL;
     const int lane = threadIdx.x & 31, lt = lane % TL;
     const bool vec = ((reinterpret_cast<uintptr_t>(p.q) | (p.qs[0] * 2) | (p.qs[1] * 2) | (p.qs[2] * 2)) & 15) == 0;
     const uint32_t neg = p.sign_bits[lt >> 1] >> (16 * (lt & 1));
     auto load = [&](int r, uint32_t (&w)[8]) {
-        const int row = x.rb * R + r;
+        const int row = rb * R + r;
 #pragma unroll
         for (int i = 0; i < 8; i++) w[i] = 0;
         if (row >= p.N * p.g) return;
-        const uint16_t *src = p.q + x.b * p.qs[0] + (row / p.g) * p.qs[1] + (x.h * p.g + row % p.g) * p.qs[2] + 16 * lt;
+        const uint16_t *src = p.q + b * p.qs[0] + (row / p.g) * p.qs[1] + (h * p.g + row % p.g) * p.qs[2] + 16 * lt;
         if (vec) {
             const uint4 a = __ldg(reinterpret_cast<const uint4 *>(src)), c = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
             w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = c.x, w[5] = c.y, w[6] = c.z, w[7] = c.w;
@@ -428,7 +443,7 @@ __device__ __forceinline__ void prepare_queries(const TreeParams &p, const Pos &
         }
         mx = __reduce_max_sync(0xffffffffu, mx);
         if (lane == 0) red[wi] = mx;
-        named_sync(id, 32 * nw);
+        __syncthreads();
         for (int i = 0; i < nw; i++) mx = max(mx, red[i]);
         const unsigned f = __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(mx))));
         if (mx) e = static_cast<int>((f >> 23) & 0xFFu) - 126 + (D == 128 ? 4 : 3);
@@ -516,6 +531,21 @@ __device__ __forceinline__ void prepare_queries(const TreeParams &p, const Pos &
             *reinterpret_cast<uint4 *>(line + C::QPART + at) = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
         }
     }
+}
+
+constexpr int kPrepWarps = 8;
+// A CTA per (b, h, rb) and image.  (The main kernel may start meanwhile: it waits
+// for this grid before it touches the images.)
+template <int D, int R>
+__global__ void __launch_bounds__(32 * kPrepWarps) tree_queries_kernel(const __grid_constant__ TreeParams p) {
+    __shared__ unsigned red[kPrepWarps];
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.error = 0;
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int v = blockIdx.x % p.n_var, group = blockIdx.x / p.n_var;
+    const int bh = group / p.n_rb, rb = group - bh * p.n_rb, b = bh / p.H, h = bh - b * p.H;
+    uint8_t *image = p.images + (static_cast<size_t>(group) * p.n_var + v) * tree_image_stride<D, R>();
+    prepare_queries<D, R>(p, b, h, rb, p.var_bits[v][h], image, reinterpret_cast<float *>(image + Mma<D, R>::QIMG), red,
+                          threadIdx.x >> 5, kPrepWarps);
 }
 
 template <int KB, int D>
@@ -616,18 +646,21 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
     auto s_empty = [&](int i) { return bars + 8u * (10 + i); };
     auto p_full = [&](int i) { return bars + 8u * (12 + i); };
     auto p_empty = [&](int i) { return bars + 8u * (14 + i); };
-    auto c_full = [&](int i) { return bars + 8u * (16 + i); };
+    auto q_full = [&](int i) { return bars + 8u * (16 + i); };
+    auto q_empty = [&](int i) { return bars + 8u * (18 + i); };
     const unsigned o_free = bars + 8u * 20, drain = bars + 8u * 21;
     auto r_full = [&](int i) { return bars + 8u * (22 + i); };
     auto r_empty = [&](int i) { return bars + 8u * (22 + kMaxStages + i); };
     int *dead = reinterpret_cast<int *>(sm + C::O_B + C::kBars * 8);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(dead + 1);
 
-    if (blockIdx.x == 0 && threadIdx.x == 0 && p.wait_polls > 0) *p.error = 0;
-    const long long T = total_tiles(p), G = workers_of(p, T), worker = blockIdx.x;
-    if (worker >= G) return;
-    const long long at0 = worker * T / G;
-    const int n_tiles = static_cast<int>((worker + 1) * T / G - at0);
+    asm volatile("griddepcontrol.launch_dependents;");  // (the merge waits for this grid's end)
+    const unsigned T = total_tiles(p), per = worker_tiles(p, T), worker = blockIdx.x, at0 = worker * per;
+    if (at0 >= T) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // no CTA ends before the grid that it depends on
+        return;
+    }
+    const int n_tiles = static_cast<int>(min(per, T - at0));
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; i++) {
@@ -640,7 +673,10 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             bar_init(p_full(i), 4 * C::NWG);
             bar_init(p_empty(i), 1);
         }
-        for (int i = 0; i < 4; i++) bar_init(c_full(i), 4);
+        for (int i = 0; i < 2; i++) {
+            bar_init(q_full(i), 1);
+            bar_init(q_empty(i), 1);
+        }
         bar_init(o_free, 4 * C::NWG);
         bar_init(drain, 1);
         for (int i = 0; i < kMaxStages; i++) {
@@ -662,24 +698,15 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
     constexpr unsigned tbase = 0;
     const Waiter wait{dead, p.error, p.wait_polls};
 
-    // the first queries, by every warp that has nothing to do yet
-    if (warp < kValueWarp) {
-        const Walk w = walk_begin(p, at0);
-        prepare_queries<D, R>(p, w.x, p.seg[w.seg].seg.fp16 ? 0 : p.seg[w.seg].seg.kbits[w.x.h], sm + C::O_Q,
-                              reinterpret_cast<float *>(sm + C::O_A), reinterpret_cast<unsigned *>(sm + C::O_A) + 4, warp,
-                              kValueWarp, 6);
-        fence_async();
-        named_sync(6, 32 * kValueWarp);
-    }
-
     if (warp >= kLoadWarp) {
         // ------------------------------------------------------ records and scales: keys, values
         const int kv = warp - kLoadWarp;
         const uint8_t *src = nullptr;
         const float *scale = nullptr;
-        int rec = 0, off = 0, st = 0, kind = 0;
-        float inv = 1.f;
+        int rec = 0, off = 0, st = 0, kind = 0, ev = -1, issued = -1;
+        float inv = 1.f, A = 1.f;
         Walk w = walk_begin(p, at0);
+        if (kv == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // the query images
         for (int j = 0; j < n_tiles; j++) {
             if (w.fresh) {
                 const SegView &s = p.seg[w.seg].seg;
@@ -696,11 +723,26 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                     scale = (kv ? s.vs : s.ks) + (static_cast<size_t>(w.x.b) * p.H + w.x.h) * s.capacity + 4 * lane;
                 }
             }
+            if (w.fresh && kv == 0) {
+                // the queries for this segment's key width, into the buffer of two changes ago
+                ev++;
+                const uint8_t *image = p.images + (static_cast<size_t>(group_of(p, w.x)) * p.n_var + p.var[w.seg][w.x.h]) *
+                                                      tree_image_stride<D, R>();
+                wait(q_empty(ev & 1), ((ev >> 1) & 1) ^ 1);
+                __syncwarp();
+                if (lane == 0 && !*dead) {
+                    issued = ev;
+                    bar_expect_tx(q_full(ev & 1), C::QIMG);
+                    bulk_load(sb + C::O_Q + (ev & 1) * C::QBUF, image, C::QIMG, q_full(ev & 1));
+                }
+                A = __ldcg(reinterpret_cast<const float *>(image + C::QIMG));
+            }
             TileDesc d;
+            d.A = A;
             d.left = w.n - w.t * kTreeTile;
             d.part = w.part;
             d.inv = inv;
-            d.b = w.x.b, d.h = w.x.h, d.rb = w.x.rb, d.seg = w.seg, d.t = w.t;
+            d.b = w.x.b, d.h = w.x.h, d.seg = w.seg, d.t = w.t;
             d.flags = kind | (w.first ? kFirst : 0) | (w.fresh || j == 0 ? kFresh : 0);
             const int n = min(kTreeTile, d.left), chunks = (n * rec + 15) / 16;
             const uint8_t *from = src + static_cast<size_t>(w.t) * (kTreeTile * rec);
@@ -712,7 +754,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             if (kv == 0 && lane == 0) {
                 TileDesc *to = reinterpret_cast<TileDesc *>(sm + C::O_D) + j % kSlots;
                 to->flags = d.flags, to->left = d.left, to->part = d.part, to->inv = d.inv;
-                to->b = d.b, to->h = d.h, to->rb = d.rb, to->seg = d.seg, to->t = d.t;
+                to->b = d.b, to->h = d.h, to->seg = d.seg, to->t = d.t, to->A = d.A;
                 bar_arrive(r_full(st));
             }
             // chunk c = lane + 32 i goes to c ^ ((c >> 3) & m): the same for every i but m = 7's third bit
@@ -727,6 +769,11 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             if (++st == ring.stages) st = 0;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
+        // the last query images have landed before shared memory goes away
+        if (kv == 0 && lane == 0)
+            for (int e = max(issued - 1, 0); e <= issued; e++)
+                for (int i = 0; i < kDrainPolls; i++)
+                    if (bar_try(q_full(e & 1), (e >> 1) & 1)) break;
     } else if (warp == kIssueWarp) {
         // ------------------------------------------------------ MMA issue
         constexpr uint32_t id_s = idesc(R, false), id_o = idesc(R, true);
@@ -740,7 +787,13 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 const int flags = reinterpret_cast<const TileDesc *>(sm + C::O_D)[j % kSlots].flags;
                 first = flags & kFirst;
                 const bool fp16 = flags & kFp16;
-                if (flags & kFresh) ev++;
+                if (flags & kFresh) {
+                    // the products with the old queries are behind this point; the new ones' image
+                    if (ev >= 0 && elect_one()) mma_commit(q_empty(ev & 1));
+                    __syncwarp();
+                    ev++;
+                    wait(q_full(ev & 1), (ev >> 1) & 1);
+                }
                 wait(s_empty(b), ((j >> 1) & 1) ^ 1);
                 tc_after();
                 const uint64_t q = desc_k(sb + C::O_Q + (ev & 1) * C::QBUF);
@@ -844,10 +897,10 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             if (lane == 0) bar_arrive(v_full(b));
         }
     } else if (warp >= kKeyWarp) {
-        // ------------------------------------------------------ queries, and keys into TMEM
+        // ------------------------------------------------------ keys into TMEM
         const int kw = warp - kKeyWarp, tid = threadIdx.x - kKeyWarp * 32;
         const unsigned lanes = static_cast<unsigned>(32 * kw) << 16;
-        int ev = -1, st = 0, kb = 0;
+        int st = 0;
         {
             const uint32_t c[8] = {0x10001000u, 0, 0, 0, 0, 0, 0, 0};  // 2^-11 twice, zeros
             tmem_st8(tbase + lanes + C::T_C, c);
@@ -859,25 +912,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             wait(r_full(st), (j / ring.stages) & 1);
             __syncwarp();
             const TileDesc &d = reinterpret_cast<const TileDesc *>(sm + C::O_D)[j % kSlots];
-            if (d.flags & kFresh) {
-                ev++;
-                kb = (d.flags >> 8) & 15;
-                if (ev > 0) {
-                    // this segment's queries: the buffer was last read two changes ago, by products
-                    // that came before those of tile j - 2 or were those
-                    wait(ke, par);
-                    __syncwarp();
-                    Pos x;
-                    x.b = d.b, x.h = d.h, x.rb = d.rb;
-                    prepare_queries<D, R>(p, x, kb, sm + C::O_Q + (ev & 1) * C::QBUF,
-                                          reinterpret_cast<float *>(sm + C::O_A) + (ev & 3),
-                                          // (maxima of two changes: a warp may be a change ahead of another's reads)
-                                          reinterpret_cast<unsigned *>(sm + C::O_A) + 28 + 4 * (ev & 1), kw, 4, 7);
-                    fence_async();
-                    __syncwarp();
-                }
-                if (lane == 0) bar_arrive(c_full(ev & 3));
-            }
+            const int kb = (d.flags >> 8) & 15;
             switch (kb) {
                 case 0: {
                     const SegView &s = p.seg[d.seg].seg;
@@ -923,7 +958,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
         const unsigned lanes = static_cast<unsigned>(32 * qw) << 16;
         float *m_row = reinterpret_cast<float *>(sm + C::O_M) + wg * CW;  // m; + R: -m as used; + 2R: factors
         float *maxima = reinterpret_cast<float *>(sm + C::O_X) + wg * 4 * (CW + 1);
-        int ev = -1, E = 0;
+        int E = 0;
         float l[CW], A = 1.f, down_e = 1.f;  // down_e: 2^-E
 #pragma unroll
         for (int c = 0; c < CW; c++) l[c] = 0.f;
@@ -936,11 +971,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             tc_after();
             const int4 d = *reinterpret_cast<const int4 *>(sm + C::O_D + (j % kSlots) * 64);  // flags, left, part, inv
             const bool first = d.x & kFirst, fp16 = d.x & kFp16, valid = tok < d.y;
-            if (d.x & kFresh) {
-                ev++;
-                wait(c_full(ev & 3), (ev >> 2) & 1);
-                A = reinterpret_cast<const float *>(sm + C::O_A)[ev & 3];
-            }
+            if (d.x & kFresh) A = reinterpret_cast<const TileDesc *>(sm + C::O_D)[j % kSlots].A;
             // the token's scales (behind the last token: anything)
             float ks = 1.f, sig = 1.f;
             if (!fp16) {
@@ -1056,7 +1087,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             __syncwarp();
             if (lane == 0) bar_arrive(p_full(b));
             if (d.x & kLast) {  // the part's record
-                float *rec = p.part + static_cast<size_t>(worker + d.z) * R * (D + 4);
+                float *rec = p.part + (static_cast<size_t>(worker) + d.z) * R * (D + 4);
                 // row sums over the tokens
 #pragma unroll
                 for (int c = 0; c < CW; c++) {
@@ -1142,12 +1173,23 @@ cudaError_t tree_mma(const TreeParams &p, const TreeLevels &lv, cudaStream_t s) 
     ring.stage = std::max(stage, 128);
     ring.stages = std::min(kMaxStages, C::kRing / ring.stage);
     if (ring.stages < 1) return cudaErrorInvalidConfiguration;
-    const size_t smem = kSmemMax;
-    cudaError_t e = cudaFuncSetAttribute(tree_mma_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    cudaError_t e = cudaFuncSetAttribute(tree_mma_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return e;
-    tree_mma_kernel<D, R><<<p.workers, C::kThreads, smem, s>>>(p, lv, ring);
-    return cudaGetLastError();
+    const int images = p.B * p.H * p.n_rb * p.n_var;
+    tree_queries_kernel<D, R><<<images, 32 * kPrepWarps, 0, s>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.workers);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = kSmemMax;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_mma_kernel<D, R>, p, lv, ring);
 }
 
 }  // namespace
