@@ -29,10 +29,12 @@
 // V^T needs the dims on the lanes, so V goes through shared memory with tokens
 // as the K dimension (MN-major operand).
 //
-// Roles (31 warps, 23 with 16 rows): softmax in four groups of four warps (two), an
-// equal share of the rows each, four warps of keys, eight of values, one that
-// issues the MMAs, two that walk the list and load records and scales (cp.async
-// into a ring); the others learn from a descriptor what a tile is.
+// Roles (19 warps): softmax in two groups of four warps, half of the rows each, four
+// warps of keys, four of values, one that issues the MMAs, two that walk the list
+// and load records and scales (cp.async into a ring); the others learn from a
+// descriptor what a tile is.  What a tile costs beyond its arithmetic is paid per
+// warp (waits, signals, the descriptor: over 100 instructions), so the roles have as
+// few warps as their registers allow.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -120,20 +122,29 @@ __device__ __forceinline__ bool named_or(int id, int threads, bool x) {
     return r != 0;
 }
 
-// A wait that gave up marks the CTA dead: from then on nothing waits, every role
-// walks its range to the end (all addresses come from the list, none from
-// data), and the error flag tells the host that the output is incomplete.
+// A bounded wait.  A thread whose wait ran out waits no more: it walks its range to
+// the end (all addresses come from the list, none from data, and what it signals
+// lets the others end too), and the error flag tells the host that the output is
+// incomplete.
 struct Waiter {
-    volatile int *dead;
     int *error;
     int polls;
-    __device__ __forceinline__ void operator()(unsigned bar, unsigned parity) const {
-        for (int i = 0; i < polls; i++) {
-            if (bar_try(bar, parity)) return;
-            if (*dead) return;
+    bool gone;
+    __device__ __forceinline__ void operator()(unsigned bar, unsigned parity) {
+        if (gone) return;
+        unsigned ok = 0;
+        if (polls > 0)
+            asm volatile(
+                "{\n .reg .pred p, q;\n .reg .s32 n;\n mov.s32 n, %3;\n mov.u32 %0, 1;\n"
+                "POLL:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %4;\n @p bra DONE;\n"
+                " sub.s32 n, n, 1;\n setp.gt.s32 q, n, 0;\n @q bra POLL;\n mov.u32 %0, 0;\nDONE:\n}"
+                : "=r"(ok)
+                : "r"(bar), "r"(parity), "r"(polls), "r"(1000u)
+                : "memory");
+        if (!ok) {
+            gone = true;
+            atomicExch(error, 1);
         }
-        *dead = 1;
-        atomicExch(error, 1);
     }
 };
 
@@ -182,35 +193,51 @@ __device__ __forceinline__ void mma_commit(unsigned bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld16(unsigned a, float *v) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];\ntcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(a)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
+// C columns (8, 16 or 32) of this thread's TMEM lane: the load, and the wait for it, which
+// passes every register through so that no use is scheduled before.
+template <int C>
+__device__ __forceinline__ void tmem_issue(unsigned a, float (&v)[C]) {
+    static_assert(C == 8 || C == 16 || C == 32, "8, 16 or 32 columns");
+    if constexpr (C == 8) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                     : "r"(a)
+                     : "memory");
+    } else if constexpr (C == 16) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+                     : "r"(a)
+                     : "memory");
+    } else {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+                     : "r"(a)
+                     : "memory");
+    }
 }
-// C columns (8 or 16), waited for in the same statement so that no use is scheduled before
+template <int C>
+__device__ __forceinline__ void tmem_wait(float (&v)[C]) {
+    if constexpr (C == 8) {
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7])
+                     :
+                     : "memory");
+    } else if constexpr (C == 16) {
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+                     :
+                     : "memory");
+    } else {
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+                     :
+                     : "memory");
+    }
+}
 template <int C>
 __device__ __forceinline__ void tmem_ld(unsigned a, float (&v)[C]) {
-    if constexpr (C == 8) {
-        uint32_t r[8];
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
-            "tcgen05.wait::ld.sync.aligned;"
-            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-            : "r"(a)
-            : "memory");
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = __uint_as_float(r[i]);
-    } else {
-        static_assert(C == 16, "8 or 16 columns");
-        tmem_ld16(a, v);
-    }
+    tmem_issue<C>(a, v);
+    tmem_wait<C>(v);
 }
 __device__ __forceinline__ void tmem_st8(unsigned a, const uint32_t *r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a), "r"(r[0]),
@@ -348,7 +375,7 @@ __device__ __forceinline__ uint4 level_chunk(const uint32_t *w, const uint8_t *t
 // ---------------------------------------------------------------- tile descriptors
 // What the loader tells the other roles about a tile.
 struct TileDesc {
-    int flags;     // kFirst.. | key bits << 8 | value bits << 16
+    int flags;     // kFirst.. | key bits << 8 | value bits << 16 | law << 20
     int left;      // tokens from the tile's first to the sequence's last in this segment
     int part;
     float inv;     // 1 / s of the value levels
@@ -366,7 +393,7 @@ template <int D, int R>
 struct Mma {
     static constexpr int NWG = R == 16 ? 2 : 4;     // softmax groups of four warps
     static constexpr int CW = R / NWG;              // rows per group
-    static constexpr int kKeyWarp = 4 * NWG, kValueWarp = kKeyWarp + 4, kIssueWarp = kValueWarp + 8,
+    static constexpr int kKeyWarp = 4 * NWG, kValueWarp = kKeyWarp + 4, kIssueWarp = kValueWarp + 4,
                          kLoadWarp = kIssueWarp + 1;
     static constexpr int kThreads = 32 * (kLoadWarp + 2);
     static constexpr int HALVES = D / 64;
@@ -548,67 +575,96 @@ __global__ void __launch_bounds__(32 * kPrepWarps) tree_queries_kernel(const __g
                           threadIdx.x >> 5, kPrepWarps);
 }
 
+// State of a key or value warp's walk through the ring.
+struct RingPos {
+    int j, st;      // tile, ring stage
+    unsigned par;   // parity of the stage's fill
+    __device__ __forceinline__ void next(int stages) {
+        j++;
+        if (++st == stages) st = 0, par ^= 1;
+    }
+};
+// Shared-memory addresses that the key and value warps need.
+struct RoleBars {
+    unsigned r_full, r_empty, full, empty;  // of buffer / stage 0; the next 8 bytes further
+};
+
+// Keys of KB bits from the ring into TMEM, one token a thread, while the tiles have that width.
 template <int KB, int D>
-__device__ __forceinline__ void keys_to_tmem(unsigned raw, int token, unsigned release, unsigned dst, const Waiter &wait,
-                                             unsigned kempty, unsigned parity) {
-    uint32_t w[D / 32 * KB];
-    load_record<D / 32 * KB>(raw, token, w);
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) bar_arrive(release);
-    wait(kempty, parity);
-    __syncwarp();
-    tc_after();
+__device__ __forceinline__ void keys_loop(RingPos &q, int n_tiles, const RingGeo &ring, unsigned ring_base, const uint8_t *descs,
+                                          const RoleBars &bar, unsigned dst, int token, Waiter &wait) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (; q.j < n_tiles; q.next(ring.stages)) {
+        wait(bar.r_full + 8 * q.st, q.par);
+        __syncwarp();
+        if (((reinterpret_cast<const TileDesc *>(descs)[q.j % kSlots].flags >> 8) & 15) != KB) return;
+        uint32_t w[D / 32 * KB];
+        load_record<D / 32 * KB>(ring_base + q.st * ring.stage, token, w);
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar.r_empty + 8 * q.st);
+        const int b = q.j & 1;
+        wait(bar.empty + 8 * b, ((q.j >> 1) & 1) ^ 1);
+        __syncwarp();
+        tc_after();
+        // (a loop that shifts the record down: a quarter of the code, which the instruction caches feel)
+#pragma unroll 1
+        for (int g = 0; g < D / 32; g++) {
+            uint32_t out[16];
+            key_words<KB>(w, out);
+            tmem_st16(dst + b * (D / 2) + 16 * g, out);
 #pragma unroll
-    for (int g = 0; g < D / 32; g++) {
-        uint32_t out[16];
-        key_words<KB>(w + g * KB, out);
-        tmem_st16(dst + 16 * g, out);
-    }
-}
-
-// WORDS words of a token's record (of REC bytes) from word `first` on.
-template <int WORDS, int REC>
-__device__ __forceinline__ void load_part(const uint8_t *base, int token, int first, uint32_t (&w)[WORDS]) {
-    constexpr int m = chunk_mask(REC), step = WORDS % 2 ? 1 : 2;
-#pragma unroll
-    for (int i = 0; i < WORDS; i += step) {
-        const int at = token * REC + 4 * (first + i), c = at >> 4;
-        const uint8_t *q = base + 16 * (c ^ ((c >> 3) & m)) + (at & 15);
-        if constexpr (step == 2) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(q);
-            w[i] = x.x, w[i + 1] = x.y;
-        } else {
-            w[i] = *reinterpret_cast<const uint32_t *>(q);
+            for (int i = 0; i + KB < D / 32 * KB; i++) w[i] = w[i + KB];
         }
+        tmem_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar.full + 8 * b);
     }
 }
-// Half u of the dims of a token's values: record in the ring to fp16 rows.
-template <int VB, int D, int... C>
-__device__ __forceinline__ void level_chunks(const uint32_t *w, const uint8_t *table, uint8_t *line, int token, int u,
-                                             std::integer_sequence<int, C...>) {
-    // chunk C of the half: D = 128, block u of 64 dims; D = 64, chunk 4 u + C of the one block
-    ((*reinterpret_cast<uint4 *>(line + (D == 128 ? u * 16384 + ((C ^ (token & 7)) << 4) : (((4 * u + C) ^ (token & 7)) << 4))) =
-          level_chunk<VB, C>(w, table)),
-     ...);
-}
+
+// Values of VB bits from the ring to fp16 rows, one token a thread, while the tiles have that width (and law).
 template <int VB, int D>
-__device__ __forceinline__ void values_to_smem(const uint8_t *raw, int token, int u, unsigned release, const uint8_t *table,
-                                               uint8_t *dst, const Waiter &wait, unsigned vempty, unsigned parity) {
-    constexpr int words = D / 64 * VB;
-    uint32_t w[words];
-    load_part<words, D / 8 * VB>(raw, token, words * u, w);
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) bar_arrive(release);
-    wait(vempty, parity);
-    level_chunks<VB, D>(w, table + (token & (level_columns(VB) - 1)) * level_bytes(VB), dst + token * 128, token, u,
-                        std::make_integer_sequence<int, D / 16>{});
+__device__ __forceinline__ void values_loop(RingPos &q, int n_tiles, const RingGeo &ring, unsigned ring_base, const uint8_t *descs,
+                                            const RoleBars &bar, const uint8_t *table, uint8_t *dst, int buf, int token,
+                                            int width, Waiter &wait) {
+    const int lane = threadIdx.x & 31;
+    table += (token & (level_columns(VB) - 1)) * level_bytes(VB);
+    dst += token * 128;
+#pragma unroll 1
+    for (; q.j < n_tiles; q.next(ring.stages)) {
+        wait(bar.r_full + 8 * q.st, q.par);
+        __syncwarp();
+        const int flags = reinterpret_cast<const TileDesc *>(descs)[q.j % kSlots].flags;
+        if (flags >> 16 != width) return;
+        uint32_t w[D / 32 * VB];
+        load_record<D / 32 * VB>(ring_base + q.st * ring.stage + kTreeTile * (D / 8) * ((flags >> 8) & 15), token, w);
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar.r_empty + 8 * q.st);
+        const int b = q.j & 1;
+        wait(bar.empty + 8 * b, ((q.j >> 1) & 1) ^ 1);
+#pragma unroll 1
+        for (int g = 0; g < D / 32; g++) {  // 32 dims: four chunks of the line
+            uint8_t *line = dst + b * buf + (g >> 1) * 16384;
+            const int c0 = 4 * (g & 1);
+            *reinterpret_cast<uint4 *>(line + ((c0 ^ (token & 7)) << 4)) = level_chunk<VB, 0>(w, table);
+            *reinterpret_cast<uint4 *>(line + (((c0 + 1) ^ (token & 7)) << 4)) = level_chunk<VB, 1>(w, table);
+            *reinterpret_cast<uint4 *>(line + (((c0 + 2) ^ (token & 7)) << 4)) = level_chunk<VB, 2>(w, table);
+            *reinterpret_cast<uint4 *>(line + (((c0 + 3) ^ (token & 7)) << 4)) = level_chunk<VB, 3>(w, table);
+#pragma unroll
+            for (int i = 0; i + VB < D / 32 * VB; i++) w[i] = w[i + VB];
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar.full + 8 * b);
+    }
 }
 
-// Fill the value table of a width (the eight value warps together).
+// Fill the value table of a width (the four value warps together).
 __device__ __forceinline__ void fill_levels(uint8_t *table, const uint16_t *half, int vb, int tid) {
     const int codes = level_codes(vb), entries = level_entries(vb), cols = level_columns(vb);
     const uint32_t m = (1u << vb) - 1u;
-    for (int i = tid; i < entries * cols; i += 256) {
+    for (int i = tid; i < entries * cols; i += 128) {
         const int e = i / cols;
         if (codes == 4) {
             uint32_t lo = half[e & 1] | static_cast<uint32_t>(half[(e >> 1) & 1]) << 16;
@@ -651,8 +707,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
     const unsigned o_free = bars + 8u * 20, drain = bars + 8u * 21;
     auto r_full = [&](int i) { return bars + 8u * (22 + i); };
     auto r_empty = [&](int i) { return bars + 8u * (22 + kMaxStages + i); };
-    int *dead = reinterpret_cast<int *>(sm + C::O_B + C::kBars * 8);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(dead + 1);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::O_B + C::kBars * 8);
 
     asm volatile("griddepcontrol.launch_dependents;");  // (the merge waits for this grid's end)
     const unsigned T = total_tiles(p), per = worker_tiles(p, T), worker = blockIdx.x, at0 = worker * per;
@@ -666,7 +721,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
         for (int i = 0; i < 2; i++) {
             bar_init(k_full(i), 4);
             bar_init(k_empty(i), 1);
-            bar_init(v_full(i), 8);
+            bar_init(v_full(i), 4);
             bar_init(v_empty(i), 1);
             bar_init(s_full(i), 1);
             bar_init(s_empty(i), 4 * C::NWG);
@@ -681,9 +736,8 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
         bar_init(drain, 1);
         for (int i = 0; i < kMaxStages; i++) {
             bar_init(r_full(i), 65);
-            bar_init(r_empty(i), 12);
+            bar_init(r_empty(i), 8);
         }
-        *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kIssueWarp) {
@@ -696,7 +750,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
     __syncthreads();
     tc_after();
     constexpr unsigned tbase = 0;
-    const Waiter wait{dead, p.error, p.wait_polls};
+    Waiter wait{p.error, p.wait_polls, false};
 
     if (warp >= kLoadWarp) {
         // ------------------------------------------------------ records and scales: keys, values
@@ -715,7 +769,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 inv = 1.f;
                 if (!s.fp16) {
                     const int kb = s.kbits[w.x.h], vb = s.vbits[w.x.h];
-                    kind = kb << 8 | vb << 16;
+                    kind = kb << 8 | vb << 16 | p.seg[w.seg].law << 20;
                     inv = lv.inv[p.seg[w.seg].law][vb];
                     rec = D / 8 * (kv ? vb : kb);
                     off = C::O_RING + (kv ? kTreeTile * (D / 8) * kb : 0);
@@ -730,7 +784,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                                                       tree_image_stride<D, R>();
                 wait(q_empty(ev & 1), ((ev >> 1) & 1) ^ 1);
                 __syncwarp();
-                if (lane == 0 && !*dead) {
+                if (lane == 0 && !wait.gone) {
                     issued = ev;
                     bar_expect_tx(q_full(ev & 1), C::QIMG);
                     bulk_load(sb + C::O_Q + (ev & 1) * C::QBUF, image, C::QIMG, q_full(ev & 1));
@@ -842,86 +896,83 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             if (bar_try(drain, 0)) break;
     } else if (warp >= kValueWarp) {
         // ------------------------------------------------------ values into shared memory
-        const int tid = threadIdx.x - kValueWarp * 32, token = tid & 127, half = tid >> 7;
-        int st = 0, table = 0, vb = 0, raw_off = 0;
-        for (int j = 0; j < n_tiles; j++) {
-            const int b = j & 1;
-            uint8_t *dst = sm + C::O_V + b * C::VBUF;
-            const unsigned par = ((j >> 1) & 1) ^ 1, rel = r_empty(st), ve = v_empty(b);
-            wait(r_full(st), (j / ring.stages) & 1);
+        const int tid = threadIdx.x - kValueWarp * 32;
+        const RoleBars bar{r_full(0), r_empty(0), v_full(0), v_empty(0)};
+        const uint8_t *descs = sm + C::O_D, *table = sm + C::O_T;
+        const unsigned base = sb + C::O_RING;
+        RingPos q{0, 0, 0};
+        while (q.j < n_tiles) {
+            wait(r_full(q.st), q.par);
             __syncwarp();
-            const TileDesc &d = reinterpret_cast<const TileDesc *>(sm + C::O_D)[j % kSlots];
-            if (d.flags & kFresh) {
-                vb = (d.flags >> 16) & 15;
-                raw_off = C::O_RING + kTreeTile * (D / 8) * ((d.flags >> 8) & 15);
-                const int law = p.seg[d.seg].law;
-                if (vb && vb * 2 + law != table) {
-                    named_sync(5, 256);  // the other warps have done with the old table
-                    fill_levels(sm + C::O_T, lv.half[law] + cb_off(vb), vb, tid);
-                    named_sync(5, 256);
-                    table = vb * 2 + law;
-                }
+            const TileDesc &d = reinterpret_cast<const TileDesc *>(descs)[q.j % kSlots];
+            const int width = d.flags >> 16, vb = width & 15;
+            if (vb) {
+                const uint16_t *half = lv.half[width >> 4] + cb_off(vb);
+                named_sync(5, 128);  // the other warps have done with the old table
+                fill_levels(sm + C::O_T, half, vb, tid);
+                named_sync(5, 128);
             }
-            const uint8_t *raw = sm + raw_off + st * ring.stage, *tab = sm + C::O_T;
+            uint8_t *dst = sm + C::O_V;
             switch (vb) {
                 case 0: {
+                    const int b = q.j & 1;
                     const SegView &s = p.seg[d.seg].seg;
                     const uint4 *src = reinterpret_cast<const uint4 *>(s.v + d.b * s.vblock + s.voff[d.h]) +
                                        static_cast<size_t>(d.t) * (kTreeTile * D / 8);
                     const int n = d.left;
                     __syncwarp();
-                    if (lane == 0) bar_arrive(rel);
-                    wait(ve, par);
+                    if (lane == 0) bar_arrive(r_empty(q.st));
+                    wait(v_empty(b), ((q.j >> 1) & 1) ^ 1);
                     // 16-byte chunks, consecutive threads on consecutive ones; rows behind the tokens are zeros
 #pragma unroll 4
-                    for (int c = tid; c < kTreeTile * D / 8; c += 256) {
+                    for (int c = tid; c < kTreeTile * D / 8; c += 128) {
                         const int t = c / (D / 8), e = c % (D / 8);
                         uint4 v = make_uint4(0, 0, 0, 0);
                         if (t < n) v = __ldg(src + c);
-                        *reinterpret_cast<uint4 *>(dst + (e >> 3) * 16384 + t * 128 + (((e & 7) ^ (t & 7)) << 4)) = v;
+                        *reinterpret_cast<uint4 *>(dst + b * C::VBUF + (e >> 3) * 16384 + t * 128 + (((e & 7) ^ (t & 7)) << 4)) = v;
                     }
+                    fence_async();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(v_full(b));
+                    q.next(ring.stages);
                     break;
                 }
-                case 1: values_to_smem<1, D>(raw, token, half, rel, tab, dst, wait, ve, par); break;
-                case 2: values_to_smem<2, D>(raw, token, half, rel, tab, dst, wait, ve, par); break;
-                case 3: values_to_smem<3, D>(raw, token, half, rel, tab, dst, wait, ve, par); break;
-                case 4: values_to_smem<4, D>(raw, token, half, rel, tab, dst, wait, ve, par); break;
-                case 5: values_to_smem<5, D>(raw, token, half, rel, tab, dst, wait, ve, par); break;
-                case 6: values_to_smem<6, D>(raw, token, half, rel, tab, dst, wait, ve, par); break;
-                case 7: values_to_smem<7, D>(raw, token, half, rel, tab, dst, wait, ve, par); break;
-                default: values_to_smem<8, D>(raw, token, half, rel, tab, dst, wait, ve, par); break;
+                case 1: values_loop<1, D>(q, n_tiles, ring, base, descs, bar, table, dst, C::VBUF, tid, width, wait); break;
+                case 2: values_loop<2, D>(q, n_tiles, ring, base, descs, bar, table, dst, C::VBUF, tid, width, wait); break;
+                case 3: values_loop<3, D>(q, n_tiles, ring, base, descs, bar, table, dst, C::VBUF, tid, width, wait); break;
+                case 4: values_loop<4, D>(q, n_tiles, ring, base, descs, bar, table, dst, C::VBUF, tid, width, wait); break;
+                case 5: values_loop<5, D>(q, n_tiles, ring, base, descs, bar, table, dst, C::VBUF, tid, width, wait); break;
+                case 6: values_loop<6, D>(q, n_tiles, ring, base, descs, bar, table, dst, C::VBUF, tid, width, wait); break;
+                case 7: values_loop<7, D>(q, n_tiles, ring, base, descs, bar, table, dst, C::VBUF, tid, width, wait); break;
+                default: values_loop<8, D>(q, n_tiles, ring, base, descs, bar, table, dst, C::VBUF, tid, width, wait); break;
             }
-            if (++st == ring.stages) st = 0;
-            fence_async();
-            __syncwarp();
-            if (lane == 0) bar_arrive(v_full(b));
         }
     } else if (warp >= kKeyWarp) {
         // ------------------------------------------------------ keys into TMEM
         const int kw = warp - kKeyWarp, tid = threadIdx.x - kKeyWarp * 32;
         const unsigned lanes = static_cast<unsigned>(32 * kw) << 16;
-        int st = 0;
+        const RoleBars bar{r_full(0), r_empty(0), k_full(0), k_empty(0)};
+        const uint8_t *descs = sm + C::O_D;
+        const unsigned base = sb + C::O_RING, dst = tbase + lanes + C::T_K;
         {
             const uint32_t c[8] = {0x10001000u, 0, 0, 0, 0, 0, 0, 0};  // 2^-11 twice, zeros
             tmem_st8(tbase + lanes + C::T_C, c);
         }
-        for (int j = 0; j < n_tiles; j++) {
-            const int b = j & 1;
-            const unsigned dst = tbase + lanes + C::T_K + b * C::KCOLS, par = ((j >> 1) & 1) ^ 1, rel = r_empty(st),
-                           ke = k_empty(b), raw = sb + C::O_RING + st * ring.stage;
-            wait(r_full(st), (j / ring.stages) & 1);
+        RingPos q{0, 0, 0};
+        while (q.j < n_tiles) {
+            wait(r_full(q.st), q.par);
             __syncwarp();
-            const TileDesc &d = reinterpret_cast<const TileDesc *>(sm + C::O_D)[j % kSlots];
-            const int kb = (d.flags >> 8) & 15;
-            switch (kb) {
+            const TileDesc &d = reinterpret_cast<const TileDesc *>(descs)[q.j % kSlots];
+            switch ((d.flags >> 8) & 15) {
                 case 0: {
+                    const int b = q.j & 1;
                     const SegView &s = p.seg[d.seg].seg;
                     const uint4 *src = reinterpret_cast<const uint4 *>(s.k + d.b * s.kblock + s.koff[d.h]) +
                                        (static_cast<size_t>(d.t) * kTreeTile + tid) * (D / 8);
                     const bool valid = tid < d.left;
                     __syncwarp();
-                    if (lane == 0) bar_arrive(rel);
-                    wait(ke, par);
+                    if (lane == 0) bar_arrive(r_empty(q.st));
+                    wait(k_empty(b), ((q.j >> 1) & 1) ^ 1);
                     __syncwarp();
                     tc_after();
 #pragma unroll
@@ -933,24 +984,24 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                             if (valid) v = __ldg(src + 4 * i + c);
                             out[4 * c] = v.x, out[4 * c + 1] = v.y, out[4 * c + 2] = v.z, out[4 * c + 3] = v.w;
                         }
-                        tmem_st16(dst + 16 * i, out);
+                        tmem_st16(dst + b * C::KCOLS + 16 * i, out);
                     }
+                    tmem_wait_st();
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(k_full(b));
+                    q.next(ring.stages);
                     break;
                 }
-                case 1: keys_to_tmem<1, D>(raw, tid, rel, dst, wait, ke, par); break;
-                case 2: keys_to_tmem<2, D>(raw, tid, rel, dst, wait, ke, par); break;
-                case 3: keys_to_tmem<3, D>(raw, tid, rel, dst, wait, ke, par); break;
-                case 4: keys_to_tmem<4, D>(raw, tid, rel, dst, wait, ke, par); break;
-                case 5: keys_to_tmem<5, D>(raw, tid, rel, dst, wait, ke, par); break;
-                case 6: keys_to_tmem<6, D>(raw, tid, rel, dst, wait, ke, par); break;
-                case 7: keys_to_tmem<7, D>(raw, tid, rel, dst, wait, ke, par); break;
-                default: keys_to_tmem<8, D>(raw, tid, rel, dst, wait, ke, par); break;
+                case 1: keys_loop<1, D>(q, n_tiles, ring, base, descs, bar, dst, tid, wait); break;
+                case 2: keys_loop<2, D>(q, n_tiles, ring, base, descs, bar, dst, tid, wait); break;
+                case 3: keys_loop<3, D>(q, n_tiles, ring, base, descs, bar, dst, tid, wait); break;
+                case 4: keys_loop<4, D>(q, n_tiles, ring, base, descs, bar, dst, tid, wait); break;
+                case 5: keys_loop<5, D>(q, n_tiles, ring, base, descs, bar, dst, tid, wait); break;
+                case 6: keys_loop<6, D>(q, n_tiles, ring, base, descs, bar, dst, tid, wait); break;
+                case 7: keys_loop<7, D>(q, n_tiles, ring, base, descs, bar, dst, tid, wait); break;
+                default: keys_loop<8, D>(q, n_tiles, ring, base, descs, bar, dst, tid, wait); break;
             }
-            if (++st == ring.stages) st = 0;
-            tmem_wait_st();
-            tc_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(k_full(b));
         }
     } else {
         // ------------------------------------------------------ softmax
@@ -969,6 +1020,9 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             wait(s_full(b), par);
             __syncwarp();
             tc_after();
+            float u[CW];
+            const unsigned s_addr = tbase + lanes + C::T_S + b * R + wg * CW;
+            tmem_issue<CW>(s_addr, u);
             const int4 d = *reinterpret_cast<const int4 *>(sm + C::O_D + (j % kSlots) * 64);  // flags, left, part, inv
             const bool first = d.x & kFirst, fp16 = d.x & kFp16, valid = tok < d.y;
             if (d.x & kFresh) A = reinterpret_cast<const TileDesc *>(sm + C::O_D)[j % kSlots].A;
@@ -981,11 +1035,9 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             }
             ks *= A;
             if (!valid) ks = sig = 0.f;
-            float u[CW];
-            const unsigned s_addr = tbase + lanes + C::T_S + b * R + wg * CW;
+            tmem_wait<CW>(u);
             // x - m, x = ks U (ks holds the factor A too)
             auto scores = [&] {
-                tmem_ld<CW>(s_addr, u);
 #pragma unroll
                 for (int c = 0; c < CW; c += 4) {
                     const float4 m = *reinterpret_cast<const float4 *>(m_row + R + c);
@@ -1003,8 +1055,8 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 for (int c = 2; c < CW; c += 2) top = fmax3(top, u[c], u[c + 1]);
                 raise = valid && (top > 8.0f || sig * down_e > 128.0f);
             }
-            if (named_or(1 + wg, 128, raise)) {
-                tmem_ld<CW>(s_addr, u);
+            if (__builtin_expect(named_or(1 + wg, 128, raise), 0)) {
+                tmem_ld<CW>(s_addr, u);  // (as they were)
                 float mine = -kInf;
 #pragma unroll
                 for (int c = 0; c < CW; c++) {
@@ -1058,13 +1110,14 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 }
                 E = now;
                 down_e = pow2(-E);
+                tmem_ld<CW>(s_addr, u);
                 scores();
             }
             tc_before();
             __syncwarp();
             if (lane == 0) bar_arrive(s_empty(b));
             const float sv = sig * down_e;
-            if (__any_sync(0xffffffffu, !valid)) {  // behind the last token: weight zero, whatever lies there
+            if (__builtin_expect(__any_sync(0xffffffffu, !valid), 0)) {  // behind the last token: weight zero, whatever lies there
 #pragma unroll
                 for (int c = 0; c < CW; c++) u[c] = valid ? u[c] : -kInf;
             }
@@ -1086,7 +1139,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             tc_before();
             __syncwarp();
             if (lane == 0) bar_arrive(p_full(b));
-            if (d.x & kLast) {  // the part's record
+            if (__builtin_expect(d.x & kLast, 0)) {  // the part's record
                 float *rec = p.part + (static_cast<size_t>(worker) + d.z) * R * (D + 4);
                 // row sums over the tokens
 #pragma unroll
