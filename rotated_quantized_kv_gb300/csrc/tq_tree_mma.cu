@@ -29,12 +29,11 @@
 // V^T needs the dims on the lanes, so V goes through shared memory with tokens
 // as the K dimension (MN-major operand).
 //
-// Roles (19 warps): softmax in two groups of four warps, half of the rows each, four
-// warps of keys, four of values, one that issues the MMAs, two that walk the list
-// and load records and scales (cp.async into a ring); the others learn from a
-// descriptor what a tile is.  What a tile costs beyond its arithmetic is paid per
-// warp (waits, signals, the descriptor: over 100 instructions), so the roles have as
-// few warps as their registers allow.
+// Roles (32 warps, 24 with 16 rows): softmax in four groups of four warps (two), an
+// equal share of the rows each, four warps of keys, two groups of four of values that
+// take alternate tiles, two that issue the MMAs, two that walk the list and load
+// records and scales (cp.async into a ring); the others learn from a descriptor
+// what a tile is.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -54,8 +53,8 @@ using namespace tree;
 constexpr int kTableBytes = 8192;      // value levels
 // Tiles whose descriptor and scales are kept, and ring stages: the loader is at most
 // kMaxStages tiles ahead of the key and value warps, and these, when they release
-// tile a, have waited for the MMA and the softmax of tile a - 3; so slot j % 8 has been
-// read by everyone when tile j + 8 overwrites it (5 stages would do).
+// tile a, have waited for the MMA and the softmax of tile a - 4; so slot j % 8 has been
+// read by everyone when tile j + 8 overwrites it.
 constexpr int kSlots = 8;
 constexpr int kMaxStages = 4;
 constexpr int kSmemMax = 227 * 1024;
@@ -97,6 +96,17 @@ __device__ __forceinline__ bool bar_try(unsigned bar, unsigned parity) {
         : "memory");
     return ok != 0;
 }
+// Whether the phase has completed, without waiting (asked early, the answer's
+// latency hides behind other work).
+__device__ __forceinline__ bool bar_test(unsigned bar, unsigned parity) {
+    unsigned ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ void bar_expect_tx(unsigned bar, unsigned bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
@@ -130,6 +140,19 @@ struct Waiter {
     int *error;
     int polls;
     bool gone;
+    // Two barriers at once: half of the warp's lanes poll each (a wait costs some 200
+    // cycles even when there is nothing to wait for).  The whole warp calls, and is
+    // together again afterwards.
+    __device__ __forceinline__ void both(unsigned bar0, unsigned parity0, unsigned bar1, unsigned parity1) {
+        const bool low = (threadIdx.x & 31) < 16;
+        (*this)(low ? bar0 : bar1, low ? parity0 : parity1);
+        gone = __any_sync(0xffffffffu, gone);
+    }
+    // The wait behind an early bar_test.
+    __device__ __forceinline__ void unless(bool done, unsigned bar, unsigned parity) {
+        if (!done) (*this)(bar, parity);
+        __syncwarp();
+    }
     __device__ __forceinline__ void operator()(unsigned bar, unsigned parity) {
         if (gone) return;
         unsigned ok = 0;
@@ -393,8 +416,8 @@ template <int D, int R>
 struct Mma {
     static constexpr int NWG = R == 16 ? 2 : 4;     // softmax groups of four warps
     static constexpr int CW = R / NWG;              // rows per group
-    static constexpr int kKeyWarp = 4 * NWG, kValueWarp = kKeyWarp + 4, kIssueWarp = kValueWarp + 4,
-                         kLoadWarp = kIssueWarp + 1;
+    static constexpr int kKeyWarp = 4 * NWG, kValueWarp = kKeyWarp + 4, kIssueWarp = kValueWarp + 8,
+                         kLoadWarp = kIssueWarp + 2;
     static constexpr int kThreads = 32 * (kLoadWarp + 2);
     static constexpr int HALVES = D / 64;
     static constexpr int QPART = HALVES * R * 128;  // hi or lo of a block's queries
@@ -408,13 +431,13 @@ struct Mma {
     static constexpr int O_Q = 0;
     static constexpr int O_V = (O_Q + 2 * QBUF + 1023) / 1024 * 1024;
     static constexpr int O_P = O_V + 2 * VBUF;
-    static constexpr int O_T = O_P + 2 * PBUF;
-    static constexpr int O_S = O_T + kTableBytes;   // [kSlots][2][128] scales
+    static constexpr int O_T = O_P + PBUF;
+    static constexpr int O_S = O_T + 2 * kTableBytes;   // [kSlots][2][128] scales
     static constexpr int O_D = O_S + kSlots * 1024; // [kSlots] descriptors
     static constexpr int O_M = O_D + kSlots * 64;   // [R] m, [R] -m as used, [R] factors
     static constexpr int O_X = O_M + 3 * R * 4;     // [NWG][4][CW + 1] maxima of the warps
     static constexpr int O_B = (O_X + NWG * 4 * (CW + 1) * 4 + 15) / 16 * 16;
-    static constexpr int kBars = 2 * 8 + 2 * 2 + 1 + 1 + 2 * kMaxStages;
+    static constexpr int kBars = 2 * 8 + 2 * 2 + 1 + 2 + 2 * kMaxStages;
     static constexpr int O_RING = (O_B + kBars * 8 + 16 + 127) / 128 * 128;
     static constexpr int kRing = kSmemMax - 1024 - O_RING;  // (1024: alignment)
 };
@@ -596,16 +619,15 @@ __device__ __forceinline__ void keys_loop(RingPos &q, int n_tiles, const RingGeo
     const int lane = threadIdx.x & 31;
 #pragma unroll 1
     for (; q.j < n_tiles; q.next(ring.stages)) {
-        wait(bar.r_full + 8 * q.st, q.par);
-        __syncwarp();
+        const int b = q.j & 1;
+        const bool here = bar_test(bar.r_full + 8 * q.st, q.par), free = bar_test(bar.empty + 8 * b, ((q.j >> 1) & 1) ^ 1);
+        wait.unless(here, bar.r_full + 8 * q.st, q.par);
         if (((reinterpret_cast<const TileDesc *>(descs)[q.j % kSlots].flags >> 8) & 15) != KB) return;
         uint32_t w[D / 32 * KB];
         load_record<D / 32 * KB>(ring_base + q.st * ring.stage, token, w);
         __syncwarp();
         if (lane == 0) bar_arrive(bar.r_empty + 8 * q.st);
-        const int b = q.j & 1;
-        wait(bar.empty + 8 * b, ((q.j >> 1) & 1) ^ 1);
-        __syncwarp();
+        wait.unless(free, bar.empty + 8 * b, ((q.j >> 1) & 1) ^ 1);
         tc_after();
         // (a loop that shifts the record down: a quarter of the code, which the instruction caches feel)
 #pragma unroll 1
@@ -623,29 +645,30 @@ __device__ __forceinline__ void keys_loop(RingPos &q, int n_tiles, const RingGeo
     }
 }
 
-// Values of VB bits from the ring to fp16 rows, one token a thread, while the tiles have that width (and law).
+// Values of VB bits from the ring to fp16 rows, one token a thread, while the tiles have
+// that width (and law).  Two groups of four warps take alternate tiles, each with its buffer.
 template <int VB, int D>
 __device__ __forceinline__ void values_loop(RingPos &q, int n_tiles, const RingGeo &ring, unsigned ring_base, const uint8_t *descs,
-                                            const RoleBars &bar, const uint8_t *table, uint8_t *dst, int buf, int token,
+                                            const RoleBars &bar, const uint8_t *table, uint8_t *dst, int token,
                                             int width, Waiter &wait) {
     const int lane = threadIdx.x & 31;
     table += (token & (level_columns(VB) - 1)) * level_bytes(VB);
     dst += token * 128;
 #pragma unroll 1
-    for (; q.j < n_tiles; q.next(ring.stages)) {
-        wait(bar.r_full + 8 * q.st, q.par);
-        __syncwarp();
+    for (; q.j < n_tiles; q.next(ring.stages), q.next(ring.stages)) {
+        const unsigned par = ((q.j >> 1) & 1) ^ 1;
+        const bool here = bar_test(bar.r_full + 8 * q.st, q.par), free = bar_test(bar.empty, par);
+        wait.unless(here, bar.r_full + 8 * q.st, q.par);
         const int flags = reinterpret_cast<const TileDesc *>(descs)[q.j % kSlots].flags;
         if (flags >> 16 != width) return;
         uint32_t w[D / 32 * VB];
         load_record<D / 32 * VB>(ring_base + q.st * ring.stage + kTreeTile * (D / 8) * ((flags >> 8) & 15), token, w);
         __syncwarp();
         if (lane == 0) bar_arrive(bar.r_empty + 8 * q.st);
-        const int b = q.j & 1;
-        wait(bar.empty + 8 * b, ((q.j >> 1) & 1) ^ 1);
+        wait.unless(free, bar.empty, par);
 #pragma unroll 1
         for (int g = 0; g < D / 32; g++) {  // 32 dims: four chunks of the line
-            uint8_t *line = dst + b * buf + (g >> 1) * 16384;
+            uint8_t *line = dst + (g >> 1) * 16384;
             const int c0 = 4 * (g & 1);
             *reinterpret_cast<uint4 *>(line + ((c0 ^ (token & 7)) << 4)) = level_chunk<VB, 0>(w, table);
             *reinterpret_cast<uint4 *>(line + (((c0 + 1) ^ (token & 7)) << 4)) = level_chunk<VB, 1>(w, table);
@@ -656,11 +679,11 @@ __device__ __forceinline__ void values_loop(RingPos &q, int n_tiles, const RingG
         }
         fence_async();
         __syncwarp();
-        if (lane == 0) bar_arrive(bar.full + 8 * b);
+        if (lane == 0) bar_arrive(bar.full);
     }
 }
 
-// Fill the value table of a width (the four value warps together).
+// Fill the value table of a width (the four warps of a group together).
 __device__ __forceinline__ void fill_levels(uint8_t *table, const uint16_t *half, int vb, int tid) {
     const int codes = level_codes(vb), entries = level_entries(vb), cols = level_columns(vb);
     const uint32_t m = (1u << vb) - 1u;
@@ -700,13 +723,13 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
     auto v_empty = [&](int i) { return bars + 8u * (6 + i); };
     auto s_full = [&](int i) { return bars + 8u * (8 + i); };
     auto s_empty = [&](int i) { return bars + 8u * (10 + i); };
-    auto p_full = [&](int i) { return bars + 8u * (12 + i); };
-    auto p_empty = [&](int i) { return bars + 8u * (14 + i); };
+    const unsigned p_full = bars + 8u * 12, p_empty = bars + 8u * 14;
     auto q_full = [&](int i) { return bars + 8u * (16 + i); };
     auto q_empty = [&](int i) { return bars + 8u * (18 + i); };
-    const unsigned o_free = bars + 8u * 20, drain = bars + 8u * 21;
-    auto r_full = [&](int i) { return bars + 8u * (22 + i); };
-    auto r_empty = [&](int i) { return bars + 8u * (22 + kMaxStages + i); };
+    const unsigned o_free = bars + 8u * 20;
+    auto drain = [&](int i) { return bars + 8u * (21 + i); };
+    auto r_full = [&](int i) { return bars + 8u * (23 + i); };
+    auto r_empty = [&](int i) { return bars + 8u * (23 + kMaxStages + i); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::O_B + C::kBars * 8);
 
     asm volatile("griddepcontrol.launch_dependents;");  // (the merge waits for this grid's end)
@@ -725,18 +748,19 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             bar_init(v_empty(i), 1);
             bar_init(s_full(i), 1);
             bar_init(s_empty(i), 4 * C::NWG);
-            bar_init(p_full(i), 4 * C::NWG);
-            bar_init(p_empty(i), 1);
         }
         for (int i = 0; i < 2; i++) {
             bar_init(q_full(i), 1);
             bar_init(q_empty(i), 1);
         }
+        bar_init(p_full, 4 * C::NWG);
+        bar_init(p_empty, 1);
         bar_init(o_free, 4 * C::NWG);
-        bar_init(drain, 1);
+        bar_init(drain(0), 1);
+        bar_init(drain(1), 1);
         for (int i = 0; i < kMaxStages; i++) {
             bar_init(r_full(i), 65);
-            bar_init(r_empty(i), 8);
+            bar_init(r_empty(i), 8);  // four key warps, the four value warps of the tile
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -829,78 +853,84 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 for (int i = 0; i < kDrainPolls; i++)
                     if (bar_try(q_full(e & 1), (e >> 1) & 1)) break;
     } else if (warp == kIssueWarp) {
-        // ------------------------------------------------------ MMA issue
-        constexpr uint32_t id_s = idesc(R, false), id_o = idesc(R, true);
-        int ev = -1, parts = 0;
-        bool first_prev = false;
-        for (int j = 0; j <= n_tiles; j++) {
-            bool first = false;
-            if (j < n_tiles) {
-                const int b = j & 1;
-                wait(k_full(b), (j >> 1) & 1);
-                const int flags = reinterpret_cast<const TileDesc *>(sm + C::O_D)[j % kSlots].flags;
-                first = flags & kFirst;
-                const bool fp16 = flags & kFp16;
-                if (flags & kFresh) {
-                    // the products with the old queries are behind this point; the new ones' image
-                    if (ev >= 0 && elect_one()) mma_commit(q_empty(ev & 1));
-                    __syncwarp();
-                    ev++;
-                    wait(q_full(ev & 1), (ev >> 1) & 1);
-                }
-                wait(s_empty(b), ((j >> 1) & 1) ^ 1);
-                tc_after();
-                const uint64_t q = desc_k(sb + C::O_Q + (ev & 1) * C::QBUF);
-                const unsigned a = C::T_K + b * C::KCOLS, d = C::T_S + b * R;
-                if (elect_one()) {
+        // ------------------------------------------------------ S^T = K q^T
+        constexpr uint32_t id_s = idesc(R, false);
+        int ev = -1;
+#pragma unroll 1
+        for (int j = 0; j < n_tiles; j++) {
+            const int b = j & 1;
+            const unsigned par = (j >> 1) & 1;
+            wait.both(k_full(b), par, s_empty(b), par ^ 1);
+            const int flags = reinterpret_cast<const TileDesc *>(sm + C::O_D)[j % kSlots].flags;
+            if (flags & kFresh) {
+                // the products with the old queries are behind this point; the new ones' image
+                if (ev >= 0 && elect_one()) mma_commit(q_empty(ev & 1));
+                __syncwarp();
+                ev++;
+                wait(q_full(ev & 1), (ev >> 1) & 1);
+                __syncwarp();
+            }
+            tc_after();
+            const uint64_t q = desc_k(sb + C::O_Q + (ev & 1) * C::QBUF);
+            const unsigned a = C::T_K + b * C::KCOLS, d = C::T_S + b * R;
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < D / 16; k++)
+                    mma_ts(d, a + 8 * k, q + (((k >> 2) * R * 128 + 32 * (k & 3)) >> 4), id_s, k != 0);
+                if (!(flags & kFp16)) {  // (fp16 queries are exact: no lo part)
 #pragma unroll
                     for (int k = 0; k < D / 16; k++)
-                        mma_ts(d, a + 8 * k, q + (((k >> 2) * R * 128 + 32 * (k & 3)) >> 4), id_s, k != 0);
-                    if (!fp16) {  // (fp16 queries are exact: no lo part)
-#pragma unroll
-                        for (int k = 0; k < D / 16; k++)
-                            mma_ts(d, a + 8 * k, q + ((C::QPART + (k >> 2) * R * 128 + 32 * (k & 3)) >> 4), id_s, 1);
-                        mma_ts(d, C::T_C, desc_k16(sb + C::O_Q + (ev & 1) * C::QBUF + 2 * C::QPART), id_s, 1);
-                    }
-                    mma_commit(k_empty(b));
-                    mma_commit(s_full(b));
+                        mma_ts(d, a + 8 * k, q + ((C::QPART + (k >> 2) * R * 128 + 32 * (k & 3)) >> 4), id_s, 1);
+                    mma_ts(d, C::T_C, desc_k16(sb + C::O_Q + (ev & 1) * C::QBUF + 2 * C::QPART), id_s, 1);
                 }
-                __syncwarp();
+                mma_commit(k_empty(b));
+                mma_commit(s_full(b));
             }
-            if (j > 0) {
-                const int i = j - 1, b = i & 1;
-                wait(v_full(b), (i >> 1) & 1);
-                if (first_prev) {
-                    if (parts > 0) wait(o_free, (parts - 1) & 1);
-                    parts++;
-                }
-                wait(p_full(b), (i >> 1) & 1);
-                tc_after();
-                const uint64_t v = desc_mn(sb + C::O_V + b * C::VBUF, C::HALVES == 2 ? 16384 : 0),
-                               pp = desc_mn(sb + C::O_P + b * C::PBUF, 0);
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < 8; k++)
-                        mma_ss(C::T_O, v + (2048 * k >> 4), pp + (2048 * k >> 4), id_o, k != 0 || !first_prev);
-                    mma_commit(v_empty(b));
-                    mma_commit(p_empty(b));
-                }
-                __syncwarp();
-            }
-            first_prev = first;
+            __syncwarp();
         }
-        // everything issued has completed before TMEM and shared memory go away
-        if (elect_one()) mma_commit(drain);
+        // what was issued has completed before TMEM and shared memory go away
+        if (elect_one()) mma_commit(drain(0));
         __syncwarp();
         for (int i = 0; i < kDrainPolls; i++)
-            if (bar_try(drain, 0)) break;
+            if (bar_try(drain(0), 0)) break;
+    } else if (warp == kIssueWarp + 1) {
+        // ------------------------------------------------------ O^T += V^T P^T
+        constexpr uint32_t id_o = idesc(R, true);
+        int parts = 0;
+#pragma unroll 1
+        for (int j = 0; j < n_tiles; j++) {
+            const int b = j & 1;
+            wait.both(v_full(b), (j >> 1) & 1, p_full, j & 1);
+            const bool first = reinterpret_cast<const TileDesc *>(sm + C::O_D)[j % kSlots].flags & kFirst;
+            if (first) {
+                if (parts > 0) wait(o_free, (parts - 1) & 1);
+                __syncwarp();
+                parts++;
+            }
+            tc_after();
+            const uint64_t v = desc_mn(sb + C::O_V + b * C::VBUF, C::HALVES == 2 ? 16384 : 0),
+                           pp = desc_mn(sb + C::O_P, 0);
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 8; k++) mma_ss(C::T_O, v + (2048 * k >> 4), pp + (2048 * k >> 4), id_o, k != 0 || !first);
+                mma_commit(v_empty(b));
+                mma_commit(p_empty);
+            }
+            __syncwarp();
+        }
+        if (elect_one()) mma_commit(drain(1));
+        __syncwarp();
+        for (int i = 0; i < kDrainPolls; i++)
+            if (bar_try(drain(1), 0)) break;
     } else if (warp >= kValueWarp) {
         // ------------------------------------------------------ values into shared memory
-        const int tid = threadIdx.x - kValueWarp * 32;
-        const RoleBars bar{r_full(0), r_empty(0), v_full(0), v_empty(0)};
-        const uint8_t *descs = sm + C::O_D, *table = sm + C::O_T;
+        const int vg = (warp - kValueWarp) >> 2, tid = threadIdx.x - (kValueWarp + 4 * vg) * 32;
+        const RoleBars bar{r_full(0), r_empty(0), v_full(vg), v_empty(vg)};
+        const uint8_t *descs = sm + C::O_D, *table = sm + C::O_T + vg * kTableBytes;
         const unsigned base = sb + C::O_RING;
+        uint8_t *dst = sm + C::O_V + vg * C::VBUF;
         RingPos q{0, 0, 0};
+        if (vg) q.next(ring.stages);
         while (q.j < n_tiles) {
             wait(r_full(q.st), q.par);
             __syncwarp();
@@ -908,43 +938,42 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             const int width = d.flags >> 16, vb = width & 15;
             if (vb) {
                 const uint16_t *half = lv.half[width >> 4] + cb_off(vb);
-                named_sync(5, 128);  // the other warps have done with the old table
-                fill_levels(sm + C::O_T, half, vb, tid);
-                named_sync(5, 128);
+                named_sync(5 + vg, 128);  // the other warps have done with the old table
+                fill_levels(sm + C::O_T + vg * kTableBytes, half, vb, tid);
+                named_sync(5 + vg, 128);
             }
-            uint8_t *dst = sm + C::O_V;
             switch (vb) {
                 case 0: {
-                    const int b = q.j & 1;
                     const SegView &s = p.seg[d.seg].seg;
                     const uint4 *src = reinterpret_cast<const uint4 *>(s.v + d.b * s.vblock + s.voff[d.h]) +
                                        static_cast<size_t>(d.t) * (kTreeTile * D / 8);
                     const int n = d.left;
                     __syncwarp();
                     if (lane == 0) bar_arrive(r_empty(q.st));
-                    wait(v_empty(b), ((q.j >> 1) & 1) ^ 1);
+                    wait(v_empty(vg), ((q.j >> 1) & 1) ^ 1);
                     // 16-byte chunks, consecutive threads on consecutive ones; rows behind the tokens are zeros
 #pragma unroll 4
                     for (int c = tid; c < kTreeTile * D / 8; c += 128) {
                         const int t = c / (D / 8), e = c % (D / 8);
                         uint4 v = make_uint4(0, 0, 0, 0);
                         if (t < n) v = __ldg(src + c);
-                        *reinterpret_cast<uint4 *>(dst + b * C::VBUF + (e >> 3) * 16384 + t * 128 + (((e & 7) ^ (t & 7)) << 4)) = v;
+                        *reinterpret_cast<uint4 *>(dst + (e >> 3) * 16384 + t * 128 + (((e & 7) ^ (t & 7)) << 4)) = v;
                     }
                     fence_async();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(v_full(b));
+                    if (lane == 0) bar_arrive(v_full(vg));
+                    q.next(ring.stages);
                     q.next(ring.stages);
                     break;
                 }
-                case 1: values_loop<1, D>(q, n_tiles, ring, base, descs, bar, table, dst, C::VBUF, tid, width, wait); break;
-                case 2: values_loop<2, D>(q, n_tiles, ring, base, descs, bar, table, dst, C::VBUF, tid, width, wait); break;
-                case 3: values_loop<3, D>(q, n_tiles, ring, base, descs, bar, table, dst, C::VBUF, tid, width, wait); break;
-                case 4: values_loop<4, D>(q, n_tiles, ring, base, descs, bar, table, dst, C::VBUF, tid, width, wait); break;
-                case 5: values_loop<5, D>(q, n_tiles, ring, base, descs, bar, table, dst, C::VBUF, tid, width, wait); break;
-                case 6: values_loop<6, D>(q, n_tiles, ring, base, descs, bar, table, dst, C::VBUF, tid, width, wait); break;
-                case 7: values_loop<7, D>(q, n_tiles, ring, base, descs, bar, table, dst, C::VBUF, tid, width, wait); break;
-                default: values_loop<8, D>(q, n_tiles, ring, base, descs, bar, table, dst, C::VBUF, tid, width, wait); break;
+                case 1: values_loop<1, D>(q, n_tiles, ring, base, descs, bar, table, dst, tid, width, wait); break;
+                case 2: values_loop<2, D>(q, n_tiles, ring, base, descs, bar, table, dst, tid, width, wait); break;
+                case 3: values_loop<3, D>(q, n_tiles, ring, base, descs, bar, table, dst, tid, width, wait); break;
+                case 4: values_loop<4, D>(q, n_tiles, ring, base, descs, bar, table, dst, tid, width, wait); break;
+                case 5: values_loop<5, D>(q, n_tiles, ring, base, descs, bar, table, dst, tid, width, wait); break;
+                case 6: values_loop<6, D>(q, n_tiles, ring, base, descs, bar, table, dst, tid, width, wait); break;
+                case 7: values_loop<7, D>(q, n_tiles, ring, base, descs, bar, table, dst, tid, width, wait); break;
+                default: values_loop<8, D>(q, n_tiles, ring, base, descs, bar, table, dst, tid, width, wait); break;
             }
         }
     } else if (warp >= kKeyWarp) {
@@ -1007,37 +1036,43 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
         // ------------------------------------------------------ softmax
         const int wg = warp >> 2, qw = warp & 3, tok = 32 * qw + lane;  // TMEM lane = token (or dim of O)
         const unsigned lanes = static_cast<unsigned>(32 * qw) << 16;
-        float *m_row = reinterpret_cast<float *>(sm + C::O_M) + wg * CW;  // m; + R: -m as used; + 2R: factors
+        // [CW] m; + R: -m as used (0 while nothing was seen); + 2R: factors
+        float *m_row = reinterpret_cast<float *>(sm + C::O_M) + wg * CW;
         float *maxima = reinterpret_cast<float *>(sm + C::O_X) + wg * 4 * (CW + 1);
+        const unsigned s_addr0 = tbase + lanes + C::T_S + wg * CW, o_addr = tbase + lanes + C::T_O + wg * CW;
+        uint8_t *prow = sm + C::O_P + tok * 128;
         int E = 0;
         float l[CW], A = 1.f, down_e = 1.f;  // down_e: 2^-E
 #pragma unroll
         for (int c = 0; c < CW; c++) l[c] = 0.f;
+        if (tok < CW) m_row[R + tok] = 0.f;
+        named_sync(1 + wg, 128);
+        bool ready = false;
+#pragma unroll 1
         for (int j = 0; j < n_tiles; j++) {
             const int b = j & 1;
-            const unsigned par = (j >> 1) & 1;
-            // S^T of this tile (and P^T V of tile j - 2, which came before it: its P buffer is free)
-            wait(s_full(b), par);
-            __syncwarp();
+            wait.unless(ready, s_full(b), (j >> 1) & 1);
             tc_after();
             float u[CW];
-            const unsigned s_addr = tbase + lanes + C::T_S + b * R + wg * CW;
-            tmem_issue<CW>(s_addr, u);
-            const int4 d = *reinterpret_cast<const int4 *>(sm + C::O_D + (j % kSlots) * 64);  // flags, left, part, inv
-            const bool first = d.x & kFirst, fp16 = d.x & kFp16, valid = tok < d.y;
-            if (d.x & kFresh) A = reinterpret_cast<const TileDesc *>(sm + C::O_D)[j % kSlots].A;
+            tmem_issue<CW>(s_addr0 + b * R, u);
+            const TileDesc *desc = reinterpret_cast<const TileDesc *>(sm + C::O_D) + j % kSlots;
+            const int4 d = *reinterpret_cast<const int4 *>(desc);  // flags, left, part, inv
+            if (d.x & kFresh) A = desc->A;
             // the token's scales (behind the last token: anything)
-            float ks = 1.f, sig = 1.f;
-            if (!fp16) {
-                const float *sc = reinterpret_cast<const float *>(sm + C::O_S) + (j % kSlots) * 256 + tok;
-                ks = sc[0];
+            const float *sc = reinterpret_cast<const float *>(sm + C::O_S) + (j % kSlots) * 256 + tok;
+            const bool valid = tok < d.y;
+            float ks = A, sig = 1.f;  // x = ks U
+            if (!(d.x & kFp16)) {
+                ks = sc[0] * A;
                 sig = sc[128] * __int_as_float(d.w);
             }
-            ks *= A;
             if (!valid) ks = sig = 0.f;
+            bool raise = d.x & kFirst;
             tmem_wait<CW>(u);
-            // x - m, x = ks U (ks holds the factor A too)
-            auto scores = [&] {
+#pragma unroll 1
+            for (int pass = 0;; pass++) {
+                // x - m, and whether some score outgrew its row's m (or a sigma the common power of two)
+                float top = -kInf;
 #pragma unroll
                 for (int c = 0; c < CW; c += 4) {
                     const float4 m = *reinterpret_cast<const float4 *>(m_row + R + c);
@@ -1045,22 +1080,15 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                     u[c + 1] = fmaf(u[c + 1], ks, m.y);
                     u[c + 2] = fmaf(u[c + 2], ks, m.z);
                     u[c + 3] = fmaf(u[c + 3], ks, m.w);
+                    top = fmax3(top, u[c], u[c + 1]);
+                    top = fmax3(top, u[c + 2], u[c + 3]);
                 }
-            };
-            bool raise = first;
-            if (!first) {
-                scores();
-                float top = fmaxf(u[0], u[1]);
-#pragma unroll
-                for (int c = 2; c < CW; c += 2) top = fmax3(top, u[c], u[c + 1]);
-                raise = valid && (top > 8.0f || sig * down_e > 128.0f);
-            }
-            if (__builtin_expect(named_or(1 + wg, 128, raise), 0)) {
-                tmem_ld<CW>(s_addr, u);  // (as they were)
+                raise |= valid && (top > 8.0f || sig * down_e > 128.0f);
+                if (pass || !named_or(1 + wg, 128, raise)) break;
                 float mine = -kInf;
 #pragma unroll
                 for (int c = 0; c < CW; c++) {
-                    float v = valid ? u[c] * ks : -kInf;
+                    float v = valid ? u[c] : -kInf;
                     asm("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(v));
                     if (lane == c) mine = v;
                 }
@@ -1069,17 +1097,19 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 if (lane < CW) maxima[qw * (CW + 1) + lane] = mine;
                 if (lane == 0) maxima[qw * (CW + 1) + CW] = big;
                 named_sync(1 + wg, 128);
+                const bool first = d.x & kFirst;
                 big = fmaxf(fmaxf(maxima[CW], maxima[2 * CW + 1]), fmaxf(maxima[3 * CW + 2], maxima[4 * CW + 3]));
                 // E: the largest sigma times 2^-E in [0.5, 1)
                 int e = 0;
-                if (!fp16 && big > 0.f && big < kInf)
+                if (!(d.x & kFp16) && big > 0.f && big < kInf)
                     e = max(-100, min(100, static_cast<int>((__float_as_uint(big) >> 23) & 0xFFu) - 126));
                 const int now = first ? e : max(E, e);
                 if (tok < CW) {
                     const float old = first ? -kInf : m_row[tok];
-                    float m = old;
+                    float m = maxima[tok];
 #pragma unroll
-                    for (int i = 0; i < 4; i++) m = fmaxf(m, maxima[i * (CW + 1) + tok]);
+                    for (int i = 1; i < 4; i++) m = fmaxf(m, maxima[i * (CW + 1) + tok]);
+                    m = fmaxf(old, m - m_row[R + tok]);
                     m_row[tok] = m;
                     m_row[R + tok] = m == -kInf ? 0.f : -m;
                     m_row[2 * R + tok] = old == -kInf ? 0.f : ex2(old - m);
@@ -1087,7 +1117,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 named_sync(1 + wg, 128);
                 if (!first) {
                     // earlier weights to the new max: the sums here, the accumulator in TMEM
-                    wait(p_empty((j - 1) & 1), ((j - 1) >> 1) & 1);
+                    wait(p_empty, (j - 1) & 1);
                     __syncwarp();
                     tc_after();
                     const float down = pow2(-min(now - E, 126));
@@ -1095,51 +1125,50 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                     for (int c = 0; c < CW; c += 8) {
                         float o[8];
                         uint32_t r[8];
-                        tmem_ld<8>(tbase + lanes + C::T_O + wg * CW + c, o);
+                        tmem_ld<8>(o_addr + c, o);
 #pragma unroll
-                        for (int i = 0; i < 8; i += 2) {
-                            const float f0 = m_row[2 * R + c + i], f1 = m_row[2 * R + c + i + 1];
-                            l[c + i] *= f0;
-                            l[c + i + 1] *= f1;
-                            r[i] = __float_as_uint(o[i] * (f0 * down));
-                            r[i + 1] = __float_as_uint(o[i + 1] * (f1 * down));
+                        for (int i = 0; i < 8; i++) {
+                            const float f = m_row[2 * R + c + i];
+                            l[c + i] *= f;
+                            r[i] = __float_as_uint(o[i] * (f * down));
                         }
-                        tmem_st8(tbase + lanes + C::T_O + wg * CW + c, r);
+                        tmem_st8(o_addr + c, r);
                     }
                     tmem_wait_st();
                 }
                 E = now;
                 down_e = pow2(-E);
-                tmem_ld<CW>(s_addr, u);
-                scores();
+                tmem_ld<CW>(s_addr0 + b * R, u);
             }
             tc_before();
             __syncwarp();
             if (lane == 0) bar_arrive(s_empty(b));
+            const bool p_free = bar_test(p_empty, (j & 1) ^ 1);  // the products with the last P done?
             const float sv = sig * down_e;
-            if (__builtin_expect(__any_sync(0xffffffffu, !valid), 0)) {  // behind the last token: weight zero, whatever lies there
+            if (__any_sync(0xffffffffu, !valid)) {  // behind the last token: weight zero, whatever lies there
 #pragma unroll
                 for (int c = 0; c < CW; c++) u[c] = valid ? u[c] : -kInf;
             }
-            uint8_t *prow = sm + C::O_P + b * C::PBUF + tok * 128;
+            uint32_t h[CW / 2];
 #pragma unroll
-            for (int c = 0; c < CW; c += 8) {
-                uint32_t h[4];
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const float p0 = ex2(u[c + 2 * i]), p1 = ex2(u[c + 2 * i + 1]);
-                    l[c + 2 * i] += p0;
-                    l[c + 2 * i + 1] += p1;
-                    const __half2 q = __floats2half2_rn(p0 * sv, p1 * sv);
-                    h[i] = *reinterpret_cast<const uint32_t *>(&q);
-                }
-                *reinterpret_cast<uint4 *>(prow + ((((wg * CW + c) >> 3) ^ (tok & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            for (int c = 0; c < CW; c += 2) {
+                const float p0 = ex2(u[c]), p1 = ex2(u[c + 1]);
+                l[c] += p0;
+                l[c + 1] += p1;
+                const __half2 q = __floats2half2_rn(p0 * sv, p1 * sv);
+                h[c / 2] = *reinterpret_cast<const uint32_t *>(&q);
             }
+            wait.unless(p_free, p_empty, (j & 1) ^ 1);
+#pragma unroll
+            for (int c = 0; c < CW; c += 8)
+                *reinterpret_cast<uint4 *>(prow + ((((wg * CW + c) >> 3) ^ (tok & 7)) << 4)) =
+                    make_uint4(h[c / 2], h[c / 2 + 1], h[c / 2 + 2], h[c / 2 + 3]);
             fence_async();
             tc_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(p_full(b));
-            if (__builtin_expect(d.x & kLast, 0)) {  // the part's record
+            if (lane == 0) bar_arrive(p_full);
+            ready = j + 1 < n_tiles && bar_test(s_full(b ^ 1), ((j + 1) >> 1) & 1);
+            if (d.x & kLast) {  // the part's record
                 float *rec = p.part + (static_cast<size_t>(worker) + d.z) * R * (D + 4);
                 // row sums over the tokens
 #pragma unroll
@@ -1148,29 +1177,29 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
 #pragma unroll
                     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
                     if (lane == 0) maxima[qw * (CW + 1) + c] = v;
+                    l[c] = 0.f;
                 }
-#pragma unroll
-                for (int c = 0; c < CW; c++) l[c] = 0.f;
                 named_sync(1 + wg, 128);
                 if (tok < CW) {
                     float *row = rec + (wg * CW + tok) * (D + 4);
                     row[0] = m_row[tok];
                     row[1] = (maxima[tok] + maxima[CW + 1 + tok]) + (maxima[2 * (CW + 1) + tok] + maxima[3 * (CW + 1) + tok]);
+                    m_row[R + tok] = 0.f;
                 }
-                wait(p_empty(b), par);
+                wait(p_empty, j & 1);
                 __syncwarp();
                 tc_after();
                 const float up = pow2(E);
 #pragma unroll
                 for (int c = 0; c < CW; c += 8) {
                     float o[8];
-                    tmem_ld<8>(tbase + lanes + C::T_O + wg * CW + c, o);
+                    tmem_ld<8>(o_addr + c, o);
                     if (tok < D)
 #pragma unroll
                         for (int i = 0; i < 8; i++) rec[(wg * CW + c + i) * (D + 4) + 4 + tok] = o[i] * up;
                 }
                 tc_before();
-                named_sync(1 + wg, 128);  // (also: `maxima` is free again)
+                named_sync(1 + wg, 128);  // (also: `maxima` is free again, -m is 0 for all)
                 if (lane == 0) bar_arrive(o_free);
             }
         }
