@@ -114,6 +114,16 @@ struct TreeList {
     int parts_packed, parts, workers;
     TreeListSeg seg[TQ_MAX_SEGMENTS];
 };
+struct TreeQueryParams {
+    int H, g, n_rb, n_var, rows;  // rows: N g
+    const uint16_t *q;
+    int64_t qs[3];
+    uint8_t *images;
+    int *error;
+    uint8_t var_bits[TQ_MAX_SEGMENTS][kMaxH];
+    uint32_t sign_bits[4];       // (head_dim 64 and 128)
+    float inv_sqrt_d, qk_scale;
+};
 struct TreeMergeParams {
     TreeList t;
     const uint16_t *q, *k, *v;

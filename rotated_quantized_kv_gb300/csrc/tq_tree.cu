@@ -187,10 +187,13 @@ __global__ void __launch_bounds__(kTreeThreads) tree_plain_kernel(const __grid_c
 // chain of loads, so F drafts' or U records' loads are in flight at a time, and the
 // drafts come before the wait for the records (the grid may start while the last
 // CTAs of the main kernel run).
-template <int D>
+// U: 16 where the rows are too few to fill the GPU anyway (up to 4096: measured 12.1
+// against 14.3 us at 512 rows of 24 records), else 8, with which twice the warps fit
+// (44 against 59 us at 8192 rows of 3).
+template <int D, int U>
 __global__ void __launch_bounds__(kTreeThreads) tree_merge_kernel(const __grid_constant__ TreeMergeParams p) {
     constexpr int J = (D + 31) / 32;
-    constexpr int F = J <= 8 ? 4 : 32 / J, U = J <= 4 ? 8 : 32 / J;
+    constexpr int F = J <= 8 ? 4 : 32 / J;
     __shared__ float draft_x[kTreeWarps][TQ_MAX_DRAFTS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = p.t.N * p.t.g;
@@ -294,43 +297,54 @@ __global__ void __launch_bounds__(kTreeThreads) tree_merge_kernel(const __grid_c
     const int group = bh * p.t.n_rb + rb;
     const int np = (tp + kTreePart - 1) / kTreePart, nf = (tf + kTreePart - 1) / kTreePart;
     // part i (packed ones, then the others): workers lo..hi hold its records
-    // (records in order: the parts', within one its workers')
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-#pragma unroll 1
-    for (int base = 0;; base += 32) {  // a record per lane, then U of them at a time
-        int slot = -1, kind = 0, before = 0;
+    // Record `at` of the group (in order: the parts', within one its workers'): its slot, or -1;
+    // kind: packed or not; n: the group's records
+    auto locate = [&](int at, int &kind, int &n) {
+        int slot = -1;
+        n = 0;
 #pragma unroll 1
         for (int i = 0; i < np + nf; i++) {
             const int k0 = i < np ? i * kTreePart : tp + (i - np) * kTreePart;
             const int k1 = min(k0 + kTreePart, i < np ? tp : tp + tf);
-            const int lo = (first + k0) / per, hi = (first + k1 - 1) / per, at = base + lane - before;
-            if (at >= 0 && at <= hi - lo) slot = lo + at + part_of(p.t, group, tp, k0), kind = i >= np;
-            before += hi - lo + 1;
+            const int lo = (first + k0) / per, hi = (first + k1 - 1) / per;
+            if (at >= n && at - n <= hi - lo) slot = lo + at - n + part_of(p.t, group, tp, k0), kind = i >= np;
+            n += hi - lo + 1;
         }
-        if (base >= before) break;
-        const int count = min(32, before - base);
-        const float *rec = p.part + (static_cast<size_t>(max(slot, 0)) * p.t.R + r) * (D + 4);
+        return slot;
+    };
+    int kind = 0, records, slot = locate(lane, kind, records);
+    const float *rows_at = p.part + static_cast<size_t>(r) * (D + 4);
+    const size_t stride = static_cast<size_t>(p.t.R) * (D + 4);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+#pragma unroll 1
+    for (int base = 0; base < records; base += 32) {  // a record per lane, then U of them at a time
+        if (base) slot = locate(base + lane, kind, records);
         float2 ml = make_float2(-kInf, 0.f);
-        if (slot >= 0) ml = __ldcg(reinterpret_cast<const float2 *>(rec));
-        float now = fmaxf(M, ml.x);
-        nan |= ml.y != ml.y;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
-        if (now == -kInf) continue;
-        const float old = M == -kInf ? 0.f : ex2(M - now), f = ex2(ml.x - now);
-        M = now;
-        L *= old;
-#pragma unroll
-        for (int j = 0; j < J; j++) a[0][j] *= old, a[1][j] *= old;
+        if (slot >= 0) ml = __ldcg(reinterpret_cast<const float2 *>(rows_at + slot * stride));
+        const int count = min(32, records - base);
+        float f = 0.f;
 #pragma unroll 1
         for (int u0 = 0; u0 < count; u0 += U) {
             float v[U][J];
 #pragma unroll
             for (int u = 0; u < U; u++) {
                 const int s = __shfl_sync(0xffffffffu, slot, u0 + u);
-                const float *at = p.part + (static_cast<size_t>(max(s, 0)) * p.t.R + r) * (D + 4) + 4 + lane;
+                const float *at = rows_at + max(s, 0) * stride + 4 + lane;
 #pragma unroll
                 for (int j = 0; j < J; j++) v[u][j] = s >= 0 && lane + 32 * j < D ? __ldcg(at + 32 * j) : 0.f;
+            }
+            if (u0 == 0) {  // (the first loads are on their way) the new largest m
+                float now = fmaxf(M, ml.x);
+                nan |= ml.y != ml.y;
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+                if (now == -kInf) break;
+                const float old = M == -kInf ? 0.f : ex2(M - now);
+                f = ex2(ml.x - now);
+                M = now;
+                L *= old;
+#pragma unroll
+                for (int j = 0; j < J; j++) a[0][j] *= old, a[1][j] *= old;
             }
 #pragma unroll
             for (int u = 0; u < U; u++) {
@@ -391,7 +405,12 @@ cudaError_t tree_dim(const TreeParams &p, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.n_seg > 0 ? 1 : 0;  // (behind a kernel)
-    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, m);
+    if constexpr (D <= 128) {
+        if (rows <= 4096) return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, 16>, m);
+        return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, 8>, m);
+    } else {
+        return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, 1024 / D>, m);
+    }
 }
 
 }  // namespace

@@ -451,151 +451,137 @@ struct RingGeo {
     int stage, stages;
 };
 
-// The queries of a block's rows as the MMA's B operand, for keys of kb bits (0: fp16
-// keys, unrotated queries), and the factor A.  TL lanes hold a row, 16 coordinates
-// each; warp `wi` of the block's `nw` takes every nw-th group of 32 / TL rows.  A power
-// of two 2^-e common to the block brings every rotated coordinate
-// below 1: |(R q)_i| <= |q|_2 <= sqrt(d) max |q_i|.  (A row a thousand times smaller than
-// the block's largest still has the precision of fp16, 22 bits being carried.)
+// The queries as the MMA's B operand, one image per (b, h, rb) and key width kb (0:
+// fp16 keys, unrotated queries).  A CTA writes up to 32 rows of an image, a warp a row at a
+// time, D / 32 neighbouring coordinates a lane.  A power of two 2^-e common to the block
+// brings every rotated coordinate below 1: |(R q)_i| <= |q|_2 <= sqrt(d) max |q_i|.  (A
+// row a thousand times smaller than the block's largest still has the precision of
+// fp16, 22 bits being carried.)  The main kernel may start meanwhile: it waits for this grid
+// before it touches the images.
+constexpr int kPrepWarps = 8, kPrepRows = 32;
 template <int D, int R>
-__device__ __forceinline__ void prepare_queries(const TreeParams &p, int b, int h, int rb, int kb, uint8_t *q, float *A,
-                                                unsigned *red, int wi, int nw) {
+__global__ void __launch_bounds__(32 * kPrepWarps) tree_queries_kernel(const __grid_constant__ TreeQueryParams p) {
     using C = Mma<D, R>;
-    constexpr int TL = D / 16, RPW = 32 / TL;
-    const int lane = threadIdx.x & 31, lt = lane % TL;
-    const bool vec = ((reinterpret_cast<uintptr_t>(p.q) | (p.qs[0] * 2) | (p.qs[1] * 2) | (p.qs[2] * 2)) & 15) == 0;
-    const uint32_t neg = p.sign_bits[lt >> 1] >> (16 * (lt & 1));
-    auto load = [&](int r, uint32_t (&w)[8]) {
+    constexpr int EL = D / 32, ROWS = R < kPrepRows ? R : kPrepRows, SPLIT = R / ROWS;
+    __shared__ unsigned red[kPrepWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.error = 0;
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int part = blockIdx.x % SPLIT, img = blockIdx.x / SPLIT, v = img % p.n_var, group = img / p.n_var;
+    const int bh = group / p.n_rb, rb = group - bh * p.n_rb, b = bh / p.H, h = bh - b * p.H, kb = p.var_bits[v][h];
+    uint8_t *image = p.images + static_cast<size_t>(img) * tree_image_stride<D, R>();
+    const bool vec = ((reinterpret_cast<uintptr_t>(p.q) | (p.qs[0] * 2) | (p.qs[1] * 2) | (p.qs[2] * 2)) & 7) == 0;
+    auto load = [&](int r, uint32_t (&w)[EL / 2]) {
         const int row = rb * R + r;
+        const uint16_t *src = p.q + b * p.qs[0] + (row / p.g) * p.qs[1] + (h * p.g + row % p.g) * p.qs[2] + EL * lane;
 #pragma unroll
-        for (int i = 0; i < 8; i++) w[i] = 0;
-        if (row >= p.N * p.g) return;
-        const uint16_t *src = p.q + b * p.qs[0] + (row / p.g) * p.qs[1] + (h * p.g + row % p.g) * p.qs[2] + 16 * lt;
-        if (vec) {
-            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(src)), c = __ldg(reinterpret_cast<const uint4 *>(src) + 1);
-            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = c.x, w[5] = c.y, w[6] = c.z, w[7] = c.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; i++) w[i] = __ldg(src + 2 * i) | static_cast<uint32_t>(__ldg(src + 2 * i + 1)) << 16;
+        for (int i = 0; i < EL / 2; i++) {
+            w[i] = 0;
+            if (row < p.rows)
+                w[i] = vec ? __ldg(reinterpret_cast<const unsigned *>(src) + i)
+                           : __ldg(src + 2 * i) | static_cast<uint32_t>(__ldg(src + 2 * i + 1)) << 16;
         }
     };
     int e = 0;
     if (kb) {
         unsigned mx = 0;  // fp16 bits of the block's largest finite |q_i|
-        for (int r0 = wi * RPW; r0 < R; r0 += nw * RPW) {
-            uint32_t w[8];
-            load(r0 + lane / TL, w);
+#pragma unroll 4
+        for (int r = warp; r < R; r += kPrepWarps) {
+            uint32_t w[EL / 2];
+            load(r, w);
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const unsigned a = w[i] & 0x7FFFu, c = (w[i] >> 16) & 0x7FFFu;
-                mx = max(mx, max(a < 0x7C00u ? a : 0u, c < 0x7C00u ? c : 0u));
+            for (int i = 0; i < EL / 2; i++) {
+                const unsigned x = w[i] & 0x7FFFu, y = (w[i] >> 16) & 0x7FFFu;
+                mx = max(mx, max(x < 0x7C00u ? x : 0u, y < 0x7C00u ? y : 0u));
             }
         }
         mx = __reduce_max_sync(0xffffffffu, mx);
-        if (lane == 0) red[wi] = mx;
+        if (lane == 0) red[warp] = mx;
         __syncthreads();
-        for (int i = 0; i < nw; i++) mx = max(mx, red[i]);
+#pragma unroll
+        for (int i = 0; i < kPrepWarps; i++) mx = max(mx, red[i]);
         const unsigned f = __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(mx))));
         if (mx) e = static_cast<int>((f >> 23) & 0xFFu) - 126 + (D == 128 ? 4 : 3);
     }
     // x = m_t qk_scale (2^(1-b) sum code q + (2^-b - 1) sum q) = m_t A (U + c), U = 2^(-e - 11) sum code q,
     // c = 2^(-e - 11) (1/2 - 2^(b-1)) sum q
-    if (wi == 0 && lane == 0) *A = kb ? p.qk_scale * pow2(12 - kb + e) : p.qk_scale;
-    for (int r0 = wi * RPW; r0 < R; r0 += nw * RPW) {
-        const int r = r0 + lane / TL;
-        uint32_t raw[8];
-        load(r, raw);
-        uint8_t *line = q + (R * 128) * (16 * lt / 64) + r * 128;  // the half of the row with this lane's coordinates
-        const int c0 = (16 * lt % 64) / 8;                        // its first 16-byte chunk there
+    if (part == 0 && threadIdx.x == 0)
+        *reinterpret_cast<float *>(image + C::QIMG) = kb ? p.qk_scale * pow2(12 - kb + e) : p.qk_scale;
+    const uint32_t neg = p.sign_bits[EL * lane >> 5] >> (EL * lane & 31);
+    // coordinate 32 g + i + 16 u meets the code at place 32 g + 2 i + u, at bit s_i: times 2^(13 - s_i)
+    const int u = (EL * lane >> 4) & 1, i0 = EL * lane & 15, g = EL * lane >> 5;
+#pragma unroll 1
+    for (int r = ROWS * part + warp; r < ROWS * (part + 1); r += kPrepWarps) {
+        uint32_t w[EL / 2];
+        load(r, w);
+        // byte of the row at place k: line k / 64, 16-byte chunk (k % 64) / 8 permuted by the row
+        auto place = [&](int k) {
+            return image + (k >> 6) * R * 128 + r * 128 + ((((k & 63) >> 3) ^ (r & 7)) << 4) + (k & 7) * 2;
+        };
         if (kb == 0) {
 #pragma unroll
-            for (int c = 0; c < 2; c++)
-                *reinterpret_cast<uint4 *>(line + (((c0 + c) ^ (r & 7)) << 4)) =
-                    make_uint4(raw[4 * c], raw[4 * c + 1], raw[4 * c + 2], raw[4 * c + 3]);
+            for (int i = 0; i < EL / 2; i++) reinterpret_cast<uint32_t *>(place(EL * lane))[i] = w[i];
             continue;
         }
-        float v[16];
+        float x[EL];
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&raw[i]));
-            v[2 * i] = f.x, v[2 * i + 1] = f.y;
+        for (int i = 0; i < EL / 2; i++) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            x[2 * i] = f.x, x[2 * i + 1] = f.y;
         }
-        // R q: signs, butterflies 1..8 in the lane, the others across lanes, signs, scale
+        // R q: signs, butterflies in the lane, across lanes, signs, scale
 #pragma unroll
-        for (int i = 0; i < 16; i++)
-            if ((neg >> i) & 1u) v[i] = -v[i];
+        for (int i = 0; i < EL; i++)
+            if ((neg >> i) & 1u) x[i] = -x[i];
 #pragma unroll
-        for (int h = 1; h < 16; h <<= 1)
+        for (int s = 1; s < EL; s <<= 1)
 #pragma unroll
-            for (int i = 0; i < 16; i++)
-                if (!(i & h)) {
-                    const float a = v[i], c = v[i + h];
-                    v[i] = a + c, v[i + h] = a - c;
+            for (int i = 0; i < EL; i++)
+                if (!(i & s)) {
+                    const float y = x[i], z = x[i + s];
+                    x[i] = y + z, x[i + s] = y - z;
                 }
 #pragma unroll
-        for (int h = 1; h < TL; h <<= 1) {
-            const float sg = (lt & h) ? -1.f : 1.f;
+        for (int s = 1; s < 32; s <<= 1) {
+            const float sg = (lane & s) ? -1.f : 1.f;
 #pragma unroll
-            for (int i = 0; i < 16; i++) v[i] = fmaf(v[i], sg, __shfl_xor_sync(0xffffffffu, v[i], h));
+            for (int i = 0; i < EL; i++) x[i] = fmaf(x[i], sg, __shfl_xor_sync(0xffffffffu, x[i], s));
         }
         float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; i++) {
-            v[i] *= ((neg >> i) & 1u) ? -p.inv_sqrt_d : p.inv_sqrt_d;
-            sum += v[i];
+        for (int i = 0; i < EL; i++) {
+            x[i] *= ((neg >> i) & 1u) ? -p.inv_sqrt_d : p.inv_sqrt_d;
+            sum += x[i];
         }
 #pragma unroll
-        for (int h = 1; h < TL; h <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, h);
+        for (int s = 16; s >= 1; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
         // the row's constant, met by 2^-11 twice (hi, lo): 8 rows of 16 bytes per k half
-        if (lt == 0) {
+        if (lane == 0) {
             const float y = sum * pow2(-e) * (0.5f - pow2(kb - 1));
             const __half hi = __float2half_rn(y), lo = __float2half_rn(y - __half2float(hi));
-            uint8_t *at = q + 2 * C::QPART + (r >> 3) * 256 + (r & 7) * 16;
+            uint8_t *at = image + 2 * C::QPART + (r >> 3) * 256 + (r & 7) * 16;
             *reinterpret_cast<uint4 *>(at) = make_uint4(
                 static_cast<uint32_t>(__half_as_ushort(hi)) | static_cast<uint32_t>(__half_as_ushort(lo)) << 16, 0, 0, 0);
             *reinterpret_cast<uint4 *>(at + 128) = make_uint4(0, 0, 0, 0);
         }
-        // coordinate 32 g + i + 16 u meets the code at place 32 g + 2 i + u, at bit s_i: times 2^(13 - s_i)
-        uint32_t w[16];  // hi, lo
+        uint32_t hl[EL];  // hi, lo
 #pragma unroll
-        for (int i = 0; i < 16; i++) {
-            const int pos = (kb * i) & 15, o = pos + kb <= 10 ? pos : pos >= 8 ? pos - 8 : pos;
-            const float y = v[i] * pow2(13 - e - min(o, 10 - kb));
+        for (int i = 0; i < EL; i++) {
+            const int pos = (kb * (i0 + i)) & 15, o = pos + kb <= 10 ? pos : pos >= 8 ? pos - 8 : pos;
+            const float y = x[i] * pow2(13 - e - min(o, 10 - kb));
             const __half hi = __float2half_rn(y), lo = __float2half_rn(y - __half2float(hi));
-            w[i] = static_cast<uint32_t>(__half_as_ushort(hi)) | static_cast<uint32_t>(__half_as_ushort(lo)) << 16;
+            hl[i] = static_cast<uint32_t>(__half_as_ushort(hi)) | static_cast<uint32_t>(__half_as_ushort(lo)) << 16;
         }
-        // the pair of lanes (u = 0, 1) shares its 32 places: the even lane takes i < 8
-        const int u = lt & 1;
-        uint32_t hi[8], lo[8];
+        // the pair of lanes (u = 0, 1) shares its places: lane u takes the u-th half of the coordinates i
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const uint32_t own = u ? w[8 + i] : w[i];
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, u ? w[i] : w[8 + i], 1);
-            hi[i] = u ? prmt(other, own, 0x5410u) : prmt(own, other, 0x5410u);
-            lo[i] = u ? prmt(other, own, 0x7632u) : prmt(own, other, 0x7632u);
-        }
-#pragma unroll
-        for (int c = 0; c < 2; c++) {
-            const int at = ((c0 + c) ^ (r & 7)) << 4;
-            *reinterpret_cast<uint4 *>(line + at) = make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-            *reinterpret_cast<uint4 *>(line + C::QPART + at) = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+        for (int i = 0; i < EL / 2; i++) {
+            const uint32_t own = u ? hl[EL / 2 + i] : hl[i];
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, u ? hl[i] : hl[EL / 2 + i], 16 / EL);
+            uint8_t *at = place(32 * g + 2 * (i0 + u * (EL / 2) + i));
+            *reinterpret_cast<uint32_t *>(at) = u ? prmt(other, own, 0x5410u) : prmt(own, other, 0x5410u);
+            *reinterpret_cast<uint32_t *>(at + C::QPART) = u ? prmt(other, own, 0x7632u) : prmt(own, other, 0x7632u);
         }
     }
-}
-
-constexpr int kPrepWarps = 8;
-// A CTA per (b, h, rb) and image.  (The main kernel may start meanwhile: it waits
-// for this grid before it touches the images.)
-template <int D, int R>
-__global__ void __launch_bounds__(32 * kPrepWarps) tree_queries_kernel(const __grid_constant__ TreeParams p) {
-    __shared__ unsigned red[kPrepWarps];
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.error = 0;
-    asm volatile("griddepcontrol.launch_dependents;");
-    const int v = blockIdx.x % p.n_var, group = blockIdx.x / p.n_var;
-    const int bh = group / p.n_rb, rb = group - bh * p.n_rb, b = bh / p.H, h = bh - b * p.H;
-    uint8_t *image = p.images + (static_cast<size_t>(group) * p.n_var + v) * tree_image_stride<D, R>();
-    prepare_queries<D, R>(p, b, h, rb, p.var_bits[v][h], image, reinterpret_cast<float *>(image + Mma<D, R>::QIMG), red,
-                          threadIdx.x >> 5, kPrepWarps);
 }
 
 // State of a key or value warp's walk through the ring.
@@ -1258,7 +1244,14 @@ cudaError_t tree_mma(const TreeParams &p, const TreeLevels &lv, cudaStream_t s) 
     cudaError_t e = cudaFuncSetAttribute(tree_mma_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return e;
     const int images = p.B * p.H * p.n_rb * p.n_var;
-    tree_queries_kernel<D, R><<<images, 32 * kPrepWarps, 0, s>>>(p);
+    TreeQueryParams qp;
+    qp.H = p.H, qp.g = p.g, qp.n_rb = p.n_rb, qp.n_var = p.n_var, qp.rows = p.N * p.g;
+    qp.q = p.q, qp.images = p.images, qp.error = p.error;
+    for (int i = 0; i < 3; i++) qp.qs[i] = p.qs[i];
+    std::memcpy(qp.var_bits, p.var_bits, sizeof(qp.var_bits));
+    std::memcpy(qp.sign_bits, p.sign_bits, sizeof(qp.sign_bits));
+    qp.inv_sqrt_d = p.inv_sqrt_d, qp.qk_scale = p.qk_scale;
+    tree_queries_kernel<D, R><<<images * std::max(1, R / kPrepRows), 32 * kPrepWarps, 0, s>>>(qp);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
