@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -165,14 +166,14 @@ _lib.tq_decode_attention_static.argtypes = [ctypes.POINTER(tq_layer_view), _I, _
                                             _P, _P]
 _lib.tq_rope_frequencies.argtypes = [ctypes.POINTER(tq_rope_spec), _P]
 _lib.tq_rope_table.argtypes = [ctypes.POINTER(tq_rope_spec), _I, _I, _P, _P]
-_lib.tq_rope.argtypes = [ctypes.POINTER(tq_rope_view), _I, _I, _I, _I, _P, _L, ctypes.POINTER(tq_rope_tensor), _I, _I,
+_lib.tq_rope.argtypes = [ctypes.POINTER(tq_rope_view), _I, _I, _I, _I, _P, _L, _P, _I, _I,
                          _P]
 _lib.tq_append.argtypes = [ctypes.POINTER(tq_segment), ctypes.POINTER(tq_rotation), ctypes.POINTER(tq_rope_view), _P, _L,
                            _P, _P, _P, _P, _I, _I, _P, _P, _P, _L, _P]
 _lib.tq_read.argtypes = [ctypes.POINTER(tq_segment), ctypes.POINTER(tq_rotation), _I, _P, _P, _I, _P, _P, _P, _P, _P]
 _lib.tq_tree_workspace_size.argtypes = [ctypes.POINTER(tq_layer_view), _I, _I, _I, _I, _I,
                                         ctypes.POINTER(ctypes.c_size_t)]
-_lib.tq_tree_attention.argtypes = [ctypes.POINTER(tq_layer_view), _I, _I, _I, _I, ctypes.POINTER(tq_tree), _P,
+_lib.tq_tree_attention.argtypes = [ctypes.POINTER(tq_layer_view), _I, _I, _I, _I, _P, _P,
                                    ctypes.c_size_t, _P]
 TQ_STATIC_WORKSPACE_BYTES = 16 << 20
 for _n in EXPORTED:
@@ -302,6 +303,7 @@ class PackedSegment:
     tq_packed_size reports."""
 
     kind = TQ_SEG_PACKED
+    _struct = _ref = None
     attn_mass = None  # optional float tensor [B][H][capacity]: written by tq_decode_attention
 
     def __init__(self, layout: tq_segment_layout, device="cuda", n_tokens: int = 0):
@@ -333,6 +335,18 @@ class PackedSegment:
         s.attn_mass = _ptr(self.attn_mass)
         return s
 
+    def reference(self):
+        """The segment for one call: the same structure each time, its fields set anew."""
+        s = self._struct
+        if s is None:
+            s = self._struct = tq_segment()
+            s.kind = TQ_SEG_PACKED
+            self._ref = ctypes.byref(s)
+        s.n_tokens, s.layout, p = self.n_tokens, self.layout, s.packed
+        p.kcodes, p.vcodes = self.kcodes.data_ptr(), self.vcodes.data_ptr()
+        p.kscale, p.vscale = self.kscale.data_ptr(), self.vscale.data_ptr()
+        return self._ref
+
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in
                    (self.kcodes, self.vcodes, self.kscale, self.vscale, self.qjl_signs, self.qjl_norm,
@@ -344,6 +358,7 @@ class Fp16Segment:
     """Tokens kept verbatim in fp16: [B][H][capacity][d] K and V."""
 
     kind = TQ_SEG_FP16
+    _struct = _ref = None
     attn_mass = None  # optional float tensor [B][H][capacity]: written by tq_decode_attention
 
     def __init__(self, batch, n_heads, head_dim, capacity, device="cuda", n_tokens=0, k=None, v=None):
@@ -359,6 +374,17 @@ class Fp16Segment:
         s.k16, s.v16 = _ptr(self.k), _ptr(self.v)
         s.attn_mass = _ptr(self.attn_mass)
         return s
+
+    def reference(self):
+        """The segment for one call: the same structure each time, its fields set anew."""
+        s = self._struct
+        if s is None:
+            s = self._struct = tq_segment()
+            s.kind = TQ_SEG_FP16
+            self._ref = ctypes.byref(s)
+        s.n_tokens, s.layout = self.n_tokens, self.layout
+        s.k16, s.v16 = self.k.data_ptr(), self.v.data_ptr()
+        return self._ref
 
 
 def layer_view(rot: tq_rotation, segments, qjl_estimator: int = TQ_QJL_UNBIASED) -> tq_layer_view:
@@ -489,7 +515,16 @@ def views_array(layers):
 
 
 # ----------------------------------------------------------------- serving
+# These calls run once a layer and token, so their marshalling is kept short: structures
+# and stride triples are packed in one go, devices compared as numbers, the stream
+# taken raw.
 _DTYPE = {torch.float16: TQ_DTYPE_F16, torch.bfloat16: TQ_DTYPE_BF16, torch.float32: TQ_DTYPE_F32}
+_F16, _I32 = torch.float16, torch.int32
+_pack3 = struct.Struct("3q").pack
+_pack_rope = [struct.Struct("PPi4x6q" * n).pack for n in range(TQ_MAX_ROPE_TENSORS + 1)]
+_pack_tree = struct.Struct(f"i4xPPP9qPq{TQ_MAX_SEGMENTS}PP").pack
+assert struct.calcsize("PPi4x6q") == ctypes.sizeof(tq_rope_tensor)
+assert struct.calcsize(f"i4xPPP9qPq{TQ_MAX_SEGMENTS}PP") == ctypes.sizeof(tq_tree)
 
 
 def _require(ok: bool, where: str):
@@ -497,33 +532,32 @@ def _require(ok: bool, where: str):
         raise TQError(-1, where)
 
 
-def _int32(t, where, *shape):
-    """Checks an int32 CUDA tensor of `shape` with unit stride in its last axis
-    (None: not given)."""
-    if t is not None:
-        _require(t.dtype == torch.int32 and tuple(t.shape) == shape and (shape[-1] <= 1 or t.stride(-1) == 1), where)
+def _int32(t, where, shape):
+    """Checks an int32 tensor of `shape` with unit stride in its last axis."""
+    _require(t.dtype == _I32 and t.shape == shape and (shape[-1] <= 1 or t.stride(-1) == 1), where)
 
 
-def _same_device(where, *tensors):
-    devices = {t.device for t in tensors if t is not None}
-    _require(len(devices) == 1, where)
-    return devices.pop()
-
-
-def _call(device, stream, where, fn):
-    """fn(stream) with `device` current (the library works on the current
-    device), on the given stream or the device's current one."""
-    if device.type != "cuda":
+def _call(tensors, stream, where, fn, *args):
+    """fn(*args, stream) with the tensors' device current (the library works on the
+    current device), on the given stream or that device's current one.  All tensors
+    (None: not given) have to be on one CUDA device."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise TQError(-1, where)
+    if dev < 0:
         raise TQError(-1, where)
-    if device.index == torch.cuda.current_device():
-        _check(fn(_stream(stream)), where)
+    if stream is not None:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     else:
-        with torch.cuda.device(device):
-            _check(fn(_stream(stream)), where)
-
-
-def _strides(t, axes=(0, 1, 2)):
-    return (_L * 3)(*(t.stride(a) for a in axes))
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status != 0:
+        raise TQError(status, where)
 
 
 def tq_make_rope(rotary_dim: int, base: float = 10000.0, scaling: int = TQ_ROPE_SCALE_NONE, factor: float = 1.0,
@@ -546,8 +580,7 @@ def tq_rope_table(spec: tq_rope_spec, n_pos: int, first_pos: int = 0, device="cu
     """float32 CUDA table [n_pos][2][rotary_dim / 2] of cosines and sines."""
     _require(n_pos >= 0, "tq_rope_table")
     t = torch.empty(n_pos, 2, spec.rotary_dim // 2, dtype=torch.float32, device=device)
-    _call(t.device, stream, "tq_rope_table",
-          lambda s: _lib.tq_rope_table(ctypes.byref(spec), first_pos, n_pos, _ptr(t), s))
+    _call([t], stream, "tq_rope_table", _lib.tq_rope_table, ctypes.byref(spec), first_pos, n_pos, t.data_ptr())
     return t
 
 
@@ -561,6 +594,7 @@ class Rope:
         _require(layout in (TQ_ROPE_HALF, TQ_ROPE_INTERLEAVED), "Rope")
         self.table, self.layout = table, layout
         self.view = tq_rope_view(2 * table.shape[2], layout, table.shape[0], _ptr(table))
+        self.ref = ctypes.byref(self.view)
 
 
 def tq_rope(rope: Rope, positions: torch.Tensor, x, out=None, inverse: bool = False, stream=None):
@@ -568,28 +602,30 @@ def tq_rope(rope: Rope, positions: torch.Tensor, x, out=None, inverse: bool = Fa
     stride in d, or a list of up to four of the same B, T, d and type: queries
     and keys) into `out` (likewise; None: in place).  positions: int32 [B][T] or
     [T].  inverse: the transpose (the gradient of x)."""
-    xs = [x] if isinstance(x, torch.Tensor) else list(x)
+    one = isinstance(x, torch.Tensor)
+    xs = [x] if one else list(x)
     outs = xs if out is None else ([out] if isinstance(out, torch.Tensor) else list(out))
-    _require(1 <= len(xs) <= TQ_MAX_ROPE_TENSORS and len(xs) == len(outs), "tq_rope")
+    where = "tq_rope"
+    n = len(xs)
+    _require(1 <= n <= TQ_MAX_ROPE_TENSORS and n == len(outs) and xs[0].dim() == 4, where)
+    dtype = xs[0].dtype
     B, _, T, d = xs[0].shape
-    arr = (tq_rope_tensor * len(xs))()
-    for a, i, o in zip(arr, xs, outs):
-        _require(i.dim() == 4 and i.shape == o.shape and (i.shape[0], i.shape[2], i.shape[3]) == (B, T, d) and
-                 i.dtype == o.dtype == xs[0].dtype and i.dtype in _DTYPE and
-                 (d == 1 or i.stride(3) == o.stride(3) == 1), "tq_rope")
-        a.in_, a.out, a.n_heads = _ptr(i), _ptr(o), i.shape[1]
-        a.in_stride, a.out_stride = _strides(i), _strides(o)
+    _require(dtype in _DTYPE, where)
+    fields = []
+    for i, o in zip(xs, outs):
+        shape, a, b = i.shape, i.stride(), o.stride()
+        _require(len(shape) == 4 and shape == o.shape and shape[0] == B and shape[2] == T and shape[3] == d and
+                 i.dtype == dtype and o.dtype == dtype and (d == 1 or a[3] == b[3] == 1), where)
+        fields += (i.data_ptr(), o.data_ptr(), shape[1], a[0], a[1], a[2], b[0], b[1], b[2])
     if positions.dim() == 1:
-        _int32(positions, "tq_rope", T)
+        _int32(positions, where, (T,))
         ps = 0
     else:
-        _int32(positions, "tq_rope", B, T)
+        _int32(positions, where, (B, T))
         ps = positions.stride(0)
-    dev = _same_device("tq_rope", rope.table, positions, *xs, *outs)
-    _call(dev, stream, "tq_rope",
-          lambda s: _lib.tq_rope(ctypes.byref(rope.view), _DTYPE[xs[0].dtype], B, T, d, _ptr(positions), ps, arr,
-                                 len(xs), int(inverse), s))
-    return outs[0] if isinstance(x, torch.Tensor) else outs
+    _call([positions, rope.table, *xs, *outs], stream, where, _lib.tq_rope, rope.ref, _DTYPE[dtype], B, T, d,
+          positions.data_ptr(), ps, _pack_rope[n](*fields), n, 1 if inverse else 0)
+    return outs[0] if one else outs
 
 
 def tq_append(seg, rot: tq_rotation | None, K: torch.Tensor, V: torch.Tensor, t_begin: torch.Tensor, n_new=None,
@@ -603,31 +639,36 @@ def tq_append(seg, rot: tq_rotation | None, K: torch.Tensor, V: torch.Tensor, t_
     segment are skipped.  seg.n_tokens is left to the caller."""
     where = "tq_append"
     L = seg.layout
-    _require(K.dim() == 4 and K.shape == V.shape and K.dtype == V.dtype == torch.float16 and K.stride(3) == 1 and
-             V.stride(3) == 1 and (K.shape[0], K.shape[1], K.shape[3]) == (L.batch, L.n_heads, L.head_dim), where)
-    B, _, S, _ = K.shape
+    shape = K.shape
+    _require(len(shape) == 4 and shape == V.shape and K.dtype == _F16 and V.dtype == _F16 and
+             shape[0] == L.batch and shape[1] == L.n_heads and shape[3] == L.head_dim, where)
+    a, b = K.stride(), V.stride()
+    B, S = shape[0], shape[2]
+    _require(a[3] == 1 and b[3] == 1, where)
     if n_max is None:
         n_max = index.shape[1] if index is not None else S
-    _int32(t_begin, where, B)
-    _int32(n_new, where, B)
+    tensors = [K, V, t_begin, seg.kcodes if seg.kind == TQ_SEG_PACKED else seg.k]
+    _int32(t_begin, where, (B,))
+    n_ptr = index_ptr = pos_ptr = rope_ref = None
+    index_stride = ps = 0
+    if n_new is not None:
+        _int32(n_new, where, (B,))
+        n_ptr = n_new.data_ptr()
+        tensors.append(n_new)
     if index is not None:
         _require(index.dim() == 2 and index.shape[1] >= n_max, where)
-        _int32(index, where, B, index.shape[1])
-    ps = 0
+        _int32(index, where, (B, index.shape[1]))
+        index_ptr, index_stride = index.data_ptr(), index.stride(0)
+        tensors.append(index)
     if rope is not None:
         _require(positions is not None, where)
-        _int32(positions, where, *((S,) if positions.dim() == 1 else (B, S)))
+        _int32(positions, where, (S,) if positions.dim() == 1 else (B, S))
         ps = positions.stride(0) if positions.dim() == 2 else 0
-    own = seg.kcodes if seg.kind == TQ_SEG_PACKED else seg.k
-    dev = _same_device(where, own, K, V, t_begin, n_new, index, rope.table if rope else None,
-                       positions if rope else None)
-    sg = seg.segment()
-    _call(dev, stream, where,
-          lambda s: _lib.tq_append(ctypes.byref(sg), ctypes.byref(rot) if rot is not None else None,
-                                   ctypes.byref(rope.view) if rope is not None else None,
-                                   _ptr(positions) if rope is not None else None, ps, _ptr(K), _strides(K), _ptr(V),
-                                   _strides(V), S, n_max, _ptr(t_begin), _ptr(n_new), _ptr(index),
-                                   index.stride(0) if index is not None else 0, s))
+        pos_ptr, rope_ref = positions.data_ptr(), rope.ref
+        tensors += (positions, rope.table)
+    _call(tensors, stream, where, _lib.tq_append, seg.reference(), ctypes.byref(rot) if rot is not None else None,
+          rope_ref, pos_ptr, ps, K.data_ptr(), _pack3(a[0], a[1], a[2]), V.data_ptr(), _pack3(b[0], b[1], b[2]), S, n_max,
+          t_begin.data_ptr(), n_ptr, index_ptr, index_stride)
 
 
 def tq_read(seg, rot: tq_rotation | None, t_begin: torch.Tensor, n_max: int, n_read=None, out=None,
@@ -646,18 +687,27 @@ def tq_read(seg, rot: tq_rotation | None, t_begin: torch.Tensor, n_max: int, n_r
         out = [torch.zeros(shape, dtype=dtype, device=own.device) for _ in range(2)]
     k, v = out
     some = [t for t in (k, v) if t is not None]
-    for t in some:
-        _require(tuple(t.shape) == shape and t.dtype == some[0].dtype and t.dtype in _DTYPE and t.stride(3) == 1, where)
-    _int32(t_begin, where, L.batch)
-    _int32(n_read, where, L.batch)
-    if some:
-        dev = _same_device(where, own, t_begin, n_read, *some)
-        sg = seg.segment()
-        _call(dev, stream, where,
-              lambda s: _lib.tq_read(ctypes.byref(sg), ctypes.byref(rot) if rot is not None else None, n_max,
-                                     _ptr(t_begin), _ptr(n_read), _DTYPE[some[0].dtype], _ptr(k),
-                                     _strides(k) if k is not None else None, _ptr(v),
-                                     _strides(v) if v is not None else None, s))
+    _int32(t_begin, where, (L.batch,))
+    tensors = [t_begin, own, *some]
+    n_ptr = None
+    if n_read is not None:
+        _int32(n_read, where, (L.batch,))
+        n_ptr = n_read.data_ptr()
+        tensors.append(n_read)
+    if not some:
+        return out
+    dt = some[0].dtype
+    _require(dt in _DTYPE, where)
+    args = []
+    for t in (k, v):
+        if t is None:
+            args += (None, None)
+            continue
+        a = t.stride()
+        _require(t.shape == shape and t.dtype == dt and a[3] == 1, where)
+        args += (t.data_ptr(), _pack3(a[0], a[1], a[2]))
+    _call(tensors, stream, where, _lib.tq_read, seg.reference(), ctypes.byref(rot) if rot is not None else None, n_max,
+          t_begin.data_ptr(), n_ptr, _DTYPE[dt], *args)
     return out
 
 
@@ -700,24 +750,27 @@ def tq_tree_attention(view: tq_layer_view, q: torch.Tensor, k: torch.Tensor, v: 
     _require(q.dim() == 4 and k.dim() == 4 and k.shape == v.shape, where)
     B, N, Hq, d = q.shape
     H = k.shape[1]
-    _require(tuple(k.shape) == (B, H, N, d) and q.dtype == k.dtype == v.dtype == out.dtype == torch.float16 and
-             tuple(out.shape) == (B, N, Hq, d) and out.is_contiguous() and workspace.is_contiguous() and
-             q.stride(3) == k.stride(3) == v.stride(3) == 1, where)
-    t = tq_tree()
-    t.n_drafts, t.q, t.k, t.v, t.out = N, _ptr(q), _ptr(k), _ptr(v), _ptr(out)
-    t.q_stride, t.k_stride, t.v_stride = _strides(q), _strides(k), _strides(v)
+    a, b, c = q.stride(), k.stride(), v.stride()
+    _require(k.shape == (B, H, N, d) and q.dtype == _F16 and k.dtype == _F16 and v.dtype == _F16 and out.dtype == _F16 and
+             out.shape == q.shape and out.is_contiguous() and workspace.is_contiguous() and
+             a[3] == b[3] == c[3] == 1, where)
+    tensors = [q, k, v, out, workspace]
+    mask_ptr, mask_stride = 0, 0
     if mask is not None:
         W = -(-N // 32)
-        _require(mask.dtype == torch.int32 and mask.is_contiguous() and tuple(mask.shape) in ((N, W), (B, N, W)), where)
-        t.mask = _ptr(mask)
-        t.mask_stride_b = N * W if mask.dim() == 3 else 0
-    lens = [] if seg_len is None else list(seg_len)
-    _require(len(lens) in (0, view.n_segments), where)
-    for i, n in enumerate(lens):
-        _int32(n, where, B)
-        t.seg_len[i] = _ptr(n)
-    dev = _same_device(where, q, k, v, out, workspace, mask, *lens)
-    _call(dev, stream, where,
-          lambda s: _lib.tq_tree_attention(ctypes.byref(view), B, H, Hq, d, ctypes.byref(t), _ptr(workspace),
-                                           workspace.numel() * workspace.element_size(), s))
+        _require(mask.dtype == _I32 and mask.is_contiguous() and mask.shape in ((N, W), (B, N, W)), where)
+        mask_ptr, mask_stride = mask.data_ptr(), N * W if mask.dim() == 3 else 0
+        tensors.append(mask)
+    lens = [0] * TQ_MAX_SEGMENTS
+    if seg_len is not None:
+        _require(len(seg_len) == view.n_segments, where)
+        for i, n in enumerate(seg_len):
+            if n is not None:
+                _int32(n, where, (B,))
+                lens[i] = n.data_ptr()
+                tensors.append(n)
+    tree = _pack_tree(N, q.data_ptr(), k.data_ptr(), v.data_ptr(), a[0], a[1], a[2], b[0], b[1], b[2], c[0], c[1], c[2],
+                      mask_ptr, mask_stride, *lens, out.data_ptr())
+    _call(tensors, stream, where, _lib.tq_tree_attention, ctypes.byref(view), B, H, Hq, d, tree, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
     return out
