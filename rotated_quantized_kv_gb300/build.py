@@ -23,7 +23,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CUDA_SOURCES = ["tq_compress.cu", "tq_compress_dense.cu", "tq_decode.cu", "tq_mass.cu", "tq_static.cu",
                 "tq_generic.cu", "tq_compress_rows.cu", "tq_compress_rows_nh2.cu", "tq_compress_rows_nh4.cu",
                 "tq_compress_rows_np2.cu", "tq_rope.cu", "tq_append.cu", "tq_read.cu", "tq_tree.cu",
-                "tq_tree_mma.cu"] + [
+                "tq_tree_mma.cu", "tq_append_rows_keys.cu", "tq_append_rows_values.cu", "tq_read_rows_keys.cu",
+                "tq_read_rows_values.cu"] + [
                 f"tq_decode_kb{k}.cu" for k in range(1, 9)] + [
                 f"tq_decode_wide_kb{k}.cu" for k in range(1, 9)]
 HOST_SOURCES = ["tq_host.cpp", "tq_serve_host.cpp"]
@@ -40,7 +41,8 @@ def _sources():
     return [os.path.join(CSRC, s) for s in CUDA_SOURCES + HOST_SOURCES] + [
         os.path.join(CSRC, h) for h in ("tq_internal.h", "tq_decode_common.cuh", "tq_decode_packed.cuh",
                                         "tq_mass.h", "tq_decode_geometry.h", "tq_compress_rows.cuh", "tq_serve.h",
-                                        "tq_team.cuh", "tq_tree.cuh")] + [
+                                        "tq_team.cuh", "tq_tree.cuh", "tq_row_map.cuh", "tq_append_rows.cuh",
+                                        "tq_read_rows.cuh")] + [
         os.path.join(ROOT, "include", "tq.h")]
 
 

@@ -407,6 +407,44 @@ bool value_buckets4(const float *thr, int nt, uint32_t *out) {
     return true;
 }
 
+// The rotation's sign masks and output scales of RowsParams (nh and np set).
+void rows_rotation(RowsParams &p, const uint32_t *sign_bits, int d) {
+    const float c_d = inv_sqrt_f32(d);
+    for (int i = 0; i < p.nh * kD / 2; ++i) {
+        const int j = i % (d / 2);
+        const uint32_t s0 = (sign_bits[(2 * j) >> 5] >> ((2 * j) & 31)) & 1u;
+        const uint32_t s1 = (sign_bits[(2 * j + 1) >> 5] >> ((2 * j + 1) & 31)) & 1u;
+        p.in_mask[i] = (s0 << 15) | (s1 << 31);
+    }
+    for (int i = 0; i < p.nh * kD; ++i) {
+        const int j = i % d;
+        p.out_scale[i] = ((sign_bits[j >> 5] >> (j & 31)) & 1u) ? -c_d : c_d;
+    }
+}
+
+// The thresholds and tables of a value width; false if its buckets hold two.  The
+// bucket tables are made on a width's first use (they depend on the codebook alone).
+bool rows_values(RowsParams &p, int bits, int law) {
+    struct Buckets {
+        std::once_flag once;
+        bool ok;
+        RowsParams::Bucket b[kRowsBuckets];
+    };
+    static Buckets tables[2][5];
+    const FittedCodebook &cb = fit(bits, law);
+    for (int k = 0; k + 1 < (1 << bits); ++k) p.thr[k] = static_cast<float>(cb.bound[k]);
+    p.bucket4_ok = 0;
+    if (bits > 4) return true;
+    Buckets &t = tables[law == TQ_VALUE_LAW_GAUSS ? 0 : 1][bits];
+    std::call_once(t.once, [&] {
+        t.ok = bits <= 3 ? value_buckets(p.thr, (1 << bits) - 1, t.b)
+                         : value_buckets4(p.thr, 15, reinterpret_cast<uint32_t *>(t.b));
+    });
+    std::memcpy(p.bucket, t.b, sizeof(t.b));
+    if (bits == 4) p.bucket4_ok = t.ok ? 1 : 0;
+    return bits == 4 || t.ok;
+}
+
 // Launches of the one-thread-per-slice kernels for the heads c.sel[0..n_sel)
 // (none of them sketched) at head_dim d = 128, 256 or 512 (sign_bits: the
 // rotation's d bits; c supplies the pointers, strides and widths): the keys of
@@ -440,17 +478,7 @@ cudaError_t launch_rows(const CompressParams &c, const tq_segment_layout *layout
     p.capacity = c.capacity;
     p.nh = d >= kD ? d / kD : 1;
     p.np = d >= kD ? 1 : kD / d;  // head_dim 64: two tokens per thread, the same signs for both
-    const float c_d = inv_sqrt_f32(d);
-    for (int i = 0; i < p.nh * kD / 2; ++i) {
-        const int j = i % (d / 2);
-        const uint32_t s0 = (sign_bits[(2 * j) >> 5] >> ((2 * j) & 31)) & 1u;
-        const uint32_t s1 = (sign_bits[(2 * j + 1) >> 5] >> ((2 * j + 1) & 31)) & 1u;
-        p.in_mask[i] = (s0 << 15) | (s1 << 31);
-    }
-    for (int i = 0; i < p.nh * kD; ++i) {
-        const int j = i % d;
-        p.out_scale[i] = ((sign_bits[j >> 5] >> (j & 31)) & 1u) ? -c_d : c_d;
-    }
+    rows_rotation(p, sign_bits, d);
     for (int values = 0; values < 2; ++values) {
         p.X = values ? c.V : c.K;
         p.codes = values ? c.vcodes : c.kcodes;
@@ -463,10 +491,7 @@ cudaError_t launch_rows(const CompressParams &c, const tq_segment_layout *layout
                 if (in_sel[h] && (values ? c.vbits[h] : c.kbits[h]) == bits) p.head[p.n_heads++] = static_cast<uint8_t>(h);
             if (p.n_heads == 0) continue;
             if (values) {
-                const FittedCodebook &cb = fit(bits, layout->value_law);
-                for (int k = 0; k + 1 < (1 << bits); ++k) p.thr[k] = static_cast<float>(cb.bound[k]);
-                if (bits <= 3 && !value_buckets(p.thr, (1 << bits) - 1, p.bucket)) return cudaErrorNotSupported;
-                p.bucket4_ok = bits == 4 && value_buckets4(p.thr, 15, p.bucket4) ? 1 : 0;
+                if (!rows_values(p, bits, layout->value_law)) return cudaErrorNotSupported;
             }
             const cudaError_t e = launch_compress_rows(p, bits, values != 0, s);
             if (e != cudaSuccess) return e;
@@ -1004,6 +1029,8 @@ void tqk::value_centroids(float *flat, const uint8_t *bits, int H, int law) { fi
 float tqk::rotation_scale(int d) { return inv_sqrt_f32(d); }
 int tqk::decode_wait_polls() { return g_wait_polls.load(); }
 int tqk::current_sm_count() { return sm_count(); }
+void tqk::fill_rows_rotation(RowsParams &p, const uint32_t *sign_bits, int d) { rows_rotation(p, sign_bits, d); }
+bool tqk::fill_rows_values(RowsParams &p, int bits, int law) { return rows_values(p, bits, law); }
 
 // =============================================================== C ABI
 extern "C" {

@@ -2,6 +2,7 @@
 // scales to rotated vectors, then the inverse rotation (R is its own inverse).
 // The binary32 steps are those of tq_dequantize, the result is rounded once.
 #include <algorithm>
+#include <cstring>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -19,6 +20,17 @@ __device__ __forceinline__ void put(float *p, float x) { *p = x; }
 __device__ __forceinline__ void put(__half *p, float x) { *p = __float2half_rn(x); }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
+// Four coordinates by one store.
+__device__ __forceinline__ void put4(float *p, const float *x) { *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]); }
+__device__ __forceinline__ void put4(__half *p, const float *x) {
+    __half2 v[2] = {__floats2half2_rn(x[0], x[1]), __floats2half2_rn(x[2], x[3])};
+    *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<uint2 *>(v);
+}
+__device__ __forceinline__ void put4(__nv_bfloat16 *p, const float *x) {
+    __nv_bfloat162 v[2] = {__floats2bfloat162_rn(x[0], x[1]), __floats2bfloat162_rn(x[2], x[3])};
+    *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<uint2 *>(v);
+}
+
 // Position of row j of sequence b; false: not read.
 __device__ __forceinline__ bool read_row(const RowMap &m, int b, int j, int capacity, int &pos) {
     const int n = m.n_rows ? min(m.n_rows[b], m.n_max) : m.n_max;
@@ -34,7 +46,7 @@ __global__ void __launch_bounds__(kReadThreads) read_team_kernel(const __grid_co
     constexpr int E = TM::E, TL = TM::T, VPW = TM::VPW;
     __shared__ float cent[kCbTotal];
     __shared__ __align__(16) float stage[TM::STAGE ? kReadWarps * D : 4];
-    for (int j = threadIdx.x; j < kCbTotal; j += kReadThreads) cent[j] = p.centroid[j];
+    stage_widths(cent, p.centroid, p.vwidths, 0);
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int v = lane / TL, lt = lane % TL;
@@ -45,12 +57,9 @@ __global__ void __launch_bounds__(kReadThreads) read_team_kernel(const __grid_co
     const long long step = static_cast<long long>(gridDim.x) * kReadWarps * VPW;
     for (long long base = (static_cast<long long>(blockIdx.x) * kReadWarps + warp) * VPW; base < n; base += step) {
         const long long f = base + v;
-        long long r = f < n ? f : 0;
-        const int j = static_cast<int>(r % p.rows.n_max);
-        r /= p.rows.n_max;
-        const int h = static_cast<int>(r % p.H);
-        r /= p.H;
-        const int b = static_cast<int>(r % p.B), kv = kv0 + static_cast<int>(r / p.B);
+        unsigned long long r = f < n ? f : 0;
+        const int j = split_index(r, p.rows.n_max), h = split_index(r, p.H), b = split_index(r, p.B);
+        const int kv = kv0 + static_cast<int>(r);
         int pos = 0;
         const bool valid = f < n && read_row(p.rows, b, j, p.seg.capacity, pos);
         float a[E];
@@ -60,11 +69,20 @@ __global__ void __launch_bounds__(kReadThreads) read_team_kernel(const __grid_co
                                  (kv ? p.seg.voff[h] : p.seg.koff[h]) + static_cast<size_t>(pos) * (D * bits / 8);
             const float sc = (kv ? p.seg.vs : p.seg.ks)[(static_cast<size_t>(b) * p.H + h) * p.seg.capacity + pos];
             const float inv_cells = __uint_as_float(static_cast<uint32_t>(127 - bits) << 23);  // 2^-b
+            const int rk = D * bits / 8;
 #pragma unroll
-            for (int e = 0; e < E; e++) {
-                const uint32_t k = code_at(rec, lt * E + e, bits);
-                a[e] = kv ? __fmul_rn(sc, cent[cb_off(bits) + k])
-                          : __fmul_rn(sc, __fadd_rn(__fmul_rn(static_cast<float>(2 * k + 1), inv_cells), -1.0f));
+            for (int e = 0; e < E; e += 4) {
+                uint32_t k[4];
+                if (rk % 4 == 0) {
+                    load_codes4(rec, rk / 4, lt * E + e, bits, k);
+                } else {  // d = 16 and an odd width
+#pragma unroll
+                    for (int i = 0; i < 4; i++) k[i] = code_at(rec, lt * E + e + i, bits);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    a[e + i] = kv ? __fmul_rn(sc, cent[cb_off(bits) + k[i]])
+                                  : __fmul_rn(sc, __fadd_rn(__fmul_rn(static_cast<float>(2 * k[i] + 1), inv_cells), -1.0f));
             }
         } else {
 #pragma unroll
@@ -74,6 +92,11 @@ __global__ void __launch_bounds__(kReadThreads) read_team_kernel(const __grid_co
         if (valid) {
             const int64_t *st = kv ? p.vs : p.ks;
             T *out = static_cast<T *>(kv ? p.V : p.K) + b * st[0] + h * st[1] + j * st[2];
+            if (p.vec && (!TM::STAGE || !p.rotate)) {
+#pragma unroll
+                for (int e = 0; e < E; e += 4) put4(out + lt * E + e, a + e);
+                continue;
+            }
 #pragma unroll
             for (int e = 0; e < E; e++) put(out + (p.rotate ? coord<D>(lt, e) : lt * E + e), a[e]);
         }
@@ -88,14 +111,9 @@ __global__ void __launch_bounds__(kReadThreads) read_copy_kernel(const __grid_co
     const long long n = static_cast<long long>(nkv) * p.B * p.H * p.rows.n_max * units;
     for (long long f = blockIdx.x * static_cast<long long>(kReadThreads) + threadIdx.x; f < n;
          f += gridDim.x * static_cast<long long>(kReadThreads)) {
-        long long r = f;
-        const int u = static_cast<int>(r % units);
-        r /= units;
-        const int j = static_cast<int>(r % p.rows.n_max);
-        r /= p.rows.n_max;
-        const int h = static_cast<int>(r % p.H);
-        r /= p.H;
-        const int b = static_cast<int>(r % p.B), kv = kv0 + static_cast<int>(r / p.B);
+        unsigned long long r = f;
+        const int u = split_index(r, units), j = split_index(r, p.rows.n_max), h = split_index(r, p.H);
+        const int b = split_index(r, p.B), kv = kv0 + static_cast<int>(r);
         int pos;
         if (!read_row(p.rows, b, j, p.seg.capacity, pos)) continue;
         const uint8_t *src = (kv ? p.seg.v : p.seg.k) + b * (kv ? p.seg.vblock : p.seg.kblock) +
@@ -104,8 +122,16 @@ __global__ void __launch_bounds__(kReadThreads) read_copy_kernel(const __grid_co
         const __half *x = reinterpret_cast<const __half *>(&w);
         const int64_t *st = kv ? p.vs : p.ks;
         T *out = static_cast<T *>(kv ? p.V : p.K) + b * st[0] + h * st[1] + j * st[2] + 8 * u;
+        float f8[8];
 #pragma unroll
-        for (int e = 0; e < 8; e++) put(out + e, __half2float(x[e]));
+        for (int e = 0; e < 8; e++) f8[e] = __half2float(x[e]);
+        if (p.vec) {
+            put4(out, f8);
+            put4(out + 4, f8 + 4);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++) put(out + e, f8[e]);
+        }
     }
 }
 
@@ -120,6 +146,64 @@ cudaError_t read_team(const ReadParams &p, cudaStream_t s) {
     const int per = kReadWarps * Team<D>::VPW;
     read_team_kernel<D, T><<<grid_for((vec + per - 1) / per, 8), kReadThreads, 0, s>>>(p);
     return cudaGetLastError();
+}
+
+// Head_dim 128 and many rows: one thread per vector, a launch per width
+// (tq_read_rows.cuh).  Small reads take the team kernel: one launch, 32 lanes a vector.
+// One sequence of 8 heads, 3-bit codes, team / rows: 64 tokens 3.0 / 7.0 us, 512 (8192
+// vectors) 5.6 / 7.3, 1024 (16384) 9.0 / 7.4, 4096 27.2 / 13.1.
+constexpr long long kRowsVectors = 12288;
+
+// Whether every value codebook in use is odd (the Gaussian one is, by construction).
+bool odd_levels(const ReadParams &p) {
+    for (int b = 1; b <= 8; b++) {
+        if (!((p.vwidths >> b) & 1u)) continue;
+        const float *c = p.centroid + cb_off(b);
+        for (int i = 0; i < 1 << (b - 1); i++)
+            if (c[i] != -c[(1 << b) - 1 - i]) return false;
+    }
+    return true;
+}
+
+cudaError_t read_rows(const ReadParams &p, int dtype, cudaStream_t s) {
+    ReadRowsParams q;
+    std::memset(&q, 0, sizeof(q));
+    q.rows = p.rows;
+    q.B = p.B, q.H = p.H, q.capacity = p.seg.capacity;
+    q.dtype = dtype, q.rotate = p.rotate;
+    for (int i = 0; i < kD; i++) {
+        const bool n = (p.sign_bits[i >> 5] >> (i & 31)) & 1u;
+        q.out_scale[i] = n ? -p.inv_sqrt_d : p.inv_sqrt_d;
+    }
+    bool beside = false;  // the first launch waits for the stream, the others need not wait for it
+    for (int kv = 0; kv < 2; kv++) {
+        q.out = kv ? p.V : p.K;
+        if (!q.out) continue;
+        const int per16 = dtype == TQ_DTYPE_F32 ? 4 : 8;
+        q.vec = (reinterpret_cast<uintptr_t>(q.out) & 15u) == 0;
+        for (int i = 0; i < 3; i++) {
+            q.st[i] = kv ? p.vs[i] : p.ks[i];
+            q.vec &= q.st[i] % per16 == 0;
+        }
+        q.codes = kv ? p.seg.v : p.seg.k;
+        q.scale = kv ? p.seg.vs : p.seg.ks;
+        q.block = kv ? p.seg.vblock : p.seg.kblock;
+        for (int h = 0; h < p.H; h++) q.off[h] = kv ? p.seg.voff[h] : p.seg.koff[h];
+        for (int bits = 1; bits <= 8; bits++) {
+            q.n_heads = 0;
+            for (int h = 0; h < p.H; h++)
+                if ((kv ? p.seg.vbits[h] : p.seg.kbits[h]) == bits) q.head[q.n_heads++] = static_cast<uint8_t>(h);
+            if (q.n_heads == 0) continue;
+            if (kv) std::memcpy(q.level, p.centroid + cb_off(bits), sizeof(float) << bits);
+            std::memset(q.flip, 0, sizeof(q.flip));
+            for (int i = 0; i < kD * bits && p.rotate; i++)
+                if ((p.sign_bits[i / bits >> 5] >> (i / bits & 31)) & 1u) q.flip[i >> 5] |= 1u << (i & 31);
+            const cudaError_t e = kv ? launch_read_values(q, bits, beside, s) : launch_read_keys(q, bits, beside, s);
+            if (e != cudaSuccess) return e;
+            beside = true;
+        }
+    }
+    return cudaSuccess;
 }
 
 template <typename T>
@@ -143,7 +227,15 @@ cudaError_t read_typed(const ReadParams &p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_read(const ReadParams &p, int dtype, cudaStream_t s) {
+cudaError_t launch_read(const ReadParams &params, int dtype, cudaStream_t s) {
+    ReadParams p = params;
+    const uintptr_t align = dtype == TQ_DTYPE_F32 ? 15u : 7u;
+    p.vwidths = 0;
+    for (int h = 0; h < p.H; h++) p.vwidths |= 1u << p.seg.vbits[h];
+    p.vec = ((reinterpret_cast<uintptr_t>(p.K) | reinterpret_cast<uintptr_t>(p.V)) & align) == 0;
+    for (int i = 0; i < 3; i++) p.vec &= (!p.K || p.ks[i] % 4 == 0) && (!p.V || p.vs[i] % 4 == 0);
+    const long long vec = ((p.K ? 1LL : 0) + (p.V ? 1 : 0)) * p.B * p.H * p.rows.n_max;
+    if (!p.seg.fp16 && p.d == kD && vec >= kRowsVectors && vec < (1LL << 34) && odd_levels(p)) return read_rows(p, dtype, s);
     switch (dtype) {
         case TQ_DTYPE_F16: return read_typed<__half>(p, s);
         case TQ_DTYPE_BF16: return read_typed<__nv_bfloat16>(p, s);

@@ -68,8 +68,23 @@ struct AppendParams {
     uint32_t sign_bits[kMaxD / 32];
     float inv_sqrt_d;
     float thr[kCbTotal];         // value thresholds, flat by bit width
+    int law;
+    uint32_t vwidths;            // bit b: some head's values have b bits
+    int vec;                     // 8-byte loads of the source
 };
 cudaError_t launch_append(const AppendParams &p, cudaStream_t s);
+
+// One thread per vector (head_dim 128), a launch per key and per value width: r.X,
+// its strides and r.T (rows a sequence may get) describe the source rows.
+struct AppendRowsParams {
+    RowsParams r;
+    RowMap rows;
+    RopeView rope;               // keys
+    const int *positions;
+    int64_t pos_stride;
+};
+cudaError_t launch_append_keys(const AppendRowsParams &p, int bits, bool beside, cudaStream_t s);
+cudaError_t launch_append_values(const AppendRowsParams &p, int bits, bool beside, cudaStream_t s);
 
 struct ReadParams {
     SegView seg;
@@ -81,8 +96,28 @@ struct ReadParams {
     uint32_t sign_bits[kMaxD / 32];
     float inv_sqrt_d;
     float centroid[kCbTotal];
+    uint32_t vwidths;            // bit b: some head's values have b bits
+    int vec;                     // stores of four coordinates
 };
 cudaError_t launch_read(const ReadParams &p, int dtype, cudaStream_t s);
+
+// One thread per vector (head_dim 128), a launch per key and per value width.
+struct ReadRowsParams {
+    RowMap rows;
+    const uint8_t *codes;
+    const float *scale;
+    uint64_t block, off[kMaxH];
+    int B, H, capacity, n_heads; // heads of this launch
+    uint8_t head[kMaxH];
+    void *out;
+    int64_t st[3];
+    int dtype, vec, rotate;      // vec: 16-byte stores
+    uint32_t flip[32];           // record words: ones in the fields of the coordinates to negate
+    float out_scale[kD];
+    float level[256];            // values: the centroids
+};
+cudaError_t launch_read_keys(const ReadRowsParams &p, int bits, bool beside, cudaStream_t s);
+cudaError_t launch_read_values(const ReadRowsParams &p, int bits, bool beside, cudaStream_t s);
 
 // ----------------------------------------------------------------- tree attention
 // The work is a list of 128-token tiles.  For sequence b in order, KV head h,
@@ -189,5 +224,7 @@ void value_centroids(float *flat, const uint8_t *bits, int H, int law);
 float rotation_scale(int d);
 int decode_wait_polls();
 int current_sm_count();
+void fill_rows_rotation(RowsParams &p, const uint32_t *sign_bits, int d);
+bool fill_rows_values(RowsParams &p, int bits, int law);
 
 }  // namespace tqk

@@ -339,6 +339,7 @@ tq_status tq_append(const tq_segment *dst, const tq_rotation *rot, const tq_rope
     if (packed) {
         std::memcpy(p.sign_bits, rot->sign_bits, sizeof(p.sign_bits));
         p.inv_sqrt_d = rotation_scale(p.d);
+        p.law = L.value_law;
         try {
             value_thresholds(p.thr, L.vbits, p.H, L.value_law);
         } catch (...) {

@@ -32,11 +32,13 @@ __device__ __forceinline__ int coord(int lt, int e) {
 // for coordinate lt * E + e (the input), out_neg bit e for coord<D>(lt, e).
 template <int D>
 __device__ __forceinline__ void lane_sign_masks(const uint32_t *sb, int lt, uint32_t &in_neg, uint32_t &out_neg) {
-    in_neg = out_neg = 0u;
+    constexpr int E = Team<D>::E;
+    in_neg = (sb[lt * E >> 5] >> (lt * E & 31)) & (E == 32 ? 0xFFFFFFFFu : (1u << E % 32) - 1u);
+    out_neg = in_neg;
+    if constexpr (Team<D>::STAGE) {
+        out_neg = 0u;
 #pragma unroll
-    for (int e = 0; e < Team<D>::E; e++) {
-        in_neg |= static_cast<uint32_t>(neg_coord(sb, lt * Team<D>::E + e)) << e;
-        out_neg |= static_cast<uint32_t>(neg_coord(sb, coord<D>(lt, e))) << e;
+        for (int e = 0; e < E; e++) out_neg |= ((sb[e] >> lt) & 1u) << e;
     }
 }
 
@@ -177,22 +179,22 @@ __device__ __forceinline__ void store_record(const uint8_t *cw, int bits, uint8_
     }
 }
 
-// Codes of the team's rotated vector (one byte each, cw[coordinate]) and its
-// scale: keys on the midrise grid of [-m, m], values by #{k : thr_k < y / sigma}
+// Codes of the lane's rotated coordinates (slot by slot) and the vector's scale: keys on the midrise grid of [-m, m], values by #{k : thr_k < y / sigma}
 // (S: the sum of squares; thr: the width's thresholds).
 template <int D>
-__device__ __forceinline__ float quantize_team(const float (&a)[Team<D>::E], float m, float S, int bits, bool values,
-                                               const float *thr, uint8_t *cw, int lt) {
+__device__ __forceinline__ float team_codes(const float (&a)[Team<D>::E], float m, float S, int bits, bool values,
+                                            const float *thr, uint32_t (&k)[Team<D>::E]) {
     constexpr int E = Team<D>::E;
+    float u[E];
     if (!values) {
         const float rr = m > 0.0f ? __frcp_rn(m) : 0.0f;
         const float hc = static_cast<float>(1 << (bits - 1)), top = static_cast<float>((1 << bits) - 1);
 #pragma unroll
         for (int e = 0; e < E; e++) {
             // round(v + 1) 2^(b-1) as one FMA (scaling by a power of two commutes with the rounding)
-            float u = __fmaf_rn(__fmul_rn(a[e], rr), hc, hc);
-            u = fminf(fmaxf(u, 0.0f), top);
-            cw[coord<D>(lt, e)] = static_cast<uint8_t>(__float_as_uint(__fadd_rd(u, 8388608.0f)) & 0xFFu);
+            u[e] = __fmaf_rn(__fmul_rn(a[e], rr), hc, hc);
+            u[e] = fminf(fmaxf(u[e], 0.0f), top);
+            k[e] = __float_as_uint(__fadd_rd(u[e], 8388608.0f)) & 0xFFu;
         }
         return m;
     }
@@ -200,13 +202,92 @@ __device__ __forceinline__ float quantize_team(const float (&a)[Team<D>::E], flo
     const float rr = sigma > 0.0f ? __frcp_rn(sigma) : 0.0f;
 #pragma unroll
     for (int e = 0; e < E; e++) {
-        const float u = __fmul_rn(a[e], rr);
-        int k = 0;
-        for (int s = 1 << (bits - 1); s >= 1; s >>= 1)
-            if (thr[k + s - 1] < u) k += s;
-        cw[coord<D>(lt, e)] = static_cast<uint8_t>(k);
+        u[e] = __fmul_rn(a[e], rr);
+        k[e] = 0;
+    }
+    for (int s = 1 << (bits - 1); s >= 1; s >>= 1) {
+#pragma unroll
+        for (int e = 0; e < E; e++)
+            if (thr[k[e] + s - 1] < u[e]) k[e] += s;
     }
     return sigma;
+}
+
+// The same with the codes as bytes, cw[coordinate].
+template <int D>
+__device__ __forceinline__ float quantize_team(const float (&a)[Team<D>::E], float m, float S, int bits, bool values,
+                                               const float *thr, uint8_t *cw, int lt) {
+    uint32_t k[Team<D>::E];
+    const float scale = team_codes<D>(a, m, S, bits, values, thr, k);
+#pragma unroll
+    for (int e = 0; e < Team<D>::E; e++) cw[coord<D>(lt, e)] = static_cast<uint8_t>(k[e]);
+    return scale;
+}
+
+// The record of a team of four codes a lane (d <= 128), written without shared
+// memory: the lane's codes as one field of 4 * bits bits, and lane c gathers the
+// fields that reach into word c.  Every lane of the warp calls it; store: the
+// team's vector is written.
+template <int D>
+__device__ __forceinline__ void store_fields(const uint32_t (&k)[4], int bits, uint8_t *dst, int lt, bool store) {
+    constexpr int T = Team<D>::T;
+    static_assert(Team<D>::E == 4, "four coordinates a lane");
+    const int width = 4 * bits, first = 32 * lt / width;
+    const uint32_t field = k[0] | (k[1] << bits) | (k[2] << (2 * bits)) | (k[3] << (3 * bits));
+    const int n = T == 32 ? 8 / bits + 2 : 8;  // teams of a warp may differ in width
+    uint32_t x = 0;
+    for (int i = 0; i < n; i++) {
+        const int from = first + i, off = width * from - 32 * lt;
+        const uint32_t f = __shfl_sync(0xffffffffu, field, from < T ? from : 0, T);
+        if (from < T && off < 32) x |= off >= 0 ? f << off : f >> -off;
+    }
+    if (!store) return;
+    const int rk = D * bits / 8;
+    if (rk % 4 == 0) {
+        if (lt < rk / 4) reinterpret_cast<uint32_t *>(dst)[lt] = x;
+    } else {  // d = 16 and an odd width: 2-byte halves
+        if (lt < (rk + 2) / 4) reinterpret_cast<uint16_t *>(dst)[2 * lt] = static_cast<uint16_t>(x);
+        if (lt < rk / 4) reinterpret_cast<uint16_t *>(dst)[2 * lt + 1] = static_cast<uint16_t>(x >> 16);
+    }
+}
+
+// Codes i0..i0 + 3 (i0 a multiple of four) of a record of a multiple of four bytes.
+__device__ __forceinline__ void load_codes4(const uint8_t *rec, int words, int i0, int bits, uint32_t (&k)[4]) {
+    const int bit = i0 * bits, w = bit >> 5;
+    const uint32_t *r = reinterpret_cast<const uint32_t *>(rec);
+    const uint32_t lo = r[w], hi = w + 1 < words ? r[w + 1] : 0u, mask = (1u << bits) - 1u;
+    const uint32_t f = __funnelshift_r(lo, hi, bit & 31);
+#pragma unroll
+    for (int e = 0; e < 4; e++) k[e] = (f >> (e * bits)) & mask;
+}
+
+// A kernel parameter through its generic address: lanes that read different words of
+// a table then share memory transactions (the constant path serves one word at a time).
+template <class P>
+__device__ __forceinline__ const P *param_table(const P *p) {
+    asm("" : "+l"(p));
+    return p;
+}
+
+// The tables of the widths in `used` (bit b: width b), flat by width.
+__device__ __forceinline__ void stage_widths(float *to, const float *param, uint32_t used, int count_less) {
+    const float *from = param_table(param);
+    for (int b = 1; b <= 8; b++) {
+        if (!((used >> b) & 1u)) continue;
+        for (int j = threadIdx.x; j < (1 << b) - count_less; j += blockDim.x) to[cb_off(b) + j] = from[cb_off(b) + j];
+    }
+}
+
+// vec / n and vec % n for the index of a vector: 32-bit arithmetic where it fits.
+__device__ __forceinline__ int split_index(unsigned long long &r, int n) {
+    if ((r >> 32) == 0) {
+        const uint32_t x = static_cast<uint32_t>(r), q = x / static_cast<uint32_t>(n);
+        r = q;
+        return static_cast<int>(x - q * static_cast<uint32_t>(n));
+    }
+    const int m = static_cast<int>(r % static_cast<unsigned>(n));
+    r /= static_cast<unsigned>(n);
+    return m;
 }
 
 // Load the lane's E contiguous fp16 coordinates (16- or 8-byte loads).
