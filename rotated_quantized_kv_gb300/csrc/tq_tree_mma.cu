@@ -132,29 +132,31 @@ __device__ __forceinline__ bool named_or(int id, int threads, bool x) {
     return r != 0;
 }
 
-// A bounded wait.  A thread whose wait ran out waits no more: it walks its range to
-// the end (all addresses come from the list, none from data, and what it signals
-// lets the others end too), and the error flag tells the host that the output is
-// incomplete.
+// A bounded wait, by whole warps.  A warp whose wait ran out sets the error flag (the
+// output is incomplete) and leaves its role's loop: it reads no descriptor, touches no
+// memory and signals nothing any more, so that no other warp is let past a barrier
+// early; those time out in turn.  Roles that meet at named barriers leave together.
 struct Waiter {
     int *error;
     int polls;
-    bool gone;
+    bool gone;  // the same in all lanes
     // Two barriers at once: half of the warp's lanes poll each (a wait costs some 200
-    // cycles even when there is nothing to wait for).  The whole warp calls, and is
-    // together again afterwards.
+    // cycles even when there is nothing to wait for).
     __device__ __forceinline__ void both(unsigned bar0, unsigned parity0, unsigned bar1, unsigned parity1) {
         const bool low = (threadIdx.x & 31) < 16;
         (*this)(low ? bar0 : bar1, low ? parity0 : parity1);
-        gone = __any_sync(0xffffffffu, gone);
     }
     // The wait behind an early bar_test.
     __device__ __forceinline__ void unless(bool done, unsigned bar, unsigned parity) {
-        if (!done) (*this)(bar, parity);
-        __syncwarp();
+        bool lost = gone;
+        if (!done) lost = poll(bar, parity);
+        gone = __any_sync(0xffffffffu, lost);
     }
     __device__ __forceinline__ void operator()(unsigned bar, unsigned parity) {
-        if (gone) return;
+        gone = __any_sync(0xffffffffu, poll(bar, parity));
+    }
+    __device__ __forceinline__ bool poll(unsigned bar, unsigned parity) {
+        if (gone) return true;
         unsigned ok = 0;
         if (polls > 0)
             asm volatile(
@@ -164,10 +166,8 @@ struct Waiter {
                 : "=r"(ok)
                 : "r"(bar), "r"(parity), "r"(polls), "r"(1000u)
                 : "memory");
-        if (!ok) {
-            gone = true;
-            atomicExch(error, 1);
-        }
+        if (!ok) atomicExch(error, 1);
+        return !ok;
     }
 };
 
@@ -437,8 +437,8 @@ struct Mma {
     static constexpr int O_M = O_D + kSlots * 64;   // [R] m, [R] -m as used, [R] factors
     static constexpr int O_X = O_M + 3 * R * 4;     // [NWG][4][CW + 1] maxima of the warps
     static constexpr int O_B = (O_X + NWG * 4 * (CW + 1) * 4 + 15) / 16 * 16;
-    static constexpr int kBars = 2 * 8 + 2 * 2 + 1 + 2 + 2 * kMaxStages;
-    static constexpr int O_RING = (O_B + kBars * 8 + 16 + 127) / 128 * 128;
+    static constexpr int kBars = 2 * 8 + 2 * 2 + 1 + 2 + 2 * kMaxStages + 2;
+    static constexpr int O_RING = (O_B + kBars * 8 + 32 + 127) / 128 * 128;
     static constexpr int kRing = kSmemMax - 1024 - O_RING;  // (1024: alignment)
 };
 
@@ -608,12 +608,14 @@ __device__ __forceinline__ void keys_loop(RingPos &q, int n_tiles, const RingGeo
         const int b = q.j & 1;
         const bool here = bar_test(bar.r_full + 8 * q.st, q.par), free = bar_test(bar.empty + 8 * b, ((q.j >> 1) & 1) ^ 1);
         wait.unless(here, bar.r_full + 8 * q.st, q.par);
+        if (wait.gone) return;
         if (((reinterpret_cast<const TileDesc *>(descs)[q.j % kSlots].flags >> 8) & 15) != KB) return;
         uint32_t w[D / 32 * KB];
         load_record<D / 32 * KB>(ring_base + q.st * ring.stage, token, w);
         __syncwarp();
         if (lane == 0) bar_arrive(bar.r_empty + 8 * q.st);
         wait.unless(free, bar.empty + 8 * b, ((q.j >> 1) & 1) ^ 1);
+        if (wait.gone) return;
         tc_after();
         // (a loop that shifts the record down: a quarter of the code, which the instruction caches feel)
 #pragma unroll 1
@@ -645,6 +647,7 @@ __device__ __forceinline__ void values_loop(RingPos &q, int n_tiles, const RingG
         const unsigned par = ((q.j >> 1) & 1) ^ 1;
         const bool here = bar_test(bar.r_full + 8 * q.st, q.par), free = bar_test(bar.empty, par);
         wait.unless(here, bar.r_full + 8 * q.st, q.par);
+        if (wait.gone) return;
         const int flags = reinterpret_cast<const TileDesc *>(descs)[q.j % kSlots].flags;
         if (flags >> 16 != width) return;
         uint32_t w[D / 32 * VB];
@@ -652,6 +655,7 @@ __device__ __forceinline__ void values_loop(RingPos &q, int n_tiles, const RingG
         __syncwarp();
         if (lane == 0) bar_arrive(bar.r_empty + 8 * q.st);
         wait.unless(free, bar.empty, par);
+        if (wait.gone) return;
 #pragma unroll 1
         for (int g = 0; g < D / 32; g++) {  // 32 dims: four chunks of the line
             uint8_t *line = dst + (g >> 1) * 16384;
@@ -716,6 +720,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
     auto drain = [&](int i) { return bars + 8u * (21 + i); };
     auto r_full = [&](int i) { return bars + 8u * (23 + i); };
     auto r_empty = [&](int i) { return bars + 8u * (23 + kMaxStages + i); };
+    auto t_sync = [&](int i) { return bars + 8u * (23 + 2 * kMaxStages + i); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + C::O_B + C::kBars * 8);
 
     asm volatile("griddepcontrol.launch_dependents;");  // (the merge waits for this grid's end)
@@ -739,6 +744,8 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             bar_init(q_full(i), 1);
             bar_init(q_empty(i), 1);
         }
+        for (int i = 0; i < 2; i++) bar_init(t_sync(i), 4);
+        for (int i = 0; i < 4; i++) tmem_slot[1 + i] = 0;  // a softmax group that gave up
         bar_init(p_full, 4 * C::NWG);
         bar_init(p_empty, 1);
         bar_init(o_free, 4 * C::NWG);
@@ -793,8 +800,8 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 const uint8_t *image = p.images + (static_cast<size_t>(group_of(p, w.x)) * p.n_var + p.var[w.seg][w.x.h]) *
                                                       tree_image_stride<D, R>();
                 wait(q_empty(ev & 1), ((ev >> 1) & 1) ^ 1);
-                __syncwarp();
-                if (lane == 0 && !wait.gone) {
+                if (wait.gone) break;
+                if (lane == 0) {
                     issued = ev;
                     bar_expect_tx(q_full(ev & 1), C::QIMG);
                     bulk_load(sb + C::O_Q + (ev & 1) * C::QBUF, image, C::QIMG, q_full(ev & 1));
@@ -814,7 +821,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             if (j + 1 < n_tiles) walk_next(p, w);
             if (j + 1 == n_tiles || w.first) d.flags |= kLast;
             wait(r_empty(st), ((j / ring.stages) & 1) ^ 1);
-            __syncwarp();
+            if (wait.gone) break;
             if (kv == 0 && lane == 0) {
                 TileDesc *to = reinterpret_cast<TileDesc *>(sm + C::O_D) + j % kSlots;
                 to->flags = d.flags, to->left = d.left, to->part = d.part, to->inv = d.inv;
@@ -847,6 +854,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             const int b = j & 1;
             const unsigned par = (j >> 1) & 1;
             wait.both(k_full(b), par, s_empty(b), par ^ 1);
+            if (wait.gone) break;
             const int flags = reinterpret_cast<const TileDesc *>(sm + C::O_D)[j % kSlots].flags;
             if (flags & kFresh) {
                 // the products with the old queries are behind this point; the new ones' image
@@ -854,7 +862,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 __syncwarp();
                 ev++;
                 wait(q_full(ev & 1), (ev >> 1) & 1);
-                __syncwarp();
+                if (wait.gone) break;
             }
             tc_after();
             const uint64_t q = desc_k(sb + C::O_Q + (ev & 1) * C::QBUF);
@@ -887,10 +895,11 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
         for (int j = 0; j < n_tiles; j++) {
             const int b = j & 1;
             wait.both(v_full(b), (j >> 1) & 1, p_full, j & 1);
+            if (wait.gone) break;
             const bool first = reinterpret_cast<const TileDesc *>(sm + C::O_D)[j % kSlots].flags & kFirst;
             if (first) {
                 if (parts > 0) wait(o_free, (parts - 1) & 1);
-                __syncwarp();
+                if (wait.gone) break;
                 parts++;
             }
             tc_after();
@@ -917,16 +926,25 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
         uint8_t *dst = sm + C::O_V + vg * C::VBUF;
         RingPos q{0, 0, 0};
         if (vg) q.next(ring.stages);
+        unsigned met = 0;  // (bounded, as a group's warps may give up one by one)
+        auto meet = [&]() {
+            __syncwarp();
+            if (lane == 0) bar_arrive(t_sync(vg));
+            wait(t_sync(vg), met);
+            met ^= 1;
+        };
         while (q.j < n_tiles) {
             wait(r_full(q.st), q.par);
-            __syncwarp();
+            if (wait.gone) break;
             const TileDesc &d = reinterpret_cast<const TileDesc *>(descs)[q.j % kSlots];
             const int width = d.flags >> 16, vb = width & 15;
             if (vb) {
-                const uint16_t *half = lv.half[width >> 4] + cb_off(vb);
-                named_sync(5 + vg, 128);  // the other warps have done with the old table
+                const uint16_t *half = param_table(lv.half[width >> 4] + cb_off(vb));
+                meet();  // the other warps have done with the old table
+                if (wait.gone) break;
                 fill_levels(sm + C::O_T + vg * kTableBytes, half, vb, tid);
-                named_sync(5 + vg, 128);
+                meet();
+                if (wait.gone) break;
             }
             switch (vb) {
                 case 0: {
@@ -937,6 +955,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0) bar_arrive(r_empty(q.st));
                     wait(v_empty(vg), ((q.j >> 1) & 1) ^ 1);
+                    if (wait.gone) break;
                     // 16-byte chunks, consecutive threads on consecutive ones; rows behind the tokens are zeros
 #pragma unroll 4
                     for (int c = tid; c < kTreeTile * D / 8; c += 128) {
@@ -961,6 +980,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 case 7: values_loop<7, D>(q, n_tiles, ring, base, descs, bar, table, dst, tid, width, wait); break;
                 default: values_loop<8, D>(q, n_tiles, ring, base, descs, bar, table, dst, tid, width, wait); break;
             }
+            if (wait.gone) break;
         }
     } else if (warp >= kKeyWarp) {
         // ------------------------------------------------------ keys into TMEM
@@ -976,7 +996,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
         RingPos q{0, 0, 0};
         while (q.j < n_tiles) {
             wait(r_full(q.st), q.par);
-            __syncwarp();
+            if (wait.gone) break;
             const TileDesc &d = reinterpret_cast<const TileDesc *>(descs)[q.j % kSlots];
             switch ((d.flags >> 8) & 15) {
                 case 0: {
@@ -988,7 +1008,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0) bar_arrive(r_empty(q.st));
                     wait(k_empty(b), ((q.j >> 1) & 1) ^ 1);
-                    __syncwarp();
+                    if (wait.gone) break;
                     tc_after();
 #pragma unroll
                     for (int i = 0; i < D / 32; i++) {
@@ -1017,6 +1037,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 case 7: keys_loop<7, D>(q, n_tiles, ring, base, descs, bar, dst, tid, wait); break;
                 default: keys_loop<8, D>(q, n_tiles, ring, base, descs, bar, dst, tid, wait); break;
             }
+            if (wait.gone) break;
         }
     } else {
         // ------------------------------------------------------ softmax
@@ -1033,7 +1054,10 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
         for (int c = 0; c < CW; c++) l[c] = 0.f;
         if (tok < CW) m_row[R + tok] = 0.f;
         named_sync(1 + wg, 128);
-        bool ready = false;
+        bool ready = false, lost = false;
+        // a group leaves together: a warp that gave up asks for a raise (every warp votes
+        // on one per tile, whatever it read), where all four learn of it
+        volatile uint32_t *left = tmem_slot + 1 + wg;
 #pragma unroll 1
         for (int j = 0; j < n_tiles; j++) {
             const int b = j & 1;
@@ -1053,7 +1077,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 sig = sc[128] * __int_as_float(d.w);
             }
             if (!valid) ks = sig = 0.f;
-            bool raise = d.x & kFirst;
+            bool raise = (d.x & kFirst) || wait.gone;
             tmem_wait<CW>(u);
 #pragma unroll 1
             for (int pass = 0;; pass++) {
@@ -1082,7 +1106,10 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 asm("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(big));
                 if (lane < CW) maxima[qw * (CW + 1) + lane] = mine;
                 if (lane == 0) maxima[qw * (CW + 1) + CW] = big;
+                if (lane == 0 && wait.gone) *left = 1;
                 named_sync(1 + wg, 128);
+                lost = *left != 0;
+                if (lost) break;
                 const bool first = d.x & kFirst;
                 big = fmaxf(fmaxf(maxima[CW], maxima[2 * CW + 1]), fmaxf(maxima[3 * CW + 2], maxima[4 * CW + 3]));
                 // E: the largest sigma times 2^-E in [0.5, 1)
@@ -1104,7 +1131,6 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 if (!first) {
                     // earlier weights to the new max: the sums here, the accumulator in TMEM
                     wait(p_empty, (j - 1) & 1);
-                    __syncwarp();
                     tc_after();
                     const float down = pow2(-min(now - E, 126));
 #pragma unroll
@@ -1126,9 +1152,10 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 down_e = pow2(-E);
                 tmem_ld<CW>(s_addr0 + b * R, u);
             }
+            if (lost) break;
             tc_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(s_empty(b));
+            if (lane == 0 && !wait.gone) bar_arrive(s_empty(b));
             const bool p_free = bar_test(p_empty, (j & 1) ^ 1);  // the products with the last P done?
             const float sv = sig * down_e;
             if (__any_sync(0xffffffffu, !valid)) {  // behind the last token: weight zero, whatever lies there
@@ -1152,7 +1179,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             fence_async();
             tc_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(p_full);
+            if (lane == 0 && !wait.gone) bar_arrive(p_full);
             ready = j + 1 < n_tiles && bar_test(s_full(b ^ 1), ((j + 1) >> 1) & 1);
             if (d.x & kLast) {  // the part's record
                 float *rec = p.part + (static_cast<size_t>(worker) + d.z) * R * (D + 4);
@@ -1173,7 +1200,6 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                     m_row[R + tok] = 0.f;
                 }
                 wait(p_empty, j & 1);
-                __syncwarp();
                 tc_after();
                 const float up = pow2(E);
 #pragma unroll
@@ -1186,7 +1212,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 }
                 tc_before();
                 named_sync(1 + wg, 128);  // (also: `maxima` is free again, -m is 0 for all)
-                if (lane == 0) bar_arrive(o_free);
+                if (lane == 0 && !wait.gone) bar_arrive(o_free);
             }
         }
     }
