@@ -15,7 +15,9 @@ runs through tq_decode_attention.  The segment plans follow the pages:
 decode steps against it); `ChunkedDecodeCache` builds workload 2 (sinks, a
 packed prompt, and an fp16 buffer of decode tokens that is compressed every
 64 steps).  Both expose `views` (ctypes layer views), `decode(q)` and the
-algorithmic bytes a decode step reads.
+algorithmic bytes a decode step reads.  `SpeculativeCache` serves a batch whose
+sequences differ in length: prompts are written from the unrotated keys, trees of
+drafted tokens attend to it, and what the verification accepts is written into it.
 """
 from __future__ import annotations
 
@@ -276,6 +278,81 @@ class ChunkedDecodeCache:
                 SegInfo(self.packed[l], self.sinks, self.n_prompt_packed + w0, [self.w.kbits] * H,
                         [self.w.vbits] * H, [0] * H),
                 SegInfo(None, self.T + w0, s - w0 + 1, [16] * H, [16] * H, [0] * H)]
+
+
+class SpeculativeCache:
+    """A batch of sequences, each at its own length, advanced by verified drafts.
+
+    Per layer: fp16 sinks (the first positions) and one packed segment.  A step is,
+    for each layer, `attend` (rotary positions of the drafted queries and keys in
+    place, then attention of the draft tree over the cache and the drafts) and
+    `commit` (the accepted drafts' rows into the cache), and after the last layer
+    `advance`.  The lengths stay on the device and no call waits for it, so that a
+    whole step can be captured into a CUDA graph."""
+
+    def __init__(self, layers: int, batch: int, kv_heads: int, q_heads: int, head_dim: int, capacity: int, rope: T.Rope,
+                 kbits=3, vbits=3, sinks: int = 128, drafts: int = 16, seed: int = 42, device="cuda"):
+        if sinks % 16 or capacity % 16 or capacity < 16:
+            raise ValueError("sinks and capacity are multiples of 16")
+        self.layers, self.B, self.H, self.Hq, self.d = layers, batch, kv_heads, q_heads, head_dim
+        self.rope, self.sinks, self.capacity, self.drafts = rope, sinks, capacity, drafts
+        widths = lambda b: [b] * kv_heads if isinstance(b, int) else list(b)
+        self.rot, self.head, self.body, self.views = [], [], [], []
+        for l in range(layers):
+            self.rot.append(T.tq_make_rotation(head_dim, seed + l))
+            layout = T.make_layout(batch, kv_heads, head_dim, capacity, widths(kbits), widths(vbits))
+            self.body.append(T.PackedSegment(layout, device, n_tokens=capacity))
+            self.head.append(T.Fp16Segment(batch, kv_heads, head_dim, sinks, device, n_tokens=sinks) if sinks else None)
+            self.views.append(T.layer_view(self.rot[l], ([self.head[l]] if sinks else []) + [self.body[l]]))
+        i32 = dict(dtype=torch.int32, device=device)
+        self.length = torch.zeros(batch, **i32)       # tokens of a sequence
+        self.head_len = torch.zeros(batch, **i32)     # of them in the sinks
+        self.body_len = torch.zeros(batch, **i32)     # and in the packed segment
+        self.body_at = torch.full((batch,), -sinks, **i32)  # place of the next token in the packed segment
+        self.zero = torch.zeros(batch, **i32)
+        self.workspace = torch.empty(T.tq_tree_workspace_size(self.views[0], batch, kv_heads, q_heads, drafts, head_dim),
+                                     dtype=torch.uint8, device=device)
+
+    def _write(self, l, K, V, at, body_at, n, index=None, rope=None, positions=None, stream=None):
+        kw = dict(n_new=n, index=index, rope=rope, positions=positions, stream=stream)
+        if self.sinks:  # rows past the sinks are skipped here, rows among them there
+            T.tq_append(self.head[l], None, K, V, at, **kw)
+        T.tq_append(self.body[l], self.rot[l], K, V, body_at, **kw)
+
+    def prefill(self, l, K, V, n, positions, stream=None):
+        """Prompts of n[b] tokens into the empty cache of layer l: K, V fp16 [B][H][S][d],
+        the keys without their positions (int32 [S] or [B][S])."""
+        self._write(l, K, V, self.zero, self.zero - self.sinks, n, rope=self.rope, positions=positions, stream=stream)
+
+    def attend(self, l, q, k, v, positions, out, mask=None, stream=None):
+        """Layer l's attention of N <= drafts drafted tokens per sequence: q fp16
+        [B][N][Hq][d] and k [B][H][N][d] are rotated in place by positions (int32
+        [B][N]); mask as tq_tree_attention takes it."""
+        T.tq_rope(self.rope, positions, [q.transpose(1, 2), k], stream=stream)
+        lens = ([self.head_len] if self.sinks else []) + [self.body_len]
+        T.tq_tree_attention(self.views[l], q, k, v, out, self.workspace, mask=mask, seg_len=lens, stream=stream)
+
+    def commit(self, l, k, v, index, n, stream=None):
+        """The n[b] accepted drafts index[b][:] (int32 [B][N]; a path of the tree from its
+        root) behind layer l's tokens: k, v as `attend` left them."""
+        self._write(l, k, v, self.length, self.body_at, n, index=index, stream=stream)
+
+    def advance(self, n):
+        """The lengths after a step or a prefill of n[b] tokens (int32 [B]), on the current stream."""
+        self.length.add_(n).clamp_(max=self.sinks + self.capacity)
+        torch.clamp(self.length, max=self.sinks, out=self.head_len)
+        torch.sub(self.length, self.sinks, out=self.body_at)
+        torch.clamp(self.body_at, min=0, out=self.body_len)
+
+    def read(self, l, first, n_max, dtype=torch.float16, stream=None):
+        """Rows first[b] .. first[b] + n_max - 1 of layer l as vectors ([k, v], each
+        [B][H][n_max][d]; zeros behind a sequence's last token)."""
+        shape = (self.B, self.H, n_max, self.d)
+        out = [torch.zeros(shape, dtype=dtype, device=self.length.device) for _ in range(2)]
+        if self.sinks:
+            T.tq_read(self.head[l], None, first, n_max, n_read=self.head_len - first, out=out, stream=stream)
+        T.tq_read(self.body[l], self.rot[l], first - self.sinks, n_max, n_read=self.length - first, out=out, stream=stream)
+        return out
 
 
 def record_offsets(seg: T.PackedSegment, which: str, b: int, h: int, t: np.ndarray) -> np.ndarray:
