@@ -16,7 +16,7 @@
 // level adds a constant per row, which one more 16-deep step (constant columns in TMEM)
 // brings into the sum, so that x = m_t A U with one A for the block.
 // q enters as fp16 hi + lo (22 bits; the lo products run over the same TMEM
-// operand), P as fp16 p sigma, value levels as fp16(s c_k) with s chosen on the
+// operand), P as fp16 p sigma (hi + lo beside wide values), value levels as fp16(s c_k), s chosen on the
 // host so that the levels round closely; 1/s is part of sigma.
 //
 // The running max is lazy: a row's m moves only when a score exceeds it by 8
@@ -412,8 +412,17 @@ constexpr int kFresh = 4;             // first of its (group, segment)
 constexpr int kFp16 = 8;
 
 // ---------------------------------------------------------------- shared memory
-template <int D, int R>
+// LO: P as fp16 hi + lo, the lo products in columns of their own, for layers that hold
+// values of kWideValues bits or more.  Narrower levels find a scale at which they round
+// closely; from 6 bits on they do not, and the weights' rounding on top made the error 1.51
+// (6 bits) to 1.74 (8 bits) times that of rounding the output alone.  With lo it is 1.15 to
+// 1.45 (5 bits without: 1.48).  16384 tokens of K4V8, without and with: one sequence, 64
+// rows a head 42 / 49 us; two sequences, 256 rows 122 / 199 us (there the blocks
+// have 32 rows instead of 64, whose P lines have no place for lo).
+constexpr int kWideValues = 6;
+template <int D, int R, bool LO = false>
 struct Mma {
+    static constexpr int PC = LO ? 2 * R : R;       // columns of the P operand and of the sums: hi, lo
     static constexpr int NWG = R == 16 ? 2 : 4;     // softmax groups of four warps
     static constexpr int CW = R / NWG;              // rows per group
     static constexpr int kKeyWarp = 4 * NWG, kValueWarp = kKeyWarp + 4, kIssueWarp = kValueWarp + 8,
@@ -424,9 +433,10 @@ struct Mma {
     static constexpr int QIMG = 2 * QPART + R * 32;  // hi, lo, and the 16-deep step that adds the rows' constants
     static constexpr int QBUF = (QIMG + 1023) / 1024 * 1024;
     static constexpr int VBUF = HALVES * 128 * 128;
+    static_assert(PC <= 64, "P's line");
     static constexpr int PBUF = 128 * 128;
     static constexpr int KCOLS = D / 2;             // TMEM columns of a K tile
-    static constexpr int T_K = 0, T_S = 2 * KCOLS, T_O = T_S + 2 * R, T_C = T_O + R;  // (T_C: 8 constant columns)
+    static constexpr int T_K = 0, T_S = 2 * KCOLS, T_O = T_S + 2 * R, T_C = T_O + PC;  // (T_C: 8 constant columns)
     static constexpr int TCOLS = 512;               // all of TMEM, so that its base is column 0
     static constexpr int O_Q = 0;
     static constexpr int O_V = (O_Q + 2 * QBUF + 1023) / 1024 * 1024;
@@ -696,10 +706,10 @@ __device__ __forceinline__ void cp16(unsigned dst, const void *src) {
 }
 
 // ---------------------------------------------------------------- kernel
-template <int D, int R>
+template <int D, int R, bool LO>
 __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
     tree_mma_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ TreeLevels lv, const RingGeo ring) {
-    using C = Mma<D, R>;
+    using C = Mma<D, R, LO>;
     constexpr int CW = C::CW, kKeyWarp = C::kKeyWarp, kValueWarp = C::kValueWarp, kIssueWarp = C::kIssueWarp,
                   kLoadWarp = C::kLoadWarp;
     extern __shared__ uint8_t smem_raw[];
@@ -889,7 +899,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             if (bar_try(drain(0), 0)) break;
     } else if (warp == kIssueWarp + 1) {
         // ------------------------------------------------------ O^T += V^T P^T
-        constexpr uint32_t id_o = idesc(R, true);
+        constexpr uint32_t id_o = idesc(C::PC, true);
         int parts = 0;
 #pragma unroll 1
         for (int j = 0; j < n_tiles; j++) {
@@ -1135,16 +1145,19 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                     const float down = pow2(-min(now - E, 126));
 #pragma unroll
                     for (int c = 0; c < CW; c += 8) {
-                        float o[8];
-                        uint32_t r[8];
-                        tmem_ld<8>(o_addr + c, o);
 #pragma unroll
-                        for (int i = 0; i < 8; i++) {
-                            const float f = m_row[2 * R + c + i];
-                            l[c + i] *= f;
-                            r[i] = __float_as_uint(o[i] * (f * down));
+                        for (int x = 0; x < C::PC; x += R) {
+                            float o[8];
+                            uint32_t r[8];
+                            tmem_ld<8>(o_addr + x + c, o);
+#pragma unroll
+                            for (int i = 0; i < 8; i++) {
+                                const float f = m_row[2 * R + c + i];
+                                if (x == 0) l[c + i] *= f;
+                                r[i] = __float_as_uint(o[i] * (f * down));
+                            }
+                            tmem_st8(o_addr + x + c, r);
                         }
-                        tmem_st8(o_addr + c, r);
                     }
                     tmem_wait_st();
                 }
@@ -1162,20 +1175,32 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < CW; c++) u[c] = valid ? u[c] : -kInf;
             }
-            uint32_t h[CW / 2];
+            uint32_t h[CW / 2], lo[CW / 2];
 #pragma unroll
             for (int c = 0; c < CW; c += 2) {
                 const float p0 = ex2(u[c]), p1 = ex2(u[c + 1]);
                 l[c] += p0;
                 l[c + 1] += p1;
-                const __half2 q = __floats2half2_rn(p0 * sv, p1 * sv);
+                const float w0 = p0 * sv, w1 = p1 * sv;
+                const __half2 q = __floats2half2_rn(w0, w1);
                 h[c / 2] = *reinterpret_cast<const uint32_t *>(&q);
+                if constexpr (LO) {
+                    const float2 f = __half22float2(q);
+                    const __half2 r = __floats2half2_rn(w0 - f.x, w1 - f.y);
+                    lo[c / 2] = *reinterpret_cast<const uint32_t *>(&r);
+                }
             }
             wait.unless(p_free, p_empty, (j & 1) ^ 1);
 #pragma unroll
             for (int c = 0; c < CW; c += 8)
                 *reinterpret_cast<uint4 *>(prow + ((((wg * CW + c) >> 3) ^ (tok & 7)) << 4)) =
                     make_uint4(h[c / 2], h[c / 2 + 1], h[c / 2 + 2], h[c / 2 + 3]);
+            if constexpr (LO) {
+#pragma unroll
+                for (int c = 0; c < CW; c += 8)
+                    *reinterpret_cast<uint4 *>(prow + ((((R + wg * CW + c) >> 3) ^ (tok & 7)) << 4)) =
+                        make_uint4(lo[c / 2], lo[c / 2 + 1], lo[c / 2 + 2], lo[c / 2 + 3]);
+            }
             fence_async();
             tc_before();
             __syncwarp();
@@ -1206,6 +1231,12 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 for (int c = 0; c < CW; c += 8) {
                     float o[8];
                     tmem_ld<8>(o_addr + c, o);
+                    if constexpr (LO) {
+                        float y[8];
+                        tmem_ld<8>(o_addr + R + c, y);
+#pragma unroll
+                        for (int i = 0; i < 8; i++) o[i] += y[i];
+                    }
                     if (tok < D)
 #pragma unroll
                         for (int i = 0; i < 8; i++) rec[(wg * CW + c + i) * (D + 4) + 4 + tok] = o[i] * up;
@@ -1256,18 +1287,23 @@ void fit_levels(HostLevels &h, const float *c, int bits) {
     h.inv = 1.f / s_best;
 }
 
-template <int D, int R>
+template <int D, int R, bool LO>
 cudaError_t tree_mma(const TreeParams &p, const TreeLevels &lv, cudaStream_t s) {
-    using C = Mma<D, R>;
+    using C = Mma<D, R, LO>;
     static_assert(C::T_C + 8 <= 512, "TMEM columns");
+    static_assert(R == 64 || C::kRing >= 2 * 128 * (D / 8) * 16, "two tiles of the widest records");
     int stage = 0;
     for (int i = 0; i < p.n_packed; i++)
         for (int h = 0; h < p.H; h++) stage = std::max(stage, 128 * (D / 8) * (p.seg[i].seg.kbits[h] + p.seg[i].seg.vbits[h]));
     RingGeo ring;
     ring.stage = std::max(stage, 128);
     ring.stages = std::min(kMaxStages, C::kRing / ring.stage);
-    if (ring.stages < 1) return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaFuncSetAttribute(tree_mma_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    // Two at least: the groups of value warps take alternate tiles, and a wait for a stage's
+    // fill is by parity, right for the fill behind the last one that the waiter knows of.
+    // (A group that has seen tile j filled knows that tile j - 1 was: fills end in order.  So
+    // the fill before its next tile's is known, unless one stage holds both.)
+    if (ring.stages < 2) return cudaErrorInvalidConfiguration;
+    cudaError_t e = cudaFuncSetAttribute(tree_mma_kernel<D, R, LO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return e;
     const int images = p.B * p.H * p.n_rb * p.n_var;
     TreeQueryParams qp;
@@ -1290,31 +1326,44 @@ cudaError_t tree_mma(const TreeParams &p, const TreeLevels &lv, cudaStream_t s) 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_mma_kernel<D, R>, p, lv, ring);
+    return cudaLaunchKernelEx(&cfg, tree_mma_kernel<D, R, LO>, p, lv, ring);
+}
+
+// LO with up to 32 rows a block: P's hi and lo then share the lines that 64 rows fill.
+template <int D, bool LO>
+cudaError_t tree_rows(const TreeParams &p, const TreeLevels &lv, cudaStream_t s) {
+    if (p.R == 16) return tree_mma<D, 16, LO>(p, lv, s);
+    if (p.R == 32) return tree_mma<D, 32, LO>(p, lv, s);
+    if constexpr (!LO) return tree_mma<D, 64, false>(p, lv, s);
+    return cudaErrorInvalidConfiguration;
 }
 
 }  // namespace
 
+// The least power of two that holds the rows, up to 64 columns; 32 where P takes hi and
+// lo, or where two tiles of records would not fit beside 64 rows.
+int tree_mma_rows(int rows, int d, int record_bits, int value_bits) {
+    const int ring = d == 128 ? Mma<128, 64>::kRing : Mma<64, 64>::kRing;
+    const bool narrow = value_bits >= kWideValues || 2 * 128 * (d / 8) * record_bits > ring;
+    return rows <= 16 ? 16 : rows <= 32 || narrow ? 32 : 64;
+}
+
 cudaError_t launch_tree_mma(const TreeParams &p, cudaStream_t s) {
     TreeLevels lv;
+    bool wide = false;
     std::memset(&lv, 0, sizeof(lv));
     for (int i = 0; i < p.n_packed; i++)
         for (int h = 0; h < p.H; h++) {
             const int vb = p.seg[i].seg.vbits[h], law = p.seg[i].law;
+            wide |= vb >= kWideValues;
             if (lv.inv[law][vb] != 0.f) continue;
             HostLevels &hl = g_levels[law][vb];
             std::call_once(hl.once, [&] { fit_levels(hl, p.centroid[law] + cb_off(vb), vb); });
             std::memcpy(lv.half[law] + cb_off(vb), hl.half, sizeof(uint16_t) << vb);
             lv.inv[law][vb] = hl.inv;
         }
-    if (p.d == 128) {
-        if (p.R == 16) return tree_mma<128, 16>(p, lv, s);
-        if (p.R == 32) return tree_mma<128, 32>(p, lv, s);
-        return tree_mma<128, 64>(p, lv, s);
-    }
-    if (p.R == 16) return tree_mma<64, 16>(p, lv, s);
-    if (p.R == 32) return tree_mma<64, 32>(p, lv, s);
-    return tree_mma<64, 64>(p, lv, s);
+    if (p.d == 128) return wide ? tree_rows<128, true>(p, lv, s) : tree_rows<128, false>(p, lv, s);
+    return wide ? tree_rows<64, true>(p, lv, s) : tree_rows<64, false>(p, lv, s);
 }
 
 }  // namespace tqk

@@ -296,6 +296,23 @@ def test_tree_wait_that_runs_out(tq, d, polls):
     assert torch.equal(bits(again), bits(want))
 
 
+@pytest.mark.parametrize("d,N,gqa,kb,vb", [
+    (128, 16, 4, 8, 8), (128, 16, 4, 8, 5), (128, 16, 4, 7, 5), (128, 16, 4, 4, 4), (128, 16, 4, 2, 6), (128, 5, 4, 5, 7),
+    (128, 4, 4, 8, 6), (64, 16, 4, 8, 8), (64, 8, 4, 6, 5), (64, 3, 2, 3, 7)])
+def test_tree_over_many_tiles(tq, d, N, gqa, kb, vb):
+    """Several tiles a worker, with every depth of the record ring and both forms of the weights."""
+    B, H, n = 2, 8, 5000
+    q, k, v, parts, lens, rng = base.tree_case(tq, d, H, gqa, B, N, [((kb, vb), n), ("fp16", 128)], False, seed=kb + 9 * vb)
+    out = base.run_tree(tq, q, k, v, parts)
+    _, R = base.rotation64(tq, d, 21)
+    ref = base.tree_ref(tq, q, k, v, None, clean(parts), [None] * 2, R)
+    base.check_tree(out, ref)
+    if vb >= 6:
+        # the levels' half steps alone (and the result's): sqrt(2 / 3) of a half step, where the
+        # weights' half steps would make it sqrt(3 / 3); a tenth more for the fewer samples
+        assert (out.double() - ref[0]).norm() <= 1.1 * (2 / 3) ** 0.5 * 2.0**-11 * ref[0].norm()
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_tree_of_one_unseen_draft_is_decode(tq, d):
     """A draft that does not see itself attends to the cache alone: what a decode step computes."""
