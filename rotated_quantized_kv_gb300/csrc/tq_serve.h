@@ -170,6 +170,7 @@ struct TreeMergeParams {
     const float *part;
     uint32_t sign_bits[kMaxD / 32];
     float inv_sqrt_d, qk_scale;
+    int vec;                     // wide loads of q, k and v
 };
 
 struct TreeParams {

@@ -180,21 +180,87 @@ __global__ void __launch_bounds__(kTreeThreads) tree_plain_kernel(const __grid_c
 }
 
 // ---------------------------------------------------------------- merge
+// A lane's J consecutive coordinates of a row (D < 32: lanes below D hold one); vec: by one
+// load (J >= 8: of 16 bytes).
+template <int D>
+struct RowOf {
+    static constexpr int J = D >= 32 ? D / 32 : 1;
+};
+template <int D>
+__device__ __forceinline__ void load_row(const uint16_t *row, int lane, bool vec, uint16_t (&x)[RowOf<D>::J]) {
+    constexpr int J = RowOf<D>::J;
+    row += lane * J;
+    if constexpr (J == 1) {
+        x[0] = lane < D ? __ldg(row) : 0;
+    } else if (!vec) {
+#pragma unroll
+        for (int j = 0; j < J; j++) x[j] = __ldg(row + j);
+    } else if constexpr (J == 2) {
+        *reinterpret_cast<uint32_t *>(x) = __ldg(reinterpret_cast<const uint32_t *>(row));
+    } else if constexpr (J == 4) {
+        *reinterpret_cast<uint2 *>(x) = __ldg(reinterpret_cast<const uint2 *>(row));
+    } else {
+#pragma unroll
+        for (int j = 0; j < J; j += 8)
+            *reinterpret_cast<uint4 *>(x + j) = __ldg(reinterpret_cast<const uint4 *>(row + j));
+    }
+}
+template <int D>
+__device__ __forceinline__ void load_sums(const float *row, int lane, bool valid, float (&x)[RowOf<D>::J]) {
+    constexpr int J = RowOf<D>::J;
+    row += lane * J;
+    if constexpr (J == 1) {
+        x[0] = valid && lane < D ? __ldcg(row) : 0.f;
+    } else if constexpr (J == 2) {
+        const float2 v = valid ? __ldcg(reinterpret_cast<const float2 *>(row)) : make_float2(0.f, 0.f);
+        x[0] = v.x, x[1] = v.y;
+    } else {
+#pragma unroll
+        for (int j = 0; j < J; j += 4) {
+            const float4 v = valid ? __ldcg(reinterpret_cast<const float4 *>(row + j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
+        }
+    }
+}
+// R x of a row held like that (any order of the sums: attention arithmetic).
+template <int D>
+__device__ __forceinline__ void rotate_row(float (&x)[RowOf<D>::J], const uint32_t *sb, float c, int lane) {
+    constexpr int J = RowOf<D>::J;
+    const uint32_t neg = lane * J < D ? sb[lane * J >> 5] >> (lane * J & 31) : 0u;
+#pragma unroll
+    for (int j = 0; j < J; j++)
+        if ((neg >> j) & 1u) x[j] = -x[j];
+#pragma unroll
+    for (int h = 1; h < J; h <<= 1)
+#pragma unroll
+        for (int j = 0; j < J; j++)
+            if ((j & h) == 0) {
+                const float u = x[j], v = x[j + h];
+                x[j] = u + v, x[j + h] = u - v;
+            }
+#pragma unroll
+    for (int h = J; h < D; h <<= 1) {
+        const float sg = (lane & (h / J)) ? -1.f : 1.f;
+#pragma unroll
+        for (int j = 0; j < J; j++) x[j] = fmaf(x[j], sg, __shfl_xor_sync(0xffffffffu, x[j], h / J));
+    }
+#pragma unroll
+    for (int j = 0; j < J; j++) x[j] *= ((neg >> j) & 1u) ? -c : c;
+}
+
 // A warp per query row: the drafted tokens that the row sees, in binary32 (few tokens
 // per row, so that neither the mask nor a non-finite value of an unseen draft can
 // reach the row), every record of its group in order, R on the packed share, the
 // quotient, and the fp16 row.  The call's bytes here are few; what counts is the
-// chain of loads, so F drafts' or U records' loads are in flight at a time, and the
+// chain of loads, so F drafts' keys and values or U records are in flight at a time, and the
 // drafts come before the wait for the records (the grid may start while the last
 // CTAs of the main kernel run).
-// U: 16 where the rows are too few to fill the GPU anyway (up to 4096: measured 12.1
-// against 14.3 us at 512 rows of 24 records), else 8, with which twice the warps fit
-// (44 against 59 us at 8192 rows of 3).
+// U: 16 where the rows are too few to fill the GPU anyway (up to 4096), else 8, with
+// which twice the warps fit.
 template <int D, int U>
 __global__ void __launch_bounds__(kTreeThreads) tree_merge_kernel(const __grid_constant__ TreeMergeParams p) {
-    constexpr int J = (D + 31) / 32;
+    constexpr int J = RowOf<D>::J;
     constexpr int F = J <= 8 ? 4 : 32 / J;
-    __shared__ float draft_x[kTreeWarps][TQ_MAX_DRAFTS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = p.t.N * p.t.g;
     const unsigned id = blockIdx.x * kTreeWarps + warp;  // (b, h, row)
@@ -206,75 +272,62 @@ __global__ void __launch_bounds__(kTreeThreads) tree_merge_kernel(const __grid_c
     bool nan = false;  // fmaxf passes over NaN: a row that sees only NaN scores is NaN, not empty
 #pragma unroll
     for (int j = 0; j < J; j++) a[0][j] = a[1][j] = 0.f;
-    // scores of the drafts that the row sees, each over the whole warp
-    float q[J];
+    {
+        float q[J];
+        __align__(16) uint16_t q16[J];
+        load_row<D>(p.q + b * p.qs[0] + draft * p.qs[1] + head * p.qs[2], lane, p.vec, q16);
 #pragma unroll
-    for (int j = 0; j < J; j++) {
-        const int e = lane + 32 * j;
-        q[j] = e < D ? __half2float(__ushort_as_half(__ldg(p.q + b * p.qs[0] + draft * p.qs[1] + head * p.qs[2] + e))) : 0.f;
-    }
-    const uint16_t *K = p.k + b * p.ks[0] + h * p.ks[1], *V = p.v + b * p.vs[0] + h * p.vs[1];
-    int n = 0;
+        for (int j = 0; j < J; j++) q[j] = __half2float(__ushort_as_half(q16[j]));
+        const uint16_t *K = p.k + b * p.ks[0] + h * p.ks[1], *V = p.v + b * p.vs[0] + h * p.vs[1];
 #pragma unroll 1
-    for (int w = 0; w < p.mask_words; w++) {
+        for (int w = 0; w < p.mask_words; w++) {
 #pragma unroll 1
-        for (uint32_t m = seen_word(p, p.t.N, b, draft, w); m;) {
-            const int some = min(__popc(m), F);
-            float s[F];
+            for (uint32_t m = seen_word(p, p.t.N, b, draft, w); m;) {
+                const int some = min(__popc(m), F);
+                __align__(16) uint16_t k16[F][J], v16[F][J];
+                float s[F];
 #pragma unroll
-            for (int i = 0; i < F; i++) {
-                s[i] = 0.f;
-                if (i < some) {
-                    const uint16_t *k = K + (32 * w + __ffs(m) - 1) * p.ks[2];
-                    m &= m - 1;
-#pragma unroll
-                    for (int j = 0; j < J; j++)
-                        if (lane + 32 * j < D) s[i] = fmaf(q[j], __half2float(__ushort_as_half(__ldg(k + lane + 32 * j))), s[i]);
+                for (int i = 0; i < F; i++) {
+                    if (i < some) {
+                        const int t = 32 * w + __ffs(m) - 1;
+                        m &= m - 1;
+                        load_row<D>(K + t * p.ks[2], lane, p.vec, k16[i]);
+                        load_row<D>(V + t * p.vs[2], lane, p.vec, v16[i]);
+                    }
                 }
-            }
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1)
+                for (int i = 0; i < F; i++) {
+                    s[i] = 0.f;
+                    if (i < some)
 #pragma unroll
-                for (int i = 0; i < F; i++) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
-#pragma unroll
-            for (int i = 0; i < F; i++)
-                if (i < some) {
-                    s[i] *= p.qk_scale;
-                    if (lane == 0) draft_x[warp][n + i] = s[i];
-                    M = fmaxf(M, s[i]);
-                    nan |= s[i] != s[i];
+                        for (int j = 0; j < J; j++) s[i] = fmaf(q[j], __half2float(__ushort_as_half(k16[i][j])), s[i]);
                 }
-            n += some;
-        }
-    }
-    __syncwarp();
-    n = 0;
-#pragma unroll 1
-    for (int w = 0; w < p.mask_words && M != -kInf; w++) {
-#pragma unroll 1
-        for (uint32_t m = seen_word(p, p.t.N, b, draft, w); m;) {
-            const int some = min(__popc(m), F);
-            float v[F][J], f[F];
 #pragma unroll
-            for (int i = 0; i < F; i++) {
-                f[i] = 0.f;
+                for (int o = 16; o >= 1; o >>= 1)
 #pragma unroll
-                for (int j = 0; j < J; j++) v[i][j] = 0.f;
-                if (i < some) {
-                    const uint16_t *at = V + (32 * w + __ffs(m) - 1) * p.vs[2];
-                    m &= m - 1;
-                    f[i] = ex2(draft_x[warp][n + i] - M);
+                    for (int i = 0; i < F; i++) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+                float now = M;
 #pragma unroll
-                    for (int j = 0; j < J; j++)
-                        if (lane + 32 * j < D) v[i][j] = __half2float(__ushort_as_half(__ldg(at + lane + 32 * j)));
-                }
-            }
-            n += some;
+                for (int i = 0; i < F; i++)
+                    if (i < some) {
+                        s[i] *= p.qk_scale;
+                        now = fmaxf(now, s[i]);
+                        nan |= s[i] != s[i];
+                    }
+                if (now == -kInf) continue;
+                const float old = M == -kInf ? 0.f : ex2(M - now);
+                M = now;
+                L *= old;
 #pragma unroll
-            for (int i = 0; i < F; i++) {
-                L += f[i];
+                for (int j = 0; j < J; j++) a[1][j] *= old;
 #pragma unroll
-                for (int j = 0; j < J; j++) a[1][j] = fmaf(f[i], v[i][j], a[1][j]);
+                for (int i = 0; i < F; i++)
+                    if (i < some) {
+                        const float f = ex2(s[i] - now);
+                        L += f;
+#pragma unroll
+                        for (int j = 0; j < J; j++) a[1][j] = fmaf(f, __half2float(__ushort_as_half(v16[i][j])), a[1][j]);
+                    }
             }
         }
     }
@@ -329,9 +382,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_merge_kernel(const __grid_c
 #pragma unroll
             for (int u = 0; u < U; u++) {
                 const int s = __shfl_sync(0xffffffffu, slot, u0 + u);
-                const float *at = rows_at + max(s, 0) * stride + 4 + lane;
-#pragma unroll
-                for (int j = 0; j < J; j++) v[u][j] = s >= 0 && lane + 32 * j < D ? __ldcg(at + 32 * j) : 0.f;
+                load_sums<D>(rows_at + max(s, 0) * stride + 4, lane, s >= 0, v[u]);
             }
             if (u0 == 0) {  // (the first loads are on their way) the new largest m
                 float now = fmaxf(M, ml.x);
@@ -360,12 +411,23 @@ __global__ void __launch_bounds__(kTreeThreads) tree_merge_kernel(const __grid_c
         }
     }
     nan = __any_sync(0xffffffffu, nan);
-    warp_rotate_strided<D>(a[0], p.sign_bits, p.inv_sqrt_d, lane);
+    rotate_row<D>(a[0], p.sign_bits, p.inv_sqrt_d, lane);
     const float inv = nan ? __int_as_float(0x7fffffff) : L == 0.f ? 0.f : 1.0f / L;  // nothing seen: zeros
     uint16_t *out = p.out + ((static_cast<size_t>(b) * p.t.N + draft) * p.t.H * p.t.g + head) * D;
+    __align__(16) uint16_t o16[J];
 #pragma unroll
-    for (int j = 0; j < J; j++)
-        if (lane + 32 * j < D) out[lane + 32 * j] = __half_as_ushort(__float2half_rn((a[0][j] + a[1][j]) * inv));
+    for (int j = 0; j < J; j++) o16[j] = __half_as_ushort(__float2half_rn((a[0][j] + a[1][j]) * inv));
+    out += lane * J;
+    if constexpr (J == 1) {
+        if (lane < D) *out = o16[0];
+    } else if constexpr (J == 2) {
+        *reinterpret_cast<uint32_t *>(out) = *reinterpret_cast<const uint32_t *>(o16);
+    } else if constexpr (J == 4) {
+        *reinterpret_cast<uint2 *>(out) = *reinterpret_cast<const uint2 *>(o16);
+    } else {
+#pragma unroll
+        for (int j = 0; j < J; j += 8) *reinterpret_cast<uint4 *>(out + j) = *reinterpret_cast<const uint4 *>(o16 + j);
+    }
 }
 
 template <int D>
@@ -395,6 +457,10 @@ cudaError_t tree_dim(const TreeParams &p, cudaStream_t s) {
     for (int i = 0; i < 3; i++) m.qs[i] = p.qs[i], m.ks[i] = p.ks[i], m.vs[i] = p.vs[i];
     std::copy(p.sign_bits, p.sign_bits + kMaxD / 32, m.sign_bits);
     m.inv_sqrt_d = p.inv_sqrt_d, m.qk_scale = p.qk_scale;
+    const int unit = std::min(8, RowOf<D>::J);  // elements of a lane's load
+    uintptr_t odd = reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v);
+    for (int i = 0; i < 3; i++) odd |= static_cast<uintptr_t>((p.qs[i] | p.ks[i] | p.vs[i]) * 2);
+    m.vec = odd % (2 * unit) == 0;
     const long long rows = static_cast<long long>(p.N) * p.g * p.B * p.H;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((rows + kTreeWarps - 1) / kTreeWarps));
