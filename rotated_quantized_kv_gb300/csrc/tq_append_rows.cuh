@@ -7,10 +7,10 @@
 // fastest, so that a CTA's four warps share the tokens' table rows (and, in a
 // token-major source, their lines).  Keys with rotary positions are rotated in the
 // staged rows first: 16 lanes a row, four pairs a lane, so that the table is read in
-// whole lines, the lines of eight tokens at a time (two at a time: 27 us more on the
+// whole lines, the lines of eight tokens at a time (two at a time: 17 us more on the
 // launch below).  Bound by issue slots and by the latency of few warps (12 an SM, the
-// registers' limit): 4 x 8192 tokens of 8 heads in 4 bits, keys rotated, 123 us for both
-// launches (keys without the rotation: 10 us less), 255 MB moved.
+// registers' limit): 4 x 8192 tokens of 8 heads in 4 bits, keys rotated, 75 us for both
+// launches (64 without the rotation), 172 MB moved.
 #pragma once
 
 #include "tq_compress_rows.cuh"

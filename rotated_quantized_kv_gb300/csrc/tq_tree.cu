@@ -9,7 +9,8 @@
 // This file holds the form for every head dimension and the merge.  A CTA takes an equal
 // range of the tile list (tq_serve.h), stages 8 to 32 tokens at a time as
 // binary32 rows in shared memory and keeps the running max, sum and values of up to
-// 16 query rows.
+// 16 query rows: CUDA cores in binary32, the simplest form, for head dimensions that models
+// rarely have (256: 16 drafts of 4 heads over 4096 tokens of 8 heads 610 us, 2 drafts 169).
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -256,7 +257,7 @@ __device__ __forceinline__ void rotate_row(float (&x)[RowOf<D>::J], const uint32
 // drafts come before the wait for the records (the grid may start while the last
 // CTAs of the main kernel run).
 // U: 16 where the rows are too few to fill the GPU anyway (up to 4096), else 8, with
-// which twice the warps fit.
+// which twice the warps fit.  8192 rows of 3 records: 31 us alone, 512 of 24: 12 us.
 template <int D, int U>
 __global__ void __launch_bounds__(kTreeThreads) tree_merge_kernel(const __grid_constant__ TreeMergeParams p) {
     constexpr int J = RowOf<D>::J;

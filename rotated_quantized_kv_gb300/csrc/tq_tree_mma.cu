@@ -34,6 +34,13 @@
 // take alternate tiles, two that issue the MMAs, two that walk the list and load
 // records and scales (cp.async into a ring); the others learn from a descriptor
 // what a tile is.
+//
+// What bounds it: a tile of 64 rows costs a worker 1.2 us (16 rows: 1.0), where its MMAs
+// take 0.23 us; the 32 warps unpack 128 x 128 codes twice and exponentiate 128 x 64 scores,
+// and the value rows, P and the MMA's operands share shared memory.  The first tile
+// costs about 10 us more (latencies, code that is cold).  Measured, all three kernels: 16 drafts
+// of 4 heads a KV head over 64K tokens of 8 heads K3V3 62 us, 64 drafts over 4 x 32K 282 us,
+// 13 drafts over 16 x 9K at head_dim 64 79 us.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
