@@ -552,11 +552,12 @@ typedef struct {
     int64_t mask_stride_b;     /* words between sequences; 0: one tree for all */
     const int *seg_len[TQ_MAX_SEGMENTS]; /* device int32 [batch] per segment of the view: sequence b holds
                                   min(seg_len[b], n_tokens) of its tokens; NULL: n_tokens */
-    void *out;                 /* device fp16 [batch][N][q_heads][d], 16-byte aligned */
+    void *out;                 /* device fp16 [batch][N][q_heads][d], 16-byte aligned; must not overlap the inputs */
 } tq_tree;
 
 /* Bytes of device workspace tq_tree_attention needs; depends on the segments'
- * kinds and n_tokens (an upper bound of the sequences' lengths) and the counts. */
+ * kinds, widths and n_tokens (an upper bound of the sequences' lengths) and the
+ * counts, and does not shrink with more drafts. */
 tq_status tq_tree_workspace_size(const tq_layer_view *layer, int batch, int n_heads, int q_heads, int head_dim,
                                  int n_drafts, size_t *bytes);
 

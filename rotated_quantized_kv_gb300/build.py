@@ -24,7 +24,8 @@ CUDA_SOURCES = ["tq_compress.cu", "tq_compress_dense.cu", "tq_decode.cu", "tq_ma
                 "tq_generic.cu", "tq_compress_rows.cu", "tq_compress_rows_nh2.cu", "tq_compress_rows_nh4.cu",
                 "tq_compress_rows_np2.cu", "tq_rope.cu", "tq_append.cu", "tq_read.cu", "tq_tree.cu",
                 "tq_tree_mma.cu", "tq_append_rows_keys.cu", "tq_append_rows_values.cu", "tq_read_rows_keys.cu",
-                "tq_read_rows_values.cu"] + [
+                "tq_read_rows_values.cu",
+                "tq_read_rows_keys_d64.cu", "tq_read_rows_values_d64.cu"] + [
                 f"tq_decode_kb{k}.cu" for k in range(1, 9)] + [
                 f"tq_decode_wide_kb{k}.cu" for k in range(1, 9)]
 HOST_SOURCES = ["tq_host.cpp", "tq_serve_host.cpp"]

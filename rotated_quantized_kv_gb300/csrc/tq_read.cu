@@ -1,8 +1,7 @@
 // tq_read.cu -- rows of a segment read back into the caller's type: codes and
 // scales to rotated vectors, then the inverse rotation (R is its own inverse).
 // The binary32 steps are those of tq_dequantize, the result is rounded once.
-// Small calls are bound by latency (64 rows of 8 heads 3.0 us), larger ones of the team kernel
-// by issue slots: 5 x 777 rows of 8 heads of 64 dims into bf16 14.2 us, 19 MB moved.
+// Small calls are bound by latency: 64 rows of 8 heads 3.0 us.
 #include <algorithm>
 #include <cstring>
 
@@ -150,11 +149,12 @@ cudaError_t read_team(const ReadParams &p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// Head_dim 128 and many rows: one thread per vector, a launch per width
-// (tq_read_rows.cuh).  Small reads take the team kernel: one launch, 32 lanes a vector.
-// One sequence of 8 heads, 3-bit codes, team / rows: 64 tokens 3.0 / 7.0 us, 512 (8192
-// vectors) 5.6 / 7.3, 1024 (16384) 9.0 / 7.4, 4096 27.2 / 13.1.
-constexpr long long kRowsVectors = 12288;
+// Head_dim 128 or 64 and many rows: 128 coordinates a thread, a launch per width
+// (tq_read_rows.cuh).  Small reads take the team kernel: one launch, up to 32 lanes a vector.
+// One sequence of 8 heads, 3-bit codes, team / rows: 64 tokens 3.0 / 5.9 us, 512 (8192
+// vectors) 5.5 / 6.1, 1024 8.9 / 6.3, 4096 27.0 / 11.1; head_dim 64, K5V2: 512 tokens 3.7 / 5.4,
+// 1024 5.4 / 5.7, 1536 7.2 / 5.8, 4096 14.9 / 7.0.  Counted in vectors of 128 (two of 64 make one).
+constexpr long long kRowsVectors = 9216;
 
 // Whether every value codebook in use is odd (the Gaussian one is, by construction).
 bool odd_levels(const ReadParams &p) {
@@ -173,8 +173,10 @@ cudaError_t read_rows(const ReadParams &p, int dtype, cudaStream_t s) {
     q.rows = p.rows;
     q.B = p.B, q.H = p.H, q.capacity = p.seg.capacity;
     q.dtype = dtype, q.rotate = p.rotate;
+    auto *keys = p.d == kD ? launch_read_keys : launch_read_keys_d64;
+    auto *values = p.d == kD ? launch_read_values : launch_read_values_d64;
     for (int i = 0; i < kD; i++) {
-        const bool n = (p.sign_bits[i >> 5] >> (i & 31)) & 1u;
+        const bool n = (p.sign_bits[i % p.d >> 5] >> (i & 31)) & 1u;
         q.out_scale[i] = n ? -p.inv_sqrt_d : p.inv_sqrt_d;
     }
     bool beside = false;  // the first launch waits for the stream, the others need not wait for it
@@ -199,8 +201,8 @@ cudaError_t read_rows(const ReadParams &p, int dtype, cudaStream_t s) {
             if (kv) std::memcpy(q.level, p.centroid + cb_off(bits), sizeof(float) << bits);
             std::memset(q.flip, 0, sizeof(q.flip));
             for (int i = 0; i < kD * bits && p.rotate; i++)
-                if ((p.sign_bits[i / bits >> 5] >> (i / bits & 31)) & 1u) q.flip[i >> 5] |= 1u << (i & 31);
-            const cudaError_t e = kv ? launch_read_values(q, bits, beside, s) : launch_read_keys(q, bits, beside, s);
+                if ((p.sign_bits[i / bits % p.d >> 5] >> (i / bits & 31)) & 1u) q.flip[i >> 5] |= 1u << (i & 31);
+            const cudaError_t e = kv ? values(q, bits, beside, s) : keys(q, bits, beside, s);
             if (e != cudaSuccess) return e;
             beside = true;
         }
@@ -237,7 +239,7 @@ cudaError_t launch_read(const ReadParams &params, int dtype, cudaStream_t s) {
     p.vec = ((reinterpret_cast<uintptr_t>(p.K) | reinterpret_cast<uintptr_t>(p.V)) & align) == 0;
     for (int i = 0; i < 3; i++) p.vec &= (!p.K || p.ks[i] % 4 == 0) && (!p.V || p.vs[i] % 4 == 0);
     const long long vec = ((p.K ? 1LL : 0) + (p.V ? 1 : 0)) * p.B * p.H * p.rows.n_max;
-    if (!p.seg.fp16 && p.d == kD && vec >= kRowsVectors && vec < (1LL << 34) && odd_levels(p)) return read_rows(p, dtype, s);
+    if (!p.seg.fp16 && (p.d == kD || p.d == 64) && vec * p.d >= kRowsVectors * kD && vec < (1LL << 34) && odd_levels(p)) return read_rows(p, dtype, s);
     switch (dtype) {
         case TQ_DTYPE_F16: return read_typed<__half>(p, s);
         case TQ_DTYPE_BF16: return read_typed<__nv_bfloat16>(p, s);

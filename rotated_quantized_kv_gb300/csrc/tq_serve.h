@@ -101,7 +101,7 @@ struct ReadParams {
 };
 cudaError_t launch_read(const ReadParams &p, int dtype, cudaStream_t s);
 
-// One thread per vector (head_dim 128), a launch per key and per value width.
+// One thread per vector of head_dim 128 or two of 64, a launch per key and per value width.
 struct ReadRowsParams {
     RowMap rows;
     const uint8_t *codes;
@@ -113,11 +113,13 @@ struct ReadRowsParams {
     int64_t st[3];
     int dtype, vec, rotate;      // vec: 16-byte stores
     uint32_t flip[32];           // record words: ones in the fields of the coordinates to negate
-    float out_scale[kD];
+    float out_scale[kD];         // coordinates m and m + 64 of a thread's 128
     float level[256];            // values: the centroids
 };
 cudaError_t launch_read_keys(const ReadRowsParams &p, int bits, bool beside, cudaStream_t s);
 cudaError_t launch_read_values(const ReadRowsParams &p, int bits, bool beside, cudaStream_t s);
+cudaError_t launch_read_keys_d64(const ReadRowsParams &p, int bits, bool beside, cudaStream_t s);
+cudaError_t launch_read_values_d64(const ReadRowsParams &p, int bits, bool beside, cudaStream_t s);
 
 // ----------------------------------------------------------------- tree attention
 // The work is a list of 128-token tiles.  For sequence b in order, KV head h,

@@ -288,7 +288,8 @@ class SpeculativeCache:
     place, then attention of the draft tree over the cache and the drafts) and
     `commit` (the accepted drafts' rows into the cache), and after the last layer
     `advance`.  The lengths stay on the device and no call waits for it, so that a
-    whole step can be captured into a CUDA graph."""
+    whole step can be captured into a CUDA graph.  Tokens that do not fit any more are
+    dropped: keep sinks + capacity at least at the longest sequence."""
 
     def __init__(self, layers: int, batch: int, kv_heads: int, q_heads: int, head_dim: int, capacity: int, rope: T.Rope,
                  kbits=3, vbits=3, sinks: int = 128, drafts: int = 16, seed: int = 42, device="cuda"):
@@ -339,7 +340,7 @@ class SpeculativeCache:
 
     def advance(self, n):
         """The lengths after a step or a prefill of n[b] tokens (int32 [B]), on the current stream."""
-        self.length.add_(n).clamp_(max=self.sinks + self.capacity)
+        self.length.add_(n).clamp_(0, self.sinks + self.capacity)
         torch.clamp(self.length, max=self.sinks, out=self.head_len)
         torch.sub(self.length, self.sinks, out=self.body_at)
         torch.clamp(self.body_at, min=0, out=self.body_len)

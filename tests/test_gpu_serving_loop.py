@@ -93,10 +93,12 @@ def test_large_append_is_compress(tq, H, kb, vb, B, S, n, gather, layout, r, law
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("B,n,law,token_major,off,rotate", [
-    (1, 900, 0, False, 0, True), (3, 333, 1, True, 0, True), (2, 500, 0, True, 1, True), (2, 450, 0, False, 0, False)])
-def test_large_read_is_dequantize(tq, dtype, B, n, law, token_major, off, rotate):
-    H, d, rng = 8, 128, np.random.RandomState(n)
+@pytest.mark.parametrize("d,B,n,law,token_major,off,rotate", [
+    (128, 1, 900, 0, False, 0, True), (128, 3, 333, 1, True, 0, True), (128, 2, 500, 0, True, 1, True),
+    (128, 2, 450, 0, False, 0, False), (64, 1, 1701, 0, False, 0, True), (64, 3, 555, 0, True, 0, True),
+    (64, 2, 900, 0, True, 1, True), (64, 2, 801, 0, False, 0, False)])
+def test_large_read_is_dequantize(tq, dtype, d, B, n, law, token_major, off, rotate):
+    H, rng = 8, np.random.RandomState(n)
     cap, g = 16 * (n // 16 + 5), gen(n)
     seg = base.random_segment(tq, g, B, H, d, cap, MIXED, MIXED[::-1], law)
     rot = tq.tq_make_rotation(d, 4)
