@@ -210,8 +210,7 @@ cudaError_t append_rows(const AppendParams &p, cudaStream_t s) {
     q.r.nh = q.r.np = 1;
     fill_rows_rotation(q.r, p.sign_bits, kD);
     for (int bits = 1; bits <= 8; bits++)  // before anything is launched
-        for (int h = 0; h < p.H; h++)
-            if (p.seg.vbits[h] == bits && !fill_rows_values(q.r, bits, p.law)) return cudaErrorNotSupported;
+        if (((p.vwidths >> bits) & 1u) && !fill_rows_values(q.r, bits, p.law)) return cudaErrorNotSupported;
     bool beside = false;  // the first launch waits for the stream, the others need not wait for it
     for (int kv = 0; kv < 2; kv++) {
         const int64_t *st = kv ? p.vs : p.ks;

@@ -176,7 +176,7 @@ cudaError_t read_rows(const ReadParams &p, int dtype, cudaStream_t s) {
     auto *keys = p.d == kD ? launch_read_keys : launch_read_keys_d64;
     auto *values = p.d == kD ? launch_read_values : launch_read_values_d64;
     for (int i = 0; i < kD; i++) {
-        const bool n = (p.sign_bits[i % p.d >> 5] >> (i & 31)) & 1u;
+        const bool n = (p.sign_bits[(i & (p.d - 1)) >> 5] >> (i & 31)) & 1u;
         q.out_scale[i] = n ? -p.inv_sqrt_d : p.inv_sqrt_d;
     }
     bool beside = false;  // the first launch waits for the stream, the others need not wait for it
@@ -200,8 +200,12 @@ cudaError_t read_rows(const ReadParams &p, int dtype, cudaStream_t s) {
             if (q.n_heads == 0) continue;
             if (kv) std::memcpy(q.level, p.centroid + cb_off(bits), sizeof(float) << bits);
             std::memset(q.flip, 0, sizeof(q.flip));
-            for (int i = 0; i < kD * bits && p.rotate; i++)
-                if ((p.sign_bits[i / bits % p.d >> 5] >> (i / bits & 31)) & 1u) q.flip[i >> 5] |= 1u << (i & 31);
+            for (int i = 0, bit = 0; i < kD && p.rotate; i++, bit += bits) {
+                if (!((p.sign_bits[(i & (p.d - 1)) >> 5] >> (i & 31)) & 1u)) continue;
+                const uint64_t field = static_cast<uint64_t>((1u << bits) - 1u) << (bit & 31);
+                q.flip[bit >> 5] |= static_cast<uint32_t>(field);
+                if (field >> 32) q.flip[(bit >> 5) + 1] |= static_cast<uint32_t>(field >> 32);
+            }
             const cudaError_t e = kv ? values(q, bits, beside, s) : keys(q, bits, beside, s);
             if (e != cudaSuccess) return e;
             beside = true;
