@@ -124,6 +124,46 @@ def test_large_read_is_dequantize(tq, dtype, d, B, n, law, token_major, off, rot
                 assert (got[:, ~ok] == 7).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_calls_captured(tq, d):
+    """Several launches a call, replayed on other rows and lengths, between other work of the stream."""
+    B, H, S, cap, g = 2, 8, 1200, 1216, gen(d)
+    kb, vb = [3, 4] * 4, [2, 4] * 4
+    rope = tq.Rope(tq.tq_rope_table(tq.tq_make_rope(d), cap))
+    rot = tq.tq_make_rotation(d, 5)
+    src, kv = torch.zeros(2, B, H, S, d, dtype=torch.float16, device=DEV), torch.zeros(2, B, H, S, d, dtype=torch.float16, device=DEV)
+    pos = torch.arange(S, dtype=torch.int32, device=DEV)
+    n, first = torch.zeros(B, dtype=torch.int32, device=DEV), torch.zeros(B, dtype=torch.int32, device=DEV)
+    segs = [base.filled_segment(tq, B, H, d, cap, kb, vb) for _ in range(2)]
+    outs = [[torch.zeros(B, H, S, d, dtype=torch.float16, device=DEV) for _ in range(2)] for _ in range(2)]
+
+    def calls(i):
+        kv.copy_(src)  # a kernel before, which writes what the call reads
+        tq.tq_append(segs[i], rot, kv[0], kv[1], first, n_new=n, rope=rope, positions=pos)
+        tq.tq_read(segs[i], rot, first, S, n_read=n, out=outs[i])
+        kv.zero_()     # and one behind, which overwrites it
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls(0)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            calls(0)
+    torch.cuda.synchronize()
+    for lens, at in (([1200, 1200], [0, 16]), ([700, 1133], [333, 0])):
+        src.copy_(randn(g, *src.shape, dtype=torch.float16))
+        n.copy_(torch.tensor(lens)), first.copy_(torch.tensor(at))
+        torch.cuda.synchronize()
+        graph.replay()
+        calls(1)
+        torch.cuda.synchronize()
+        for name in base.BUFS:
+            assert torch.equal(getattr(segs[0], name).view(torch.uint8), getattr(segs[1], name).view(torch.uint8)), name
+        for x, y in zip(*outs):
+            assert torch.equal(bits(x), bits(y)) and bool((x != 0).any())
+
+
 # ------------------------------------------------------------------ the loop of a server
 @pytest.mark.parametrize("d,kb,vb", [(128, 3, 3), (64, 4, 2), (256, 4, 4)])
 @pytest.mark.parametrize("captured", [False, True])
