@@ -188,7 +188,7 @@ struct TreeParams {
     int64_t mask_stride;
     int mask_words;
     uint16_t *out;
-    float *part;                 // records: [slot][R][d + 4]: m (log2 units), l, pad, pad, sum
+    float *part;                 // records: [slot][R][d + 4]: m (log2 units; any reference, the same for l and sum), l, pad, pad, sum
     // tensor-core form: the query blocks as MMA operands, one image per (b, h, rb) and
     // key width among the head's segments
     uint8_t *images;

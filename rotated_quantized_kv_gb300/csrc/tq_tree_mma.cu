@@ -19,9 +19,13 @@
 // operand), P as fp16 p sigma (hi + lo beside wide values), value levels as fp16(s c_k), s chosen on the
 // host so that the levels round closely; 1/s is part of sigma.
 //
-// The running max is lazy: a row's m moves only when a score exceeds it by 8
-// (log2 units), or a sigma outgrows its common power of two by 2^7, so that
-// most tiles neither reduce over tokens nor touch the accumulator.
+// A row's m is the running max of S + e, 2^e the power of two below the token's sigma (e in
+// [-64, 64]): it bounds the weights p sigma that fp16 has to hold, whatever the values' sizes,
+// and p = 2^(S - m) <= 2^(64 + 8) itself stays in binary32 (weights relative to the largest
+// score alone, times a power of two common to a record's sigmas, lost a row's precision to
+// one large value that it gave no weight: 0.5% at 2^16 times the others, all of it at 2^24).
+// The running max is lazy: m moves only when some S + e exceeds it by 8, so that most
+// tiles neither reduce over tokens nor touch the accumulator.
 //
 // Why K in TMEM and V in shared memory: shared-memory bandwidth (128 B a
 // clock, which the MMA's operand reads share) bounds the tile, and a K tile in
@@ -452,8 +456,8 @@ struct Mma {
     static constexpr int O_S = O_T + 2 * kTableBytes;   // [kSlots][2][128] scales
     static constexpr int O_D = O_S + kSlots * 1024; // [kSlots] descriptors
     static constexpr int O_M = O_D + kSlots * 64;   // [R] m, [R] -m as used, [R] factors
-    static constexpr int O_X = O_M + 3 * R * 4;     // [NWG][4][CW + 1] maxima of the warps
-    static constexpr int O_B = (O_X + NWG * 4 * (CW + 1) * 4 + 15) / 16 * 16;
+    static constexpr int O_X = O_M + 3 * R * 4;     // [NWG][4][CW] maxima of the warps
+    static constexpr int O_B = (O_X + NWG * 4 * CW * 4 + 15) / 16 * 16;
     static constexpr int kBars = 2 * 8 + 2 * 2 + 1 + 2 + 2 * kMaxStages + 2;
     static constexpr int O_RING = (O_B + kBars * 8 + 32 + 127) / 128 * 128;
     static constexpr int kRing = kSmemMax - 1024 - O_RING;  // (1024: alignment)
@@ -1062,11 +1066,10 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
         const unsigned lanes = static_cast<unsigned>(32 * qw) << 16;
         // [CW] m; + R: -m as used (0 while nothing was seen); + 2R: factors
         float *m_row = reinterpret_cast<float *>(sm + C::O_M) + wg * CW;
-        float *maxima = reinterpret_cast<float *>(sm + C::O_X) + wg * 4 * (CW + 1);
+        float *maxima = reinterpret_cast<float *>(sm + C::O_X) + wg * 4 * CW;
         const unsigned s_addr0 = tbase + lanes + C::T_S + wg * CW, o_addr = tbase + lanes + C::T_O + wg * CW;
         uint8_t *prow = sm + C::O_P + tok * 128;
-        int E = 0;
-        float l[CW], A = 1.f, down_e = 1.f;  // down_e: 2^-E
+        float l[CW], A = 1.f;
 #pragma unroll
         for (int c = 0; c < CW; c++) l[c] = 0.f;
         if (tok < CW) m_row[R + tok] = 0.f;
@@ -1088,17 +1091,18 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             // the token's scales (behind the last token: anything)
             const float *sc = reinterpret_cast<const float *>(sm + C::O_S) + (j % kSlots) * 256 + tok;
             const bool valid = tok < d.y;
-            float ks = A, sig = 1.f;  // x = ks U
+            float ks = A, sig = 1.f, e = 0.f;  // x = ks U; 2^e <= sig < 2^(e + 1)
             if (!(d.x & kFp16)) {
                 ks = sc[0] * A;
                 sig = sc[128] * __int_as_float(d.w);
+                e = static_cast<float>(max(-64, min(64, static_cast<int>((__float_as_uint(sig) >> 23) & 0xFFu) - 127)));
             }
             if (!valid) ks = sig = 0.f;
             bool raise = (d.x & kFirst) || wait.gone;
             tmem_wait<CW>(u);
 #pragma unroll 1
             for (int pass = 0;; pass++) {
-                // x - m, and whether some score outgrew its row's m (or a sigma the common power of two)
+                // x - m, and whether some weight outgrew its row's m
                 float top = -kInf;
 #pragma unroll
                 for (int c = 0; c < CW; c += 4) {
@@ -1110,35 +1114,26 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                     top = fmax3(top, u[c], u[c + 1]);
                     top = fmax3(top, u[c + 2], u[c + 3]);
                 }
-                raise |= valid && (top > 8.0f || sig * down_e > 128.0f);
+                raise |= valid && top + e > 8.0f;
                 if (pass || !named_or(1 + wg, 128, raise)) break;
                 float mine = -kInf;
 #pragma unroll
                 for (int c = 0; c < CW; c++) {
-                    float v = valid ? u[c] : -kInf;
+                    float v = valid ? u[c] + e : -kInf;
                     asm("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(v));
                     if (lane == c) mine = v;
                 }
-                float big = valid ? sig : 0.f;
-                asm("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(big));
-                if (lane < CW) maxima[qw * (CW + 1) + lane] = mine;
-                if (lane == 0) maxima[qw * (CW + 1) + CW] = big;
+                if (lane < CW) maxima[qw * CW + lane] = mine;
                 if (lane == 0 && wait.gone) *left = 1;
                 named_sync(1 + wg, 128);
                 lost = *left != 0;
                 if (lost) break;
                 const bool first = d.x & kFirst;
-                big = fmaxf(fmaxf(maxima[CW], maxima[2 * CW + 1]), fmaxf(maxima[3 * CW + 2], maxima[4 * CW + 3]));
-                // E: the largest sigma times 2^-E in [0.5, 1)
-                int e = 0;
-                if (!(d.x & kFp16) && big > 0.f && big < kInf)
-                    e = max(-100, min(100, static_cast<int>((__float_as_uint(big) >> 23) & 0xFFu) - 126));
-                const int now = first ? e : max(E, e);
                 if (tok < CW) {
                     const float old = first ? -kInf : m_row[tok];
                     float m = maxima[tok];
 #pragma unroll
-                    for (int i = 1; i < 4; i++) m = fmaxf(m, maxima[i * (CW + 1) + tok]);
+                    for (int i = 1; i < 4; i++) m = fmaxf(m, maxima[i * CW + tok]);
                     m = fmaxf(old, m - m_row[R + tok]);
                     m_row[tok] = m;
                     m_row[R + tok] = m == -kInf ? 0.f : -m;
@@ -1149,7 +1144,6 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                     // earlier weights to the new max: the sums here, the accumulator in TMEM
                     wait(p_empty, (j - 1) & 1);
                     tc_after();
-                    const float down = pow2(-min(now - E, 126));
 #pragma unroll
                     for (int c = 0; c < CW; c += 8) {
 #pragma unroll
@@ -1161,15 +1155,13 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                             for (int i = 0; i < 8; i++) {
                                 const float f = m_row[2 * R + c + i];
                                 if (x == 0) l[c + i] *= f;
-                                r[i] = __float_as_uint(o[i] * (f * down));
+                                r[i] = __float_as_uint(o[i] * f);
                             }
                             tmem_st8(o_addr + x + c, r);
                         }
                     }
                     tmem_wait_st();
                 }
-                E = now;
-                down_e = pow2(-E);
                 tmem_ld<CW>(s_addr0 + b * R, u);
             }
             if (lost) break;
@@ -1177,7 +1169,6 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             __syncwarp();
             if (lane == 0 && !wait.gone) bar_arrive(s_empty(b));
             const bool p_free = bar_test(p_empty, (j & 1) ^ 1);  // the products with the last P done?
-            const float sv = sig * down_e;
             if (__any_sync(0xffffffffu, !valid)) {  // behind the last token: weight zero, whatever lies there
 #pragma unroll
                 for (int c = 0; c < CW; c++) u[c] = valid ? u[c] : -kInf;
@@ -1188,7 +1179,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 const float p0 = ex2(u[c]), p1 = ex2(u[c + 1]);
                 l[c] += p0;
                 l[c + 1] += p1;
-                const float w0 = p0 * sv, w1 = p1 * sv;
+                const float w0 = p0 * sig, w1 = p1 * sig;
                 const __half2 q = __floats2half2_rn(w0, w1);
                 h[c / 2] = *reinterpret_cast<const uint32_t *>(&q);
                 if constexpr (LO) {
@@ -1221,19 +1212,18 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                     float v = l[c];
 #pragma unroll
                     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                    if (lane == 0) maxima[qw * (CW + 1) + c] = v;
+                    if (lane == 0) maxima[qw * CW + c] = v;
                     l[c] = 0.f;
                 }
                 named_sync(1 + wg, 128);
                 if (tok < CW) {
                     float *row = rec + (wg * CW + tok) * (D + 4);
                     row[0] = m_row[tok];
-                    row[1] = (maxima[tok] + maxima[CW + 1 + tok]) + (maxima[2 * (CW + 1) + tok] + maxima[3 * (CW + 1) + tok]);
+                    row[1] = (maxima[tok] + maxima[CW + tok]) + (maxima[2 * CW + tok] + maxima[3 * CW + tok]);
                     m_row[R + tok] = 0.f;
                 }
                 wait(p_empty, j & 1);
                 tc_after();
-                const float up = pow2(E);
 #pragma unroll
                 for (int c = 0; c < CW; c += 8) {
                     float o[8];
@@ -1246,7 +1236,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                     }
                     if (tok < D)
 #pragma unroll
-                        for (int i = 0; i < 8; i++) rec[(wg * CW + c + i) * (D + 4) + 4 + tok] = o[i] * up;
+                        for (int i = 0; i < 8; i++) rec[(wg * CW + c + i) * (D + 4) + 4 + tok] = o[i];
                 }
                 tc_before();
                 named_sync(1 + wg, 128);  // (also: `maxima` is free again, -m is 0 for all)

@@ -1,0 +1,80 @@
+"""Tree attention where the values of a sequence differ widely in size."""
+import math
+
+import pytest
+import torch
+
+import test_gpu_serving as base
+from test_gpu_serving import DEV, gen, randn
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tq():
+    from rotated_quantized_kv_gb300 import tq as T
+    return T
+
+
+def check(out, ref, largest):
+    """check_tree's bound, the weights' half steps counted in a row's 2-norm: each weight is off by 2^-11 of
+    itself or, below 2^-14 of the row's largest weighted value, by 2^-25 of that (its share: `largest`)."""
+    want, size, reach = ref
+    err = (out.double() - want).norm(dim=-1)
+    tol = 2.0**-11 * want.norm(dim=-1) * 1.01 + (2 * 2.0**-11 + 2 * reach * 2.0**-19) * size + largest + 1e-7
+    assert bool(torch.isfinite(out).all())
+    assert bool((err <= tol).all()), float((err / tol).max())
+    # independent roundings, in squares over the whole output: sqrt(3) half steps, as in check_tree
+    bound = (3 * 2.0**-11 + 2 * reach.max() * 2.0**-19) * want.norm() + largest.norm() / 16
+    assert err.norm() <= bound, float(err.norm() / bound)
+
+
+def one_direction(tq, d, H, gqa, B, N, kb, vb, n, seed):
+    """Queries that are positive multiples of one vector (and a little besides), so that a token whose key points
+    against it gets little weight from every row.  (q, k, v, segment, the tokens' scores for that vector, R)"""
+    g = gen(seed)
+    cap = -(-n // 16) * 16
+    seg = base.random_segment(tq, g, B, H, d, cap, [kb] * H, [vb] * H, n=n)
+    seg.kscale.fill_(1.0)
+    seg.vscale.fill_(1.0)
+    lead = randn(g, 1, 1, 1, d)
+    q = (lead * (1 + 0.2 * torch.rand(B, N, H * gqa, 1, generator=g, device=DEV)) + 0.02 * randn(g, B, N, H * gqa, d)).half()
+    k, v = (randn(g, B, H, N, d, dtype=torch.float16) for _ in range(2))
+    _, R = base.rotation64(tq, d, 21)
+    score = torch.einsum("bhtd,d->bht", base.stored64(tq, seg, R)[0], lead[0, 0, 0].double()) / math.sqrt(d)
+    return q, k, v, seg, score, R
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("N", [3, 14])
+@pytest.mark.parametrize("power", [12, 16, 20, 24, 30])
+@pytest.mark.parametrize("where", ["first", "later", "both"])
+def test_large_value_of_little_weight(tq, d, N, power, where):
+    """A token whose value is 2^power times the others' and whose weight is 2^-(power + 12): it adds 2^-12 of the
+    others' size, and must not cost them their precision."""
+    H, gqa, B, n = 1, 4, 1, 700
+    q, k, v, seg, score, R = one_direction(tq, d, H, gqa, B, N, 4, 4, n, seed=d + N)
+    usual = base.tree_ref(tq, q, k, v, None, [seg], [None], R)[2]  # the scores that have weight
+    for lo, hi in {"first": [(0, 128)], "later": [(256, 384)], "both": [(0, 128), (384, 512)]}[where]:
+        t = lo + int(score[0, 0, lo:hi].argmin())
+        assert score[0, 0, t] < -0.2
+        seg.vscale[t] = 2.0**power
+        seg.kscale[t] = (power + 12) * math.log(2) / -float(score[0, 0, t])
+    out = base.run_tree(tq, q, k, v, [seg])
+    ref = base.tree_ref(tq, q, k, v, None, [seg], [None], R)
+    # the largest weighted value of a row is at most its sum; n tokens of 2^-25 of it (in squares: sqrt(n) of them)
+    check(out, (ref[0], ref[1], usual), (n + N) * 2.0**-25 * ref[1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_of_zero_size_first(tq, d):
+    """Whole tiles of zero values, then values of 2^-6: the scale of the first is not kept for the others."""
+    H, gqa, B, N, n = 1, 4, 1, 5, 700
+    q, k, v, seg, score, R = one_direction(tq, d, H, gqa, B, N, 4, 4, n, seed=d)
+    seg.vscale[:n] = 2.0**-6
+    seg.vscale[:300] = 0.0
+    v.zero_()
+    seg.kscale[300:n] = 12.0  # a few tokens have most of the weight
+    out = base.run_tree(tq, q, k, v, [seg])
+    ref = base.tree_ref(tq, q, k, v, None, [seg], [None], R)
+    check(out, ref, (n + N) * 2.0**-25 * ref[1])
