@@ -403,9 +403,11 @@ __global__ void __launch_bounds__(kTreeThreads) tree_merge_kernel(const __grid_c
                 const float fu = __shfl_sync(0xffffffffu, f, u0 + u);
                 const bool raw = __shfl_sync(0xffffffffu, kind, u0 + u);
                 L = fmaf(__shfl_sync(0xffffffffu, ml.y, u0 + u), fu, L);
+                // (left out, not weighted by zero, of the sum that R spreads: an infinity among unrotated
+                // values stays in its coordinate)
 #pragma unroll
                 for (int j = 0; j < J; j++) {
-                    a[0][j] = fmaf(raw ? 0.f : fu, v[u][j], a[0][j]);
+                    a[0][j] = fmaf(fu, raw ? 0.f : v[u][j], a[0][j]);
                     a[1][j] = fmaf(raw ? fu : 0.f, v[u][j], a[1][j]);
                 }
             }

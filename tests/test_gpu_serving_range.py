@@ -78,3 +78,21 @@ def test_values_of_zero_size_first(tq, d):
     out = base.run_tree(tq, q, k, v, [seg])
     ref = base.tree_ref(tq, q, k, v, None, [seg], [None], R)
     check(out, ref, (n + N) * 2.0**-25 * ref[1])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_non_finite_coordinate_of_a_stored_value(tq, d, bad):
+    """One coordinate of one fp16 row: it reaches that coordinate of the result alone."""
+    H, gqa, B, N, at = 2, 2, 2, 6, 37
+    q, k, v, parts, lens, rng = base.tree_case(tq, d, H, gqa, B, N, [((4, 3), 300), ("fp16", 150)], False, seed=d)
+    parts[0].kscale.nan_to_num_(0.0)
+    parts[0].vscale.nan_to_num_(0.0)
+    want = base.run_tree(tq, q, k, v, parts)
+    parts[1].v[1, :, 70, at] = bad
+    got = base.run_tree(tq, q, k, v, parts)
+    rest = [i for i in range(d) if i != at]
+    assert torch.equal(base.bits(got[0]), base.bits(want[0]))
+    assert torch.equal(base.bits(got[1][..., rest]), base.bits(want[1][..., rest]))
+    hit = got[1][..., at].float()
+    assert bool(torch.isnan(hit).all()) if math.isnan(bad) else bool((hit == bad).all())
