@@ -217,9 +217,8 @@ cudaError_t launch_tree_mma(const TreeParams &p, cudaStream_t s);
 // Bytes of a query image: hi and lo parts (rows of d fp16), 32 bytes a row for the
 // constants' step, and the factor A.
 inline size_t tree_image_bytes(int d, int R) { return (static_cast<size_t>(4) * d * R + 32 * R + 16 + 127) / 128 * 128; }
-// record_bits: the largest sum of a head's key and value widths, value_bits: the largest value width.
-int tree_mma_rows(int rows, int d, int record_bits, int value_bits);
-TreeShape tree_shape(int B, int H, int g, int N, int d, long long tiles_per_head, int record_bits, int value_bits);
+int tree_mma_rows(int rows);
+TreeShape tree_shape(int B, int H, int g, int N, int d, long long tiles_per_head);
 cudaError_t launch_tree(const TreeParams &p, cudaStream_t s);
 
 // ----------------------------------------------------------------- from tq_host.cpp

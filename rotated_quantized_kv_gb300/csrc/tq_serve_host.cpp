@@ -182,15 +182,7 @@ tq_status tree_layout(const tq_layer_view *lv, int B, int H, int Hq, int d, int 
     int64_t tp = 0, tf = 0;
     for (int i = 0; i < lv->n_segments; ++i)
         (lv->seg[i].kind == TQ_SEG_PACKED ? tp : tf) += tiles_of(lv->seg[i].n_tokens);
-    int record_bits = 0, value_bits = 0;
-    for (int i = 0; i < lv->n_segments; ++i) {
-        const tq_segment &sg = lv->seg[i];
-        for (int h = 0; h < H && sg.kind != TQ_SEG_FP16; ++h) {
-            record_bits = std::max(record_bits, sg.layout.kbits[h] + sg.layout.vbits[h]);
-            value_bits = std::max<int>(value_bits, sg.layout.vbits[h]);
-        }
-    }
-    o.shape = tree_shape(B, H, Hq / H, N, d, tp + tf, record_bits, value_bits);
+    o.shape = tree_shape(B, H, Hq / H, N, d, tp + tf);
     const int64_t pp = (tp + kTreePart - 1) / kTreePart, pf = (tf + kTreePart - 1) / kTreePart;
     const int64_t slots = o.shape.workers + static_cast<int64_t>(B) * H * o.shape.n_rb * (pp + pf);
     if (slots > 0x7fffffff || static_cast<int64_t>(B) * H * o.shape.n_rb * (tp + tf) > 0x7fffffff)

@@ -484,11 +484,11 @@ cudaError_t tree_dim(const TreeParams &p, cudaStream_t s) {
 
 }  // namespace
 
-TreeShape tree_shape(int B, int H, int g, int N, int d, long long tiles_per_head, int record_bits, int value_bits) {
+TreeShape tree_shape(int B, int H, int g, int N, int d, long long tiles_per_head) {
     TreeShape t;
     const int rows = N * g;
     // tensor cores: one CTA per SM
-    if (tree_on_tensor_cores(d)) t.R = tree_mma_rows(rows, d, record_bits, value_bits);
+    if (tree_on_tensor_cores(d)) t.R = tree_mma_rows(rows);
     else t.R = d <= 256 ? 16 : 8;
     t.n_rb = (rows + t.R - 1) / t.R;
     const long long tiles = static_cast<long long>(B) * H * t.n_rb * tiles_per_head;

@@ -16,8 +16,11 @@
 // level adds a constant per row, which one more 16-deep step (constant columns in TMEM)
 // brings into the sum, so that x = m_t A U with one A for the block.
 // q enters as fp16 hi + lo (22 bits; the lo products run over the same TMEM
-// operand), P as fp16 p sigma (hi + lo beside wide values), value levels as fp16(s c_k), s chosen on the
-// host so that the levels round closely; 1/s is part of sigma.
+// operand), P as fp16 hi + 2^-11 lo of p sigma (22 bits; the lo products in columns of their
+// own: with hi alone the output's error was 1.4 times that of rounding it to fp16, and weights
+// below 2^-25 of the row's largest were lost; now it is 1.0 up to 4 value bits, 1.1 at 5, 1.2 at 6
+// and 1.3 at 8), value levels as fp16(s c_k), s chosen on the host so that the levels round
+// closely (those of 6 bits and more do not: the rest of that error); 1/s is part of sigma.
 //
 // A row's m is the running max of S + e, 2^e the power of two below the token's sigma (e in
 // [-64, 64]): it bounds the weights p sigma that fp16 has to hold, whatever the values' sizes,
@@ -87,6 +90,31 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// two independent binary32 operations
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+    float2 r;
+    asm("{.reg .b64 ra, rb, rr;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n add.rn.f32x2 rr, ra, rb;\n"
+        " mov.b64 {%0, %1}, rr;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fmul2(float2 a, float b) {
+    float2 r;
+    asm("{.reg .b64 ra, rb, rr;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %4};\n mul.rn.f32x2 rr, ra, rb;\n"
+        " mov.b64 {%0, %1}, rr;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 ffma2(float2 a, float b, float2 c) {
+    float2 r;
+    asm("{.reg .b64 ra, rb, rc, rr;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %4};\n mov.b64 rc, {%5, %6};\n"
+        " fma.rn.f32x2 rr, ra, rb, rc;\n mov.b64 {%0, %1}, rr;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b), "f"(c.x), "f"(c.y));
     return r;
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
@@ -421,19 +449,12 @@ static_assert(sizeof(TileDesc) == 64, "slot size");
 constexpr int kFirst = 1, kLast = 2;  // of its part
 constexpr int kFresh = 4;             // first of its (group, segment)
 constexpr int kFp16 = 8;
+constexpr int kTurn = 16;             // the next tile is fresh
 
 // ---------------------------------------------------------------- shared memory
-// LO: P as fp16 hi + lo, the lo products in columns of their own, for layers that hold
-// values of kWideValues bits or more.  Narrower levels find a scale at which they round
-// closely; from 6 bits on they do not, and the weights' rounding on top made the error 1.51
-// (6 bits) to 1.74 (8 bits) times that of rounding the output alone.  With lo it is 1.15 to
-// 1.45 (5 bits without: 1.48).  16384 tokens of K4V8, without and with: one sequence, 64
-// rows a head 42 / 49 us; two sequences, 256 rows 122 / 199 us (there the blocks
-// have 32 rows instead of 64, whose P lines have no place for lo).
-constexpr int kWideValues = 6;
-template <int D, int R, bool LO = false>
+template <int D, int R>
 struct Mma {
-    static constexpr int PC = LO ? 2 * R : R;       // columns of the P operand and of the sums: hi, lo
+    static constexpr int PC = 2 * R;                // columns of the P operand and of the sums: hi, lo
     static constexpr int NWG = R == 16 ? 2 : 4;     // softmax groups of four warps
     static constexpr int CW = R / NWG;              // rows per group
     static constexpr int kKeyWarp = 4 * NWG, kValueWarp = kKeyWarp + 4, kIssueWarp = kValueWarp + 8,
@@ -444,13 +465,13 @@ struct Mma {
     static constexpr int QIMG = 2 * QPART + R * 32;  // hi, lo, and the 16-deep step that adds the rows' constants
     static constexpr int QBUF = (QIMG + 1023) / 1024 * 1024;
     static constexpr int VBUF = HALVES * 128 * 128;
-    static_assert(PC <= 64, "P's line");
-    static constexpr int PBUF = 128 * 128;
+    static constexpr int PLO = R == 64 ? 16384 : 0; // lo: lines of their own, or behind hi in the same ones
+    static constexpr int PBUF = 128 * 128 + PLO;
     static constexpr int KCOLS = D / 2;             // TMEM columns of a K tile
     static constexpr int T_K = 0, T_S = 2 * KCOLS, T_O = T_S + 2 * R, T_C = T_O + PC;  // (T_C: 8 constant columns)
     static constexpr int TCOLS = 512;               // all of TMEM, so that its base is column 0
     static constexpr int O_Q = 0;
-    static constexpr int O_V = (O_Q + 2 * QBUF + 1023) / 1024 * 1024;
+    static constexpr int O_V = O_Q + QBUF;
     static constexpr int O_P = O_V + 2 * VBUF;
     static constexpr int O_T = O_P + PBUF;
     static constexpr int O_S = O_T + 2 * kTableBytes;   // [kSlots][2][128] scales
@@ -460,7 +481,12 @@ struct Mma {
     static constexpr int O_B = (O_X + NWG * 4 * CW * 4 + 15) / 16 * 16;
     static constexpr int kBars = 2 * 8 + 2 * 2 + 1 + 2 + 2 * kMaxStages + 2;
     static constexpr int O_RING = (O_B + kBars * 8 + 32 + 127) / 128 * 128;
-    static constexpr int kRing = kSmemMax - 1024 - O_RING;  // (1024: alignment)
+    // the ring, and behind it the second buffer of queries where two tiles of records leave
+    // room for one (1024: alignment)
+    static constexpr int kRing = kSmemMax - 1024 - O_RING;
+    static constexpr int O_Q2 = kSmemMax - 1024 - QBUF;
+    static_assert(QBUF % 1024 == 0 && O_Q2 % 1024 == 0, "swizzled operands");
+    static_assert(kRing >= 2 * 128 * (D / 8) * 16, "two tiles of the widest records");
 };
 
 template <int D, int R>
@@ -470,6 +496,7 @@ __host__ __device__ constexpr int tree_image_stride() {
 
 struct RingGeo {
     int stage, stages;
+    int q_log;  // log2 of the query buffers
 };
 
 // The queries as the MMA's B operand, one image per (b, h, rb) and key width kb (0:
@@ -717,10 +744,10 @@ __device__ __forceinline__ void cp16(unsigned dst, const void *src) {
 }
 
 // ---------------------------------------------------------------- kernel
-template <int D, int R, bool LO>
+template <int D, int R>
 __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
     tree_mma_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ TreeLevels lv, const RingGeo ring) {
-    using C = Mma<D, R, LO>;
+    using C = Mma<D, R>;
     constexpr int CW = C::CW, kKeyWarp = C::kKeyWarp, kValueWarp = C::kValueWarp, kIssueWarp = C::kIssueWarp,
                   kLoadWarp = C::kLoadWarp;
     extern __shared__ uint8_t smem_raw[];
@@ -735,8 +762,12 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
     auto s_full = [&](int i) { return bars + 8u * (8 + i); };
     auto s_empty = [&](int i) { return bars + 8u * (10 + i); };
     const unsigned p_full = bars + 8u * 12, p_empty = bars + 8u * 14;
-    auto q_full = [&](int i) { return bars + 8u * (16 + i); };
-    auto q_empty = [&](int i) { return bars + 8u * (18 + i); };
+    // image `ev` of this worker: its buffer, and the parity of the buffer's fill with it
+    auto q_buf = [&](int ev) { return ev & ring.q_log; };
+    auto q_par = [&](int ev) { return static_cast<unsigned>(ev >> ring.q_log) & 1u; };
+    auto q_at = [&](int ev) { return sb + (q_buf(ev) ? C::O_Q2 : C::O_Q); };
+    auto q_full = [&](int ev) { return bars + 8u * (16 + q_buf(ev)); };
+    auto q_empty = [&](int ev) { return bars + 8u * (18 + q_buf(ev)); };
     const unsigned o_free = bars + 8u * 20;
     auto drain = [&](int i) { return bars + 8u * (21 + i); };
     auto r_full = [&](int i) { return bars + 8u * (23 + i); };
@@ -816,16 +847,16 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 }
             }
             if (w.fresh && kv == 0) {
-                // the queries for this segment's key width, into the buffer of two changes ago
+                // the queries for this segment's key width, into the buffer that they are done with first
                 ev++;
                 const uint8_t *image = p.images + (static_cast<size_t>(group_of(p, w.x)) * p.n_var + p.var[w.seg][w.x.h]) *
                                                       tree_image_stride<D, R>();
-                wait(q_empty(ev & 1), ((ev >> 1) & 1) ^ 1);
+                wait(q_empty(ev), q_par(ev) ^ 1);
                 if (wait.gone) break;
                 if (lane == 0) {
                     issued = ev;
-                    bar_expect_tx(q_full(ev & 1), C::QIMG);
-                    bulk_load(sb + C::O_Q + (ev & 1) * C::QBUF, image, C::QIMG, q_full(ev & 1));
+                    bar_expect_tx(q_full(ev), C::QIMG);
+                    bulk_load(q_at(ev), image, C::QIMG, q_full(ev));
                 }
                 A = __ldcg(reinterpret_cast<const float *>(image + C::QIMG));
             }
@@ -839,7 +870,10 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             const int n = min(kTreeTile, d.left), chunks = (n * rec + 15) / 16;
             const uint8_t *from = src + static_cast<size_t>(w.t) * (kTreeTile * rec);
             const float *sc = scale + static_cast<size_t>(w.t) * kTreeTile;
-            if (j + 1 < n_tiles) walk_next(p, w);
+            if (j + 1 < n_tiles) {
+                walk_next(p, w);
+                if (w.fresh) d.flags |= kTurn;
+            }
             if (j + 1 == n_tiles || w.first) d.flags |= kLast;
             wait(r_empty(st), ((j / ring.stages) & 1) ^ 1);
             if (wait.gone) break;
@@ -863,9 +897,9 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
         asm volatile("cp.async.wait_all;" ::: "memory");
         // the last query images have landed before shared memory goes away
         if (kv == 0 && lane == 0)
-            for (int e = max(issued - 1, 0); e <= issued; e++)
+            for (int e = max(issued - ring.q_log, 0); e <= issued; e++)
                 for (int i = 0; i < kDrainPolls; i++)
-                    if (bar_try(q_full(e & 1), (e >> 1) & 1)) break;
+                    if (bar_try(q_full(e), q_par(e))) break;
     } else if (warp == kIssueWarp) {
         // ------------------------------------------------------ S^T = K q^T
         constexpr uint32_t id_s = idesc(R, false);
@@ -878,15 +912,12 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             if (wait.gone) break;
             const int flags = reinterpret_cast<const TileDesc *>(sm + C::O_D)[j % kSlots].flags;
             if (flags & kFresh) {
-                // the products with the old queries are behind this point; the new ones' image
-                if (ev >= 0 && elect_one()) mma_commit(q_empty(ev & 1));
-                __syncwarp();
                 ev++;
-                wait(q_full(ev & 1), (ev >> 1) & 1);
+                wait(q_full(ev), q_par(ev));
                 if (wait.gone) break;
             }
             tc_after();
-            const uint64_t q = desc_k(sb + C::O_Q + (ev & 1) * C::QBUF);
+            const uint64_t q = desc_k(q_at(ev));
             const unsigned a = C::T_K + b * C::KCOLS, d = C::T_S + b * R;
             if (elect_one()) {
 #pragma unroll
@@ -896,10 +927,11 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < D / 16; k++)
                         mma_ts(d, a + 8 * k, q + ((C::QPART + (k >> 2) * R * 128 + 32 * (k & 3)) >> 4), id_s, 1);
-                    mma_ts(d, C::T_C, desc_k16(sb + C::O_Q + (ev & 1) * C::QBUF + 2 * C::QPART), id_s, 1);
+                    mma_ts(d, C::T_C, desc_k16(q_at(ev) + 2 * C::QPART), id_s, 1);
                 }
                 mma_commit(k_empty(b));
                 mma_commit(s_full(b));
+                if (flags & kTurn) mma_commit(q_empty(ev));  // the last product with these queries
             }
             __syncwarp();
         }
@@ -925,7 +957,7 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
             }
             tc_after();
             const uint64_t v = desc_mn(sb + C::O_V + b * C::VBUF, C::HALVES == 2 ? 16384 : 0),
-                           pp = desc_mn(sb + C::O_P, 0);
+                           pp = desc_mn(sb + C::O_P, C::PLO);
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 8; k++) mma_ss(C::T_O, v + (2048 * k >> 4), pp + (2048 * k >> 4), id_o, k != 0 || !first);
@@ -1107,10 +1139,9 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < CW; c += 4) {
                     const float4 m = *reinterpret_cast<const float4 *>(m_row + R + c);
-                    u[c] = fmaf(u[c], ks, m.x);
-                    u[c + 1] = fmaf(u[c + 1], ks, m.y);
-                    u[c + 2] = fmaf(u[c + 2], ks, m.z);
-                    u[c + 3] = fmaf(u[c + 3], ks, m.w);
+                    const float2 u0 = ffma2(make_float2(u[c], u[c + 1]), ks, make_float2(m.x, m.y));
+                    const float2 u1 = ffma2(make_float2(u[c + 2], u[c + 3]), ks, make_float2(m.z, m.w));
+                    u[c] = u0.x, u[c + 1] = u0.y, u[c + 2] = u1.x, u[c + 3] = u1.y;
                     top = fmax3(top, u[c], u[c + 1]);
                     top = fmax3(top, u[c + 2], u[c + 3]);
                 }
@@ -1173,32 +1204,28 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < CW; c++) u[c] = valid ? u[c] : -kInf;
             }
-            uint32_t h[CW / 2], lo[CW / 2];
+            uint32_t h[CW / 2], lo[CW / 2];  // hi and 2^11 (w - hi), so that weights down to 2^-36 count
 #pragma unroll
             for (int c = 0; c < CW; c += 2) {
-                const float p0 = ex2(u[c]), p1 = ex2(u[c + 1]);
-                l[c] += p0;
-                l[c + 1] += p1;
-                const float w0 = p0 * sig, w1 = p1 * sig;
-                const __half2 q = __floats2half2_rn(w0, w1);
+                const float2 pr = make_float2(ex2(u[c]), ex2(u[c + 1]));
+                const float2 ls = fadd2(make_float2(l[c], l[c + 1]), pr);
+                l[c] = ls.x, l[c + 1] = ls.y;
+                const float2 w = fmul2(pr, sig);
+                const __half2 q = __floats2half2_rn(w.x, w.y);
                 h[c / 2] = *reinterpret_cast<const uint32_t *>(&q);
-                if constexpr (LO) {
-                    const float2 f = __half22float2(q);
-                    const __half2 r = __floats2half2_rn(w0 - f.x, w1 - f.y);
-                    lo[c / 2] = *reinterpret_cast<const uint32_t *>(&r);
-                }
+                const float2 left = ffma2(__half22float2(q), -2048.f, fmul2(w, 2048.f));  // (exact)
+                const __half2 r = __floats2half2_rn(left.x, left.y);
+                lo[c / 2] = *reinterpret_cast<const uint32_t *>(&r);
             }
             wait.unless(p_free, p_empty, (j & 1) ^ 1);
 #pragma unroll
             for (int c = 0; c < CW; c += 8)
                 *reinterpret_cast<uint4 *>(prow + ((((wg * CW + c) >> 3) ^ (tok & 7)) << 4)) =
                     make_uint4(h[c / 2], h[c / 2 + 1], h[c / 2 + 2], h[c / 2 + 3]);
-            if constexpr (LO) {
 #pragma unroll
-                for (int c = 0; c < CW; c += 8)
-                    *reinterpret_cast<uint4 *>(prow + ((((R + wg * CW + c) >> 3) ^ (tok & 7)) << 4)) =
-                        make_uint4(lo[c / 2], lo[c / 2 + 1], lo[c / 2 + 2], lo[c / 2 + 3]);
-            }
+            for (int c = 0; c < CW; c += 8)
+                *reinterpret_cast<uint4 *>(prow + C::PLO + (((((C::PLO ? 0 : R) + wg * CW + c) >> 3) ^ (tok & 7)) << 4)) =
+                    make_uint4(lo[c / 2], lo[c / 2 + 1], lo[c / 2 + 2], lo[c / 2 + 3]);
             fence_async();
             tc_before();
             __syncwarp();
@@ -1226,14 +1253,12 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
                 tc_after();
 #pragma unroll
                 for (int c = 0; c < CW; c += 8) {
-                    float o[8];
+                    float o[8], y[8];
                     tmem_ld<8>(o_addr + c, o);
-                    if constexpr (LO) {
-                        float y[8];
-                        tmem_ld<8>(o_addr + R + c, y);
+                    tmem_ld<8>(o_addr + R + c, y);
 #pragma unroll
-                        for (int i = 0; i < 8; i++) o[i] += y[i];
-                    }
+                    for (int i = 0; i < 8; i++)  // (an infinite value: hi's sum tells its sign, lo may be 0 or negative)
+                        o[i] = fabsf(o[i]) == kInf ? o[i] : fmaf(y[i], 1.f / 2048.f, o[i]);
                     if (tok < D)
 #pragma unroll
                         for (int i = 0; i < 8; i++) rec[(wg * CW + c + i) * (D + 4) + 4 + tok] = o[i];
@@ -1254,8 +1279,8 @@ __global__ void __launch_bounds__(Mma<D, R>::kThreads, 1)
 
 // ---------------------------------------------------------------- value levels (host)
 // fp16(s c_k), s in [1, 2) chosen so that the levels' rounding errors, weighted as
-// N(0, 1) weighs their cells, are smallest: 4096 candidates for up to 6 bits
-// (wider codebooks have too many levels for a choice to matter).
+// N(0, 1) weighs their cells, are smallest of 4096 candidates (relative to the levels, all
+// alike: 2e-8 at 1 bit, 2e-5 at 3, 9e-5 at 5, 1.7e-4 at 8; s = 1 at 8: 2.3e-4).
 struct HostLevels {
     std::once_flag once;
     uint16_t half[256];
@@ -1267,16 +1292,18 @@ void fit_levels(HostLevels &h, const float *c, int bits) {
     const int n = 1 << bits;
     double best = HUGE_VAL;
     float s_best = 1.f;
-    const int tries = bits <= 6 ? 4096 : 1;
-    for (int i = 0; i < tries; i++) {
+    double mass[128];
+    for (int k = n / 2; k < n; k++) {
+        const double a = k == n / 2 ? 0.0 : 0.5 * (static_cast<double>(c[k - 1]) + c[k]);
+        const double b = k + 1 == n ? 1e9 : 0.5 * (static_cast<double>(c[k]) + c[k + 1]);
+        mass[k - n / 2] = std::erfc(a * 0.70710678118654752) - std::erfc(b * 0.70710678118654752);
+    }
+    for (int i = 0; i < 4096; i++) {
         const float s = 1.f + static_cast<float>(i) / 4096.f;
         double err = 0.0;
         for (int k = n / 2; k < n; k++) {
-            const double a = k == n / 2 ? 0.0 : 0.5 * (static_cast<double>(c[k - 1]) + c[k]);
-            const double b = k + 1 == n ? 1e9 : 0.5 * (static_cast<double>(c[k]) + c[k + 1]);
-            const double mass = std::erfc(a * 0.70710678118654752) - std::erfc(b * 0.70710678118654752);
             const double d = static_cast<double>(__half2float(__float2half_rn(s * c[k]))) / s - c[k];
-            err += mass * d * d;
+            err += mass[k - n / 2] * d * d;
         }
         if (err < best) best = err, s_best = s;
     }
@@ -1284,23 +1311,25 @@ void fit_levels(HostLevels &h, const float *c, int bits) {
     h.inv = 1.f / s_best;
 }
 
-template <int D, int R, bool LO>
+template <int D, int R>
 cudaError_t tree_mma(const TreeParams &p, const TreeLevels &lv, cudaStream_t s) {
-    using C = Mma<D, R, LO>;
+    using C = Mma<D, R>;
     static_assert(C::T_C + 8 <= 512, "TMEM columns");
-    static_assert(R == 64 || C::kRing >= 2 * 128 * (D / 8) * 16, "two tiles of the widest records");
     int stage = 0;
     for (int i = 0; i < p.n_packed; i++)
         for (int h = 0; h < p.H; h++) stage = std::max(stage, 128 * (D / 8) * (p.seg[i].seg.kbits[h] + p.seg[i].seg.vbits[h]));
     RingGeo ring;
     ring.stage = std::max(stage, 128);
-    ring.stages = std::min(kMaxStages, C::kRing / ring.stage);
-    // Two at least: the groups of value warps take alternate tiles, and a wait for a stage's
+    // A second buffer of queries, so that a segment's first tile does not wait for them, where
+    // the ring keeps two stages.
+    ring.q_log = (C::kRing - C::QBUF) / ring.stage >= 2 ? 1 : 0;
+    ring.stages = std::min(kMaxStages, (C::kRing - ring.q_log * C::QBUF) / ring.stage);
+    // Two stages at least: the groups of value warps take alternate tiles, and a wait for a stage's
     // fill is by parity, right for the fill behind the last one that the waiter knows of.
     // (A group that has seen tile j filled knows that tile j - 1 was: fills end in order.  So
     // the fill before its next tile's is known, unless one stage holds both.)
     if (ring.stages < 2) return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaFuncSetAttribute(tree_mma_kernel<D, R, LO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    cudaError_t e = cudaFuncSetAttribute(tree_mma_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return e;
     const int images = p.B * p.H * p.n_rb * p.n_var;
     TreeQueryParams qp;
@@ -1323,44 +1352,32 @@ cudaError_t tree_mma(const TreeParams &p, const TreeLevels &lv, cudaStream_t s) 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_mma_kernel<D, R, LO>, p, lv, ring);
+    return cudaLaunchKernelEx(&cfg, tree_mma_kernel<D, R>, p, lv, ring);
 }
 
-// LO with up to 32 rows a block: P's hi and lo then share the lines that 64 rows fill.
-template <int D, bool LO>
+template <int D>
 cudaError_t tree_rows(const TreeParams &p, const TreeLevels &lv, cudaStream_t s) {
-    if (p.R == 16) return tree_mma<D, 16, LO>(p, lv, s);
-    if (p.R == 32) return tree_mma<D, 32, LO>(p, lv, s);
-    if constexpr (!LO) return tree_mma<D, 64, false>(p, lv, s);
-    return cudaErrorInvalidConfiguration;
+    return p.R == 16 ? tree_mma<D, 16>(p, lv, s) : p.R == 32 ? tree_mma<D, 32>(p, lv, s) : tree_mma<D, 64>(p, lv, s);
 }
 
 }  // namespace
 
-// The least power of two that holds the rows, up to 64 columns; 32 where P takes hi and
-// lo, or where two tiles of records would not fit beside 64 rows.
-int tree_mma_rows(int rows, int d, int record_bits, int value_bits) {
-    const int ring = d == 128 ? Mma<128, 64>::kRing : Mma<64, 64>::kRing;
-    const bool narrow = value_bits >= kWideValues || 2 * 128 * (d / 8) * record_bits > ring;
-    return rows <= 16 ? 16 : rows <= 32 || narrow ? 32 : 64;
-}
+// The least power of two that holds the rows, up to 64.
+int tree_mma_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 cudaError_t launch_tree_mma(const TreeParams &p, cudaStream_t s) {
     TreeLevels lv;
-    bool wide = false;
     std::memset(&lv, 0, sizeof(lv));
     for (int i = 0; i < p.n_packed; i++)
         for (int h = 0; h < p.H; h++) {
             const int vb = p.seg[i].seg.vbits[h], law = p.seg[i].law;
-            wide |= vb >= kWideValues;
             if (lv.inv[law][vb] != 0.f) continue;
             HostLevels &hl = g_levels[law][vb];
             std::call_once(hl.once, [&] { fit_levels(hl, p.centroid[law] + cb_off(vb), vb); });
             std::memcpy(lv.half[law] + cb_off(vb), hl.half, sizeof(uint16_t) << vb);
             lv.inv[law][vb] = hl.inv;
         }
-    if (p.d == 128) return wide ? tree_rows<128, true>(p, lv, s) : tree_rows<128, false>(p, lv, s);
-    return wide ? tree_rows<64, true>(p, lv, s) : tree_rows<64, false>(p, lv, s);
+    return p.d == 128 ? tree_rows<128>(p, lv, s) : tree_rows<64>(p, lv, s);
 }
 
 }  // namespace tqk

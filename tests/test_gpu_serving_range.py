@@ -96,3 +96,65 @@ def test_non_finite_coordinate_of_a_stored_value(tq, d, bad):
     assert torch.equal(base.bits(got[1][..., rest]), base.bits(want[1][..., rest]))
     hit = got[1][..., at].float()
     assert bool(torch.isnan(hit).all()) if math.isnan(bad) else bool((hit == bad).all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N", [3, 14])
+def test_large_fp16_value_of_little_weight(tq, d, N):
+    """An fp16 row near fp16's end, 2^24 times the others' size, at a weight of 2^-26 of theirs: a hundredth of the
+    result's size, by a weight that one fp16 beside the row's largest does not hold."""
+    H, gqa, B, n, at = 1, 4, 1, 300, 170
+    g = gen(d + N)
+    lead = randn(g, 1, 1, 1, d)
+    q = (lead * (1 + 0.01 * torch.rand(B, N, H * gqa, 1, generator=g, device=DEV))).half()
+    seg = tq.Fp16Segment(B, H, d, 304, n_tokens=n, k=(0.1 * randn(g, B, H, 304, d)).half(),
+                         v=(2.0**-8 * randn(g, B, H, 304, d)).half())
+    k, v = ((s * randn(g, B, H, N, d)).half() for s in (0.1, 2.0**-8))
+    usual = base.tree_ref(tq, q, k, v, None, [seg], [None], torch.eye(d, device=DEV).double())[2]
+    x = lead[0, 0, 0].half()
+    seg.k[0, 0, at] = (-26 * math.log(2) * math.sqrt(d) / float((x.float() ** 2).sum()) * x.float()).half()
+    seg.v[0, 0, at] = (60000 * torch.sign(randn(g, d))).half()
+    out = base.run_tree(tq, q, k, v, [seg])
+    ref = base.tree_ref(tq, q, k, v, None, [seg], [None], torch.eye(d, device=DEV).double())
+    # half a step of 2^-35 of the row's largest weight, which is a hundredth of their sum at most, for the large
+    # row, and half a step of fp16's smallest, 2^-24, for each coordinate of the result
+    check(out, (ref[0], ref[1], usual), math.sqrt(d) * (2.0**-36 * 60000 / 100 + 2.0**-25) * torch.ones_like(usual))
+    share = (ref[0] - base.tree_ref(tq, q, k, v, None, [without(tq, seg, at)], [None], torch.eye(d, device=DEV).double())[0])
+    assert share.norm() > 0.003 * ref[0].norm()  # (what the test is about)
+
+
+def without(tq, seg, at):
+    keep = [t for t in range(seg.k.shape[2]) if t != at]
+    return tq.Fp16Segment(1, 1, seg.k.shape[3], len(keep), n_tokens=seg.n_tokens - 1, k=seg.k[:, :, keep].contiguous(),
+                          v=seg.v[:, :, keep].contiguous())
+
+
+def level_error(tq, bits):
+    """Root mean square error of fp16(s c) / s over the levels c, of their own, s in [1, 2) the scale in steps of
+    1/4096 at which the levels' errors, weighted by the share of N(0, 1) in their cells, are smallest."""
+    c = tq.tq_fit_codebook(bits)[0].double()
+    edge = torch.cat([torch.tensor([-math.inf]).double(), (c[1:] + c[:-1]) / 2, torch.tensor([math.inf]).double()])
+    mass = torch.special.ndtr(edge[1:]) - torch.special.ndtr(edge[:-1])
+    s = (1 + torch.arange(4096) / 4096.0)[:, None]
+    e = ((s * c.float()).half().double() / s.double() - c) ** 2
+    return float(e[(e * mass).sum(1).argmin()].mean().sqrt() / (c**2).mean().sqrt())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N", [4, 8, 16, 40])
+@pytest.mark.parametrize("vb", range(1, 9))
+def test_weights_round_no_further_than_the_result(tq, d, N, vb):
+    """Weights of 22 bits, and levels whose rounding is known: beside it the error is that of rounding the result to
+    fp16."""
+    H, gqa, B, n = 2, 4, 1, 1500
+    q, k, v, parts, lens, rng = base.tree_case(tq, d, H, gqa, B, N, [((4, vb), n)], False, seed=vb + N)
+    parts[0].kscale.nan_to_num_(0.0).clamp_(max=0.5)
+    parts[0].vscale.nan_to_num_(0.0)
+    out = base.run_tree(tq, q, k, v, parts)
+    _, R = base.rotation64(tq, d, 21)
+    want, _, reach = base.tree_ref(tq, q, k, v, None, parts, lens, R)
+    best = (want.half().double() - want).norm() / want.norm()
+    # random codes: the levels' errors are as independent as the values; scores as in check_tree; a tenth
+    # more for the samples' spread (rows of one cache share its tokens)
+    bound = 1.1 * math.hypot(float(best), level_error(tq, vb)) + float(2 * reach.max()) * 2.0**-19
+    assert float((out.double() - want).norm() / want.norm()) <= bound
