@@ -289,7 +289,10 @@ class SpeculativeCache:
     `commit` (the accepted drafts' rows into the cache), and after the last layer
     `advance`.  The lengths stay on the device and no call waits for it, so that a
     whole step can be captured into a CUDA graph.  Tokens that do not fit any more are
-    dropped: keep sinks + capacity at least at the longest sequence."""
+    dropped: keep sinks + capacity at least at the longest sequence.  `stream` (a torch
+    stream or a raw handle, None: the current one) takes all of a call's work; the calls of a
+    cache share its lengths and workspace, so that they have to be ordered: give all of
+    them one stream, behind the one that was current at construction."""
 
     def __init__(self, layers: int, batch: int, kv_heads: int, q_heads: int, head_dim: int, capacity: int, rope: T.Rope,
                  kbits=3, vbits=3, sinks: int = 128, drafts: int = 16, seed: int = 42, device="cuda"):
@@ -311,6 +314,7 @@ class SpeculativeCache:
         self.body_len = torch.zeros(batch, **i32)     # and in the packed segment
         self.body_at = torch.full((batch,), -sinks, **i32)  # place of the next token in the packed segment
         self.zero = torch.zeros(batch, **i32)
+        self.body_first = self.body_at.clone()        # that of a sequence's first token
         self.workspace = torch.empty(T.tq_tree_workspace_size(self.views[0], batch, kv_heads, q_heads, drafts, head_dim),
                                      dtype=torch.uint8, device=device)
 
@@ -323,7 +327,7 @@ class SpeculativeCache:
     def prefill(self, l, K, V, n, positions, stream=None):
         """Prompts of n[b] tokens into the empty cache of layer l: K, V fp16 [B][H][S][d],
         the keys without their positions (int32 [S] or [B][S])."""
-        self._write(l, K, V, self.zero, self.zero - self.sinks, n, rope=self.rope, positions=positions, stream=stream)
+        self._write(l, K, V, self.zero, self.body_first, n, rope=self.rope, positions=positions, stream=stream)
 
     def attend(self, l, q, k, v, positions, out, mask=None, stream=None):
         """Layer l's attention of N <= drafts drafted tokens per sequence: q fp16
@@ -338,21 +342,23 @@ class SpeculativeCache:
         root) behind layer l's tokens: k, v as `attend` left them."""
         self._write(l, k, v, self.length, self.body_at, n, index=index, stream=stream)
 
-    def advance(self, n):
-        """The lengths after a step or a prefill of n[b] tokens (int32 [B]), on the current stream."""
-        self.length.add_(n).clamp_(0, self.sinks + self.capacity)
-        torch.clamp(self.length, max=self.sinks, out=self.head_len)
-        torch.sub(self.length, self.sinks, out=self.body_at)
-        torch.clamp(self.body_at, min=0, out=self.body_len)
+    def advance(self, n, stream=None):
+        """The lengths after a step or a prefill of n[b] tokens (int32 [B])."""
+        with T.on_stream(stream, self.length.device):
+            self.length.add_(n).clamp_(0, self.sinks + self.capacity)
+            torch.clamp(self.length, max=self.sinks, out=self.head_len)
+            torch.sub(self.length, self.sinks, out=self.body_at)
+            torch.clamp(self.body_at, min=0, out=self.body_len)
 
     def read(self, l, first, n_max, dtype=torch.float16, stream=None):
         """Rows first[b] .. first[b] + n_max - 1 of layer l as vectors ([k, v], each
-        [B][H][n_max][d]; zeros behind a sequence's last token)."""
+        [B][H][n_max][d], allocated for `stream`; zeros behind a sequence's last token)."""
         shape = (self.B, self.H, n_max, self.d)
-        out = [torch.zeros(shape, dtype=dtype, device=self.length.device) for _ in range(2)]
-        if self.sinks:
-            T.tq_read(self.head[l], None, first, n_max, n_read=self.head_len - first, out=out, stream=stream)
-        T.tq_read(self.body[l], self.rot[l], first - self.sinks, n_max, n_read=self.length - first, out=out, stream=stream)
+        with T.on_stream(stream, self.length.device):
+            out = [torch.zeros(shape, dtype=dtype, device=self.length.device) for _ in range(2)]
+            if self.sinks:
+                T.tq_read(self.head[l], None, first, n_max, n_read=self.head_len - first, out=out)
+            T.tq_read(self.body[l], self.rot[l], first - self.sinks, n_max, n_read=self.length - first, out=out)
         return out
 
 

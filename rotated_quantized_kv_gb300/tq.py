@@ -14,6 +14,7 @@ Errors come back as ``TQError`` carrying the status and its message.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -198,6 +199,17 @@ def _stream(stream) -> int | None:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def on_stream(stream, device):
+    """Context in which torch's own work goes to `stream` (a torch stream, a raw handle of one of `device`, or
+    None: the current one), as what a call prepares has to go where its kernels run."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        raw = int(stream)
+        stream = torch.cuda.ExternalStream(raw, device) if raw else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 # ----------------------------------------------------------------- host calls
@@ -425,13 +437,15 @@ def tq_requantize(src: PackedSegment, src_t_begin: int, n_tokens: int, dst: Pack
 
 def tq_dequantize(seg: PackedSegment, t_begin: int, n_tokens: int, rot: tq_rotation | None = None,
                   rotated: bool = True, original: bool = False, stream=None):
-    """(k_rot, v_rot, k_orig, v_orig) float32 [B][H][n][d] CUDA tensors (None where not asked)."""
+    """(k_rot, v_rot, k_orig, v_orig) float32 [B][H][n][d] CUDA tensors (None where not asked), allocated
+    for `stream`."""
     L = seg.layout
     shape = (L.batch, L.n_heads, n_tokens, L.head_dim)
     dev = seg.kcodes.device
     mk = (lambda: torch.empty(shape, dtype=torch.float32, device=dev))
-    kr, vr = (mk(), mk()) if rotated else (None, None)
-    ko, vo = (mk(), mk()) if original else (None, None)
+    with on_stream(stream, dev):
+        kr, vr = (mk(), mk()) if rotated else (None, None)
+        ko, vo = (mk(), mk()) if original else (None, None)
     _check(_lib.tq_dequantize(ctypes.byref(L), ctypes.byref(seg.bufs()),
                               ctypes.byref(rot) if rot is not None else None, t_begin, n_tokens,
                               _ptr(kr), _ptr(vr), _ptr(ko), _ptr(vo), _stream(stream)), "tq_dequantize")
@@ -577,9 +591,10 @@ def tq_rope_frequencies(spec: tq_rope_spec) -> np.ndarray:
 
 
 def tq_rope_table(spec: tq_rope_spec, n_pos: int, first_pos: int = 0, device="cuda", stream=None) -> torch.Tensor:
-    """float32 CUDA table [n_pos][2][rotary_dim / 2] of cosines and sines."""
+    """float32 CUDA table [n_pos][2][rotary_dim / 2] of cosines and sines, allocated for `stream`."""
     _require(n_pos >= 0, "tq_rope_table")
-    t = torch.empty(n_pos, 2, spec.rotary_dim // 2, dtype=torch.float32, device=device)
+    with on_stream(stream, device):
+        t = torch.empty(n_pos, 2, spec.rotary_dim // 2, dtype=torch.float32, device=device)
     _call([t], stream, "tq_rope_table", _lib.tq_rope_table, ctypes.byref(spec), first_pos, n_pos, t.data_ptr())
     return t
 
@@ -677,14 +692,15 @@ def tq_read(seg, rot: tq_rotation | None, t_begin: torch.Tensor, n_max: int, n_r
     min(n_read[b], n_max) of sequence b is position t_begin[b] + j (int32 [B]
     tensors).  out: [k, v] tensors [B][H][n_max][d] of fp16, bf16 or fp32 (any
     strides with unit stride in d, None entries: not wanted), default new ones of
-    `dtype`, zero where nothing is read.  rot None: rotated-space vectors."""
+    `dtype` on `stream`, zero where nothing is read.  rot None: rotated-space vectors."""
     where = "tq_read"
     L = seg.layout
     shape = (L.batch, L.n_heads, n_max, L.head_dim)
     own = seg.kcodes if seg.kind == TQ_SEG_PACKED else seg.k
     if out is None:
-        _require(n_max >= 0, where)
-        out = [torch.zeros(shape, dtype=dtype, device=own.device) for _ in range(2)]
+        _require(n_max >= 0 and own.is_cuda, where)
+        with on_stream(stream, own.device):  # behind this the kernel writes them
+            out = [torch.zeros(shape, dtype=dtype, device=own.device) for _ in range(2)]
     k, v = out
     some = [t for t in (k, v) if t is not None]
     _int32(t_begin, where, (L.batch,))
