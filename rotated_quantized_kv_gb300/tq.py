@@ -169,9 +169,9 @@ _lib.tq_rope_frequencies.argtypes = [ctypes.POINTER(tq_rope_spec), _P]
 _lib.tq_rope_table.argtypes = [ctypes.POINTER(tq_rope_spec), _I, _I, _P, _P]
 _lib.tq_rope.argtypes = [ctypes.POINTER(tq_rope_view), _I, _I, _I, _I, _P, _L, _P, _I, _I,
                          _P]
-_lib.tq_append.argtypes = [ctypes.POINTER(tq_segment), ctypes.POINTER(tq_rotation), ctypes.POINTER(tq_rope_view), _P, _L,
+_lib.tq_append.argtypes = [_P, ctypes.POINTER(tq_rotation), ctypes.POINTER(tq_rope_view), _P, _L,
                            _P, _P, _P, _P, _I, _I, _P, _P, _P, _L, _P]
-_lib.tq_read.argtypes = [ctypes.POINTER(tq_segment), ctypes.POINTER(tq_rotation), _I, _P, _P, _I, _P, _P, _P, _P, _P]
+_lib.tq_read.argtypes = [_P, ctypes.POINTER(tq_rotation), _I, _P, _P, _I, _P, _P, _P, _P, _P]
 _lib.tq_tree_workspace_size.argtypes = [ctypes.POINTER(tq_layer_view), _I, _I, _I, _I, _I,
                                         ctypes.POINTER(ctypes.c_size_t)]
 _lib.tq_tree_attention.argtypes = [ctypes.POINTER(tq_layer_view), _I, _I, _I, _I, _P, _P,
@@ -310,12 +310,15 @@ def tq_age_tiers(n_tokens: int, age_bounds):
 
 
 # ----------------------------------------------------------------- segments
+_pack_segment = struct.Struct(f"ii{ctypes.sizeof(tq_segment_layout)}s8PPPP").pack
+assert struct.calcsize(f"ii{ctypes.sizeof(tq_segment_layout)}s8PPPP") == ctypes.sizeof(tq_segment)
+
+
 class PackedSegment:
     """Device buffers of one packed segment, allocated with torch from the sizes
     tq_packed_size reports."""
 
     kind = TQ_SEG_PACKED
-    _struct = _ref = None
     attn_mass = None  # optional float tensor [B][H][capacity]: written by tq_decode_attention
 
     def __init__(self, layout: tq_segment_layout, device="cuda", n_tokens: int = 0):
@@ -347,17 +350,11 @@ class PackedSegment:
         s.attn_mass = _ptr(self.attn_mass)
         return s
 
-    def reference(self):
-        """The segment for one call: the same structure each time, its fields set anew."""
-        s = self._struct
-        if s is None:
-            s = self._struct = tq_segment()
-            s.kind = TQ_SEG_PACKED
-            self._ref = ctypes.byref(s)
-        s.n_tokens, s.layout, p = self.n_tokens, self.layout, s.packed
-        p.kcodes, p.vcodes = self.kcodes.data_ptr(), self.vcodes.data_ptr()
-        p.kscale, p.vscale = self.kscale.data_ptr(), self.vscale.data_ptr()
-        return self._ref
+    def reference(self) -> bytes:
+        """The segment as a serving call is handed it: a tq_segment of its own each time, the fields that these
+        calls read (no sketches, no attn_mass)."""
+        return _pack_segment(TQ_SEG_PACKED, self.n_tokens, bytes(self.layout), self.kcodes.data_ptr(), self.vcodes.data_ptr(),
+                             self.kscale.data_ptr(), self.vscale.data_ptr(), 0, 0, 0, 0, 0, 0, 0)
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in
@@ -370,7 +367,6 @@ class Fp16Segment:
     """Tokens kept verbatim in fp16: [B][H][capacity][d] K and V."""
 
     kind = TQ_SEG_FP16
-    _struct = _ref = None
     attn_mass = None  # optional float tensor [B][H][capacity]: written by tq_decode_attention
 
     def __init__(self, batch, n_heads, head_dim, capacity, device="cuda", n_tokens=0, k=None, v=None):
@@ -387,16 +383,10 @@ class Fp16Segment:
         s.attn_mass = _ptr(self.attn_mass)
         return s
 
-    def reference(self):
-        """The segment for one call: the same structure each time, its fields set anew."""
-        s = self._struct
-        if s is None:
-            s = self._struct = tq_segment()
-            s.kind = TQ_SEG_FP16
-            self._ref = ctypes.byref(s)
-        s.n_tokens, s.layout = self.n_tokens, self.layout
-        s.k16, s.v16 = self.k.data_ptr(), self.v.data_ptr()
-        return self._ref
+    def reference(self) -> bytes:
+        """The segment as a serving call is handed it (see PackedSegment.reference)."""
+        return _pack_segment(TQ_SEG_FP16, self.n_tokens, bytes(self.layout), 0, 0, 0, 0, 0, 0, 0, 0, self.k.data_ptr(),
+                             self.v.data_ptr(), 0)
 
 
 def layer_view(rot: tq_rotation, segments, qjl_estimator: int = TQ_QJL_UNBIASED) -> tq_layer_view:
