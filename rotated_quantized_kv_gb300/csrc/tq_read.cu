@@ -74,9 +74,9 @@ __global__ void __launch_bounds__(kReadThreads) read_team_kernel(const __grid_co
 #pragma unroll
             for (int e = 0; e < E; e += 4) {
                 uint32_t k[4];
-                if (rk % 4 == 0) {
+                if (whole_words<D>(rec, rk)) {
                     load_codes4(rec, rk / 4, lt * E + e, bits, k);
-                } else {  // d = 16 and an odd width
+                } else {
 #pragma unroll
                     for (int i = 0; i < 4; i++) k[i] = code_at(rec, lt * E + e + i, bits);
                 }

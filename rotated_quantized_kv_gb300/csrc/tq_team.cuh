@@ -162,16 +162,23 @@ __device__ __forceinline__ uint32_t record_word(const uint8_t *cw, int bits, int
     return x;
 }
 
+// Whether a record of rk bytes is one of whole 32-bit words: records of d = 16 at an odd
+// width are not, nor one of even width behind an odd number of 2-byte units (an odd capacity
+// of a head of odd width); all other head dims have records of a multiple of four bytes.
+template <int D>
+__device__ __forceinline__ bool whole_words(const uint8_t *rec, int rk) {
+    return D > 16 || (rk % 4 == 0 && (reinterpret_cast<uintptr_t>(rec) & 3u) == 0);
+}
+
 // Store the d*bits/8-byte record built from the code bytes: each team lane
-// assembles whole 32-bit words (coalesced 4-byte stores); records of d = 16 at
-// an odd width in 2-byte halves.
+// assembles whole 32-bit words (coalesced 4-byte stores), or 2-byte halves.
 template <int D>
 __device__ __forceinline__ void store_record(const uint8_t *cw, int bits, uint8_t *dst, int lt) {
     constexpr int T = Team<D>::T;
     const int rk = D * bits / 8;
-    if (rk % 4 == 0) {
+    if (whole_words<D>(dst, rk)) {
         for (int c = lt; c < rk / 4; c += T) reinterpret_cast<uint32_t *>(dst)[c] = record_word(cw, bits, D, c);
-    } else {  // d = 16 and an odd width: 2-byte halves
+    } else {
         for (int c = lt; c < rk / 2; c += T) {
             const uint32_t w = record_word(cw, bits, D, c >> 1);
             reinterpret_cast<uint16_t *>(dst)[c] = static_cast<uint16_t>((c & 1) ? (w >> 16) : (w & 0xFFFFu));
@@ -243,9 +250,9 @@ __device__ __forceinline__ void store_fields(const uint32_t (&k)[4], int bits, u
     }
     if (!store) return;
     const int rk = D * bits / 8;
-    if (rk % 4 == 0) {
+    if (whole_words<D>(dst, rk)) {
         if (lt < rk / 4) reinterpret_cast<uint32_t *>(dst)[lt] = x;
-    } else {  // d = 16 and an odd width: 2-byte halves
+    } else {
         if (lt < (rk + 2) / 4) reinterpret_cast<uint16_t *>(dst)[2 * lt] = static_cast<uint16_t>(x);
         if (lt < rk / 4) reinterpret_cast<uint16_t *>(dst)[2 * lt + 1] = static_cast<uint16_t>(x >> 16);
     }
