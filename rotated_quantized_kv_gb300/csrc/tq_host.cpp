@@ -454,8 +454,10 @@ bool rows_values(RowsParams &p, int bits, int law) {
 // its thresholds (the caller then takes another kernel).
 cudaError_t launch_rows(const CompressParams &c, const tq_segment_layout *layout, const uint32_t *sign_bits, int d,
                         cudaStream_t s) {
-    // head_dim 64: token pairs starting at even positions (whole 16-byte stores)
-    if (d != kD && d != 2 * kD && d != 4 * kD && !(d == kD / 2 && c.t_begin % 2 == 0)) return cudaErrorNotSupported;
+    // head_dim 64: token pairs starting at even positions of heads that begin at a multiple of 16
+    // bytes, as behind an even capacity (whole 16-byte stores)
+    if (d != kD && d != 2 * kD && d != 4 * kD && !(d == kD / 2 && c.t_begin % 2 == 0 && c.capacity % 2 == 0))
+        return cudaErrorNotSupported;
     bool in_sel[kMaxH] = {};
     for (int i = 0; i < c.n_sel; ++i) in_sel[c.sel[i]] = true;
     for (int h = 0; h < c.H; ++h) {

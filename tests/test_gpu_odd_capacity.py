@@ -50,3 +50,26 @@ def test_16_dims(tq, cap, widths):
         ref = tq.tq_dequantize(want, 0, n, rot, rotated=use is None, original=use is not None)
         for x, y in zip(got, ref[2:] if use is not None else ref[:2]):
             assert torch.equal(bits(x), bits(y))
+
+
+# 64 dims: records of 8 b bytes, two of which are stored at once where 16-byte boundaries allow
+@pytest.mark.parametrize("cap", [33, 47])
+def test_64_dims(tq, cap):
+    d, B, H, n = 64, 3, 5, 30
+    widths = ([1, 2, 8, 3, 4], [3, 2, 5, 4, 7])
+    g = gen(cap)
+    K, V = (randn(g, B, H, n, d, dtype=torch.float16) for _ in range(2))
+    rot = tq.tq_make_rotation(d, 3)
+    make = lambda c: base.filled_segment(tq, B, H, d, c, *widths)  # noqa: E731
+    want, written, compressed = make(48), make(cap), make(cap)
+    tq.tq_compress(want, rot, K, V, 0)
+    tq.tq_compress(compressed, rot, K, V, 0)
+    tq.tq_append(written, rot, K, V, torch.zeros(B, dtype=torch.int32, device=DEV))
+    same(compressed, want, n)
+    same(written, want, n)
+    ref = tq.tq_dequantize(want, 0, n, rot, rotated=False, original=True)[2:]
+    for m in (n, 700):  # small and large reads (rows behind the capacity are not read)
+        zero = torch.zeros(B, dtype=torch.int32, device=DEV)
+        got = tq.tq_read(written, rot, zero, m, n_read=zero + n, dtype=torch.float32)
+        for x, y in zip(got, ref):
+            assert torch.equal(bits(x[:, :, :n].contiguous()), bits(y)) and not x[:, :, n:].any()
