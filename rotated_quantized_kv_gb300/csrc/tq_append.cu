@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kAppThreads) append_team_kernel(const __grid_c
         const int h = split_index(r, p.H), j = split_index(r, p.rows.n_max), b = split_index(r, p.B), kv = static_cast<int>(r);
         int src = 0, pos = 0;
         const bool valid = f < n && map_row(p.rows, b, j, p.seg.capacity, src, pos);
+        if (!__any_sync(0xffffffffu, valid)) continue;  // (n_max may be far above the sequences' counts)
         float a[E];
         if (valid) {
             const int64_t *st = kv ? p.vs : p.ks;
@@ -194,7 +195,7 @@ cudaError_t append_team(const AppendParams &p, cudaStream_t s) {
 constexpr long long kRowsVectors = 12288;
 
 bool rows_fit(const AppendParams &p) {
-    if (p.d != kD || 2LL * p.B * p.H * p.rows.n_max < kRowsVectors) return false;
+    if (p.d != kD || 2LL * p.B * p.H * p.rows.n_max < kRowsVectors || !blocks_fit(p.B, p.H, p.rows.n_max, 1)) return false;
     if (p.seg.kblock >> 32 || p.seg.vblock >> 32) return false;
     if ((reinterpret_cast<uintptr_t>(p.K) | reinterpret_cast<uintptr_t>(p.V)) & 15u) return false;
     for (int i = 0; i < 3; i++)

@@ -182,7 +182,6 @@ cudaError_t append_rows_launch(const AppendRowsParams &p, bool beside, cudaStrea
                                                static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     const long long blocks = (static_cast<long long>((p.r.T + 31) / 32) * p.r.n_heads * p.r.B + kWarps - 1) / kWarps;
-    if (blocks * kWarps > 0x7fffffff) return cudaErrorNotSupported;
     const long long grid = std::min<long long>(blocks, static_cast<long long>(current_sm_count()) * 3);
     return launch_beside(append_rows_kernel<BITS, VAL>, static_cast<unsigned>(grid), kThreads, smem, s, beside, p);
 }

@@ -8,6 +8,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "tq_row_map.cuh"
 #include "tq_serve.h"
 #include "tq_team.cuh"
 
@@ -63,6 +64,7 @@ __global__ void __launch_bounds__(kReadThreads) read_team_kernel(const __grid_co
         const int kv = kv0 + static_cast<int>(r);
         int pos = 0;
         const bool valid = f < n && read_row(p.rows, b, j, p.seg.capacity, pos);
+        if (!__any_sync(0xffffffffu, valid)) continue;  // (n_max may be far above the sequences' counts)
         float a[E];
         if (valid) {
             const int bits = kv ? p.seg.vbits[h] : p.seg.kbits[h];
@@ -243,7 +245,9 @@ cudaError_t launch_read(const ReadParams &params, int dtype, cudaStream_t s) {
     p.vec = ((reinterpret_cast<uintptr_t>(p.K) | reinterpret_cast<uintptr_t>(p.V)) & align) == 0;
     for (int i = 0; i < 3; i++) p.vec &= (!p.K || p.ks[i] % 4 == 0) && (!p.V || p.vs[i] % 4 == 0);
     const long long vec = ((p.K ? 1LL : 0) + (p.V ? 1 : 0)) * p.B * p.H * p.rows.n_max;
-    if (!p.seg.fp16 && (p.d == kD || p.d == 64) && vec * p.d >= kRowsVectors * kD && vec < (1LL << 34) && odd_levels(p)) return read_rows(p, dtype, s);
+    if (!p.seg.fp16 && (p.d == kD || p.d == 64) && vec * p.d >= kRowsVectors * kD &&
+        blocks_fit(p.B, p.H, p.rows.n_max, kD / p.d) && odd_levels(p))
+        return read_rows(p, dtype, s);
     switch (dtype) {
         case TQ_DTYPE_F16: return read_typed<__half>(p, s);
         case TQ_DTYPE_BF16: return read_typed<__nv_bfloat16>(p, s);

@@ -292,7 +292,6 @@ cudaError_t read_rows_launch(const ReadRowsParams &p, bool beside, cudaStream_t 
                                                static_cast<int>(read_smem_bytes<BITS, VAL>(TQ_DTYPE_F32)));
     if (e != cudaSuccess) return e;
     const long long blocks = (static_cast<long long>((p.rows.n_max + 32 * NP - 1) / (32 * NP)) * p.n_heads * p.B + kWarps - 1) / kWarps;
-    if (blocks * kWarps > 0x7fffffff) return cudaErrorNotSupported;
     const long long grid = std::min<long long>(blocks, static_cast<long long>(current_sm_count()) * 3);
     return launch_beside(read_rows_kernel<BITS, VAL, NP>, static_cast<unsigned>(grid), kThreads, smem, s, beside, p);
 }

@@ -23,6 +23,12 @@ cudaError_t launch_beside(void (*kernel)(P), unsigned grid, int threads, size_t 
     return cudaLaunchKernelEx(&c, kernel, p);
 }
 
+// Whether the kernels that take 32 threads' rows of `per` vectors each as a block can count
+// their blocks, and the rows, in 32 bits (with a grid's warps to spare).
+inline bool blocks_fit(int B, int H, int n_max, int per) {
+    return n_max <= 1 << 30 && (static_cast<long long>(n_max) + 32 * per - 1) / (32 * per) * H * B <= 1 << 30;
+}
+
 // Source row and target position of row j of sequence b; false: not written.
 __device__ __forceinline__ bool map_row(const RowMap &m, int b, int j, int capacity, int &src, int &pos) {
     const int n = m.n_rows ? min(m.n_rows[b], m.n_max) : m.n_max;

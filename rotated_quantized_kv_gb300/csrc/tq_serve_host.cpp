@@ -320,7 +320,7 @@ tq_status tq_append(const tq_segment *dst, const tq_rotation *rot, const tq_rope
     p.rows.n_rows = n_new;
     p.rows.index = index;
     p.rows.index_stride = index_stride_b;
-    p.rows.n_max = n_max;
+    p.rows.n_max = index ? n_max : std::min(n_max, n_source);  // (row j is source row j)
     p.rows.n_source = n_source;
     if (rope) {
         p.rope = rope_view(rope);
