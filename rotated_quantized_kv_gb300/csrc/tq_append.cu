@@ -189,13 +189,22 @@ cudaError_t append_team(const AppendParams &p, cudaStream_t s) {
 
 // Head_dim 128 and many rows: one thread per vector, a launch per width
 // (tq_append_rows.cuh).  Small writes take the team kernel: one launch, 32 lanes a
-// vector, no cold start of 2000 straight instructions.  One sequence of 8 heads, 4-bit
-// codes, keys rotated, team / rows: 64 tokens 4.0 / 10.9 us, 512 7.2 / 10.9, 768 (12288
-// vectors) 10.2 / 10.3, 1024 13.8 / 10.5, 4096 42.1 / 14.1.
-constexpr long long kRowsVectors = 12288;
+// vector, no cold start of 2000 straight instructions.  So the rows that make up for the
+// launches grow with their number.  One sequence of 8 heads, keys rotated, team / rows, us:
+//   tokens               512         768         1024        1536        2048        4096        8192
+//   1 + 1 widths      7.5 / 10.2  10.3 / 10.2  13.3 / 10.4  17.8 / 10.6  23.5 / 11.2  43.2 / 18.4  87.6 / 26.9
+//   2 + 2             7.6 / 13.9  10.5 / 14.1  13.4 / 14.1  18.0 / 14.7  23.6 / 15.0  43.5 / 20.8  87.9 / 33.4
+//   4 + 4             8.0 / 18.7  10.8 / 19.0  13.9 / 19.6  18.5 / 19.8  24.2 / 20.1  44.5 / 26.8  89.6 / 40.9
+//   8 + 8             9.2 / 37.3  12.0 / 37.5  15.2 / 38.5  20.0 / 39.1  25.9 / 40.4  47.1 / 42.7  94.2 / 61.3
+// (16 vectors a token: they cross at about 12300, 17300, 26000 and 59000 vectors)
+constexpr long long rows_vectors(int launches) { return 5700 + 3300LL * launches; }
 
 bool rows_fit(const AppendParams &p) {
-    if (p.d != kD || 2LL * p.B * p.H * p.rows.n_max < kRowsVectors || !blocks_fit(p.B, p.H, p.rows.n_max, 1)) return false;
+    uint32_t kwidths = 0;
+    for (int h = 0; h < p.H; h++) kwidths |= 1u << p.seg.kbits[h];
+    const int launches = __builtin_popcount(kwidths) + __builtin_popcount(p.vwidths);
+    if (p.d != kD || 2LL * p.B * p.H * p.rows.n_max < rows_vectors(launches) || !blocks_fit(p.B, p.H, p.rows.n_max, 1))
+        return false;
     if (p.seg.kblock >> 32 || p.seg.vblock >> 32) return false;
     if ((reinterpret_cast<uintptr_t>(p.K) | reinterpret_cast<uintptr_t>(p.V)) & 15u) return false;
     for (int i = 0; i < 3; i++)

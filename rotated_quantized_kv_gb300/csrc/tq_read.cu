@@ -153,10 +153,14 @@ cudaError_t read_team(const ReadParams &p, cudaStream_t s) {
 
 // Head_dim 128 or 64 and many rows: 128 coordinates a thread, a launch per width
 // (tq_read_rows.cuh).  Small reads take the team kernel: one launch, up to 32 lanes a vector.
-// One sequence of 8 heads, 3-bit codes, team / rows: 64 tokens 3.0 / 5.9 us, 512 (8192
-// vectors) 5.5 / 6.1, 1024 8.9 / 6.3, 4096 27.0 / 11.1; head_dim 64, K5V2: 512 tokens 3.7 / 5.4,
-// 1024 5.4 / 5.7, 1536 7.2 / 5.8, 4096 14.9 / 7.0.  Counted in vectors of 128 (two of 64 make one).
-constexpr long long kRowsVectors = 9216;
+// One sequence of 8 heads, team / rows, us (head_dim 128; at 64 twice the tokens take about the same):
+//   tokens               512         768         1024        1536        2048        4096        8192
+//   1 + 1 widths      5.4 /  6.0   7.0 /  6.0   8.7 /  6.1  11.5 /  6.9  14.6 /  7.3  26.3 / 10.8  52.9 / 17.2
+//   2 + 2             5.4 /  8.1   7.1 /  8.1   8.8 /  8.1  11.6 /  9.9  14.7 / 11.0  26.5 / 13.7  53.0 / 19.6
+//   4 + 4             5.7 / 12.7   7.4 / 13.5   9.1 / 13.8  11.9 / 13.9  15.1 / 14.7  26.7 / 17.3  53.5 / 25.2
+//   8 + 8             6.4 / 21.8   8.1 / 22.1   9.8 / 19.9  12.6 / 23.8  15.8 / 25.0  27.5 / 30.6  53.9 / 36.7
+// Counted in vectors of 128 (two of 64 make one): 16 a token here.
+constexpr long long rows_vectors(int launches) { return 1600 + 3800LL * launches; }
 
 // Whether every value codebook in use is odd (the Gaussian one is, by construction).
 bool odd_levels(const ReadParams &p) {
@@ -245,7 +249,10 @@ cudaError_t launch_read(const ReadParams &params, int dtype, cudaStream_t s) {
     p.vec = ((reinterpret_cast<uintptr_t>(p.K) | reinterpret_cast<uintptr_t>(p.V)) & align) == 0;
     for (int i = 0; i < 3; i++) p.vec &= (!p.K || p.ks[i] % 4 == 0) && (!p.V || p.vs[i] % 4 == 0);
     const long long vec = ((p.K ? 1LL : 0) + (p.V ? 1 : 0)) * p.B * p.H * p.rows.n_max;
-    if (!p.seg.fp16 && (p.d == kD || p.d == 64) && vec * p.d >= kRowsVectors * kD &&
+    uint32_t kwidths = 0;
+    for (int h = 0; h < p.H; h++) kwidths |= 1u << p.seg.kbits[h];
+    const int launches = (p.K ? __builtin_popcount(kwidths) : 0) + (p.V ? __builtin_popcount(p.vwidths) : 0);
+    if (!p.seg.fp16 && (p.d == kD || p.d == 64) && vec * p.d >= rows_vectors(launches) * kD &&
         blocks_fit(p.B, p.H, p.rows.n_max, kD / p.d) && odd_levels(p))
         return read_rows(p, dtype, s);
     switch (dtype) {

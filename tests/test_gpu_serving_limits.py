@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import test_gpu_serving as base
+import test_gpu_serving_loop as loop
 from test_gpu_serving import DEV, bits, gen, randn
 
 pytestmark = pytest.mark.gpu
@@ -57,3 +58,15 @@ def test_append_of_few_rows_of_many(tq, d, kind, gather, n_max):
     torch.cuda.synchronize()
     for name in (base.BUFS if kind == 0 else ("k", "v")):
         assert torch.equal(getattr(seg, name).view(torch.uint8), getattr(want, name).view(torch.uint8)), name
+
+
+# ------------------------------------------------------------------ many rows of many widths
+@pytest.mark.parametrize("B,S,n,gather,layout,r", [(1, 4100, 4100, False, 0, 128), (3, 1500, 1400, True, 1, 64)])
+def test_append_of_many_rows_of_every_width(tq, B, S, n, gather, layout, r):
+    loop.test_large_append_is_compress(tq, 8, loop.MIXED, loop.MIXED[::-1], B, S, n, gather, layout, r, 0, 0)
+
+
+@pytest.mark.parametrize("d,B,n", [(128, 1, 4200), (64, 2, 4200)])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_read_of_many_rows_of_every_width(tq, d, B, n, dtype):
+    loop.test_large_read_is_dequantize(tq, dtype, d, B, n, 0, False, 0, True)
