@@ -721,16 +721,17 @@ def tree_mask(parents: torch.Tensor) -> torch.Tensor:
     """Visibility words of draft trees: parents int [B][N] (or [N]), the index of
     each draft's parent (before it) or -1 at a root; a draft sees itself and its
     ancestors.  int32 [B][N][ceil(N / 32)] (or without B), as tq_tree_attention
-    takes it, on the parents' device."""
+    takes it, on the parents' device.  A parent that is not before its draft is none."""
     p = parents if parents.dim() == 2 else parents[None]
     B, N = p.shape
     W = -(-N // 32)
     i = torch.arange(N, device=p.device)
+    p = torch.where((p >= 0) & (p < i), p.long(), -1)  # (they index below)
     see = torch.zeros(B, N, W * 32, dtype=torch.bool, device=p.device)
     at = i.expand(B, N).long()
     for _ in range(N):  # one generation a step
         see.scatter_(2, at.clamp(min=0)[..., None], (at >= 0)[..., None] | see.gather(2, at.clamp(min=0)[..., None]))
-        at = torch.where(at >= 0, p.long().gather(1, at.clamp(min=0)), at)
+        at = torch.where(at >= 0, p.gather(1, at.clamp(min=0)), at)
     w = (see.view(B, N, W, 32).long() << torch.arange(32, device=p.device)).sum(-1)
     w = torch.where(w >= 1 << 31, w - (1 << 32), w).int()
     return w if parents.dim() == 2 else w[0]

@@ -78,3 +78,14 @@ def test_two_threads_at_once(tq):
     seg.reference()
     assert all(len(bytes(r if isinstance(r, bytes) else r._obj)) == size for r in held)
     assert all(tq.tq_segment.from_buffer_copy(r if isinstance(r, bytes) else r._obj).n_tokens == 7 for r in held)
+
+
+def test_tree_mask_of_parents_that_are_none(tq):
+    """A parent that is not before its draft is none: the draft is a root, and nothing is read out of bounds."""
+    import torch
+    p = torch.tensor([[-1, 0, 2, 7, 100, -5, 5, 2**31 - 1]], dtype=torch.int32)
+    want = torch.tensor([[-1, 0, -1, -1, -1, -1, 5, -1]], dtype=torch.int32)
+    assert torch.equal(tq.tree_mask(p), tq.tree_mask(want))
+    for t in (torch.int8, torch.int16, torch.int32, torch.int64):
+        assert torch.equal(tq.tree_mask(want.to(t)), tq.tree_mask(want))
+    assert tq.tree_mask(want)[0, :, 0].tolist() == [1, 3, 4, 8, 16, 32, 96, 128]
