@@ -572,8 +572,8 @@ tq_status tq_tree_workspace_size(const tq_layer_view *layer, int batch, int n_he
  * operands, binary32 sums, the result rounded to fp16.  All numbers on the device
  * (lengths, mask) may change between replays of a captured call; two calls that
  * may overlap need two workspaces.  QJL heads (key or value), dense rotations and
- * segments with attn_mass return TQ_ERR_UNSUPPORTED, as does the sphere law at
- * head dims other than 128.  No device memory is allocated and nothing is
+ * segments with attn_mass return TQ_ERR_UNSUPPORTED, as do the sphere law at
+ * head dims other than 128 and an n_tokens above 2^31 - 128.  No device memory is allocated and nothing is
  * copied from the host.  tq_decode_error_flag reads the workspace's error flag
  * (a wait for copies or tensor-core work that ran out; cleared by the next call). */
 tq_status tq_tree_attention(const tq_layer_view *layer, int batch, int n_heads, int q_heads, int head_dim,

@@ -156,6 +156,7 @@ tq_status check_tree_view(const tq_layer_view *lv, int B, int H, int Hq, int d, 
         const tq_segment_layout &L = sg.layout;
         if (L.batch != B || L.n_heads != H || L.head_dim != d) return TQ_ERR_ARG;
         if (sg.n_tokens < 0 || sg.n_tokens > L.capacity) return TQ_ERR_SIZE;
+        if (sg.n_tokens > 0x7fffffff - (kTreeTile - 1)) return TQ_ERR_UNSUPPORTED;  // rounded up to tiles in 32 bits
         if (sg.attn_mass) return TQ_ERR_UNSUPPORTED;
         if (sg.kind == TQ_SEG_PACKED) {
             if (any_sketch(L) || sphere_elsewhere(L)) return TQ_ERR_UNSUPPORTED;

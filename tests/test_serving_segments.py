@@ -89,3 +89,20 @@ def test_tree_mask_of_parents_that_are_none(tq):
     for t in (torch.int8, torch.int16, torch.int32, torch.int64):
         assert torch.equal(tq.tree_mask(want.to(t)), tq.tree_mask(want))
     assert tq.tree_mask(want)[0, :, 0].tolist() == [1, 3, 4, 8, 16, 32, 96, 128]
+
+
+@pytest.mark.parametrize("d", [64, 16])
+def test_tree_over_a_segment_at_the_end_of_32_bits(tq, d):
+    """Token counts that rounded up to whole tiles pass 2^31 - 1 are refused; the largest others are counted."""
+    lv = tq.tq_layer_view()
+    lv.rot, lv.n_segments = tq.tq_make_rotation(d, 1), 1
+    for n, ok in ((2**31 - 16, False), (2**31 - 127, False), (2**31 - 128, True)):
+        s = tq.tq_segment()
+        s.kind, s.n_tokens, s.layout = tq.TQ_SEG_PACKED, n, tq.make_layout(1, 1, d, 2**31 - 16, 1, 1)
+        lv.seg[0] = s
+        if ok:
+            assert tq.tq_tree_workspace_size(lv, 1, 1, 1, 1, d) > 0
+        else:
+            with pytest.raises(tq.TQError) as e:
+                tq.tq_tree_workspace_size(lv, 1, 1, 1, 1, d)
+            assert e.value.status == -2
