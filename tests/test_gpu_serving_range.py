@@ -158,3 +158,26 @@ def test_weights_round_no_further_than_the_result(tq, d, N, vb):
     # more for the samples' spread (rows of one cache share its tokens)
     bound = 1.1 * math.hypot(float(best), level_error(tq, vb)) + float(2 * reach.max()) * 2.0**-19
     assert float((out.double() - want).norm() / want.norm()) <= bound
+
+
+@pytest.mark.parametrize("d,N,widths", [(64, 5, (3, 4)), (128, 5, (3, 4)), (128, 16, (8, 8)), (128, 8, (5, 6))])
+@pytest.mark.parametrize("polls", [0, 1, 2, 3, 5, 8, 16, 64])
+def test_a_wait_that_ran_out_is_reported(tq, d, N, widths, polls):
+    """Few polls a wait: some roles go on and others give up.  Either the flag says so or the output is whole."""
+    q, k, v, parts, lens, rng = base.tree_case(tq, d, 2, 4, 2, N, [(widths, 1500), ((8, 1), 300), ("fp16", 200)], False, seed=N)
+    want = base.run_tree(tq, q, k, v, parts)
+    lv = tq.layer_view(tq.tq_make_rotation(d, 21), parts)
+    ws = torch.empty(tq.tq_tree_workspace_size(lv, 2, 2, 8, N, d), dtype=torch.uint8, device=DEV)
+    flags = 0
+    for _ in range(4):
+        out = torch.zeros_like(want)
+        try:
+            tq.tq_set_decode_wait_polls(polls)
+            tq.tq_tree_attention(lv, q, k, v, out, ws)
+            flag = tq.tq_decode_error_flag(ws)
+        finally:
+            tq.tq_set_decode_wait_polls(tq.TQ_WAIT_POLLS_DEFAULT)
+        flags += flag != 0
+        assert flag != 0 or torch.equal(base.bits(out), base.bits(want))
+    assert flags == 4 or polls > 0
+    assert torch.equal(base.bits(base.run_tree(tq, q, k, v, parts, ws=ws)), base.bits(want))
