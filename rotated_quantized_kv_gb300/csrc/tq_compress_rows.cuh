@@ -197,206 +197,206 @@ __device__ __forceinline__ void rows_vector(const uint8_t *row, const uint32_t *
                                             const uint2 *vtab, bool bucket4_ok, int lane, int sl,
                                             uint32_t (&w)[4 * BITS], float &scale, float &scale_b) {
     constexpr int TPW = 32 * NP / NH;
-            // ---- load, input sign flip on the fp16 bits, widen: chunks c and
-            // c + 8 (coordinates 8c.. and 64 + 8c..) are permuted into half2 pairs
-            // (m, m + 64) that widen straight into the register pairs
-            float2 a[64];
-    #pragma unroll
-            for (int c = 0; c < 8; c++) {
-                const uint4 v0 = *reinterpret_cast<const uint4 *>(row + 16 * (c ^ (lane & 7)));
-                const uint4 v1 = *reinterpret_cast<const uint4 *>(row + 16 * ((c + 8) ^ (lane & 7)));
-                const uint4 m0 = *reinterpret_cast<const uint4 *>(im + 4 * c);
-                const uint4 m1 = *reinterpret_cast<const uint4 *>(im + 4 * (c + 8));
-                const uint32_t w0[4] = {v0.x ^ m0.x, v0.y ^ m0.y, v0.z ^ m0.z, v0.w ^ m0.w};
-                const uint32_t w1[4] = {v1.x ^ m1.x, v1.y ^ m1.y, v1.z ^ m1.z, v1.w ^ m1.w};
-    #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int i = 8 * c + 2 * e;  // pairs (i, i + 64) and (i + 1, i + 65)
-                    const uint32_t lo = prmt(w0[e], w1[e], 0x5410u), hi = prmt(w0[e], w1[e], 0x7632u);
-                    a[i] = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
-                    a[i + 1] = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-                }
-            }
-            __syncwarp();  // every lane has read its row: the buffer may be restaged
+    // ---- load, input sign flip on the fp16 bits, widen: chunks c and
+    // c + 8 (coordinates 8c.. and 64 + 8c..) are permuted into half2 pairs
+    // (m, m + 64) that widen straight into the register pairs
+    float2 a[64];
+#pragma unroll
+    for (int c = 0; c < 8; c++) {
+        const uint4 v0 = *reinterpret_cast<const uint4 *>(row + 16 * (c ^ (lane & 7)));
+        const uint4 v1 = *reinterpret_cast<const uint4 *>(row + 16 * ((c + 8) ^ (lane & 7)));
+        const uint4 m0 = *reinterpret_cast<const uint4 *>(im + 4 * c);
+        const uint4 m1 = *reinterpret_cast<const uint4 *>(im + 4 * (c + 8));
+        const uint32_t w0[4] = {v0.x ^ m0.x, v0.y ^ m0.y, v0.z ^ m0.z, v0.w ^ m0.w};
+        const uint32_t w1[4] = {v1.x ^ m1.x, v1.y ^ m1.y, v1.z ^ m1.z, v1.w ^ m1.w};
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const int i = 8 * c + 2 * e;  // pairs (i, i + 64) and (i + 1, i + 65)
+            const uint32_t lo = prmt(w0[e], w1[e], 0x5410u), hi = prmt(w0[e], w1[e], 0x7632u);
+            a[i] = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+            a[i + 1] = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+        }
+    }
+    __syncwarp();  // every lane has read its row: the buffer may be restaged
 
-            // ---- butterflies h = 1..32 on register pairs (packed), then h = 64
-    #pragma unroll
-            for (int hh = 1; hh < 64; hh <<= 1) {
-    #pragma unroll
-                for (int m = 0; m < 64; m++) {
-                    if ((m & hh) == 0) {
-                        const float2 u = a[m], v = a[m + hh];
-                        a[m] = fadd2(u, v);
-                        a[m + hh] = fsub2(u, v);
-                    }
-                }
+    // ---- butterflies h = 1..32 on register pairs (packed), then h = 64
+#pragma unroll
+    for (int hh = 1; hh < 64; hh <<= 1) {
+#pragma unroll
+        for (int m = 0; m < 64; m++) {
+            if ((m & hh) == 0) {
+                const float2 u = a[m], v = a[m + hh];
+                a[m] = fadd2(u, v);
+                a[m + hh] = fsub2(u, v);
             }
-            if constexpr (NP == 1) {
-    #pragma unroll
-                for (int m = 0; m < 64; m++) {
-                    const float u = a[m].x, v = a[m].y;
-                    a[m].x = __fadd_rn(u, v);
-                    a[m].y = __fsub_rn(u, v);
-                }
-            }
-            // h = 128 (256): the same register of slice sl ^ x, x = 1 (2), from
-            // lane ^ x TPW; fma(+-1, own, other) rounds the exact sum once
-    #pragma unroll
-            for (int x = 1; x < NH; x <<= 1) {
-                const float sg = (sl & x) ? -1.0f : 1.0f;
-    #pragma unroll
-                for (int m = 0; m < 64; m++) {
-                    const float2 o = make_float2(__shfl_xor_sync(0xffffffffu, a[m].x, x * TPW),
-                                                 __shfl_xor_sync(0xffffffffu, a[m].y, x * TPW));
-                    a[m] = ffma2(a[m], make_float2(sg, sg), o);
-                }
-            }
-            // output sign flip and binary32(1/sqrt(d)): one rounded multiply each
-            // (op[m] = the scales of coordinates m and m + 64 of the slice)
-    #pragma unroll
+        }
+    }
+    if constexpr (NP == 1) {
+#pragma unroll
+        for (int m = 0; m < 64; m++) {
+            const float u = a[m].x, v = a[m].y;
+            a[m].x = __fadd_rn(u, v);
+            a[m].y = __fsub_rn(u, v);
+        }
+    }
+    // h = 128 (256): the same register of slice sl ^ x, x = 1 (2), from
+    // lane ^ x TPW; fma(+-1, own, other) rounds the exact sum once
+#pragma unroll
+    for (int x = 1; x < NH; x <<= 1) {
+        const float sg = (sl & x) ? -1.0f : 1.0f;
+#pragma unroll
+        for (int m = 0; m < 64; m++) {
+            const float2 o = make_float2(__shfl_xor_sync(0xffffffffu, a[m].x, x * TPW),
+                                         __shfl_xor_sync(0xffffffffu, a[m].y, x * TPW));
+            a[m] = ffma2(a[m], make_float2(sg, sg), o);
+        }
+    }
+    // output sign flip and binary32(1/sqrt(d)): one rounded multiply each
+    // (op[m] = the scales of coordinates m and m + 64 of the slice)
+#pragma unroll
+    for (int m = 0; m < 64; m += 2) {
+        const float4 sc = *reinterpret_cast<const float4 *>(op + 2 * m);
+        a[m] = fmul2(a[m], make_float2(sc.x, sc.y));
+        a[m + 1] = fmul2(a[m + 1], make_float2(sc.z, sc.w));
+    }
+
+#pragma unroll
+    for (int j = 0; j < 4 * BITS; j++) w[j] = 0u;
+    scale_b = 0.0f;
+    if constexpr (!VAL) {
+        // ---- keys: m = max |y|, v = y * binary32(1/m), u = round(v + 1) 2^(b-1),
+        // code = clamp(floor(u), 0, 2^b - 1)
+        float mx = 0.0f, mxb = 0.0f;
+        if constexpr (NP == 2) {
+#pragma unroll
             for (int m = 0; m < 64; m += 2) {
-                const float4 sc = *reinterpret_cast<const float4 *>(op + 2 * m);
-                a[m] = fmul2(a[m], make_float2(sc.x, sc.y));
-                a[m + 1] = fmul2(a[m + 1], make_float2(sc.z, sc.w));
+                mx = fmax3(mx, fabsf(a[m].x), fabsf(a[m + 1].x));
+                mxb = fmax3(mxb, fabsf(a[m].y), fabsf(a[m + 1].y));
             }
-
-    #pragma unroll
-            for (int j = 0; j < 4 * BITS; j++) w[j] = 0u;
-            scale_b = 0.0f;
-            if constexpr (!VAL) {
-                // ---- keys: m = max |y|, v = y * binary32(1/m), u = round(v + 1) 2^(b-1),
-                // code = clamp(floor(u), 0, 2^b - 1)
-                float mx = 0.0f, mxb = 0.0f;
-                if constexpr (NP == 2) {
-    #pragma unroll
-                    for (int m = 0; m < 64; m += 2) {
-                        mx = fmax3(mx, fabsf(a[m].x), fabsf(a[m + 1].x));
-                        mxb = fmax3(mxb, fabsf(a[m].y), fabsf(a[m + 1].y));
-                    }
-                } else {
-    #pragma unroll
-                    for (int m = 0; m < 64; m++) mx = fmax3(mx, fabsf(a[m].x), fabsf(a[m].y));
-                }
-    #pragma unroll
-                for (int x = 1; x < NH; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x * TPW));
-                scale = mx;
-                scale_b = mxb;
-                const float r = mx > 0.0f ? __frcp_rn(mx) : 0.0f;
-                const float rb = NP == 2 ? (mxb > 0.0f ? __frcp_rn(mxb) : 0.0f) : r;
-                constexpr float hc = static_cast<float>(1 << (BITS - 1));
-                // v = y r lies in [-1, 1]: r = binary32(1/m) is within 2^-24 of 1/m
-                // and |y| <= m, so |y r| <= 1 + 2^-24 rounds to at most 1.  Hence
-                // u = round(v + 1) 2^(b-1) >= 0 and only the top clamp can act (at
-                // v = 1).  floor(u): the round-down of u + 2^23 + 512 has the exponent
-                // of 2^23, so its bit pattern is kLo + floor(u).
-                constexpr float kMagic = 8388608.0f + 512.0f;
-                constexpr uint32_t kHi = kKeyLo + (1u << BITS) - 1u;
-    #pragma unroll
-                for (int m = 0; m < 64; m++) {
-                    const float2 v = fmul2(a[m], make_float2(r, rb));
-                    // fma(v, 2^(b-1), 2^(b-1)) is round(v + 1) 2^(b-1): scaling by a
-                    // power of two commutes with the rounding
-                    const float2 u = ffma2(v, make_float2(hc, hc), make_float2(hc, hc));
-                    const float2 f = fadd2_rm(u, make_float2(kMagic, kMagic));
-                    // kLo + code, placed as is: the words take off the kLo parts below
-                    put<BITS>(w, m, min(__float_as_uint(f.x), kHi));
-                    put<BITS>(w, m + 64, min(__float_as_uint(f.y), kHi));
-                }
-    #pragma unroll
-                for (int j = 0; j < 4 * BITS; j++) w[j] -= key_offset_word<BITS>(j);
-            } else {
-                // ---- values: sigma = sqrt(pairwise-tree sum of y^2 in index order / d),
-                // u = y * binary32(1/sigma), code = #{k : thr_k < u}
-                // first level scalar: the compiler fuses a packed multiply into a
-                // packed add (one rounding instead of two), which the scalar _rn
-                // intrinsics rule out; the later levels are additions only
-                float2 s[32];
-    #pragma unroll
-                for (int j = 0; j < 32; j++) {
-                    s[j].x = __fadd_rn(__fmul_rn(a[2 * j].x, a[2 * j].x), __fmul_rn(a[2 * j + 1].x, a[2 * j + 1].x));
-                    s[j].y = __fadd_rn(__fmul_rn(a[2 * j].y, a[2 * j].y), __fmul_rn(a[2 * j + 1].y, a[2 * j + 1].y));
-                }
-    #pragma unroll
-                for (int len = 32; len > 1; len >>= 1) {
-    #pragma unroll
-                    for (int j = 0; j < len / 2; j++) s[j] = fadd2(s[2 * j], s[2 * j + 1]);
-                }
-                // NP = 2: the two halves' trees are the two tokens' sums (no root join)
-                float tot = NP == 2 ? s[0].x : __fadd_rn(s[0].x, s[0].y);
-                // blocks of 256 (512) coordinates: slices (2i, 2i + 1), then (4i, 4i + 2)
-    #pragma unroll
-                for (int x = 1; x < NH; x <<= 1) tot = __fadd_rn(tot, __shfl_xor_sync(0xffffffffu, tot, x * TPW));
-                constexpr float inv_d = 1.0f / (kD * NH / NP);  // exact (a power of two)
-                const float sigma = __fsqrt_rn(__fmul_rn(tot, inv_d));
-                const float sigma_b = NP == 2 ? __fsqrt_rn(__fmul_rn(s[0].y, inv_d)) : sigma;
-                scale = sigma;
-                scale_b = sigma_b;
-                const float r = sigma > 0.0f ? __frcp_rn(sigma) : 0.0f;
-                const float rb = NP == 2 ? (sigma_b > 0.0f ? __frcp_rn(sigma_b) : 0.0f) : r;
-                constexpr int NT = (1 << BITS) - 1;
-                if constexpr (BITS <= 3) {
-                    // #{k : thr_k < u} from the bucket of u's top ten bits (sign,
-                    // exponent, one mantissa bit): every u in a bucket exceeds the
-                    // same k_base thresholds, and at most one threshold t_c lies in
-                    // the bucket (the host checks), so the count is k_base + [t_c < u]
-                    const uint32_t tab = static_cast<uint32_t>(__cvta_generic_to_shared(vtab));
-    #pragma unroll
-                    for (int m = 0; m < 64; m++) {
-                        const float2 u = fmul2(a[m], make_float2(r, rb));
-                        const uint2 e0 = lds64(tab + ((__float_as_uint(u.x) >> 22) << 3));
-                        const uint2 e1 = lds64(tab + ((__float_as_uint(u.y) >> 22) << 3));
-                        put<BITS>(w, m, e0.y + (__uint_as_float(e0.x) < u.x ? 1u : 0u));
-                        put<BITS>(w, m + 64, e1.y + (__uint_as_float(e1.x) < u.y ? 1u : 0u));
-                    }
-                } else if constexpr (BITS == 4) {
-                  if (bucket4_ok) {
-                    const uint32_t tab = static_cast<uint32_t>(__cvta_generic_to_shared(vtab));
-    #pragma unroll
-                    for (int m = 0; m < 64; m++) {
-                        const float2 u = fmul2(a[m], make_float2(r, rb));
-                        put<BITS>(w, m, bucket4_code(tab, u.x));
-                        put<BITS>(w, m + 64, bucket4_code(tab, u.y));
-                    }
-                  } else {
-                    float th[NT];
-    #pragma unroll
-                    for (int j = 0; j < NT; j++) th[j] = thr[j];
-    #pragma unroll
-                    for (int m = 0; m < 64; m++) {
-                        const float2 u = fmul2(a[m], make_float2(r, rb));
-                        uint32_t k0 = 0, k1 = 0;
-    #pragma unroll
-                        for (int st = 1 << (BITS - 1); st >= 1; st >>= 1) {
-                            // threshold k + st - 1 for the current prefix k: a select
-                            // tree over the candidates of this level
-                            float t0 = th[st - 1], t1 = th[st - 1];
-    #pragma unroll
-                            for (int c = 2 * st; c < (1 << BITS); c += 2 * st) {
-                                t0 = (k0 >= static_cast<uint32_t>(c)) ? th[c + st - 1] : t0;
-                                t1 = (k1 >= static_cast<uint32_t>(c)) ? th[c + st - 1] : t1;
-                            }
-                            k0 += (t0 < u.x) ? st : 0;
-                            k1 += (t1 < u.y) ? st : 0;
-                        }
-                        put<BITS>(w, m, k0);
-                        put<BITS>(w, m + 64, k1);
-                    }
-                  }
-                } else {
-    #pragma unroll
-                    for (int m = 0; m < 64; m++) {
-                        const float2 u = fmul2(a[m], make_float2(r, rb));
-                        uint32_t k0 = 0, k1 = 0;
-    #pragma unroll
-                        for (int st = 1 << (BITS - 1); st >= 1; st >>= 1) {
-                            if (thr[k0 + st - 1] < u.x) k0 += st;
-                            if (thr[k1 + st - 1] < u.y) k1 += st;
-                        }
-                        put<BITS>(w, m, k0);
-                        put<BITS>(w, m + 64, k1);
-                    }
-                }
+        } else {
+#pragma unroll
+            for (int m = 0; m < 64; m++) mx = fmax3(mx, fabsf(a[m].x), fabsf(a[m].y));
+        }
+#pragma unroll
+        for (int x = 1; x < NH; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x * TPW));
+        scale = mx;
+        scale_b = mxb;
+        const float r = mx > 0.0f ? __frcp_rn(mx) : 0.0f;
+        const float rb = NP == 2 ? (mxb > 0.0f ? __frcp_rn(mxb) : 0.0f) : r;
+        constexpr float hc = static_cast<float>(1 << (BITS - 1));
+        // v = y r lies in [-1, 1]: r = binary32(1/m) is within 2^-24 of 1/m
+        // and |y| <= m, so |y r| <= 1 + 2^-24 rounds to at most 1.  Hence
+        // u = round(v + 1) 2^(b-1) >= 0 and only the top clamp can act (at
+        // v = 1).  floor(u): the round-down of u + 2^23 + 512 has the exponent
+        // of 2^23, so its bit pattern is kLo + floor(u).
+        constexpr float kMagic = 8388608.0f + 512.0f;
+        constexpr uint32_t kHi = kKeyLo + (1u << BITS) - 1u;
+#pragma unroll
+        for (int m = 0; m < 64; m++) {
+            const float2 v = fmul2(a[m], make_float2(r, rb));
+            // fma(v, 2^(b-1), 2^(b-1)) is round(v + 1) 2^(b-1): scaling by a
+            // power of two commutes with the rounding
+            const float2 u = ffma2(v, make_float2(hc, hc), make_float2(hc, hc));
+            const float2 f = fadd2_rm(u, make_float2(kMagic, kMagic));
+            // kLo + code, placed as is: the words take off the kLo parts below
+            put<BITS>(w, m, min(__float_as_uint(f.x), kHi));
+            put<BITS>(w, m + 64, min(__float_as_uint(f.y), kHi));
+        }
+#pragma unroll
+        for (int j = 0; j < 4 * BITS; j++) w[j] -= key_offset_word<BITS>(j);
+    } else {
+        // ---- values: sigma = sqrt(pairwise-tree sum of y^2 in index order / d),
+        // u = y * binary32(1/sigma), code = #{k : thr_k < u}
+        // first level scalar: the compiler fuses a packed multiply into a
+        // packed add (one rounding instead of two), which the scalar _rn
+        // intrinsics rule out; the later levels are additions only
+        float2 s[32];
+#pragma unroll
+        for (int j = 0; j < 32; j++) {
+            s[j].x = __fadd_rn(__fmul_rn(a[2 * j].x, a[2 * j].x), __fmul_rn(a[2 * j + 1].x, a[2 * j + 1].x));
+            s[j].y = __fadd_rn(__fmul_rn(a[2 * j].y, a[2 * j].y), __fmul_rn(a[2 * j + 1].y, a[2 * j + 1].y));
+        }
+#pragma unroll
+        for (int len = 32; len > 1; len >>= 1) {
+#pragma unroll
+            for (int j = 0; j < len / 2; j++) s[j] = fadd2(s[2 * j], s[2 * j + 1]);
+        }
+        // NP = 2: the two halves' trees are the two tokens' sums (no root join)
+        float tot = NP == 2 ? s[0].x : __fadd_rn(s[0].x, s[0].y);
+        // blocks of 256 (512) coordinates: slices (2i, 2i + 1), then (4i, 4i + 2)
+#pragma unroll
+        for (int x = 1; x < NH; x <<= 1) tot = __fadd_rn(tot, __shfl_xor_sync(0xffffffffu, tot, x * TPW));
+        constexpr float inv_d = 1.0f / (kD * NH / NP);  // exact (a power of two)
+        const float sigma = __fsqrt_rn(__fmul_rn(tot, inv_d));
+        const float sigma_b = NP == 2 ? __fsqrt_rn(__fmul_rn(s[0].y, inv_d)) : sigma;
+        scale = sigma;
+        scale_b = sigma_b;
+        const float r = sigma > 0.0f ? __frcp_rn(sigma) : 0.0f;
+        const float rb = NP == 2 ? (sigma_b > 0.0f ? __frcp_rn(sigma_b) : 0.0f) : r;
+        constexpr int NT = (1 << BITS) - 1;
+        if constexpr (BITS <= 3) {
+            // #{k : thr_k < u} from the bucket of u's top ten bits (sign,
+            // exponent, one mantissa bit): every u in a bucket exceeds the
+            // same k_base thresholds, and at most one threshold t_c lies in
+            // the bucket (the host checks), so the count is k_base + [t_c < u]
+            const uint32_t tab = static_cast<uint32_t>(__cvta_generic_to_shared(vtab));
+#pragma unroll
+            for (int m = 0; m < 64; m++) {
+                const float2 u = fmul2(a[m], make_float2(r, rb));
+                const uint2 e0 = lds64(tab + ((__float_as_uint(u.x) >> 22) << 3));
+                const uint2 e1 = lds64(tab + ((__float_as_uint(u.y) >> 22) << 3));
+                put<BITS>(w, m, e0.y + (__uint_as_float(e0.x) < u.x ? 1u : 0u));
+                put<BITS>(w, m + 64, e1.y + (__uint_as_float(e1.x) < u.y ? 1u : 0u));
             }
+        } else if constexpr (BITS == 4) {
+          if (bucket4_ok) {
+            const uint32_t tab = static_cast<uint32_t>(__cvta_generic_to_shared(vtab));
+#pragma unroll
+            for (int m = 0; m < 64; m++) {
+                const float2 u = fmul2(a[m], make_float2(r, rb));
+                put<BITS>(w, m, bucket4_code(tab, u.x));
+                put<BITS>(w, m + 64, bucket4_code(tab, u.y));
+            }
+          } else {
+            float th[NT];
+#pragma unroll
+            for (int j = 0; j < NT; j++) th[j] = thr[j];
+#pragma unroll
+            for (int m = 0; m < 64; m++) {
+                const float2 u = fmul2(a[m], make_float2(r, rb));
+                uint32_t k0 = 0, k1 = 0;
+#pragma unroll
+                for (int st = 1 << (BITS - 1); st >= 1; st >>= 1) {
+                    // threshold k + st - 1 for the current prefix k: a select
+                    // tree over the candidates of this level
+                    float t0 = th[st - 1], t1 = th[st - 1];
+#pragma unroll
+                    for (int c = 2 * st; c < (1 << BITS); c += 2 * st) {
+                        t0 = (k0 >= static_cast<uint32_t>(c)) ? th[c + st - 1] : t0;
+                        t1 = (k1 >= static_cast<uint32_t>(c)) ? th[c + st - 1] : t1;
+                    }
+                    k0 += (t0 < u.x) ? st : 0;
+                    k1 += (t1 < u.y) ? st : 0;
+                }
+                put<BITS>(w, m, k0);
+                put<BITS>(w, m + 64, k1);
+            }
+          }
+        } else {
+#pragma unroll
+            for (int m = 0; m < 64; m++) {
+                const float2 u = fmul2(a[m], make_float2(r, rb));
+                uint32_t k0 = 0, k1 = 0;
+#pragma unroll
+                for (int st = 1 << (BITS - 1); st >= 1; st >>= 1) {
+                    if (thr[k0 + st - 1] < u.x) k0 += st;
+                    if (thr[k1 + st - 1] < u.y) k1 += st;
+                }
+                put<BITS>(w, m, k0);
+                put<BITS>(w, m + 64, k1);
+            }
+        }
+    }
 }
 
 template <int BITS, bool VAL, int NH, int NP = 1>
