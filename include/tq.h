@@ -566,10 +566,14 @@ tq_status tq_tree_workspace_size(const tq_layer_view *layer, int batch, int n_he
  * over the cached tokens of every segment (as tq_decode_attention; all drafts
  * see all of them) and the drafted tokens that draft i sees.  A draft that sees
  * nothing (an empty cache, an empty mask row) yields zeros.  q_heads: any
- * multiple of n_heads.  The N drafts of the q_heads / n_heads query heads of one KV
- * head share each unpacking of the cache.  Scores and the value sum of packed
- * tokens run in the rotated space; one inverse rotation follows the merge.  fp16
- * operands, binary32 sums, the result rounded to fp16.  All numbers on the device
+ * multiple of n_heads.  The rows of a KV head (N drafts of q_heads / n_heads query heads)
+ * share each unpacking of the cache, 64 at a time (16 at head dims other than 64 and 128,
+ * 8 from 512 on).  Scores and the value sum of packed tokens run in the rotated space; one
+ * inverse rotation follows the merge.  Sums are binary32, the result is rounded to fp16.
+ * At head dims 64 and 128 queries and weights enter with 22 bits (weights relative to the
+ * row's largest weighted value scale, those below 2^-36 of it as zero) and the value levels as
+ * fp16, which adds to the rounding of the result: nothing up to 4 bits, a third at 8; at the
+ * others everything is binary32.  All numbers on the device
  * (lengths, mask) may change between replays of a captured call; two calls that
  * may overlap need two workspaces.  QJL heads (key or value), dense rotations and
  * segments with attn_mass return TQ_ERR_UNSUPPORTED, as do the sphere law at

@@ -42,12 +42,13 @@
 // records and scales (cp.async into a ring); the others learn from a descriptor
 // what a tile is.
 //
-// What bounds it: a tile of 64 rows costs a worker 1.2 us (16 rows: 1.0), where its MMAs
-// take 0.23 us; the 32 warps unpack 128 x 128 codes twice and exponentiate 128 x 64 scores,
-// and the value rows, P and the MMA's operands share shared memory.  The first tile
-// costs about 10 us more (latencies, code that is cold).  Measured, all three kernels: 16 drafts
-// of 4 heads a KV head over 64K tokens of 8 heads K3V3 62 us, 64 drafts over 4 x 32K 282 us,
-// 13 drafts over 16 x 9K at head_dim 64 79 us.
+// What bounds it: a tile costs a worker 1.57 us with 64 rows, 1.28 with 32, 1.04 with 16
+// (head_dim 64: 1.63, 1.14, 0.97), where the tensor pipe is busy for 0.6 us (64 rows); the 32
+// warps unpack 128 x 128 codes twice and exponentiate 128 x 64 scores, and the value rows, P and
+// the MMA's operands share shared memory.  Start and end of the three kernels are some 22 us
+// (64 rows; latencies, code that is cold).  Measured, all three: 16 drafts of 4 heads a KV head
+// over 64K tokens of 8 heads K3V3 67 us, 64 drafts over 4 x 32K 304 us, 13 drafts over 16 x 9K at
+// head_dim 64 80 us.  The weights' lo half is 0.17 us of a tile of 64 rows.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -1321,7 +1322,10 @@ cudaError_t tree_mma(const TreeParams &p, const TreeLevels &lv, cudaStream_t s) 
     RingGeo ring;
     ring.stage = std::max(stage, 128);
     // A second buffer of queries, so that a segment's first tile does not wait for them, where
-    // the ring keeps two stages.
+    // the ring keeps two stages.  (64 rows of head_dim 128: up to 8 bits of key and value.  One
+    // buffer everywhere: 13 drafts over 16 x 9K at head_dim 64 92 us for 85.  Wider records: 32
+    // sequences of 512 tokens, 64 rows, K5V4 92 us, in blocks of 64 rows with two buffers
+    // and one-fp16 weights 89; K8V8 99, in blocks of 32 rows 116.)
     ring.q_log = (C::kRing - C::QBUF) / ring.stage >= 2 ? 1 : 0;
     ring.stages = std::min(kMaxStages, (C::kRing - ring.q_log * C::QBUF) / ring.stage);
     // Two stages at least: the groups of value warps take alternate tiles, and a wait for a stage's

@@ -325,7 +325,7 @@ class SpeculativeCache:
         T.tq_append(self.body[l], self.rot[l], K, V, body_at, **kw)
 
     def prefill(self, l, K, V, n, positions, stream=None):
-        """Prompts of n[b] tokens into the empty cache of layer l: K, V fp16 [B][H][S][d],
+        """Prompts of n[b] <= S tokens into the empty cache of layer l: K, V fp16 [B][H][S][d],
         the keys without their positions (int32 [S] or [B][S])."""
         self._write(l, K, V, self.zero, self.body_first, n, rope=self.rope, positions=positions, stream=stream)
 
@@ -338,12 +338,12 @@ class SpeculativeCache:
         T.tq_tree_attention(self.views[l], q, k, v, out, self.workspace, mask=mask, seg_len=lens, stream=stream)
 
     def commit(self, l, k, v, index, n, stream=None):
-        """The n[b] accepted drafts index[b][:] (int32 [B][N]; a path of the tree from its
+        """The n[b] <= N accepted drafts index[b][:] (int32 [B][N]; a path of the tree from its
         root) behind layer l's tokens: k, v as `attend` left them."""
         self._write(l, k, v, self.length, self.body_at, n, index=index, stream=stream)
 
     def advance(self, n, stream=None):
-        """The lengths after a step or a prefill of n[b] tokens (int32 [B])."""
+        """The lengths after a step or a prefill of n[b] >= 0 tokens (int32 [B]), those that were written."""
         with T.on_stream(stream, self.length.device):
             self.length.add_(n).clamp_(0, self.sinks + self.capacity)
             torch.clamp(self.length, max=self.sinks, out=self.head_len)
