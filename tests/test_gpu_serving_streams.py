@@ -20,7 +20,7 @@ class Behind:
 
     def __enter__(self):
         torch.cuda.synchronize()
-        torch.cuda._sleep(200_000_000)  # about a tenth of a second
+        torch.cuda._sleep(1_000_000_000)  # about half a second
         self.after = torch.cuda.Event()
         self.after.record()
 
@@ -114,3 +114,40 @@ def test_null_handle_is_the_default_stream(tq):
         got = tq.tq_read(seg, None, first, 16, stream=0)
     torch.cuda.synchronize()
     assert all(torch.equal(bits(x), bits(y)) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_captured_calls_that_name_their_stream(tq, raw):
+    """Results that a captured call allocates belong to the graph, whether the stream is current or named."""
+    from rotated_quantized_kv_gb300.model_cache import SpeculativeCache
+    B, H, Hq, d, S, cap = 2, 2, 4, 128, 30, 64
+    g = gen(6)
+    rope = tq.Rope(tq.tq_rope_table(tq.tq_make_rope(d), 100))
+    caches = [SpeculativeCache(1, B, H, Hq, d, cap, rope, 3, 4, sinks=16, drafts=4) for _ in range(2)]
+    K, V = (torch.zeros(B, H, S, d, dtype=torch.float16, device=DEV) for _ in range(2))
+    n, first = torch.zeros(B, dtype=torch.int32, device=DEV), torch.zeros(B, dtype=torch.int32, device=DEV)
+    pos = torch.arange(S, dtype=torch.int32, device=DEV)
+
+    def calls(c, stream):
+        c.length.zero_()
+        c.prefill(0, K, V, n, pos, stream=stream)
+        c.advance(n, stream=stream)
+        return c.read(0, first, 20, stream=stream)
+
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        calls(caches[0], None)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            got = calls(caches[0], side.cuda_stream if raw else side)
+    torch.cuda.synchronize()
+    for lens, at in (([30, 4], [10, 0]), ([17, 29], [0, 16])):
+        K.copy_(randn(g, *K.shape, dtype=torch.float16)), V.copy_(randn(g, *V.shape, dtype=torch.float16))
+        n.copy_(torch.tensor(lens)), first.copy_(torch.tensor(at))
+        torch.cuda.synchronize()
+        graph.replay()
+        want = calls(caches[1], None)
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(bits(x), bits(y)) and bool((x != 0).any())
