@@ -38,7 +38,7 @@
  *     SRHT rotation and the Gaussian value codebook; QJL sketches (keys or
  *     values), dense rotations, the sphere codebook, attention-mass outputs
  *     and tq_requantize return TQ_ERR_UNSUPPORTED there.  tq_rope, tq_append,
- *     tq_read and tq_tree_attention take every head_dim.
+ *     tq_read, tq_tree_attention and the calls on pages take every head_dim.
  */
 #ifndef TQ_H
 #define TQ_H
@@ -582,6 +582,132 @@ tq_status tq_tree_workspace_size(const tq_layer_view *layer, int batch, int n_he
  * (a wait for copies or tensor-core work that ran out; cleared by the next call). */
 tq_status tq_tree_attention(const tq_layer_view *layer, int batch, int n_heads, int q_heads, int head_dim,
                             const tq_tree *tree, void *workspace, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Serving from pages: sequences that come and go share pools of pages.  (No    */
+/* counterpart on the pages.)                                                  */
+/*                                                                             */
+/* A pool is a segment (packed, or fp16) whose batch axis counts pages: batch =   */
+/* n_pages, capacity = tokens a page, element (page, head, token of the page).     */
+/* Token t of sequence b lies on page table[b][t / capacity] at t % capacity; its   */
+/* slot is page * capacity + t % capacity.  One table serves every layer (a pool a  */
+/* layer, all with as many pages).  The conventions are those of the serving calls  */
+/* above: int32 numbers on the device, checked there, never read by the host.      */
+/* ------------------------------------------------------------------------ */
+
+/* Places for new tokens.  Sequence b holds length[b] tokens on the first pages of its
+ * row of `table`; it gets up to min(n_new[b], n_max) more, page by page from the top of a
+ * stack of free pages (free_pages[0 .. n_free - 1], its top at the end; n_free: one
+ * number).  Sequences are served in order, each as far as the pages last and its row of the table
+ * reaches; one that is short of pages keeps what it got, and later ones get none that it asked
+ * for.  With the tokens granted:
+ *   table       new pages in the entries behind those held; other entries stay
+ *   length[b]   grows by granted[b]; n_free falls by the pages taken
+ *   slots       [batch][n_max] (may be NULL): the slot of new token j, -1 from granted[b] on and
+ *               where the table's entry is outside [0, n_pages)
+ *   positions   [batch][n_max] (may be NULL): length[b] (as it was) + j, -1 likewise
+ *   granted     [batch]
+ * All device int32, 4-byte aligned, that must not overlap.  A length outside [0, max_pages page_size] and
+ * an n_free outside [0, n_pages] count as the nearest one inside.  free_pages has room for
+ * n_pages entries.  max_pages * page_size and n_pages * page_size: below 2^31. */
+tq_status tq_page_tables(int batch, int page_size, int max_pages, int n_pages, int *table, int64_t table_stride_b, int *length,
+                         const int *n_new, int n_max, int *free_pages, int *n_free, int *slots, int *positions, int *granted,
+                         void *stream);
+
+/* Pages given back: length[b] becomes min(length[b], keep[b]) (keep 0: the sequence ends; the
+ * length before a step: the step's rejected tokens), and the pages that held only tokens
+ * behind that go onto the stack, in the order that undoes the call that took them (the same sequences
+ * released to the lengths before it: the stack is what it was).  Table entries stay (stale).
+ * A page given back must be no other sequence's: pages may be shared by rows of
+ * the table, but only one of them releases.  What does not fit behind free_pages[n_pages - 1] is dropped. */
+tq_status tq_page_release(int batch, int page_size, int max_pages, int n_pages, const int *table, int64_t table_stride_b,
+                          int *length, const int *keep, int *free_pages, int *n_free, void *stream);
+
+/* tq_append by slot: row j < min(n_new[b], n_max) of sequence b goes to slot
+ * slots[b*slot_stride_b + j] of the pool (pool->layout.batch pages); rows whose slot is outside
+ * the pool are skipped.  batch: sequences (K's and V's first axis).  The slots of a call must
+ * be distinct.  Everything else, and the stored bits, as tq_append.  n_pages * capacity:
+ * below 2^31 (TQ_ERR_UNSUPPORTED). */
+tq_status tq_paged_append(const tq_segment *pool, const tq_rotation *rot, const tq_rope_view *rope, const int *positions,
+                          int64_t pos_stride_b, const void *K, const int64_t *k_stride, const void *V,
+                          const int64_t *v_stride, int batch, int n_source, int n_max, const int *slots,
+                          int64_t slot_stride_b, const int *n_new, const int *index, int64_t index_stride_b, void *stream);
+
+/* tq_read by slot, likewise. */
+tq_status tq_paged_read(const tq_segment *pool, const tq_rotation *rot, int batch, int n_max, const int *slots,
+                        int64_t slot_stride_b, const int *n_read, int dtype, void *K, const int64_t *k_stride, void *V,
+                        const int64_t *v_stride, void *stream);
+
+typedef struct {
+    const int *table;        /* device int32: pages of sequence b from table[b*table_stride_b] on, max_pages entries;
+                                NULL: the segment is no pool but holds sequence b in its batch element b (its
+                                batch is the call's) */
+    int64_t table_stride_b;  /* at least max_pages */
+    int max_pages;
+    const int *len;          /* device int32 [batch]: tokens sequence b holds, at most max_pages * capacity
+                                (n_tokens without a table) of them are taken; NULL: n_tokens (no table) */
+} tq_pages;
+
+/* Bytes of device workspace tq_paged_attention needs; depends on the segments' kinds and
+ * widths and on the counts, not on lengths or tables. */
+tq_status tq_paged_workspace_size(const tq_layer_view *pools, int batch, int n_heads, int q_heads, int head_dim, size_t *bytes);
+
+/* Attention of one new token of each sequence over one layer's segments, in one pass over
+ * the cache, split over its length and joined: out[b][j] = softmax(q . k / sqrt(d)) . v over the tokens
+ * that sequence b holds of every segment of the view (pages[i] says how segment i is laid out).  A
+ * sequence without tokens yields zeros.  A token whose page is outside the pool is left out.
+ * q_heads: any multiple of n_heads.
+ *   q    device fp16, element (b, j, e) at b*q_stride[0] + j*q_stride[1] + e, 2-byte aligned
+ *   out  device fp16 [batch][q_heads][d], 16-byte aligned; must not overlap the inputs
+ * Scores and the value sum of packed tokens run in the rotated space; one inverse rotation follows the
+ * merge.  Sums are binary32, the result is rounded to fp16.  At head dims 64 and 128 queries
+ * and weights enter with 22 bits (weights relative to the row's largest weighted value scale, those below
+ * 2^-36 of it as zero) and the value levels as fp16, as in tq_tree_attention; at the others
+ * everything is binary32.  All numbers on the device may change between replays of a captured call;
+ * two calls that may overlap need two workspaces.  QJL heads (key or value), dense
+ * rotations and segments with attn_mass return TQ_ERR_UNSUPPORTED, as do the sphere law at head dims other
+ * than 128 and a packed segment's capacity that is no multiple of 16 (TQ_ERR_ALIGN).  No device memory is
+ * allocated and nothing is copied from the host.  tq_decode_error_flag reads the
+ * workspace's error flag (a wait for copies that ran out; cleared by the next call; the rows it concerns
+ * stay unwritten). */
+tq_status tq_paged_attention(const tq_layer_view *pools, const tq_pages *pages, int batch, int n_heads, int q_heads, int head_dim,
+                             const void *q, const int64_t *q_stride, void *out, void *workspace, size_t ws_bytes, void *stream);
+
+typedef struct {
+    int batch, n_drafts, vocab;    /* n_drafts N: 0..TQ_MAX_DRAFTS; vocab: 1..2^30 */
+    int dtype;                     /* of target and draft: TQ_DTYPE_* */
+    const int *tokens;             /* device int32: drafted token i of sequence b at b*tokens_stride_b + i; one outside
+                                      [0, vocab) is no candidate (sequences with fewer drafts) */
+    int64_t tokens_stride_b;
+    const int *parents;            /* device int32, likewise: the draft that i continues (before it), -1: the
+                                      last cached token; others: no candidate.  NULL: a chain (i - 1) */
+    int64_t parents_stride_b;      /* 0: one tree for all */
+    const void *target;            /* device: weight of token t behind the last cached token at b*target_stride[0] + t, behind
+                                      draft i at b*target_stride[0] + (i + 1)*target_stride[1] + t (N + 1 rows) */
+    int64_t target_stride[2];
+    const void *draft;             /* device, rows likewise (N of them are read at most): what the drafts were drawn from,
+                                      row 0 the root's children, row i + 1 the children of draft i.  NULL: drafts
+                                      that stand for themselves (a lookup's, a greedy model's) */
+    int64_t draft_stride[2];
+    const float *uniform;          /* device: N + 1 numbers in [0, 1) a sequence, at b*uniform_stride_b + i: draft i's test;
+                                      the last: the draw of the token */
+    int64_t uniform_stride_b;
+    int *accepted;                 /* device int32 [batch][N]: the accepted drafts, a path from the root, -1 behind them */
+    int *n_accepted;               /* device int32 [batch] */
+    int *token;                    /* device int32 [batch]: the token behind the path */
+} tq_verification;
+
+/* Verification of drafted tokens (rejection sampling: what comes out is distributed as the
+ * target's own samples).  From the root on, at a node with weights r = its target row p and mass s = 1, its
+ * children are tried in index order: draft i with token t is accepted if u_i q(t) s < r(t), q the
+ * node's draft row (draft NULL: q(t) = 1), and the walk goes on from it.  A
+ * rejection leaves r = max(r - s q, 0) (draft NULL: r(t) = 0) and s = sum r; where that is nothing, r = p and
+ * s = sum p.  Where no child is accepted, the token is the smallest t with r(0) + ... + r(t) > u_N sum r,
+ * or -1 if the row has no weight.  Entries of the rows that are not positive numbers below 2^90
+ * count as 0; rows need not sum to 1 (the first test takes p and q as they are).  Products are binary64, a difference
+ * is rounded once to binary32, sums carry 48 bits.  accepted and n_accepted are what
+ * tq_append takes as index and n_new.  Outputs must not overlap. */
+tq_status tq_verify(const tq_verification *v, void *stream);
 
 #ifdef __cplusplus
 }

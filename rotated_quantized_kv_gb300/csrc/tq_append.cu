@@ -105,8 +105,8 @@ __global__ void __launch_bounds__(kAppThreads) append_team_kernel(const __grid_c
         const long long f = base + v;
         unsigned long long r = f < n ? f : 0;
         const int h = split_index(r, p.H), j = split_index(r, p.rows.n_max), b = split_index(r, p.B), kv = static_cast<int>(r);
-        int src = 0, pos = 0;
-        const bool valid = f < n && map_row(p.rows, b, j, p.seg.capacity, src, pos);
+        int src = 0, at = 0, pos = 0;
+        const bool valid = f < n && map_row(p.rows, b, j, p.seg.capacity, src, at, pos);
         if (!__any_sync(0xffffffffu, valid)) continue;  // (n_max may be far above the sequences' counts)
         float a[E];
         if (valid) {
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kAppThreads) append_team_kernel(const __grid_c
         for (int x = 1; x < T; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
         const float S = tree_sum_squares<D>(a, lt, stage + (TM::STAGE ? warp * D : 0));
         const int bits = kv ? p.seg.vbits[h] : p.seg.kbits[h];
-        uint8_t *dst = const_cast<uint8_t *>(kv ? p.seg.v : p.seg.k) + b * (kv ? p.seg.vblock : p.seg.kblock) +
+        uint8_t *dst = const_cast<uint8_t *>(kv ? p.seg.v : p.seg.k) + at * (kv ? p.seg.vblock : p.seg.kblock) +
                        (kv ? p.seg.voff[h] : p.seg.koff[h]) + static_cast<size_t>(pos) * (D * bits / 8);
         float scale;
         if constexpr (E == 4) {
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kAppThreads) append_team_kernel(const __grid_c
             if (valid) store_record<D>(codes[warp], bits, dst, lt);
         }
         if (valid && lt == 0)
-            const_cast<float *>(kv ? p.seg.vs : p.seg.ks)[(static_cast<size_t>(b) * p.H + h) * p.seg.capacity + pos] = scale;
+            const_cast<float *>(kv ? p.seg.vs : p.seg.ks)[(static_cast<size_t>(at) * p.H + h) * p.seg.capacity + pos] = scale;
         __syncwarp();
     }
 }
@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(kAppThreads) append_copy_kernel(const __grid_c
         unsigned long long r = f;
         const int u = split_index(r, units), h = split_index(r, p.H), j = split_index(r, p.rows.n_max);
         const int b = split_index(r, p.B), kv = static_cast<int>(r);
-        int src, pos;
-        if (!map_row(p.rows, b, j, p.seg.capacity, src, pos)) continue;
+        int src, at, pos;
+        if (!map_row(p.rows, b, j, p.seg.capacity, src, at, pos)) continue;
         const int64_t *st = kv ? p.vs : p.ks;
         const uint16_t *row = (kv ? p.V : p.K) + b * st[0] + h * st[1] + src * st[2];
         const float *cs = table_row(p, kv, b, src);
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kAppThreads) append_copy_kernel(const __grid_c
         load_coords4(row, 8 * u, p.rope, cs, p.vec != 0, lo);
         load_coords4(row, 8 * u + 4, p.rope, cs, p.vec != 0, hi);
         __align__(16) const __half x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        uint8_t *dst = const_cast<uint8_t *>(kv ? p.seg.v : p.seg.k) + b * (kv ? p.seg.vblock : p.seg.kblock) +
+        uint8_t *dst = const_cast<uint8_t *>(kv ? p.seg.v : p.seg.k) + at * (kv ? p.seg.vblock : p.seg.kblock) +
                        (kv ? p.seg.voff[h] : p.seg.koff[h]) + (static_cast<size_t>(pos) * p.d + 8 * u) * 2;
         *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(x);
     }

@@ -23,7 +23,7 @@ namespace {
 
 struct RowBlock {
     int b, h, j;            // sequence, head, this lane's row
-    int src, pos;           // its source row and position
+    int src, at, pos;       // its source row, batch element (or page) and position
     bool valid;
 };
 
@@ -33,8 +33,8 @@ __device__ __forceinline__ RowBlock row_block(const AppendRowsParams &p, int n_t
     const int rest = blk / p.r.n_heads;
     r.j = (rest % n_tblk) * 32 + lane;
     r.b = rest / n_tblk;
-    r.src = r.pos = 0;
-    r.valid = map_row(p.rows, r.b, r.j, p.r.capacity, r.src, r.pos);
+    r.src = r.at = r.pos = 0;
+    r.valid = map_row(p.rows, r.b, r.j, p.r.capacity, r.src, r.at, r.pos);
     return r;
 }
 
@@ -165,11 +165,11 @@ __global__ void __launch_bounds__(kThreads, 3) append_rows_kernel(const __grid_c
         rows_vector<BITS, VAL, 1, 1>(buf + lane * kRowBytes, in_mask, out_pair, thr, vtab, p.r.bucket4_ok != 0, lane, 0, w,
                                      scale, scale_b);
         if (r.valid) {
-            uint4 *dst = reinterpret_cast<uint4 *>(p.r.codes + static_cast<size_t>(r.b) * p.r.block + p.r.off[r.h] +
+            uint4 *dst = reinterpret_cast<uint4 *>(p.r.codes + static_cast<size_t>(r.at) * p.r.block + p.r.off[r.h] +
                                                    static_cast<size_t>(r.pos) * (16 * BITS));
 #pragma unroll
             for (int j = 0; j < BITS; j++) dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-            p.r.scale[(static_cast<size_t>(r.b) * p.r.H + r.h) * p.r.capacity + r.pos] = scale;
+            p.r.scale[(static_cast<size_t>(r.at) * p.r.H + r.h) * p.r.capacity + r.pos] = scale;
         }
     }
     asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the call's last launch ends behind its first

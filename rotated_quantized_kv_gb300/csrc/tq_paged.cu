@@ -1,0 +1,326 @@
+// tq_paged.cu -- attention of one new token of each sequence over paged segments: the
+// form for every head dimension, and the merge of the records.
+//
+// The plain form works in binary32 on the CUDA cores: a CTA takes a range of the stage
+// list (tq_paged.cuh), dequantizes some tokens at a time into shared memory, scores them
+// against the block's rotated queries (fp16 segments: the queries as they are) with an
+// online softmax, and sums the values.  Head dimensions 64 and 128 take tq_paged_mma.cuh.
+#include <algorithm>
+#include <cstring>
+
+#include <cuda_fp16.h>
+
+#include "tq_paged.cuh"
+#include "tq_serve.h"
+#include "tq_team.cuh"
+
+namespace tqk {
+namespace {
+
+using namespace paged;
+
+constexpr float kInf = __builtin_huge_valf();
+constexpr int kPlainThreads = 256;
+constexpr int kPlainWarps = kPlainThreads / 32;
+constexpr int kPlainRows = 4;
+constexpr int kPlainUnit = 64;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <int D>
+struct Plain {
+    static constexpr int R = kPlainRows, TT = D >= 512 ? 16 : 32, LD = D + 1;
+    static constexpr int DPT = (D + kPlainThreads - 1) / kPlainThreads;
+    static constexpr size_t smem = (2 * R * LD + TT * LD + R * TT + 3 * R) * sizeof(float);
+};
+
+// Coordinate i of a token's key (kv 0) or value, in the rotated space.
+template <int D>
+__device__ __forceinline__ float token_value(const PagedParams &p, const PagedSeg &s, int kv, int page, int h, int t, int i) {
+    const SegView &v = s.seg;
+    const uint8_t *head = (kv ? v.v : v.k) + page * (kv ? v.vblock : v.kblock) + (kv ? v.voff[h] : v.koff[h]);
+    if (v.fp16) return __half2float(__ushort_as_half(reinterpret_cast<const uint16_t *>(head)[static_cast<size_t>(t) * D + i]));
+    const int bits = kv ? p.cls.vb : p.cls.kb;
+    const uint32_t code = code_at(head + static_cast<size_t>(t) * (D * bits / 8), i, bits);
+    const float scale = (kv ? v.vs : v.ks)[(static_cast<size_t>(page) * p.list.H + h) * v.capacity + t];
+    if (kv) return scale * p.centroid[cb_off(bits) + code];
+    return scale * (static_cast<float>(2 * code + 1) / static_cast<float>(1 << bits) - 1.0f);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPlainThreads) paged_plain_kernel(const __grid_constant__ PagedParams p) {
+    using C = Plain<D>;
+    constexpr int R = C::R, TT = C::TT, LD = C::LD, DPT = C::DPT;
+    extern __shared__ float sm[];
+    __shared__ int buf[kPlainWarps + 2];
+    float *q = sm, *raw = q + R * LD, *tok = raw + R * LD, *S = tok + TT * LD;  // queries of the segment's space, as they are; tokens; scores
+    float *row_m = S + R * TT, *row_l = row_m + R, *row_c = row_l + R;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, worker = blockIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (threadIdx.x == 0) p.state[worker] = 0;
+    const PagedList &l = p.list;
+    const Range r = range_of<kPlainThreads>(l, p.cls, worker, p.first, buf);
+    if (r.begin < r.end) {
+        Walk w = seek(l, p.cls, r.b, r.rest);
+        float acc[R][DPT];
+        bool fresh = true;
+        for (int at = r.begin; at < r.end; at++) {
+            if (fresh) {
+                __syncthreads();
+                for (int i = threadIdx.x; i < R; i += kPlainThreads) row_m[i] = -kInf, row_l[i] = 0.f;
+#pragma unroll
+                for (int i = 0; i < R; i++)
+#pragma unroll
+                    for (int e = 0; e < DPT; e++) acc[i][e] = 0.f;
+                for (int i = warp; i < R; i += kPlainWarps) {
+                    const int row = w.rb * R + i;
+                    float v[(D + 31) / 32];
+#pragma unroll
+                    for (int j = 0; j < (D + 31) / 32; j++) {
+                        const int e = lane + 32 * j;
+                        v[j] = row < p.g && e < D ? __half2float(__ushort_as_half(p.q[w.b * p.qs[0] + (w.h * p.g + row) * p.qs[1] + e])) : 0.f;
+                    }
+                    if (p.cls.kb) warp_rotate_strided<D>(v, p.sign_bits, p.inv_sqrt_d, lane);
+#pragma unroll
+                    for (int j = 0; j < (D + 31) / 32; j++)
+                        if (lane + 32 * j < D) q[i * LD + lane + 32 * j] = v[j];
+                }
+                __syncthreads();
+            }
+            const PagedSeg &s = p.seg[p.cls.seg[w.i]];
+            const int hi = min(w.tokens, (w.st + 1) * kPlainUnit);
+            for (int t0 = w.st * kPlainUnit; t0 < hi; t0 += TT) {
+                const int nt = min(TT, hi - t0);
+                __syncthreads();
+                for (int i = threadIdx.x; i < nt * D; i += kPlainThreads) {
+                    const int t = t0 + i / D, page = page_at(s, w.b, t / s.page);
+                    tok[(i / D) * LD + i % D] = page < 0 ? 0.f : token_value<D>(p, s, 0, page, w.h, t % s.page, i % D);
+                }
+                __syncthreads();
+                for (int i = threadIdx.x; i < R * TT; i += kPlainThreads) {
+                    const int row = i / TT, t = i % TT;
+                    float x = -kInf;
+                    if (t < nt && page_at(s, w.b, (t0 + t) / s.page) >= 0) {
+                        x = 0.f;
+                        for (int e = 0; e < D; e++) x = fmaf(q[row * LD + e], tok[t * LD + e], x);
+                        x *= p.qk_scale;
+                    }
+                    S[i] = x;
+                }
+                __syncthreads();
+                for (int row = warp; row < R; row += kPlainWarps) {
+                    const float x = lane < TT ? S[row * TT + lane] : -kInf;
+                    float m = x;
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    const float old = row_m[row], now = fmaxf(old, m);
+                    const float pr = x == -kInf ? 0.f : ex2(x - now);
+                    float sum = pr;
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    const float f = now == -kInf ? 1.f : ex2(old - now);
+                    if (lane < TT) S[row * TT + lane] = pr;
+                    __syncwarp();
+                    if (lane == 0) row_m[row] = now, row_l[row] = row_l[row] * f + sum, row_c[row] = f;
+                }
+                for (int i = threadIdx.x; i < nt * D; i += kPlainThreads) {
+                    const int t = t0 + i / D, page = page_at(s, w.b, t / s.page);
+                    tok[(i / D) * LD + i % D] = page < 0 ? 0.f : token_value<D>(p, s, 1, page, w.h, t % s.page, i % D);
+                }
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < DPT; e++) {
+                    const int i = threadIdx.x + e * kPlainThreads;
+                    if (i < D) {
+#pragma unroll
+                        for (int row = 0; row < R; row++) acc[row][e] *= row_c[row];
+                        for (int t = 0; t < nt; t++) {
+                            const float v = tok[t * LD + i];
+#pragma unroll
+                            for (int row = 0; row < R; row++) acc[row][e] = fmaf(S[row * TT + t], v, acc[row][e]);
+                        }
+                    }
+                }
+            }
+            const Walk x = w;
+            const bool last = at + 1 == r.end;
+            fresh = !last && next(l, p.cls, w);
+            if (!fresh && !last) continue;
+            __syncthreads();
+            float *rec = p.part + group_slot(l, p.cls, worker, x.b, x.h, x.rb) * R * (D + 4);
+            for (int i = threadIdx.x; i < R; i += kPlainThreads) {
+                rec[i * (D + 4)] = row_m[i];
+                rec[i * (D + 4) + 1] = row_l[i];
+            }
+#pragma unroll
+            for (int i = 0; i < R; i++)
+#pragma unroll
+                for (int e = 0; e < DPT; e++) {
+                    const int k = threadIdx.x + e * kPlainThreads;
+                    if (k < D) rec[i * (D + 4) + 4 + k] = acc[i][e];
+                }
+        }
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the call's last launch ends behind its first
+}
+
+// ------------------------------------------------------------------- merge
+// A CTA for each row (sequence, query head): the records of its (b, h, rb), class by class, with
+// the weights 2^(m - M); packed classes' sums turn back from the rotated space together.  Threads: quads of
+// coordinates times records in flight.
+constexpr int kMergeThreads = 256;
+
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ PagedMergeParams p) {
+    __shared__ __align__(16) float sum[2][kMergeThreads * 4];  // [space][record lane][d]
+    __shared__ float red[2][kMergeThreads / 32];
+    __shared__ int span[kPagedClasses][2];                    // first and last worker of the row's group
+    const int d = p.d, B = p.list.B, H = p.list.H, R = p.list.R, n_rb = p.list.n_rb;
+    const int row = blockIdx.x, b = row / (H * p.g), h = row / p.g % H, j = row % p.g, rb = j / R;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (threadIdx.x < p.n_classes) {
+        const PagedClass &c = p.cls[threadIdx.x];
+        const int *first = p.first + static_cast<size_t>(threadIdx.x) * (B + 1);
+        const int n = head_stages(p.list, c, b, h);
+        int w0 = 0, w1 = -1;
+        if (n > 0) {
+            int s = first[b] + rb * n;
+            for (int i = 0; i < h; i++) s += n_rb * head_stages(p.list, c, b, i);
+            const int workers = workers_of(c, first[B]);
+            w0 = max(worker_of(first[B], s, workers), 0);
+            w1 = min(worker_of(first[B], s + n - 1, workers), workers - 1);
+        }
+        span[threadIdx.x][0] = w0;
+        span[threadIdx.x][1] = w1;
+    }
+    __syncthreads();
+    const size_t step = static_cast<size_t>(R) * (d + 4);
+    auto record = [&](int c, int w) { return p.part + group_slot(p.list, p.cls[c], w, b, h, rb) * step + (j % R) * (d + 4); };
+    // the largest m, and whether a worker gave up
+    float M = -kInf;
+    int bad = 0;
+    for (int c = 0; c < p.n_classes; c++)
+        for (int w = span[c][0] + threadIdx.x; w <= span[c][1]; w += kMergeThreads) {
+            M = fmaxf(M, record(c, w)[0]);
+            bad |= p.state[p.state0[c] + w];
+        }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (lane == 0) red[0][warp] = M;
+    bad = __syncthreads_or(bad);
+    for (int i = 0; i < kMergeThreads / 32; i++) M = fmaxf(M, red[0][i]);
+    if (blockIdx.x == 0) {  // the call's flag
+        int any = 0;
+        for (int c = 0; c < p.n_classes; c++)
+            for (int w = threadIdx.x; w < p.cls[c].workers; w += kMergeThreads) any |= p.state[p.state0[c] + w];
+        any = __syncthreads_or(any);
+        if (threadIdx.x == 0) *p.error = any ? 1 : 0;
+    }
+    if (bad) return;
+    const int quads = d / 4, lanes = kMergeThreads / quads, quad = threadIdx.x % quads, rl = threadIdx.x / quads;
+    float L = 0.f;  // (of the record lane)
+    float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (M != -kInf) {
+        for (int c = 0; c < p.n_classes; c++) {
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int w = span[c][0] + rl; w <= span[c][1]; w += lanes) {
+                const float *rec = record(c, w);
+                const float2 ml = *reinterpret_cast<const float2 *>(rec);
+                const float4 x = *reinterpret_cast<const float4 *>(rec + 4 + 4 * quad);
+                const float f = ex2(ml.x - M);
+                L = fmaf(ml.y, f, L);
+                a.x = fmaf(x.x, f, a.x);
+                a.y = fmaf(x.y, f, a.y);
+                a.z = fmaf(x.z, f, a.z);
+                a.w = fmaf(x.w, f, a.w);
+            }
+            float4 &to = s[p.cls[c].kb ? 1 : 0];
+            to.x += a.x, to.y += a.y, to.z += a.z, to.w += a.w;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; k++) *reinterpret_cast<float4 *>(&sum[k][rl * d + 4 * quad]) = s[k];
+    __shared__ float lsum[kMergeThreads];  // [record lane]
+    if (quad == 0) lsum[rl] = L;
+    __syncthreads();
+    L = 0.f;
+    for (int i = 0; i < lanes; i++) L += lsum[i];
+    for (int i = threadIdx.x; i < 2 * d; i += kMergeThreads) {
+        float *x = sum[i >= d] + i % d;
+        float a = x[0];
+        for (int k = 1; k < lanes; k++) a += x[k * d];
+        // the rotated sum's first sign flip
+        x[0] = i >= d && ((p.sign_bits[(i - d) >> 5] >> ((i - d) & 31)) & 1u) ? -a : a;
+    }
+    __syncthreads();
+    for (int o = 1; o < d; o <<= 1) {
+        for (int i = threadIdx.x; i < d / 2; i += kMergeThreads) {
+            const int at = 2 * o * (i / o) + i % o;
+            const float x = sum[1][at], y = sum[1][at + o];
+            sum[1][at] = x + y;
+            sum[1][at + o] = x - y;
+        }
+        __syncthreads();
+    }
+    const float scale = L != 0.f ? 1.f / L : 0.f;  // (no token: zeros; a NaN stays one)
+    for (int i = threadIdx.x; i < d; i += kMergeThreads) {
+        const float y = ((p.sign_bits[i >> 5] >> (i & 31)) & 1u) ? -p.inv_sqrt_d : p.inv_sqrt_d;
+        p.out[static_cast<size_t>(row) * d + i] = __half_as_ushort(__float2half_rn(fmaf(sum[1][i], y, sum[0][i]) * scale));
+    }
+}
+
+template <int D>
+cudaError_t plain(const PagedParams &p, cudaStream_t s) {
+    const cudaError_t e = cudaFuncSetAttribute(paged_plain_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(Plain<D>::smem));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.cls.workers));
+    cfg.blockDim = dim3(kPlainThreads);
+    cfg.dynamicSmemBytes = Plain<D>::smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.first_class ? 0 : 1;
+    return cudaLaunchKernelEx(&cfg, paged_plain_kernel<D>, p);
+}
+
+}  // namespace
+
+PagedShape paged_shape(int, int, int) { return {kPlainUnit, 2 * current_sm_count()}; }
+int paged_rows(int, int) { return kPlainRows; }
+
+cudaError_t launch_paged(const PagedParams &p, cudaStream_t s) {
+    switch (p.d) {
+        case 16: return plain<16>(p, s);
+        case 32: return plain<32>(p, s);
+        case 64: return plain<64>(p, s);
+        case 128: return plain<128>(p, s);
+        case 256: return plain<256>(p, s);
+        case 512: return plain<512>(p, s);
+        case 1024: return plain<1024>(p, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_paged_merge(const PagedMergeParams &p, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.list.B) * p.list.H * p.g);
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_merge_kernel, p);
+}
+
+}  // namespace tqk

@@ -33,14 +33,6 @@ __device__ __forceinline__ void put4(__nv_bfloat16 *p, const float *x) {
     *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<uint2 *>(v);
 }
 
-// Position of row j of sequence b; false: not read.
-__device__ __forceinline__ bool read_row(const RowMap &m, int b, int j, int capacity, int &pos) {
-    const int n = m.n_rows ? min(m.n_rows[b], m.n_max) : m.n_max;
-    const long long t = static_cast<long long>(m.t_begin[b]) + j;
-    pos = static_cast<int>(t);
-    return j < n && t >= 0 && t < capacity;
-}
-
 // One team of lanes per vector (kv, b, h, j), rows of a head consecutive.
 template <int D, typename T>
 __global__ void __launch_bounds__(kReadThreads) read_team_kernel(const __grid_constant__ ReadParams p) {
@@ -62,15 +54,15 @@ __global__ void __launch_bounds__(kReadThreads) read_team_kernel(const __grid_co
         unsigned long long r = f < n ? f : 0;
         const int j = split_index(r, p.rows.n_max), h = split_index(r, p.H), b = split_index(r, p.B);
         const int kv = kv0 + static_cast<int>(r);
-        int pos = 0;
-        const bool valid = f < n && read_row(p.rows, b, j, p.seg.capacity, pos);
+        int at = 0, pos = 0;
+        const bool valid = f < n && place_row(p.rows, b, j, p.seg.capacity, at, pos);
         if (!__any_sync(0xffffffffu, valid)) continue;  // (n_max may be far above the sequences' counts)
         float a[E];
         if (valid) {
             const int bits = kv ? p.seg.vbits[h] : p.seg.kbits[h];
-            const uint8_t *rec = (kv ? p.seg.v : p.seg.k) + b * (kv ? p.seg.vblock : p.seg.kblock) +
+            const uint8_t *rec = (kv ? p.seg.v : p.seg.k) + at * (kv ? p.seg.vblock : p.seg.kblock) +
                                  (kv ? p.seg.voff[h] : p.seg.koff[h]) + static_cast<size_t>(pos) * (D * bits / 8);
-            const float sc = (kv ? p.seg.vs : p.seg.ks)[(static_cast<size_t>(b) * p.H + h) * p.seg.capacity + pos];
+            const float sc = (kv ? p.seg.vs : p.seg.ks)[(static_cast<size_t>(at) * p.H + h) * p.seg.capacity + pos];
             const float inv_cells = __uint_as_float(static_cast<uint32_t>(127 - bits) << 23);  // 2^-b
             const int rk = D * bits / 8;
 #pragma unroll
@@ -117,9 +109,9 @@ __global__ void __launch_bounds__(kReadThreads) read_copy_kernel(const __grid_co
         unsigned long long r = f;
         const int u = split_index(r, units), j = split_index(r, p.rows.n_max), h = split_index(r, p.H);
         const int b = split_index(r, p.B), kv = kv0 + static_cast<int>(r);
-        int pos;
-        if (!read_row(p.rows, b, j, p.seg.capacity, pos)) continue;
-        const uint8_t *src = (kv ? p.seg.v : p.seg.k) + b * (kv ? p.seg.vblock : p.seg.kblock) +
+        int at, pos;
+        if (!place_row(p.rows, b, j, p.seg.capacity, at, pos)) continue;
+        const uint8_t *src = (kv ? p.seg.v : p.seg.k) + at * (kv ? p.seg.vblock : p.seg.kblock) +
                              (kv ? p.seg.voff[h] : p.seg.koff[h]) + (static_cast<size_t>(pos) * p.d + 8 * u) * 2;
         const uint4 w = *reinterpret_cast<const uint4 *>(src);
         const __half *x = reinterpret_cast<const __half *>(&w);

@@ -89,8 +89,9 @@ __device__ __forceinline__ void all_levels(const uint32_t *w, const float *table
 
 struct ReadBlock {
     int b, h, tb;           // sequence, head, block of 32 threads' rows
-    long long t;            // this lane's (first) position
-    bool valid, valid2;     // valid2: the second vector (head_dim 64)
+    int at, t;              // this lane's (first) batch element (or page) and position
+    int at2, t2;            // those of the second vector (head_dim 64)
+    bool valid, valid2;
 };
 
 template <int NP>
@@ -100,10 +101,9 @@ __device__ __forceinline__ ReadBlock read_block(const ReadRowsParams &p, int n_t
     const int rest = blk / n_tblk;
     r.h = p.head[rest % p.n_heads];
     r.b = rest / p.n_heads;
-    const int j = (32 * r.tb + lane) * NP, n = p.rows.n_rows ? min(p.rows.n_rows[r.b], p.rows.n_max) : p.rows.n_max;
-    r.t = static_cast<long long>(p.rows.t_begin[r.b]) + j;
-    r.valid = j < n && r.t >= 0 && r.t < p.capacity;
-    r.valid2 = NP == 2 && j + 1 < n && r.t + 1 >= 0 && r.t + 1 < p.capacity;
+    const int j = (32 * r.tb + lane) * NP;
+    r.valid = place_row(p.rows, r.b, j, p.capacity, r.at, r.t);
+    r.valid2 = NP == 2 && place_row(p.rows, r.b, j + 1, p.capacity, r.at2, r.t2);
     return r;
 }
 
@@ -116,28 +116,29 @@ __device__ __forceinline__ void cp_async8(void *dst, const void *src) {
 // The lane's records and scales on their way (records lie at the lane's place).
 template <int BITS, int NP>
 __device__ __forceinline__ float2 fetch_record(const ReadRowsParams &p, const ReadBlock &r, uint8_t *buf, int lane) {
-    const uint8_t *head = p.codes + r.b * p.block + p.off[r.h];
-    const float *scale = p.scale + (static_cast<size_t>(r.b) * p.H + r.h) * p.capacity + r.t;
     buf += lane * (16 * BITS);
+    auto record = [&](int at, int t) { return p.codes + at * p.block + p.off[r.h] + static_cast<size_t>(t) * (16 * BITS / NP); };
+    auto scale = [&](int at, int t) { return __ldg(p.scale + (static_cast<size_t>(at) * p.H + r.h) * p.capacity + t); };
     float2 s = make_float2(0.f, 0.f);
     if constexpr (NP == 1) {
         if (r.valid) {
-            const uint8_t *rec = head + r.t * (16 * BITS);
+            const uint8_t *rec = record(r.at, r.t);
 #pragma unroll
             for (int i = 0; i < BITS; i++) cp_async16(buf + 16 * i, rec + 16 * i);
-            s.x = __ldg(scale);
+            s.x = scale(r.at, r.t);
         }
     } else {
-        const uint8_t *rec = head + r.t * (8 * BITS);
         if (r.valid) {
+            const uint8_t *rec = record(r.at, r.t);
 #pragma unroll
             for (int i = 0; i < BITS; i++) cp_async8(buf + 8 * i, rec + 8 * i);
-            s.x = __ldg(scale);
+            s.x = scale(r.at, r.t);
         }
         if (r.valid2) {
+            const uint8_t *rec = record(r.at2, r.t2);
 #pragma unroll
-            for (int i = BITS; i < 2 * BITS; i++) cp_async8(buf + 8 * i, rec + 8 * i);
-            s.y = __ldg(scale + 1);
+            for (int i = 0; i < BITS; i++) cp_async8(buf + 8 * (BITS + i), rec + 8 * i);
+            s.y = scale(r.at2, r.t2);
         }
     }
     return s;

@@ -1,4 +1,4 @@
-// tq_row_map.cuh -- rows of a ragged write.
+// tq_row_map.cuh -- rows of a ragged write or read.
 #pragma once
 
 #include "tq_serve.h"
@@ -29,14 +29,28 @@ inline bool blocks_fit(int B, int H, int n_max, int per) {
     return n_max <= 1 << 30 && (static_cast<long long>(n_max) + 32 * per - 1) / (32 * per) * H * B <= 1 << 30;
 }
 
-// Source row and target position of row j of sequence b; false: not written.
-__device__ __forceinline__ bool map_row(const RowMap &m, int b, int j, int capacity, int &src, int &pos) {
+// Place of row j of sequence b in the segment: batch element (a page, where rows have
+// slots) and position in it; false: nowhere.
+__device__ __forceinline__ bool place_row(const RowMap &m, int b, int j, int capacity, int &block, int &pos) {
     const int n = m.n_rows ? min(m.n_rows[b], m.n_max) : m.n_max;
     if (j >= n) return false;
-    src = m.index ? m.index[b * m.index_stride + j] : j;
+    if (m.slots) {
+        const int slot = m.slots[b * m.slot_stride + j];
+        block = slot / capacity;
+        pos = slot - block * capacity;
+        return slot >= 0 && block < m.n_blocks;
+    }
     const long long t = static_cast<long long>(m.t_begin[b]) + j;
+    block = b;
     pos = static_cast<int>(t);
-    return src >= 0 && src < m.n_source && t >= 0 && t < capacity;
+    return t >= 0 && t < capacity;
+}
+
+// The same with the source row of a write.
+__device__ __forceinline__ bool map_row(const RowMap &m, int b, int j, int capacity, int &src, int &block, int &pos) {
+    if (!place_row(m, b, j, capacity, block, pos)) return false;
+    src = m.index ? m.index[b * m.index_stride + j] : j;
+    return src >= 0 && src < m.n_source;
 }
 
 }  // namespace

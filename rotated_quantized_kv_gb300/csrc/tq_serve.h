@@ -51,6 +51,9 @@ struct SegView {
 
 struct RowMap {                  // rows of a ragged write or read
     const int *t_begin, *n_rows; // n_rows: nullptr: n_max
+    const int *slots;            // or (t_begin nullptr) the slot of row j in a pool of n_blocks pages
+    int64_t slot_stride;
+    int n_blocks;
     const int *index;            // source row of row j (writes), or nullptr
     int64_t index_stride;
     int n_max, n_source;
@@ -218,8 +221,106 @@ cudaError_t launch_tree_mma(const TreeParams &p, cudaStream_t s);
 // constants' step, and the factor A.
 inline size_t tree_image_bytes(int d, int R) { return (static_cast<size_t>(4) * d * R + 32 * R + 16 + 127) / 128 * 128; }
 int tree_mma_rows(int rows);
+// The levels of a value codebook as fp16(s c_k), s such that they round closely, and 1/s.
+void value_levels(int law, int bits, const float *centroid, uint16_t *half, float *inv);
 TreeShape tree_shape(int B, int H, int g, int N, int d, long long tiles_per_head);
 cudaError_t launch_tree(const TreeParams &p, cudaStream_t s);
+
+// ----------------------------------------------------------------- pages
+struct PageParams {
+    int B, page, width, n_pages;     // width: entries of a sequence's row of the table
+    int n_max;
+    int *table;
+    int64_t table_stride;
+    int *length;
+    const int *count;                // tokens to place, or (release) to keep
+    int *free_pages, *n_free;
+    int *slots, *positions;          // [B][n_max], or nullptr
+    int *granted;
+};
+cudaError_t launch_page_tables(const PageParams &p, cudaStream_t s);
+cudaError_t launch_page_release(const PageParams &p, cudaStream_t s);
+
+// ----------------------------------------------------------------- paged attention
+// The (key bits, value bits) of a (segment, head) make its class (fp16 segments: 0, 0); the kernel
+// of a class takes all that belong to it.  Its work is a list of stages of U tokens:
+// sequence b in order, KV head h, block of R query heads rb, segment, stage.  The W workers
+// take contiguous ranges of the list, equal to one stage (the first T, where there are
+// fewer stages).  A worker leaves one record
+// (m, l, sum per row) for each (b, h, rb) that it touches, at slot worker + (b H + h) n_rb +
+// rb (along the list one or the other grows, so that the sums are distinct).
+struct PagedSeg {
+    SegView seg;                         // its batch elements are pages
+    const int *table;                    // pages of a sequence, or nullptr: page b
+    int64_t table_stride;
+    const int *len;                      // tokens of a sequence, or nullptr: limit
+    int n_pages, page, limit;            // limit: most tokens a sequence can hold
+};
+struct PagedClass {
+    int kb, vb, law;
+    int n;                               // segments with heads of the class
+    uint8_t seg[TQ_MAX_SEGMENTS];
+    uint16_t heads[TQ_MAX_SEGMENTS];     // bit h: head h of that segment
+    int unit, workers;                   // U, W
+    int64_t slot0;                       // first record
+};
+constexpr int kPagedClasses = 1 + TQ_MAX_SEGMENTS * kMaxH;
+// What the list is made of: lengths without the segments' data.
+struct PagedList {
+    int B, H, R, n_rb;
+    const int *len[TQ_MAX_SEGMENTS];
+    int limit[TQ_MAX_SEGMENTS];
+};
+struct PagedParams {
+    PagedList list;
+    PagedClass cls;                      // of this launch
+    int g, d, n_seg;
+    PagedSeg seg[TQ_MAX_SEGMENTS];
+    const uint16_t *q;
+    int64_t qs[2];                       // strides of (b, head)
+    float *part;                         // records [slot][R][d + 4]: m (log2 units), l, pad, pad, sum
+    int *first;                          // [B + 1]: stages of the class before a sequence
+    int *state;                          // [W]: not 0: the worker gave up a wait
+    int first_class;                     // the call's first launch
+    int wait_polls;
+    uint32_t sign_bits[kMaxD / 32];
+    float inv_sqrt_d, qk_scale;
+    float centroid[kCbTotal];            // of the class's law
+};
+struct PagedMergeParams {
+    PagedList list;
+    int n_classes, g, d;
+    uint16_t *out;                       // [B][H g][d]
+    const float *part;
+    const int *first;                    // [class][B + 1]
+    const int *state;                    // [class][workers]
+    int64_t state0[kPagedClasses];
+    int *error;
+    PagedClass cls[kPagedClasses];
+    uint32_t sign_bits[kMaxD / 32];
+    float inv_sqrt_d;
+};
+// A class's stage length and the most workers that its kernel runs at once.
+struct PagedShape {
+    int unit, workers;
+};
+PagedShape paged_shape(int d, int kb, int vb);
+int paged_rows(int d, int g);            // R
+cudaError_t launch_paged(const PagedParams &p, cudaStream_t s);
+cudaError_t launch_paged_merge(const PagedMergeParams &p, cudaStream_t s);
+
+// ----------------------------------------------------------------- verification of drafts
+struct VerifyParams {
+    int B, N, V;
+    const int *tokens, *parents;         // parents nullptr: a chain
+    int64_t tokens_stride, parents_stride;
+    const void *target, *draft;          // draft nullptr: drafts without a distribution
+    int64_t ts[2], ds[2];                // strides of (b, row)
+    const float *uniform;
+    int64_t uniform_stride;
+    int *accepted, *n_accepted, *token;
+};
+cudaError_t launch_verify(const VerifyParams &p, int dtype, cudaStream_t s);
 
 // ----------------------------------------------------------------- from tq_host.cpp
 tq_status layout_status(const tq_segment_layout *L, bool need_bits);

@@ -8,14 +8,11 @@
 #include <cuda_runtime.h>
 
 #include "tq_serve.h"
+#include "tq_serve_args.h"
 
 using namespace tqk;
 
 namespace {
-
-bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-tq_status launched(cudaError_t e) { return e == cudaSuccess ? TQ_OK : record_cuda_error(e); }
 
 bool finite_positive(double x) { return std::isfinite(x) && x > 0.0; }
 
@@ -57,89 +54,126 @@ void frequencies(const tq_rope_spec &s, double *freq) {
     }
 }
 
-tq_status check_rope_view(const tq_rope_view *v, int head_dim) {
-    if (v->rotary_dim < 2 || v->rotary_dim % 2 || v->rotary_dim > head_dim) return TQ_ERR_ARG;
-    if (v->layout != TQ_ROPE_HALF && v->layout != TQ_ROPE_INTERLEAVED) return TQ_ERR_ARG;
-    if (v->n_pos < 0 || (v->n_pos > 0 && !v->table)) return TQ_ERR_ARG;
-    if (!aligned(v->table, 16)) return TQ_ERR_ALIGN;
-    return TQ_OK;
-}
-
-RopeView rope_view(const tq_rope_view *v) {
-    RopeView r;
-    r.table = v->table;
-    r.half = v->rotary_dim / 2;
-    r.interleaved = v->layout == TQ_ROPE_INTERLEAVED;
-    r.n_pos = v->n_pos;
-    return r;
-}
-
-// no two rows of d elements at the same place: every axis longer than one steps
-// over at least a row
-bool rows_apart(const int64_t *st, int B, int H, int T, int64_t d) {
-    const int n[3] = {B, H, T};
-    for (int i = 0; i < 3; ++i)
-        if (n[i] > 1 && std::llabs(st[i]) < d) return false;
-    return true;
-}
-
-// A segment of `B` sequences and `d` dims; `packed_ptrs` false: sizes only.
-tq_status check_segment(const tq_segment *sg, bool check_ptrs) {
-    if (!sg || (sg->kind != TQ_SEG_PACKED && sg->kind != TQ_SEG_FP16)) return TQ_ERR_ARG;
-    const tq_segment_layout &L = sg->layout;
-    const bool packed = sg->kind == TQ_SEG_PACKED;
-    const tq_status st = layout_status(&L, packed);
+// A write of n_max rows of each of B sequences to the places that `rows` gives.
+tq_status append_rows(const tq_segment *dst, const tq_rotation *rot, const tq_rope_view *rope, const int *positions,
+                      int64_t pos_stride_b, const void *K, const int64_t *k_stride, const void *V, const int64_t *v_stride,
+                      int B, int n_source, int n_max, const RowMap &rows, void *stream) {
+    tq_status st = check_segment(dst, true);
     if (st != TQ_OK) return st;
-    if (!check_ptrs || L.capacity == 0) return TQ_OK;
+    const tq_segment_layout &L = dst->layout;
+    const bool packed = dst->kind == TQ_SEG_PACKED;
+    if (n_source < 0 || n_max < 0 || !k_stride || !v_stride) return TQ_ERR_ARG;
     if (packed) {
-        const tq_packed_bufs &b = sg->packed;
-        if (!b.kcodes || !b.vcodes || !b.kscale || !b.vscale) return TQ_ERR_ARG;
-        if (!aligned(b.kcodes, 16) || !aligned(b.vcodes, 16) || !aligned(b.kscale, 16) || !aligned(b.vscale, 16))
-            return TQ_ERR_ALIGN;
-    } else {
-        if (!sg->k16 || !sg->v16) return TQ_ERR_ARG;
-        if (!aligned(sg->k16, 16) || !aligned(sg->v16, 16)) return TQ_ERR_ALIGN;
+        if (!rot || rot->head_dim != L.head_dim) return TQ_ERR_ARG;
+        if (rot->dense || any_sketch(L) || sphere_elsewhere(L)) return TQ_ERR_UNSUPPORTED;
     }
-    return TQ_OK;
-}
-
-bool sphere_elsewhere(const tq_segment_layout &L) {
-    return L.value_law == TQ_VALUE_LAW_SPHERE && L.head_dim != kD;
-}
-
-SegView seg_view(const tq_segment *sg) {
-    SegView v;
-    std::memset(&v, 0, sizeof(v));
-    const tq_segment_layout &L = sg->layout;
-    v.fp16 = sg->kind == TQ_SEG_FP16;
-    v.capacity = L.capacity;
-    const uint64_t cap = static_cast<uint64_t>(L.capacity);
-    if (v.fp16) {
-        v.k = static_cast<const uint8_t *>(sg->k16);
-        v.v = static_cast<const uint8_t *>(sg->v16);
-        for (int h = 0; h < L.n_heads; ++h) v.koff[h] = v.voff[h] = h * cap * L.head_dim * 2;
-        v.kblock = v.vblock = L.n_heads * cap * L.head_dim * 2;
-    } else {
-        v.k = static_cast<const uint8_t *>(sg->packed.kcodes);
-        v.v = static_cast<const uint8_t *>(sg->packed.vcodes);
-        v.ks = sg->packed.kscale;
-        v.vs = sg->packed.vscale;
-        for (int h = 0; h < L.n_heads; ++h) {
-            v.koff[h] = v.kblock;
-            v.voff[h] = v.vblock;
-            v.kbits[h] = L.kbits[h];
-            v.vbits[h] = L.vbits[h];
-            v.kblock += cap * L.head_dim * L.kbits[h] / 8;
-            v.vblock += cap * L.head_dim * L.vbits[h] / 8;
+    if (rope) {
+        st = check_rope_view(rope, L.head_dim);
+        if (st != TQ_OK) return st;
+    }
+    if (n_max == 0 || n_source == 0 || L.capacity == 0 || B == 0) return TQ_OK;
+    if (!K || !V || !(rows.t_begin || rows.slots) || (rope && !positions)) return TQ_ERR_ARG;
+    if (!aligned(K, 2) || !aligned(V, 2) || !aligned(rows.t_begin, 4) || !aligned(rows.slots, 4) || !aligned(rows.n_rows, 4) ||
+        !aligned(rows.index, 4) || (rope && !aligned(positions, 4)))
+        return TQ_ERR_ALIGN;
+    AppendParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.seg = seg_view(dst);
+    p.rows = rows;
+    p.rows.n_max = rows.index ? n_max : std::min(n_max, n_source);  // (row j is source row j)
+    p.rows.n_source = n_source;
+    if (rope) {
+        p.rope = rope_view(rope);
+        p.positions = positions;
+        p.pos_stride = pos_stride_b;
+    }
+    p.K = static_cast<const uint16_t *>(K);
+    p.V = static_cast<const uint16_t *>(V);
+    for (int i = 0; i < 3; ++i) {
+        p.ks[i] = k_stride[i];
+        p.vs[i] = v_stride[i];
+    }
+    p.B = B;
+    p.H = L.n_heads;
+    p.d = L.head_dim;
+    if (packed) {
+        std::memcpy(p.sign_bits, rot->sign_bits, sizeof(p.sign_bits));
+        p.inv_sqrt_d = rotation_scale(p.d);
+        p.law = L.value_law;
+        try {
+            value_thresholds(p.thr, L.vbits, p.H, L.value_law);
+        } catch (...) {
+            return TQ_ERR_SIZE;  // no host memory for the codebook fit
         }
     }
-    return v;
+    return launched(launch_append(p, static_cast<cudaStream_t>(stream)));
 }
 
-bool any_sketch(const tq_segment_layout &L) {
-    for (int h = 0; h < L.n_heads; ++h)
-        if (L.qjl[h] || L.qjl_v[h]) return true;
-    return false;
+// A read of n_max rows of each of B sequences from the places that `rows` gives.
+tq_status read_rows(const tq_segment *src, const tq_rotation *rot, int B, int n_max, const RowMap &rows, int dtype, void *K,
+                    const int64_t *k_stride, void *V, const int64_t *v_stride, void *stream) {
+    const tq_status st = check_segment(src, true);
+    if (st != TQ_OK) return st;
+    const tq_segment_layout &L = src->layout;
+    const bool packed = src->kind == TQ_SEG_PACKED;
+    if (dtype < TQ_DTYPE_F16 || dtype > TQ_DTYPE_F32 || n_max < 0) return TQ_ERR_ARG;
+    if (packed) {
+        if (rot && rot->head_dim != L.head_dim) return TQ_ERR_ARG;
+        if ((rot && rot->dense) || sphere_elsewhere(L)) return TQ_ERR_UNSUPPORTED;
+    }
+    if ((K && !k_stride) || (V && !v_stride)) return TQ_ERR_ARG;
+    if (n_max == 0 || L.capacity == 0 || B == 0 || (!K && !V)) return TQ_OK;
+    if (!rows.t_begin && !rows.slots) return TQ_ERR_ARG;
+    const size_t elem = dtype == TQ_DTYPE_F32 ? 4 : 2;
+    if (!aligned(K, elem) || !aligned(V, elem) || !aligned(rows.t_begin, 4) || !aligned(rows.slots, 4) || !aligned(rows.n_rows, 4))
+        return TQ_ERR_ALIGN;
+    ReadParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.seg = seg_view(src);
+    p.rows = rows;
+    p.rows.n_max = n_max;
+    p.K = K;
+    p.V = V;
+    for (int i = 0; i < 3; ++i) {
+        p.ks[i] = K ? k_stride[i] : 0;
+        p.vs[i] = V ? v_stride[i] : 0;
+    }
+    p.B = B;
+    p.H = L.n_heads;
+    p.d = L.head_dim;
+    if ((K && !rows_apart(p.ks, p.B, p.H, n_max, p.d)) || (V && !rows_apart(p.vs, p.B, p.H, n_max, p.d)))
+        return TQ_ERR_ARG;
+    if (packed) {
+        p.rotate = rot != nullptr;
+        if (rot) std::memcpy(p.sign_bits, rot->sign_bits, sizeof(p.sign_bits));
+        p.inv_sqrt_d = rotation_scale(p.d);
+        try {
+            value_centroids(p.centroid, L.vbits, p.H, L.value_law);
+        } catch (...) {
+            return TQ_ERR_SIZE;
+        }
+    }
+    return launched(launch_read(p, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+RowMap ragged_rows(const int *t_begin, const int *n_rows) {
+    RowMap m;
+    std::memset(&m, 0, sizeof(m));
+    m.t_begin = t_begin;
+    m.n_rows = n_rows;
+    return m;
+}
+
+// Rows by slot; a slot counts the tokens of the pool in 32 bits.
+tq_status slot_rows(const tq_segment *pool, int batch, const int *slots, int64_t slot_stride, const int *n_rows, RowMap &m) {
+    if (!pool || batch < 0) return TQ_ERR_ARG;
+    const tq_segment_layout &L = pool->layout;
+    if (L.batch > 0 && L.capacity > 0x7fffffff / L.batch) return TQ_ERR_UNSUPPORTED;
+    m = ragged_rows(nullptr, n_rows);
+    m.slots = slots;
+    m.slot_stride = slot_stride;
+    m.n_blocks = L.batch;
+    return TQ_OK;
 }
 
 // ---------------------------------------------------------------- tree attention
@@ -296,104 +330,37 @@ tq_status tq_append(const tq_segment *dst, const tq_rotation *rot, const tq_rope
                     int64_t pos_stride_b, const void *K, const int64_t *k_stride, const void *V,
                     const int64_t *v_stride, int n_source, int n_max, const int *t_begin, const int *n_new,
                     const int *index, int64_t index_stride_b, void *stream) {
-    tq_status st = check_segment(dst, true);
-    if (st != TQ_OK) return st;
-    const tq_segment_layout &L = dst->layout;
-    const bool packed = dst->kind == TQ_SEG_PACKED;
-    if (n_source < 0 || n_max < 0 || !k_stride || !v_stride) return TQ_ERR_ARG;
-    if (packed) {
-        if (!rot || rot->head_dim != L.head_dim) return TQ_ERR_ARG;
-        if (rot->dense || any_sketch(L) || sphere_elsewhere(L)) return TQ_ERR_UNSUPPORTED;
-    }
-    if (rope) {
-        st = check_rope_view(rope, L.head_dim);
-        if (st != TQ_OK) return st;
-    }
-    if (n_max == 0 || n_source == 0 || L.capacity == 0) return TQ_OK;
-    if (!K || !V || !t_begin || (rope && !positions)) return TQ_ERR_ARG;
-    if (!aligned(K, 2) || !aligned(V, 2) || !aligned(t_begin, 4) || !aligned(n_new, 4) || !aligned(index, 4) ||
-        (rope && !aligned(positions, 4)))
-        return TQ_ERR_ALIGN;
-    AppendParams p;
-    std::memset(&p, 0, sizeof(p));
-    p.seg = seg_view(dst);
-    p.rows.t_begin = t_begin;
-    p.rows.n_rows = n_new;
-    p.rows.index = index;
-    p.rows.index_stride = index_stride_b;
-    p.rows.n_max = index ? n_max : std::min(n_max, n_source);  // (row j is source row j)
-    p.rows.n_source = n_source;
-    if (rope) {
-        p.rope = rope_view(rope);
-        p.positions = positions;
-        p.pos_stride = pos_stride_b;
-    }
-    p.K = static_cast<const uint16_t *>(K);
-    p.V = static_cast<const uint16_t *>(V);
-    for (int i = 0; i < 3; ++i) {
-        p.ks[i] = k_stride[i];
-        p.vs[i] = v_stride[i];
-    }
-    p.B = L.batch;
-    p.H = L.n_heads;
-    p.d = L.head_dim;
-    if (packed) {
-        std::memcpy(p.sign_bits, rot->sign_bits, sizeof(p.sign_bits));
-        p.inv_sqrt_d = rotation_scale(p.d);
-        p.law = L.value_law;
-        try {
-            value_thresholds(p.thr, L.vbits, p.H, L.value_law);
-        } catch (...) {
-            return TQ_ERR_SIZE;  // no host memory for the codebook fit
-        }
-    }
-    return launched(launch_append(p, static_cast<cudaStream_t>(stream)));
+    RowMap m = ragged_rows(t_begin, n_new);
+    m.index = index;
+    m.index_stride = index_stride_b;
+    return append_rows(dst, rot, rope, positions, pos_stride_b, K, k_stride, V, v_stride, dst ? dst->layout.batch : 0, n_source,
+                       n_max, m, stream);
 }
 
 tq_status tq_read(const tq_segment *src, const tq_rotation *rot, int n_max, const int *t_begin, const int *n_read,
                   int dtype, void *K, const int64_t *k_stride, void *V, const int64_t *v_stride, void *stream) {
-    const tq_status st = check_segment(src, true);
+    return read_rows(src, rot, src ? src->layout.batch : 0, n_max, ragged_rows(t_begin, n_read), dtype, K, k_stride, V, v_stride,
+                     stream);
+}
+
+tq_status tq_paged_append(const tq_segment *pool, const tq_rotation *rot, const tq_rope_view *rope, const int *positions,
+                          int64_t pos_stride_b, const void *K, const int64_t *k_stride, const void *V,
+                          const int64_t *v_stride, int batch, int n_source, int n_max, const int *slots,
+                          int64_t slot_stride_b, const int *n_new, const int *index, int64_t index_stride_b, void *stream) {
+    RowMap m;
+    const tq_status st = slot_rows(pool, batch, slots, slot_stride_b, n_new, m);
     if (st != TQ_OK) return st;
-    const tq_segment_layout &L = src->layout;
-    const bool packed = src->kind == TQ_SEG_PACKED;
-    if (dtype < TQ_DTYPE_F16 || dtype > TQ_DTYPE_F32 || n_max < 0) return TQ_ERR_ARG;
-    if (packed) {
-        if (rot && rot->head_dim != L.head_dim) return TQ_ERR_ARG;
-        if ((rot && rot->dense) || sphere_elsewhere(L)) return TQ_ERR_UNSUPPORTED;
-    }
-    if ((K && !k_stride) || (V && !v_stride)) return TQ_ERR_ARG;
-    if (n_max == 0 || L.capacity == 0 || (!K && !V)) return TQ_OK;
-    if (!t_begin) return TQ_ERR_ARG;
-    const size_t elem = dtype == TQ_DTYPE_F32 ? 4 : 2;
-    if (!aligned(K, elem) || !aligned(V, elem) || !aligned(t_begin, 4) || !aligned(n_read, 4)) return TQ_ERR_ALIGN;
-    ReadParams p;
-    std::memset(&p, 0, sizeof(p));
-    p.seg = seg_view(src);
-    p.rows.t_begin = t_begin;
-    p.rows.n_rows = n_read;
-    p.rows.n_max = n_max;
-    p.K = K;
-    p.V = V;
-    for (int i = 0; i < 3; ++i) {
-        p.ks[i] = K ? k_stride[i] : 0;
-        p.vs[i] = V ? v_stride[i] : 0;
-    }
-    p.B = L.batch;
-    p.H = L.n_heads;
-    p.d = L.head_dim;
-    if ((K && !rows_apart(p.ks, p.B, p.H, n_max, p.d)) || (V && !rows_apart(p.vs, p.B, p.H, n_max, p.d)))
-        return TQ_ERR_ARG;
-    if (packed) {
-        p.rotate = rot != nullptr;
-        if (rot) std::memcpy(p.sign_bits, rot->sign_bits, sizeof(p.sign_bits));
-        p.inv_sqrt_d = rotation_scale(p.d);
-        try {
-            value_centroids(p.centroid, L.vbits, p.H, L.value_law);
-        } catch (...) {
-            return TQ_ERR_SIZE;
-        }
-    }
-    return launched(launch_read(p, dtype, static_cast<cudaStream_t>(stream)));
+    m.index = index;
+    m.index_stride = index_stride_b;
+    return append_rows(pool, rot, rope, positions, pos_stride_b, K, k_stride, V, v_stride, batch, n_source, n_max, m, stream);
+}
+
+tq_status tq_paged_read(const tq_segment *pool, const tq_rotation *rot, int batch, int n_max, const int *slots,
+                        int64_t slot_stride_b, const int *n_read, int dtype, void *K, const int64_t *k_stride, void *V,
+                        const int64_t *v_stride, void *stream) {
+    RowMap m;
+    const tq_status st = slot_rows(pool, batch, slots, slot_stride_b, n_read, m);
+    return st == TQ_OK ? read_rows(pool, rot, batch, n_max, m, dtype, K, k_stride, V, v_stride, stream) : st;
 }
 
 tq_status tq_tree_workspace_size(const tq_layer_view *layer, int batch, int n_heads, int q_heads, int head_dim,

@@ -1369,6 +1369,13 @@ cudaError_t tree_rows(const TreeParams &p, const TreeLevels &lv, cudaStream_t s)
 // The least power of two that holds the rows, up to 64.
 int tree_mma_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
+void value_levels(int law, int bits, const float *centroid, uint16_t *half, float *inv) {
+    HostLevels &hl = g_levels[law][bits];
+    std::call_once(hl.once, [&] { fit_levels(hl, centroid, bits); });
+    std::memcpy(half, hl.half, sizeof(uint16_t) << bits);
+    *inv = hl.inv;
+}
+
 cudaError_t launch_tree_mma(const TreeParams &p, cudaStream_t s) {
     TreeLevels lv;
     std::memset(&lv, 0, sizeof(lv));
@@ -1376,10 +1383,7 @@ cudaError_t launch_tree_mma(const TreeParams &p, cudaStream_t s) {
         for (int h = 0; h < p.H; h++) {
             const int vb = p.seg[i].seg.vbits[h], law = p.seg[i].law;
             if (lv.inv[law][vb] != 0.f) continue;
-            HostLevels &hl = g_levels[law][vb];
-            std::call_once(hl.once, [&] { fit_levels(hl, p.centroid[law] + cb_off(vb), vb); });
-            std::memcpy(lv.half[law] + cb_off(vb), hl.half, sizeof(uint16_t) << vb);
-            lv.inv[law][vb] = hl.inv;
+            value_levels(law, vb, p.centroid[law] + cb_off(vb), lv.half[law] + cb_off(vb), &lv.inv[law][vb]);
         }
     return p.d == 128 ? tree_rows<128>(p, lv, s) : tree_rows<64>(p, lv, s);
 }

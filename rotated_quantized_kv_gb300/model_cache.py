@@ -18,6 +18,7 @@ packed prompt, and an fp16 buffer of decode tokens that is compressed every
 algorithmic bytes a decode step reads.  `SpeculativeCache` serves a batch whose
 sequences differ in length: prompts are written from the unrotated keys, trees of
 drafted tokens attend to it, and what the verification accepts is written into it.
+`PagedCache` serves sequences that come and go from pools of pages, a token a step.
 """
 from __future__ import annotations
 
@@ -337,6 +338,12 @@ class SpeculativeCache:
         lens = ([self.head_len] if self.sinks else []) + [self.body_len]
         T.tq_tree_attention(self.views[l], q, k, v, out, self.workspace, mask=mask, seg_len=lens, stream=stream)
 
+    def verify(self, tokens, target, uniform, draft=None, parents=None, stream=None):
+        """(accepted [B][N], n_accepted [B], token [B]): the path of drafts (int32 tokens [B][N]) that the target's
+        probabilities [B][N + 1][V] and the random numbers [B][N + 1] accept, as `commit` and `advance` take it, and the
+        token behind it; draft and parents as tq_verify takes them."""
+        return T.tq_verify(tokens, target, uniform, draft=draft, parents=parents, stream=stream)
+
     def commit(self, l, k, v, index, n, stream=None):
         """The n[b] <= N accepted drafts index[b][:] (int32 [B][N]; a path of the tree from its
         root) behind layer l's tokens: k, v as `attend` left them."""
@@ -360,6 +367,65 @@ class SpeculativeCache:
                 T.tq_read(self.head[l], None, first, n_max, n_read=self.head_len - first, out=out)
             T.tq_read(self.body[l], self.rot[l], first - self.sinks, n_max, n_read=self.length - first, out=out)
         return out
+
+
+class PagedCache:
+    """Sequences that come and go, their tokens on pages of one pool a layer (kbits, vbits; None: fp16 pages).
+
+    The rows of the batch are places for sequences; row b holds length[b] tokens, none where it is free.  A step is
+    `grow` (places for the new tokens of every row: a prompt's where a sequence enters, one where it goes on), for each
+    layer `write` (the new keys, rotated by their positions, and values) and `attend` (one query token a row), and `release`
+    where sequences end or are cut.  Lengths, page table and the stack of free pages stay on the device and no call waits for it, so
+    that a step can be captured into a CUDA graph.  Tokens that find no page are not stored: `grow` says how
+    many each row was granted.  `stream` as in SpeculativeCache."""
+
+    def __init__(self, layers: int, batch: int, kv_heads: int, q_heads: int, head_dim: int, n_pages: int, max_pages: int,
+                 rope: T.Rope, kbits=3, vbits=3, page: int = 64, seed: int = 42, device="cuda"):
+        if page % 16 or page < 16:
+            raise ValueError("page is a multiple of 16")
+        self.layers, self.B, self.H, self.Hq, self.d, self.page, self.rope = layers, batch, kv_heads, q_heads, head_dim, page, rope
+        widths = lambda b: [b] * kv_heads if isinstance(b, int) else list(b)
+        self.rot, self.pool, self.views = [], [], []
+        for l in range(layers):
+            self.rot.append(T.tq_make_rotation(head_dim, seed + l))
+            if kbits is None:
+                self.pool.append(T.Fp16Segment(n_pages, kv_heads, head_dim, page, device, n_tokens=page))
+            else:
+                layout = T.make_layout(n_pages, kv_heads, head_dim, page, widths(kbits), widths(vbits))
+                self.pool.append(T.PackedSegment(layout, device, n_tokens=page))
+            self.views.append(T.layer_view(self.rot[l], [self.pool[l]]))
+        i32 = dict(dtype=torch.int32, device=device)
+        self.length = torch.zeros(batch, **i32)
+        self.table = torch.full((batch, max_pages), -1, **i32)
+        self.free = torch.arange(n_pages, **i32)           # the stack of free pages
+        self.n_free = torch.full((1,), n_pages, **i32)
+        self.workspace = torch.empty(T.tq_paged_workspace_size(self.views[0], batch, kv_heads, q_heads, head_dim),
+                                     dtype=torch.uint8, device=device)
+
+    def grow(self, n, n_max, stream=None):
+        """Places for n[b] <= n_max new tokens of each row (int32 [B]): (slots, positions [B][n_max], granted [B])."""
+        return T.tq_page_tables(self.table, self.length, n, self.free, self.n_free, self.page, n_max, stream=stream)
+
+    def write(self, l, K, V, slots, positions, stream=None):
+        """The new tokens of layer l: K without positions, V (fp16 [B][H][S][d], S at least the slots' width),
+        with `grow`'s slots and positions."""
+        S = slots.shape[1]
+        T.tq_paged_append(self.pool[l], self.rot[l], K[:, :, :S], V[:, :, :S], slots, rope=self.rope, positions=positions,
+                          stream=stream)
+
+    def attend(self, l, q, positions, out, stream=None):
+        """Layer l's attention of one token a row, over all that the row holds: q fp16 [B][Hq][d] is rotated in place
+        by positions (int32 [B]), out fp16 [B][Hq][d]."""
+        T.tq_rope(self.rope, positions[:, None], q[:, :, None], stream=stream)
+        T.tq_paged_attention(self.views[l], q, out, self.workspace, [self.table], [self.length], stream=stream)
+
+    def release(self, keep, stream=None):
+        """Rows cut to keep[b] tokens (int32 [B]; 0: free, the length or more: as it was)."""
+        T.tq_page_release(self.table, self.length, keep, self.free, self.n_free, self.page, stream=stream)
+
+    def read(self, l, slots, dtype=torch.float16, stream=None):
+        """Layer l's rows at `slots` (int32 [B][n], -1: zeros) as vectors, [k, v], each [B][H][n][d]."""
+        return T.tq_paged_read(self.pool[l], self.rot[l], slots, dtype=dtype, stream=stream)
 
 
 def record_offsets(seg: T.PackedSegment, which: str, b: int, h: int, t: np.ndarray) -> np.ndarray:

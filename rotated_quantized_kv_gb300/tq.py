@@ -9,7 +9,9 @@ Functions keep the C names: ``tq_make_rotation``, ``tq_fit_codebook``,
 ``tq_make_qjl``, ``tq_packed_size``, ``tq_compress``, ``tq_dequantize``,
 ``tq_age_tiers``, ``tq_decode_workspace_size``, ``tq_decode_attention``, and
 the serving calls ``tq_rope_table``, ``tq_rope``, ``tq_append``, ``tq_read``,
-``tq_tree_workspace_size``, ``tq_tree_attention``.
+``tq_tree_workspace_size``, ``tq_tree_attention``, and those on pages and drafts
+``tq_page_tables``, ``tq_page_release``, ``tq_paged_append``, ``tq_paged_read``,
+``tq_paged_workspace_size``, ``tq_paged_attention``, ``tq_verify``.
 Errors come back as ``TQError`` carrying the status and its message.
 """
 from __future__ import annotations
@@ -56,7 +58,8 @@ EXPORTED = ["tq_status_string", "tq_last_cuda_error", "tq_version", "tq_make_rot
             "tq_set_decode_kernel_events", "tq_decode_attention_static", "tq_decode_error_flag",
             "tq_requantize", "tq_fit_codebook_sphere", "tq_make_haar_rotation", "tq_compress_error_flag", "tq_decode_last_launches",
             "tq_set_decode_wait_polls", "tq_value_code_table", "tq_rope_frequencies", "tq_rope_table", "tq_rope",
-            "tq_append", "tq_read", "tq_tree_workspace_size", "tq_tree_attention"]
+            "tq_append", "tq_read", "tq_tree_workspace_size", "tq_tree_attention", "tq_page_tables", "tq_page_release",
+            "tq_paged_append", "tq_paged_read", "tq_paged_workspace_size", "tq_paged_attention", "tq_verify"]
 
 TQ_DTYPE_F16, TQ_DTYPE_BF16, TQ_DTYPE_F32 = 0, 1, 2
 TQ_ROPE_SCALE_NONE, TQ_ROPE_SCALE_LINEAR, TQ_ROPE_SCALE_BASE, TQ_ROPE_SCALE_TURNS, TQ_ROPE_SCALE_INDEX = range(5)
@@ -131,6 +134,20 @@ class tq_tree(ctypes.Structure):
                 ("seg_len", ctypes.c_void_p * TQ_MAX_SEGMENTS), ("out", ctypes.c_void_p)]
 
 
+class tq_pages(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("table_stride_b", ctypes.c_int64), ("max_pages", ctypes.c_int),
+                ("len", ctypes.c_void_p)]
+
+
+class tq_verification(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("batch", "n_drafts", "vocab", "dtype")] + [
+        ("tokens", ctypes.c_void_p), ("tokens_stride_b", ctypes.c_int64), ("parents", ctypes.c_void_p),
+        ("parents_stride_b", ctypes.c_int64), ("target", ctypes.c_void_p), ("target_stride", ctypes.c_int64 * 2),
+        ("draft", ctypes.c_void_p), ("draft_stride", ctypes.c_int64 * 2), ("uniform", ctypes.c_void_p),
+        ("uniform_stride_b", ctypes.c_int64), ("accepted", ctypes.c_void_p), ("n_accepted", ctypes.c_void_p),
+        ("token", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _L = ctypes.c_int64
@@ -176,6 +193,15 @@ _lib.tq_tree_workspace_size.argtypes = [ctypes.POINTER(tq_layer_view), _I, _I, _
                                         ctypes.POINTER(ctypes.c_size_t)]
 _lib.tq_tree_attention.argtypes = [ctypes.POINTER(tq_layer_view), _I, _I, _I, _I, _P, _P,
                                    ctypes.c_size_t, _P]
+_lib.tq_page_tables.argtypes = [_I, _I, _I, _I, _P, _L, _P, _P, _I, _P, _P, _P, _P, _P, _P]
+_lib.tq_page_release.argtypes = [_I, _I, _I, _I, _P, _L, _P, _P, _P, _P, _P]
+_lib.tq_paged_append.argtypes = [_P, ctypes.POINTER(tq_rotation), ctypes.POINTER(tq_rope_view), _P, _L,
+                                 _P, _P, _P, _P, _I, _I, _I, _P, _L, _P, _P, _L, _P]
+_lib.tq_paged_read.argtypes = [_P, ctypes.POINTER(tq_rotation), _I, _I, _P, _L, _P, _I, _P, _P, _P, _P, _P]
+_lib.tq_paged_workspace_size.argtypes = [ctypes.POINTER(tq_layer_view), _I, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]
+_lib.tq_paged_attention.argtypes = [ctypes.POINTER(tq_layer_view), _P, _I, _I, _I, _I, _P, _P, _P, _P,
+                                    ctypes.c_size_t, _P]
+_lib.tq_verify.argtypes = [_P, _P]
 TQ_STATIC_WORKSPACE_BYTES = 16 << 20
 for _n in EXPORTED:
     if _n not in ("tq_status_string", "tq_last_cuda_error", "tq_version", "tq_decode_last_launches"):
@@ -780,4 +806,221 @@ def tq_tree_attention(view: tq_layer_view, q: torch.Tensor, k: torch.Tensor, v: 
                       mask_ptr, mask_stride, *lens, out.data_ptr())
     _call(tensors, stream, where, _lib.tq_tree_attention, ctypes.byref(view), B, H, Hq, d, tree, workspace.data_ptr(),
           workspace.numel() * workspace.element_size())
+    return out
+
+
+# ----------------------------------------------------------------- pages
+_pack2 = struct.Struct("2q").pack
+_pack_pages = [struct.Struct("PqixxxxP" * n).pack for n in range(TQ_MAX_SEGMENTS + 1)]
+_pack_verification = struct.Struct("4iPqPqP2qP2qPqPPP").pack
+assert struct.calcsize("PqixxxxP") == ctypes.sizeof(tq_pages)
+assert struct.calcsize("4iPqPqP2qP2qPqPPP") == ctypes.sizeof(tq_verification)
+
+
+def _page_args(table, length, count, free_pages, n_free, where):
+    B = length.shape[0]
+    _require(table.dim() == 2 and length.dim() == 1 and free_pages.dim() == 1, where)
+    _int32(table, where, (B, table.shape[1]))
+    _int32(length, where, (B,))
+    _int32(count, where, (B,))
+    _int32(free_pages, where, (free_pages.shape[0],))
+    _int32(n_free, where, (1,))
+    return B, table.shape[1], table.stride(0) if B > 1 else table.shape[1]
+
+
+def tq_page_tables(table: torch.Tensor, length: torch.Tensor, n_new: torch.Tensor, free_pages: torch.Tensor,
+                   n_free: torch.Tensor, page_size: int, n_max: int, out=None, stream=None):
+    """Places for min(n_new[b], n_max) new tokens of each sequence: pages from the stack
+    free_pages[:n_free] (int32 [n_pages], [1]) into `table` (int32 [B][max_pages]), length (int32
+    [B]) advanced by what was granted.  Returns (slots, positions [B][n_max], granted [B]), int32, -1 behind the
+    granted rows; `out`: these three, the first two may be None (not wanted)."""
+    where = "tq_page_tables"
+    B, width, stride = _page_args(table, length, n_new, free_pages, n_free, where)
+    if out is None:
+        _require(n_max >= 0 and table.is_cuda, where)
+        with on_stream(stream, table.device):
+            new = lambda *shape: torch.empty(shape, dtype=_I32, device=table.device)  # noqa: E731
+            out = (new(B, n_max), new(B, n_max), new(B))
+    slots, positions, granted = out
+    _int32(granted, where, (B,))
+    for t in (slots, positions):
+        _require(t is None or (t.dtype == _I32 and t.shape == (B, n_max) and t.is_contiguous()), where)
+    _call([table, length, n_new, free_pages, n_free, granted, slots, positions], stream, where, _lib.tq_page_tables, B,
+          page_size, width, free_pages.shape[0], table.data_ptr(), stride, length.data_ptr(), n_new.data_ptr(), n_max,
+          free_pages.data_ptr(), n_free.data_ptr(), _ptr(slots), _ptr(positions), granted.data_ptr())
+    return out
+
+
+def tq_page_release(table: torch.Tensor, length: torch.Tensor, keep: torch.Tensor, free_pages: torch.Tensor,
+                    n_free: torch.Tensor, page_size: int, stream=None):
+    """Sequences cut to min(length[b], keep[b]) tokens (int32 [B]; 0: ended): the pages behind go back onto the
+    stack.  Tensors as tq_page_tables takes them."""
+    where = "tq_page_release"
+    B, width, stride = _page_args(table, length, keep, free_pages, n_free, where)
+    _call([table, length, keep, free_pages, n_free], stream, where, _lib.tq_page_release, B, page_size, width,
+          free_pages.shape[0], table.data_ptr(), stride, length.data_ptr(), keep.data_ptr(), free_pages.data_ptr(),
+          n_free.data_ptr())
+
+
+def tq_paged_append(pool, rot: tq_rotation | None, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, n_new=None,
+                    index=None, n_max: int | None = None, rope: Rope | None = None, positions=None, stream=None):
+    """Write rows of K, V (fp16 CUDA [B][H][S][d], unit stride in d) into the pages of `pool` (PackedSegment
+    or Fp16Segment of n_pages x page size): row j < min(n_new[b], n_max) of sequence b is source row
+    index[b][j] (None: j) and goes to slot slots[b][j] (int32 [B][>= n_max]; outside the pool: skipped).  n_max: default
+    the index's width, else the slots' width.  rope, positions, and all else, as tq_append."""
+    where = "tq_paged_append"
+    L = pool.layout
+    shape = K.shape
+    _require(len(shape) == 4 and shape == V.shape and K.dtype == _F16 and V.dtype == _F16 and shape[1] == L.n_heads and
+             shape[3] == L.head_dim, where)
+    a, b = K.stride(), V.stride()
+    B, S = shape[0], shape[2]
+    _require(a[3] == 1 and b[3] == 1 and slots.dim() == 2, where)
+    if n_max is None:
+        n_max = index.shape[1] if index is not None else slots.shape[1]
+    _int32(slots, where, (B, slots.shape[1]))
+    _require(slots.shape[1] >= n_max, where)
+    tensors = [K, V, slots, pool.kcodes if pool.kind == TQ_SEG_PACKED else pool.k]
+    n_ptr = index_ptr = pos_ptr = rope_ref = None
+    index_stride = ps = 0
+    if n_new is not None:
+        _int32(n_new, where, (B,))
+        n_ptr = n_new.data_ptr()
+        tensors.append(n_new)
+    if index is not None:
+        _require(index.dim() == 2 and index.shape[1] >= n_max, where)
+        _int32(index, where, (B, index.shape[1]))
+        index_ptr, index_stride = index.data_ptr(), index.stride(0)
+        tensors.append(index)
+    if rope is not None:
+        _require(positions is not None, where)
+        _int32(positions, where, (S,) if positions.dim() == 1 else (B, S))
+        ps = positions.stride(0) if positions.dim() == 2 else 0
+        pos_ptr, rope_ref = positions.data_ptr(), rope.ref
+        tensors += (positions, rope.table)
+    _call(tensors, stream, where, _lib.tq_paged_append, pool.reference(), ctypes.byref(rot) if rot is not None else None,
+          rope_ref, pos_ptr, ps, K.data_ptr(), _pack3(a[0], a[1], a[2]), V.data_ptr(), _pack3(b[0], b[1], b[2]), B, S, n_max,
+          slots.data_ptr(), slots.stride(0), n_ptr, index_ptr, index_stride)
+
+
+def tq_paged_read(pool, rot: tq_rotation | None, slots: torch.Tensor, n_read=None, out=None, dtype=torch.float16,
+                  stream=None):
+    """Rows of the pages of `pool` back as vectors: row j < min(n_read[b], n) of sequence b is slot slots[b][j] (int32
+    [B][n]; outside the pool: left as it is).  out, dtype and rot as tq_read takes them ([B][H][n][d])."""
+    where = "tq_paged_read"
+    L = pool.layout
+    _require(slots.dim() == 2, where)
+    B, n = slots.shape
+    _int32(slots, where, (B, n))
+    shape = (B, L.n_heads, n, L.head_dim)
+    own = pool.kcodes if pool.kind == TQ_SEG_PACKED else pool.k
+    if out is None:
+        _require(own.is_cuda, where)
+        with on_stream(stream, own.device):  # behind this the kernel writes them
+            out = [torch.zeros(shape, dtype=dtype, device=own.device) for _ in range(2)]
+    k, v = out
+    some = [t for t in (k, v) if t is not None]
+    tensors = [slots, own, *some]
+    n_ptr = None
+    if n_read is not None:
+        _int32(n_read, where, (B,))
+        n_ptr = n_read.data_ptr()
+        tensors.append(n_read)
+    if not some:
+        return out
+    dt = some[0].dtype
+    _require(dt in _DTYPE, where)
+    args = []
+    for t in (k, v):
+        if t is None:
+            args += (None, None)
+            continue
+        a = t.stride()
+        _require(t.shape == shape and t.dtype == dt and a[3] == 1, where)
+        args += (t.data_ptr(), _pack3(a[0], a[1], a[2]))
+    _call(tensors, stream, where, _lib.tq_paged_read, pool.reference(), ctypes.byref(rot) if rot is not None else None, B, n,
+          slots.data_ptr(), slots.stride(0), n_ptr, _DTYPE[dt], *args)
+    return out
+
+
+def tq_paged_workspace_size(view: tq_layer_view, batch: int, n_heads: int, q_heads: int, head_dim: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.tq_paged_workspace_size(ctypes.byref(view), batch, n_heads, q_heads, head_dim, ctypes.byref(n)),
+           "tq_paged_workspace_size")
+    return n.value
+
+
+def tq_paged_attention(view: tq_layer_view, q: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor, tables, lens,
+                       stream=None):
+    """out[b][j] = attention of one new token, query head j, over the tokens that sequence b holds of the segments of
+    `view`.  q fp16 [B][Hq][d] (unit stride in d), out fp16 [B][Hq][d] contiguous.  tables: per segment int32
+    [B][max_pages] (the segment is a pool of pages) or None (it holds sequence b in its batch element b); lens: per
+    segment int32 [B] (None: all n_tokens of a segment without a table)."""
+    where = "tq_paged_attention"
+    _require(q.dim() == 3, where)
+    B, Hq, d = q.shape
+    n = view.n_segments
+    _require(q.dtype == _F16 and out.dtype == _F16 and out.shape == q.shape and out.is_contiguous() and
+             workspace.is_contiguous() and (d == 1 or q.stride(2) == 1) and len(tables) == n and len(lens) == n, where)
+    tensors = [q, out, workspace]
+    fields = []
+    for t, c in zip(tables, lens):
+        at = stride = width = 0
+        if t is not None:
+            _require(t.dim() == 2 and c is not None, where)
+            width = t.shape[1]
+            _int32(t, where, (B, width))
+            at, stride = t.data_ptr(), t.stride(0) if B > 1 else width
+            tensors.append(t)
+        if c is not None:
+            _int32(c, where, (B,))
+            tensors.append(c)
+        fields += (at, stride, width, 0 if c is None else c.data_ptr())
+    H = view.seg[0].layout.n_heads if n else Hq
+    _call(tensors, stream, where, _lib.tq_paged_attention, ctypes.byref(view), _pack_pages[n](*fields), B, H, Hq, d,
+          q.data_ptr(), _pack2(q.stride(0), q.stride(1)), out.data_ptr(), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+    return out
+
+
+# ----------------------------------------------------------------- verification of drafts
+def tq_verify(tokens: torch.Tensor, target: torch.Tensor, uniform: torch.Tensor, draft: torch.Tensor | None = None,
+              parents: torch.Tensor | None = None, out=None, stream=None):
+    """Verify drafted tokens (int32 [B][N]; outside the vocabulary: no candidate) against the target's
+    probabilities (fp16, bf16 or fp32 [B][N + 1][V]: row 0 behind the last cached token, row i + 1 behind draft i) from
+    given random numbers (float32 [B][N + 1], the last for the final token).  draft: the distributions that the drafts were
+    drawn from ([B][>= N][V], row 0 the root's children, row i + 1 those of draft i), None: drafts that stand for
+    themselves.  parents: int32 [B][N] or [N] (tree_mask takes the same), None: a chain.  Returns (accepted [B][N], n_accepted
+    [B], token [B]), int32: the path of accepted drafts (-1 behind it) and the token that follows it."""
+    where = "tq_verify"
+    _require(tokens.dim() == 2 and target.dim() == 3 and uniform.dim() == 2, where)
+    B, N = tokens.shape
+    V = target.shape[2]
+    _int32(tokens, where, (B, N))
+    _require(target.dtype in _DTYPE and target.shape == (B, N + 1, V) and (V == 1 or target.stride(2) == 1), where)
+    _require(uniform.dtype == torch.float32 and uniform.shape == (B, N + 1) and (N == 0 or uniform.stride(1) == 1), where)
+    tensors = [target, tokens, uniform]
+    q_ptr = par_ptr = par_stride = 0
+    q_stride = (0, 0)
+    if draft is not None:
+        _require(draft.dtype == target.dtype and draft.dim() == 3 and draft.shape[0] == B and draft.shape[1] >= N and
+                 draft.shape[2] == V and (V == 1 or draft.stride(2) == 1), where)
+        q_ptr, q_stride = draft.data_ptr(), draft.stride()[:2]
+        tensors.append(draft)
+    if parents is not None:
+        _int32(parents, where, (N,) if parents.dim() == 1 else (B, N))
+        par_ptr, par_stride = parents.data_ptr(), parents.stride(0) if parents.dim() == 2 else 0
+        tensors.append(parents)
+    if out is None:
+        _require(target.is_cuda, where)
+        with on_stream(stream, target.device):
+            out = tuple(torch.empty(s, dtype=_I32, device=target.device) for s in ((B, N), (B,), (B,)))
+    for t, s in zip(out, ((B, N), (B,), (B,))):
+        _require(t.dtype == _I32 and t.shape == s and t.is_contiguous(), where)
+        tensors.append(t)
+    accepted, count, token = out
+    _call(tensors, stream, where, _lib.tq_verify,
+          _pack_verification(B, N, V, _DTYPE[target.dtype], tokens.data_ptr(), tokens.stride(0), par_ptr, par_stride,
+                             target.data_ptr(), target.stride(0), target.stride(1), q_ptr, q_stride[0], q_stride[1],
+                             uniform.data_ptr(), uniform.stride(0), accepted.data_ptr(), count.data_ptr(), token.data_ptr()))
     return out
