@@ -26,7 +26,8 @@ CUDA_SOURCES = ["tq_compress.cu", "tq_compress_dense.cu", "tq_decode.cu", "tq_ma
                 "tq_tree_mma.cu", "tq_append_rows_keys.cu", "tq_append_rows_values.cu", "tq_read_rows_keys.cu",
                 "tq_read_rows_values.cu",
                 "tq_read_rows_keys_d64.cu", "tq_read_rows_values_d64.cu", "tq_pages.cu", "tq_paged.cu",
-                "tq_verify.cu"] + [
+                "tq_paged_fp16.cu", "tq_verify.cu"] + [
+                f"tq_paged_kb{k}_d{d}.cu" for k in range(1, 9) for d in (128, 64)] + [
                 f"tq_decode_kb{k}.cu" for k in range(1, 9)] + [
                 f"tq_decode_wide_kb{k}.cu" for k in range(1, 9)]
 HOST_SOURCES = ["tq_host.cpp", "tq_serve_host.cpp", "tq_paged_host.cpp"]
@@ -44,7 +45,8 @@ def _sources():
         os.path.join(CSRC, h) for h in ("tq_internal.h", "tq_decode_common.cuh", "tq_decode_packed.cuh",
                                         "tq_mass.h", "tq_decode_geometry.h", "tq_compress_rows.cuh", "tq_serve.h",
                                         "tq_team.cuh", "tq_tree.cuh", "tq_row_map.cuh", "tq_append_rows.cuh",
-                                        "tq_read_rows.cuh", "tq_serve_args.h", "tq_paged.cuh")] + [
+                                        "tq_read_rows.cuh", "tq_serve_args.h", "tq_paged.cuh",
+                                        "tq_paged_mma.cuh")] + [
         os.path.join(ROOT, "include", "tq.h")]
 
 

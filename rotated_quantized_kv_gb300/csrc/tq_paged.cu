@@ -294,15 +294,56 @@ cudaError_t plain(const PagedParams &p, cudaStream_t s) {
 
 }  // namespace
 
-PagedShape paged_shape(int, int, int) { return {kPlainUnit, 2 * current_sm_count()}; }
-int paged_rows(int, int) { return kPlainRows; }
+#define TQ_PAGED_KB(KB)                                                       \
+    cudaError_t launch_paged_kb##KB##_np1(const PagedParams &p, cudaStream_t s);  \
+    cudaError_t launch_paged_kb##KB##_np2(const PagedParams &p, cudaStream_t s);  \
+    PagedShape paged_shape_kb##KB##_np1(int vb);                              \
+    PagedShape paged_shape_kb##KB##_np2(int vb);
+TQ_PAGED_KB(1)
+TQ_PAGED_KB(2)
+TQ_PAGED_KB(3)
+TQ_PAGED_KB(4)
+TQ_PAGED_KB(5)
+TQ_PAGED_KB(6)
+TQ_PAGED_KB(7)
+TQ_PAGED_KB(8)
+#undef TQ_PAGED_KB
+cudaError_t launch_paged_fp16(const PagedParams &p, cudaStream_t s);
+PagedShape paged_shape_fp16(int d);
+
+namespace {
+using PackedLaunch = cudaError_t (*)(const PagedParams &, cudaStream_t);
+using PackedShape = PagedShape (*)(int);
+#define TQ_PAGED_EACH(f, np)                                                                              \
+    { f##1_np##np, f##2_np##np, f##3_np##np, f##4_np##np, f##5_np##np, f##6_np##np, f##7_np##np, f##8_np##np }
+constexpr PackedLaunch kPackedLaunch[2][8] = {TQ_PAGED_EACH(launch_paged_kb, 1), TQ_PAGED_EACH(launch_paged_kb, 2)};
+constexpr PackedShape kPackedShape[2][8] = {TQ_PAGED_EACH(paged_shape_kb, 1), TQ_PAGED_EACH(paged_shape_kb, 2)};
+#undef TQ_PAGED_EACH
+
+// Head dims that take the tensor cores.
+bool on_tensor_cores(int d) { return d == 64 || d == 128; }
+}  // namespace
+
+PagedShape paged_shape(int d, int kb, int vb) {
+    PagedShape s = {kPlainUnit, 2};
+    if (on_tensor_cores(d)) s = kb ? kPackedShape[d == 64][kb - 1](vb) : paged_shape_fp16(d);
+    s.workers *= current_sm_count();
+    return s;
+}
+
+// Rows a block: a warp of the tensor-core form takes four (two of head_dim 64), a CTA has four
+// warps for blocks of rows or parts of the tokens.
+int paged_rows(int d, int g) {
+    if (!on_tensor_cores(d)) return kPlainRows;
+    const int per = d == 64 ? 2 : 4;
+    return g <= per ? per : g <= 2 * per ? 2 * per : 4 * per;
+}
 
 cudaError_t launch_paged(const PagedParams &p, cudaStream_t s) {
+    if (on_tensor_cores(p.d)) return p.cls.kb ? kPackedLaunch[p.d == 64][p.cls.kb - 1](p, s) : launch_paged_fp16(p, s);
     switch (p.d) {
         case 16: return plain<16>(p, s);
         case 32: return plain<32>(p, s);
-        case 64: return plain<64>(p, s);
-        case 128: return plain<128>(p, s);
         case 256: return plain<256>(p, s);
         case 512: return plain<512>(p, s);
         case 1024: return plain<1024>(p, s);

@@ -1,0 +1,4 @@
+// tq_paged_kb4_d128.cu -- attention over packed pages with 4-bit keys, head_dim 128 (every value width).
+#include "tq_paged_mma.cuh"
+
+TQ_INSTANTIATE_PAGED(4, 1)

@@ -300,7 +300,7 @@ struct PagedMergeParams {
     uint32_t sign_bits[kMaxD / 32];
     float inv_sqrt_d;
 };
-// A class's stage length and the most workers that its kernel runs at once.
+// A class's stage length and the most workers that its kernel runs at once (of the class's kernel: on an SM).
 struct PagedShape {
     int unit, workers;
 };
