@@ -63,12 +63,14 @@ __global__ void __launch_bounds__(kPlainThreads) paged_plain_kernel(const __grid
     asm volatile("griddepcontrol.launch_dependents;");
     if (threadIdx.x == 0) p.state[worker] = 0;
     const PagedList &l = p.list;
-    const Range r = range_of<kPlainThreads>(l, p.cls, worker, p.first, buf);
-    if (r.begin < r.end) {
-        Walk w = seek(l, p.cls, r.b, r.rest);
+    const int total = ranges_of<kPlainThreads, 1>(l, p.cls, worker, 0, p.first, buf);
+    int begin, end;
+    worker_range(p.cls, total, worker, begin, end);
+    if (begin < end) {
+        Walk w = seek(l, p.cls, buf[kPlainWarps], buf[kPlainWarps + 1]);
         float acc[R][DPT];
         bool fresh = true;
-        for (int at = r.begin; at < r.end; at++) {
+        for (int at = begin; at < end; at++) {
             if (fresh) {
                 __syncthreads();
                 for (int i = threadIdx.x; i < R; i += kPlainThreads) row_m[i] = -kInf, row_l[i] = 0.f;
@@ -147,7 +149,7 @@ __global__ void __launch_bounds__(kPlainThreads) paged_plain_kernel(const __grid
                 }
             }
             const Walk x = w;
-            const bool last = at + 1 == r.end;
+            const bool last = at + 1 == end;
             fresh = !last && next(l, p.cls, w);
             if (!fresh && !last) continue;
             __syncthreads();

@@ -121,14 +121,11 @@ __device__ __forceinline__ bool next(const PagedList &l, const PagedClass &c, Wa
     }
 }
 
-struct Range {
-    int total, begin, end;
-    int b, rest;         // sequence of stage `begin`, and stages of it before that
-};
-
-// The worker's range (THREADS threads, all of the CTA).  buf: THREADS / 32 + 2 ints of shared memory.
-template <int THREADS>
-__device__ __forceinline__ Range range_of(const PagedList &l, const PagedClass &c, int worker, int *first, int *buf) {
+// Ranges of a CTA's TEAMS workers, worker t * step + first_worker for team t (THREADS threads, all of the CTA;
+// synchronises).  buf: THREADS / 32 + 2 TEAMS ints of shared memory; team t's first sequence and the stages of it before
+// its range are at THREADS / 32 + 2 t.  Returns the total.
+template <int THREADS, int TEAMS>
+__device__ __forceinline__ int ranges_of(const PagedList &l, const PagedClass &c, int first_worker, int step, int *first, int *buf) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int chunk = (l.B + THREADS - 1) / THREADS, b0 = min(static_cast<int>(threadIdx.x) * chunk, l.B), b1 = min(b0 + chunk, l.B);
     int sum = 0;
@@ -146,7 +143,7 @@ __device__ __forceinline__ Range range_of(const PagedList &l, const PagedClass &
         if (w < warp) before += buf[w];
         total += buf[w];
     }
-    if (worker == 0) {
+    if (first_worker == 0) {
         int at = before;
         for (int b = b0; b < b1; b++) {
             first[b] = at;
@@ -154,24 +151,34 @@ __device__ __forceinline__ Range range_of(const PagedList &l, const PagedClass &
         }
         if (threadIdx.x == 0) first[l.B] = total;
     }
-    Range r;
-    r.total = total;
     const int workers = workers_of(c, total);
-    r.begin = worker < workers ? worker_begin(total, worker, workers) : total;
-    r.end = worker < workers ? worker_begin(total, worker + 1, workers) : total;
-    if (r.begin < r.end && before <= r.begin && r.begin < before + sum) {
-        int at = before, b = b0;
-        for (int n; b + 1 < b1 && r.begin >= at + (n = sequence_stages(l, c, b)); b++) at += n;
-        buf[THREADS / 32] = b;
-        buf[THREADS / 32 + 1] = r.begin - at;
+#pragma unroll
+    for (int t = 0; t < TEAMS; t++) {
+        const int worker = t * step + first_worker;
+        if (worker >= workers) break;
+        const int begin = worker_begin(total, worker, workers);
+        if (sum > 0 && before <= begin && begin < before + sum) {
+            int at = before, b = b0;
+            for (int n; b + 1 < b1 && begin >= at + (n = sequence_stages(l, c, b)); b++) at += n;
+            buf[THREADS / 32 + 2 * t] = b;
+            buf[THREADS / 32 + 2 * t + 1] = begin - at;
+        }
     }
     __syncthreads();
-    r.b = buf[THREADS / 32];
-    r.rest = buf[THREADS / 32 + 1];
-    return r;
+    return total;
+}
+// The range [begin, end) of a worker.
+__device__ __forceinline__ void worker_range(const PagedClass &c, int total, int worker, int &begin, int &end) {
+    const int workers = workers_of(c, total);
+    begin = worker < workers ? worker_begin(total, worker, workers) : total;
+    end = worker < workers ? worker_begin(total, worker + 1, workers) : total;
 }
 
-// The page of a sequence's tokens [t, ...) in the pool, or -1.
+// The index of the page that holds token t.
+__device__ __forceinline__ int page_index(const PagedSeg &s, int t) {
+    return static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned>(t)) * s.magic) >> s.shift);
+}
+// The index-th page of sequence b in the pool, or -1.
 __device__ __forceinline__ int page_at(const PagedSeg &s, int b, int index) {
     const int page = s.table ? s.table[b * s.table_stride + index] : b;
     return page >= 0 && page < s.n_pages ? page : -1;

@@ -14,11 +14,10 @@ namespace {
 template <int D>
 struct Fp16 {
     static constexpr int PT = 64, row = 2 * D, offV = PT * row, stage = 2 * PT * row;
-    static constexpr int fixed = kCopyBytes + static_cast<int>(sizeof(Small));
-    static constexpr int CTAS = 3;
-    static constexpr int fit = (232448 / CTAS - 1024 - fixed) / stage;
-    static constexpr int NS = fit > 4 ? 4 : fit, AHEAD = NS - 1;
-    static constexpr int smem = NS * stage + fixed;
+    static constexpr int team = kCopyBytes + static_cast<int>(sizeof(Small));
+    static constexpr int fit = (kSmemMax - kBufBytes - kTeams * team) / (kTeams * stage);
+    static constexpr int NS = fit > 4 ? 4 : fit;
+    static constexpr int smem = kBufBytes + kTeams * (team + NS * stage);
     static_assert(NS >= 2, "stages");
 };
 
@@ -37,94 +36,115 @@ __device__ __forceinline__ void arrive_when_copied(uint64_t *bar) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, Fp16<D>::CTAS) paged_fp16_kernel(const __grid_constant__ PagedParams p, const int nhb) {
+__global__ void __launch_bounds__(kTeamThreads, 1) paged_fp16_kernel(const __grid_constant__ PagedParams p, const int nhb) {
     using G = Fp16<D>;
     constexpr int NS = G::NS, MT = D / 16, CH = D / 8;  // m-tiles of the dims, chunks of a row
     extern __shared__ __align__(128) uint8_t smem[];
-    float *copies = reinterpret_cast<float *>(smem + NS * G::stage);
-    Small &sm = *reinterpret_cast<Small *>(smem + NS * G::stage + kCopyBytes);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, worker = blockIdx.x;
+    int *bufs = reinterpret_cast<int *>(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool loads = warp >= kTeams * kWarps;
+    const int team = loads ? warp - kTeams * kWarps : warp / kWarps;  // (from kTeams on: no work)
+    uint8_t *mine = smem + kBufBytes + team * (G::team + NS * G::stage);
+    float *copies = reinterpret_cast<float *>(mine + NS * G::stage);
+    Small &sm = *reinterpret_cast<Small *>(mine + NS * G::stage + kCopyBytes);
+    const int worker = team * gridDim.x + blockIdx.x;
     const PagedList &l = p.list;
     pdl_launch_dependents();
-    if (threadIdx.x == 0) {
+    if (loads && lane == 0 && team < kTeams) {
 #pragma unroll
         for (int i = 0; i < NS; i++) {
             mbar_init(&sm.full[i], 33);  // the loader's lanes when their copies are there, and its word on the stage
             mbar_init(&sm.empty[i], kWarps);
         }
         mbar_init(&sm.sync, kWarps);
+        mbar_init(&sm.head, 1);
         mbar_init_fence();
         sm.dead = 0;
-        p.state[worker] = 0;
+        if (worker < p.cls.workers) p.state[worker] = 0;
     }
-    const paged::Range range = paged::range_of<kThreads>(l, p.cls, worker, p.first, sm.buf);  // (synchronises)
-    const int n_st = range.end - range.begin;
-    int k = 0;
-    bool ok = true;
-
-    paged::Walk w;
-    int pid[2] = {-1, -1}, t0 = 0, n = 0;  // pages of rows lane, lane + 32
-    auto look = [&]() {
-        const PagedSeg &s = p.seg[p.cls.seg[w.i]];
-        t0 = w.st * G::PT;
-        n = min(G::PT, w.tokens - t0);
+    const int total = paged::ranges_of<kTeamThreads, kTeams>(l, p.cls, blockIdx.x, gridDim.x, p.first, bufs);  // (synchronises)
+    int begin, end;
+    paged::worker_range(p.cls, total, worker, begin, end);
+    const int n_st = team < kTeams ? end - begin : 0;
+    if (loads) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (n_st > 0) {
+            paged::Walk w = paged::seek(l, p.cls, bufs[kTeamThreads / 32 + 2 * team], bufs[kTeamThreads / 32 + 2 * team + 1]);
+            if (lane == 0) {
+                sm.stage[0].b = w.b;
+                sm.stage[0].h_rb = w.h | (w.rb << 8);
+                arrive(&sm.head);
+            }
+            int pid[2], n = 0;  // pages of rows lane, lane + 32
+            auto look = [&]() {
+                const PagedSeg &s = p.seg[p.cls.seg[w.i]];
+                const int t0 = w.st * G::PT;
+                n = max(min(G::PT, w.tokens - t0), 0);
 #pragma unroll
-        for (int i = 0; i < 2; i++) pid[i] = lane + 32 * i < n ? paged::page_at(s, w.b, (t0 + lane + 32 * i) / s.page) : -1;
-    };
-    auto load = [&](int j) {
-        const int at = j % NS;
-        if (j >= NS && !wait(&sm.empty[at], (j / NS - 1) & 1, p.wait_polls, &sm.dead)) return false;
-        const PagedSeg &s = p.seg[p.cls.seg[w.i]];
-        const SegView &v = s.seg;
-        long long off[2];
-        unsigned miss[2];
+                for (int i = 0; i < 2; i++)
+                    pid[i] = lane + 32 * i < n ? paged::page_at(s, w.b, paged::page_index(s, t0 + lane + 32 * i)) : -1;
+            };
+            look();
+            int at = 0, round = 0, issued = -1;
+            bool fresh = true;
+            for (int j = 0; j < n_st; j++) {
+                if (round > 0 && !wait(&sm.empty[at], (round - 1) & 1, p.wait_polls, &sm.dead)) break;
+                const PagedSeg &s = p.seg[p.cls.seg[w.i]];
+                const SegView &v = s.seg;
+                long long off[2];
+                unsigned miss[2];
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-            const int t = t0 + lane + 32 * i;
-            off[i] = pid[i] < 0 ? -1 : static_cast<long long>(pid[i] * v.kblock + v.koff[w.h] + static_cast<size_t>(t % s.page) * G::row);
-            miss[i] = __ballot_sync(0xffffffffu, lane + 32 * i < n && pid[i] < 0);
-        }
-        if (lane == 0) {  // (rows of the stage outside the pool: page and skip hold their bits)
-            sm.stage[at] = {n, w.b, w.h | (w.rb << 8), miss[0] | miss[1], static_cast<int>(miss[0]), static_cast<int>(miss[1])};
-            arrive(&sm.full[at]);
-        }
-        const int row0 = lane / CH, chunk = lane % CH;
-        uint8_t *dst = smem + at * G::stage;
+                for (int i = 0; i < 2; i++) {
+                    const int t = w.st * G::PT + lane + 32 * i;
+                    off[i] = -1;
+                    if (pid[i] >= 0)
+                        off[i] = static_cast<long long>(pid[i] * v.kblock + v.koff[w.h] + static_cast<size_t>(t - paged::page_index(s, t) * s.page) * G::row);
+                    miss[i] = __ballot_sync(0xffffffffu, lane + 32 * i < n && pid[i] < 0);
+                }
+                if (lane == 0) {  // (rows of the stage outside the pool: page and skip hold their bits)
+                    sm.stage[at] = {n | (fresh ? kFresh : 0) | (miss[0] | miss[1] ? kBad : 0), w.b, w.h | (w.rb << 8), 0u,
+                                    static_cast<int>(miss[0]), static_cast<int>(miss[1])};
+                    arrive(&sm.full[at]);
+                }
+                issued = j;
+                const int row0 = lane / CH, chunk = lane % CH;
+                uint8_t *dst = mine + at * G::stage;
 #pragma unroll 4
-        for (int i = 0; i < G::PT; i += 32 / CH) {
-            const int row = i + row0;
-            const long long o = __shfl_sync(0xffffffffu, i < 32 ? off[0] : off[1], row & 31);
-            const int to = row * G::row + 16 * (chunk ^ (row & 7));
-            const size_t from = o < 0 ? 0 : static_cast<size_t>(o) + 16 * chunk;
-            if (o >= 0) cp_async16_zfill(dst + to, v.k + from, 16);
-            cp_async16_zfill(dst + G::offV + to, v.v + from, o < 0 ? 0 : 16);
+                for (int i = 0; i < G::PT; i += 32 / CH) {
+                    const int row = i + row0;
+                    const long long o = __shfl_sync(0xffffffffu, i < 32 ? off[0] : off[1], row & 31);
+                    const int to = row * G::row + 16 * (chunk ^ (row & 7));
+                    const size_t from = o < 0 ? 0 : static_cast<size_t>(o) + 16 * chunk;
+                    if (o >= 0) cp_async16_zfill(dst + to, v.k + from, 16);
+                    cp_async16_zfill(dst + G::offV + to, v.v + from, o < 0 ? 0 : 16);
+                }
+                arrive_when_copied(&sm.full[at]);
+                if (j + 1 < n_st) {
+                    fresh = paged::next(l, p.cls, w);
+                    look();
+                }
+                if (++at == NS) at = 0, ++round;
+            }
+            if (issued + 1 < n_st && lane == 0) {
+                *const_cast<volatile int *>(&sm.dead) = 1;
+                p.state[worker] = 1;
+            }
+            cp_async_wait<0>();  // no copy outlives its warp
         }
-        arrive_when_copied(&sm.full[at]);
-        if (j + kWarps < n_st) {
-            skip(l, p.cls, w, kWarps);
-            look();
-        }
-        return true;
-    };
-
-    if (n_st > 0) {
-        w = paged::seek(l, p.cls, range.b, range.rest);
-        if (warp < n_st) {
-            if (warp > 0) skip(l, p.cls, w, warp);
-            look();
-        }
-        for (int j = warp; j < G::AHEAD && j < n_st && ok; j += kWarps) ok = load(j);
-
-        const int hb = warp % nhb, tp = warp / nhb, parts = kWarps / nhb;
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        const int tw = warp % kWarps, g = lane >> 2, c = lane & 3;
+        const int hb = tw % nhb, tp = tw / nhb, parts = kWarps / nhb;
         const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
         uint32_t bq[2 * MT];
         Run<MT> r;
         unsigned phase = 0;
-        int now_b = -1, now_h = -1;
+        int now_b = 0, now_h = 0;
+        bool ok = true;
         // the lane's row address of an ldmatrix
         const int krow = (lane & 7) + ((lane >> 3) & 1) * 8, kch = lane >> 4, vrow = (lane & 7) + (lane >> 4) * 8, vch = (lane >> 3) & 1;
 
-        auto tile = [&](unsigned buf, int tA, const Stage &sg) {
+        auto tile = [&](unsigned buf, int tA, int n, bool bad, const Stage &sg) {
             float e[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int kk = 0; kk < MT; kk++) {
@@ -132,13 +152,15 @@ __global__ void __launch_bounds__(kThreads, Fp16<D>::CTAS) paged_fp16_kernel(con
                 ldmatrix4(a, buf + (tA + krow) * G::row + 16 * ((2 * kk + kch) ^ (krow & 7)));
                 mma16816(e, a[0], a[1], a[2], a[3], bq[2 * kk], bq[2 * kk + 1]);
             }
-            float s[2], v[2] = {1.f, 1.f};
+            float s[2];
+            const float v[2] = {1.f, 1.f};
             bool have[2];
 #pragma unroll
             for (int i = 0; i < 2; i++) {
                 const int tok = tA + g + 8 * i;
                 s[i] = e[2 * i] * p.qk_scale;
-                have[i] = tok < sg.n && !(sg.bad && ((static_cast<unsigned>(tok < 32 ? sg.page : sg.skip) >> (tok & 31)) & 1u));
+                have[i] = tok < n;
+                if (bad) have[i] = have[i] && !((static_cast<unsigned>(tok < 32 ? sg.page : sg.skip) >> (tok & 31)) & 1u);
             }
             uint32_t bp[2];
             softmax<false, 1>(r, s, have, v, g, c, sel, bp);
@@ -151,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, Fp16<D>::CTAS) paged_fp16_kernel(con
             r.tiles++;
         };
         auto fold = [&]() {
-            float *to = copies + (warp * 4 + c) * kHeadStride + g;
+            float *to = copies + (tw * 4 + c) * kHeadStride + g;
             const float f = r.m_ref == r.m ? 1.f : ex2(r.m_ref - r.m);
 #pragma unroll
             for (int mt = 0; mt < MT; mt++)
@@ -167,14 +189,14 @@ __global__ void __launch_bounds__(kThreads, Fp16<D>::CTAS) paged_fp16_kernel(con
         auto flush = [&]() {
             fold();
             const float sum = warp_sum_g(r.l);
-            if (g == 0) sm.m[warp][c] = r.m, sm.l[warp][c] = sum;
+            if (g == 0) sm.m[tw][c] = r.m, sm.l[tw][c] = sum;
             if (!meet(sm, phase, p.wait_polls, lane)) return false;
             write_record<D, 1>(sm, copies, p.part + paged::group_slot(l, p.cls, worker, now_b, now_h & 255, now_h >> 8) * l.R * (D + 4), l.R, nhb);
             return meet(sm, phase, p.wait_polls, lane);
         };
         auto start = [&]() {
             __half *q = reinterpret_cast<__half *>(copies);
-            stage_queries<D, false>(p, sm, q, now_b, now_h & 255, now_h >> 8, l.R, warp, lane);
+            stage_queries<D, false>(p, sm, q, now_b, now_h & 255, now_h >> 8, l.R, tw, lane);
             if (!meet(sm, phase, p.wait_polls, lane)) return false;
             const int head = hb * 4 + (g >> 1);
             const uint32_t *from = reinterpret_cast<const uint32_t *>(q + 2 * head * D) + c;
@@ -184,29 +206,37 @@ __global__ void __launch_bounds__(kThreads, Fp16<D>::CTAS) paged_fp16_kernel(con
             return meet(sm, phase, p.wait_polls, lane);
         };
 
-        for (; k < n_st && ok; k++) {
-            const int at = k % NS, j = k + G::AHEAD;
-            if (j < n_st && j % kWarps == warp && !(ok = load(j))) break;
-            if (!(ok = wait(&sm.full[at], (k / NS) & 1, p.wait_polls, &sm.dead))) break;
-            const Stage sg = sm.stage[at];
-            if (sg.b != now_b || sg.h_rb != now_h) {
-                if (k > 0 && !(ok = flush())) break;
-                now_b = sg.b;
-                now_h = sg.h_rb;
-                if (!(ok = start())) break;
+        if (n_st > 0) {
+            ok = wait(&sm.head, 0, p.wait_polls, &sm.dead);
+            if (ok) {
+                now_b = sm.stage[0].b;
+                now_h = sm.stage[0].h_rb;
+                ok = start();  // (while the first stage is on its way)
             }
-            const unsigned buf = smem_u32(smem + at * G::stage);
-            for (int tA = tp * 16; tA < sg.n; tA += 16 * parts) tile(buf, tA, sg);
-            __syncwarp();
-            if (lane == 0) arrive(&sm.empty[at]);
-            if (__builtin_expect(r.tiles >= kFold, 0)) fold();
+            int at = 0;
+            unsigned parity = 0;
+            for (int k = 0; k < n_st && ok; k++) {
+                if (!(ok = wait(&sm.full[at], parity, p.wait_polls, &sm.dead))) break;
+                const int word = sm.stage[at].word, n = word & (kFresh - 1);
+                if (__builtin_expect((word & kFresh) && k > 0, 0)) {
+                    if (!(ok = flush())) break;
+                    now_b = sm.stage[at].b;
+                    now_h = sm.stage[at].h_rb;
+                    if (!(ok = start())) break;
+                }
+                const unsigned buf = smem_u32(mine + at * G::stage);
+                for (int tA = tp * 16; tA < n; tA += 16 * parts) tile(buf, tA, n, (word & kBad) != 0, sm.stage[at]);
+                __syncwarp();
+                if (lane == 0) arrive(&sm.empty[at]);
+                if (++at == NS) at = 0, parity ^= 1u;
+                if (__builtin_expect(r.tiles >= kFold, 0)) fold();
+            }
+            if (ok) ok = flush();
+            if (!ok && lane == 0) {
+                *const_cast<volatile int *>(&sm.dead) = 1;
+                p.state[worker] = 1;
+            }
         }
-        if (ok) ok = flush();
-        if (!ok && lane == 0) {
-            *const_cast<volatile int *>(&sm.dead) = 1;
-            p.state[worker] = 1;
-        }
-        cp_async_wait<0>();  // no copy outlives its warp
     }
     pdl_wait();
 }
@@ -217,12 +247,12 @@ __global__ void __launch_bounds__(kThreads, Fp16<D>::CTAS) paged_fp16_kernel(con
 cudaError_t launch_paged_fp16(const PagedParams &p, cudaStream_t s) {
     int nhb = pmma::head_blocks(p.list.R, 4);
     void *args[] = {const_cast<PagedParams *>(&p), &nhb};
-    return p.d == 128 ? pmma::launch(reinterpret_cast<const void *>(pmma::paged_fp16_kernel<128>), pmma::Fp16<128>::smem, p, args, s)
-                      : pmma::launch(reinterpret_cast<const void *>(pmma::paged_fp16_kernel<64>), pmma::Fp16<64>::smem, p, args, s);
+    return p.d == 128 ? pmma::launch(reinterpret_cast<const void *>(pmma::paged_fp16_kernel<128>), pmma::Fp16<128>::smem,
+                                     pmma::kTeamThreads, pmma::kTeams, p, args, s)
+                      : pmma::launch(reinterpret_cast<const void *>(pmma::paged_fp16_kernel<64>), pmma::Fp16<64>::smem,
+                                     pmma::kTeamThreads, pmma::kTeams, p, args, s);
 }
 
-PagedShape paged_shape_fp16(int d) {
-    return d == 128 ? PagedShape{pmma::Fp16<128>::PT, pmma::Fp16<128>::CTAS} : PagedShape{pmma::Fp16<64>::PT, pmma::Fp16<64>::CTAS};
-}
+PagedShape paged_shape_fp16(int) { return {64, pmma::kTeams}; }
 
 }  // namespace tqk

@@ -179,6 +179,10 @@ tq_status tq_paged_attention(const tq_layer_view *pools, const tq_pages *pages, 
             if (sg.n_tokens < 0 || sg.n_tokens > sg.layout.capacity) return TQ_ERR_SIZE;
             s.limit = sg.n_tokens;
         }
+        // 2^shift / page rounded up, shift = 31 + ceil(log2 page): the excess times t stays below 2^shift / page
+        s.shift = 31;
+        while (s.page > 1 && (1LL << (s.shift - 31)) < s.page) ++s.shift;
+        if (s.page > 0) s.magic = static_cast<uint32_t>(((1ULL << s.shift) + s.page - 1) / s.page);
         if (s.limit > 0x7fffffff - 1024) return TQ_ERR_UNSUPPORTED;  // rounded up to stages in 32 bits
         p.list.len[i] = s.len;
         p.list.limit[i] = s.limit;

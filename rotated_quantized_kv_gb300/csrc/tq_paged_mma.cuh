@@ -23,6 +23,9 @@
 //     up marks its worker, sees its own copies land and leaves; it waits for no one.
 #pragma once
 
+#include <algorithm>
+#include <type_traits>
+
 #include "tq_decode_packed.cuh"
 #include "tq_paged.cuh"
 
@@ -57,18 +60,18 @@ __device__ __forceinline__ void arrive(uint64_t *bar) {
 
 // What the loader tells the others of a stage.
 struct Stage {
-    int n;               // tokens (0 or less: none)
+    int word;            // tokens (none: 0), kFresh: another (sequence, head, block), kBad: some page outside the pool
     int b, h_rb;         // sequence; KV head and block of rows
     unsigned bad;        // bit i: the i-th page of it is outside the pool
     int page, skip;      // tokens a page, and tokens of the first page before the stage
 };
+constexpr int kFresh = 1 << 16, kBad = 1 << 17;
 
-struct Small {           // shared memory besides stages, tables and copies
-    uint64_t full[8], empty[8], sync;
+struct alignas(16) Small {  // a team's shared memory besides stages, tables and copies
+    uint64_t full[8], empty[8], sync, head;
     Stage stage[8];
     float m[kWarps][4], l[kWarps][4];
     float qsum[kMaxRows], qexp[kMaxRows];
-    int buf[kWarps + 2];
     int dead;
 };
 
@@ -146,17 +149,7 @@ __device__ __forceinline__ void softmax(Run<MT> &r, const float (&s)[2 * T], con
     }
 }
 
-// Copies with a bound on their walk: `skip` stages on.
-__device__ __forceinline__ void skip(const PagedList &l, const PagedClass &c, paged::Walk &w, int stages) {
-    while (stages >= w.n_st - w.st) {
-        stages -= w.n_st - w.st;
-        w.st = w.n_st - 1;
-        paged::next(l, c, w);
-    }
-    w.st += stages;
-}
-
-// The CTA's four warps meet (bounded).
+// A team's four warps meet (bounded).
 __device__ __forceinline__ bool meet(Small &sm, unsigned &phase, int polls, int lane) {
     __syncwarp();
     if (lane == 0) arrive(&sm.sync);
@@ -236,7 +229,7 @@ template <int D, int NP>
 __device__ __forceinline__ void write_record(const Small &sm, const float *copies, float *rec, int rows, int nhb) {
     constexpr int HPW = 4 / NP;
     const int parts = kWarps / nhb, dim = threadIdx.x % D;
-    for (int i = threadIdx.x / D; i < rows; i += kThreads / D) {
+    for (int i = static_cast<int>(threadIdx.x % kThreads) / D; i < rows; i += kThreads / D) {
         const int hb = i / HPW, c0 = i % HPW;
         float M = kNegInf;
         for (int tp = 0; tp < parts; tp++)
@@ -259,153 +252,180 @@ __device__ __forceinline__ void write_record(const Small &sm, const float *copie
 }
 
 // ------------------------------------------------------------------- packed
+constexpr int kTeams = 3;
+constexpr int kTeamThreads = 512;       // three teams of four warps, and a warp that loads for each
+constexpr int kSmemMax = 232448 - 1024;
+constexpr int kBufBytes = 128;           // of ranges_of
+static_assert(kBufBytes >= 4 * (kTeamThreads / 32 + 2 * kTeams), "ranges");
+
 template <int KB, int VB, int NP>
 struct Geom {
     static constexpr int ROWS = 128, PT = ROWS * NP;             // rows and tokens of a stage
     static constexpr int RK = 16 * KB, RV = 16 * VB;             // bytes of a row
     static constexpr int offV = ROWS * RK, offKS = offV + ROWS * RV, offVS = offKS + PT * 4, stage = offVS + PT * 4;
-    static constexpr int entries = (VB == 2 || VB == 3) ? 1 << (2 * VB) : 0;
-    static constexpr int copies = 32, TS = 7;                    // a column of the pair table a lane
-    static constexpr int table = entries * copies * 4 + (VB >= 5 ? 512 : 0);
-    static constexpr int fixed = table + kCopyBytes + static_cast<int>(sizeof(Small));
-    static constexpr int fit(int ctas) { return (232448 / ctas - 1024 - fixed) / stage; }
-    // three CTAs an SM (168 registers a thread) where three stages or more fit, else two
-    static constexpr int CTAS = fit(3) >= 3 ? 3 : 2;
-    static constexpr int NS = fit(CTAS) > 6 ? 6 : fit(CTAS);
-    static constexpr int AHEAD = NS - 1;                         // stages on their way
-    static constexpr int smem = NS * stage + fixed;
+    static constexpr int entries = VB >= 2 && VB <= 4 ? 1 << (2 * VB) : 0;
+    static constexpr int TS = 7;                                 // a column of the pair table a lane
+    static constexpr int table = entries * 128 + (VB >= 5 ? 512 : 0);
+    static constexpr int team = kCopyBytes + static_cast<int>(sizeof(Small));
+    static constexpr int fit(int teams) { return (kSmemMax - table - kBufBytes - teams * team) / (teams * stage); }
+    static constexpr int TEAMS = fit(kTeams) >= 2 ? kTeams : kTeams - 1;  // (the widest at head_dim 64: two)
+    static constexpr int NS = fit(TEAMS) > 6 ? 6 : fit(TEAMS);
+    static constexpr int smem = table + kBufBytes + TEAMS * (team + NS * stage);
     static_assert(NS >= 2 && NS <= 8, "stages");
 };
 
+// 4-bit values: pair table of 256 entries; E/O fields of 8 bits: dims (2mt, 2mt+1)
+struct Pairs4 {
+    static constexpr bool kLinear = false;
+    static constexpr __host__ __device__ int dim(int mt, int r) { return 2 * mt + r; }
+    template <int K>
+    static __device__ __forceinline__ uint32_t at(uint32_t F) { return pair_off<8 * K, 8, 7>(F); }
+    static __device__ __forceinline__ void pair(const uint8_t *p, int RV, const VCtx &cx, uint32_t (&ra)[8], uint32_t (&rb)[8]) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(p + cx.off), y = *reinterpret_cast<const uint2 *>(p + cx.off + RV);
+        constexpr uint32_t M = 0x0F0F0F0Fu;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const uint32_t wx = i ? x.y : x.x, wy = i ? y.y : y.x;
+            const uint32_t E = (wx & M) | ((wy << 4) & ~M), O = ((wx >> 4) & M) | (wy & ~M);
+            ra[4 * i] = lds32(cx.tab + at<0>(E));
+            ra[4 * i + 1] = lds32(cx.tab + at<1>(E));
+            ra[4 * i + 2] = lds32(cx.tab + at<2>(E));
+            ra[4 * i + 3] = lds32(cx.tab + at<3>(E));
+            rb[4 * i] = lds32(cx.tab + at<0>(O));
+            rb[4 * i + 1] = lds32(cx.tab + at<1>(O));
+            rb[4 * i + 2] = lds32(cx.tab + at<2>(O));
+            rb[4 * i + 3] = lds32(cx.tab + at<3>(O));
+        }
+    }
+};
+
 template <int KB, int VB, int NP>
-__global__ void __launch_bounds__(kThreads, Geom<KB, VB, NP>::CTAS)
+__global__ void __launch_bounds__(kTeamThreads, 1)
     paged_packed_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ Levels lv, const int nhb) {
     using G = Geom<KB, VB, NP>;
     using KU = KUnpack<KB>;
-    using VD = VDec<VB, G::TS>;
+    using VD = typename std::conditional<VB == 4, Pairs4, VDec<VB, G::TS>>::type;
     constexpr int NS = G::NS, D = 128 / NP, HPW = 4 / NP;
-    extern __shared__ __align__(16) uint8_t smem[];
-    uint8_t *tab = smem + NS * G::stage;
-    float *copies = reinterpret_cast<float *>(tab + G::table);
-    Small &sm = *reinterpret_cast<Small *>(tab + G::table + kCopyBytes);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, worker = blockIdx.x;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t *tab = smem;
+    int *bufs = reinterpret_cast<int *>(smem + G::table);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool loads = warp >= kTeams * kWarps;                  // a team's loader
+    const int team = loads ? warp - kTeams * kWarps : warp / kWarps;  // (from TEAMS on: no work)
+    uint8_t *mine = smem + G::table + kBufBytes + team * (G::team + NS * G::stage);
+    float *copies = reinterpret_cast<float *>(mine + NS * G::stage);
+    Small &sm = *reinterpret_cast<Small *>(mine + NS * G::stage + kCopyBytes);
+    const int worker = team * gridDim.x + blockIdx.x;
     const PagedList &l = p.list;
     pdl_launch_dependents();
-    if (threadIdx.x == 0) {
+    if (loads && lane == 0 && team < G::TEAMS) {
 #pragma unroll
         for (int i = 0; i < NS; i++) {
             mbar_init(&sm.full[i], 1);
             mbar_init(&sm.empty[i], kWarps);
         }
         mbar_init(&sm.sync, kWarps);
+        mbar_init(&sm.head, 1);
         mbar_init_fence();
         sm.dead = 0;
-        p.state[worker] = 0;
+        if (worker < p.cls.workers) p.state[worker] = 0;
     }
-    // ---- value decoder
-    VCtx vx;
-    vx.ctab = reinterpret_cast<const unsigned short *>(tab);
-    vx.tab = smem_u32(tab) + 4 * lane;
-    if constexpr (VB == 1) {
-        vx.off = 2 * c * G::RV + 4 * (g >> 1);
-        vx.sh = (g & 1) ? 0x7632 : 0x5410;
-    } else if constexpr (VB == 3) {
-        vx.off = 2 * c * G::RV + 4 * ((3 * g) >> 1);
-        vx.sh = (g & 1) * 16;
-    } else {
-        vx.off = 2 * c * G::RV + ((2 * VB * g) & ~3);
-        vx.sh = ((2 * VB * g) & 3) * 8;
-    }
+    // ---- value tables
     if constexpr (VB >= 5)
-        for (int i = threadIdx.x; i < (1 << VB); i += kThreads) reinterpret_cast<unsigned short *>(tab)[i] = lv.half[i];
+        for (int i = threadIdx.x; i < (1 << VB); i += kTeamThreads) reinterpret_cast<unsigned short *>(tab)[i] = lv.half[i];
     if constexpr (G::entries > 0)
-        for (int i = threadIdx.x; i < G::entries * 32; i += kThreads) {
+        for (int i = threadIdx.x; i < G::entries * 32; i += kTeamThreads) {
             const int e = i / 32;
             reinterpret_cast<uint32_t *>(tab)[i] = static_cast<uint32_t>(lv.half[e & ((1 << VB) - 1)]) |
                                                    (static_cast<uint32_t>(lv.half[e >> VB]) << 16);
         }
-    if constexpr (VB == 4) {
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            uint32_t lo = 0, hi = 0;
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const uint32_t v = lv.half[4 * i + e];
-                lo |= (v & 0xFFu) << (8 * e);
-                hi |= (v >> 8) << (8 * e);
+    const int total = paged::ranges_of<kTeamThreads, kTeams>(l, p.cls, blockIdx.x, gridDim.x, p.first, bufs);  // (synchronises)
+    int begin, end;
+    paged::worker_range(p.cls, total, worker, begin, end);
+    const int n_st = team < G::TEAMS ? end - begin : 0;
+    if (loads) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (n_st > 0) {
+            paged::Walk w = paged::seek(l, p.cls, bufs[kTeamThreads / 32 + 2 * team], bufs[kTeamThreads / 32 + 2 * team + 1]);
+            if (lane == 0) {
+                sm.stage[0].b = w.b;
+                sm.stage[0].h_rb = w.h | (w.rb << 8);
+                arrive(&sm.head);
             }
-            vx.pt.tl[i] = lo;
-            vx.pt.th[i] = hi;
-        }
-    }
-    const paged::Range range = paged::range_of<kThreads>(l, p.cls, worker, p.first, sm.buf);  // (synchronises)
-    const int n_st = range.end - range.begin;
-    int k = 0, issued = -1;  // the stage this warp is at, and the last one that it has sent for
-    bool ok = true;
-
-    // ---- the copies of stage j: its place is `w`, the lane's page number `pid`
-    paged::Walk w;
-    int pid = -1, n = 0, skipped = 0;
-    bool mine = false;
-    auto look = [&]() {  // the stage at `w`: n tokens, the first page's tokens before it, whether there is a page for the lane
-        const PagedSeg &s = p.seg[p.cls.seg[w.i]];
-        const int t0 = w.st * G::PT, page = t0 / s.page;
-        n = min(G::PT, w.tokens - t0);
-        skipped = t0 - page * s.page;
-        mine = n > 0 && lane <= (skipped + n - 1) / s.page;
-        pid = mine ? paged::page_at(s, w.b, page + lane) : -1;
-    };
-    auto load = [&](int j) {
-        const int at = j % NS;
-        if (j >= NS && !wait(&sm.empty[at], (j / NS - 1) & 1, p.wait_polls, &sm.dead)) return false;
-        const PagedSeg &s = p.seg[p.cls.seg[w.i]];
-        uint8_t *dst = smem + at * G::stage;
-        uint64_t *bar = &sm.full[at];
-        const int from = lane == 0 || !mine ? 0 : lane * s.page - skipped;  // the run's first token in the stage
-        const int in_page = lane == 0 ? skipped : 0;
-        const int run = mine ? min(s.page - in_page, n - from) : 0;
-        const bool bad = mine && pid < 0;
-        unsigned nk = 0, nv = 0, nsc = 0;
-        if (mine && !bad) {  // (runs start at multiples of 16 tokens; an odd end rounds up inside the page)
-            nk = (run * (G::RK / NP) + 15) & ~15u;
-            nv = (run * (G::RV / NP) + 15) & ~15u;
-            nsc = (run * 4 + 15) & ~15u;
-        }
-        const unsigned total = __reduce_add_sync(0xffffffffu, nk + nv + 2 * nsc);
-        const unsigned bads = __ballot_sync(0xffffffffu, bad);
-        fence_proxy_async();
-        if (lane == 0) {
-            sm.stage[at] = {n, w.b, w.h | (w.rb << 8), bads, s.page, skipped};
-            mbar_expect_tx(bar, total);
-        }
-        issued = j;
-        __syncwarp();
-        if (nk) {
             const uint64_t pol = policy_evict_first();
-            const SegView &v = s.seg;
-            const size_t sc = (static_cast<size_t>(pid) * l.H + w.h) * v.capacity + in_page;
-            bulk_g2s_hint(dst + from * (G::RK / NP), v.k + pid * v.kblock + v.koff[w.h] + static_cast<size_t>(in_page) * (G::RK / NP), nk, bar, pol);
-            bulk_g2s_hint(dst + G::offV + from * (G::RV / NP), v.v + pid * v.vblock + v.voff[w.h] + static_cast<size_t>(in_page) * (G::RV / NP), nv, bar, pol);
-            bulk_g2s_hint(dst + G::offKS + from * 4, v.ks + sc, nsc, bar, pol);
-            bulk_g2s_hint(dst + G::offVS + from * 4, v.vs + sc, nsc, bar, pol);
-        }
-        if (j + kWarps < n_st) {  // this warp's next
-            skip(l, p.cls, w, kWarps);
+            int pid = -1, n = 0, skipped = 0, runs = 0;
+            auto look = [&]() {  // the stage at `w`: n tokens on `runs` pages, the first page's tokens before it, the lane's page
+                const PagedSeg &s = p.seg[p.cls.seg[w.i]];
+                const int t0 = w.st * G::PT, page = paged::page_index(s, t0);
+                n = max(min(G::PT, w.tokens - t0), 0);
+                skipped = t0 - page * s.page;
+                runs = n > 0 ? paged::page_index(s, t0 + n - 1) - page + 1 : 0;
+                pid = lane < runs ? paged::page_at(s, w.b, page + lane) : -1;
+            };
             look();
+            int at = 0, round = 0, issued = -1;
+            bool fresh = true;
+            for (int j = 0; j < n_st; j++) {
+                if (round > 0 && !wait(&sm.empty[at], (round - 1) & 1, p.wait_polls, &sm.dead)) break;
+                const PagedSeg &s = p.seg[p.cls.seg[w.i]];
+                const SegView &v = s.seg;
+                uint8_t *dst = mine + at * G::stage;
+                uint64_t *bar = &sm.full[at];
+                const bool some = lane < runs;
+                const int from = lane == 0 || !some ? 0 : lane * s.page - skipped;  // the run's first token in the stage
+                const int in_page = lane == 0 ? skipped : 0;
+                const int run = some ? min(s.page - in_page, n - from) : 0;
+                const bool bad = some && pid < 0;
+                // (runs start at multiples of 16 tokens; an odd end rounds up inside the page)
+                const unsigned nk = some && !bad ? (run * (G::RK / NP) + 15) & ~15u : 0u;
+                const unsigned nv = (run * (G::RV / NP) + 15) & ~15u, ns = (run * 4 + 15) & ~15u;
+                const unsigned bytes = __reduce_add_sync(0xffffffffu, nk ? nk + nv + 2 * ns : 0u);
+                const unsigned bads = __ballot_sync(0xffffffffu, bad);
+                if (lane == 0) {
+                    sm.stage[at] = {n | (fresh ? kFresh : 0) | (bads ? kBad : 0), w.b, w.h | (w.rb << 8), bads, s.page, skipped};
+                    fence_proxy_async();
+                    mbar_expect_tx(bar, bytes);
+                }
+                issued = j;
+                __syncwarp();
+                if (nk) {
+                    const size_t sc = (static_cast<size_t>(pid) * l.H + w.h) * v.capacity + in_page;
+                    fence_proxy_async();
+                    bulk_g2s_hint(dst + from * (G::RK / NP), v.k + pid * v.kblock + v.koff[w.h] + static_cast<size_t>(in_page) * (G::RK / NP), nk, bar, pol);
+                    bulk_g2s_hint(dst + G::offV + from * (G::RV / NP), v.v + pid * v.vblock + v.voff[w.h] + static_cast<size_t>(in_page) * (G::RV / NP), nv, bar, pol);
+                    bulk_g2s_hint(dst + G::offKS + from * 4, v.ks + sc, ns, bar, pol);
+                    bulk_g2s_hint(dst + G::offVS + from * 4, v.vs + sc, ns, bar, pol);
+                }
+                if (j + 1 < n_st) {
+                    fresh = paged::next(l, p.cls, w);
+                    look();
+                }
+                if (++at == NS) at = 0, ++round;
+            }
+            if (issued + 1 < n_st && lane == 0) {
+                *const_cast<volatile int *>(&sm.dead) = 1;
+                p.state[worker] = 1;
+            }
+            // no copy outlives its warp: the last fill of each buffer
+            for (int j = max(issued - NS + 1, 0); j <= issued; j++) mbar_wait(&sm.full[j % NS], (j / NS) & 1);
         }
-        return true;
-    };
-
-    if (n_st > 0) {
-        w = paged::seek(l, p.cls, range.b, range.rest);
-        if (warp < n_st) {
-            if (warp > 0) skip(l, p.cls, w, warp);
-            look();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        const int tw = warp % kWarps, g = lane >> 2, c = lane & 3;
+        VCtx vx;
+        vx.ctab = reinterpret_cast<const unsigned short *>(tab);
+        vx.tab = smem_u32(tab) + 4 * lane;
+        if constexpr (VB == 1) {
+            vx.off = 2 * c * G::RV + 4 * (g >> 1);
+            vx.sh = (g & 1) ? 0x7632 : 0x5410;
+        } else if constexpr (VB == 3) {
+            vx.off = 2 * c * G::RV + 4 * ((3 * g) >> 1);
+            vx.sh = (g & 1) * 16;
+        } else {
+            vx.off = 2 * c * G::RV + ((2 * VB * g) & ~3);
+            vx.sh = ((2 * VB * g) & 3) * 8;
         }
-        for (int j = warp; j < G::AHEAD && j < n_st && ok; j += kWarps) ok = load(j);
-
-        // ---- consumer
-        const int hb = warp % nhb, tp = warp / nhb, parts = kWarps / nhb;
+        const int hb = tw % nhb, tp = tw / nhb, parts = kWarps / nhb;
         const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
         constexpr float alpha = static_cast<float>(1 << (24 - KU::kA)) * 2.0f / static_cast<float>(1 << KB);
         constexpr float beta = 1.0f / static_cast<float>(1 << KB) - 1.0f;
@@ -414,9 +434,10 @@ __global__ void __launch_bounds__(kThreads, Geom<KB, VB, NP>::CTAS)
         float aq = 0.f, bqs = 0.f;
         Run<8> r;
         unsigned phase = 0;
-        int now_b = -1, now_h = -1;
+        int now_b = 0, now_h = 0;
+        bool ok = true;
 
-        auto tile_pair = [&](const uint8_t *buf, int tA, int tokens, unsigned bads, const Stage &sg, auto full_tag) {
+        auto tile_pair = [&](const uint8_t *buf, int tA, int tokens, const Stage &sg, auto full_tag) {
             constexpr bool FULL = decltype(full_tag)::value;
             const float *kss = reinterpret_cast<const float *>(buf + G::offKS), *vss = reinterpret_cast<const float *>(buf + G::offVS);
             float s[4], v[4];
@@ -434,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, Geom<KB, VB, NP>::CTAS)
                     have[i] = true;
                     if constexpr (!FULL) {
                         have[i] = tok < tokens;
-                        if (bads) have[i] = have[i] && !((bads >> ((sg.skip + tok) / sg.page)) & 1u);
+                        if (sg.bad) have[i] = have[i] && !((sg.bad >> ((sg.skip + tok) / sg.page)) & 1u);
                     }
                 }
             }
@@ -455,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, Geom<KB, VB, NP>::CTAS)
         };
         // the accumulators into the warp's copy: head c, coordinates 16 g ..
         auto fold = [&]() {
-            float *to = copies + (warp * 4 + c) * kHeadStride + 16 * g;
+            float *to = copies + (tw * 4 + c) * kHeadStride + 16 * g;
             float W = 0.f;
             if constexpr (VD::kLinear) W = warp_sum_g(r.w);
             float x[16];
@@ -485,14 +506,14 @@ __global__ void __launch_bounds__(kThreads, Geom<KB, VB, NP>::CTAS)
         auto flush = [&]() {
             fold();
             const float sum = warp_sum_g(r.l);
-            if (g == 0) sm.m[warp][c] = r.m, sm.l[warp][c] = sum;
+            if (g == 0) sm.m[tw][c] = r.m, sm.l[tw][c] = sum;
             if (!meet(sm, phase, p.wait_polls, lane)) return false;
             write_record<D, NP>(sm, copies, p.part + paged::group_slot(l, p.cls, worker, now_b, now_h & 255, now_h >> 8) * l.R * (D + 4), l.R, nhb);
             return meet(sm, phase, p.wait_polls, lane);
         };
         auto start = [&]() {
             __half *q = reinterpret_cast<__half *>(copies);
-            stage_queries<D, true>(p, sm, q, now_b, now_h & 255, now_h >> 8, l.R, warp, lane);
+            stage_queries<D, true>(p, sm, q, now_b, now_h & 255, now_h >> 8, l.R, tw, lane);
             if (!meet(sm, phase, p.wait_polls, lane)) return false;
             const int v = g >> 1, part = g & 1;
             const int head = hb * HPW + (NP == 2 ? v & 1 : v);
@@ -509,52 +530,60 @@ __global__ void __launch_bounds__(kThreads, Geom<KB, VB, NP>::CTAS)
                 }
             }
             gather_b<KU>(x, bq);
-            const int mine = hb * HPW + (NP == 2 ? c & 1 : c);
-            aq = alpha * sm.qexp[mine] * p.qk_scale;
-            bqs = beta * sm.qsum[mine] * p.qk_scale;
+            const int own = hb * HPW + (NP == 2 ? c & 1 : c);
+            aq = alpha * sm.qexp[own] * p.qk_scale;
+            bqs = beta * sm.qsum[own] * p.qk_scale;
             r.start();
             return meet(sm, phase, p.wait_polls, lane);
         };
 
-        for (; k < n_st && ok; k++) {
-            const int at = k % NS, j = k + G::AHEAD;
-            if (j < n_st && j % kWarps == warp && !(ok = load(j))) break;
-            if (!(ok = wait(&sm.full[at], (k / NS) & 1, p.wait_polls, &sm.dead))) break;
-            const Stage sg = sm.stage[at];
-            if (sg.b != now_b || sg.h_rb != now_h) {
-                if (k > 0 && !(ok = flush())) break;
-                now_b = sg.b;
-                now_h = sg.h_rb;
-                if (!(ok = start())) break;
+        if (n_st > 0) {
+            ok = wait(&sm.head, 0, p.wait_polls, &sm.dead);
+            if (ok) {
+                now_b = sm.stage[0].b;
+                now_h = sm.stage[0].h_rb;
+                ok = start();  // (while the first stage is on its way)
             }
-            const uint8_t *buf = smem + at * G::stage;
-            for (int tA = tp * 32; NP * tA < sg.n; tA += 32 * parts) {
-                if (NP * (tA + 32) <= sg.n && sg.bad == 0) tile_pair(buf, tA, sg.n, 0u, sg, std::true_type{});
-                else tile_pair(buf, tA, sg.n, sg.bad, sg, std::false_type{});
+            int at = 0;
+            unsigned parity = 0;
+            for (int k = 0; k < n_st && ok; k++) {
+                if (!(ok = wait(&sm.full[at], parity, p.wait_polls, &sm.dead))) break;
+                const int word = sm.stage[at].word, n = word & (kFresh - 1);
+                if (__builtin_expect((word & kFresh) && k > 0, 0)) {
+                    if (!(ok = flush())) break;
+                    now_b = sm.stage[at].b;
+                    now_h = sm.stage[at].h_rb;
+                    if (!(ok = start())) break;
+                }
+                const uint8_t *buf = mine + at * G::stage;
+                for (int tA = tp * 32; NP * tA < n; tA += 32 * parts) {
+                    if (NP * (tA + 32) <= n && !(word & kBad)) tile_pair(buf, tA, n, sm.stage[at], std::true_type{});
+                    else tile_pair(buf, tA, n, sm.stage[at], std::false_type{});
+                }
+                __syncwarp();
+                if (lane == 0) arrive(&sm.empty[at]);
+                if (++at == NS) at = 0, parity ^= 1u;
+                if (__builtin_expect(r.tiles >= kFold, 0)) fold();
             }
-            __syncwarp();
-            if (lane == 0) arrive(&sm.empty[at]);
-            if (__builtin_expect(r.tiles >= kFold, 0)) fold();
-        }
-        if (ok) ok = flush();
-        if (!ok) {  // let this warp's copies land before it leaves
-            if (lane == 0) {
+            if (ok) ok = flush();
+            if (!ok && lane == 0) {
                 *const_cast<volatile int *>(&sm.dead) = 1;
                 p.state[worker] = 1;
             }
-            for (int j = k; j <= issued; j++)
-                if (j % kWarps == warp) mbar_wait(&sm.full[j % NS], (j / NS) & 1);
         }
     }
     pdl_wait();  // the call's last launch ends behind its first
 }
 
-inline cudaError_t launch(const void *kernel, size_t smem, const PagedParams &p, void **args, cudaStream_t s) {
+// teams: workers of a CTA.
+inline cudaError_t launch(const void *kernel, size_t smem, int threads, int teams, const PagedParams &p, void **args, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.cls.workers));
-    cfg.blockDim = dim3(kThreads);
+    // workers t, t + grid, t + 2 grid ... are one CTA's: few stages go to as many SMs
+    const int ctas = std::max(1, p.cls.workers / teams);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.cls.workers < current_sm_count() * teams ? std::min(p.cls.workers, current_sm_count()) : ctas));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -575,12 +604,13 @@ cudaError_t launch_packed(const PagedParams &p, cudaStream_t s) {
     lv.c1 = p.centroid[cb_off(VB) + 1];
     int nhb = head_blocks(p.list.R, 4 / NP);
     void *args[] = {const_cast<PagedParams *>(&p), &lv, &nhb};
-    return launch(reinterpret_cast<const void *>(paged_packed_kernel<KB, VB, NP>), Geom<KB, VB, NP>::smem, p, args, s);
+    return launch(reinterpret_cast<const void *>(paged_packed_kernel<KB, VB, NP>), Geom<KB, VB, NP>::smem, kTeamThreads,
+                  Geom<KB, VB, NP>::TEAMS, p, args, s);
 }
 
 template <int KB, int VB, int NP>
 PagedShape shape_packed() {
-    return {Geom<KB, VB, NP>::PT, Geom<KB, VB, NP>::CTAS};
+    return {Geom<KB, VB, NP>::PT, Geom<KB, VB, NP>::TEAMS};
 }
 
 }  // namespace pmma

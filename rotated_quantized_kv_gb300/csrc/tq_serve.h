@@ -255,6 +255,8 @@ struct PagedSeg {
     int64_t table_stride;
     const int *len;                      // tokens of a sequence, or nullptr: limit
     int n_pages, page, limit;            // limit: most tokens a sequence can hold
+    uint32_t magic;                      // t / page = t magic >> shift for 0 <= t < 2^31
+    int shift;
 };
 struct PagedClass {
     int kb, vb, law;
