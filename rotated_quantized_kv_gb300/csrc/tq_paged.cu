@@ -61,9 +61,8 @@ __global__ void __launch_bounds__(kPlainThreads) paged_plain_kernel(const __grid
     float *row_m = S + R * TT, *row_l = row_m + R, *row_c = row_l + R;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, worker = blockIdx.x;
     asm volatile("griddepcontrol.launch_dependents;");
-    if (threadIdx.x == 0) p.state[worker] = 0;
     const PagedList &l = p.list;
-    const int total = ranges_of<kPlainThreads, 1>(l, p.cls, worker, 0, p.first, buf);
+    const int total = ranges_of<kPlainThreads, 1>(l, p.cls, Share<kPlainThreads>(l, p.cls), worker, 0, p.first, buf);
     int begin, end;
     worker_range(p.cls, total, worker, begin, end);
     if (begin < end) {
@@ -150,10 +149,14 @@ __global__ void __launch_bounds__(kPlainThreads) paged_plain_kernel(const __grid
             }
             const Walk x = w;
             const bool last = at + 1 == end;
-            fresh = !last && next(l, p.cls, w);
+            fresh = false;
+            if (!last && ++w.st == w.n_st) {
+                w = next(l, p.cls, w);
+                fresh = w.fresh;
+            }
             if (!fresh && !last) continue;
             __syncthreads();
-            float *rec = p.part + group_slot(l, p.cls, worker, x.b, x.h, x.rb) * R * (D + 4);
+            float *rec = p.part + p.cls.part0 + group_slot(l, p.cls, worker, x.b, x.h, x.rb) * R * (D + 4);
             for (int i = threadIdx.x; i < R; i += kPlainThreads) {
                 rec[i * (D + 4)] = row_m[i];
                 rec[i * (D + 4) + 1] = row_l[i];
@@ -178,10 +181,10 @@ constexpr int kMergeThreads = 256;
 
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ PagedMergeParams p) {
     __shared__ __align__(16) float sum[2][kMergeThreads * 4];  // [space][record lane][d]
-    __shared__ float red[2][kMergeThreads / 32];
+    __shared__ float red[kMergeThreads / 32];
     __shared__ int span[kPagedClasses][2];                    // first and last worker of the row's group
-    const int d = p.d, B = p.list.B, H = p.list.H, R = p.list.R, n_rb = p.list.n_rb;
-    const int row = blockIdx.x, b = row / (H * p.g), h = row / p.g % H, j = row % p.g, rb = j / R;
+    const int d = p.d, B = p.list.B, H = p.list.H;
+    const int row = blockIdx.x, b = row / (H * p.g), h = row / p.g % H, j = row % p.g;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x < p.n_classes) {
@@ -190,8 +193,8 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
         const int n = head_stages(p.list, c, b, h);
         int w0 = 0, w1 = -1;
         if (n > 0) {
-            int s = first[b] + rb * n;
-            for (int i = 0; i < h; i++) s += n_rb * head_stages(p.list, c, b, i);
+            int s = first[b] + j / c.R * n;
+            for (int i = 0; i < h; i++) s += c.n_rb * head_stages(p.list, c, b, i);
             const int workers = workers_of(c, first[B]);
             w0 = max(worker_of(first[B], s, workers), 0);
             w1 = min(worker_of(first[B], s + n - 1, workers), workers - 1);
@@ -199,30 +202,21 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
         span[threadIdx.x][0] = w0;
         span[threadIdx.x][1] = w1;
     }
+    if (row == 0 && threadIdx.x == 0) *p.error = 0;
     __syncthreads();
-    const size_t step = static_cast<size_t>(R) * (d + 4);
-    auto record = [&](int c, int w) { return p.part + group_slot(p.list, p.cls[c], w, b, h, rb) * step + (j % R) * (d + 4); };
-    // the largest m, and whether a worker gave up
+    auto record = [&](int c, int w) {
+        const PagedClass &k = p.cls[c];
+        return p.part + k.part0 + (group_slot(p.list, k, w, b, h, j / k.R) * k.R + j % k.R) * (d + 4);
+    };
+    // the largest m
     float M = -kInf;
-    int bad = 0;
     for (int c = 0; c < p.n_classes; c++)
-        for (int w = span[c][0] + threadIdx.x; w <= span[c][1]; w += kMergeThreads) {
-            M = fmaxf(M, record(c, w)[0]);
-            bad |= p.state[p.state0[c] + w];
-        }
+        for (int w = span[c][0] + threadIdx.x; w <= span[c][1]; w += kMergeThreads) M = fmaxf(M, record(c, w)[0]);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (lane == 0) red[0][warp] = M;
-    bad = __syncthreads_or(bad);
-    for (int i = 0; i < kMergeThreads / 32; i++) M = fmaxf(M, red[0][i]);
-    if (blockIdx.x == 0) {  // the call's flag
-        int any = 0;
-        for (int c = 0; c < p.n_classes; c++)
-            for (int w = threadIdx.x; w < p.cls[c].workers; w += kMergeThreads) any |= p.state[p.state0[c] + w];
-        any = __syncthreads_or(any);
-        if (threadIdx.x == 0) *p.error = any ? 1 : 0;
-    }
-    if (bad) return;
+    if (lane == 0) red[warp] = M;
+    __syncthreads();
+    for (int i = 0; i < kMergeThreads / 32; i++) M = fmaxf(M, red[i]);
     const int quads = d / 4, lanes = kMergeThreads / quads, quad = threadIdx.x % quads, rl = threadIdx.x / quads;
     float L = 0.f;  // (of the record lane)
     float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
@@ -298,9 +292,7 @@ cudaError_t plain(const PagedParams &p, cudaStream_t s) {
 
 #define TQ_PAGED_KB(KB)                                                       \
     cudaError_t launch_paged_kb##KB##_np1(const PagedParams &p, cudaStream_t s);  \
-    cudaError_t launch_paged_kb##KB##_np2(const PagedParams &p, cudaStream_t s);  \
-    PagedShape paged_shape_kb##KB##_np1(int vb);                              \
-    PagedShape paged_shape_kb##KB##_np2(int vb);
+    cudaError_t launch_paged_kb##KB##_np2(const PagedParams &p, cudaStream_t s);
 TQ_PAGED_KB(1)
 TQ_PAGED_KB(2)
 TQ_PAGED_KB(3)
@@ -311,34 +303,23 @@ TQ_PAGED_KB(7)
 TQ_PAGED_KB(8)
 #undef TQ_PAGED_KB
 cudaError_t launch_paged_fp16(const PagedParams &p, cudaStream_t s);
-PagedShape paged_shape_fp16(int d);
 
 namespace {
 using PackedLaunch = cudaError_t (*)(const PagedParams &, cudaStream_t);
-using PackedShape = PagedShape (*)(int);
-#define TQ_PAGED_EACH(f, np)                                                                              \
-    { f##1_np##np, f##2_np##np, f##3_np##np, f##4_np##np, f##5_np##np, f##6_np##np, f##7_np##np, f##8_np##np }
+#define TQ_PAGED_EACH(f, np) {f##1_np##np, f##2_np##np, f##3_np##np, f##4_np##np, f##5_np##np, f##6_np##np, f##7_np##np, f##8_np##np}
 constexpr PackedLaunch kPackedLaunch[2][8] = {TQ_PAGED_EACH(launch_paged_kb, 1), TQ_PAGED_EACH(launch_paged_kb, 2)};
-constexpr PackedShape kPackedShape[2][8] = {TQ_PAGED_EACH(paged_shape_kb, 1), TQ_PAGED_EACH(paged_shape_kb, 2)};
 #undef TQ_PAGED_EACH
 
 // Head dims that take the tensor cores.
 bool on_tensor_cores(int d) { return d == 64 || d == 128; }
 }  // namespace
 
-PagedShape paged_shape(int d, int kb, int vb) {
-    PagedShape s = {kPlainUnit, 2};
-    if (on_tensor_cores(d)) s = kb ? kPackedShape[d == 64][kb - 1](vb) : paged_shape_fp16(d);
-    s.workers *= current_sm_count();
-    return s;
-}
-
-// Rows a block: a warp of the tensor-core form takes four (two of head_dim 64), a CTA has four
-// warps for blocks of rows or parts of the tokens.
-int paged_rows(int d, int g) {
-    if (!on_tensor_cores(d)) return kPlainRows;
-    const int per = d == 64 ? 2 : 4;
-    return g <= per ? per : g <= 2 * per ? 2 * per : 4 * per;
+// A warp of the tensor-core forms takes four rows, two of packed pages of head_dim 64.
+PagedShape paged_shape(int d, bool packed) {
+    if (!on_tensor_cores(d)) return {kPlainUnit, kPlainRows, 2 * current_sm_count()};
+    const int workers = kPagedWarps * current_sm_count();
+    if (!packed) return {16, 4, workers};
+    return d == 64 ? PagedShape{64, 2, workers} : PagedShape{32, 4, workers};
 }
 
 cudaError_t launch_paged(const PagedParams &p, cudaStream_t s) {

@@ -22,6 +22,7 @@ __device__ __forceinline__ int seg_stages(const PagedList &l, const PagedClass &
 // Stages of (b, h, any rb).
 __device__ __forceinline__ int head_stages(const PagedList &l, const PagedClass &c, int b, int h) {
     int n = 0;
+#pragma unroll 1
     for (int i = 0; i < c.n; i++)
         if ((c.heads[i] >> h) & 1) n += seg_stages(l, c, i, b);
     return n;
@@ -29,8 +30,9 @@ __device__ __forceinline__ int head_stages(const PagedList &l, const PagedClass 
 // Stages of sequence b (below 2^31 over all sequences: the host checks it for the limits).
 __device__ __forceinline__ int sequence_stages(const PagedList &l, const PagedClass &c, int b) {
     int n = 0;
+#pragma unroll 1
     for (int i = 0; i < c.n; i++) n += __popc(c.heads[i]) * seg_stages(l, c, i, b);
-    return n * l.n_rb;
+    return n * c.n_rb;
 }
 
 // Workers that have a stage: those of a launch are sized for the segments' limits.
@@ -52,6 +54,7 @@ struct Walk {
     int i;               // segment of the class
     int st, n_st;        // stage, and stages of the segment
     int tokens;          // of the segment
+    bool fresh;          // begins a (b, h, rb)
 };
 
 __device__ __forceinline__ void lost(Walk &w) { w.h = w.rb = w.i = w.st = w.tokens = 0, w.n_st = 1; }
@@ -61,18 +64,35 @@ __device__ __forceinline__ void bind(const PagedList &l, const PagedClass &c, Wa
     w.n_st = w.tokens / c.unit + (w.tokens % c.unit ? 1 : 0);
 }
 
-// Stage `at` of sequence b.
-__device__ __forceinline__ Walk seek(const PagedList &l, const PagedClass &c, int b, int at) {
+// Stage `at` of sequence b.  (This and what follows are no part of a kernel's loop and would be most of its code, a
+// quarter of a megabyte, if they were inlined: warps then waited for instructions.)
+static __device__ __noinline__ Walk seek(const PagedList &l, const PagedClass &c, int b, int at) {
     Walk w;
     w.b = b;
+    w.fresh = true;
+    if (c.n == 1) {  // one segment: all its heads have as many stages
+        w.i = 0;
+        bind(l, c, w);
+        if (w.n_st > 0) {
+            const int block = at / w.n_st, head = block / c.n_rb;
+            w.st = at - block * w.n_st;
+            w.rb = block - head * c.n_rb;
+            w.h = static_cast<int>(__fns(c.heads[0], 0, head + 1));
+            if (w.h < l.H) return w;
+        }
+        lost(w);
+        return w;
+    }
+#pragma unroll 1
     for (w.h = 0; w.h < l.H; w.h++) {
         const int n = head_stages(l, c, b, w.h);
-        if (at >= n * l.n_rb) {
-            at -= n * l.n_rb;
+        if (at >= n * c.n_rb) {
+            at -= n * c.n_rb;
             continue;
         }
         w.rb = at / n;
         at -= w.rb * n;
+#pragma unroll 1
         for (w.i = 0; w.i < c.n; w.i++) {
             if (!((c.heads[w.i] >> w.h) & 1)) continue;
             bind(l, c, w);
@@ -88,23 +108,26 @@ __device__ __forceinline__ Walk seek(const PagedList &l, const PagedClass &c, in
     return w;
 }
 
-// The next stage (whole warps; there is one).  True: of another (b, h, rb).
-__device__ __forceinline__ bool next(const PagedList &l, const PagedClass &c, Walk &w) {
-    if (++w.st < w.n_st) return false;
+// The first stage behind the segment's last one (whole warps; there is one).  fresh: it is of another (b, h, rb).
+static __device__ __noinline__ Walk next(const PagedList &l, const PagedClass &c, Walk w) {
     w.st = 0;
-    bool other = false;
+    bool other = false, moved = false;
     for (;;) {
         while (++w.i < c.n) {
             if (!((c.heads[w.i] >> w.h) & 1)) continue;
-            bind(l, c, w);
-            if (w.n_st > 0) return other;
+            if (c.n > 1 || moved) bind(l, c, w);  // (one segment: as the head before)
+            if (w.n_st > 0) {
+                w.fresh = other;
+                return w;
+            }
         }
         w.i = -1;
         other = true;
-        if (++w.rb < l.n_rb) continue;
+        if (++w.rb < c.n_rb) continue;
         w.rb = 0;
         if (++w.h < l.H) continue;
         w.h = 0;
+        moved = true;
         // the next sequence that has a stage, 32 at a time
         unsigned some = 0;
         int b0 = w.b + 1;
@@ -115,22 +138,34 @@ __device__ __forceinline__ bool next(const PagedList &l, const PagedClass &c, Wa
         }
         if (!some) {
             lost(w);
-            return true;
+            w.fresh = true;
+            return w;
         }
         w.b = b0 + __ffs(some) - 1;
     }
 }
 
-// Ranges of a CTA's TEAMS workers, worker t * step + first_worker for team t (THREADS threads, all of the CTA;
-// synchronises).  buf: THREADS / 32 + 2 TEAMS ints of shared memory; team t's first sequence and the stages of it before
-// its range are at THREADS / 32 + 2 t.  Returns the total.
+// The stages of the thread's share of the sequences [b0, b1) (THREADS threads).
+template <int THREADS>
+struct Share {
+    int b0, b1, sum;
+    __device__ __forceinline__ Share(const PagedList &l, const PagedClass &c) {
+        const int chunk = (l.B + THREADS - 1) / THREADS;
+        b0 = min(static_cast<int>(threadIdx.x) * chunk, l.B);
+        b1 = min(b0 + chunk, l.B);
+        sum = 0;
+#pragma unroll 1
+        for (int b = b0; b < b1; b++) sum += sequence_stages(l, c, b);
+    }
+};
+// Ranges of a CTA's TEAMS workers, worker t * step + first_worker for team t (all of the CTA's threads with their
+// shares; synchronises).  buf: THREADS / 32 + 2 TEAMS ints of shared memory; team t's first sequence and the stages of it
+// before its range are at THREADS / 32 + 2 t.  Returns the total.
 template <int THREADS, int TEAMS>
-__device__ __forceinline__ int ranges_of(const PagedList &l, const PagedClass &c, int first_worker, int step, int *first, int *buf) {
+__device__ __forceinline__ int ranges_of(const PagedList &l, const PagedClass &c, const Share<THREADS> &own, int first_worker, int step,
+                                         int *first, int *buf) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int chunk = (l.B + THREADS - 1) / THREADS, b0 = min(static_cast<int>(threadIdx.x) * chunk, l.B), b1 = min(b0 + chunk, l.B);
-    int sum = 0;
-    for (int b = b0; b < b1; b++) sum += sequence_stages(l, c, b);
-    int incl = sum;
+    int incl = own.sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -138,28 +173,30 @@ __device__ __forceinline__ int ranges_of(const PagedList &l, const PagedClass &c
     }
     if (lane == 31) buf[warp] = incl;
     __syncthreads();
-    int before = incl - sum, total = 0;
+    int before = incl - own.sum, total = 0;
     for (int w = 0; w < THREADS / 32; w++) {
         if (w < warp) before += buf[w];
         total += buf[w];
     }
     if (first_worker == 0) {
         int at = before;
-        for (int b = b0; b < b1; b++) {
+#pragma unroll 1
+        for (int b = own.b0; b < own.b1; b++) {
             first[b] = at;
             at += sequence_stages(l, c, b);
         }
         if (threadIdx.x == 0) first[l.B] = total;
     }
     const int workers = workers_of(c, total);
-#pragma unroll
+#pragma unroll 1
     for (int t = 0; t < TEAMS; t++) {
         const int worker = t * step + first_worker;
         if (worker >= workers) break;
         const int begin = worker_begin(total, worker, workers);
-        if (sum > 0 && before <= begin && begin < before + sum) {
-            int at = before, b = b0;
-            for (int n; b + 1 < b1 && begin >= at + (n = sequence_stages(l, c, b)); b++) at += n;
+        if (own.sum > 0 && before <= begin && begin < before + own.sum) {
+            int at = before, b = own.b0;
+#pragma unroll 1
+            for (int n; b + 1 < own.b1 && begin >= at + (n = sequence_stages(l, c, b)); b++) at += n;
             buf[THREADS / 32 + 2 * t] = b;
             buf[THREADS / 32 + 2 * t + 1] = begin - at;
         }
@@ -184,8 +221,37 @@ __device__ __forceinline__ int page_at(const PagedSeg &s, int b, int index) {
     return page >= 0 && page < s.n_pages ? page : -1;
 }
 
+// A warp's view of a sequence's row of the table: two windows of 32 entries, so that a walk along the
+// sequence reads the table once every 32 pages, and ahead.
+struct Pages {
+    int now, then;       // the lane's entries of the windows at `base` and behind it
+    int base;
+    __device__ __forceinline__ int entry(const PagedSeg &s, int b, int last, int index) const {
+        return index > last ? -1 : s.table ? s.table[b * s.table_stride + index] : 0;
+    }
+    // The row of sequence b from page `index` on; `last`: its last page.
+    __device__ __forceinline__ void open(const PagedSeg &s, int b, int last, int index, int lane) {
+        base = index & ~31;
+        now = entry(s, b, last, base + lane);
+        then = entry(s, b, last, base + 32 + lane);
+    }
+    // Moves on to a place at page `index` (not before base).
+    __device__ __forceinline__ void move(const PagedSeg &s, int b, int last, int index, int lane) {
+        if (index < base + 32) return;
+        if (index >= base + 64) return open(s, b, last, index, lane);
+        base += 32;
+        now = then;
+        then = entry(s, b, last, base + 32 + lane);
+    }
+    // Entry `index` (in the windows; its own for each lane, all lanes).
+    __device__ __forceinline__ int at(int index) const {
+        const int x = __shfl_sync(0xffffffffu, now, index & 31), y = __shfl_sync(0xffffffffu, then, index & 31);
+        return index < base + 32 ? x : y;
+    }
+};
+
 __device__ __forceinline__ size_t group_slot(const PagedList &l, const PagedClass &c, int worker, int b, int h, int rb) {
-    return static_cast<size_t>(c.slot0 + worker + (static_cast<long long>(b) * l.H + h) * l.n_rb + rb);
+    return static_cast<size_t>(worker + (static_cast<long long>(b) * l.H + h) * c.n_rb + rb);
 }
 
 }  // namespace paged

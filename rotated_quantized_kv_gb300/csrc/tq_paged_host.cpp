@@ -29,10 +29,9 @@ tq_status check_pages(int batch, int page_size, int max_pages, int n_pages, cons
 
 // The classes of a view's heads, their workers and the workspace's areas.
 struct PagedLayout {
-    int R, n_rb, n_classes;
+    int n_classes;
     PagedClass cls[kPagedClasses];
-    int64_t state0[kPagedClasses];
-    size_t state_off, first_off, part_off, total;
+    size_t first_off, part_off, total;
 };
 
 tq_status check_paged_view(const tq_layer_view *lv, int B, int H, int Hq, int d, bool check_ptrs) {
@@ -58,8 +57,6 @@ tq_status check_paged_view(const tq_layer_view *lv, int B, int H, int Hq, int d,
 
 tq_status paged_layout(const tq_layer_view *lv, int B, int H, int Hq, int d, PagedLayout &o) {
     const int g = Hq / H;
-    o.R = paged_rows(d, g);
-    o.n_rb = (g + o.R - 1) / o.R;
     o.n_classes = 0;
     for (int i = 0; i < lv->n_segments; ++i) {
         const tq_segment &sg = lv->seg[i];
@@ -74,7 +71,9 @@ tq_status paged_layout(const tq_layer_view *lv, int B, int H, int Hq, int d, Pag
                 if (k == kPagedClasses) return TQ_ERR_UNSUPPORTED;
                 std::memset(&c, 0, sizeof(c));
                 c.kb = kb, c.vb = vb, c.law = law;
-                const PagedShape s = paged_shape(d, kb, vb);
+                const PagedShape s = paged_shape(d, packed);
+                c.R = s.rows;
+                c.n_rb = (g + s.rows - 1) / s.rows;
                 c.unit = s.unit;
                 c.workers = s.workers;
                 ++o.n_classes;
@@ -86,19 +85,15 @@ tq_status paged_layout(const tq_layer_view *lv, int B, int H, int Hq, int d, Pag
             c.heads[c.n - 1] |= static_cast<uint16_t>(1u << h);
         }
     }
-    const int64_t groups = static_cast<int64_t>(B) * H * o.n_rb;
-    int64_t slots = 0, states = 0;
+    int64_t floats = 0;
     for (int k = 0; k < o.n_classes; ++k) {
-        o.state0[k] = states;
-        o.cls[k].slot0 = slots;
-        states += o.cls[k].workers;
-        slots += o.cls[k].workers + groups;
+        PagedClass &c = o.cls[k];
+        c.part0 = floats;
+        floats += (c.workers + static_cast<int64_t>(B) * H * c.n_rb) * c.R * (d + 4);
     }
-    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    o.state_off = 256;  // the error flag has the first 256 bytes
-    o.first_off = up(o.state_off + sizeof(int) * states);
-    o.part_off = up(o.first_off + sizeof(int) * o.n_classes * (static_cast<size_t>(B) + 1));
-    o.total = o.part_off + static_cast<size_t>(slots) * o.R * (d + 4) * sizeof(float);
+    o.first_off = 256;  // the error flag has the first 256 bytes
+    o.part_off = (o.first_off + sizeof(int) * o.n_classes * (static_cast<size_t>(B) + 1) + 255) / 256 * 256;
+    o.total = o.part_off + static_cast<size_t>(floats) * sizeof(float);
     return TQ_OK;
 }
 
@@ -171,6 +166,8 @@ tq_status tq_paged_attention(const tq_layer_view *pools, const tq_pages *pages, 
             if (pg.max_pages < 0 || pg.table_stride_b < 0 || (batch > 1 && pg.table_stride_b < pg.max_pages) || !pg.len)
                 return TQ_ERR_ARG;
             if (s.page > 0 && pg.max_pages > 0x7fffffff / s.page) return TQ_ERR_UNSUPPORTED;
+            // bytes of a page in 32 bits
+            if ((s.seg.kblock | s.seg.vblock | (static_cast<uint64_t>(n_heads) * s.page * 4)) >> 32) return TQ_ERR_UNSUPPORTED;
             s.table = pg.table;
             s.table_stride = pg.table_stride_b;
             s.limit = pg.max_pages * s.page;
@@ -191,16 +188,14 @@ tq_status tq_paged_attention(const tq_layer_view *pools, const tq_pages *pages, 
     st = paged_layout(pools, batch, n_heads, q_heads, head_dim, o);
     if (st != TQ_OK) return st;
     if (ws_bytes < o.total) return TQ_ERR_SIZE;
-    p.list.R = o.R;
-    p.list.n_rb = o.n_rb;
     int64_t most[kPagedClasses];  // stages at the limits
     for (int k = 0; k < o.n_classes; ++k) {
         PagedClass &c = o.cls[k];
         most[k] = 0;
         for (int i = 0; i < c.n; ++i)
             most[k] += static_cast<int64_t>(__builtin_popcount(c.heads[i])) * ((p.list.limit[c.seg[i]] + c.unit - 1) / c.unit);
-        if (most[k] > 0x7fffffff / (static_cast<int64_t>(batch) * o.n_rb)) return TQ_ERR_UNSUPPORTED;
-        most[k] *= static_cast<int64_t>(batch) * o.n_rb;
+        if (most[k] > 0x7fffffff / (static_cast<int64_t>(batch) * c.n_rb)) return TQ_ERR_UNSUPPORTED;
+        most[k] *= static_cast<int64_t>(batch) * c.n_rb;
         c.workers = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(c.workers, most[k])));
     }
     uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -209,7 +204,6 @@ tq_status tq_paged_attention(const tq_layer_view *pools, const tq_pages *pages, 
     p.q = static_cast<const uint16_t *>(q);
     p.qs[0] = q_stride[0], p.qs[1] = q_stride[1];
     p.part = reinterpret_cast<float *>(ws + o.part_off);
-    p.wait_polls = decode_wait_polls();
     std::memcpy(p.sign_bits, pools->rot.sign_bits, sizeof(p.sign_bits));
     p.inv_sqrt_d = rotation_scale(head_dim);
     p.qk_scale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(head_dim)));
@@ -221,14 +215,10 @@ tq_status tq_paged_attention(const tq_layer_view *pools, const tq_pages *pages, 
     m.out = static_cast<uint16_t *>(out);
     m.part = p.part;
     m.first = reinterpret_cast<int *>(ws + o.first_off);
-    m.state = reinterpret_cast<int *>(ws + o.state_off);
     m.error = reinterpret_cast<int *>(ws);
     std::memcpy(m.sign_bits, p.sign_bits, sizeof(m.sign_bits));
     m.inv_sqrt_d = p.inv_sqrt_d;
-    for (int k = 0; k < o.n_classes; ++k) {
-        m.cls[k] = o.cls[k];
-        m.state0[k] = o.state0[k];
-    }
+    std::copy(o.cls, o.cls + o.n_classes, m.cls);
     try {  // the codebooks before anything is launched
         for (int k = 0; k < o.n_classes; ++k) {
             const uint8_t vb = static_cast<uint8_t>(o.cls[k].vb);
@@ -242,7 +232,6 @@ tq_status tq_paged_attention(const tq_layer_view *pools, const tq_pages *pages, 
         const uint8_t vb = static_cast<uint8_t>(p.cls.vb);
         if (vb) value_centroids(p.centroid, &vb, 1, p.cls.law);
         p.first = const_cast<int *>(m.first) + static_cast<size_t>(k) * (batch + 1);
-        p.state = const_cast<int *>(m.state) + o.state0[k];
         p.first_class = k == 0;
         st = launched(launch_paged(p, static_cast<cudaStream_t>(stream)));
         if (st != TQ_OK) return st;

@@ -1,26 +1,26 @@
-// tq_paged_mma.cuh -- attention of one new token over paged segments at head dims 64 and 128:
-// what the kernels of packed and of fp16 pages share, and the packed one, specialised by
-// (key bits, value bits).
+// tq_paged_mma.cuh -- attention of one new token over paged segments at head dims 64 and 128: the
+// kernel, and its form for packed pages, specialised by (key bits, value bits).
 //
 // The arithmetic of a tile is that of decode attention (tq_decode_packed.cuh: raw key codes as
 // fp16 subnormals against the query's hi and lo parts, values by table into the P.V product,
 // mma.m16n8k16).  What differs:
-//   - a warp takes four query heads, and the eight columns of the P.V product hold the weights as fp16 hi + 2^-11 lo
-//     (22 bits, down to 2^-36 of the row's largest);
-//     more heads of a KV head go to other warps of the CTA, on the same rows in shared memory;
-//   - head_dim 64: a tile row is a pair of tokens read as one record of 128 dims; the four columns
+//   - the eight columns of the P.V product are four query heads' weights as fp16 hi + 2^-11 lo (22 bits, down to
+//     2^-36 of the row's largest);
+//   - head_dim 64: a tile row is a pair of tokens read as one record of 128 dims, and the four columns
 //     are two heads times two parities, a query with zeros in the other token's half, so that a (head, parity) is a
-//     head of its own until the CTA joins its parts;
+//     head of its own until the record;
 //   - weights are relative to the row's largest weighted value, as in tq_tree_mma.cu: the running
-//     maximum is that of S + log2 sigma (sigma in [2^-64, 2^64], its logarithm read off the bits: within 0.09 above), so
+//     maximum is that of S + log2 sigma (sigma from 2^-64 up, its logarithm read off the bits: within 0.09 above), so
 //     that fp16 holds the weights that count whatever the values' sizes;
 //   - sums leave the tensor cores every kFold tiles: mma.sync adds with truncation, which drifts by some
-//     2^-19 of the sum a tile.  They go to a copy in shared memory, by binary32 additions, and at the
-//     end of a (sequence, head) the warps' copies join there into one record;
-//   - nothing stops the CTA between stages: warps take turns at issuing the copies of a stage (so that no
-//     scheduler of the SM has all of that work), lane i those of the i-th page of it, page numbers read
-//     a turn ahead; buffers go round by full and empty barriers.  Every wait is bounded, and a warp that gives
-//     up marks its worker, sees its own copies land and leaves; it waits for no one.
+//     2^-19 of the sum a tile.  They go to the warp's copy in shared memory, by binary32 additions.
+//
+// Every warp is a worker of its own: a range of the stage list (tq_paged.cuh), a ring of stages that it fills
+// itself by cp.async, its queries, its sums, its records; warps meet nowhere behind the prologue, and nothing waits but for
+// its own copies.  (Measured against it on 32 x 32768 tokens of 8 heads, K4V4, 64-token pages: CTAs of four warps that share a
+// stage, the warps issuing bulk copies in turn, then teams of four warps with a loader warp each by bulk copies and by cp.async:
+// the loader's serial instructions, some 2000 cycles a stage, and the barriers bounded all of these.)  Twelve
+// warps an SM are what 168 registers leave; they share one value table, a column a lane.
 #pragma once
 
 #include <algorithm>
@@ -34,11 +34,14 @@ namespace pmma {
 
 using namespace dec;
 
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = kPagedWarps;
+constexpr int kPagedThreads = 32 * kWarps;
 constexpr int kFold = 16;               // tiles of 16 rows between folds
-constexpr int kHeadStride = 128 + 4;    // floats of a head's copy of the sums (apart in banks)
-constexpr int kCopyBytes = kWarps * 4 * kHeadStride * 4;
-constexpr int kMaxRows = 16;
+constexpr int kMaxRing = 6;
+// Floats of a head's copy of the sums (heads apart in banks), and bytes of a warp's four.
+__host__ __device__ constexpr int copy_stride(int d) { return d + 4; }
+__host__ __device__ constexpr int copy_bytes(int d) { return 4 * copy_stride(d) * 4; }
+constexpr int kSmemMax = 232448;
 
 // Value levels of the class: fp16(s c_k), 1/s, and level 1 of a 1-bit codebook.
 struct Levels {
@@ -46,36 +49,28 @@ struct Levels {
     float inv, c1;
 };
 
-// A wait that ends early where another warp gave up.
-__device__ __forceinline__ bool wait(uint64_t *bar, unsigned parity, int polls, const volatile int *dead) {
-    for (int i = 0; i < polls; i++) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (*dead) return false;
-    }
-    return false;
+// 16 bytes into shared memory; a cache that is read once streams through L2: evicted first.
+__device__ __forceinline__ void copy16(unsigned dst, const void *src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy) : "memory");
 }
-__device__ __forceinline__ void arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ uint64_t policy_for(bool once) {
+    uint64_t first, normal;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(normal));
+    return once ? first : normal;
 }
 
-// What the loader tells the others of a stage.
-struct Stage {
-    int word;            // tokens (none: 0), kFresh: another (sequence, head, block), kBad: some page outside the pool
+// What a special stage of the ring is.
+struct alignas(16) Stage {
+    int word;            // tokens, and kFresh (another sequence, head or block of rows), kPart (not whole)
     int b, h_rb;         // sequence; KV head and block of rows
-    unsigned bad;        // bit i: the i-th page of it is outside the pool
-    int page, skip;      // tokens a page, and tokens of the first page before the stage
+    unsigned bad;        // kPart: bit i: the i-th page of it is outside the pool
+    int page, skip;      // kPart: tokens a page, and tokens of the first page before the stage
+    int pad[2];
 };
-constexpr int kFresh = 1 << 16, kBad = 1 << 17;
+constexpr int kFresh = 1 << 16, kPart = 1 << 17;
 
-struct alignas(16) Small {  // a team's shared memory besides stages, tables and copies
-    uint64_t full[8], empty[8], sync, head;
-    Stage stage[8];
-    float m[kWarps][4], l[kWarps][4];
-    float qsum[kMaxRows], qexp[kMaxRows];
-    int dead;
-};
-
-// Running state of a warp: lane (g, c) has head c of its four; columns 2c, 2c + 1 of the
+// A warp's running state: lane (g, c) has head c of its four; columns 2c, 2c + 1 of the
 // accumulator are that head's hi and lo parts.
 template <int MT>
 struct Run {
@@ -83,9 +78,9 @@ struct Run {
     float l, w;          // sums of p, and of p sigma since the last fold
     float m_ref;         // reference of the copy
     float acc[MT][4];
-    __device__ __forceinline__ float sum(int mt, int k) const { return fmaf(acc[mt][2 * k + 1], 0x1p-11f, acc[mt][2 * k]); }
     int tiles;           // since the last fold
     bool some;           // the copy holds something
+    __device__ __forceinline__ float sum(int mt_, int k) const { return fmaf(acc[mt_][2 * k + 1], 0x1p-11f, acc[mt_][2 * k]); }
     __device__ __forceinline__ void clear() {
         w = 0.f;
         tiles = 0;
@@ -111,7 +106,7 @@ __device__ __forceinline__ void softmax(Run<MT> &r, const float (&s)[2 * T], con
 #pragma unroll
     for (int i = 0; i < 2 * T; i++) {
         // log2 v + 127 within [0, 0.09]: the exponent, and the mantissa as its fraction
-        const float lg = static_cast<float>(__float_as_int(fminf(fmaxf(v[i], 0x1p-64f), 0x1p64f)));
+        const float lg = static_cast<float>(__float_as_int(fmaxf(v[i], 0x1p-64f)));
         const float t = fmaf(lg, 0x1p-23f, s[i]);
         top = fmaxf(top, FULL || ok[i] ? t : kNegInf);
     }
@@ -149,137 +144,330 @@ __device__ __forceinline__ void softmax(Run<MT> &r, const float (&s)[2 * T], con
     }
 }
 
-// A team's four warps meet (bounded).
-__device__ __forceinline__ bool meet(Small &sm, unsigned &phase, int polls, int lane) {
-    __syncwarp();
-    if (lane == 0) arrive(&sm.sync);
-    const bool ok = wait(&sm.sync, phase & 1u, polls, &sm.dead);
-    phase++;
-    return ok;
-}
-
-// The block's queries, rotated or not, as fp16 hi and lo parts [row][part][D] of q 2^-e, e their sum's
-// and the row's exponent (the largest coordinate in [0.5, 1)).
-template <int D, bool ROTATE>
-__device__ __forceinline__ void stage_queries(const PagedParams &p, Small &sm, __half *q, int b, int h, int rb, int rows, int warp, int lane) {
+// Four query rows of a block (those behind the last head: zeros), as fp16 hi and lo parts [row][part][D] of R q 2^-e, and
+// in lane i of the warp row i's sum and 2^e (the largest coordinate in [0.5, 1)).  Four at once: their shuffles overlap.
+template <int D>
+__device__ __forceinline__ void rotate_queries(const PagedParams &p, __half *to, int b, int h, int rb, int lane, float &qsum, float &qexp) {
     constexpr int J = D / 32;
-    for (int i = warp; i < rows; i += kWarps) {
-        const int row = rb * rows + i;
-        float x[J];
+    float x[4][J], sum[4], top[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int row = rb * p.cls.R + i;
+        const uint16_t *q = p.q + b * p.qs[0] + (static_cast<int64_t>(h) * p.g + row) * p.qs[1] + lane;
+#pragma unroll
+        for (int j = 0; j < J; j++) x[i][j] = i < p.cls.R && row < p.g ? __half2float(__ushort_as_half(q[32 * j])) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < J; j++)
+        if ((p.sign_bits[j] >> lane) & 1u) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) x[i][j] = -x[i][j];
+        }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const bool up = (lane & o) != 0;
 #pragma unroll
         for (int j = 0; j < J; j++)
-            x[j] = row < p.g ? __half2float(__ushort_as_half(p.q[b * p.qs[0] + (static_cast<int64_t>(h) * p.g + row) * p.qs[1] + lane + 32 * j])) : 0.f;
-        if constexpr (ROTATE) {
 #pragma unroll
-            for (int j = 0; j < J; j++)
-                if ((p.sign_bits[j] >> lane) & 1u) x[j] = -x[j];
+            for (int i = 0; i < 4; i++) {
+                const float y = __shfl_xor_sync(0xffffffffu, x[i][j], o);
+                x[i][j] = up ? y - x[i][j] : x[i][j] + y;
+            }
+    }
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const bool up = (lane & o) != 0;
+    for (int o = 1; o < J; o <<= 1)
 #pragma unroll
-                for (int j = 0; j < J; j++) {
-                    const float y = __shfl_xor_sync(0xffffffffu, x[j], o);
-                    x[j] = up ? y - x[j] : x[j] + y;
+        for (int j = 0; j < J; j++)
+            if (!(j & o)) {
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float a = x[i][j], y = x[i][j + o];
+                    x[i][j] = a + y;
+                    x[i][j + o] = a - y;
                 }
             }
 #pragma unroll
-            for (int o = 1; o < J; o <<= 1)
+    for (int i = 0; i < 4; i++) sum[i] = top[i] = 0.f;
 #pragma unroll
-                for (int j = 0; j < J; j++)
-                    if (!(j & o)) {
-                        const float a = x[j], y = x[j + o];
-                        x[j] = a + y;
-                        x[j + o] = a - y;
-                    }
+    for (int j = 0; j < J; j++) {
+        const float f = ((p.sign_bits[j] >> lane) & 1u) ? -p.inv_sqrt_d : p.inv_sqrt_d;
 #pragma unroll
-            for (int j = 0; j < J; j++) x[j] *= ((p.sign_bits[j] >> lane) & 1u) ? -p.inv_sqrt_d : p.inv_sqrt_d;
+        for (int i = 0; i < 4; i++) {
+            x[i][j] *= f;
+            sum[i] += x[i][j];
+            top[i] = fmaxf(top[i], fabsf(x[i][j]));
         }
-        float sum = 0.f, top = 0.f;
+    }
 #pragma unroll
-        for (int j = 0; j < J; j++) {
-            sum += x[j];
-            top = fmaxf(top, fabsf(x[j]));
+    for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
         }
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) {
-            sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        }
-        // 2^e: rotated fp16 coordinates reach 2^21, the least is 2^-28; a row of zeros or of what is no number keeps e = 0
+    for (int i = 0; i < 4; i++) {
+        // (rotated fp16 coordinates reach 2^21, the least is 2^-28; a row of zeros or of what is no number: e = 0)
         int e = 0;
-        if (ROTATE && top > 0.f && top < 0x1p100f) e = static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 126;
+        if (top[i] > 0.f && top[i] < 0x1p100f) e = static_cast<int>(__float_as_uint(top[i]) >> 23) - 126;
         const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
         for (int j = 0; j < J; j++) {
-            const float y = x[j] * down;
+            const float y = x[i][j] * down;
             const __half hi = __float2half_rn(y);
-            q[(2 * i) * D + lane + 32 * j] = hi;
-            q[(2 * i + 1) * D + lane + 32 * j] = ROTATE ? __float2half_rn(y - __half2float(hi)) : __float2half_rn(0.f);
+            to[2 * i * D + lane + 32 * j] = hi;
+            to[(2 * i + 1) * D + lane + 32 * j] = __float2half_rn(y - __half2float(hi));
         }
-        if (lane == 0) {
-            sm.qsum[i] = sum;
-            sm.qexp[i] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        if (lane == i) {
+            qsum = sum[i];
+            qexp = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
         }
     }
 }
 
-// The joined record of the CTA's warps: row i, coordinates [0, D).  NP = 2: rows' even and odd tokens
-// (heads c and c + 2 of a warp, halves of 128 coordinates).  Warp tp nhb + hb has part tp of the rows of block hb.
-template <int D, int NP>
-__device__ __forceinline__ void write_record(const Small &sm, const float *copies, float *rec, int rows, int nhb) {
-    constexpr int HPW = 4 / NP;
-    const int parts = kWarps / nhb, dim = threadIdx.x % D;
-    for (int i = static_cast<int>(threadIdx.x % kThreads) / D; i < rows; i += kThreads / D) {
-        const int hb = i / HPW, c0 = i % HPW;
-        float M = kNegInf;
-        for (int tp = 0; tp < parts; tp++)
-#pragma unroll
-            for (int par = 0; par < NP; par++) M = fmaxf(M, sm.m[tp * nhb + hb][c0 + HPW * par]);
-        float L = 0.f, sum = 0.f;
-        if (M != kNegInf)
-            for (int tp = 0; tp < parts; tp++)
-#pragma unroll
-                for (int par = 0; par < NP; par++) {
-                    const int w = tp * nhb + hb, c = c0 + HPW * par;
-                    const float f = ex2(sm.m[w][c] - M);
-                    L = fmaf(sm.l[w][c], f, L);
-                    sum = fmaf(copies[(w * 4 + c) * kHeadStride + D * par + dim], f, sum);
-                }
-        float *to = rec + static_cast<size_t>(i) * (D + 4);
-        to[4 + dim] = sum;
-        if (dim == 0) to[0] = M, to[1] = L;
+// The pages of a segment, sequence and head, and the place of the next stage in them.
+struct Source {
+    const uint8_t *k, *v;
+    const char *s;                         // scales: keys' for the first half of the warp, values' for the second
+    uint32_t kblock, vblock, sblock;       // bytes a page (below 2^32: the host checks)
+    int page, n_pages, last;               // tokens a page; pages of the pool; the sequence's last page
+    int index, left;                       // page of the stage's first token, and tokens of it from there on
+    bool good;                             // that page is in the pool
+    const uint8_t *ka, *va;                // the lane's 16 bytes of the stage
+    const char *sa;
+    paged::Pages pages;
+    template <class F>
+    static __device__ __noinline__ Source open(const PagedParams &p, paged::Walk w, int lane) {
+        Source o;
+        const PagedSeg &g = p.seg[p.cls.seg[w.i]];
+        const SegView &x = g.seg;
+        const size_t sc = static_cast<size_t>(w.h) * x.capacity * 4, sb = static_cast<size_t>(p.list.H) * x.capacity * 4;
+        o.k = x.k + x.koff[w.h] + 16 * lane, o.v = x.v + x.voff[w.h] + 16 * lane;
+        o.s = reinterpret_cast<const char *>(lane < 16 ? x.ks : x.vs) + sc + 16 * (lane & 15);
+        if (g.table) {
+            o.kblock = static_cast<uint32_t>(x.kblock), o.vblock = static_cast<uint32_t>(x.vblock), o.sblock = static_cast<uint32_t>(sb);
+            o.n_pages = g.n_pages;
+        } else {  // (no pages: entry 0 of them)
+            o.k += w.b * x.kblock, o.v += w.b * x.vblock, o.s += w.b * sb;
+            o.kblock = o.vblock = o.sblock = 0;
+            o.n_pages = p.list.B;
+        }
+        o.page = g.page;
+        o.last = w.tokens > 0 ? paged::page_index(g, w.tokens - 1) : 0;
+        o.index = paged::page_index(g, w.st * F::PT);
+        o.pages.open(g, w.b, o.last, o.index, lane);
+        o.point<F>(w);
+        return o;
     }
+    // The addresses of page `page_` from its token `skip` on.
+    template <class F>
+    __device__ __forceinline__ void aim(uint32_t page_, uint32_t skip, const uint8_t *&ka_, const uint8_t *&va_, const char *&sa_) const {
+        ka_ = k + static_cast<uint64_t>(page_) * kblock + skip * F::kTokenK;
+        va_ = v + static_cast<uint64_t>(page_) * vblock + skip * F::kTokenV;
+        sa_ = s + static_cast<uint64_t>(page_) * sblock + skip * 4u;
+    }
+    // At page `index`, for the stage at w.
+    template <class F>
+    __device__ __forceinline__ void point(const paged::Walk &w) {
+        const int skip = w.st * F::PT - index * page;
+        const uint32_t at = static_cast<uint32_t>(pages.at(index));
+        left = page - skip;
+        good = at < static_cast<uint32_t>(n_pages);
+        aim<F>(at, static_cast<uint32_t>(skip), ka, va, sa);
+    }
+    // On to the next stage of the same.
+    template <class F>
+    __device__ __forceinline__ void step(const PagedParams &p, const paged::Walk &w, int lane) {
+        left -= F::PT;
+        ka += F::PT * F::kTokenK;
+        va += F::PT * F::kTokenV;
+        sa += F::PT * 4;
+        if (left > 0) return;
+        const PagedSeg &g = p.seg[p.cls.seg[w.i]];
+        index = paged::page_index(g, w.st * F::PT);
+        pages.move(g, w.b, last, index, lane);
+        point<F>(w);
+    }
+};
+
+// A warp's attention over its range, in the form F:
+//   D, R, MT                    dims, query rows, m-tiles of the sums
+//   PT, kSlot, kTable           tokens and bytes of a stage, bytes of the CTA's table
+//   kTokenK, kTokenV            bytes of a token's rows
+//   fill_all(...), fill(...)    a whole stage, a run of tokens of a page into the slot; clear(...): a slot that will not be full
+//   queries(...), stage(...)    a block's queries; the tiles of a stage
+//   fold(...), record(...)      the sums into the copy, the copy into the record
+// What a stage costs beside its tiles is kept short: addresses move by constants inside a page, and only stages that
+// begin a block or are not whole (special) have a description in shared memory.
+template <class F, int NS>
+__device__ __forceinline__ void attend(const PagedParams &p, F &f, int worker, int n_st, int b0, int rest, uint8_t *mine, float *copy, int lane) {
+    const PagedList &l = p.list;
+    const uint32_t sel = (lane & 4) ? 0x7632u : 0x5410u;
+    const uint64_t pol = policy_for(p.cls.n_rb == 1);
+    Stage *stages = reinterpret_cast<Stage *>(mine + NS * F::kSlot);
+    paged::Walk w = paged::seek(l, p.cls, b0, rest);
+    Source src = Source::open<F>(p, w, lane);
+    unsigned special = 0;                // bit i: the i-th last of the stages sent for
+    int to = 0;                          // slot of the next stage to fill
+    auto fill = [&](int j) {             // stage j, the one at `w`
+        const unsigned slot = smem_u32(mine + to * F::kSlot);
+        const int n = max(min(F::PT, w.tokens - w.st * F::PT), 0);
+        const bool whole = n == F::PT && src.left >= F::PT && src.good;
+        if (__builtin_expect(whole, 1)) {
+            F::fill_all(src, slot, pol, lane);
+        } else {
+            unsigned bad = 0;
+            F::clear(mine + to * F::kSlot, lane);
+            int skip = src.page - src.left;
+#pragma unroll 1
+            for (int from = 0, i = 0; from < n; i++) {
+                const int run = min(src.page - skip, n - from);
+                const uint32_t page = static_cast<uint32_t>(src.pages.at(src.index + i));
+                const uint8_t *ka, *va;
+                const char *sa;
+                src.aim<F>(page, static_cast<uint32_t>(skip), ka, va, sa);
+                if (page < static_cast<uint32_t>(src.n_pages)) F::fill(ka, va, sa, slot, from, run, pol, lane);
+                else bad |= 1u << i;
+                from += run;
+                skip = 0;
+            }
+            if (lane == 0) {
+                stages[to].bad = bad;
+                stages[to].page = src.page;
+                stages[to].skip = src.page - src.left;
+            }
+        }
+        if (w.fresh || !whole) {
+            special |= 1u;
+            if (lane == 0) {
+                stages[to].word = n | (w.fresh ? kFresh : 0) | (whole ? 0 : kPart);
+                stages[to].b = w.b;
+                stages[to].h_rb = w.h | (w.rb << 8);
+            }
+        }
+        if (++to == NS) to = 0;
+        w.fresh = false;
+        if (++w.st < w.n_st) {
+            src.step<F>(p, w, lane);
+        } else if (j + 1 < n_st) {
+            w = paged::next(l, p.cls, w);
+            src = Source::open<F>(p, w, lane);
+            if (w.fresh) {  // its queries into the cache
+                const int row = w.rb * p.cls.R + (lane >> 1);
+                if (lane < 2 * p.cls.R && row < p.g)
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(p.q + w.b * p.qs[0] + (static_cast<int64_t>(w.h) * p.g + row) * p.qs[1] + (lane & 1) * (F::D / 2)));
+            }
+        }
+    };
+    Run<F::MT> r;
+    auto fold = [&]() {
+        const float W = F::kLinear ? warp_sum_g(r.w) : 0.f;
+        const float scale = r.m_ref == r.m ? 1.f : ex2(r.m_ref - r.m);
+        f.fold(r, copy, W, scale, lane);
+        r.m_ref = r.m;
+        r.some = true;
+        r.clear();
+    };
+    int now_b = 0, now_h = 0, at = 0;
+    // one pass more than stages (k = n_st), so that a block ends in one place
+#pragma unroll 1
+    for (int k = 1 - NS; k <= n_st; k++) {  // (below 0: stages on their way first)
+        special <<= 1;
+        if (k + NS - 1 < n_st) fill(k + NS - 1);
+        cp_async_commit();
+        if (k < 0) continue;
+        cp_async_wait<NS - 1>();
+        __syncwarp();
+        int word = F::PT;
+        if (__builtin_expect(((special >> (NS - 1)) & 1u) || k == n_st, 0)) {
+            word = k < n_st ? stages[at].word : kFresh;
+            if (word & kFresh) {
+                if (k > 0) {
+                    fold();
+                    const float sum = warp_sum_g(r.l);
+                    __syncwarp();
+                    F::record(p.part + p.cls.part0 + paged::group_slot(l, p.cls, worker, now_b, now_h & 255, now_h >> 8) * F::R * (F::D + 4), copy,
+                              r.m, sum, lane);
+                    __syncwarp();
+                }
+                if (k == n_st) break;
+                now_b = stages[at].b;
+                now_h = stages[at].h_rb;
+                f.queries(p, reinterpret_cast<__half *>(copy), now_b, now_h & 255, now_h >> 8, lane);
+                __syncwarp();
+                r.start();
+            }
+        }
+        const uint8_t *buf = mine + at * F::kSlot;
+        if (!(word & kPart)) f.stage(r, buf, F::PT, stages[at], sel, lane, std::true_type{});
+        else f.stage(r, buf, word & (kFresh - 1), stages[at], sel, lane, std::false_type{});
+        __syncwarp();
+        if (++at == NS) at = 0;
+        if (__builtin_expect(r.tiles >= kFold, 0)) fold();
+    }
+}
+
+// Whether token `tok` of a stage is there.
+__device__ __forceinline__ bool have_token(const Stage &sg, int tok, int n) {
+    return tok < n && !(sg.bad && ((sg.bad >> ((sg.skip + tok) / sg.page)) & 1u));
+}
+
+template <class F>
+struct Ring {
+    static constexpr int slot = F::kSlot + static_cast<int>(sizeof(Stage));
+    static constexpr int fit = ((kSmemMax - 256 - F::kTable) / kWarps - copy_bytes(F::D)) / slot;
+    static constexpr int NS = fit > kMaxRing ? kMaxRing : fit;
+    static constexpr int warp_bytes = NS * slot + copy_bytes(F::D);
+    static constexpr int smem = F::kTable + kWarps * warp_bytes;
+    static_assert(NS >= 2, "a stage on its way beside the one at work");
+};
+
+template <class F, int NS>
+__global__ void __launch_bounds__(kPagedThreads, 1) paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ Levels lv) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int bufs[kWarps + 2 * kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int worker = warp * gridDim.x + blockIdx.x;  // (few stages go to as many SMs)
+    const paged::Share<kPagedThreads> share(p.list, p.cls);
+    pdl_launch_dependents();
+    F::fill_table(smem, lv);
+    const int total = paged::ranges_of<kPagedThreads, kWarps>(p.list, p.cls, share, blockIdx.x, gridDim.x, p.first, bufs);  // (synchronises)
+    int begin, end;
+    paged::worker_range(p.cls, total, worker, begin, end);
+    if (begin < end) {
+        uint8_t *mine = smem + F::kTable + warp * Ring<F>::warp_bytes;
+        F f(smem, lv, lane);
+        attend<F, NS>(p, f, worker, end - begin, bufs[kWarps + 2 * warp], bufs[kWarps + 2 * warp + 1], mine,
+                      reinterpret_cast<float *>(mine + NS * Ring<F>::slot), lane);
+    }
+    pdl_wait();  // the call's last launch ends behind its first
+}
+
+template <class F>
+cudaError_t launch(const PagedParams &p, const Levels &lv, cudaStream_t s) {
+    const cudaError_t e = cudaFuncSetAttribute(paged_kernel<F, Ring<F>::NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<F>::smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min(p.cls.workers, current_sm_count())));
+    cfg.blockDim = dim3(kPagedThreads);
+    cfg.dynamicSmemBytes = Ring<F>::smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.first_class ? 0 : 1;
+    return cudaLaunchKernelEx(&cfg, paged_kernel<F, Ring<F>::NS>, p, lv);
 }
 
 // ------------------------------------------------------------------- packed
-constexpr int kTeams = 3;
-constexpr int kTeamThreads = 512;       // three teams of four warps, and a warp that loads for each
-constexpr int kSmemMax = 232448 - 1024;
-constexpr int kBufBytes = 128;           // of ranges_of
-static_assert(kBufBytes >= 4 * (kTeamThreads / 32 + 2 * kTeams), "ranges");
-
-template <int KB, int VB, int NP>
-struct Geom {
-    static constexpr int ROWS = 128, PT = ROWS * NP;             // rows and tokens of a stage
-    static constexpr int RK = 16 * KB, RV = 16 * VB;             // bytes of a row
-    static constexpr int offV = ROWS * RK, offKS = offV + ROWS * RV, offVS = offKS + PT * 4, stage = offVS + PT * 4;
-    static constexpr int entries = VB >= 2 && VB <= 4 ? 1 << (2 * VB) : 0;
-    static constexpr int TS = 7;                                 // a column of the pair table a lane
-    static constexpr int table = entries * 128 + (VB >= 5 ? 512 : 0);
-    static constexpr int team = kCopyBytes + static_cast<int>(sizeof(Small));
-    static constexpr int fit(int teams) { return (kSmemMax - table - kBufBytes - teams * team) / (teams * stage); }
-    static constexpr int TEAMS = fit(kTeams) >= 2 ? kTeams : kTeams - 1;  // (the widest at head_dim 64: two)
-    static constexpr int NS = fit(TEAMS) > 6 ? 6 : fit(TEAMS);
-    static constexpr int smem = table + kBufBytes + TEAMS * (team + NS * stage);
-    static_assert(NS >= 2 && NS <= 8, "stages");
-};
-
 // 4-bit values: pair table of 256 entries; E/O fields of 8 bits: dims (2mt, 2mt+1)
 struct Pairs4 {
     static constexpr bool kLinear = false;
     static constexpr __host__ __device__ int dim(int mt, int r) { return 2 * mt + r; }
+    // address of the entry of field K: 128 bytes an entry, the byte's product and the sum in one instruction
     template <int K>
-    static __device__ __forceinline__ uint32_t at(uint32_t F) { return pair_off<8 * K, 8, 7>(F); }
+    static __device__ __forceinline__ uint32_t at(uint32_t F, uint32_t tab) { return __dp4a(F, 128u << (8 * K), tab); }
     static __device__ __forceinline__ void pair(const uint8_t *p, int RV, const VCtx &cx, uint32_t (&ra)[8], uint32_t (&rb)[8]) {
         const uint2 x = *reinterpret_cast<const uint2 *>(p + cx.off), y = *reinterpret_cast<const uint2 *>(p + cx.off + RV);
         constexpr uint32_t M = 0x0F0F0F0Fu;
@@ -287,330 +475,195 @@ struct Pairs4 {
         for (int i = 0; i < 2; i++) {
             const uint32_t wx = i ? x.y : x.x, wy = i ? y.y : y.x;
             const uint32_t E = (wx & M) | ((wy << 4) & ~M), O = ((wx >> 4) & M) | (wy & ~M);
-            ra[4 * i] = lds32(cx.tab + at<0>(E));
-            ra[4 * i + 1] = lds32(cx.tab + at<1>(E));
-            ra[4 * i + 2] = lds32(cx.tab + at<2>(E));
-            ra[4 * i + 3] = lds32(cx.tab + at<3>(E));
-            rb[4 * i] = lds32(cx.tab + at<0>(O));
-            rb[4 * i + 1] = lds32(cx.tab + at<1>(O));
-            rb[4 * i + 2] = lds32(cx.tab + at<2>(O));
-            rb[4 * i + 3] = lds32(cx.tab + at<3>(O));
+            ra[4 * i] = lds32(at<0>(E, cx.tab));
+            ra[4 * i + 1] = lds32(at<1>(E, cx.tab));
+            ra[4 * i + 2] = lds32(at<2>(E, cx.tab));
+            ra[4 * i + 3] = lds32(at<3>(E, cx.tab));
+            rb[4 * i] = lds32(at<0>(O, cx.tab));
+            rb[4 * i + 1] = lds32(at<1>(O, cx.tab));
+            rb[4 * i + 2] = lds32(at<2>(O, cx.tab));
+            rb[4 * i + 3] = lds32(at<3>(O, cx.tab));
         }
     }
 };
 
 template <int KB, int VB, int NP>
-__global__ void __launch_bounds__(kTeamThreads, 1)
-    paged_packed_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ Levels lv, const int nhb) {
-    using G = Geom<KB, VB, NP>;
+struct Packed {
+    static constexpr int D = 128 / NP, R = 4 / NP, MT = 8;
+    static constexpr int ROWS = 32, PT = ROWS * NP;              // rows and tokens of a stage
+    static constexpr int RK = 16 * KB, RV = 16 * VB;             // bytes of a row
+    static constexpr int kKs = ROWS * (RK + RV), kVs = kKs + PT * 4, kSlot = kVs + PT * 4;
+    static constexpr int entries = VB >= 2 && VB <= 4 ? 1 << (2 * VB) : 0;
+    static constexpr int kTable = entries * 128 + (VB >= 5 ? 512 : 0);  // pair table: a column a lane
     using KU = KUnpack<KB>;
-    using VD = typename std::conditional<VB == 4, Pairs4, VDec<VB, G::TS>>::type;
-    constexpr int NS = G::NS, D = 128 / NP, HPW = 4 / NP;
-    extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t *tab = smem;
-    int *bufs = reinterpret_cast<int *>(smem + G::table);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool loads = warp >= kTeams * kWarps;                  // a team's loader
-    const int team = loads ? warp - kTeams * kWarps : warp / kWarps;  // (from TEAMS on: no work)
-    uint8_t *mine = smem + G::table + kBufBytes + team * (G::team + NS * G::stage);
-    float *copies = reinterpret_cast<float *>(mine + NS * G::stage);
-    Small &sm = *reinterpret_cast<Small *>(mine + NS * G::stage + kCopyBytes);
-    const int worker = team * gridDim.x + blockIdx.x;
-    const PagedList &l = p.list;
-    pdl_launch_dependents();
-    if (loads && lane == 0 && team < G::TEAMS) {
-#pragma unroll
-        for (int i = 0; i < NS; i++) {
-            mbar_init(&sm.full[i], 1);
-            mbar_init(&sm.empty[i], kWarps);
-        }
-        mbar_init(&sm.sync, kWarps);
-        mbar_init(&sm.head, 1);
-        mbar_init_fence();
-        sm.dead = 0;
-        if (worker < p.cls.workers) p.state[worker] = 0;
+    using VD = typename std::conditional<VB == 4, Pairs4, VDec<VB, 7>>::type;
+    static constexpr bool kLinear = VD::kLinear;
+
+    VCtx vx;
+    int koff;
+    float inv, c1;
+    uint32_t bq[16];
+    float aq, bqs;
+
+    static __device__ __forceinline__ void fill_table(uint8_t *tab, const Levels &lv) {
+        if constexpr (VB >= 5)
+            for (int i = threadIdx.x; i < (1 << VB); i += kPagedThreads) reinterpret_cast<unsigned short *>(tab)[i] = lv.half[i];
+        if constexpr (entries > 0)
+            for (int i = threadIdx.x; i < entries * 32; i += kPagedThreads) {
+                const int e = i / 32;
+                reinterpret_cast<uint32_t *>(tab)[i] = static_cast<uint32_t>(lv.half[e & ((1 << VB) - 1)]) |
+                                                       (static_cast<uint32_t>(lv.half[e >> VB]) << 16);
+            }
     }
-    // ---- value tables
-    if constexpr (VB >= 5)
-        for (int i = threadIdx.x; i < (1 << VB); i += kTeamThreads) reinterpret_cast<unsigned short *>(tab)[i] = lv.half[i];
-    if constexpr (G::entries > 0)
-        for (int i = threadIdx.x; i < G::entries * 32; i += kTeamThreads) {
-            const int e = i / 32;
-            reinterpret_cast<uint32_t *>(tab)[i] = static_cast<uint32_t>(lv.half[e & ((1 << VB) - 1)]) |
-                                                   (static_cast<uint32_t>(lv.half[e >> VB]) << 16);
-        }
-    const int total = paged::ranges_of<kTeamThreads, kTeams>(l, p.cls, blockIdx.x, gridDim.x, p.first, bufs);  // (synchronises)
-    int begin, end;
-    paged::worker_range(p.cls, total, worker, begin, end);
-    const int n_st = team < G::TEAMS ? end - begin : 0;
-    if (loads) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (n_st > 0) {
-            paged::Walk w = paged::seek(l, p.cls, bufs[kTeamThreads / 32 + 2 * team], bufs[kTeamThreads / 32 + 2 * team + 1]);
-            if (lane == 0) {
-                sm.stage[0].b = w.b;
-                sm.stage[0].h_rb = w.h | (w.rb << 8);
-                arrive(&sm.head);
-            }
-            const uint64_t pol = policy_evict_first();
-            int pid = -1, n = 0, skipped = 0, runs = 0;
-            auto look = [&]() {  // the stage at `w`: n tokens on `runs` pages, the first page's tokens before it, the lane's page
-                const PagedSeg &s = p.seg[p.cls.seg[w.i]];
-                const int t0 = w.st * G::PT, page = paged::page_index(s, t0);
-                n = max(min(G::PT, w.tokens - t0), 0);
-                skipped = t0 - page * s.page;
-                runs = n > 0 ? paged::page_index(s, t0 + n - 1) - page + 1 : 0;
-                pid = lane < runs ? paged::page_at(s, w.b, page + lane) : -1;
-            };
-            look();
-            int at = 0, round = 0, issued = -1;
-            bool fresh = true;
-            for (int j = 0; j < n_st; j++) {
-                if (round > 0 && !wait(&sm.empty[at], (round - 1) & 1, p.wait_polls, &sm.dead)) break;
-                const PagedSeg &s = p.seg[p.cls.seg[w.i]];
-                const SegView &v = s.seg;
-                uint8_t *dst = mine + at * G::stage;
-                uint64_t *bar = &sm.full[at];
-                const bool some = lane < runs;
-                const int from = lane == 0 || !some ? 0 : lane * s.page - skipped;  // the run's first token in the stage
-                const int in_page = lane == 0 ? skipped : 0;
-                const int run = some ? min(s.page - in_page, n - from) : 0;
-                const bool bad = some && pid < 0;
-                // (runs start at multiples of 16 tokens; an odd end rounds up inside the page)
-                const unsigned nk = some && !bad ? (run * (G::RK / NP) + 15) & ~15u : 0u;
-                const unsigned nv = (run * (G::RV / NP) + 15) & ~15u, ns = (run * 4 + 15) & ~15u;
-                const unsigned bytes = __reduce_add_sync(0xffffffffu, nk ? nk + nv + 2 * ns : 0u);
-                const unsigned bads = __ballot_sync(0xffffffffu, bad);
-                if (lane == 0) {
-                    sm.stage[at] = {n | (fresh ? kFresh : 0) | (bads ? kBad : 0), w.b, w.h | (w.rb << 8), bads, s.page, skipped};
-                    fence_proxy_async();
-                    mbar_expect_tx(bar, bytes);
-                }
-                issued = j;
-                __syncwarp();
-                if (nk) {
-                    const size_t sc = (static_cast<size_t>(pid) * l.H + w.h) * v.capacity + in_page;
-                    fence_proxy_async();
-                    bulk_g2s_hint(dst + from * (G::RK / NP), v.k + pid * v.kblock + v.koff[w.h] + static_cast<size_t>(in_page) * (G::RK / NP), nk, bar, pol);
-                    bulk_g2s_hint(dst + G::offV + from * (G::RV / NP), v.v + pid * v.vblock + v.voff[w.h] + static_cast<size_t>(in_page) * (G::RV / NP), nv, bar, pol);
-                    bulk_g2s_hint(dst + G::offKS + from * 4, v.ks + sc, ns, bar, pol);
-                    bulk_g2s_hint(dst + G::offVS + from * 4, v.vs + sc, ns, bar, pol);
-                }
-                if (j + 1 < n_st) {
-                    fresh = paged::next(l, p.cls, w);
-                    look();
-                }
-                if (++at == NS) at = 0, ++round;
-            }
-            if (issued + 1 < n_st && lane == 0) {
-                *const_cast<volatile int *>(&sm.dead) = 1;
-                p.state[worker] = 1;
-            }
-            // no copy outlives its warp: the last fill of each buffer
-            for (int j = max(issued - NS + 1, 0); j <= issued; j++) mbar_wait(&sm.full[j % NS], (j / NS) & 1);
-        }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-        const int tw = warp % kWarps, g = lane >> 2, c = lane & 3;
-        VCtx vx;
+    __device__ __forceinline__ Packed(const uint8_t *tab, const Levels &lv, int lane) : inv(lv.inv), c1(lv.c1) {
+        const int g = lane >> 2, c = lane & 3;
         vx.ctab = reinterpret_cast<const unsigned short *>(tab);
         vx.tab = smem_u32(tab) + 4 * lane;
         if constexpr (VB == 1) {
-            vx.off = 2 * c * G::RV + 4 * (g >> 1);
+            vx.off = 2 * c * RV + 4 * (g >> 1);
             vx.sh = (g & 1) ? 0x7632 : 0x5410;
         } else if constexpr (VB == 3) {
-            vx.off = 2 * c * G::RV + 4 * ((3 * g) >> 1);
+            vx.off = 2 * c * RV + 4 * ((3 * g) >> 1);
             vx.sh = (g & 1) * 16;
+        } else if constexpr (VB == 4) {
+            vx.off = 2 * c * RV + 16 * ((g >> 1) ^ c) + 8 * (g & 1);
         } else {
-            vx.off = 2 * c * G::RV + ((2 * VB * g) & ~3);
+            vx.off = 2 * c * RV + ((2 * VB * g) & ~3);
             vx.sh = ((2 * VB * g) & 3) * 8;
         }
-        const int hb = tw % nhb, tp = tw / nhb, parts = kWarps / nhb;
-        const uint32_t sel = (g & 1) ? 0x7632u : 0x5410u;
+        koff = g * RK + 4 * KB * c;
+    }
+    static constexpr uint32_t kTokenK = RK / NP, kTokenV = RV / NP;
+    static __device__ __forceinline__ void clear(uint8_t *, int) {}
+    // 16-byte chunk i of a value row of 4 bits lies at i ^ (row / 2 & 3): the four row pairs that a load takes at once share
+    // two bank groups instead of one (the keys' rows, and the others', meet in fewer).
+    static __device__ __forceinline__ unsigned value_chunk(int lane) { return VB == 4 ? 16 * (lane ^ ((lane >> 3) & 3)) : 16 * lane; }
+    static __device__ __forceinline__ void fill_all(const Source &s, unsigned slot, uint64_t pol, int lane) {
+        const unsigned dk = slot + 16 * lane, dv = slot + ROWS * RK + value_chunk(lane);
+#pragma unroll
+        for (int i = 0; i < KB; i++) copy16(dk + 512 * i, s.ka + 512 * i, pol);
+#pragma unroll
+        for (int i = 0; i < VB; i++) copy16(dv + 512 * i, s.va + 512 * i, pol);
+        if ((lane & 15) < PT / 4) copy16(slot + (lane >= 16 ? kVs : kKs) + 16 * (lane & 15), s.sa, pol);
+    }
+    // (runs start at multiples of 16 tokens, eight rows at least; an odd end rounds up inside the page)
+    static __device__ __forceinline__ void fill(const uint8_t *k, const uint8_t *v, const char *sc, unsigned slot, int from, int run,
+                                                uint64_t pol, int lane) {
+        const unsigned dk = slot + from * kTokenK + 16 * lane, dv = slot + ROWS * RK + from * kTokenV + value_chunk(lane);
+        const int nk = run * static_cast<int>(kTokenK) - 16 * lane, nv = run * static_cast<int>(kTokenV) - 16 * lane;
+#pragma unroll 1
+        for (int o = 0; o < nk; o += 512) copy16(dk + o, k + o, pol);
+#pragma unroll 1
+        for (int o = 0; o < nv; o += 512) copy16(dv + o, v + o, pol);
+        if (4 * (lane & 15) < run) copy16(slot + (lane >= 16 ? kVs : kKs) + from * 4 + 16 * (lane & 15), sc, pol);
+    }
+    __device__ __forceinline__ void queries(const PagedParams &p, __half *q, int b, int h, int rb, int lane) {
         constexpr float alpha = static_cast<float>(1 << (24 - KU::kA)) * 2.0f / static_cast<float>(1 << KB);
         constexpr float beta = 1.0f / static_cast<float>(1 << KB) - 1.0f;
-        const int koff = g * G::RK + 4 * KB * c;
-        uint32_t bq[16];
-        float aq = 0.f, bqs = 0.f;
-        Run<8> r;
-        unsigned phase = 0;
-        int now_b = 0, now_h = 0;
-        bool ok = true;
-
-        auto tile_pair = [&](const uint8_t *buf, int tA, int tokens, const Stage &sg, auto full_tag) {
-            constexpr bool FULL = decltype(full_tag)::value;
-            const float *kss = reinterpret_cast<const float *>(buf + G::offKS), *vss = reinterpret_cast<const float *>(buf + G::offVS);
-            float s[4], v[4];
-            bool have[4];
+        float qsum = 0.f, qexp = 0.f;
+        rotate_queries<D>(p, q, b, h, rb, lane, qsum, qexp);
+        __syncwarp();
+        const int g = lane >> 2, c = lane & 3, v = g >> 1, part = g & 1;
+        const int own = NP == 2 ? c & 1 : c;
+        aq = alpha * __shfl_sync(0xffffffffu, qexp, own) * p.qk_scale;
+        bqs = beta * __shfl_sync(0xffffffffu, qsum, own) * p.qk_scale;
+        uint32_t x[16];
+        const uint4 *from = reinterpret_cast<const uint4 *>(q + (2 * (NP == 2 ? v & 1 : v) + part) * D + 32 * (NP == 2 ? c & 1 : c));
+        const bool zero = NP == 2 && (v >> 1) != (c >> 1);
 #pragma unroll
-            for (int t = 0; t < 2; t++) {
-                const int t0r = tA + 16 * t;
-                float raw0, raw1;
-                qk_raw<KU, KB, false>(buf + t0r * G::RK + koff, buf + (t0r + 8) * G::RK + koff, bq, raw0, raw1);
+        for (int i = 0; i < 4; i++) {
+            const uint4 y = from[i];
+            x[4 * i] = zero ? 0u : y.x, x[4 * i + 1] = zero ? 0u : y.y, x[4 * i + 2] = zero ? 0u : y.z, x[4 * i + 3] = zero ? 0u : y.w;
+        }
+        gather_b<KU>(x, bq);
+    }
+    template <bool FULL>
+    __device__ __forceinline__ void stage(Run<MT> &r, const uint8_t *buf, int n, const Stage &sg, uint32_t sel, int lane,
+                                          std::integral_constant<bool, FULL>) {
+        const int g = lane >> 2, c = lane & 3;
+        const float *kss = reinterpret_cast<const float *>(buf + kKs), *vss = reinterpret_cast<const float *>(buf + kVs);
+        float s[4], v[4];
+        bool have[4];
 #pragma unroll
-                for (int k2 = 0; k2 < 2; k2++) {
-                    const int tok = NP * (t0r + g + 8 * k2) + (NP == 2 ? c >> 1 : 0), i = 2 * t + k2;
-                    s[i] = kss[tok] * fmaf(aq, k2 ? raw1 : raw0, bqs);
-                    v[i] = vss[tok];
-                    have[i] = true;
-                    if constexpr (!FULL) {
-                        have[i] = tok < tokens;
-                        if (sg.bad) have[i] = have[i] && !((sg.bad >> ((sg.skip + tok) / sg.page)) & 1u);
-                    }
-                }
+        for (int t = 0; t < 2; t++) {
+            float raw0, raw1;
+            qk_raw<KU, KB, false>(buf + 16 * t * RK + koff, buf + (16 * t + 8) * RK + koff, bq, raw0, raw1);
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                const int tok = NP * (16 * t + g + 8 * k) + (NP == 2 ? c >> 1 : 0), i = 2 * t + k;
+                s[i] = kss[tok] * fmaf(aq, k ? raw1 : raw0, bqs);
+                v[i] = vss[tok];
+                have[i] = FULL || have_token(sg, tok, n);
             }
-            uint32_t bp[4];
-            softmax<FULL, 2>(r, s, have, v, g, c, sel, bp);
-            const uint8_t *vst = buf + G::offV;
+        }
+        uint32_t bp[4];
+        softmax<FULL, 2>(r, s, have, v, g, c, sel, bp);
+        const uint8_t *vst = buf + ROWS * RK;
 #pragma unroll
-            for (int t = 0; t < 2; t++) {
-                const uint8_t *vrow = vst + (tA + 16 * t) * G::RV;
-                uint32_t ra[8], rb[8], rc[8], rd[8];
-                VD::pair(vrow, G::RV, vx, ra, rb);
-                VD::pair(vrow + 8 * G::RV, G::RV, vx, rc, rd);
-#pragma unroll
-                for (int mt = 0; mt < 8; mt++)
-                    mma16816(r.acc[mt], ra[mt], rb[mt], rc[mt], rd[mt], bp[2 * t], bp[2 * t + 1]);
-            }
-            r.tiles += 2;
-        };
-        // the accumulators into the warp's copy: head c, coordinates 16 g ..
-        auto fold = [&]() {
-            float *to = copies + (tw * 4 + c) * kHeadStride + 16 * g;
-            float W = 0.f;
-            if constexpr (VD::kLinear) W = warp_sum_g(r.w);
-            float x[16];
+        for (int t = 0; t < 2; t++) {
+            const uint8_t *vrow = vst + 16 * t * RV;
+            uint32_t ra[8], rb[8], rc[8], rd[8];
+            VD::pair(vrow, RV, vx, ra, rb);
+            VD::pair(vrow + 8 * RV, RV, vx, rc, rd);
 #pragma unroll
             for (int mt = 0; mt < 8; mt++)
+                mma16816(r.acc[mt], ra[mt], rb[mt], rc[mt], rd[mt], bp[2 * t], bp[2 * t + 1]);
+        }
+        r.tiles += 2;
+    }
+    // head c's coordinates 16 g .. of the copy; NP = 2: (head, parity) c's, the lanes of its half
+    __device__ __forceinline__ void fold(const Run<MT> &r, float *copy, float W, float scale, int lane) const {
+        const int g = lane >> 2, c = lane & 3;
+        if (NP == 2 && (g >> 2) != (c >> 1)) return;
+        copy += c * copy_stride(D) + 16 * (NP == 2 ? g & 3 : g);
+        float x[16];
 #pragma unroll
-                for (int k2 = 0; k2 < 2; k2++) {
-                    const float a = r.sum(mt, k2);
-                    if constexpr (VD::kLinear) x[VD::dim(mt, k2)] = lv.c1 * (2.0f * a * VDec<1, 7>::unscale(mt, k2) - W);
-                    else x[VD::dim(mt, k2)] = a * lv.inv;
-                }
-            const float f = r.m_ref == r.m ? 1.f : ex2(r.m_ref - r.m);
+        for (int mt = 0; mt < 8; mt++)
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                float4 y = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                float4 *at = reinterpret_cast<float4 *>(to) + i;
-                if (r.some) {
-                    const float4 z = *at;
-                    y.x = fmaf(z.x, f, y.x), y.y = fmaf(z.y, f, y.y), y.z = fmaf(z.z, f, y.z), y.w = fmaf(z.w, f, y.w);
-                }
-                *at = y;
+            for (int k = 0; k < 2; k++) {
+                const float a = r.sum(mt, k);
+                if constexpr (kLinear) x[VD::dim(mt, k)] = c1 * (2.0f * a * VDec<1, 7>::unscale(mt, k) - W);
+                else x[VD::dim(mt, k)] = a * inv;
             }
-            r.m_ref = r.m;
-            r.some = true;
-            r.clear();
-        };
-        auto flush = [&]() {
-            fold();
-            const float sum = warp_sum_g(r.l);
-            if (g == 0) sm.m[tw][c] = r.m, sm.l[tw][c] = sum;
-            if (!meet(sm, phase, p.wait_polls, lane)) return false;
-            write_record<D, NP>(sm, copies, p.part + paged::group_slot(l, p.cls, worker, now_b, now_h & 255, now_h >> 8) * l.R * (D + 4), l.R, nhb);
-            return meet(sm, phase, p.wait_polls, lane);
-        };
-        auto start = [&]() {
-            __half *q = reinterpret_cast<__half *>(copies);
-            stage_queries<D, true>(p, sm, q, now_b, now_h & 255, now_h >> 8, l.R, tw, lane);
-            if (!meet(sm, phase, p.wait_polls, lane)) return false;
-            const int v = g >> 1, part = g & 1;
-            const int head = hb * HPW + (NP == 2 ? v & 1 : v);
-            uint32_t x[16];
-            if (NP == 2 && (v >> 1) != (c >> 1)) {
 #pragma unroll
-                for (int i = 0; i < 16; i++) x[i] = 0u;
+        for (int i = 0; i < 4; i++) {
+            float4 y = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            float4 *at = reinterpret_cast<float4 *>(copy) + i;
+            if (r.some) {
+                const float4 z = *at;
+                y.x = fmaf(z.x, scale, y.x), y.y = fmaf(z.y, scale, y.y), y.z = fmaf(z.z, scale, y.z), y.w = fmaf(z.w, scale, y.w);
+            }
+            *at = y;
+        }
+    }
+    // The record from the copy; m and l of head c in lane c.  NP = 2: head i's even and odd tokens are heads i and i + 2 of the
+    // copy.
+    static __device__ __forceinline__ void record(float *rec, const float *copy, float m, float l, int lane) {
+#pragma unroll
+        for (int i = 0; i < R; i++) {
+            float *to = rec + i * (D + 4);
+            const float m0 = __shfl_sync(0xffffffffu, m, i), l0 = __shfl_sync(0xffffffffu, l, i);
+            if constexpr (NP == 1) {
+                if (lane == 0) *reinterpret_cast<float2 *>(to) = make_float2(m0, l0);
+                *reinterpret_cast<float4 *>(to + 4 + 4 * lane) = *reinterpret_cast<const float4 *>(copy + i * copy_stride(D) + 4 * lane);
             } else {
-                const uint4 *from = reinterpret_cast<const uint4 *>(q + (2 * head + part) * D + 32 * (NP == 2 ? c & 1 : c));
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const uint4 y = from[i];
-                    x[4 * i] = y.x, x[4 * i + 1] = y.y, x[4 * i + 2] = y.z, x[4 * i + 3] = y.w;
-                }
-            }
-            gather_b<KU>(x, bq);
-            const int own = hb * HPW + (NP == 2 ? c & 1 : c);
-            aq = alpha * sm.qexp[own] * p.qk_scale;
-            bqs = beta * sm.qsum[own] * p.qk_scale;
-            r.start();
-            return meet(sm, phase, p.wait_polls, lane);
-        };
-
-        if (n_st > 0) {
-            ok = wait(&sm.head, 0, p.wait_polls, &sm.dead);
-            if (ok) {
-                now_b = sm.stage[0].b;
-                now_h = sm.stage[0].h_rb;
-                ok = start();  // (while the first stage is on its way)
-            }
-            int at = 0;
-            unsigned parity = 0;
-            for (int k = 0; k < n_st && ok; k++) {
-                if (!(ok = wait(&sm.full[at], parity, p.wait_polls, &sm.dead))) break;
-                const int word = sm.stage[at].word, n = word & (kFresh - 1);
-                if (__builtin_expect((word & kFresh) && k > 0, 0)) {
-                    if (!(ok = flush())) break;
-                    now_b = sm.stage[at].b;
-                    now_h = sm.stage[at].h_rb;
-                    if (!(ok = start())) break;
-                }
-                const uint8_t *buf = mine + at * G::stage;
-                for (int tA = tp * 32; NP * tA < n; tA += 32 * parts) {
-                    if (NP * (tA + 32) <= n && !(word & kBad)) tile_pair(buf, tA, n, sm.stage[at], std::true_type{});
-                    else tile_pair(buf, tA, n, sm.stage[at], std::false_type{});
-                }
-                __syncwarp();
-                if (lane == 0) arrive(&sm.empty[at]);
-                if (++at == NS) at = 0, parity ^= 1u;
-                if (__builtin_expect(r.tiles >= kFold, 0)) fold();
-            }
-            if (ok) ok = flush();
-            if (!ok && lane == 0) {
-                *const_cast<volatile int *>(&sm.dead) = 1;
-                p.state[worker] = 1;
+                const float m1 = __shfl_sync(0xffffffffu, m, i + 2), l1 = __shfl_sync(0xffffffffu, l, i + 2);
+                const float M = fmaxf(m0, m1), f0 = m0 == M ? 1.f : ex2(m0 - M), f1 = m1 == M ? 1.f : ex2(m1 - M);
+                if (lane == 0) *reinterpret_cast<float2 *>(to) = make_float2(M, l0 * f0 + l1 * f1);
+                const float2 x = *reinterpret_cast<const float2 *>(copy + i * copy_stride(D) + 2 * lane);
+                const float2 y = *reinterpret_cast<const float2 *>(copy + (i + 2) * copy_stride(D) + 2 * lane);
+                *reinterpret_cast<float2 *>(to + 4 + 2 * lane) = make_float2(x.x * f0 + y.x * f1, x.y * f0 + y.y * f1);
             }
         }
     }
-    pdl_wait();  // the call's last launch ends behind its first
-}
-
-// teams: workers of a CTA.
-inline cudaError_t launch(const void *kernel, size_t smem, int threads, int teams, const PagedParams &p, void **args, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    // workers t, t + grid, t + 2 grid ... are one CTA's: few stages go to as many SMs
-    const int ctas = std::max(1, p.cls.workers / teams);
-    cfg.gridDim = dim3(static_cast<unsigned>(p.cls.workers < current_sm_count() * teams ? std::min(p.cls.workers, current_sm_count()) : ctas));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.first_class ? 0 : 1;
-    return cudaLaunchKernelExC(&cfg, kernel, args);
-}
-
-// Blocks of heads among a CTA's warps.
-inline int head_blocks(int rows, int per_warp) { return rows <= per_warp ? 1 : rows <= 2 * per_warp ? 2 : 4; }
+};
 
 template <int KB, int VB, int NP>
 cudaError_t launch_packed(const PagedParams &p, cudaStream_t s) {
     Levels lv;
     value_levels(p.cls.law, VB, p.centroid + cb_off(VB), lv.half, &lv.inv);
     lv.c1 = p.centroid[cb_off(VB) + 1];
-    int nhb = head_blocks(p.list.R, 4 / NP);
-    void *args[] = {const_cast<PagedParams *>(&p), &lv, &nhb};
-    return launch(reinterpret_cast<const void *>(paged_packed_kernel<KB, VB, NP>), Geom<KB, VB, NP>::smem, kTeamThreads,
-                  Geom<KB, VB, NP>::TEAMS, p, args, s);
-}
-
-template <int KB, int VB, int NP>
-PagedShape shape_packed() {
-    return {Geom<KB, VB, NP>::PT, Geom<KB, VB, NP>::TEAMS};
+    return launch<Packed<KB, VB, NP>>(p, lv, s);
 }
 
 }  // namespace pmma
@@ -630,18 +683,6 @@ PagedShape shape_packed() {
             case 7: return pmma::launch_packed<KB, 7, NP>(p, s);                                  \
             case 8: return pmma::launch_packed<KB, 8, NP>(p, s);                                  \
             default: return cudaErrorInvalidValue;                                                \
-        }                                                                                         \
-    }                                                                                             \
-    PagedShape paged_shape_kb##KB##_np##NP(int vb) {                                              \
-        switch (vb) {                                                                             \
-            case 1: return pmma::shape_packed<KB, 1, NP>();                                       \
-            case 2: return pmma::shape_packed<KB, 2, NP>();                                       \
-            case 3: return pmma::shape_packed<KB, 3, NP>();                                       \
-            case 4: return pmma::shape_packed<KB, 4, NP>();                                       \
-            case 5: return pmma::shape_packed<KB, 5, NP>();                                       \
-            case 6: return pmma::shape_packed<KB, 6, NP>();                                       \
-            case 7: return pmma::shape_packed<KB, 7, NP>();                                       \
-            default: return pmma::shape_packed<KB, 8, NP>();                                      \
         }                                                                                         \
     }                                                                                             \
     }

@@ -260,16 +260,18 @@ struct PagedSeg {
 };
 struct PagedClass {
     int kb, vb, law;
+    int R, n_rb;                         // query heads a block, and blocks of a KV head
     int n;                               // segments with heads of the class
     uint8_t seg[TQ_MAX_SEGMENTS];
     uint16_t heads[TQ_MAX_SEGMENTS];     // bit h: head h of that segment
     int unit, workers;                   // U, W
-    int64_t slot0;                       // first record
+    int64_t part0;                       // first float of its records
 };
+constexpr int kPagedWarps = 12;          // workers an SM on the tensor cores
 constexpr int kPagedClasses = 1 + TQ_MAX_SEGMENTS * kMaxH;
 // What the list is made of: lengths without the segments' data.
 struct PagedList {
-    int B, H, R, n_rb;
+    int B, H;
     const int *len[TQ_MAX_SEGMENTS];
     int limit[TQ_MAX_SEGMENTS];
 };
@@ -280,11 +282,9 @@ struct PagedParams {
     PagedSeg seg[TQ_MAX_SEGMENTS];
     const uint16_t *q;
     int64_t qs[2];                       // strides of (b, head)
-    float *part;                         // records [slot][R][d + 4]: m (log2 units), l, pad, pad, sum
+    float *part;                         // records, of a class [slot][R][d + 4]: m (log2 units), l, pad, pad, sum
     int *first;                          // [B + 1]: stages of the class before a sequence
-    int *state;                          // [W]: not 0: the worker gave up a wait
     int first_class;                     // the call's first launch
-    int wait_polls;
     uint32_t sign_bits[kMaxD / 32];
     float inv_sqrt_d, qk_scale;
     float centroid[kCbTotal];            // of the class's law
@@ -295,19 +295,16 @@ struct PagedMergeParams {
     uint16_t *out;                       // [B][H g][d]
     const float *part;
     const int *first;                    // [class][B + 1]
-    const int *state;                    // [class][workers]
-    int64_t state0[kPagedClasses];
     int *error;
     PagedClass cls[kPagedClasses];
     uint32_t sign_bits[kMaxD / 32];
     float inv_sqrt_d;
 };
-// A class's stage length and the most workers that its kernel runs at once (of the class's kernel: on an SM).
+// A class's stage length, rows a block and workers at once.
 struct PagedShape {
-    int unit, workers;
+    int unit, rows, workers;
 };
-PagedShape paged_shape(int d, int kb, int vb);
-int paged_rows(int d, int g);            // R
+PagedShape paged_shape(int d, bool packed);
 cudaError_t launch_paged(const PagedParams &p, cudaStream_t s);
 cudaError_t launch_paged_merge(const PagedMergeParams &p, cudaStream_t s);
 
