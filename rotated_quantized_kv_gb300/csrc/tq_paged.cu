@@ -270,6 +270,166 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     }
 }
 
+// The merge at the head dims of the tensor-core forms: warps instead of a CTA for a row, W of them where the records
+// are many, a lane four (two) coordinates of every record, four records in flight.  Where they lie is worked out from
+// the lengths before the records are waited for (up to kScan sequences; behind that from the scan that the first CTA left).
+constexpr int kRowWarps = 8;
+constexpr int kScan = 256;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kRowWarps) paged_merge_rows_kernel(const __grid_constant__ PagedMergeParams p, const int W) {
+    constexpr int E = D / 32;
+    struct alignas(16) Part {
+        float x[2][D];
+        float m, l, pad[2];
+    };
+    __shared__ Part parts[kRowWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, share = warp % W;
+    const PagedList &l = p.list;
+    const int rows = l.B * l.H * p.g, row = blockIdx.x * (kRowWarps / W) + warp / W;
+    const int b = min(row, rows - 1) / (l.H * p.g), h = min(row, rows - 1) / p.g % l.H, j = min(row, rows - 1) % p.g;
+    // the first and the last worker of the row's group in class k
+    auto span = [&](int k, bool scan, int &w0, int &w1) {
+        const PagedClass &c = p.cls[k];
+        const int n = head_stages(l, c, b, h);
+        int before = 0, total = 0;
+        if (scan) {
+            for (int i = lane; i < l.B; i += 32) {
+                const int x = sequence_stages(l, c, i);
+                total += x;
+                if (i < b) before += x;
+            }
+            total = __reduce_add_sync(0xffffffffu, total);
+            before = __reduce_add_sync(0xffffffffu, before);
+        } else {
+            before = p.first[static_cast<size_t>(k) * (l.B + 1) + b];
+            total = p.first[static_cast<size_t>(k) * (l.B + 1) + l.B];
+        }
+        w0 = 0, w1 = -1;
+        if (n == 0) return;
+        int s = before + j / c.R * n;
+        if (c.n == 1) s += __popc(c.heads[0] & ((1u << h) - 1u)) * c.n_rb * n;
+        else
+            for (int i = 0; i < h; i++) s += c.n_rb * head_stages(l, c, b, i);
+        const int workers = workers_of(c, total);
+        w0 = max(worker_of(total, s, workers), 0);
+        w1 = min(worker_of(total, s + n - 1, workers), workers - 1);
+    };
+    const bool scan = l.B <= kScan;
+    int w0 = 0, w1 = -1;
+    if (scan && p.n_classes > 0) span(0, true, w0, w1);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.error = 0;
+    float M = -kInf, L = 0.f, x[2][E];
+#pragma unroll
+    for (int e = 0; e < E; e++) x[0][e] = x[1][e] = 0.f;
+    for (int k = 0; k < p.n_classes; k++) {
+        if (k > 0 || !scan) span(k, scan, w0, w1);
+        const PagedClass &c = p.cls[k];
+        const float *rec = p.part + c.part0 + (group_slot(l, c, 0, b, h, j / c.R) * c.R + j % c.R) * (D + 4);
+        const size_t step = static_cast<size_t>(c.R) * (D + 4);
+        float a[E];
+#pragma unroll
+        for (int e = 0; e < E; e++) a[e] = 0.f;
+        float was = M;  // the reference of a
+        for (int w = w0 + share; w <= w1; w += 4 * W) {
+            float2 ml[4];
+            float y[4][E];
+            float top = M;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const bool some = w + i * W <= w1;
+                const float *r = rec + (some ? w + i * W : w) * step;
+                ml[i] = *reinterpret_cast<const float2 *>(r);
+                if constexpr (E == 4) *reinterpret_cast<float4 *>(y[i]) = *reinterpret_cast<const float4 *>(r + 4 + 4 * lane);
+                else *reinterpret_cast<float2 *>(y[i]) = *reinterpret_cast<const float2 *>(r + 4 + 2 * lane);
+                if (!some) ml[i] = make_float2(-kInf, 0.f);
+                top = fmaxf(top, ml[i].x);
+            }
+            if (top == -kInf) continue;  // (records without a token)
+            const float f = ex2(M - top), fa = ex2(was - top);
+            L *= f;
+#pragma unroll
+            for (int e = 0; e < E; e++) a[e] *= fa;
+#pragma unroll
+            for (int s = 0; s < 2; s++)
+#pragma unroll
+                for (int e = 0; e < E; e++) x[s][e] *= f;
+            M = was = top;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                if (ml[i].x == -kInf) continue;
+                const float g = ex2(ml[i].x - M);
+                L = fmaf(ml[i].y, g, L);
+#pragma unroll
+                for (int e = 0; e < E; e++) a[e] = fmaf(y[i][e], g, a[e]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            if (c.kb) x[1][e] += a[e];
+            else x[0][e] += a[e];
+        }
+    }
+    if (W > 1) {
+        Part &mine = parts[warp];
+#pragma unroll
+        for (int e = 0; e < E; e++) mine.x[0][E * lane + e] = x[0][e], mine.x[1][E * lane + e] = x[1][e];
+        if (lane == 0) mine.m = M, mine.l = L;
+        __syncthreads();
+        if (share != 0) return;
+        float top = M;
+        for (int i = 1; i < W; i++) top = fmaxf(top, parts[warp + i].m);
+        const float f = M == top ? 1.f : ex2(M - top);
+        L *= f;
+#pragma unroll
+        for (int e = 0; e < E; e++) x[0][e] *= f, x[1][e] *= f;
+        for (int i = 1; i < W; i++) {
+            const Part &o = parts[warp + i];
+            if (o.m == -kInf) continue;
+            const float g = ex2(o.m - top);
+            L = fmaf(o.l, g, L);
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+                x[0][e] = fmaf(o.x[0][E * lane + e], g, x[0][e]);
+                x[1][e] = fmaf(o.x[1][E * lane + e], g, x[1][e]);
+            }
+        }
+    }
+    if (row >= rows) return;
+    // the rotated sum turns back: signs, butterflies in the lane and across lanes, signs
+    const uint32_t neg = p.sign_bits[E * lane >> 5] >> (E * lane & 31);
+#pragma unroll
+    for (int e = 0; e < E; e++)
+        if ((neg >> e) & 1u) x[1][e] = -x[1][e];
+#pragma unroll
+    for (int o = 1; o < E; o <<= 1)
+#pragma unroll
+        for (int e = 0; e < E; e++)
+            if (!(e & o)) {
+                const float u = x[1][e], v = x[1][e + o];
+                x[1][e] = u + v;
+                x[1][e + o] = u - v;
+            }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            const float v = __shfl_xor_sync(0xffffffffu, x[1][e], o);
+            x[1][e] = up ? v - x[1][e] : x[1][e] + v;
+        }
+    }
+    const float scale = L != 0.f ? 1.f / L : 0.f;  // (no token: zeros; a NaN stays one)
+    __align__(8) __half out[E];
+#pragma unroll
+    for (int e = 0; e < E; e++)
+        out[e] = __float2half_rn(fmaf(x[1][e], (neg >> e) & 1u ? -p.inv_sqrt_d : p.inv_sqrt_d, x[0][e]) * scale);
+    uint16_t *to = p.out + static_cast<size_t>(row) * D + E * lane;
+    if constexpr (E == 4) *reinterpret_cast<uint2 *>(to) = *reinterpret_cast<const uint2 *>(out);
+    else *reinterpret_cast<uint32_t *>(to) = *reinterpret_cast<const uint32_t *>(out);
+}
+
 template <int D>
 cudaError_t plain(const PagedParams &p, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(paged_plain_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -336,15 +496,28 @@ cudaError_t launch_paged(const PagedParams &p, cudaStream_t s) {
 
 cudaError_t launch_paged_merge(const PagedMergeParams &p, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.list.B) * p.list.H * p.g);
-    cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_merge_kernel, p);
+    const long long rows = static_cast<long long>(p.list.B) * p.list.H * p.g;
+    if (!on_tensor_cores(p.d)) {
+        cfg.gridDim = dim3(static_cast<unsigned>(rows));
+        cfg.blockDim = dim3(kMergeThreads);
+        return cudaLaunchKernelEx(&cfg, paged_merge_kernel, p);
+    }
+    // warps a row: the records that a long row has, eight a warp (two rounds of loads).  (Of all workers, not of those
+    // that the table's width leaves: a result does not depend on how wide the table is.)
+    long long records = 0;
+    for (int k = 0; k < p.n_classes; k++)
+        records += 1 + paged_shape(p.d, p.cls[k].kb > 0).workers / (static_cast<long long>(p.list.B) * __builtin_popcount(p.cls[k].heads[0]) * p.cls[k].n_rb);
+    int W = 1;
+    while (W < kRowWarps && 8 * W < records) W *= 2;
+    cfg.gridDim = dim3(static_cast<unsigned>((rows + kRowWarps / W - 1) / (kRowWarps / W)));
+    cfg.blockDim = dim3(32 * kRowWarps);
+    return p.d == 128 ? cudaLaunchKernelEx(&cfg, paged_merge_rows_kernel<128>, p, W) : cudaLaunchKernelEx(&cfg, paged_merge_rows_kernel<64>, p, W);
 }
 
 }  // namespace tqk
