@@ -312,26 +312,28 @@ __device__ __forceinline__ void attend(const PagedParams &p, F &f, int worker, i
     auto fill = [&](int j) {             // stage j, the one at `w`
         const unsigned slot = smem_u32(mine + to * F::kSlot);
         const int n = max(min(F::PT, w.tokens - w.st * F::PT), 0);
-        const bool whole = n == F::PT && src.left >= F::PT && src.good;
-        if (__builtin_expect(whole, 1)) {
+        bool whole = n == F::PT;
+        if (__builtin_expect(whole && src.left >= F::PT && src.good, 1)) {
             F::fill_all(src, slot, pol, lane);
-        } else {
-            unsigned bad = 0;
-            F::clear(mine + to * F::kSlot, lane);
+        } else {                         // its end, or several pages: page i to lane i
+            const uint32_t pages = static_cast<uint32_t>(src.pages.at(src.index + lane));
+            const bool used = lane == 0 ? n > 0 : src.left + (lane - 1) * min(src.page, F::PT) < n;
+            const unsigned bad = __ballot_sync(0xffffffffu, used && pages >= static_cast<uint32_t>(src.n_pages));
+            whole = whole && bad == 0;
+            if (!whole) F::clear(mine + to * F::kSlot, lane);
             int skip = src.page - src.left;
 #pragma unroll 1
             for (int from = 0, i = 0; from < n; i++) {
                 const int run = min(src.page - skip, n - from);
-                const uint32_t page = static_cast<uint32_t>(src.pages.at(src.index + i));
+                const uint32_t page = __shfl_sync(0xffffffffu, pages, i);
                 const uint8_t *ka, *va;
                 const char *sa;
                 src.aim<F>(page, static_cast<uint32_t>(skip), ka, va, sa);
-                if (page < static_cast<uint32_t>(src.n_pages)) F::fill(ka, va, sa, slot, from, run, pol, lane);
-                else bad |= 1u << i;
+                if (!((bad >> i) & 1u)) F::fill(ka, va, sa, slot, from, run, pol, lane);
                 from += run;
                 skip = 0;
             }
-            if (lane == 0) {
+            if (!whole && lane == 0) {
                 stages[to].bad = bad;
                 stages[to].page = src.page;
                 stages[to].skip = src.page - src.left;
