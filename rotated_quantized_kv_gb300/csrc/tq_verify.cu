@@ -70,17 +70,23 @@ struct Row {
     static __device__ __forceinline__ int own_skew(const T *p) {
         return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
     }
-    __device__ __forceinline__ void load(int i, float (&x)[VEC]) const {
+    // Vector i as it is; what is behind an end: zeros.
+    __device__ __forceinline__ uint4 load(int i) const {
         const int e = i * VEC - skew;
-        if (vec && e >= 0 && e + VEC <= V) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(at + e));
-            const T *v = reinterpret_cast<const T *>(&w);
+        if (vec && e >= 0 && e + VEC <= V) return __ldg(reinterpret_cast<const uint4 *>(at + e));
+        return ragged(at, e, V);
+    }
+    // (the code of a call runs once or twice: what is not on every vector's way is kept out of it)
+    static __device__ __noinline__ uint4 ragged(const T *at, int e, int V) {
+        union {
+            T x[VEC];
+            uint4 w;
+        } v;
+        v.w = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-            for (int k = 0; k < VEC; k++) x[k] = to_float(v[k]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < VEC; k++) x[k] = e + k >= 0 && e + k < V ? to_float(at[e + k]) : 0.f;
-        }
+        for (int k = 0; k < VEC; k++)
+            if (e + k >= 0 && e + k < V) v.x[k] = at[e + k];
+        return v.w;
     }
 };
 
@@ -98,9 +104,78 @@ struct Shared {
         int out[TQ_MAX_DRAFTS];
     };
     double total[2][kVerMaxCtas];    // a pass's sums of the CTAs, two passes in turn
-    double tile[kMaxTiles];
+    Level tile[kMaxTiles];
     int path[TQ_MAX_DRAFTS];
+    int want, node;                  // what warp 0 asks for: rejections at the node (-1: the walk is over), the node
 };
+
+// r behind `gone` rejections of a vector (element e on) from its p and q, and its sum.
+template <typename T>
+__device__ __forceinline__ void residual(const Shared &sh, bool draft, uint4 pv, uint4 qv, int e, int gone, float (&r)[Row<T>::VEC]) {
+    constexpr int VEC = Row<T>::VEC;
+    const T *p = reinterpret_cast<const T *>(&pv), *qq = reinterpret_cast<const T *>(&qv);
+#pragma unroll
+    for (int k = 0; k < VEC; k++) r[k] = weight(to_float(p[k]));
+    if (gone == 0) return;
+    if (draft) {
+        float q[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; k++) q[k] = weight(to_float(qq[k]));
+#pragma unroll 1
+        for (int j = 0; j < gone; j++) {
+            const Level s = sh.level[j];
+#pragma unroll
+            for (int k = 0; k < VEC; k++) r[k] = fmaxf(__fmaf_rn(-s.lo, q[k], __fmaf_rn(-s.hi, q[k], r[k])), 0.f);
+        }
+    } else {
+#pragma unroll 1
+        for (int j = 0; j < gone; j++) {
+            const int at = sh.out[j] - e;
+#pragma unroll
+            for (int k = 0; k < VEC; k++)
+                if (at == k) r[k] = 0.f;
+        }
+    }
+}
+template <typename T>
+__device__ __noinline__ Level vector_sum(const Shared &sh, bool draft, uint4 p, uint4 q, int e, int gone) {
+    float r[Row<T>::VEC];
+    residual<T>(sh, draft, p, q, e, gone, r);
+    Level s = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < Row<T>::VEC; k++) add_exact(s.hi, s.lo, r[k]);
+    return s;
+}
+
+// Sum over the warp (the same in every lane).
+__device__ __forceinline__ Level warp_sum(Level s) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        const float h = __shfl_xor_sync(0xffffffffu, s.hi, o), l = __shfl_xor_sync(0xffffffffu, s.lo, o);
+        add_exact(s.hi, s.lo, h);
+        s.lo = __fadd_rn(s.lo, l);
+    }
+    return s;
+}
+__device__ __forceinline__ double to_double(Level s) { return static_cast<double>(s.hi) + static_cast<double>(s.lo); }
+
+// The lane where `before` and the inclusive prefix of x pass the goal (found), else the last with x > 0 (none: -1), and the
+// sum before it; `before` moves on by all of x.
+__device__ __noinline__ int find_lane(double x, double goal, double &before, double &at_sum, bool &found) {
+    const int lane = threadIdx.x & 31;
+    double y = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
+    }
+    const unsigned some = __ballot_sync(0xffffffffu, x > 0.0), over = __ballot_sync(0xffffffffu, x > 0.0 && before + y > goal);
+    const int at = over ? __ffs(over) - 1 : 31 - __clz(some);
+    if (some) at_sum = before + __shfl_sync(0xffffffffu, y - x, at);
+    before += __shfl_sync(0xffffffffu, y, 31);
+    found = over != 0;
+    return at;
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_constant__ VerifyParams p) {
@@ -137,33 +212,7 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
     }
     cluster.sync();
 
-    // ---- passes: weights r of a node's row behind `gone` rejections
-    // r of a vector's elements from p and q
-    auto residual = [&](const Row<T> &P, const Row<T> &Q, int i, int gone, float (&r)[VEC]) {
-        P.load(i, r);
-#pragma unroll
-        for (int k = 0; k < VEC; k++) r[k] = weight(r[k]);
-        if (gone == 0) return;
-        if (draft) {
-            float q[VEC];
-            Q.load(i, q);
-#pragma unroll
-            for (int k = 0; k < VEC; k++) q[k] = weight(q[k]);
-            for (int j = 0; j < gone; j++) {
-                const Level s = sh.level[j];
-#pragma unroll
-                for (int k = 0; k < VEC; k++) r[k] = fmaxf(__fmaf_rn(-s.lo, q[k], __fmaf_rn(-s.hi, q[k], r[k])), 0.f);
-            }
-        } else {
-            const int e = i * VEC - P.skew;
-            for (int j = 0; j < gone; j++) {
-                const int at = sh.out[j] - e;
-#pragma unroll
-                for (int k = 0; k < VEC; k++)
-                    if (at == k) r[k] = 0.f;
-            }
-        }
-    };
+    // ---- passes: sums of the weights r of a node's row behind `gone` rejections
     int passes = 0;
     // vectors of this CTA's slice, and of a tile
     int v0 = 0, v1 = 0, per_tile = 32 * kUnroll;
@@ -179,28 +228,33 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
         while (static_cast<long long>(per_tile) * kMaxTiles < each) per_tile *= 2;
         fn(Row<T>(pr, V, skew), Row<T>(qr, V, skew));
     };
-    // sum of the weights (every thread of the cluster gets it); the CTA keeps its tiles' sums
+    // (warp 0 of every CTA gets the sum; the CTA keeps its tiles')
     auto pass = [&](int node, int gone) {
         rows(node, [&](const Row<T> &P, const Row<T> &Q) {
+#pragma unroll 1
             for (int t = warp; v0 + t * per_tile < v1; t += kVerWarps) {
-                const int from = v0 + t * per_tile, to = min(from + per_tile, v1);
-                double sum = 0.0;
-                for (int i0 = from; i0 < to; i0 += 32 * kUnroll) {
-                    float hi = 0.f, lo = 0.f;
-#pragma unroll
-                    for (int u = 0; u < kUnroll; u++) {
-                        const int i = i0 + 32 * u + lane;
-                        if (i < to) {
-                            float r[VEC];
-                            residual(P, Q, i, gone, r);
-#pragma unroll
-                            for (int k = 0; k < VEC; k++) add_exact(hi, lo, r[k]);
-                        }
+                const int to = min(v0 + (t + 1) * per_tile, v1);
+                uint4 pv[3], qv[3];  // the vector at work and the two behind it
+                auto fetch = [&](int i, uint4 &x, uint4 &y) {
+                    x = y = make_uint4(0u, 0u, 0u, 0u);
+                    if (i < to) {
+                        x = P.load(i);
+                        if (draft && gone) y = Q.load(i);
                     }
-                    sum += static_cast<double>(hi) + static_cast<double>(lo);
+                };
+                int i = v0 + t * per_tile + lane;
+                fetch(i, pv[0], qv[0]);
+                fetch(i + 32, pv[1], qv[1]);
+                Level sum = {0.f, 0.f};
+#pragma unroll 1
+                for (; i - lane < to; i += 32) {
+                    fetch(i + 64, pv[2], qv[2]);
+                    const Level x = vector_sum<T>(sh, draft != nullptr, pv[0], qv[0], i * VEC - P.skew, gone);
+                    add_exact(sum.hi, sum.lo, x.hi);
+                    sum.lo = __fadd_rn(sum.lo, x.lo);
+                    pv[0] = pv[1], qv[0] = qv[1], pv[1] = pv[2], qv[1] = qv[2];
                 }
-#pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                sum = warp_sum(sum);
                 if (lane == 0) sh.tile[t] = sum;
             }
         });
@@ -208,142 +262,150 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
         const int at = passes++ & 1;
         if (warp == 0) {
             const int n_tiles = (v1 - v0 + per_tile - 1) / per_tile;
-            double sum = 0.0;
-            for (int t = lane; t < n_tiles; t += 32) sum += sh.tile[t];
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane < n_cta) cluster.map_shared_rank(&sh, lane)->total[at][rank] = sum;
+            Level sum = {0.f, 0.f};
+            for (int t = lane; t < n_tiles; t += 32) {
+                add_exact(sum.hi, sum.lo, sh.tile[t].hi);
+                sum.lo = __fadd_rn(sum.lo, sh.tile[t].lo);
+            }
+            sum = warp_sum(sum);
+            if (lane < n_cta) cluster.map_shared_rank(&sh, lane)->total[at][rank] = to_double(sum);
         }
         cluster.sync();
         double total = 0.0;
-        for (int c = 0; c < n_cta; c++) total += sh.total[at][c];
+        if (warp == 0) {
+            total = (lane & 7) < n_cta ? sh.total[at][lane & 7] : 0.0;
+#pragma unroll
+            for (int o = 4; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        }
         return total;
     };
 
-    // ---- the walk, by every thread alike
+    // ---- the walk, by warp 0 of every CTA alike (sixteen warps take sixteen times as long for its binary64 products);
+    // it stops at what needs a pass of the CTA
     int node = -1, count = 0, gone = 0;
+    int next = 0;                    // the first draft that has not been looked at
     double mass = 1.0, sum = 0.0;
     bool summed = false;             // the tiles' sums are those of r
-    for (int i = 0; i < N; i++) {
-        if (sh.parent[i] != node) continue;
-        const int t = sh.token[i];
-        const float pt = sh.p[i], qt = sh.q[i];
-        float r = pt;                // r(t)
-        for (int j = 0; j < gone; j++) {
-            if (draft) r = fmaxf(__fmaf_rn(-sh.level[j].lo, qt, __fmaf_rn(-sh.level[j].hi, qt, r)), 0.f);
-            else if (sh.out[j] == t) r = 0.f;
-        }
-        if (static_cast<double>(sh.u[i]) * static_cast<double>(qt) * mass < static_cast<double>(r)) {
-            if (threadIdx.x == 0) sh.path[count] = i;
-            ++count;
-            node = i;
-            gone = 0;
-            mass = 1.0;
-            summed = false;
-            continue;
-        }
-        __syncthreads();             // the list has been read
-        if (threadIdx.x == 0) {
-            if (draft) {
-                const float hi = static_cast<float>(mass);
-                sh.level[gone] = {hi, static_cast<float>(mass - static_cast<double>(hi))};
-            } else {
-                sh.out[gone] = t;
+    for (;;) {
+        if (warp == 0) {
+            // (nothing is left behind a rejection: the target's own row takes the rest's place)
+            bool rejected = summed && gone > 0 && !(sum > 0.0);
+            if (rejected) gone = 0;
+            while (next < N && !rejected) {
+                const int from = next & ~31;
+                const unsigned child = __ballot_sync(0xffffffffu, from + lane >= next && from + lane < N && sh.parent[from + lane] == node);
+                if (child == 0) {
+                    next = from + 32;
+                    continue;
+                }
+                const int i = from + __ffs(child) - 1, t = sh.token[i];
+                next = i + 1;
+                const float qt = sh.q[i];
+                float r = sh.p[i];       // r(t)
+                for (int j = 0; j < gone; j++) {
+                    if (draft) r = fmaxf(__fmaf_rn(-sh.level[j].lo, qt, __fmaf_rn(-sh.level[j].hi, qt, r)), 0.f);
+                    else if (sh.out[j] == t) r = 0.f;
+                }
+                if (static_cast<double>(sh.u[i]) * static_cast<double>(qt) * mass < static_cast<double>(r)) {
+                    if (lane == 0) sh.path[count] = i;
+                    ++count;
+                    node = i;
+                    gone = 0;
+                    mass = 1.0;
+                    summed = false;
+                    continue;
+                }
+                rejected = true;
+                if (lane == 0) {
+                    if (draft) {
+                        const float hi = static_cast<float>(mass);
+                        sh.level[gone] = {hi, static_cast<float>(mass - static_cast<double>(hi))};
+                    } else {
+                        sh.out[gone] = t;
+                    }
+                }
+                ++gone;
             }
+            if (lane == 0) sh.want = rejected || !summed ? gone : -1, sh.node = node;
         }
         __syncthreads();
-        sum = pass(node, ++gone);
-        if (!(sum > 0.0)) sum = pass(node, gone = 0);
-        mass = sum;
+        const int want = sh.want;    // (the node does not change in a pass)
+        if (want < 0) break;
+        mass = sum = pass(sh.node, want);
         summed = true;
     }
-    if (!summed) sum = pass(node, gone);
 
     // ---- results: the token's CTA draws it
+    if (warp != 0) return;
+    node = sh.node;
     if (rank == 0) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < N; i += kVerThreads) p.accepted[static_cast<size_t>(b) * N + i] = i < count ? sh.path[i] : -1;
-        if (threadIdx.x == 0) {
+        for (int i = lane; i < N; i += 32) p.accepted[static_cast<size_t>(b) * N + i] = i < count ? sh.path[i] : -1;
+        if (lane == 0) {
             p.n_accepted[b] = count;
             if (!(sum > 0.0)) p.token[b] = -1;
         }
     }
-    if (!(sum > 0.0) || warp != 0) return;
+    if (!(sum > 0.0)) return;
     const double goal = static_cast<double>(sh.u[N]) * sum;
-    const double *total = sh.total[(passes - 1) & 1];
-    int last = 0, mine = -1;         // the last CTA that has weights; the one where the sum passes the goal
-    double before = 0.0, prefix = 0.0;
-    for (int c = 0; c < n_cta; c++) {
-        if (total[c] > 0.0) {
-            last = c;
-            if (c == rank) before = prefix;
-        }
-        prefix += total[c];
-        if (mine < 0 && prefix > goal) mine = c;
-    }
-    if ((mine < 0 ? last : mine) != rank) return;  // (none: the goal is the sum itself, by rounding)
-    // the tile, likewise
+    // the CTA where the sum passes the goal (or the last that has weights: the goal is the sum itself, by rounding)
+    double before = 0.0, at_sum = 0.0;
+    bool found;
+    if (find_lane(lane < n_cta ? sh.total[(passes - 1) & 1][lane] : 0.0, goal, before, at_sum, found) != rank) return;
+    before = at_sum;
+    // its tile, likewise
     const int n_tiles = (v1 - v0 + per_tile - 1) / per_tile;
-    int tile = -1, last_tile = 0;
-    double tile_before = before, last_before = before;
-    for (int t0 = 0; t0 < n_tiles && tile < 0; t0 += 32) {
-        const double x = t0 + lane < n_tiles ? sh.tile[t0 + lane] : 0.0;
-        double y = x;                // inclusive prefix
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double z = __shfl_up_sync(0xffffffffu, y, o);
-            if (lane >= o) y += z;
-        }
-        const unsigned some = __ballot_sync(0xffffffffu, x > 0.0), over = __ballot_sync(0xffffffffu, x > 0.0 && before + y > goal);
-        const int at = over ? __ffs(over) - 1 : (some ? 31 - __clz(some) : 0);
-        const double at_before = before + __shfl_sync(0xffffffffu, y - x, at);
-        if (over) tile = t0 + at, tile_before = at_before;
-        else if (some) last_tile = t0 + at, last_before = at_before;
-        before += __shfl_sync(0xffffffffu, y, 31);
+    int tile = 0;
+    found = false;
+    double tile_sum = before;
+#pragma unroll 1
+    for (int t0 = 0; t0 < n_tiles && !found; t0 += 32) {
+        const int at = find_lane(t0 + lane < n_tiles ? to_double(sh.tile[t0 + lane]) : 0.0, goal, before, tile_sum, found);
+        if (at >= 0) tile = t0 + at;
     }
-    if (tile < 0) tile = last_tile, tile_before = last_before;
     rows(node, [&](const Row<T> &P, const Row<T> &Q) {
+        // its vector
         const int from = v0 + tile * per_tile, to = min(from + per_tile, v1);
-        double run = tile_before;
-        int token = -1;              // the last one with a weight, until one passes the goal
-        for (int i0 = from; i0 < to; i0 += 32) {
-            float r[VEC];
-#pragma unroll
-            for (int k = 0; k < VEC; k++) r[k] = 0.f;
-            if (i0 + lane < to) residual(P, Q, i0 + lane, gone, r);
-            double x = 0.0;
-#pragma unroll
-            for (int k = 0; k < VEC; k++) x += static_cast<double>(r[k]);
-            double y = x;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double z = __shfl_up_sync(0xffffffffu, y, o);
-                if (lane >= o) y += z;
+        int vec = -1;
+        uint4 pv, qv, pn, qn;        // the lane's vector, the one behind it
+        auto fetch = [&](int i, uint4 &x, uint4 &y) {
+            x = y = make_uint4(0u, 0u, 0u, 0u);
+            if (i < to) {
+                x = P.load(i);
+                if (draft && gone) y = Q.load(i);
             }
-            const unsigned some = __ballot_sync(0xffffffffu, x > 0.0), over = __ballot_sync(0xffffffffu, x > 0.0 && run + y > goal);
-            const int at = over ? __ffs(over) - 1 : (some ? 31 - __clz(some) : -1);
-            if (at >= 0) {
-                int e = -1;
-                double s = run + y - x;
-#pragma unroll
-                for (int k = 0; k < VEC; k++) {
-                    if (r[k] > 0.f && !(s > goal)) e = k;
-                    s += static_cast<double>(r[k]);
-                }
-                token = __shfl_sync(0xffffffffu, (i0 + lane) * VEC - P.skew + e, at);
-                if (over) break;
-            }
-            run += __shfl_sync(0xffffffffu, y, 31);
+        };
+        uint4 pa, qa;                // that vector
+        pa = qa = make_uint4(0u, 0u, 0u, 0u);
+        found = false;
+        before = tile_sum;
+        fetch(from + lane, pv, qv);
+#pragma unroll 1
+        for (int i0 = from; i0 < to && !found; i0 += 32) {
+            fetch(i0 + 32 + lane, pn, qn);
+            const int at = find_lane(to_double(vector_sum<T>(sh, draft != nullptr, pv, qv, (i0 + lane) * VEC - P.skew, gone)), goal, before,
+                                     at_sum, found);
+            if (at >= 0) vec = i0 + at, pa = pv, qa = qv;
+            pv = pn, qv = qn;
         }
-        if (lane == 0) p.token[b] = token;
+        if (vec < 0 || lane != ((vec - from) & 31)) return;
+        // its element
+        float r[VEC];
+        residual<T>(sh, draft != nullptr, pa, qa, vec * VEC - P.skew, gone, r);
+        int token = -1;
+#pragma unroll
+        for (int k = 0; k < VEC; k++) {
+            if (r[k] > 0.f && (token < 0 || !(at_sum > goal))) token = vec * VEC - P.skew + k;
+            at_sum += static_cast<double>(r[k]);
+        }
+        p.token[b] = token;
     });
 }
 
 template <typename T>
 cudaError_t verify(const VerifyParams &p, cudaStream_t s) {
-    // a slice of 8192 elements or more a CTA: 16 a thread
+    // a slice of 4096 elements or more a CTA (32000 fp32: 4 CTAs 15.3 us, 2 CTAs 16.8, 8 no less)
     int ctas = 1;
-    while (ctas < kVerMaxCtas && p.V / (2 * ctas) >= 8192) ctas *= 2;
+    while (ctas < kVerMaxCtas && p.V / (2 * ctas) >= 4096) ctas *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.B) * ctas);
     cfg.blockDim = dim3(kVerThreads);
