@@ -53,6 +53,21 @@ struct Place {
     long long base;
 };
 
+// A warp's n entries from one place to another, 256 at once: a prompt's entries are as many waits for memory as loads
+// that follow one another (16384 tokens in pages of 16 by 32 at once: 32 of them).
+template <class Load, class Store>
+__device__ __forceinline__ void move_entries(int lane, int n, Load load, Store store) {
+    constexpr int U = 8;
+    for (int k0 = lane; k0 < n; k0 += 32 * U) {
+        int x[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) x[u] = k0 + 32 * u < n ? load(k0 + 32 * u) : 0;
+#pragma unroll
+        for (int u = 0; u < U; u++)
+            if (k0 + 32 * u < n) store(k0 + 32 * u, x[u]);
+    }
+}
+
 // Slot and position of row j of a sequence (held tokens len, granted tokens behind them).
 __device__ __forceinline__ void put_row(const PageParams &p, int b, int j, int len, int granted, const int *entries) {
     const bool fits = j < granted;
@@ -96,7 +111,7 @@ __global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads
         for (int i = warp * kPageCtas + rank; i < n; i += kPageWarps * kPageCtas) {
             const Place y = place[i];
             int *entries = p.table + (b0 + i) * p.table_stride;
-            for (int k = lane; k < y.got; k += 32) entries[y.held + k] = p.free_pages[free - 1 - y.base - k];
+            move_entries(lane, y.got, [&](int k) { return p.free_pages[free - 1 - y.base - k]; }, [&](int k, int page) { entries[y.held + k] = page; });
             __syncwarp();
             if (lane == 0) p.granted[b0 + i] = y.granted;
             if (p.n_max <= kFusedRows && lane < p.n_max) put_row(p, b0 + i, lane, y.len, y.granted, entries);
@@ -158,10 +173,11 @@ __global__ void __cluster_dims__(kPageCtas, 1, 1) __launch_bounds__(kPageThreads
         for (int i = warp * kPageCtas + rank; i < n; i += kPageWarps * kPageCtas) {
             const Place y = place[i];
             const int *entries = p.table + (b0 + i) * p.table_stride;
-            for (int k = lane; k < y.got; k += 32) {  // the last given back lies deepest: what was taken last comes back first
+            // the last given back lies deepest: what was taken last comes back first
+            move_entries(lane, y.got, [&](int k) { return entries[y.held + k]; }, [&](int k, int page) {
                 const long long at = free + total - 1 - y.base - k;
-                if (at < p.n_pages) p.free_pages[at] = entries[y.held + k];
-            }
+                if (at < p.n_pages) p.free_pages[at] = page;
+            });
         }
     }
     cooperative_groups::this_cluster().sync();
