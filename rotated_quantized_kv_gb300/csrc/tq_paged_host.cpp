@@ -51,8 +51,8 @@ tq_status check_paged_view(const tq_layer_view *lv, int B, int H, int Hq, int d,
             if (L.capacity % 16) return TQ_ERR_ALIGN;
         }
     }
-    // query rows are counted in 32 bits
-    return Hq > 0x7fffffff / B ? TQ_ERR_UNSUPPORTED : TQ_OK;
+    // query rows are counted in 32 bits (rounded up to a CTA's)
+    return Hq > (0x7fffffff - 64) / B ? TQ_ERR_UNSUPPORTED : TQ_OK;
 }
 
 tq_status paged_layout(const tq_layer_view *lv, int B, int H, int Hq, int d, PagedLayout &o) {

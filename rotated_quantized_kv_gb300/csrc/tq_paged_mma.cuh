@@ -17,10 +17,16 @@
 //
 // Every warp is a worker of its own: a range of the stage list (tq_paged.cuh), a ring of stages that it fills
 // itself by cp.async, its queries, its sums, its records; warps meet nowhere behind the prologue, and nothing waits but for
-// its own copies.  (Measured against it on 32 x 32768 tokens of 8 heads, K4V4, 64-token pages: CTAs of four warps that share a
-// stage, the warps issuing bulk copies in turn, then teams of four warps with a loader warp each by bulk copies and by cp.async:
-// the loader's serial instructions, some 2000 cycles a stage, and the barriers bounded all of these.)  Twelve
-// warps an SM are what 168 registers leave; they share one value table, a column a lane.
+// its own copies.  (Measured against it: CTAs of four warps that share a stage, the warps issuing bulk copies in turn, then
+// teams of four warps with a loader warp each by bulk copies and by cp.async: the loader's serial instructions, some
+// 2000 cycles a stage, and the barriers bounded all of these, 145 us on the first case below.)  Twelve
+// warps an SM are what 168 registers leave (14 and 16 with fewer registers: no faster); they share one value table, a
+// column a lane.
+//
+// Bound by instruction issue (unpacking) at K1 to K8, by memory at fp16: whole calls, 4 query heads a KV head, 64-token pages,
+// 8 KV heads, of the 6677 GB/s of a copy: 32 x 16384 K4V4 118 us (4.82 TB/s), 32 x 32768 K4V4 210 us (5.4), K3V3 252 us
+// (3.4 TB/s), 32 x 16384 fp16 336 us (6.40 TB/s), 32 x 9000 at d = 64, two heads a KV head, K8V3 57 us (3.88 TB/s; pages of
+// 16 tokens, four runs a stage: 73 us).
 #pragma once
 
 #include <algorithm>

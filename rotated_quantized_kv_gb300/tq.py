@@ -970,7 +970,8 @@ def tq_paged_attention(view: tq_layer_view, q: torch.Tensor, out: torch.Tensor, 
             _require(t.dim() == 2 and c is not None, where)
             width = t.shape[1]
             _int32(t, where, (B, width))
-            at, stride = t.data_ptr(), t.stride(0) if B > 1 else width
+            # (no entries, no storage: a table all the same)
+            at, stride = t.data_ptr() if width else c.data_ptr(), t.stride(0) if B > 1 and width else width
             tensors.append(t)
         if c is not None:
             _int32(c, where, (B,))

@@ -317,9 +317,18 @@ def test_page_tables_and_drafts_on_a_stream_that_is_not_current(tq):
     assert want and all(torch.equal(a, b) for a, b in zip((*one, *two, *args), (*got, *sec, *again)))
 
 
+def test_table_without_entries(tq):
+    """A table of no columns is a table: no sequence holds a token, however many pages the pool has."""
+    B, H, d = 4, 2, 128
+    c = Case(tq, d, H, 2, B, [((4, 4), 64, 64)], seed=9, lens=[[64, 1, 0, 64]])
+    c.tables = [t[:, :0] for t in c.tables]
+    out = c.run(c.workspace())
+    assert (out == 0).all()
+
+
 @pytest.mark.parametrize("d,kind", [(128, (4, 4)), (64, (3, 3)), (128, "fp16")])
-def test_waits_that_run_out(tq, d, kind):
-    """A wait that gives up is reported, the rows it concerns stay unwritten, and the next call is whole."""
+def test_no_wait_to_run_out(tq, d, kind):
+    """The limit of the waits of other calls' kernels has no part in this one: nothing in it polls for another part."""
     c = Case(tq, d, 2, 4, 3, [(kind, 64, 700)], seed=3)
     ws = c.workspace()
     want = c.run(ws).clone()
@@ -327,16 +336,10 @@ def test_waits_that_run_out(tq, d, kind):
     try:
         tq.tq_set_decode_wait_polls(0)
         c.run(ws, out)
-        flag = tq.tq_decode_error_flag(ws)
+        assert tq.tq_decode_error_flag(ws) == 0
     finally:
         tq.tq_set_decode_wait_polls(tq.TQ_WAIT_POLLS_DEFAULT)
-    held = torch.stack(c.lens).sum(0) > 0
-    if flag:
-        assert torch.isnan(out).any()
-        assert torch.equal(torch.isnan(out).any(-1), torch.isnan(out).all(-1))
-    ok = ~torch.isnan(out).any(-1)
-    assert torch.equal(bits(out[ok]), bits(want[ok])) and (out[~held] == 0).all()
-    assert torch.equal(bits(c.run(ws)), bits(want)) and tq.tq_decode_error_flag(ws) == 0
+    assert torch.equal(bits(out), bits(want))
 
 
 def test_offsets_past_32_bits(tq):
