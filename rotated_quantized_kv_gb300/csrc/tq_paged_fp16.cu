@@ -51,6 +51,7 @@ struct Half {
         }
     }
     static __device__ __forceinline__ void fill_all(const Source &s, unsigned slot, uint64_t pol, int lane) { copy(s.ka, s.va, slot, 0, PT, pol, lane); }
+    static __device__ __forceinline__ bool fill_blocks(const PagedParams &, const Source &, const paged::Walk &, unsigned, uint64_t, int) { return false; }
     static __device__ __forceinline__ void fill(const uint8_t *k, const uint8_t *v, const char *, unsigned slot, int from, int run,
                                                 uint64_t pol, int lane) {
         copy(k, v, slot, from, run, pol, lane);

@@ -23,10 +23,10 @@
 // warps an SM are what 168 registers leave (14 and 16 with fewer registers: no faster); they share one value table, a
 // column a lane.
 //
-// Bound by instruction issue (unpacking) at K1 to K8, by memory at fp16: whole calls, 4 query heads a KV head, 64-token pages,
-// 8 KV heads, of the 6677 GB/s of a copy: 32 x 16384 K4V4 118 us (4.82 TB/s), 32 x 32768 K4V4 210 us (5.4), K3V3 252 us
-// (3.4 TB/s), 32 x 16384 fp16 336 us (6.40 TB/s), 32 x 9000 at d = 64, two heads a KV head, K8V3 57 us (3.88 TB/s; pages of
-// 16 tokens, four runs a stage: 73 us).
+// Bound by instruction issue and the latency of dependent instructions at K1 to K8, by memory at fp16: whole calls, 4
+// query heads a KV head, 64-token pages, 8 KV heads, a copy being 6677 GB/s: 32 x 16384 K4V4 118 us (4.82 TB/s; pages
+// of 48 and 16 tokens, whose stages come from several pages: 125 and 135 us), 32 x 32768 K4V4 211 us (5.42), K3V3 248 us
+// (3.53), 32 x 16384 fp16 336 us (6.40), 32 x 9000 at d = 64, two heads a KV head, K8V3 57 us (3.88; pages of 16: 62 us).
 #pragma once
 
 #include <algorithm>
@@ -301,6 +301,7 @@ struct Source {
 //   PT, kSlot, kTable           tokens and bytes of a stage, bytes of the CTA's table
 //   kTokenK, kTokenV            bytes of a token's rows
 //   fill_all(...), fill(...)    a whole stage, a run of tokens of a page into the slot; clear(...): a slot that will not be full
+//   fill_blocks(...)            a whole stage from several pages, where the form has a way of its own
 //   queries(...), stage(...)    a block's queries; the tiles of a stage
 //   fold(...), record(...)      the sums into the copy, the copy into the record
 // What a stage costs beside its tiles is kept short: addresses move by constants inside a page, and only stages that
@@ -321,6 +322,7 @@ __device__ __forceinline__ void attend(const PagedParams &p, F &f, int worker, i
         bool whole = n == F::PT;
         if (__builtin_expect(whole && src.left >= F::PT && src.good, 1)) {
             F::fill_all(src, slot, pol, lane);
+        } else if (whole && F::fill_blocks(p, src, w, slot, pol, lane)) {
         } else {                         // its end, or several pages: page i to lane i
             const uint32_t pages = static_cast<uint32_t>(src.pages.at(src.index + lane));
             const bool used = lane == 0 ? n > 0 : src.left + (lane - 1) * min(src.page, F::PT) < n;
@@ -545,7 +547,8 @@ struct Packed {
     static __device__ __forceinline__ void clear(uint8_t *, int) {}
     // 16-byte chunk i of a value row of 4 bits lies at i ^ (row / 2 & 3): the four row pairs that a load takes at once share
     // two bank groups instead of one (the keys' rows, and the others', meet in fewer).
-    static __device__ __forceinline__ unsigned value_chunk(int lane) { return VB == 4 ? 16 * (lane ^ ((lane >> 3) & 3)) : 16 * lane; }
+    static __device__ __forceinline__ unsigned value_at(int i) { return VB == 4 ? i ^ ((i >> 3) & 3) : i; }
+    static __device__ __forceinline__ unsigned value_chunk(int lane) { return 16 * value_at(lane); }
     static __device__ __forceinline__ void fill_all(const Source &s, unsigned slot, uint64_t pol, int lane) {
         const unsigned dk = slot + 16 * lane, dv = slot + ROWS * RK + value_chunk(lane);
 #pragma unroll
@@ -553,6 +556,38 @@ struct Packed {
 #pragma unroll
         for (int i = 0; i < VB; i++) copy16(dv + 512 * i, s.va + 512 * i, pol);
         if ((lane & 15) < PT / 4) copy16(slot + (lane >= 16 ? kVs : kKs) + 16 * (lane & 15), s.sa, pol);
+    }
+    // A whole stage from several pages: they are multiples of 16 tokens, so LB lanes take a block of 16 each, wherever it lies
+    // (32 x 16384 tokens K4V4 in pages of 16: 159 us page by page).  False: not all of them are in the pool.
+    static __device__ __forceinline__ bool fill_blocks(const PagedParams &p, const Source &s, const paged::Walk &w, unsigned slot, uint64_t pol,
+                                                       int lane) {
+        constexpr int LB = 32 * 16 / PT;
+        const PagedSeg &g = p.seg[p.cls.seg[w.i]];
+        const int t0 = w.st * PT;
+        auto place = [&](int block, uint32_t &page, uint32_t &skip) {
+            const int t = t0 + 16 * block, i = paged::page_index(g, t);
+            page = static_cast<uint32_t>(s.pages.at(i));
+            skip = static_cast<uint32_t>(t - i * s.page);
+        };
+        uint32_t page, skip;
+        const uint8_t *ka, *va;
+        const char *sa;
+        const int block = lane / LB, l = lane % LB;
+        place(block, page, skip);
+        if (__any_sync(0xffffffffu, page >= static_cast<uint32_t>(s.n_pages))) return false;
+        s.aim<Packed>(page, skip, ka, va, sa);
+        ka -= 16 * (lane - l);
+        va -= 16 * (lane - l);
+        const unsigned dk = slot + block * 16 * kTokenK + 16 * l, dv = slot + ROWS * RK + block * 16 * kTokenV;
+#pragma unroll
+        for (int i = 0; i < KB; i++) copy16(dk + 16 * LB * i, ka + 16 * LB * i, pol);
+#pragma unroll
+        for (int i = 0; i < VB; i++) copy16(dv + 16 * value_at(l + LB * i), va + 16 * LB * i, pol);
+        const int sl = lane & 15;        // four scales a lane
+        place(min(sl / 4, PT / 16 - 1), page, skip);
+        s.aim<Packed>(page, skip, ka, va, sa);
+        if (sl < PT / 4) copy16(slot + (lane >= 16 ? kVs : kKs) + 16 * sl, sa - 16 * (sl & ~3), pol);
+        return true;
     }
     // (runs start at multiples of 16 tokens, eight rows at least; an odd end rounds up inside the page)
     static __device__ __forceinline__ void fill(const uint8_t *k, const uint8_t *v, const char *sc, unsigned slot, int from, int run,
