@@ -25,7 +25,10 @@ CUDA_SOURCES = ["tq_compress.cu", "tq_compress_dense.cu", "tq_decode.cu", "tq_ma
                 "tq_compress_rows_np2.cu", "tq_rope.cu", "tq_append.cu", "tq_read.cu", "tq_tree.cu",
                 "tq_tree_mma.cu", "tq_append_rows_keys.cu", "tq_append_rows_values.cu", "tq_read_rows_keys.cu",
                 "tq_read_rows_values.cu",
-                "tq_read_rows_keys_d64.cu", "tq_read_rows_values_d64.cu", "tq_pages.cu", "tq_paged.cu",
+                "tq_read_rows_keys_d64.cu", "tq_read_rows_values_d64.cu",
+                "tq_append_rows_keys_slots.cu", "tq_append_rows_values_slots.cu", "tq_read_rows_keys_slots.cu",
+                "tq_read_rows_values_slots.cu", "tq_read_rows_keys_d64_slots.cu", "tq_read_rows_values_d64_slots.cu",
+                "tq_pages.cu", "tq_paged.cu",
                 "tq_paged_fp16.cu", "tq_verify.cu"] + [
                 f"tq_paged_kb{k}_d{d}.cu" for k in range(1, 9) for d in (128, 64)] + [
                 f"tq_decode_kb{k}.cu" for k in range(1, 9)] + [

@@ -27,6 +27,7 @@ struct RowBlock {
     bool valid;
 };
 
+template <bool SLOTS>
 __device__ __forceinline__ RowBlock row_block(const AppendRowsParams &p, int n_tblk, int blk, int lane) {
     RowBlock r;
     r.h = p.r.head[blk % p.r.n_heads];
@@ -34,7 +35,7 @@ __device__ __forceinline__ RowBlock row_block(const AppendRowsParams &p, int n_t
     r.j = (rest % n_tblk) * 32 + lane;
     r.b = rest / n_tblk;
     r.src = r.at = r.pos = 0;
-    r.valid = map_row(p.rows, r.b, r.j, p.r.capacity, r.src, r.at, r.pos);
+    r.valid = map_row<SLOTS>(p.rows, r.b, r.j, p.r.capacity, r.src, r.at, r.pos);
     return r;
 }
 
@@ -119,7 +120,7 @@ __device__ __forceinline__ void rope_rows(const AppendRowsParams &p, const RowBl
     }
 }
 
-template <int BITS, bool VAL>
+template <int BITS, bool VAL, bool SLOTS>
 __global__ void __launch_bounds__(kThreads, 3) append_rows_kernel(const __grid_constant__ AppendRowsParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
     uint32_t *in_mask = reinterpret_cast<uint32_t *>(smem + kWarps * 2 * kWarpBuf);
@@ -144,14 +145,14 @@ __global__ void __launch_bounds__(kThreads, 3) append_rows_kernel(const __grid_c
     uint8_t *bufs = smem + warp * 2 * kWarpBuf;
     const int n_tblk = (p.r.T + 31) / 32, n_blk = n_tblk * p.r.n_heads * p.r.B;
     const int gw = blockIdx.x * kWarps + warp, nw = gridDim.x * kWarps;
-    if (gw < n_blk) stage_mapped(p, row_block(p, n_tblk, gw, lane), bufs, lane);
+    if (gw < n_blk) stage_mapped(p, row_block<SLOTS>(p, n_tblk, gw, lane), bufs, lane);
     asm volatile("cp.async.commit_group;\n" ::);
     for (int blk = gw, it = 0; blk < n_blk; blk += nw, it++) {
-        if (blk + nw < n_blk) stage_mapped(p, row_block(p, n_tblk, blk + nw, lane), bufs + ((it + 1) & 1) * kWarpBuf, lane);
+        if (blk + nw < n_blk) stage_mapped(p, row_block<SLOTS>(p, n_tblk, blk + nw, lane), bufs + ((it + 1) & 1) * kWarpBuf, lane);
         asm volatile("cp.async.commit_group;\n" ::);
         asm volatile("cp.async.wait_group 1;\n" ::: "memory");
         __syncwarp();
-        const RowBlock r = row_block(p, n_tblk, blk, lane);
+        const RowBlock r = row_block<SLOTS>(p, n_tblk, blk, lane);
         uint8_t *buf = bufs + (it & 1) * kWarpBuf;
         if (!__any_sync(0xffffffffu, r.valid)) continue;  // (its buffer holds nothing new)
         if constexpr (!VAL) {
@@ -165,38 +166,39 @@ __global__ void __launch_bounds__(kThreads, 3) append_rows_kernel(const __grid_c
         rows_vector<BITS, VAL, 1, 1>(buf + lane * kRowBytes, in_mask, out_pair, thr, vtab, p.r.bucket4_ok != 0, lane, 0, w,
                                      scale, scale_b);
         if (r.valid) {
-            uint4 *dst = reinterpret_cast<uint4 *>(p.r.codes + static_cast<size_t>(r.at) * p.r.block + p.r.off[r.h] +
+            const int at = SLOTS ? r.at : r.b;
+            uint4 *dst = reinterpret_cast<uint4 *>(p.r.codes + static_cast<size_t>(at) * p.r.block + p.r.off[r.h] +
                                                    static_cast<size_t>(r.pos) * (16 * BITS));
 #pragma unroll
             for (int j = 0; j < BITS; j++) dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-            p.r.scale[(static_cast<size_t>(r.at) * p.r.H + r.h) * p.r.capacity + r.pos] = scale;
+            p.r.scale[(static_cast<size_t>(at) * p.r.H + r.h) * p.r.capacity + r.pos] = scale;
         }
     }
     asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the call's last launch ends behind its first
 }
 
-template <int BITS, bool VAL>
+template <int BITS, bool VAL, bool SLOTS>
 cudaError_t append_rows_launch(const AppendRowsParams &p, bool beside, cudaStream_t s) {
     constexpr size_t smem = rows_smem_bytes<1>(VAL && BITS <= 4);
-    const cudaError_t e = cudaFuncSetAttribute(append_rows_kernel<BITS, VAL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(append_rows_kernel<BITS, VAL, SLOTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     const long long blocks = (static_cast<long long>((p.r.T + 31) / 32) * p.r.n_heads * p.r.B + kWarps - 1) / kWarps;
     const long long grid = std::min<long long>(blocks, static_cast<long long>(current_sm_count()) * 3);
-    return launch_beside(append_rows_kernel<BITS, VAL>, static_cast<unsigned>(grid), kThreads, smem, s, beside, p);
+    return launch_beside(append_rows_kernel<BITS, VAL, SLOTS>, static_cast<unsigned>(grid), kThreads, smem, s, beside, p);
 }
 
-template <bool VAL>
+template <bool VAL, bool SLOTS>
 cudaError_t append_rows_dispatch(const AppendRowsParams &p, int bits, bool beside, cudaStream_t s) {
     switch (bits) {
-        case 1: return append_rows_launch<1, VAL>(p, beside, s);
-        case 2: return append_rows_launch<2, VAL>(p, beside, s);
-        case 3: return append_rows_launch<3, VAL>(p, beside, s);
-        case 4: return append_rows_launch<4, VAL>(p, beside, s);
-        case 5: return append_rows_launch<5, VAL>(p, beside, s);
-        case 6: return append_rows_launch<6, VAL>(p, beside, s);
-        case 7: return append_rows_launch<7, VAL>(p, beside, s);
-        case 8: return append_rows_launch<8, VAL>(p, beside, s);
+        case 1: return append_rows_launch<1, VAL, SLOTS>(p, beside, s);
+        case 2: return append_rows_launch<2, VAL, SLOTS>(p, beside, s);
+        case 3: return append_rows_launch<3, VAL, SLOTS>(p, beside, s);
+        case 4: return append_rows_launch<4, VAL, SLOTS>(p, beside, s);
+        case 5: return append_rows_launch<5, VAL, SLOTS>(p, beside, s);
+        case 6: return append_rows_launch<6, VAL, SLOTS>(p, beside, s);
+        case 7: return append_rows_launch<7, VAL, SLOTS>(p, beside, s);
+        case 8: return append_rows_launch<8, VAL, SLOTS>(p, beside, s);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -3,6 +3,6 @@
 
 namespace tqk {
 cudaError_t launch_append_keys(const AppendRowsParams &p, int bits, bool beside, cudaStream_t s) {
-    return append_rows_dispatch<false>(p, bits, beside, s);
+    return p.rows.slots ? launch_append_keys_slots(p, bits, beside, s) : append_rows_dispatch<false, false>(p, bits, beside, s);
 }
 }  // namespace tqk

@@ -3,6 +3,6 @@
 
 namespace tqk {
 cudaError_t launch_append_values(const AppendRowsParams &p, int bits, bool beside, cudaStream_t s) {
-    return append_rows_dispatch<true>(p, bits, beside, s);
+    return p.rows.slots ? launch_append_values_slots(p, bits, beside, s) : append_rows_dispatch<true, false>(p, bits, beside, s);
 }
 }  // namespace tqk

@@ -94,7 +94,7 @@ struct ReadBlock {
     bool valid, valid2;
 };
 
-template <int NP>
+template <int NP, bool SLOTS>
 __device__ __forceinline__ ReadBlock read_block(const ReadRowsParams &p, int n_tblk, int blk, int lane) {
     ReadBlock r;
     r.tb = blk % n_tblk;
@@ -102,8 +102,10 @@ __device__ __forceinline__ ReadBlock read_block(const ReadRowsParams &p, int n_t
     r.h = p.head[rest % p.n_heads];
     r.b = rest / p.n_heads;
     const int j = (32 * r.tb + lane) * NP;
-    r.valid = place_row(p.rows, r.b, j, p.capacity, r.at, r.t);
-    r.valid2 = NP == 2 && place_row(p.rows, r.b, j + 1, p.capacity, r.at2, r.t2);
+    r.at = r.t = 0;
+    r.valid = place_row<SLOTS>(p.rows, r.b, j, p.capacity, r.at, r.t);
+    r.at2 = r.t2 = 0;
+    r.valid2 = NP == 2 && place_row<SLOTS>(p.rows, r.b, j + 1, p.capacity, r.at2, r.t2);
     return r;
 }
 
@@ -114,31 +116,33 @@ __device__ __forceinline__ void cp_async8(void *dst, const void *src) {
 }
 
 // The lane's records and scales on their way (records lie at the lane's place).
-template <int BITS, int NP>
+template <int BITS, int NP, bool SLOTS>
 __device__ __forceinline__ float2 fetch_record(const ReadRowsParams &p, const ReadBlock &r, uint8_t *buf, int lane) {
     buf += lane * (16 * BITS);
-    auto record = [&](int at, int t) { return p.codes + at * p.block + p.off[r.h] + static_cast<size_t>(t) * (16 * BITS / NP); };
-    auto scale = [&](int at, int t) { return __ldg(p.scale + (static_cast<size_t>(at) * p.H + r.h) * p.capacity + t); };
+    auto block = [&](int at) { return SLOTS ? at : r.b; };
+    auto record = [&](int at, int t) { return p.codes + block(at) * p.block + p.off[r.h] + static_cast<size_t>(t) * (16 * BITS / NP); };
+    auto scale = [&](int at, int t) { return p.scale + (static_cast<size_t>(block(at)) * p.H + r.h) * p.capacity + t; };
     float2 s = make_float2(0.f, 0.f);
     if constexpr (NP == 1) {
         if (r.valid) {
             const uint8_t *rec = record(r.at, r.t);
 #pragma unroll
             for (int i = 0; i < BITS; i++) cp_async16(buf + 16 * i, rec + 16 * i);
-            s.x = scale(r.at, r.t);
+            s.x = __ldg(scale(r.at, r.t));
         }
     } else {
+        const uint8_t *rec = record(r.at, r.t);
+        const float *sc = scale(r.at, r.t);
         if (r.valid) {
-            const uint8_t *rec = record(r.at, r.t);
 #pragma unroll
             for (int i = 0; i < BITS; i++) cp_async8(buf + 8 * i, rec + 8 * i);
-            s.x = scale(r.at, r.t);
+            s.x = __ldg(sc);
         }
+        if constexpr (SLOTS) rec = record(r.at2, r.t2) - 8 * BITS, sc = scale(r.at2, r.t2) - 1;  // (else they follow one another)
         if (r.valid2) {
-            const uint8_t *rec = record(r.at2, r.t2);
 #pragma unroll
-            for (int i = 0; i < BITS; i++) cp_async8(buf + 8 * (BITS + i), rec + 8 * i);
-            s.y = scale(r.at2, r.t2);
+            for (int i = BITS; i < 2 * BITS; i++) cp_async8(buf + 8 * i, rec + 8 * i);
+            s.y = __ldg(sc + 1);
         }
     }
     return s;
@@ -166,7 +170,7 @@ __device__ __forceinline__ void put_row16(const float2 (&a)[64], uint8_t *row, i
     }
 }
 
-template <int BITS, bool VAL, int NP>
+template <int BITS, bool VAL, int NP, bool SLOTS>
 __global__ void __launch_bounds__(kThreads, 3) read_rows_kernel(const __grid_constant__ ReadRowsParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
     const int rows_bytes = read_rows_bytes(p.dtype), per_warp = rows_bytes + 2 * read_records_bytes<BITS>();
@@ -186,17 +190,17 @@ __global__ void __launch_bounds__(kThreads, 3) read_rows_kernel(const __grid_con
     const int n_tblk = (p.rows.n_max + 32 * NP - 1) / (32 * NP), n_blk = n_tblk * p.n_heads * p.B;
     const int gw = blockIdx.x * kWarps + warp, nw = gridDim.x * kWarps;
     float2 sc, sc_next = make_float2(0.f, 0.f);
-    if (gw < n_blk) sc_next = fetch_record<BITS, NP>(p, read_block<NP>(p, n_tblk, gw, lane), recs, lane);
+    if (gw < n_blk) sc_next = fetch_record<BITS, NP, SLOTS>(p, read_block<NP, SLOTS>(p, n_tblk, gw, lane), recs, lane);
     asm volatile("cp.async.commit_group;\n" ::);
     for (int blk = gw, it = 0; blk < n_blk; blk += nw, it++) {
         sc = sc_next;
         if constexpr (NP == 1) sc.y = sc.x;
         if (blk + nw < n_blk)  // each lane reads its own place alone
-            sc_next = fetch_record<BITS, NP>(p, read_block<NP>(p, n_tblk, blk + nw, lane),
+            sc_next = fetch_record<BITS, NP, SLOTS>(p, read_block<NP, SLOTS>(p, n_tblk, blk + nw, lane),
                                          recs + ((it + 1) & 1) * read_records_bytes<BITS>(), lane);
         asm volatile("cp.async.commit_group;\n" ::);
         asm volatile("cp.async.wait_group 1;\n" ::: "memory");
-        const ReadBlock r = read_block<NP>(p, n_tblk, blk, lane);
+        const ReadBlock r = read_block<NP, SLOTS>(p, n_tblk, blk, lane);
         const unsigned some = __ballot_sync(0xffffffffu, r.valid);
         const unsigned some2 = NP == 2 ? __ballot_sync(0xffffffffu, r.valid2) : 0u;
         if (!(some | some2)) continue;
@@ -286,28 +290,28 @@ __global__ void __launch_bounds__(kThreads, 3) read_rows_kernel(const __grid_con
     asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the call's last launch ends behind its first
 }
 
-template <int BITS, bool VAL, int NP>
+template <int BITS, bool VAL, int NP, bool SLOTS>
 cudaError_t read_rows_launch(const ReadRowsParams &p, bool beside, cudaStream_t s) {
     const size_t smem = read_smem_bytes<BITS, VAL>(p.dtype);
-    const cudaError_t e = cudaFuncSetAttribute(read_rows_kernel<BITS, VAL, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(read_rows_kernel<BITS, VAL, NP, SLOTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(read_smem_bytes<BITS, VAL>(TQ_DTYPE_F32)));
     if (e != cudaSuccess) return e;
     const long long blocks = (static_cast<long long>((p.rows.n_max + 32 * NP - 1) / (32 * NP)) * p.n_heads * p.B + kWarps - 1) / kWarps;
     const long long grid = std::min<long long>(blocks, static_cast<long long>(current_sm_count()) * 3);
-    return launch_beside(read_rows_kernel<BITS, VAL, NP>, static_cast<unsigned>(grid), kThreads, smem, s, beside, p);
+    return launch_beside(read_rows_kernel<BITS, VAL, NP, SLOTS>, static_cast<unsigned>(grid), kThreads, smem, s, beside, p);
 }
 
-template <bool VAL, int NP>
+template <bool VAL, int NP, bool SLOTS>
 cudaError_t read_rows_dispatch(const ReadRowsParams &p, int bits, bool beside, cudaStream_t s) {
     switch (bits) {
-        case 1: return read_rows_launch<1, VAL, NP>(p, beside, s);
-        case 2: return read_rows_launch<2, VAL, NP>(p, beside, s);
-        case 3: return read_rows_launch<3, VAL, NP>(p, beside, s);
-        case 4: return read_rows_launch<4, VAL, NP>(p, beside, s);
-        case 5: return read_rows_launch<5, VAL, NP>(p, beside, s);
-        case 6: return read_rows_launch<6, VAL, NP>(p, beside, s);
-        case 7: return read_rows_launch<7, VAL, NP>(p, beside, s);
-        case 8: return read_rows_launch<8, VAL, NP>(p, beside, s);
+        case 1: return read_rows_launch<1, VAL, NP, SLOTS>(p, beside, s);
+        case 2: return read_rows_launch<2, VAL, NP, SLOTS>(p, beside, s);
+        case 3: return read_rows_launch<3, VAL, NP, SLOTS>(p, beside, s);
+        case 4: return read_rows_launch<4, VAL, NP, SLOTS>(p, beside, s);
+        case 5: return read_rows_launch<5, VAL, NP, SLOTS>(p, beside, s);
+        case 6: return read_rows_launch<6, VAL, NP, SLOTS>(p, beside, s);
+        case 7: return read_rows_launch<7, VAL, NP, SLOTS>(p, beside, s);
+        case 8: return read_rows_launch<8, VAL, NP, SLOTS>(p, beside, s);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -3,6 +3,6 @@
 
 namespace tqk {
 cudaError_t launch_read_keys(const ReadRowsParams &p, int bits, bool beside, cudaStream_t s) {
-    return read_rows_dispatch<false, 1>(p, bits, beside, s);
+    return p.rows.slots ? launch_read_keys_slots(p, bits, beside, s) : read_rows_dispatch<false, 1, false>(p, bits, beside, s);
 }
 }  // namespace tqk

@@ -3,6 +3,6 @@
 
 namespace tqk {
 cudaError_t launch_read_values_d64(const ReadRowsParams &p, int bits, bool beside, cudaStream_t s) {
-    return read_rows_dispatch<true, 2>(p, bits, beside, s);
+    return p.rows.slots ? launch_read_values_d64_slots(p, bits, beside, s) : read_rows_dispatch<true, 2, false>(p, bits, beside, s);
 }
 }  // namespace tqk

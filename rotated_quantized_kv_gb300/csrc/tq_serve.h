@@ -87,7 +87,9 @@ struct AppendRowsParams {
     int64_t pos_stride;
 };
 cudaError_t launch_append_keys(const AppendRowsParams &p, int bits, bool beside, cudaStream_t s);
+cudaError_t launch_append_keys_slots(const AppendRowsParams &p, int bits, bool beside, cudaStream_t s);
 cudaError_t launch_append_values(const AppendRowsParams &p, int bits, bool beside, cudaStream_t s);
+cudaError_t launch_append_values_slots(const AppendRowsParams &p, int bits, bool beside, cudaStream_t s);
 
 struct ReadParams {
     SegView seg;
@@ -120,9 +122,13 @@ struct ReadRowsParams {
     float level[256];            // values: the centroids
 };
 cudaError_t launch_read_keys(const ReadRowsParams &p, int bits, bool beside, cudaStream_t s);
+cudaError_t launch_read_keys_slots(const ReadRowsParams &p, int bits, bool beside, cudaStream_t s);
 cudaError_t launch_read_values(const ReadRowsParams &p, int bits, bool beside, cudaStream_t s);
+cudaError_t launch_read_values_slots(const ReadRowsParams &p, int bits, bool beside, cudaStream_t s);
 cudaError_t launch_read_keys_d64(const ReadRowsParams &p, int bits, bool beside, cudaStream_t s);
+cudaError_t launch_read_keys_d64_slots(const ReadRowsParams &p, int bits, bool beside, cudaStream_t s);
 cudaError_t launch_read_values_d64(const ReadRowsParams &p, int bits, bool beside, cudaStream_t s);
+cudaError_t launch_read_values_d64_slots(const ReadRowsParams &p, int bits, bool beside, cudaStream_t s);
 
 // ----------------------------------------------------------------- tree attention
 // The work is a list of 128-token tiles.  For sequence b in order, KV head h,
