@@ -57,15 +57,14 @@ __global__ void __launch_bounds__(kPlainThreads) paged_plain_kernel(const __grid
     using C = Plain<D>;
     constexpr int R = C::R, TT = C::TT, LD = C::LD, DPT = C::DPT;
     extern __shared__ float sm[];
-    __shared__ int buf[kPlainWarps + 2];
+    __shared__ int buf[kPlainWarps + 4];
     float *q = sm, *raw = q + R * LD, *tok = raw + R * LD, *S = tok + TT * LD;  // queries of the segment's space, as they are; tokens; scores
     float *row_m = S + R * TT, *row_l = row_m + R, *row_c = row_l + R;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, worker = blockIdx.x;
     asm volatile("griddepcontrol.launch_dependents;");
     const PagedList &l = p.list;
-    const int total = ranges_of<kPlainThreads, 1>(l, p.cls, Share<kPlainThreads>(l, p.cls), worker, 0, p.first, buf);
-    int begin, end;
-    worker_range(p.cls, total, worker, begin, end);
+    ranges_of<kPlainThreads, 1>(l, p.cls, Share<kPlainThreads>(l, p.cls), worker, 0, p.first, buf);
+    const int begin = buf[kPlainWarps + 2], end = buf[kPlainWarps + 3];
     if (begin < end) {
         Walk w = seek(l, p.cls, buf[kPlainWarps], buf[kPlainWarps + 1]);
         float acc[R][DPT];
@@ -313,8 +312,10 @@ __global__ void __launch_bounds__(32 * kRowWarps) paged_merge_rows_kernel(const 
         else
             for (int i = 0; i < h; i++) s += c.n_rb * head_stages(l, c, b, i);
         const int workers = workers_of(c, total);
-        w0 = max(worker_of(total, s, workers), 0);
-        w1 = min(worker_of(total, s + n - 1, workers), workers - 1);
+        // (divisions of 64 bits: one lane's for the first, another's for the last)
+        const int w = worker_of(total, lane & 1 ? s + n - 1 : s, workers);
+        w0 = max(__shfl_sync(0xffffffffu, w, 0), 0);
+        w1 = min(__shfl_sync(0xffffffffu, w, 1), workers - 1);
     };
     const bool scan = l.B <= kScan;
     int w0 = 0, w1 = -1;

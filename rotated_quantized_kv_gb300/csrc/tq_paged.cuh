@@ -159,10 +159,11 @@ struct Share {
     }
 };
 // Ranges of a CTA's TEAMS workers, worker t * step + first_worker for team t (all of the CTA's threads with their
-// shares; synchronises).  buf: THREADS / 32 + 2 TEAMS ints of shared memory; team t's first sequence and the stages of it
-// before its range are at THREADS / 32 + 2 t.  Returns the total.
+// shares; synchronises).  buf: THREADS / 32 + 4 TEAMS ints of shared memory; team t's first sequence and the stages of it
+// before its range, and the range [begin, end), are at THREADS / 32 + 4 t.  (A division of 64 bits for each bound, by a
+// thread of its own: all threads doing all of them were 3 us of 32 with 8 sequences of up to 4096 tokens, fp16.)
 template <int THREADS, int TEAMS>
-__device__ __forceinline__ int ranges_of(const PagedList &l, const PagedClass &c, const Share<THREADS> &own, int first_worker, int step,
+__device__ __forceinline__ void ranges_of(const PagedList &l, const PagedClass &c, const Share<THREADS> &own, int first_worker, int step,
                                          int *first, int *buf) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int incl = own.sum;
@@ -187,30 +188,25 @@ __device__ __forceinline__ int ranges_of(const PagedList &l, const PagedClass &c
         }
         if (threadIdx.x == 0) first[l.B] = total;
     }
-    const int workers = workers_of(c, total);
+    buf += THREADS / 32;
+    if (threadIdx.x < 2 * TEAMS) {
+        const int workers = workers_of(c, total), t = threadIdx.x >> 1, worker = t * step + first_worker;
+        buf[4 * t + 2 + (threadIdx.x & 1)] = worker < workers ? worker_begin(total, worker + (threadIdx.x & 1), workers) : total;
+    }
+    __syncthreads();
 #pragma unroll 1
     for (int t = 0; t < TEAMS; t++) {
-        const int worker = t * step + first_worker;
-        if (worker >= workers) break;
-        const int begin = worker_begin(total, worker, workers);
+        const int begin = buf[4 * t + 2];
         if (own.sum > 0 && before <= begin && begin < before + own.sum) {
             int at = before, b = own.b0;
 #pragma unroll 1
             for (int n; b + 1 < own.b1 && begin >= at + (n = sequence_stages(l, c, b)); b++) at += n;
-            buf[THREADS / 32 + 2 * t] = b;
-            buf[THREADS / 32 + 2 * t + 1] = begin - at;
+            buf[4 * t] = b;
+            buf[4 * t + 1] = begin - at;
         }
     }
     __syncthreads();
-    return total;
 }
-// The range [begin, end) of a worker.
-__device__ __forceinline__ void worker_range(const PagedClass &c, int total, int worker, int &begin, int &end) {
-    const int workers = workers_of(c, total);
-    begin = worker < workers ? worker_begin(total, worker, workers) : total;
-    end = worker < workers ? worker_begin(total, worker + 1, workers) : total;
-}
-
 // The index of the page that holds token t.
 __device__ __forceinline__ int page_index(const PagedSeg &s, int t) {
     return static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned>(t)) * s.magic) >> s.shift);

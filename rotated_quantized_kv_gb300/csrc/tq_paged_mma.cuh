@@ -435,19 +435,19 @@ struct Ring {
 template <class F, int NS>
 __global__ void __launch_bounds__(kPagedThreads, 1) paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ Levels lv) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int bufs[kWarps + 2 * kWarps];
+    __shared__ int bufs[kWarps + 4 * kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int worker = warp * gridDim.x + blockIdx.x;  // (few stages go to as many SMs)
     const paged::Share<kPagedThreads> share(p.list, p.cls);
     pdl_launch_dependents();
     F::fill_table(smem, lv);
-    const int total = paged::ranges_of<kPagedThreads, kWarps>(p.list, p.cls, share, blockIdx.x, gridDim.x, p.first, bufs);  // (synchronises)
-    int begin, end;
-    paged::worker_range(p.cls, total, worker, begin, end);
+    paged::ranges_of<kPagedThreads, kWarps>(p.list, p.cls, share, blockIdx.x, gridDim.x, p.first, bufs);  // (synchronises)
+    const int *range = bufs + kWarps + 4 * warp;
+    const int begin = range[2], end = range[3];
     if (begin < end) {
         uint8_t *mine = smem + F::kTable + warp * Ring<F>::warp_bytes;
         F f(smem, lv, lane);
-        attend<F, NS>(p, f, worker, end - begin, bufs[kWarps + 2 * warp], bufs[kWarps + 2 * warp + 1], mine,
+        attend<F, NS>(p, f, worker, end - begin, range[0], range[1], mine,
                       reinterpret_cast<float *>(mine + NS * Ring<F>::slot), lane);
     }
     pdl_wait();  // the call's last launch ends behind its first
