@@ -160,6 +160,9 @@ __device__ __forceinline__ Level warp_sum(Level s) {
         add_exact(s.hi, s.lo, h);
         s.lo = __fadd_rn(s.lo, l);
     }
+    // (partners add their low parts in two orders; the CTAs of a cluster, to which lanes send it, have to agree on every bit)
+    s.hi = __shfl_sync(0xffffffffu, s.hi, 0);
+    s.lo = __shfl_sync(0xffffffffu, s.lo, 0);
     return s;
 }
 __device__ __forceinline__ double to_double(Level s) { return static_cast<double>(s.hi) + static_cast<double>(s.lo); }
