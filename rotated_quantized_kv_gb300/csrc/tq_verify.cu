@@ -25,7 +25,7 @@
 //
 // Bound by waits that follow one another: the drafts, their numbers, a pass for each rejection at the path's nodes
 // (about 3 us: 20 instructions a weight, then the CTAs meet), the draw.  One chain of 4 drafts, 32000
-// fp32: 12.3 us; 32 trees of 16 drafts, 131072 bf16, with their distributions: 31.5 us (clusters of four CTAs instead of
+// fp32: 13 us; 32 trees of 16 drafts, 131072 bf16, with their distributions: 33 us (clusters of four CTAs instead of
 // eight: 6 us more; the walk by all warps, binary64 sums of tiles and bodies unrolled four times: 13 us more).
 #include <algorithm>
 
