@@ -235,7 +235,7 @@ __device__ __forceinline__ void rotate_queries(const PagedParams &p, __half *to,
 struct Source {
     const uint8_t *k, *v;
     const char *s;                         // scales: keys' for the first half of the warp, values' for the second
-    uint32_t kblock, vblock, sblock;       // bytes a page (below 2^32: the host checks)
+    uint32_t kblock, vblock, sblock;       // bytes a page (below 2^32: the host checks; without a table: 0)
     int page, n_pages, last;               // tokens a page; pages of the pool; the sequence's last page
     int index, left;                       // page of the stage's first token, and tokens of it from there on
     bool good;                             // that page is in the pool
@@ -265,12 +265,12 @@ struct Source {
         o.point<F>(w);
         return o;
     }
-    // The addresses of page `page_` from its token `skip` on.
+    // The addresses of page `page_` from its token `skip` on.  (In 64 bits: a segment without a table is one page of any size.)
     template <class F>
     __device__ __forceinline__ void aim(uint32_t page_, uint32_t skip, const uint8_t *&ka_, const uint8_t *&va_, const char *&sa_) const {
-        ka_ = k + static_cast<uint64_t>(page_) * kblock + skip * F::kTokenK;
-        va_ = v + static_cast<uint64_t>(page_) * vblock + skip * F::kTokenV;
-        sa_ = s + static_cast<uint64_t>(page_) * sblock + skip * 4u;
+        ka_ = k + static_cast<uint64_t>(page_) * kblock + static_cast<uint64_t>(skip) * F::kTokenK;
+        va_ = v + static_cast<uint64_t>(page_) * vblock + static_cast<uint64_t>(skip) * F::kTokenV;
+        sa_ = s + static_cast<uint64_t>(page_) * sblock + static_cast<uint64_t>(skip) * 4u;
     }
     // At page `index`, for the stage at w.
     template <class F>
