@@ -11,16 +11,16 @@
 namespace tqk {
 namespace paged {
 
-__device__ __forceinline__ int seg_tokens(const PagedList &l, int seg, int b) {
+__host__ __device__ __forceinline__ int seg_tokens(const PagedList &l, int seg, int b) {
     return l.len[seg] ? min(max(l.len[seg][b], 0), l.limit[seg]) : l.limit[seg];
 }
 // Stages of the class's i-th segment.
-__device__ __forceinline__ int seg_stages(const PagedList &l, const PagedClass &c, int i, int b) {
+__host__ __device__ __forceinline__ int seg_stages(const PagedList &l, const PagedClass &c, int i, int b) {
     const int n = seg_tokens(l, c.seg[i], b);
     return n / c.unit + (n % c.unit ? 1 : 0);
 }
 // Stages of (b, h, any rb).
-__device__ __forceinline__ int head_stages(const PagedList &l, const PagedClass &c, int b, int h) {
+__host__ __device__ __forceinline__ int head_stages(const PagedList &l, const PagedClass &c, int b, int h) {
     int n = 0;
 #pragma unroll 1
     for (int i = 0; i < c.n; i++)
@@ -57,16 +57,24 @@ struct Walk {
     bool fresh;          // begins a (b, h, rb)
 };
 
-__device__ __forceinline__ void lost(Walk &w) { w.h = w.rb = w.i = w.st = w.tokens = 0, w.n_st = 1; }
+__host__ __device__ __forceinline__ void lost(Walk &w) { w.h = w.rb = w.i = w.st = w.tokens = 0, w.n_st = 1; }
 
-__device__ __forceinline__ void bind(const PagedList &l, const PagedClass &c, Walk &w) {
+__host__ __device__ __forceinline__ void bind(const PagedList &l, const PagedClass &c, Walk &w) {
     w.tokens = seg_tokens(l, c.seg[w.i], w.b);
     w.n_st = w.tokens / c.unit + (w.tokens % c.unit ? 1 : 0);
 }
 
+// The n-th head of a set (from 0), or -1.
+__host__ __device__ __forceinline__ int head_of(unsigned heads, int n) {
+#pragma unroll 1
+    for (int h = 0; h < kMaxH; h++)
+        if (((heads >> h) & 1) && n-- == 0) return h;
+    return -1;
+}
+
 // Stage `at` of sequence b.  (This and what follows are no part of a kernel's loop and would be most of its code, a
 // quarter of a megabyte, if they were inlined: warps then waited for instructions.)
-static __device__ __noinline__ Walk seek(const PagedList &l, const PagedClass &c, int b, int at) {
+static __host__ __device__ __noinline__ Walk seek(const PagedList &l, const PagedClass &c, int b, int at) {
     Walk w;
     w.b = b;
     w.fresh = true;
@@ -77,8 +85,8 @@ static __device__ __noinline__ Walk seek(const PagedList &l, const PagedClass &c
             const int block = at / w.n_st, head = block / c.n_rb;
             w.st = at - block * w.n_st;
             w.rb = block - head * c.n_rb;
-            w.h = static_cast<int>(__fns(c.heads[0], 0, head + 1));
-            if (w.h < l.H) return w;
+            w.h = head_of(c.heads[0], head);
+            if (w.h >= 0) return w;  // (a length that has become shorter: there is no such head)
         }
         lost(w);
         return w;

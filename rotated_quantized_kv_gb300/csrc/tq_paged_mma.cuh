@@ -236,7 +236,7 @@ struct Source {
     const uint8_t *k, *v;
     const char *s;                         // scales: keys' for the first half of the warp, values' for the second
     uint32_t kblock, vblock, sblock;       // bytes a page (below 2^32: the host checks; without a table: 0)
-    int page, n_pages, last;               // tokens a page; pages of the pool; the sequence's last page
+    int page, n_pages, last;               // tokens a page; pages of the pool; the sequence's last page (-1: none)
     int index, left;                       // page of the stage's first token, and tokens of it from there on
     bool good;                             // that page is in the pool
     const uint8_t *ka, *va;                // the lane's 16 bytes of the stage
@@ -259,7 +259,7 @@ struct Source {
             o.n_pages = p.list.B;
         }
         o.page = g.page;
-        o.last = w.tokens > 0 ? paged::page_index(g, w.tokens - 1) : 0;
+        o.last = w.tokens > 0 ? paged::page_index(g, w.tokens - 1) : -1;
         o.index = paged::page_index(g, w.st * F::PT);
         o.pages.open(g, w.b, o.last, o.index, lane);
         o.point<F>(w);
