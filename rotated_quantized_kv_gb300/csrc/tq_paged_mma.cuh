@@ -95,8 +95,12 @@ struct Run {
 #pragma unroll
             for (int k = 0; k < 4; k++) acc[i][k] = 0.f;
     }
+    // The reference, or that there is none yet: no score, or only scores of minus infinity, whose weights are 0 at
+    // any finite m (against a reference of minus infinity they would be NaN).
+    __device__ __forceinline__ float reference() const { return mt == kNegInf ? kNegInf : m; }
     __device__ __forceinline__ void start() {
-        m = mt = m_ref = kNegInf;
+        m = 0.f;
+        mt = m_ref = kNegInf;
         l = 0.f;
         some = false;
         clear();
@@ -120,7 +124,7 @@ __device__ __forceinline__ void softmax(Run<MT> &r, const float (&s)[2 * T], con
         const float now = fmaxf(r.mt, warp_max_g(top));
         const float f = now == kNegInf ? 1.f : ex2(r.mt - now);
         r.mt = now;
-        r.m = now - 127.f;
+        r.m = now == kNegInf ? 0.f : now - 127.f;
         r.l *= f;
         r.w *= f;
 #pragma unroll
@@ -374,7 +378,7 @@ __device__ __forceinline__ void attend(const PagedParams &p, F &f, int worker, i
         const float W = F::kLinear ? warp_sum_g(r.w) : 0.f;
         const float scale = r.m_ref == r.m ? 1.f : ex2(r.m_ref - r.m);
         f.fold(r, copy, W, scale, lane);
-        r.m_ref = r.m;
+        r.m_ref = r.reference();
         r.some = true;
         r.clear();
     };
@@ -397,7 +401,7 @@ __device__ __forceinline__ void attend(const PagedParams &p, F &f, int worker, i
                     const float sum = warp_sum_g(r.l);
                     __syncwarp();
                     F::record(p.part + p.cls.part0 + paged::group_slot(l, p.cls, worker, now_b, now_h & 255, now_h >> 8) * F::R * (F::D + 4), copy,
-                              r.m, sum, lane);
+                              r.reference(), sum, lane);
                     __syncwarp();
                 }
                 if (k == n_st) break;

@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import test_gpu_paged as paged
 from test_gpu_serving import DEV, gen, randn
 
 pytestmark = pytest.mark.gpu
@@ -54,3 +55,46 @@ def test_segment_without_a_table_beyond_four_gigabytes(tq, d, kb, vb, row):
     assert want.abs().max() > 0.1
     # (other workers' shares, so other roundings: each result is off by half a step, and by 2^-11 of a level)
     assert (out.double() - want.double()).norm() <= 2.0**-10 * want.double().norm()
+
+
+INF = float("inf")
+
+
+def infinite_case(tq, d, seed, kinds, lens, gqa=4):
+    B, H = len(lens), 2
+    c = paged.Case(tq, d, H, gqa, B, [(k, 32, max(lens)) for k in kinds], seed=seed, lens=[lens] * len(kinds))
+    c.q[:, :, 0] = c.q[:, :, 0].abs() + 0.5          # the sign of an infinite coordinate is that of the score
+    return c
+
+
+def place(c, i, b, t):
+    """Pages of segment i, and places on them, of tokens t of sequence b."""
+    P = c.parts[i].layout.capacity
+    return c.tables[i][b].long()[t // P], t % P
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("beside", [False, True])
+def test_keys_at_minus_infinity(tq, d, beside):
+    """Tokens whose score is minus infinity have no weight, wherever a worker's share begins; a row of nothing else is zeros."""
+    lens = [40000, 33, 16, 70000, 64]                # (a share is several stages)
+    c = infinite_case(tq, d, d + 1, ["fp16", (4, 4)] if beside else ["fp16"], lens)
+    gone = {(0, 0): range(30000), (0, 1): range(0, 40000, 3), (1, 1): range(33), (2, 0): range(16), (2, 1): range(1, 16),
+            (3, 0): range(16, 70000), (3, 1): range(69950)}
+    for (b, h), t in gone.items():
+        t = torch.tensor(list(t), device=DEV)
+        page, at = place(c, 0, b, t)
+        c.parts[0].k[page, h, at, 0] = -INF
+        c.rows[0][b][0][h, t, 0] = -INF
+    out = c.run()
+    want, size, reach = c.reference()
+    if not beside:
+        for b, h in ((1, 1), (2, 0)):
+            assert torch.isnan(want[b, 4 * h:4 * h + 4]).all()  # (0 / 0 of the definition)
+            assert (out[b, 4 * h:4 * h + 4] == 0).all()
+            want[b, 4 * h:4 * h + 4] = size[b, 4 * h:4 * h + 4] = 0.0
+    assert torch.isfinite(out).all()
+    # (Case.check's bound; the largest finite score is below 40 here)
+    err = (out.double() - want).norm(dim=-1)
+    tol = 2.0**-11 * 1.01 * want.norm(dim=-1) + ((2.0**-11 if beside else 0.0) + 2.0**-18 + 80 * 2.0**-19) * size + 1e-7
+    assert bool((err <= tol).all()), float((err / tol).max())
