@@ -656,7 +656,9 @@ tq_status tq_paged_workspace_size(const tq_layer_view *pools, int batch, int n_h
  * the cache, split over its length and joined: out[b][j] = softmax(q . k / sqrt(d)) . v over the tokens
  * that sequence b holds of every segment of the view (pages[i] says how segment i is laid out).  A
  * sequence without tokens yields zeros.  A token whose page is outside the pool is left out, and one whose score
- * is minus infinity has no weight (where there is no other: zeros).
+ * is minus infinity has no weight (where there is no other: zeros).  A coordinate of an fp16 value that is no finite
+ * number leaves that coordinate of the result not finite, and no other: an infinite one infinite, if its weight is not
+ * rounded to zero.
  * q_heads: any multiple of n_heads.
  *   q    device fp16, element (b, j, e) at b*q_stride[0] + j*q_stride[1] + e, 2-byte aligned
  *   out  device fp16 [batch][q_heads][d], 16-byte aligned; must not overlap the inputs

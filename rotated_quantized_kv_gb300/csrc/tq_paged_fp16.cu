@@ -21,6 +21,8 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&a)[4], unsigned at) {
                  : "r"(at));
 }
 
+constexpr float kInfinity = __builtin_huge_valf();
+
 template <int DIM>
 struct Half {
     static constexpr int D = DIM, R = 4, MT = D / 16;
@@ -104,7 +106,9 @@ struct Half {
 #pragma unroll
             for (int i = 0; i < 2; i++) {
                 float &at = copy[16 * mt + 8 * i];
-                at = r.some ? fmaf(at, f, r.sum(mt, i)) : r.sum(mt, i);
+                // (an infinite value: hi's sum tells its sign, lo may be 0 or negative)
+                const float hi = r.acc[mt][2 * i], x = fabsf(hi) == kInfinity ? hi : r.sum(mt, i);
+                at = r.some ? fmaf(at, f, x) : x;
             }
     }
     static __device__ __forceinline__ void record(float *rec, const float *copy, float m, float l, int lane) {

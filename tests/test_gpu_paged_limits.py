@@ -98,3 +98,23 @@ def test_keys_at_minus_infinity(tq, d, beside):
     err = (out.double() - want).norm(dim=-1)
     tol = 2.0**-11 * 1.01 * want.norm(dim=-1) + ((2.0**-11 if beside else 0.0) + 2.0**-18 + 80 * 2.0**-19) * size + 1e-7
     assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("beside", [False, True])
+def test_infinite_values(tq, d, beside):
+    """An infinite coordinate of an fp16 value makes that coordinate of the outputs infinite, and no other."""
+    lens = [40, 3, 130]
+    c = infinite_case(tq, d, d + 3, ["fp16", (4, 4)] if beside else ["fp16"], lens)
+    c.q *= 0.25                                      # (weights near one another)
+    for b, h, t, e, x in ((0, 0, 7, 5, INF), (0, 1, 20, d - 1, -INF), (1, 0, 0, 3, INF), (1, 0, 1, 3, -INF), (2, 1, 129, 0, INF),
+                          (2, 1, 0, 9, -INF), (2, 1, 100, 9, -INF)):
+        page, at = place(c, 0, b, t)
+        c.parts[0].v[page, h, at, e] = x
+        c.rows[0][b][1][h, t, e] = x
+    out = c.run().double()
+    want, _, _ = c.reference()
+    assert torch.isinf(want).sum() == 4 * 4 and torch.isnan(want).sum() == 4
+    odd = ~torch.isfinite(want)
+    assert torch.equal(torch.isnan(out), torch.isnan(want)) and torch.equal(out[torch.isinf(want)], want[torch.isinf(want)])
+    assert (out - want)[~odd].abs().max() < 0.01
