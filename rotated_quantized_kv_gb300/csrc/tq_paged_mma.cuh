@@ -69,7 +69,7 @@ __device__ __forceinline__ uint64_t policy_for(bool once) {
 // What a special stage of the ring is.
 struct alignas(16) Stage {
     int word;            // tokens, and kFresh (another sequence, head or block of rows), kPart (not whole)
-    int b, h_rb;         // sequence; KV head and block of rows
+    int b, block;        // sequence; KV head and block of rows as h n_rb + rb
     unsigned bad;        // kPart: bit i: the i-th page of it is outside the pool
     int page, skip;      // kPart: tokens a page, and tokens of the first page before the stage
     int pad[2];
@@ -356,7 +356,7 @@ __device__ __forceinline__ void attend(const PagedParams &p, F &f, int worker, i
             if (lane == 0) {
                 stages[to].word = n | (w.fresh ? kFresh : 0) | (whole ? 0 : kPart);
                 stages[to].b = w.b;
-                stages[to].h_rb = w.h | (w.rb << 8);
+                stages[to].block = w.h * p.cls.n_rb + w.rb;
             }
         }
         if (++to == NS) to = 0;
@@ -382,7 +382,7 @@ __device__ __forceinline__ void attend(const PagedParams &p, F &f, int worker, i
         r.some = true;
         r.clear();
     };
-    int now_b = 0, now_h = 0, at = 0;
+    int now_b = 0, now_block = 0, at = 0;
     // one pass more than stages (k = n_st), so that a block ends in one place
 #pragma unroll 1
     for (int k = 1 - NS; k <= n_st; k++) {  // (below 0: stages on their way first)
@@ -400,14 +400,15 @@ __device__ __forceinline__ void attend(const PagedParams &p, F &f, int worker, i
                     fold();
                     const float sum = warp_sum_g(r.l);
                     __syncwarp();
-                    F::record(p.part + p.cls.part0 + paged::group_slot(l, p.cls, worker, now_b, now_h & 255, now_h >> 8) * F::R * (F::D + 4), copy,
+                    F::record(p.part + p.cls.part0 + paged::group_slot(l, p.cls, worker, now_b, 0, now_block) * F::R * (F::D + 4), copy,
                               r.reference(), sum, lane);
                     __syncwarp();
                 }
                 if (k == n_st) break;
                 now_b = stages[at].b;
-                now_h = stages[at].h_rb;
-                f.queries(p, reinterpret_cast<__half *>(copy), now_b, now_h & 255, now_h >> 8, lane);
+                now_block = stages[at].block;
+                const int h = now_block / p.cls.n_rb;
+                f.queries(p, reinterpret_cast<__half *>(copy), now_b, h, now_block - h * p.cls.n_rb, lane);
                 __syncwarp();
                 r.start();
             }

@@ -118,3 +118,19 @@ def test_infinite_values(tq, d, beside):
     odd = ~torch.isfinite(want)
     assert torch.equal(torch.isnan(out), torch.isnan(want)) and torch.equal(out[torch.isinf(want)], want[torch.isinf(want)])
     assert (out - want)[~odd].abs().max() < 0.01
+
+
+def test_query_heads_beyond_24_bits(tq):
+    """More blocks of query rows than 2^23, all with the same query: every row is what one row alone is."""
+    d, Hq, n = 64, (1 << 24) + 10, 30
+    g = gen(3)
+    rot = tq.tq_make_rotation(d, 21)
+    seg = tq.PackedSegment(tq.make_layout(1, 1, d, 32, 4, 4), n_tokens=n)
+    k, v = (randn(g, 1, 1, n, d, dtype=torch.float16) for _ in range(2))
+    tq.tq_append(seg, rot, k, v, torch.zeros(1, dtype=torch.int32, device=DEV))
+    q = randn(g, 1, 1, d, dtype=torch.float16)
+    want = attend(tq, rot, q, [seg], [None], [None])
+    out = attend(tq, rot, q.expand(1, Hq, d), [seg], [None], [None])
+    assert want.abs().max() > 0.01
+    for part in out[0].split(1 << 22):
+        assert torch.equal(part, want[0].expand(len(part), d))
