@@ -503,7 +503,7 @@ cudaError_t launch_paged_merge(const PagedMergeParams &p, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = p.n_classes > 0 ? 1 : 0;  // (behind a kernel of the call)
     const long long rows = static_cast<long long>(p.list.B) * p.list.H * p.g;
     if (!on_tensor_cores(p.d)) {
         cfg.gridDim = dim3(static_cast<unsigned>(rows));

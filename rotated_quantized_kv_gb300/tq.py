@@ -977,7 +977,7 @@ def tq_paged_attention(view: tq_layer_view, q: torch.Tensor, out: torch.Tensor, 
             _int32(c, where, (B,))
             tensors.append(c)
         fields += (at, stride, width, 0 if c is None else c.data_ptr())
-    H = view.seg[0].layout.n_heads if n else Hq
+    H = view.seg[0].layout.n_heads if n else 1  # (no segment: whatever divides the query heads)
     _call(tensors, stream, where, _lib.tq_paged_attention, ctypes.byref(view), _pack_pages[n](*fields), B, H, Hq, d,
           q.data_ptr(), _pack2(q.stride(0), q.stride(1)), out.data_ptr(), workspace.data_ptr(),
           workspace.numel() * workspace.element_size())

@@ -134,3 +134,24 @@ def test_query_heads_beyond_24_bits(tq):
     assert want.abs().max() > 0.01
     for part in out[0].split(1 << 22):
         assert torch.equal(part, want[0].expand(len(part), d))
+
+
+@pytest.mark.parametrize("Hq", [1, 4, 40])
+def test_view_without_segments(tq, Hq):
+    """No segment, no token: zeros, for any number of query heads, eager and in a graph behind other work."""
+    d, B = 128, 3
+    q = randn(gen(1), B, Hq, d, dtype=torch.float16)
+    view = tq.layer_view(tq.tq_make_rotation(d, 1), [])
+    ws = torch.empty(max(tq.tq_paged_workspace_size(view, B, 1, Hq, d), 1), dtype=torch.uint8, device=DEV)
+    out = torch.full((B, Hq, d), 7.0, dtype=torch.float16, device=DEV)
+    tq.tq_paged_attention(view, q, out, ws, [], [])
+    assert (out == 0).all()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        out.zero_()
+        out.add_(3.0)
+        tq.tq_paged_attention(view, q, out, ws, [], [])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert (out == 0).all()
