@@ -609,7 +609,8 @@ tq_status tq_tree_attention(const tq_layer_view *layer, int batch, int n_heads, 
  *   granted     [batch]
  * All device int32, 4-byte aligned, that must not overlap.  A length outside [0, max_pages page_size] and
  * an n_free outside [0, n_pages] count as the nearest one inside.  free_pages has room for
- * n_pages entries.  max_pages * page_size and n_pages * page_size: below 2^31. */
+ * n_pages entries.  max_pages * page_size and n_pages * page_size: below 2^31; batch: up to 2^30
+ * (TQ_ERR_UNSUPPORTED). */
 tq_status tq_page_tables(int batch, int page_size, int max_pages, int n_pages, int *table, int64_t table_stride_b, int *length,
                          const int *n_new, int n_max, int *free_pages, int *n_free, int *slots, int *positions, int *granted,
                          void *stream);

@@ -17,8 +17,8 @@ namespace {
 tq_status check_pages(int batch, int page_size, int max_pages, int n_pages, const int *table, int64_t table_stride,
                       const int *length, const int *count, const int *free_pages, const int *n_free) {
     if (batch < 0 || page_size < 1 || max_pages < 0 || n_pages < 0 || table_stride < 0) return TQ_ERR_ARG;
-    // tokens of a sequence and slots of the pool are counted in 32 bits
-    if (max_pages > 0x7fffffff / page_size || n_pages > 0x7fffffff / page_size) return TQ_ERR_UNSUPPORTED;
+    // tokens of a sequence, slots of the pool and sequences (rounded up to a CTA's) are counted in 32 bits
+    if (max_pages > 0x7fffffff / page_size || n_pages > 0x7fffffff / page_size || batch > 1 << 30) return TQ_ERR_UNSUPPORTED;
     if (batch == 0) return TQ_OK;
     if (batch > 1 && table_stride < max_pages) return TQ_ERR_ARG;
     if (!length || !count || !n_free || (max_pages > 0 && !table) || (n_pages > 0 && !free_pages)) return TQ_ERR_ARG;
