@@ -36,7 +36,7 @@ template <int D>
 struct Plain {
     static constexpr int R = kPlainRows, TT = D >= 512 ? 16 : 32, LD = D + 1;
     static constexpr int DPT = (D + kPlainThreads - 1) / kPlainThreads;
-    static constexpr size_t smem = (2 * R * LD + TT * LD + R * TT + 3 * R) * sizeof(float);
+    static constexpr size_t smem = (R * LD + TT * LD + R * TT + 3 * R) * sizeof(float);
 };
 
 // Coordinate i of a token's key (kv 0) or value, in the rotated space.
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kPlainThreads) paged_plain_kernel(const __grid
     constexpr int R = C::R, TT = C::TT, LD = C::LD, DPT = C::DPT;
     extern __shared__ float sm[];
     __shared__ int buf[kPlainWarps + 4];
-    float *q = sm, *raw = q + R * LD, *tok = raw + R * LD, *S = tok + TT * LD;  // queries of the segment's space, as they are; tokens; scores
+    float *q = sm, *tok = q + R * LD, *S = tok + TT * LD;  // queries in the segment's space; tokens; scores
     float *row_m = S + R * TT, *row_l = row_m + R, *row_c = row_l + R;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, worker = blockIdx.x;
     asm volatile("griddepcontrol.launch_dependents;");

@@ -152,7 +152,6 @@ tq_status tq_paged_attention(const tq_layer_view *pools, const tq_pages *pages, 
     std::memset(&p, 0, sizeof(p));
     p.list.B = batch;
     p.list.H = n_heads;
-    p.n_seg = pools->n_segments;
     for (int i = 0; i < pools->n_segments; ++i) {
         const tq_segment &sg = pools->seg[i];
         const tq_pages &pg = pages[i];
@@ -161,7 +160,7 @@ tq_status tq_paged_attention(const tq_layer_view *pools, const tq_pages *pages, 
         s.seg = seg_view(&sg);
         s.n_pages = sg.layout.batch;
         s.page = sg.layout.capacity;
-        s.len = pg.len;
+        int limit;  // most tokens a sequence can hold
         if (pg.table) {
             if (pg.max_pages < 0 || pg.table_stride_b < 0 || (batch > 1 && pg.table_stride_b < pg.max_pages) || !pg.len)
                 return TQ_ERR_ARG;
@@ -170,19 +169,19 @@ tq_status tq_paged_attention(const tq_layer_view *pools, const tq_pages *pages, 
             if ((s.seg.kblock | s.seg.vblock | (static_cast<uint64_t>(n_heads) * s.page * 4)) >> 32) return TQ_ERR_UNSUPPORTED;
             s.table = pg.table;
             s.table_stride = pg.table_stride_b;
-            s.limit = pg.max_pages * s.page;
+            limit = pg.max_pages * s.page;
         } else {  // a page a sequence
             if (sg.layout.batch != batch) return TQ_ERR_ARG;
             if (sg.n_tokens < 0 || sg.n_tokens > sg.layout.capacity) return TQ_ERR_SIZE;
-            s.limit = sg.n_tokens;
+            limit = sg.n_tokens;
         }
         // 2^shift / page rounded up, shift = 31 + ceil(log2 page): the excess times t stays below 2^shift / page
         s.shift = 31;
         while (s.page > 1 && (1LL << (s.shift - 31)) < s.page) ++s.shift;
         if (s.page > 0) s.magic = static_cast<uint32_t>(((1ULL << s.shift) + s.page - 1) / s.page);
-        if (s.limit > 0x7fffffff - 1024) return TQ_ERR_UNSUPPORTED;  // rounded up to stages in 32 bits
-        p.list.len[i] = s.len;
-        p.list.limit[i] = s.limit;
+        if (limit > 0x7fffffff - 1024) return TQ_ERR_UNSUPPORTED;  // rounded up to stages in 32 bits
+        p.list.len[i] = pg.len;
+        p.list.limit[i] = limit;
     }
     PagedLayout o;
     st = paged_layout(pools, batch, n_heads, q_heads, head_dim, o);

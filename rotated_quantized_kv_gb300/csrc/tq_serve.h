@@ -259,8 +259,7 @@ struct PagedSeg {
     SegView seg;                         // its batch elements are pages
     const int *table;                    // pages of a sequence, or nullptr: page b
     int64_t table_stride;
-    const int *len;                      // tokens of a sequence, or nullptr: limit
-    int n_pages, page, limit;            // limit: most tokens a sequence can hold
+    int n_pages, page;                   // pages of the pool, tokens a page
     uint32_t magic;                      // t / page = t magic >> shift for 0 <= t < 2^31
     int shift;
 };
@@ -278,13 +277,13 @@ constexpr int kPagedClasses = 1 + TQ_MAX_SEGMENTS * kMaxH;
 // What the list is made of: lengths without the segments' data.
 struct PagedList {
     int B, H;
-    const int *len[TQ_MAX_SEGMENTS];
-    int limit[TQ_MAX_SEGMENTS];
+    const int *len[TQ_MAX_SEGMENTS];     // tokens of a sequence, or nullptr: limit
+    int limit[TQ_MAX_SEGMENTS];          // most tokens a sequence can hold
 };
 struct PagedParams {
     PagedList list;
     PagedClass cls;                      // of this launch
-    int g, d, n_seg;
+    int g, d;
     PagedSeg seg[TQ_MAX_SEGMENTS];
     const uint16_t *q;
     int64_t qs[2];                       // strides of (b, head)
