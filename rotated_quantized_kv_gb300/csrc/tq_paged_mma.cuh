@@ -81,7 +81,7 @@ constexpr int kFresh = 1 << 16, kPart = 1 << 17;
 template <int MT>
 struct Run {
     float m, mt;         // reference of the weights; the maximum of S + log2 sigma (+ 127)
-    float l, w;          // sums of p, and of p sigma since the last fold
+    float l, w;          // sums of p, and of p sigma since the last fold (of the lane's rows: even or odd ones)
     float m_ref;         // reference of the copy
     float acc[MT][4];
     int tiles;           // since the last fold
@@ -375,7 +375,7 @@ __device__ __forceinline__ void attend(const PagedParams &p, F &f, int worker, i
     };
     Run<F::MT> r;
     auto fold = [&]() {
-        const float W = F::kLinear ? warp_sum_g(r.w) : 0.f;
+        const float W = F::kLinear ? warp_sum_g(lane & 4 ? -r.w : r.w) : 0.f;  // even rows' less odd rows'
         const float scale = r.m_ref == r.m ? 1.f : ex2(r.m_ref - r.m);
         f.fold(r, copy, W, scale, lane);
         r.m_ref = r.reference();
@@ -476,6 +476,33 @@ cudaError_t launch(const PagedParams &p, const Levels &lv, cudaStream_t s) {
 }
 
 // ------------------------------------------------------------------- packed
+// 1-bit values: a set bit of fp16's exponent field (bits 10 to 14) is a normal number by itself, so that a code is one mask
+// away from its word.  Even rows enter as b, odd rows as b - 1 (1 - b against negative weights): what is left to add is the even
+// rows' weights less the odd rows', and the sums are no larger than what they are the sums of.  (As subnormals, bits 0
+// to 9, the tensor cores align products by the exponent that all subnormals share, up to 10 bits off: weights that
+// differ had errors of 3.3e-4 of the result, 30000 tokens, on top of fp16's own 2.1e-4, at 104 us for the 108 us of 32
+// x 16384 tokens K4V1 here; +-1 by the sign bit takes a shift a code: 122 us.)
+struct Bits1 {
+    static constexpr bool kLinear = true;
+    static constexpr __host__ __device__ int dim(int mt, int r) { return mt + 8 * r; }
+    // the place of code j in its word
+    static constexpr __host__ __device__ int place(int j) { return j < 5 ? j + 10 : j < 10 ? j + 5 : j < 15 ? j : 14; }
+    static __device__ __forceinline__ void pair(const uint8_t *p, int RV, const VCtx &cx, uint32_t (&ra)[8], uint32_t (&rb)[8]) {
+        const uint32_t x = *reinterpret_cast<const uint32_t *>(p + cx.off), y = *reinterpret_cast<const uint32_t *>(p + cx.off + RV);
+        const uint32_t z = prmt(x, y, static_cast<uint32_t>(cx.sh)) ^ 0xFFFF0000u;  // the even row's 16 codes | the odd row's, inverted
+        const uint32_t word[4] = {z << 10, z << 5, z, z >> 1};
+#pragma unroll
+        for (int mt = 0; mt < 8; mt++) {
+            ra[mt] = word[mt / 5] & (0x00010001u << place(mt));
+            rb[mt] = word[(mt + 8) / 5] & (0x00010001u << place(mt + 8));
+        }
+    }
+    // 1 / the value of a set bit
+    static __device__ __forceinline__ float unscale(int mt, int r) {
+        return __uint_as_float(static_cast<uint32_t>(127 + 15 - (1 << (place(dim(mt, r)) - 10))) << 23);
+    }
+};
+
 // 4-bit values: pair table of 256 entries; E/O fields of 8 bits: dims (2mt, 2mt+1)
 struct Pairs4 {
     static constexpr bool kLinear = false;
@@ -511,7 +538,7 @@ struct Packed {
     static constexpr int entries = VB >= 2 && VB <= 4 ? 1 << (2 * VB) : 0;
     static constexpr int kTable = entries * 128 + (VB >= 5 ? 512 : 0);  // pair table: a column a lane
     using KU = KUnpack<KB>;
-    using VD = typename std::conditional<VB == 4, Pairs4, VDec<VB, 7>>::type;
+    using VD = typename std::conditional<VB == 1, Bits1, typename std::conditional<VB == 4, Pairs4, VDec<VB, 7>>::type>::type;
     static constexpr bool kLinear = VD::kLinear;
 
     VCtx vx;
@@ -646,6 +673,10 @@ struct Packed {
         }
         uint32_t bp[4];
         softmax<FULL, 2>(r, s, have, v, g, c, sel, bp);
+        if constexpr (VB == 1) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) bp[i] ^= 0x80000000u;  // (odd rows')
+        }
         const uint8_t *vst = buf + ROWS * RK;
 #pragma unroll
         for (int t = 0; t < 2; t++) {
@@ -670,7 +701,7 @@ struct Packed {
 #pragma unroll
             for (int k = 0; k < 2; k++) {
                 const float a = r.sum(mt, k);
-                if constexpr (kLinear) x[VD::dim(mt, k)] = c1 * (2.0f * a * VDec<1, 7>::unscale(mt, k) - W);
+                if constexpr (kLinear) x[VD::dim(mt, k)] = c1 * (2.0f * a * VD::unscale(mt, k) - W);
                 else x[VD::dim(mt, k)] = a * inv;
             }
 #pragma unroll

@@ -155,3 +155,31 @@ def test_view_without_segments(tq, Hq):
     graph.replay()
     torch.cuda.synchronize()
     assert (out == 0).all()
+
+
+@pytest.mark.parametrize("spread", [0.02, 2.0])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kind", [(4, 1), (3, 1), (3, 2), (4, 3), (8, 4), (2, 5), (1, 8), "fp16"])
+def test_long_sums_are_as_good_as_their_rounding(tq, d, kind, spread):
+    """40000 tokens of 8 heads (some twenty tiles a worker), vectors of one size, scores of standard deviation `spread`: a
+    mean far smaller than its values, and weights far apart.  The error of the whole is that of rounding the result (uniform in a
+    step: step / sqrt(12) each), once more that of the levels above 4 bits (independent of it, at most as large: sqrt(2)),
+    0.3 of it up to 4 bits (levels are scaled to round well: sqrt(1.09)), and a tenth for all else: 4096 and more
+    roundings, whose squares' mean is within 5 x 1.4% of its expectation, and sums and weights of 22 bits."""
+    H = 8
+    c = paged.Case(tq, d, H, 4, 2, [(kind, 64, 40000)], seed=5, scale=0.25, lens=[[40000, 39000]])
+    if kind != "fp16":
+        for i, scale in enumerate((c.parts[0].kscale, c.parts[0].vscale)):
+            own = scale[:c.parts[0].layout.batch * H * 64].view(-1, H, 64)
+            for b in range(2):
+                page, at = place(c, 0, b, torch.arange(int(c.lens[0][b]), device=DEV))
+                c.rows[0][b][i] = c.rows[0][b][i] / own[page, :, at].t()[:, :, None].double()
+            scale[~torch.isnan(scale)] = 1.0
+    x = torch.cat([(c.q[b].double().view(H, 4, d) @ c.rows[0][b][0].transpose(1, 2)).flatten() for b in range(2)]) / d**0.5
+    c.q *= spread / float(x.std())
+    out = c.run().double()
+    want, _, _ = c.reference()
+    step = torch.exp2(torch.floor(torch.log2(want.abs().clamp(min=2.0**-14))) - 10)
+    some = 1.41 if kind != "fp16" and kind[1] > 4 else 1.05
+    far = float((out - want).norm() / (step.norm() / 12**0.5))
+    assert far <= 1.1 * some, far
