@@ -605,7 +605,7 @@ tq_status tq_tree_attention(const tq_layer_view *layer, int batch, int n_heads, 
  *   length[b]   grows by granted[b]; n_free falls by the pages taken
  *   slots       [batch][n_max] (may be NULL): the slot of new token j, -1 from granted[b] on and
  *               where the table's entry is outside [0, n_pages)
- *   positions   [batch][n_max] (may be NULL): length[b] (as it was) + j, -1 likewise
+ *   positions   [batch][n_max] (may be NULL): length[b] (as it was) + j, -1 from granted[b] on
  *   granted     [batch]
  * All device int32, 4-byte aligned, that must not overlap.  A length outside [0, max_pages page_size] and
  * an n_free outside [0, n_pages] count as the nearest one inside.  free_pages has room for
@@ -658,23 +658,25 @@ tq_status tq_paged_workspace_size(const tq_layer_view *pools, int batch, int n_h
  * that sequence b holds of every segment of the view (pages[i] says how segment i is laid out).  A
  * sequence without tokens yields zeros.  A token whose page is outside the pool is left out, and one whose score
  * is minus infinity has no weight (where there is no other: zeros).  A coordinate of an fp16 value that is no finite
- * number leaves that coordinate of the result not finite, and no other: an infinite one infinite, if its weight is not
- * rounded to zero.
- * q_heads: any multiple of n_heads.
+ * number leaves that coordinate of the result not finite, and no other: an infinite one infinite, if its weight is
+ * not rounded to zero.  q_heads: any multiple of n_heads.
  *   q    device fp16, element (b, j, e) at b*q_stride[0] + j*q_stride[1] + e, 2-byte aligned
  *   out  device fp16 [batch][q_heads][d], 16-byte aligned; must not overlap the inputs
  * Scores and the value sum of packed tokens run in the rotated space; one inverse rotation follows the
  * merge.  Sums are binary32, the result is rounded to fp16.  At head dims 64 and 128 queries
  * and weights enter with 22 bits (weights relative to the row's largest weighted value scale, those below
- * 2^-36 of it as zero) and the value levels as fp16, as in tq_tree_attention; at the others
- * everything is binary32.  All numbers on the device may change between replays of a captured call;
- * two calls that may overlap need two workspaces.  QJL heads (key or value), dense
+ * 2^-36 of it as zero) and the value levels as fp16, as in tq_tree_attention, which adds to the rounding of the
+ * result: nothing at 1 and 2 bits, a hundredth at 3, a thirtieth at 4, a tenth at 5, a sixth, a quarter and a
+ * third at 6, 7 and 8; at the others everything is binary32.  All numbers on the device may change between
+ * replays of a captured call; two calls that may overlap need two workspaces.  QJL heads (key or value), dense
  * rotations and segments with attn_mass return TQ_ERR_UNSUPPORTED, as do the sphere law at head dims other
  * than 128 and a packed segment's capacity that is no multiple of 16 (TQ_ERR_ALIGN).  No device memory is
  * allocated and nothing is copied from the host.  Pools whose page is 4 GiB or more of codes
- * return TQ_ERR_UNSUPPORTED.  No part of the call polls for another, so that the workspace's error flag
- * (tq_decode_error_flag) is 0 behind it.  Value scales are below 2^100 at head dims
- * 64 and 128 (what those below 2^-64 give is nothing in fp16). */
+ * return TQ_ERR_UNSUPPORTED, as do segments of which a sequence may hold more than 2^31 - 1025 tokens
+ * (max_pages * capacity, or n_tokens), and calls of 2^31 - 64 or more query rows (batch * q_heads) or of 2^31 or
+ * more stages (16 to 64 tokens of a sequence and KV head for 2 or 4 query heads each).  No part of the call
+ * polls for another, so that the workspace's error flag (tq_decode_error_flag) is 0 behind it.  Value scales are
+ * below 2^100 at head dims 64 and 128 (what those below 2^-64 give is nothing in fp16). */
 tq_status tq_paged_attention(const tq_layer_view *pools, const tq_pages *pages, int batch, int n_heads, int q_heads, int head_dim,
                              const void *q, const int64_t *q_stride, void *out, void *workspace, size_t ws_bytes, void *stream);
 
@@ -709,8 +711,12 @@ typedef struct {
  * rejection leaves r = max(r - s q, 0) (draft NULL: r(t) = 0) and s = sum r; where that is nothing, r = p and
  * s = sum p.  Where no child is accepted, the token is the smallest t with r(0) + ... + r(t) > u_N sum r,
  * or -1 if the row has no weight.  Entries of the rows that are not positive numbers below 2^90
- * count as 0; rows need not sum to 1 (the first test takes p and q as they are).  Products are binary64, a difference
- * is rounded once to binary32, sums carry 48 bits.  accepted and n_accepted are what
+ * count as 0.  The first test takes p and q as they are (s = 1): what comes out is distributed as the target's
+ * samples where its rows and the draft's sum to 1; rows that were filtered are divided by their sums before.  Products
+ * are binary64, a difference is rounded to binary32 (twice where s has more than 24 bits), sums carry 48 bits.  Rows are
+ * read 16 bytes at a time; a draft row whose address is off a 16-byte boundary by another number of bytes than its
+ * target row's is read element by element (N draft rows beside N + 1 target rows of 50257 bf16: 50 us for the 42 of N + 1
+ * draft rows, 32 trees of 16): equal strides, or a vocabulary stride that is a multiple of 16 bytes, avoid it.  accepted and n_accepted are what
  * tq_append takes as index and n_new.  Outputs must not overlap. */
 tq_status tq_verify(const tq_verification *v, void *stream);
 

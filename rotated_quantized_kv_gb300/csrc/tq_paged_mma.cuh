@@ -10,10 +10,13 @@
 //     are two heads times two parities, a query with zeros in the other token's half, so that a (head, parity) is a
 //     head of its own until the record;
 //   - weights are relative to the row's largest weighted value, as in tq_tree_mma.cu: the running
-//     maximum is that of S + log2 sigma (sigma from 2^-64 up, its logarithm read off the bits: within 0.09 above), so
+//     maximum is that of S + log2 sigma (sigma from 2^-64 up, its logarithm read off the bits: at most 0.09 below), so
 //     that fp16 holds the weights that count whatever the values' sizes;
-//   - sums leave the tensor cores every kFold tiles: mma.sync adds with truncation, which drifts by some
-//     2^-19 of the sum a tile.  They go to the warp's copy in shared memory, by binary32 additions.
+//   - value levels are fp16 operands, scaled together so that they round closely (value_levels): beside the result's own
+//     fp16 rounding (2.07e-4 of it) the error against 64 bits is 2.09, 2.12, 2.13, 2.27, 2.38, 2.53 and 2.7e-4 at 2 to
+//     8 bits, 3000 tokens; a second part of the levels would double the products and the tables;
+//   - sums leave the tensor cores every kFold tiles: mma.sync adds with truncation, relative to the largest
+//     of what it adds.  They go to the warp's copy in shared memory, by binary32 additions.
 //
 // Every warp is a worker of its own: a range of the stage list (tq_paged.cuh), a ring of stages that it fills
 // itself by cp.async, its queries, its sums, its records; warps meet nowhere behind the prologue, and nothing waits but for
@@ -115,7 +118,7 @@ __device__ __forceinline__ void softmax(Run<MT> &r, const float (&s)[2 * T], con
     float top = kNegInf;
 #pragma unroll
     for (int i = 0; i < 2 * T; i++) {
-        // log2 v + 127 within [0, 0.09]: the exponent, and the mantissa as its fraction
+        // log2 v + 127, less up to 0.09: the exponent, and the mantissa as its fraction
         const float lg = static_cast<float>(__float_as_int(fmaxf(v[i], 0x1p-64f)));
         const float t = fmaf(lg, 0x1p-23f, s[i]);
         top = fmaxf(top, FULL || ok[i] ? t : kNegInf);

@@ -21,7 +21,7 @@
 // Sums decide at borders between tokens: a row of 10^5 weights has as many borders, and sums with
 // an error of 10^-8 draw another token once in 10^3 draws.  Lanes, warps and tiles keep their sums as two
 // binary32 numbers (exact sums of two, 2^-48); CTAs' sums and prefixes are binary64, of which there are few (its
-// rate is 1/64).  The difference r - s q takes s as two binary32 numbers, one rounding of the result.
+// rate is 1/64).  The difference r - s q takes s as two binary32 numbers, a rounding for each of them that is not 0.
 //
 // Bound by waits that follow one another: the drafts, their numbers, a pass for each rejection at the path's nodes
 // (about 3 us: 20 instructions a weight, then the CTAs meet), the draw.  One chain of 4 drafts, 32000
@@ -411,7 +411,8 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
 
 template <typename T>
 cudaError_t verify(const VerifyParams &p, cudaStream_t s) {
-    // a slice of 4096 elements or more a CTA (32000 fp32: 4 CTAs 15.3 us, 2 CTAs 16.8, 8 no less)
+    // a slice of 4096 elements or more a CTA (32000 fp32, before the walk was one warp's: 4 CTAs 15.3 us, 2 CTAs 16.8, 8
+    // no less; now 12.8 us with 4)
     int ctas = 1;
     while (ctas < kVerMaxCtas && p.V / (2 * ctas) >= 4096) ctas *= 2;
     cudaLaunchConfig_t cfg = {};
